@@ -54,6 +54,7 @@ typedef enum xqa_status {
   XQA_ERR_WORKSPACE = 4,   /* workspace smaller than xqa_workspace_size */
   XQA_ERR_LAUNCH = 5,      /* a CUDA call or kernel launch failed */
   XQA_ERR_DEVICE = 6,      /* no usable CUDA device / attribute query failed */
+  XQA_ERR_VALUE = 7,       /* a scale that cannot be divided by (not finite, or <= 0) */
   /* written by the device into the workspace status word: */
   XQA_ERR_BAD_BLOCK_ID = 16,    /* block_tables entry outside [0, num_blocks) */
   XQA_ERR_CTX_TOO_LONG = 17,    /* context length < 0 or > MBS * block_size */
@@ -65,6 +66,18 @@ typedef enum xqa_status {
 /* KV cache code formats (xqa_shape_t.kv_dtype). */
 #define XQA_KV_E5M2 0 /* 1 sign, 5 exponent (bias 15), 2 mantissa bits */
 #define XQA_KV_E4M3 1 /* 1 sign, 4 exponent (bias 7), 3 mantissa bits, no inf */
+/* 4 bits: E2M1 codes (1 sign, 2 exponent bits of bias 1, 1 mantissa bit: 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6) with one E4M3 scale for every 16 dims of a token. A (page, kv
+ * head) slice is XQA_E2M1_SLICE_BYTES contiguous bytes: 16 tokens x 64 code bytes
+ * (dim 2i in the low nibble of byte i, dim 2i + 1 in the high one), then 16 tokens x
+ * 8 scale bytes. The caches are [NB, Hkv, XQA_E2M1_SLICE_BYTES] (XQA_LAYOUT_HND
+ * only), and a value is scale * E4M3(group scale) * E2M1(code). */
+#define XQA_KV_E2M1 4
+#define XQA_E2M1_SLICE_BYTES 1152
+
+/* 16-bit element types of packed rows. */
+#define XQA_F16 0
+#define XQA_BF16 1
 
 /* KV cache layouts (xqa_shape_t.kv_layout). */
 #define XQA_LAYOUT_HND 0 /* [NB, Hkv, BS, D]: one (page, kv head) slice is contiguous */
@@ -200,6 +213,68 @@ xqa_status_t xqa_dequant_e5m2(const uint8_t* in, size_t n, float scale, uint16_t
  * Same argument conventions as xqa_dequant_e5m2. */
 xqa_status_t xqa_dequant_e4m3(const uint8_t* in, size_t n, float scale, uint16_t* out_fp16_bits,
                               float* out_f32, void* stream);
+
+/* Packed rows of keys and values beside a paged cache (xqa_append, xqa_gather).
+ * Row r holds one token's Hkv heads; sequence b owns the rows cu_seqlens[b] ..
+ * cu_seqlens[b+1] - 1. Strides are in elements, multiples of 8 (16 bytes); 0
+ * selects the contiguous value (Hkv * 128 between rows, 128 between heads), so the
+ * rows may be views of a wider tensor. */
+typedef struct xqa_rows {
+  int32_t batch;              /* B: sequences, >= 1 */
+  int32_t num_kv_heads;       /* Hkv */
+  int32_t head_dim;           /* D = 128 */
+  int32_t block_size;         /* BS = 16 tokens per page */
+  int32_t max_blocks_per_seq; /* MBS: row length of block_tables */
+  int32_t num_blocks;         /* NB: pages in the K (and V) pool */
+  int32_t num_rows;           /* rows of k and v (>= 0); rows that belong to no sequence
+                                 (behind cu_seqlens[B]) are left alone */
+  int32_t kv_dtype;           /* XQA_KV_E5M2, XQA_KV_E4M3 or XQA_KV_E2M1 */
+  int32_t kv_layout;          /* XQA_LAYOUT_HND or (8-bit formats) XQA_LAYOUT_NHD */
+  int32_t dtype;              /* XQA_F16 or XQA_BF16: type of k and v */
+  int64_t k_row_stride, k_head_stride;
+  int64_t v_row_stride, v_head_stride;
+} xqa_rows_t;
+
+/* Writes new tokens' keys and values into the paged cache.
+ *
+ *   k, v          device, rows->dtype [num_rows, Hkv, 128] (strided), 16-byte aligned
+ *   cu_seqlens    device, int32 [B+1], ascending: sequence b's new rows
+ *   block_tables  device, int32 [B, MBS], as for xqa_decode
+ *   context_lens  device, int32 [B]: tokens of each sequence, the new ones counted, so
+ *                 b's n_b rows go to positions ctx_b - n_b .. ctx_b - 1 (what
+ *                 xqa_decode then expects)
+ *   k_scale, v_scale  per-tensor scales; k_scale_dev / v_scale_dev, when not NULL,
+ *                 point to one device float each, read when the kernel runs
+ *   k_cache, v_cache  device, 16-byte aligned; only the new tokens' bytes are written
+ *   device_status device int32 or NULL: receives XQA_ERR_CTX_TOO_LONG (a length below
+ *                 0, above MBS * 16 or below n_b: none of the sequence's rows is
+ *                 written) or XQA_ERR_BAD_BLOCK_ID (the token is not written) if it
+ *                 holds XQA_OK; never cleared
+ *
+ * FP8: code = x / scale in 32 bits, rounded to nearest even, saturated; a NaN stays
+ * a NaN code. E2M1, for each group of 16 dims: s = E4M3((max |x| / scale) / 6), code =
+ * E2M1(x / (scale * s)), both to nearest even and saturated; a group whose s is 0
+ * holds zeros, and one that has a NaN reads back as NaN throughout. Two rows must not
+ * name the same cache slot. One kernel, no host synchronisation, no workspace; may be
+ * captured into a CUDA graph. A host scale that is not finite or not above 0 is
+ * refused (XQA_ERR_VALUE). */
+xqa_status_t xqa_append(const void* k, const void* v, const int32_t* cu_seqlens,
+                        const int32_t* block_tables, const int32_t* context_lens, float k_scale,
+                        float v_scale, const float* k_scale_dev, const float* v_scale_dev,
+                        uint8_t* k_cache, uint8_t* v_cache, const xqa_rows_t* rows,
+                        int32_t* device_status, void* stream);
+
+/* Reads cached tokens back as packed rows: the other direction of xqa_append, with
+ * the same arguments (k, v written, caches read). Sequence b's n_b rows receive its
+ * tokens ctx_b - n_b .. ctx_b - 1 (all of them when n_b = ctx_b), each value scale *
+ * code (scale * s * code) in 32 bits, rounded once to rows->dtype. Rows that
+ * xqa_append would not write are written as NaN; rows behind the last sequence are
+ * left as they are. */
+xqa_status_t xqa_gather(const uint8_t* k_cache, const uint8_t* v_cache, const int32_t* cu_seqlens,
+                        const int32_t* block_tables, const int32_t* context_lens, float k_scale,
+                        float v_scale, const float* k_scale_dev, const float* v_scale_dev,
+                        void* k, void* v, const xqa_rows_t* rows, int32_t* device_status,
+                        void* stream);
 
 /* Self-check of the device-side failure detection: launches one CTA whose
  * threads wait, through the same bounded mbarrier wait the attention kernel

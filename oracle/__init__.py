@@ -10,6 +10,7 @@ Modules:
 
 * :mod:`oracle.e5m2` — E5M2 code -> value, by the closed form of the format and
   by the fp16 bit-view route (the two are checked against each other).
+* :mod:`oracle.e2m1` — the 4-bit cache: encoding, slice layout, decode attention.
 * :mod:`oracle.attention` — masked softmax attention over the paged cache.
 * :mod:`oracle.plan` — the integer work partition the device planner must
   reproduce bit-exactly (pages per (sequence, kv head), equal page shares per

@@ -9,7 +9,8 @@ The names mirror the C ABI declared in ``include/xqa.h``:
 ``xqa_workspace_size``, ``xqa_decode``, ``xqa_plan``, ``xqa_attend_partial``,
 ``xqa_combine``, ``xqa_decode_device_scales``, ``xqa_dequant_e5m2``,
 ``xqa_dequant_e4m3``, ``xqa_read_status``, ``xqa_read_plan``, ``xqa_status_string``,
-``xqa_decode_static_workspace``, ``xqa_kernels_per_call``.
+``xqa_decode_static_workspace``, ``xqa_kernels_per_call``, ``xqa_append``,
+``xqa_gather``.
 """
 from __future__ import annotations
 
@@ -27,6 +28,7 @@ XQA_ERR_ALIGN = 3
 XQA_ERR_WORKSPACE = 4
 XQA_ERR_LAUNCH = 5
 XQA_ERR_DEVICE = 6
+XQA_ERR_VALUE = 7
 XQA_ERR_BAD_BLOCK_ID = 16
 XQA_ERR_CTX_TOO_LONG = 17
 XQA_ERR_DEVICE_TIMEOUT = 18
@@ -48,10 +50,15 @@ EXPORTED = (
     "xqa_dequant_e4m3",
     "xqa_selftest_wait_timeout",
     "xqa_kernels_per_call",
+    "xqa_append",
+    "xqa_gather",
 )
 
-KV_DTYPES = {"e5m2": 0, "e4m3": 1}
+KV_DTYPES = {"e5m2": 0, "e4m3": 1, "e2m1": 4}
 KV_LAYOUTS = {"hnd": 0, "nhd": 1}
+#: bytes of a (page, kv head) slice of a 4-bit cache (XQA_E2M1_SLICE_BYTES)
+E2M1_SLICE_BYTES = 1152
+ROW_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 
 
 class XqaShape(ctypes.Structure):
@@ -75,6 +82,16 @@ class XqaShape(ctypes.Structure):
     ]
 
 
+class XqaRows(ctypes.Structure):
+    """Mirror of ``xqa_rows_t``."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "num_kv_heads", "head_dim", "block_size", "max_blocks_per_seq", "num_blocks",
+        "num_rows", "kv_dtype", "kv_layout", "dtype")]
+    _fields_ += [(n, ctypes.c_int64) for n in (
+        "k_row_stride", "k_head_stride", "v_row_stride", "v_head_stride")]
+
+
 class XqaError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = int(code)
@@ -87,6 +104,7 @@ _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
 _SHAPE = ctypes.POINTER(XqaShape)
+_ROWS = ctypes.POINTER(XqaRows)
 _SIGS = {
     "xqa_workspace_size": [_SHAPE, ctypes.POINTER(_SZ)],
     "xqa_decode": [_P, _P, _P, _P, _P, _F, _F, _P, _SHAPE, _P, _SZ, _P],
@@ -102,6 +120,8 @@ _SIGS = {
     "xqa_dequant_e4m3": [_P, _SZ, _F, _P, _P, _P],
     "xqa_selftest_wait_timeout": [_P, ctypes.c_uint64, _P],
     "xqa_kernels_per_call": [_SHAPE, ctypes.POINTER(ctypes.c_int32)],
+    "xqa_append": [_P, _P, _P, _P, _P, _F, _F, _P, _P, _P, _P, _ROWS, _P, _P],
+    "xqa_gather": [_P, _P, _P, _P, _P, _F, _F, _P, _P, _P, _P, _ROWS, _P, _P],
 }
 
 
@@ -275,6 +295,123 @@ def xqa_dequant_e5m2(codes: torch.Tensor, scale: float = 1.0, with_f32: bool = T
 def xqa_dequant_e4m3(codes: torch.Tensor, scale: float = 1.0, with_f32: bool = True, stream=None):
     """Exact E4M3 dequantisation: (fp16 bit patterns as int16 tensor, fp32 scaled or None)."""
     return _dequant("xqa_dequant_e4m3", codes, scale, with_f32, stream)
+
+
+def _device_stream(stream, *tensors) -> int:
+    """Handle of ``stream`` (default: the current one). The library works on the
+    current device, so the stream and every tensor must be there."""
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    elif stream.device_index != torch.cuda.current_device():
+        raise ValueError("the stream belongs to another device than the current one")
+    for t in tensors:
+        if t is not None and t.device.index != stream.device_index:
+            raise ValueError(f"a tensor is on {t.device}, the current device is "
+                             f"cuda:{stream.device_index}")
+    return int(stream.cuda_stream)
+
+
+def _heads(t: torch.Tensor, name: str, dtype=None):
+    """Pointer, row stride and head stride of a [rows, heads, 128] view whose
+    last dim is contiguous (strides of dims of size 1 play no part)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in ROW_DTYPES or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must have dtype {dtype or 'float16 or bfloat16'}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [rows, heads, head_dim], got {tuple(t.shape)}")
+    n, h, d = t.shape
+    if t.numel() == 0:
+        return t.data_ptr(), h * d, d
+    rs, hs, es = t.stride()
+    hs = hs if h > 1 else d
+    rs = rs if n > 1 else h * d
+    if (d > 1 and es != 1) or rs <= 0 or hs <= 0:
+        raise ValueError(f"{name}: the last dim must be contiguous and no stride may be 0")
+    return t.data_ptr(), rs, hs
+
+
+def _cache_dims(cache: torch.Tensor, kv_dtype: str, kv_layout: str):
+    """(num_blocks, num_kv_heads, block_size) of a cache tensor."""
+    if kv_dtype == "e2m1":
+        if cache.dim() != 3 or cache.shape[2] != E2M1_SLICE_BYTES or kv_layout != "hnd":
+            raise ValueError("an e2m1 cache is [num_blocks, num_kv_heads, 1152], kv_layout 'hnd'")
+        return cache.shape[0], cache.shape[1], 16
+    if cache.dim() != 4:
+        raise ValueError("an FP8 cache has four dims")
+    nb, a, b, d = cache.shape
+    if d != 128:
+        raise ValueError("head_dim must be 128")
+    return (nb, a, b) if kv_layout == "hnd" else (nb, b, a)
+
+
+def _scale_args(k_scale, v_scale):
+    """(k value, v value, k pointer, v pointer): floats, or CUDA tensors of one element."""
+    val, ptr = [], []
+    for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        dev = isinstance(s, torch.Tensor)
+        if dev and s.numel() != 1:
+            raise ValueError(f"{name} must have one element")
+        ptr.append(_cuda(s, torch.float32, name) if dev else None)
+        val.append(0.0 if dev else float(s))
+    return (*val, *ptr)
+
+
+def _move_rows(fn_name, k, v, cu_seqlens, k_cache, v_cache, block_tables, context_lens, k_scale,
+               v_scale, kv_dtype, kv_layout, status, stream):
+    kp, krs, khs = _heads(k, "k")
+    vp, vrs, vhs = _heads(v, "v", k.dtype)
+    nb, hkv, bs = _cache_dims(k_cache, kv_dtype, kv_layout)
+    b = context_lens.numel()
+    if (v.shape != k.shape or v_cache.shape != k_cache.shape or k.shape[1] != hkv
+            or k.shape[2] != 128 or block_tables.dim() != 2 or block_tables.shape[0] != b
+            or cu_seqlens.numel() != b + 1):
+        raise ValueError("inconsistent rows / cache / block_tables / cu_seqlens shapes")
+    rows = XqaRows(b, hkv, 128, bs, block_tables.shape[1], nb, k.shape[0], KV_DTYPES[kv_dtype],
+                   KV_LAYOUTS[kv_layout], ROW_DTYPES[k.dtype], krs, khs, vrs, vhs)
+    caches = (_cuda(k_cache, torch.uint8, "k_cache"), _cuda(v_cache, torch.uint8, "v_cache"))
+    a, c = ((kp, vp), caches) if fn_name == "xqa_append" else (caches, (kp, vp))
+    _check(getattr(load_library(), fn_name)(
+        *a, _cuda(cu_seqlens, torch.int32, "cu_seqlens"),
+        _cuda(block_tables, torch.int32, "block_tables"),
+        _cuda(context_lens, torch.int32, "context_lens"), *_scale_args(k_scale, v_scale), *c,
+        ctypes.byref(rows), None if status is None else _cuda(status, torch.int32, "status"),
+        _device_stream(stream, k, v, k_cache, v_cache, cu_seqlens, block_tables, context_lens,
+                       status)), fn_name)
+
+
+def xqa_append(k, v, cu_seqlens, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale,
+               kv_dtype: str = "e5m2", kv_layout: str = "hnd", status=None, stream=None) -> None:
+    """Write new tokens' keys and values into the paged cache. k, v: fp16 or bf16
+    [rows, Hkv, 128] (views with strides are fine), packed by sequence through
+    cu_seqlens int32 [B+1]; context_lens int32 [B] counts the new tokens, which
+    go to each sequence's last positions. k_cache / v_cache: uint8, [NB, Hkv, 16,
+    128] ("hnd"), [NB, 16, Hkv, 128] ("nhd") or, for kv_dtype "e2m1", [NB, Hkv,
+    1152]. Scales are floats, or float32 CUDA tensors of one element. ``status``
+    (int32 CUDA tensor, optional) receives the first device-side error."""
+    _move_rows("xqa_append", k, v, cu_seqlens, k_cache, v_cache, block_tables, context_lens,
+               k_scale, v_scale, kv_dtype, kv_layout, status, stream)
+
+
+def xqa_gather(k_cache, v_cache, block_tables, context_lens, cu_seqlens, num_rows: int, k_scale,
+               v_scale, dtype=torch.float16, kv_dtype: str = "e5m2", kv_layout: str = "hnd",
+               k=None, v=None, status=None, stream=None):
+    """Read cached tokens back as packed rows of ``dtype``: sequence b's rows
+    cu_seqlens[b] .. cu_seqlens[b+1]-1 receive its last tokens (all of them when
+    there are context_lens[b] rows). Returns (k, v), [num_rows, Hkv, 128]; pass
+    ``k`` and ``v`` to write into existing tensors or views (rows behind the last
+    sequence are left as they are)."""
+    if (k is None) != (v is None):
+        raise ValueError("pass both k and v, or neither")
+    if k is None:
+        hkv = _cache_dims(k_cache, kv_dtype, kv_layout)[1]
+        k = torch.empty((int(num_rows), hkv, 128), dtype=dtype, device=k_cache.device)
+        v = torch.empty_like(k)
+    elif k.shape[0] != num_rows:
+        raise ValueError("k and v must have num_rows rows")
+    _move_rows("xqa_gather", k, v, cu_seqlens, k_cache, v_cache, block_tables, context_lens,
+               k_scale, v_scale, kv_dtype, kv_layout, status, stream)
+    return k, v
 
 
 def xqa_read_status(workspace: torch.Tensor, stream=None) -> int:

@@ -1,0 +1,294 @@
+// rows.cu — packed rows of keys and values into the paged cache (xqa_append)
+// and back (xqa_gather).
+//
+// Row r of k and v is one token (Hkv heads x 128 dims, fp16 or bf16). Sequence
+// b owns the rows cu_seqlens[b] .. cu_seqlens[b+1]-1, which are the last n_b of
+// its context_lens[b] tokens: row r sits at position
+// context_lens[b] - (cu_seqlens[b+1] - r).
+//
+//   append, FP8:   code = RNE(x / scale), saturated; NaN stays NaN
+//   append, E2M1:  per group of 16 dims s = E4M3(max |x| / scale / 6), then
+//                  code = E2M1(x / (scale * s)), ties to even, saturated at 6
+//   gather:        x = RNE16(scale * code) or RNE16(scale * (s * code)); the
+//                  product s * code is exact in 32 bits
+//
+// Both move bytes and compute little: 256 B on the 16-bit side of a (row, kv
+// head) and 128 B (72 B in 4 bits) on the cache side, for K and V each. Eight
+// threads take one (row, kv head): 16 dims each, so a thread's part of an FP8
+// row is one 16-byte access and of a 4-bit row exactly one scale group, and no
+// value crosses threads. A thread does K and V of its row together: the walk
+// from row to cache slot (a search in cu_seqlens, a length, a table entry) is
+// paid once, with four 16-byte loads in flight.
+#include <cuda_bf16.h>
+
+#include "xqa_device.cuh"
+#include "xqa_launch.h"
+
+namespace xqa {
+
+namespace {
+
+constexpr int kRowThreads = 128;
+constexpr int kLanesPerRow = 8;  // threads of one (row, kv head): 16 dims each
+
+// Quotients by one divisor t > 0: q0 = x r with r = RN(1/t), then one
+// correction q0 + (x - q0 t) r (Markstein, "Computation of elementary functions
+// on the IBM RISC System/6000 processor", 1990): exact whenever x / t is
+// representable, so ties are seen as ties. Quotients past 2^20 saturate in
+// every format and are left as they are (infinities and NaN among them).
+struct Divisor {
+  float t, r;
+  bool slow;  // 1 / t or the correction could leave the normal range
+};
+
+__device__ __forceinline__ Divisor make_divisor(float t) {
+  Divisor d;
+  d.t = t;
+  d.r = __frcp_rn(t);
+  d.slow = !(t >= 0x1p-60f && t <= 0x1p60f);
+  return d;
+}
+
+__device__ __forceinline__ float divide(float x, const Divisor& d) {
+  if (d.slow) return __fdiv_rn(x, d.t);
+  const float q0 = x * d.r;
+  const float q = __fmaf_rn(__fmaf_rn(-q0, d.t, x), d.r, q0);
+  return fabsf(q0) < 0x1p20f ? copysignf(q, x) : q0;  // the correction turns -0 into +0
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Two fp32 -> two codes, the first in the low bits.
+template <int kFmt>
+__device__ __forceinline__ uint32_t cvt_fp8x2(float lo, float hi) {
+  unsigned short d;
+  if (kFmt == XQA_KV_E5M2)
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// Eight fp32 -> eight E2M1 codes, the first in the low nibble.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float* x) {
+  uint32_t d;
+  asm("{\n\t.reg .b8 a, b, c, e;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 e, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, e};\n\t}"
+      : "=r"(d)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return d;
+}
+
+template <int kType>
+__device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float (&x)[16]) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (kType == XQA_F16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    } else {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
+template <int kType>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if (kType == XQA_F16) return pack_half2(lo, hi);
+  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// Where one (row, kv head) lives. `at` indexes 128-value rows of the cache:
+// FP8 (any layout): byte offset at * 128; E2M1: slice = at / 16, token = at % 16.
+struct RowPlace {
+  long long at;
+  int state;  // 1: in the cache, 0: not a row of any sequence, -1: bad
+};
+
+__device__ __forceinline__ RowPlace find_row(const RowsParams& p, int row, int head) {
+  RowPlace r{0, 0};
+  // largest b with cu[b] <= row
+  int lo = 0, hi = p.batch;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(p.cu_seqlens + mid) <= row) lo = mid;
+    else hi = mid - 1;
+  }
+  if (lo >= p.batch) return r;
+  const int beg = __ldg(p.cu_seqlens + lo), end = __ldg(p.cu_seqlens + lo + 1);
+  if (row < beg || row >= end) return r;
+  const int ctx = __ldg(p.context_lens + lo);
+  const long long pos = (long long)ctx - ((long long)end - row);
+  // every row of a sequence with a bad length is bad, not only those in front
+  // of its first token
+  if (ctx < 0 || (long long)ctx > (long long)p.max_blocks_per_seq * kBlockSize ||
+      (long long)ctx < (long long)end - beg) {
+    r.state = -1;
+    if (p.status && head == 0 && (threadIdx.x & (kLanesPerRow - 1)) == 0)
+      atomicCAS(p.status, XQA_OK, XQA_ERR_CTX_TOO_LONG);
+    return r;
+  }
+  const int id =
+      __ldg(p.block_tables + (size_t)lo * p.max_blocks_per_seq + (size_t)(pos / kBlockSize));
+  if (id < 0 || id >= p.num_blocks) {
+    r.state = -1;
+    if (p.status && head == 0 && (threadIdx.x & (kLanesPerRow - 1)) == 0)
+      atomicCAS(p.status, XQA_OK, XQA_ERR_BAD_BLOCK_ID);
+    return r;
+  }
+  const int slot = (int)(pos % kBlockSize);
+  r.at = p.kv_layout == XQA_LAYOUT_HND
+             ? ((long long)id * p.num_kv_heads + head) * kBlockSize + slot
+             : ((long long)id * kBlockSize + slot) * p.num_kv_heads + head;
+  r.state = 1;
+  return r;
+}
+
+template <int kFmt, int kType>
+__device__ __forceinline__ void store_codes(uint8_t* cache, long long at, int part, const uint4& a,
+                                            const uint4& b, float scale) {
+  float x[16];
+  unpack16<kType>(a, b, x);
+  if (kFmt != XQA_KV_E2M1) {
+    const Divisor d = make_divisor(scale);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = cvt_fp8x2<kFmt>(divide(x[4 * i], d), divide(x[4 * i + 1], d)) |
+             cvt_fp8x2<kFmt>(divide(x[4 * i + 2], d), divide(x[4 * i + 3], d)) << 16;
+    *reinterpret_cast<uint4*>(cache + at * kHeadDim + 16 * part) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(x[i]));
+    const uint32_t s8 = cvt_fp8x2<XQA_KV_E4M3>(__fdiv_rn(__fdiv_rn(amax, scale), 6.f), 0.f) & 0xffu;
+    const uint32_t sh = e4m3x2_to_f16x2(s8);
+    const float s = __low2float(*reinterpret_cast<const __half2*>(&sh));
+    const Divisor d = make_divisor(s * scale);
+    float q[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)  // a group whose s is 0 (or NaN) holds zeros
+      q[i] = d.t > 0.f ? divide(x[i], d) : copysignf(0.f, x[i]);
+    uint8_t* slice = cache + (at / kBlockSize) * kSliceBytes4;
+    const int token = (int)(at % kBlockSize);
+    *reinterpret_cast<uint2*>(slice + token * (kHeadDim / 2) + 8 * part) =
+        make_uint2(cvt_e2m1x8(q), cvt_e2m1x8(q + 8));
+    slice[kCodeBytes4 + token * (kHeadDim / kGroup4) + part] = (uint8_t)s8;
+  }
+}
+
+template <int kFmt, int kType>
+__device__ __forceinline__ void load_values(const uint8_t* cache, long long at, int part,
+                                            float scale, uint4 (&out)[2]) {
+  uint32_t h[8];  // the codes' values in pairs, fp16 (exact)
+  float s = 1.f;
+  if (kFmt != XQA_KV_E2M1) {
+    const uint4 c = __ldg(reinterpret_cast<const uint4*>(cache + at * kHeadDim + 16 * part));
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[2 * i] = KvConv<kFmt == XQA_KV_E2M1 ? XQA_KV_E4M3 : kFmt>::k_lo(w[i]);
+      h[2 * i + 1] = KvConv<kFmt == XQA_KV_E2M1 ? XQA_KV_E4M3 : kFmt>::k_hi(w[i]);
+    }
+  } else {
+    const uint8_t* slice = cache + (at / kBlockSize) * kSliceBytes4;
+    const int token = (int)(at % kBlockSize);
+    const uint2 c = __ldg(reinterpret_cast<const uint2*>(slice + token * (kHeadDim / 2) + 8 * part));
+    const uint32_t sh =
+        e4m3x2_to_f16x2(__ldg(slice + kCodeBytes4 + token * (kHeadDim / kGroup4) + part));
+    s = __low2float(*reinterpret_cast<const __half2*>(&sh));
+    e2m1x8_to_f16x2(c.x, h);
+    e2m1x8_to_f16x2(c.y, h + 4);
+  }
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    o[i] = pack16<kType>((f.x * s) * scale, (f.y * s) * scale);
+  }
+  out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+template <int kFmt, int kType, bool kAppend>
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsParams p) {
+  griddep_launch_dependents();
+  const long long u = ((long long)blockIdx.x * kRowThreads + threadIdx.x) / kLanesPerRow;
+  const int part = threadIdx.x % kLanesPerRow;
+  griddep_wait();  // every input may come from the kernels before this one
+  if (u >= (long long)p.num_rows * p.num_kv_heads) return;
+  const int row = (int)((uint32_t)u / (uint32_t)p.num_kv_heads);
+  const int head = (int)u - row * p.num_kv_heads;
+  const long long ko = row * p.k_row_stride + head * p.k_head_stride + 16 * part;
+  const long long vo = row * p.v_row_stride + head * p.v_head_stride + 16 * part;
+  uint4* k = reinterpret_cast<uint4*>(p.k + ko);
+  uint4* v = reinterpret_cast<uint4*>(p.v + vo);
+  const float k_scale = p.k_scale_ptr ? __ldg(p.k_scale_ptr) : p.k_scale;
+  const float v_scale = p.v_scale_ptr ? __ldg(p.v_scale_ptr) : p.v_scale;
+  if (kAppend) {
+    // in flight while the slot is looked up; rows of no sequence are readable too
+    const uint4 k0 = __ldg(k), k1 = __ldg(k + 1), v0 = __ldg(v), v1 = __ldg(v + 1);
+    const RowPlace r = find_row(p, row, head);
+    if (r.state != 1) return;
+    store_codes<kFmt, kType>(p.k_cache, r.at, part, k0, k1, k_scale);
+    store_codes<kFmt, kType>(p.v_cache, r.at, part, v0, v1, v_scale);
+  } else {
+    const RowPlace r = find_row(p, row, head);
+    if (r.state == 0) return;
+    uint4 a[2], b[2];
+    if (r.state > 0) {
+      load_values<kFmt, kType>(p.k_cache, r.at, part, k_scale, a);
+      load_values<kFmt, kType>(p.v_cache, r.at, part, v_scale, b);
+    } else {
+      const uint32_t nan = kType == XQA_F16 ? 0x7fff7fffu : 0x7fc07fc0u;
+      a[0] = a[1] = b[0] = b[1] = make_uint4(nan, nan, nan, nan);
+    }
+    k[0] = a[0];
+    k[1] = a[1];
+    v[0] = b[0];
+    v[1] = b[1];
+  }
+}
+
+template <bool kAppend, int kType>
+cudaError_t launch(int fmt, const cudaLaunchConfig_t& cfg, const RowsParams& p) {
+  switch (fmt) {
+    case XQA_KV_E5M2: return cudaLaunchKernelEx(&cfg, rows_kernel<XQA_KV_E5M2, kType, kAppend>, p);
+    case XQA_KV_E4M3: return cudaLaunchKernelEx(&cfg, rows_kernel<XQA_KV_E4M3, kType, kAppend>, p);
+    default: return cudaLaunchKernelEx(&cfg, rows_kernel<XQA_KV_E2M1, kType, kAppend>, p);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rows(bool append, const RowsParams& p, cudaStream_t stream) {
+  const long long threads = (long long)p.num_rows * p.num_kv_heads * kLanesPerRow;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((threads + kRowThreads - 1) / kRowThreads));
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (append)
+    return p.dtype == XQA_F16 ? launch<true, XQA_F16>(p.kv_dtype, cfg, p)
+                              : launch<true, XQA_BF16>(p.kv_dtype, cfg, p);
+  return p.dtype == XQA_F16 ? launch<false, XQA_F16>(p.kv_dtype, cfg, p)
+                            : launch<false, XQA_BF16>(p.kv_dtype, cfg, p);
+}
+
+}  // namespace xqa

@@ -277,6 +277,74 @@ xqa_status_t combine_impl(const int32_t* context_lens, float v_scale, const floa
   return e == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
 }
 
+// Row / head stride of one side of xqa_append / xqa_gather (0: contiguous).
+bool row_strides(const xqa_rows_t& s, int64_t row, int64_t head, bool written, long long* rs,
+                 long long* hs) {
+  *hs = head != 0 ? head : kHeadDim;
+  *rs = row != 0 ? row : (long long)s.num_kv_heads * kHeadDim;
+  if (*hs < 0 || *rs < 0 || *hs % 8 != 0 || *rs % 8 != 0) return false;
+  if (*rs >= (1ll << 40) || *hs >= (1ll << 40)) return false;  // 64-bit offsets of 2^31 rows
+  if (!written) return true;
+  // heads and rows that are written must not overlap one another
+  if ((s.num_kv_heads > 1 && *hs < kHeadDim) || (s.num_rows > 1 && *rs < kHeadDim)) return false;
+  return *rs >= (s.num_kv_heads - 1) * *hs + kHeadDim ||
+         *hs >= (long long)(s.num_rows - 1) * *rs + kHeadDim;
+}
+
+xqa_status_t rows_impl(bool append, void* k, void* v, const int32_t* cu_seqlens,
+                       const int32_t* block_tables, const int32_t* context_lens, float k_scale,
+                       float v_scale, const float* k_scale_dev, const float* v_scale_dev,
+                       uint8_t* k_cache, uint8_t* v_cache, const xqa_rows_t* rows,
+                       int32_t* device_status, void* stream) {
+  if (!rows) return XQA_ERR_NULL;
+  const xqa_rows_t& s = *rows;
+  if (s.head_dim != kHeadDim || s.block_size != kBlockSize) return XQA_ERR_SHAPE;
+  if (s.batch < 1 || s.num_kv_heads < 1 || s.max_blocks_per_seq < 1 || s.num_blocks < 1 ||
+      s.num_rows < 0 || s.batch == 0x7fffffff)
+    return XQA_ERR_SHAPE;
+  if (s.kv_dtype != XQA_KV_E5M2 && s.kv_dtype != XQA_KV_E4M3 && s.kv_dtype != XQA_KV_E2M1)
+    return XQA_ERR_SHAPE;
+  if (s.kv_layout != XQA_LAYOUT_HND &&
+      (s.kv_layout != XQA_LAYOUT_NHD || s.kv_dtype == XQA_KV_E2M1))
+    return XQA_ERR_SHAPE;
+  if (s.dtype != XQA_F16 && s.dtype != XQA_BF16) return XQA_ERR_SHAPE;
+  if ((long long)s.num_blocks * s.num_kv_heads >= (1ll << 31) / kBlockSize) return XQA_ERR_SHAPE;
+  if ((long long)s.num_rows * s.num_kv_heads >= (1ll << 31)) return XQA_ERR_SHAPE;
+  xqa::RowsParams p;
+  if (!row_strides(s, s.k_row_stride, s.k_head_stride, !append, &p.k_row_stride,
+                   &p.k_head_stride) ||
+      !row_strides(s, s.v_row_stride, s.v_head_stride, !append, &p.v_row_stride,
+                   &p.v_head_stride))
+    return XQA_ERR_SHAPE;
+  if (s.num_rows == 0) return XQA_OK;
+  if (!k || !v || !cu_seqlens || !block_tables || !context_lens || !k_cache || !v_cache)
+    return XQA_ERR_NULL;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache))
+    return XQA_ERR_ALIGN;
+  p.k = reinterpret_cast<uint16_t*>(k);
+  p.v = reinterpret_cast<uint16_t*>(v);
+  p.cu_seqlens = cu_seqlens;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.status = device_status;
+  p.batch = s.batch;
+  p.num_kv_heads = s.num_kv_heads;
+  p.max_blocks_per_seq = s.max_blocks_per_seq;
+  p.num_blocks = s.num_blocks;
+  p.num_rows = s.num_rows;
+  p.kv_dtype = s.kv_dtype;
+  p.kv_layout = s.kv_layout;
+  p.dtype = s.dtype;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.k_scale_ptr = k_scale_dev;
+  p.v_scale_ptr = v_scale_dev;
+  const cudaError_t e = xqa::launch_rows(append, p, (cudaStream_t)stream);
+  return e == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
+}
+
 }  // namespace
 
 extern "C" {
@@ -361,6 +429,29 @@ xqa_status_t xqa_dequant_e4m3(const uint8_t* in, size_t n, float scale, uint16_t
   return e == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
 }
 
+xqa_status_t xqa_append(const void* k, const void* v, const int32_t* cu_seqlens,
+                        const int32_t* block_tables, const int32_t* context_lens, float k_scale,
+                        float v_scale, const float* k_scale_dev, const float* v_scale_dev,
+                        uint8_t* k_cache, uint8_t* v_cache, const xqa_rows_t* rows,
+                        int32_t* device_status, void* stream) {
+  if ((!k_scale_dev && !(k_scale > 0.f && isfinite(k_scale))) ||
+      (!v_scale_dev && !(v_scale > 0.f && isfinite(v_scale))))
+    return XQA_ERR_VALUE;
+  return rows_impl(true, const_cast<void*>(k), const_cast<void*>(v), cu_seqlens, block_tables,
+                   context_lens, k_scale, v_scale, k_scale_dev, v_scale_dev, k_cache, v_cache,
+                   rows, device_status, stream);
+}
+
+xqa_status_t xqa_gather(const uint8_t* k_cache, const uint8_t* v_cache, const int32_t* cu_seqlens,
+                        const int32_t* block_tables, const int32_t* context_lens, float k_scale,
+                        float v_scale, const float* k_scale_dev, const float* v_scale_dev,
+                        void* k, void* v, const xqa_rows_t* rows, int32_t* device_status,
+                        void* stream) {
+  return rows_impl(false, k, v, cu_seqlens, block_tables, context_lens, k_scale, v_scale,
+                   k_scale_dev, v_scale_dev, const_cast<uint8_t*>(k_cache),
+                   const_cast<uint8_t*>(v_cache), rows, device_status, stream);
+}
+
 xqa_status_t xqa_selftest_wait_timeout(int32_t* device_status, uint64_t budget_ns,
                                        void* stream) {
   if (!device_status) return XQA_ERR_NULL;
@@ -425,6 +516,7 @@ const char* xqa_status_string(xqa_status_t status) {
     case XQA_ERR_WORKSPACE: return "workspace smaller than xqa_workspace_size";
     case XQA_ERR_LAUNCH: return "a CUDA call or kernel launch failed";
     case XQA_ERR_DEVICE: return "no usable CUDA device";
+    case XQA_ERR_VALUE: return "a scale is not finite or not above 0";
     case XQA_ERR_BAD_BLOCK_ID: return "device: block table entry outside [0, num_blocks)";
     case XQA_ERR_CTX_TOO_LONG: return "device: context length < 0 or > max_blocks_per_seq*16";
     case XQA_ERR_DEVICE_TIMEOUT: return "device: pipeline wait exceeded its time budget";

@@ -44,6 +44,13 @@ struct PartialGeom {
                                kSegCache * 4 /* cost prefix */;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
+// 4-bit cache: a (page, kv head) slice is 16 tokens x 64 code bytes (dim 2i in
+// the low nibble of byte i), then 16 tokens x 8 E4M3 scales, one for each group
+// of 16 dims.
+constexpr int kGroup4 = 16;
+constexpr int kCodeBytes4 = kBlockSize * kHeadDim / 2;
+constexpr int kSliceBytes4 = kCodeBytes4 + kBlockSize * (kHeadDim / kGroup4);
+static_assert(kSliceBytes4 == XQA_E2M1_SLICE_BYTES, "slice size in the header");
 constexpr int kDefaultMinPagesPerCta = 16;
 // Split rule cost line: every non-empty segment costs kSegCost page units on
 // top of its pages (a segment switch inside a CTA, and the split-piece merge
@@ -397,6 +404,18 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair16) {
   uint32_t d;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<unsigned short>(pair16)));
   return d;
+}
+
+// Eight E2M1 codes of one word -> four half2 of neighbouring dims (exact).
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t* o) {
+  asm("{\n\t.reg .b8 a, b, c, e;\n\t"
+      "mov.b32 {a, b, c, e}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, e;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
 }
 
 // Per-format conversions in the two shapes the attention kernel needs:

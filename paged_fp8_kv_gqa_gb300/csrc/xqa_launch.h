@@ -45,6 +45,25 @@ struct CombineParams {
   const float* v_scale_ptr;  // optional device scalar (overrides v_scale)
 };
 
+// xqa_append (k, v read, caches written) and xqa_gather (the other way round).
+struct RowsParams {
+  uint16_t* k;  // [num_rows, Hkv, 128] 16-bit values, strides in elements
+  uint16_t* v;
+  const int32_t* cu_seqlens;  // [batch + 1]
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  int32_t* status;  // optional: first error of the call
+  int batch, num_kv_heads, max_blocks_per_seq, num_blocks, num_rows;
+  int kv_dtype, kv_layout, dtype;
+  long long k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+  float k_scale, v_scale;
+  const float* k_scale_ptr;  // optional device scalars (override the values)
+  const float* v_scale_ptr;
+};
+
+cudaError_t launch_rows(bool append, const RowsParams& p, cudaStream_t stream);
 cudaError_t launch_plan(const int32_t* context_lens, int batch, int num_kv_heads,
                         int max_blocks_per_seq, int n_max, int min_pages_per_cta,
                         int32_t* workspace, cudaStream_t stream);
