@@ -59,8 +59,9 @@ typedef enum xqa_status {
   XQA_ERR_BAD_BLOCK_ID = 16,    /* block_tables entry outside [0, num_blocks) */
   XQA_ERR_CTX_TOO_LONG = 17,    /* context length < 0 or > MBS * block_size */
   XQA_ERR_DEVICE_TIMEOUT = 18,  /* a pipeline or merge-ticket wait exceeded its time budget */
-  XQA_ERR_DRAIN_TIMEOUT = 19    /* after a timeout, a copy was still in flight when its
+  XQA_ERR_DRAIN_TIMEOUT = 19,   /* after a timeout, a copy was still in flight when its
                                    CTA exited: the device state is not to be trusted */
+  XQA_ERR_BAD_OFFSETS = 20      /* cu_seqlens descending, negative or past the rows */
 } xqa_status_t;
 
 /* KV cache code formats (xqa_shape_t.kv_dtype). */
@@ -275,6 +276,60 @@ xqa_status_t xqa_gather(const uint8_t* k_cache, const uint8_t* v_cache, const in
                         float v_scale, const float* k_scale_dev, const float* v_scale_dev,
                         void* k, void* v, const xqa_rows_t* rows, int32_t* device_status,
                         void* stream);
+
+/* Problem dimensions of xqa_prefill. Strides are in elements, multiples of 8 (16
+ * bytes); 0 selects the contiguous value (heads * 128 between rows, 128 between
+ * heads), so q, k and v may be views of one projection. */
+typedef struct xqa_prefill_shape {
+  int32_t batch;        /* B: sequences, >= 1 */
+  int32_t num_q_heads;  /* Hq, a multiple of Hkv; G = Hq / Hkv <= 128 */
+  int32_t num_kv_heads; /* Hkv */
+  int32_t head_dim;     /* D = 128 */
+  int32_t total_q;      /* rows of q and out (>= 0) */
+  int32_t total_k;      /* rows of k and v (>= 0) */
+  int32_t dtype;        /* XQA_F16 or XQA_BF16: q, k, v and out */
+  int32_t causal;       /* 1: query i of a sequence sees keys 0 .. len_k - len_q + i
+                           (the last query sees every key); 0: every key */
+  float sm_scale;       /* softmax scale; <= 0 selects 1/sqrt(D) */
+  int32_t max_ctas;     /* upper bound on CTAs; 0 = SM count */
+  int64_t q_row_stride, q_head_stride;
+  int64_t k_row_stride, k_head_stride;
+  int64_t v_row_stride, v_head_stride;
+  int64_t out_row_stride, out_head_stride;
+} xqa_prefill_shape_t;
+
+/* Bytes of device workspace xqa_prefill needs for `shape`. Host only. */
+xqa_status_t xqa_prefill_workspace_size(const xqa_prefill_shape_t* shape, size_t* bytes);
+
+/* Attention of whole prompts, packed by sequence.
+ *
+ *   q             device, shape->dtype [total_q, Hq, 128] (strided), 16-byte aligned
+ *   k, v          device, [total_k, Hkv, 128] (strided), 16-byte aligned
+ *   cu_seqlens_q  device, int32 [B+1], ascending: sequence b's rows of q and out
+ *   cu_seqlens_k  device, int32 [B+1], ascending: its rows of k and v (as many as of q
+ *                 for a whole prompt; more when the prompt goes on after cached
+ *                 tokens; fewer is allowed)
+ *   out           device, [total_q, Hq, 128] (strided), 16-byte aligned
+ *   lse           device, fp32 [total_q, Hq] contiguous, or NULL: the natural
+ *                 logarithm of the row's sum of exponentials
+ *   workspace     device, >= xqa_prefill_workspace_size bytes, 256-byte aligned,
+ *                 zero-filled once before its first use; every completed call leaves
+ *                 it ready for the next. A decode workspace of at least that size may
+ *                 serve both. Concurrent calls must not share one
+ *
+ * out[i, h] = sum_j softmax_j(sm_scale * <q[i, h], k[j, h / G]>) * v[j, h / G] over the
+ * keys that query i sees. A row that sees none is zero, its lse -inf. Products
+ * accumulate in 32 bits, the softmax is in 32 bits, its weights are rounded to
+ * shape->dtype for the second product, out is rounded once. What a query does not see
+ * does not reach its row, infinities and NaN included. Rows of q and out behind
+ * cu_seqlens_q[B] are left alone. A sequence whose offsets are bad
+ * (XQA_ERR_BAD_OFFSETS, see xqa_read_status) is skipped; if only its key offsets are,
+ * its rows are NaN. One kernel, no host synchronisation; may be captured into a CUDA
+ * graph. */
+xqa_status_t xqa_prefill(const void* q, const void* k, const void* v, const int32_t* cu_seqlens_q,
+                         const int32_t* cu_seqlens_k, void* out, float* lse,
+                         const xqa_prefill_shape_t* shape, void* workspace,
+                         size_t workspace_bytes, void* stream);
 
 /* Self-check of the device-side failure detection: launches one CTA whose
  * threads wait, through the same bounded mbarrier wait the attention kernel

@@ -10,7 +10,7 @@ The names mirror the C ABI declared in ``include/xqa.h``:
 ``xqa_combine``, ``xqa_decode_device_scales``, ``xqa_dequant_e5m2``,
 ``xqa_dequant_e4m3``, ``xqa_read_status``, ``xqa_read_plan``, ``xqa_status_string``,
 ``xqa_decode_static_workspace``, ``xqa_kernels_per_call``, ``xqa_append``,
-``xqa_gather``.
+``xqa_gather``, ``xqa_prefill``, ``xqa_prefill_workspace_size``.
 """
 from __future__ import annotations
 
@@ -33,6 +33,7 @@ XQA_ERR_BAD_BLOCK_ID = 16
 XQA_ERR_CTX_TOO_LONG = 17
 XQA_ERR_DEVICE_TIMEOUT = 18
 XQA_ERR_DRAIN_TIMEOUT = 19
+XQA_ERR_BAD_OFFSETS = 20
 
 #: C symbols the library exports (kept in step with include/xqa.h).
 EXPORTED = (
@@ -52,6 +53,8 @@ EXPORTED = (
     "xqa_kernels_per_call",
     "xqa_append",
     "xqa_gather",
+    "xqa_prefill",
+    "xqa_prefill_workspace_size",
 )
 
 KV_DTYPES = {"e5m2": 0, "e4m3": 1, "e2m1": 4}
@@ -92,6 +95,18 @@ class XqaRows(ctypes.Structure):
         "k_row_stride", "k_head_stride", "v_row_stride", "v_head_stride")]
 
 
+class XqaPrefillShape(ctypes.Structure):
+    """Mirror of ``xqa_prefill_shape_t``."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "num_q_heads", "num_kv_heads", "head_dim", "total_q", "total_k", "dtype",
+        "causal")]
+    _fields_ += [("sm_scale", ctypes.c_float), ("max_ctas", ctypes.c_int32)]
+    _fields_ += [(n, ctypes.c_int64) for n in (
+        "q_row_stride", "q_head_stride", "k_row_stride", "k_head_stride", "v_row_stride",
+        "v_head_stride", "out_row_stride", "out_head_stride")]
+
+
 class XqaError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = int(code)
@@ -105,6 +120,7 @@ _SZ = ctypes.c_size_t
 _F = ctypes.c_float
 _SHAPE = ctypes.POINTER(XqaShape)
 _ROWS = ctypes.POINTER(XqaRows)
+_PREFILL = ctypes.POINTER(XqaPrefillShape)
 _SIGS = {
     "xqa_workspace_size": [_SHAPE, ctypes.POINTER(_SZ)],
     "xqa_decode": [_P, _P, _P, _P, _P, _F, _F, _P, _SHAPE, _P, _SZ, _P],
@@ -120,6 +136,8 @@ _SIGS = {
     "xqa_dequant_e4m3": [_P, _SZ, _F, _P, _P, _P],
     "xqa_selftest_wait_timeout": [_P, ctypes.c_uint64, _P],
     "xqa_kernels_per_call": [_SHAPE, ctypes.POINTER(ctypes.c_int32)],
+    "xqa_prefill": [_P, _P, _P, _P, _P, _P, _P, _PREFILL, _P, _SZ, _P],
+    "xqa_prefill_workspace_size": [_PREFILL, ctypes.POINTER(_SZ)],
     "xqa_append": [_P, _P, _P, _P, _P, _F, _F, _P, _P, _P, _P, _ROWS, _P, _P],
     "xqa_gather": [_P, _P, _P, _P, _P, _F, _F, _P, _P, _P, _P, _ROWS, _P, _P],
 }
@@ -412,6 +430,87 @@ def xqa_gather(k_cache, v_cache, block_tables, context_lens, cu_seqlens, num_row
     _move_rows("xqa_gather", k, v, cu_seqlens, k_cache, v_cache, block_tables, context_lens,
                k_scale, v_scale, kv_dtype, kv_layout, status, stream)
     return k, v
+
+
+def make_prefill_shape(q, k, v, cu_seqlens_q, causal: bool = True, sm_scale: float = 0.0,
+                       max_ctas: int = 0, out=None) -> XqaPrefillShape:
+    """Shape descriptor of xqa_prefill from q [total_q, Hq, 128], k and v
+    [total_k, Hkv, 128] (fp16 or bf16; views whose last dim is contiguous are
+    fine) and cu_seqlens_q [B+1]. It holds for every call with tensors of these
+    shapes, types and strides (out: contiguous unless given)."""
+    _, qr, qh = _heads(q, "q")
+    _, kr, kh = _heads(k, "k", q.dtype)
+    _, vr, vh = _heads(v, "v", q.dtype)
+    if k.shape != v.shape or k.shape[2] != q.shape[2]:
+        raise ValueError("inconsistent q / k / v shapes")
+    orow, oh = (0, 0) if out is None else _heads(out, "out", q.dtype)[1:]
+    return XqaPrefillShape(cu_seqlens_q.numel() - 1, q.shape[1], k.shape[1], q.shape[2],
+                           q.shape[0], k.shape[0], ROW_DTYPES[q.dtype], int(bool(causal)),
+                           float(sm_scale), int(max_ctas), qr, qh, kr, kh, vr, vh, orow, oh)
+
+
+def xqa_prefill_workspace_size(shape: XqaPrefillShape) -> int:
+    n = _SZ(0)
+    _check(load_library().xqa_prefill_workspace_size(ctypes.byref(shape), ctypes.byref(n)),
+           "xqa_prefill_workspace_size")
+    return int(n.value)
+
+
+def alloc_prefill_workspace(shape: XqaPrefillShape, device=None) -> torch.Tensor:
+    """A zero-filled uint8 device buffer of xqa_prefill_workspace_size bytes;
+    every call leaves it ready for the next."""
+    return torch.zeros(xqa_prefill_workspace_size(shape), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def xqa_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=None, lse=None, workspace=None,
+                shape: XqaPrefillShape | None = None, stream=None, causal: bool = True,
+                sm_scale: float = 0.0, max_ctas: int = 0):
+    """Attention of whole prompts, packed by sequence: q fp16 or bf16 [total_q,
+    Hq, 128], k and v [total_k, Hkv, 128], cu_seqlens_q / cu_seqlens_k int32
+    [B+1] (keys default to the queries' offsets). With ``causal`` the last query
+    of a sequence sees all its keys and each one before it one key less. ``lse``
+    (fp32 [total_q, Hq], optional) receives the log-sum-exp. Returns ``out``;
+    rows that see nothing are zero, rows behind the last sequence are not
+    written."""
+    made = shape is None
+    if made:
+        shape = make_prefill_shape(q, k, v, cu_seqlens_q, causal, sm_scale, max_ctas, out)
+    if cu_seqlens_k is None:
+        cu_seqlens_k = cu_seqlens_q
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if workspace is None:
+        workspace = alloc_prefill_workspace(shape, q.device)
+    qp, qr, qh = _heads(q, "q")
+    kp, kr, kh = _heads(k, "k", q.dtype)
+    vp, vr, vh = _heads(v, "v", q.dtype)
+    op, orow, oh = _heads(out, "out", q.dtype)
+    s = shape
+    if not made and (
+            (s.total_q, s.num_q_heads, s.head_dim) != q.shape or q.dtype not in ROW_DTYPES
+            or ROW_DTYPES[q.dtype] != s.dtype
+            or (s.q_row_stride, s.q_head_stride, s.k_row_stride, s.k_head_stride, s.v_row_stride,
+                s.v_head_stride) != (qr, qh, kr, kh, vr, vh)):
+        raise ValueError("q, k, v do not match the shape descriptor")
+    if ((s.total_k, s.num_kv_heads, s.head_dim) != k.shape or k.shape != v.shape
+            or out.shape != q.shape
+            or (s.out_row_stride or s.num_q_heads * 128, s.out_head_stride or 128) != (orow, oh)):
+        raise ValueError("k, v or out do not match the shape descriptor")
+    if cu_seqlens_q.numel() != s.batch + 1 or cu_seqlens_k.numel() != s.batch + 1:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must have batch + 1 entries")
+    lp = None
+    if lse is not None:
+        lp = _cuda(lse, torch.float32, "lse")
+        if lse.shape != q.shape[:2]:
+            raise ValueError("lse must be [total_q, num_q_heads]")
+    _check(load_library().xqa_prefill(
+        qp, kp, vp, _cuda(cu_seqlens_q, torch.int32, "cu_seqlens_q"),
+        _cuda(cu_seqlens_k, torch.int32, "cu_seqlens_k"), op, lp, ctypes.byref(shape),
+        _cuda(workspace, torch.uint8, "workspace"), workspace.numel(),
+        _device_stream(stream, q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, workspace)),
+        "xqa_prefill")
+    return out
 
 
 def xqa_read_status(workspace: torch.Tensor, stream=None) -> int:

@@ -1,0 +1,805 @@
+// prefill.cu — attention over whole prompts, packed by sequence (xqa_prefill).
+//
+//   out[i, h] = sum_j softmax_j(sm_scale <q[i, h], k[j, h / G]>) v[j, h / G],
+//   j < len_k, and for causal calls j <= len_k - len_q + i (i, j counted within
+//   the sequence); a row that sees nothing is zero.
+//
+// One persistent CTA per SM works through units of 2 x 128 rows: the G query
+// heads of one kv head for 2 x T consecutive tokens of one sequence, T =
+// floor(128 / G), row = token * G + head. So a K or V tile is read once for all
+// heads of its group, a short prompt still fills its rows, and the diagonal is
+// cut in steps of 2 T tokens. A unit walks the 128-key tiles it can see from the
+// last (the diagonal) to the first, with the usual running maximum and sum:
+//
+//   S = Q K^T             tcgen05, 128 x 128 x 128, fp32 in TMEM
+//   P = 2^(S c - m)       softmax warps: TMEM -> registers -> TMEM, 16 bit
+//   O = O + P V           tcgen05, P from TMEM, V from shared memory
+//
+// What bounds it: per 128 x 128 tile the tensor core needs 2 x 512 cycles (8192
+// flop per cycle and SM), the exponentials 512 cycles (32 per cycle and SM), so
+// the two row tiles of a unit are worked in turn: while one is in the tensor
+// core, the other's softmax runs. The running maximum only moves when a logit
+// exceeds it by more than 8 (log2), so O is rescaled seldom (P <= 2^8 stays
+// exact enough: its rounding is relative); O and the row sum l stay in 32 bits,
+// l sums the unrounded P. P is rounded to the inputs' type because a tcgen05
+// product has both operands in 16 bits: 2^-9 (bf16) or 2^-12 (fp16) of each
+// weight, the size of the rounding of out itself.
+//
+// Warps: 0-3 and 4-7 softmax of row tile 0 and 1 (a thread owns a row), 8-11
+// epilogue, 12 tensor core, 13 units and TMA loads, 14-15 the masked V tiles
+// (below). TMEM: S0, S1 (P over them), O0, O1: 4 x 128 columns.
+//
+// Hidden values do not leak: a weight of exactly 0 times an infinity or NaN
+// would be NaN, so in V tiles that some row of the unit sees in part, rows past
+// the sequence are zeroed in shared memory, and values that are not finite are
+// zeroed and their rows' sums patched in the epilogue (only for tokens that see
+// them). A hidden key only makes its own column of S, which is replaced.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "xqa_device.cuh"
+#include "xqa_launch.h"
+
+namespace xqa {
+
+namespace {
+
+constexpr int kTile = 128;                       // rows of a row tile, keys of a KV tile
+constexpr int kHalfBytes = kTile * 128;          // 128 rows x 64 dims of 16 bits
+constexpr int kTileBytes = 2 * kHalfBytes;       // a Q, K or V tile
+constexpr int kKvStages = 5;
+constexpr int kUnitSlots = 3;
+constexpr int kPrefillThreads = 512;
+constexpr float kNoRowMax = -1e30f;              // as in the decode kernel
+constexpr float kLazyMax = 8.0f;                 // log2 units
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kUnitReaders = 15;  // 8 softmax, 4 epilogue, 1 tensor-core, 2 V warps
+
+// One unit of work, written by the loading warp.
+struct Unit {
+  int end;       // 1: no more units
+  int bad;       // 1: the sequence's key range is invalid: NaN rows
+  int q_row;     // first token's row in q and out
+  int tokens;    // tokens of the unit (1 .. 2 T)
+  int head;      // kv head
+  int k_row;     // first key's row in k and v
+  int len_k;
+  int vis0;      // keys the unit's first token sees (causal: one more per token)
+  int n[2];      // KV tiles row tile 0 / 1 sees (0: no tokens, or nothing to see)
+  int hidden;    // first key hidden from some token (tiles past it are masked)
+};
+
+struct Shared {
+  uint64_t kv_full[kKvStages], kv_empty[kKvStages];
+  uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
+  uint64_t q_full, q_empty;
+  uint64_t v_clean[kKvStages];   // the stage's V tile may be used (masked tiles only)
+  uint64_t s_full[2], p_full[2]; // S ready / P written
+  uint64_t o_full[2], o_free[2]; // O complete / read by the epilogue
+  uint64_t stat_full[2], stat_free[2];
+  uint64_t drain;
+  Unit unit[kUnitSlots];
+  int not_finite[kUnitSlots];    // the unit's masked V tiles held infinities or NaN
+  int abort_flag, status;
+  uint32_t tmem;
+};
+
+constexpr int kSmemTiles = (2 + kKvStages) * kTileBytes;
+constexpr int kSmemStats = 2 * kTile * 2 * 4;  // (m, l) of every row
+constexpr int kPrefillSmem = kSmemTiles + kSmemStats + 1024;
+static_assert(sizeof(Shared) <= 1024, "shared state");
+static_assert(kPrefillSmem <= 227 * 1024, "shared memory budget");
+
+// ---- tcgen05 ----
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, int cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_addr(dst)),
+               "r"(cols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t addr, int cols) {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+}
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_addr(bar))
+      : "memory");
+}
+// D (+)= A B, both operands in shared memory
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((int)add)
+      : "memory");
+}
+// D (+)= A B, A in TMEM
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((int)add)
+      : "memory");
+}
+
+#define XQA_R8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), \
+    "=r"(a[i + 4]), "=r"(a[i + 5]), "=r"(a[i + 6]), "=r"(a[i + 7])
+#define XQA_I8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), \
+    "r"(a[i + 5]), "r"(a[i + 6]), "r"(a[i + 7])
+#define XQA_LIST32                                                                            \
+  "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, " \
+  "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}"
+
+// 32 columns of this thread's TMEM lane (its row)
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 " XQA_LIST32 ", [%32];"
+               : XQA_R8(r, 0), XQA_R8(r, 8), XQA_R8(r, 16), XQA_R8(r, 24)
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], " XQA_LIST32 ";" ::XQA_I8(r, 0),
+      XQA_I8(r, 8), XQA_I8(r, 16), XQA_I8(r, 24), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Shared-memory matrix descriptors, 128-byte swizzle (layout 2), version 1.
+// K-major (Q, K): rows of 128 bytes, 8-row groups 1024 bytes apart.
+// MN-major (V, whose dims are contiguous): 64 dims x 8 tokens per group, groups
+// of 8 tokens 1024 bytes apart, the second 64 dims kHalfBytes on.
+__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)(kHalfBytes >> 4) << 16 |
+         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// Instruction descriptor: fp32 accumulator, fp16 or bf16 operands, M = N = 128.
+template <int kType>
+__device__ __forceinline__ constexpr uint32_t instr_desc(bool b_mn_major) {
+  return 1u << 4 | (uint32_t)(kType == XQA_BF16) << 7 | (uint32_t)(kType == XQA_BF16) << 10 |
+         (uint32_t)b_mn_major << 16 | (uint32_t)(kTile >> 3) << 17 | (uint32_t)(kTile >> 4) << 24;
+}
+
+template <int kType>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (kType == XQA_F16) return pack_half2(lo, hi);
+  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
+                                            int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_kv(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
+                                            int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// What every warp role works on.
+struct Ctx {
+  const PrefillParams& p;
+  Shared& sh;
+  uint8_t* tiles;  // Q0, Q1, then the KV ring
+  float* stats;    // [2][128][2]
+  uint32_t tmem;
+
+  __device__ __forceinline__ uint8_t* kv(int stage) const { return tiles + (2 + stage) * kTileBytes; }
+
+  // Warp-uniform bounded wait; false ends the role (the CTA is aborted).
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
+    const bool ok = mbar_wait_bounded(bar, parity, &sh.abort_flag);
+    if (__all_sync(kAll, ok)) return true;
+    if ((threadIdx.x & 31) == 0) {
+      *(volatile int*)&sh.abort_flag = 1;
+      record_status(&sh.status, XQA_ERR_DEVICE_TIMEOUT);
+    }
+    __syncwarp();
+    return false;
+  }
+  __device__ __forceinline__ bool get_unit(int i, Unit& u) const {
+    const int slot = i % kUnitSlots;
+    if (!wait(&sh.unit_full[slot], (i / kUnitSlots) & 1)) return false;
+    u = sh.unit[slot];
+    return !u.end;
+  }
+  // One arrival of this warp, after all its lanes are done.
+  __device__ __forceinline__ void arrive(uint64_t* bar) const {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  }
+  __device__ __forceinline__ void free_unit(int i) const { arrive(&sh.unit_empty[i % kUnitSlots]); }
+};
+
+// ---- warp 13: the units of this CTA and their TMA loads ----
+__device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
+                                          const CUtensorMap* tm_k, const CUtensorMap* tm_v,
+                                          int& kv_issued, int& q_issued) {
+  const PrefillParams& p = c.p;
+  Shared& sh = c.sh;
+  const int lane = threadIdx.x & 31;
+  const int per_unit = 2 * p.tile_tokens;
+  // sequences base .. base + 31, one per lane; units are numbered sequence by
+  // sequence, within one from its last tokens (the longest rows) to its first,
+  // the kv heads innermost
+  int base = -32, total = 0;  // total: units of the chunk
+  long long first = 0;        // units before it
+  int q0 = 0, len_q = 0, mine = 0, incl = 0;
+  int next = blockIdx.x;
+  for (int i = 0;; ++i) {
+    const int u = next;
+    while (base < p.batch && u >= first + total) {  // the chunk that holds unit u
+      first += total;
+      base += 32;
+      total = 0;
+      if (base >= p.batch) break;
+      q0 = len_q = mine = 0;
+      if (base + lane < p.batch) {
+        q0 = __ldg(p.cu_q + base + lane);
+        const int q1 = __ldg(p.cu_q + base + lane + 1);
+        if (q0 >= 0 && q1 >= q0 && q1 <= p.total_q) len_q = q1 - q0;
+        else record_status(&sh.status, XQA_ERR_BAD_OFFSETS);
+        mine = (int)(((long long)len_q + per_unit - 1) / per_unit) * p.num_kv_heads;
+      }
+      incl = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(kAll, incl, off);
+        if (lane >= off) incl += v;
+      }
+      total = __shfl_sync(kAll, incl, 31);
+    }
+    const int slot = i % kUnitSlots;
+    if (i >= kUnitSlots && !c.wait(&sh.unit_empty[slot], (i / kUnitSlots - 1) & 1)) return;
+    if (base >= p.batch) {  // none left
+      if (lane == 0) {
+        sh.unit[slot].end = 1;
+        mbar_arrive(&sh.unit_full[slot]);
+      }
+      return;
+    }
+    const int at = (int)(u - first);
+    const int src = __popc(__ballot_sync(kAll, incl <= at));  // lane of the sequence
+    const int s_incl = __shfl_sync(kAll, incl, src), s_mine = __shfl_sync(kAll, mine, src);
+    const int s_q0 = __shfl_sync(kAll, q0, src), s_len = __shfl_sync(kAll, len_q, src);
+    const int local = at - (s_incl - s_mine);
+    const int pairs = s_mine / p.num_kv_heads;
+    const int pair = pairs - 1 - local / p.num_kv_heads;
+    const int head = local - local / p.num_kv_heads * p.num_kv_heads;
+    const int k0 = __ldg(p.cu_k + base + src), k1 = __ldg(p.cu_k + base + src + 1);
+    Unit w;
+    w.end = 0;
+    w.bad = (k0 < 0 || k1 < k0 || k1 > p.total_k) ? 1 : 0;
+    const int tok0 = pair * per_unit;
+    w.q_row = s_q0 + tok0;
+    w.tokens = min(per_unit, s_len - tok0);
+    w.head = head;
+    w.k_row = w.bad ? 0 : k0;
+    w.len_k = w.bad ? 0 : k1 - k0;
+    // keys seen by the first token; clamped where it is used
+    w.vis0 = p.causal ? w.len_k - s_len + tok0 + 1 : w.len_k;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int toks = min(p.tile_tokens, w.tokens - s * p.tile_tokens);
+      const int last = p.causal ? min(w.len_k, w.vis0 + s * p.tile_tokens + toks - 1) : w.len_k;
+      w.n[s] = toks > 0 && last > 0 ? (last - 1) / kTile + 1 : 0;
+    }
+    w.hidden = max(0, min(w.vis0, w.len_k));
+    if (lane == 0) {
+      sh.unit[slot] = w;
+      sh.not_finite[slot] = 0;
+      mbar_arrive(&sh.unit_full[slot]);
+      if (w.bad) record_status(&sh.status, XQA_ERR_BAD_OFFSETS);
+      next = gridDim.x + atomicAdd(p.counters, 1);
+    }
+    next = __shfl_sync(kAll, next, 0);
+    const int n = max(w.n[0], w.n[1]);
+    if (n == 0) continue;
+    if (q_issued > 0 && !c.wait(&sh.q_empty, (q_issued - 1) & 1)) return;
+    if (lane == 0) {
+      const int box = p.group * p.tile_tokens * 128;  // bytes of a half tile
+      mbar_arrive_expect_tx(&sh.q_full, 4 * box);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          tma_load_4d(c.tiles + s * kTileBytes + h * kHalfBytes, tm_q, &sh.q_full, 64 * h, 0,
+                      w.head, w.q_row + s * p.tile_tokens);
+    }
+    ++q_issued;
+    for (int j = n - 1; j >= 0; --j) {
+#pragma unroll 1
+      for (int v = 0; v < 2; ++v) {
+        const int st = kv_issued % kKvStages;
+        if (kv_issued >= kKvStages && !c.wait(&sh.kv_empty[st], (kv_issued / kKvStages - 1) & 1))
+          return;
+        if (lane == 0) {
+          const CUtensorMap* tm = v ? tm_v : tm_k;
+          mbar_arrive_expect_tx(&sh.kv_full[st], kTileBytes);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            tma_load_kv(c.kv(st) + h * kHalfBytes, tm, &sh.kv_full[st], 64 * h, w.head,
+                        w.k_row + j * kTile);
+        }
+        ++kv_issued;
+      }
+    }
+  }
+}
+
+// ---- warp 12: the products ----
+template <int kType>
+__device__ __forceinline__ void tensor_role(const Ctx& c) {
+  Shared& sh = c.sh;
+  const int lane = threadIdx.x & 31;
+  const uint32_t id_qk = instr_desc<kType>(false), id_pv = instr_desc<kType>(true);
+  const uint32_t q_addr = smem_addr(c.tiles);
+  int kv = 0, units_with_work = 0;
+  uint32_t cleaned = 0;     // phase of v_clean, one bit per stage
+  int np[2] = {0, 0};       // P tiles consumed
+  int no[2] = {0, 0};       // O tiles started
+  auto qk = [&](int s, int st) {
+    if (lane == 0) {
+      const uint32_t a = q_addr + s * kTileBytes, b = smem_addr(c.kv(st));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t off = (k >> 2) * kHalfBytes + (k & 3) * 32;
+        tc_mma_ss(c.tmem + s * kTile, desc_k_major(a + off), desc_k_major(b + off), id_qk, k > 0);
+      }
+      tc_commit(&sh.s_full[s]);
+    }
+  };
+  for (int i = 0;; ++i) {
+    Unit u;
+    if (!c.get_unit(i, u)) return;
+    c.free_unit(i);
+    const int n = max(u.n[0], u.n[1]);
+    if (n == 0) continue;
+    if (!c.wait(&sh.q_full, units_with_work & 1)) return;
+    ++units_with_work;
+    int st = kv % kKvStages;
+    if (!c.wait(&sh.kv_full[st], (kv / kKvStages) & 1)) return;
+    tc_fence_after();
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      if (u.n[s] == n) qk(s, st);
+    if (lane == 0) {
+      tc_commit(&sh.kv_empty[st]);
+      if (n == 1) tc_commit(&sh.q_empty);
+    }
+    ++kv;
+    for (int j = n - 1; j >= 0; --j) {
+      const int sv = kv % kKvStages, sk = (kv + 1) % kKvStages;
+      if (!c.wait(&sh.kv_full[sv], (kv / kKvStages) & 1)) return;
+      if ((j + 1) * kTile > u.hidden) {  // masked: after the V warps are done with it
+        if (!c.wait(&sh.v_clean[sv], (cleaned >> sv) & 1)) return;
+        cleaned ^= 1u << sv;
+      }
+      if (j > 0 && !c.wait(&sh.kv_full[sk], ((kv + 1) / kKvStages) & 1)) return;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (j < u.n[s]) {
+          if (!c.wait(&sh.p_full[s], np[s] & 1)) return;
+          ++np[s];
+          const bool start = j == u.n[s] - 1;
+          if (start) {
+            if (no[s] > 0 && !c.wait(&sh.o_free[s], (no[s] - 1) & 1)) return;
+            ++no[s];
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t b = smem_addr(c.kv(sv));
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              tc_mma_ts(c.tmem + 256 + s * kTile, c.tmem + s * kTile + 8 * k,
+                        desc_mn_major(b + k * 2048), id_pv, !start || k > 0);
+            if (j == 0) tc_commit(&sh.o_full[s]);
+          }
+        }
+        if (j > 0 && j - 1 < u.n[s]) qk(s, sk);
+      }
+      if (lane == 0) {
+        tc_commit(&sh.kv_empty[sv]);
+        if (j > 0) tc_commit(&sh.kv_empty[sk]);
+        if (j == 1) tc_commit(&sh.q_empty);
+      }
+      kv += j > 0 ? 2 : 1;
+    }
+  }
+}
+
+// ---- warps 14, 15: V tiles that some row of the unit sees in part ----
+template <int kType>
+__device__ __forceinline__ void clean_role(const Ctx& c) {
+  Shared& sh = c.sh;
+  const int t = threadIdx.x & 63;  // 64 threads
+  const uint32_t exp_mask = kType == XQA_F16 ? 0x7c00u : 0x7f80u;
+  int kv = 0;
+  for (int i = 0;; ++i) {
+    Unit u;
+    if (!c.get_unit(i, u)) return;
+    const int n = max(u.n[0], u.n[1]);
+    bool found = false;
+    for (int k = 0; k < 2 * n; ++k, ++kv) {  // every tile: K, V of tile n - 1, then n - 2, ...
+      const int st = kv % kKvStages, j = n - 1 - (k >> 1);
+      if (!c.wait(&sh.kv_full[st], (kv / kKvStages) & 1)) return;
+      if ((k & 1) && (j + 1) * kTile > u.hidden) {
+        const int from = max(0, u.hidden - j * kTile);     // first row some token does not see
+        const int past = min(kTile, u.len_k - j * kTile);  // first row past the sequence
+        uint4* rows = reinterpret_cast<uint4*>(c.kv(st));
+        for (int x = from * 8 + t; x < kTile * 8; x += 64) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint4& cell = rows[h * (kHalfBytes / 16) + x];
+            if ((x >> 3) >= past) {
+              cell = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint32_t w[4] = {cell.x, cell.y, cell.z, cell.w};
+            bool hit = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if ((w[e] & exp_mask) == exp_mask) {
+                w[e] &= 0xffff0000u;
+                hit = true;
+              }
+              if ((w[e] & exp_mask << 16) == exp_mask << 16) {
+                w[e] &= 0x0000ffffu;
+                hit = true;
+              }
+            }
+            if (hit) {
+              cell = make_uint4(w[0], w[1], w[2], w[3]);
+              found = true;
+            }
+          }
+        }
+        if (found) *(volatile int*)&sh.not_finite[i % kUnitSlots] = 1;
+        fence_proxy_async_smem();  // before the tensor core reads the tile
+        c.arrive(&sh.v_clean[st]);
+      }
+      c.arrive(&sh.kv_empty[st]);
+    }
+    c.free_unit(i);
+  }
+}
+
+// Row of this thread within its row tile.
+struct RowPos {
+  int token;  // within the unit
+  int head;   // within the group
+  bool valid;
+};
+__device__ __forceinline__ RowPos row_pos(const PrefillParams& p, const Unit& u, int s, int row) {
+  RowPos r;
+  const int t = row / p.group;
+  r.head = row - t * p.group;
+  r.token = s * p.tile_tokens + t;
+  r.valid = t < p.tile_tokens && r.token < u.tokens;
+  return r;
+}
+__device__ __forceinline__ int visible(const PrefillParams& p, const Unit& u, const RowPos& r) {
+  if (!r.valid) return 0;
+  return p.causal ? max(0, min(u.len_k, u.vis0 + r.token)) : u.len_k;
+}
+
+// ---- warps 0-7: softmax of row tile s; a thread owns a row ----
+template <int kType>
+__device__ __forceinline__ void softmax_role(const Ctx& c, int s) {
+  const PrefillParams& p = c.p;
+  Shared& sh = c.sh;
+  const int row = threadIdx.x & 127;
+  const uint32_t lane_base = c.tmem + ((uint32_t)(row & ~31) << 16);
+  const uint32_t s_addr = lane_base + s * kTile, o_addr = lane_base + 256 + s * kTile;
+  const float sc = p.scale_log2;
+  int ns = 0, nstat = 0;  // S tiles, units with work so far
+  for (int i = 0;; ++i) {
+    Unit u;
+    if (!c.get_unit(i, u)) return;
+    const int vis = visible(p, u, row_pos(p, u, s, row));
+    c.free_unit(i);
+    const int n = s == 0 ? u.n[0] : u.n[1];
+    if (n == 0) continue;
+    // keys that every token of this row tile sees
+    const int clear = p.causal ? min(u.len_k, u.vis0 + s * p.tile_tokens) : u.len_k;
+    float m = kNoRowMax, l = 0.f;
+    for (int j = n - 1; j >= 0; --j) {
+      if (!c.wait(&sh.s_full[s], ns & 1)) return;
+      tc_fence_after();
+      uint32_t r[kTile];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32 * q, r + 32 * q);
+      tmem_wait_ld();
+      if ((j + 1) * kTile > clear) {
+        const int lim = vis - j * kTile;
+#pragma unroll
+        for (int k = 0; k < kTile; ++k)
+          if (k >= lim) r[k] = 0xff800000u;  // -inf
+      }
+      float mx[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(r[k]);
+#pragma unroll
+      for (int k = 4; k < kTile; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(r[k]));
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+      const bool moves = top > m + kLazyMax;
+      if (j < n - 1) {
+        // O holds something: rows whose maximum moves are rescaled (the product
+        // that last wrote O was issued before the one that made this S)
+        const bool scale_o = moves && m != kNoRowMax;
+        if (__any_sync(kAll, scale_o)) {
+          const float a = scale_o ? ex2(m - top) : 1.f;
+          l *= a;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + 32 * q, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+            tmem_st32(o_addr + 32 * q, o);
+          }
+        }
+      }
+      if (moves) m = top;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float a = ex2(__fmaf_rn(__uint_as_float(r[64 * h + 2 * k]), sc, -m));
+          const float b = ex2(__fmaf_rn(__uint_as_float(r[64 * h + 2 * k + 1]), sc, -m));
+          sum[(2 * k) & 3] += a;
+          sum[(2 * k + 1) & 3] += b;
+          pk[k] = pack2<kType>(a, b);
+        }
+        tmem_st32(s_addr + 32 * h, pk);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      c.arrive(&sh.p_full[s]);
+      ++ns;
+    }
+    if (nstat > 0 && !c.wait(&sh.stat_free[s], (nstat - 1) & 1)) return;
+    ++nstat;
+    float2* st = reinterpret_cast<float2*>(c.stats) + s * kTile + row;
+    *st = make_float2(m, l);
+    c.arrive(&sh.stat_full[s]);
+  }
+}
+
+// ---- warps 8-11: normalise and write ----
+template <int kType>
+__device__ __forceinline__ void epilogue_role(const Ctx& c) {
+  const PrefillParams& p = c.p;
+  Shared& sh = c.sh;
+  const int row = threadIdx.x & 127;
+  const uint32_t lane_base = c.tmem + ((uint32_t)(row & ~31) << 16);
+  const uint32_t exp_mask = kType == XQA_F16 ? 0x7c00u : 0x7f80u;
+  int done[2] = {0, 0};
+  for (int i = 0;; ++i) {
+    Unit u;
+    if (!c.get_unit(i, u)) return;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const RowPos rp = row_pos(p, u, s, row);
+      const long long at = (long long)u.q_row + rp.token;
+      const int h = u.head * p.group + rp.head;
+      uint16_t* out = p.out + at * p.out_row_stride + h * p.out_head_stride;
+      if (u.n[s] == 0) {  // no tokens, or tokens that see nothing
+        if (rp.valid) {
+          const uint32_t f = !u.bad ? 0u : kType == XQA_F16 ? 0x7fff7fffu : 0x7fc07fc0u;
+#pragma unroll 1
+          for (int k = 0; k < kHeadDim / 8; ++k)
+            reinterpret_cast<uint4*>(out)[k] = make_uint4(f, f, f, f);
+          if (p.lse) p.lse[at * p.num_q_heads + h] = u.bad ? __int_as_float(0x7fc00000) : -INFINITY;
+        }
+        continue;
+      }
+      if (!c.wait(&sh.stat_full[s], done[s] & 1)) return;
+      const float2 ml = reinterpret_cast<const float2*>(c.stats)[s * kTile + row];
+      c.arrive(&sh.stat_free[s]);
+      if (!c.wait(&sh.o_full[s], done[s] & 1)) return;
+      ++done[s];
+      tc_fence_after();
+      // infinities and NaN of masked V tiles (zeroed there), for rows that see them
+      const bool patch = *(volatile int*)&sh.not_finite[i % kUnitSlots] != 0;
+      const int vis = visible(p, u, rp);
+      const float rl = ml.y == 0.f ? 0.f : 1.f / ml.y;  // a row that sees nothing: 0
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t o[32];
+        __syncwarp();  // rows part ways below
+        tmem_ld32(lane_base + 256 + s * kTile + 32 * q, o);
+        tmem_wait_ld();
+        if (q == 3) {  // O is read
+          tc_fence_before();
+          c.arrive(&sh.o_free[s]);
+        }
+        if (patch) {
+#pragma unroll 1
+          for (int key = u.hidden; key < vis; ++key) {
+            const uint16_t* v = p.v + ((long long)u.k_row + key) * p.v_row_stride +
+                                u.head * p.v_head_stride + 32 * q;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const uint32_t bits = v[k];
+              if ((bits & exp_mask) == exp_mask)
+                o[k] = __float_as_uint(
+                    __uint_as_float(o[k]) +
+                    (kType == XQA_F16 ? __half2float(__ushort_as_half((unsigned short)bits))
+                                      : __uint_as_float(bits << 16)));
+            }
+          }
+        }
+        if (rp.valid) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack2<kType>(__uint_as_float(o[8 * k + 2 * e]) * rl,
+                                  __uint_as_float(o[8 * k + 2 * e + 1]) * rl);
+            reinterpret_cast<uint4*>(out + 32 * q)[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (p.lse && rp.valid)
+        p.lse[at * p.num_q_heads + h] =
+            ml.y == 0.f ? -INFINITY : (ml.x + __log2f(ml.y)) * 0.6931471805599453f;
+    }
+    c.free_unit(i);
+  }
+}
+
+template <int kType>
+__global__ void __launch_bounds__(kPrefillThreads, 1)
+    prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const PrefillParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float* stats = reinterpret_cast<float*>(smem + kSmemTiles);
+  Shared& sh = *reinterpret_cast<Shared*>(smem + kSmemTiles + kSmemStats);
+  const int warp = threadIdx.x >> 5;
+  const bool aligned = (smem_addr(smem) & 1023u) == 0;  // as the swizzle needs
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kKvStages; ++i) {
+      mbar_init(&sh.kv_full[i], 1);
+      mbar_init(&sh.kv_empty[i], 3);  // the tensor-core warp and the two V warps
+      mbar_init(&sh.v_clean[i], 2);
+    }
+    for (int i = 0; i < kUnitSlots; ++i) {
+      mbar_init(&sh.unit_full[i], 1);
+      mbar_init(&sh.unit_empty[i], kUnitReaders);
+    }
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sh.s_full[s], 1);
+      mbar_init(&sh.p_full[s], 4);
+      mbar_init(&sh.o_full[s], 1);
+      mbar_init(&sh.o_free[s], 4);
+      mbar_init(&sh.stat_full[s], 4);
+      mbar_init(&sh.stat_free[s], 4);
+    }
+    mbar_init(&sh.drain, 1);
+    sh.abort_flag = 0;
+    sh.status = aligned ? XQA_OK : XQA_ERR_LAUNCH;
+    fence_mbar_init();
+  }
+  if (warp == 13 && (threadIdx.x & 31) == 0) {
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
+  if (warp == 12) tmem_alloc(&sh.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_wait();  // inputs are read, and outputs written, after the kernels before this one
+  int kv_issued = 0, q_issued = 0;
+  if (aligned) {
+    const Ctx c{p, sh, smem, stats, sh.tmem};
+    __syncwarp();
+    if (warp >= 12) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+      if (warp == 12) tensor_role<kType>(c);
+      else if (warp == 13) load_role(c, &tm_q, &tm_k, &tm_v, kv_issued, q_issued);
+      else clean_role<kType>(c);
+    } else if (warp >= 8) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+      epilogue_role<kType>(c);
+    } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+      softmax_role<kType>(c, warp >> 2);
+    }
+  }
+  __syncwarp();
+  // Products and their arrivals, and after an abort copies, may be in flight:
+  // they end before the CTA's shared memory and TMEM are given up.
+  if (aligned && (warp == 12 || warp == 13)) {
+    int never = 0;
+    bool ok = true;
+    if (warp == 12) {
+      if ((threadIdx.x & 31) == 0) tc_commit(&sh.drain);
+      __syncwarp();
+      ok = mbar_wait_bounded(&sh.drain, 0, &never);
+    } else if (*(volatile int*)&sh.abort_flag) {
+      for (int k = max(0, kv_issued - kKvStages); k < kv_issued; ++k)
+        ok = mbar_wait_bounded(&sh.kv_full[k % kKvStages], (k / kKvStages) & 1, &never) && ok;
+      if (q_issued > 0) ok = mbar_wait_bounded(&sh.q_full, (q_issued - 1) & 1, &never) && ok;
+    }
+    if (!ok) atomicExch(&sh.status, XQA_ERR_DRAIN_TIMEOUT);
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(sh.tmem, 512);
+  if (threadIdx.x == 0) {
+    p.status[blockIdx.x] = sh.status;
+    if (blockIdx.x == 0) p.header[0] = gridDim.x;
+    // the last CTA leaves the counters at zero for the next call
+    __threadfence();
+    if (atomicAdd(p.counters + 1, 1) == (int)gridDim.x - 1) {
+      p.counters[0] = 0;
+      p.counters[1] = 0;
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                           const CUtensorMap& tm_v, const PrefillParams& p, int dtype, int ctas,
+                           cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kPrefillThreads);
+  cfg.dynamicSmemBytes = kPrefillSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return dtype == XQA_F16 ? cudaLaunchKernelEx(&cfg, prefill_kernel<XQA_F16>, tm_q, tm_k, tm_v, p)
+                          : cudaLaunchKernelEx(&cfg, prefill_kernel<XQA_BF16>, tm_q, tm_k, tm_v, p);
+}
+
+cudaError_t set_prefill_attributes() {
+  const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  const cudaError_t e = cudaFuncSetAttribute(prefill_kernel<XQA_F16>, a, kPrefillSmem);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(prefill_kernel<XQA_BF16>, a, kPrefillSmem);
+}
+
+}  // namespace xqa

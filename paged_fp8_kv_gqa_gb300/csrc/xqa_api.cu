@@ -15,6 +15,7 @@
 
 namespace xqa {
 cudaError_t set_partial_attributes();
+cudaError_t set_prefill_attributes();
 }
 
 namespace {
@@ -101,7 +102,9 @@ xqa_status_t ensure_device_setup() {
   if (cudaGetDevice(&dev) != cudaSuccess) return XQA_ERR_DEVICE;
   if (dev < 0 || dev >= kMaxDevices) return XQA_ERR_DEVICE;
   if (g_attrs_set[dev].load(std::memory_order_acquire) == 0) {
-    if (xqa::set_partial_attributes() != cudaSuccess) return XQA_ERR_LAUNCH;
+    if (xqa::set_partial_attributes() != cudaSuccess ||
+        xqa::set_prefill_attributes() != cudaSuccess)
+      return XQA_ERR_LAUNCH;
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return XQA_ERR_DEVICE;
@@ -291,6 +294,94 @@ bool row_strides(const xqa_rows_t& s, int64_t row, int64_t head, bool written, l
          *hs >= (long long)(s.num_rows - 1) * *rs + kHeadDim;
 }
 
+// The regions of a prefill workspace: those of a decode workspace in front of
+// its first-page hints (header, tickets, status words).
+constexpr size_t kPrefillWorkspaceBytes = 12544;
+
+struct Side {  // a strided [rows, heads, 128] tensor
+  long long rs, hs;
+};
+
+bool prefill_side(int rows, int heads, int64_t row, int64_t head, bool written, Side* s) {
+  s->hs = head != 0 ? head : kHeadDim;
+  s->rs = row != 0 ? row : (long long)heads * kHeadDim;
+  // dims of size 1 have no stride of their own: any value that a tensor map takes
+  if (heads == 1) s->hs = kHeadDim;
+  if (rows <= 1) s->rs = (long long)heads * kHeadDim;
+  if (s->hs < 0 || s->rs < 0 || s->hs % 8 != 0 || s->rs % 8 != 0) return false;
+  if (s->rs >= (1ll << 38) || s->hs >= (1ll << 38) / heads) return false;  // tensor map: 2^40 bytes
+  if (!written) return true;
+  if ((heads > 1 && s->hs < kHeadDim) || (rows > 1 && s->rs < kHeadDim)) return false;
+  return s->rs >= (heads - 1) * s->hs + kHeadDim ||
+         s->hs >= (long long)(rows - 1) * s->rs + kHeadDim;
+}
+
+struct PrefillResolved {
+  Side q, k, v, out;
+  int group, ctas;
+  float sm_scale;
+};
+
+xqa_status_t resolve_prefill(const xqa_prefill_shape_t* s, PrefillResolved* r) {
+  if (!s) return XQA_ERR_NULL;
+  if (s->head_dim != kHeadDim || s->batch < 1 || s->num_kv_heads < 1 || s->num_q_heads < 1 ||
+      s->num_q_heads % s->num_kv_heads != 0 || s->total_q < 0 || s->total_k < 0 ||
+      s->max_ctas < 0)
+    return XQA_ERR_SHAPE;
+  if (s->dtype != XQA_F16 && s->dtype != XQA_BF16) return XQA_ERR_SHAPE;
+  if (s->causal != 0 && s->causal != 1) return XQA_ERR_SHAPE;
+  r->group = s->num_q_heads / s->num_kv_heads;
+  if (r->group > 128) return XQA_ERR_SHAPE;  // a 128-row tile holds whole tokens
+  // int32 row and unit arithmetic on the device
+  if ((long long)s->total_q * s->num_q_heads >= (1ll << 27) || s->total_k > 0x7ffffe00 ||
+      s->batch > (1 << 24) || s->num_q_heads > (1 << 20))
+    return XQA_ERR_SHAPE;
+  if (!prefill_side(s->total_q, s->num_q_heads, s->q_row_stride, s->q_head_stride, false, &r->q) ||
+      !prefill_side(s->total_k, s->num_kv_heads, s->k_row_stride, s->k_head_stride, false, &r->k) ||
+      !prefill_side(s->total_k, s->num_kv_heads, s->v_row_stride, s->v_head_stride, false, &r->v) ||
+      !prefill_side(s->total_q, s->num_q_heads, s->out_row_stride, s->out_head_stride, true,
+                    &r->out))
+    return XQA_ERR_SHAPE;
+  r->sm_scale = s->sm_scale > 0.f ? s->sm_scale : (float)(1.0 / sqrt((double)kHeadDim));
+  if (!isfinite(r->sm_scale)) return XQA_ERR_SHAPE;
+  // units of 2 x floor(128 / G) tokens and one kv head, at most
+  const long long tokens = 2 * (128 / r->group);
+  const long long seqs = s->batch < s->total_q ? s->batch : s->total_q;
+  const long long units = (s->total_q / tokens + seqs) * s->num_kv_heads;
+  r->ctas = s->max_ctas;
+  if (r->ctas == 0) {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return XQA_ERR_DEVICE;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+      return XQA_ERR_DEVICE;
+    r->ctas = sms;
+  }
+  if (r->ctas > xqa::kMaxCtas) r->ctas = xqa::kMaxCtas;
+  if (r->ctas > units) r->ctas = units > 0 ? (int)units : 1;
+  return XQA_OK;
+}
+
+// q: x = D, y = head in the group, z = kv head, w = row; k, v: x = D, y = kv
+// head, z = row. Boxes of 64 dims (128 bytes, the swizzle's width) by the rows of
+// a tile.
+xqa_status_t encode_rows_map(CUtensorMap* map, const void* base, const Side& s, int rows,
+                             int kv_heads, int group, int box_rows, int dtype, bool is_q) {
+  const cuuint64_t es = 2;
+  const cuuint64_t n = rows > 0 ? rows : 1;
+  cuuint64_t dims[4] = {(cuuint64_t)kHeadDim, (cuuint64_t)(is_q ? group : kv_heads),
+                        is_q ? (cuuint64_t)kv_heads : n, n};
+  cuuint64_t strides[3] = {es * s.hs, is_q ? es * s.hs * group : es * s.rs, es * s.rs};
+  cuuint32_t box[4] = {64, (cuuint32_t)(is_q ? group : 1), (cuuint32_t)(is_q ? 1 : box_rows),
+                       (cuuint32_t)box_rows};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult res = g_encode.load(std::memory_order_acquire)(
+      map, dtype == XQA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+      is_q ? 4 : 3, const_cast<void*>(base), dims, strides, box, estr,
+      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return res == CUDA_SUCCESS ? XQA_OK : XQA_ERR_LAUNCH;
+}
+
 xqa_status_t rows_impl(bool append, void* k, void* v, const int32_t* cu_seqlens,
                        const int32_t* block_tables, const int32_t* context_lens, float k_scale,
                        float v_scale, const float* k_scale_dev, const float* v_scale_dev,
@@ -429,6 +520,74 @@ xqa_status_t xqa_dequant_e4m3(const uint8_t* in, size_t n, float scale, uint16_t
   return e == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
 }
 
+xqa_status_t xqa_prefill_workspace_size(const xqa_prefill_shape_t* shape, size_t* bytes) {
+  if (!bytes) return XQA_ERR_NULL;
+  PrefillResolved r;
+  const xqa_status_t st = resolve_prefill(shape, &r);
+  if (st != XQA_OK) return st;
+  static_assert(kPrefillWorkspaceBytes >=
+                    4 * xqa::kHeaderWords + 8 * (size_t)xqa::kMaxCtas + 4 * (size_t)xqa::kMaxCtas,
+                "header, tickets and status words");
+  *bytes = kPrefillWorkspaceBytes;
+  return XQA_OK;
+}
+
+xqa_status_t xqa_prefill(const void* q, const void* k, const void* v, const int32_t* cu_seqlens_q,
+                         const int32_t* cu_seqlens_k, void* out, float* lse,
+                         const xqa_prefill_shape_t* shape, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  PrefillResolved r;
+  xqa_status_t st = resolve_prefill(shape, &r);
+  if (st != XQA_OK) return st;
+  if (shape->total_q == 0) return XQA_OK;
+  const bool keys = shape->total_k > 0;
+  if (!q || !out || !cu_seqlens_q || !cu_seqlens_k || !workspace || (keys && (!k || !v)))
+    return XQA_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return XQA_ERR_ALIGN;
+  if (workspace_bytes < kPrefillWorkspaceBytes) return XQA_ERR_WORKSPACE;
+  if (!aligned16(q) || !aligned16(out) || (keys && (!aligned16(k) || !aligned16(v))))
+    return XQA_ERR_ALIGN;
+  if ((st = ensure_device_setup()) != XQA_OK) return st;
+  const int tokens = 128 / r.group;
+  alignas(64) CUtensorMap tm_q, tm_k, tm_v;
+  if ((st = encode_rows_map(&tm_q, q, r.q, shape->total_q, shape->num_kv_heads, r.group, tokens,
+                            shape->dtype, true)) != XQA_OK)
+    return st;
+  // without keys no tile is ever loaded; the maps then only need a valid base
+  if ((st = encode_rows_map(&tm_k, keys ? k : q, r.k, shape->total_k, shape->num_kv_heads, 1, 128,
+                            shape->dtype, false)) != XQA_OK ||
+      (st = encode_rows_map(&tm_v, keys ? v : q, r.v, shape->total_k, shape->num_kv_heads, 1, 128,
+                            shape->dtype, false)) != XQA_OK)
+    return st;
+  const xqa::WsLayout lay = xqa::ws_layout(0, 0);
+  uint8_t* base = reinterpret_cast<uint8_t*>(workspace);
+  xqa::PrefillParams p;
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k;
+  p.v = reinterpret_cast<const uint16_t*>(v);
+  p.out = reinterpret_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.header = ws_i32(workspace);
+  p.counters = ws_i32(workspace) + 4;
+  p.status = reinterpret_cast<int32_t*>(base + lay.status_off);
+  p.batch = shape->batch;
+  p.num_q_heads = shape->num_q_heads;
+  p.num_kv_heads = shape->num_kv_heads;
+  p.group = r.group;
+  p.total_q = shape->total_q;
+  p.total_k = shape->total_k;
+  p.causal = shape->causal;
+  p.tile_tokens = tokens;
+  p.scale_log2 = (float)((double)r.sm_scale * 1.4426950408889634);
+  p.v_row_stride = r.v.rs;
+  p.v_head_stride = r.v.hs;
+  p.out_row_stride = r.out.rs;
+  p.out_head_stride = r.out.hs;
+  const cudaError_t e =
+      xqa::launch_prefill(tm_q, tm_k, tm_v, p, shape->dtype, r.ctas, (cudaStream_t)stream);
+  return e == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
+}
+
 xqa_status_t xqa_append(const void* k, const void* v, const int32_t* cu_seqlens,
                         const int32_t* block_tables, const int32_t* context_lens, float k_scale,
                         float v_scale, const float* k_scale_dev, const float* v_scale_dev,
@@ -522,6 +681,7 @@ const char* xqa_status_string(xqa_status_t status) {
     case XQA_ERR_DEVICE_TIMEOUT: return "device: pipeline wait exceeded its time budget";
     case XQA_ERR_DRAIN_TIMEOUT:
       return "device: a copy was still in flight when its CTA gave up; device state not trusted";
+    case XQA_ERR_BAD_OFFSETS: return "device: cu_seqlens descending, negative or past the rows";
   }
   return "unknown status";
 }

@@ -63,6 +63,24 @@ struct RowsParams {
   const float* v_scale_ptr;
 };
 
+struct PrefillParams {
+  const int32_t* cu_q;  // [batch + 1]
+  const int32_t* cu_k;
+  const uint16_t* v;    // for values that are not finite (read through TMA otherwise)
+  uint16_t* out;
+  float* lse;         // optional [total_q, Hq]
+  int32_t* header;    // workspace header (CTAs launched)
+  int32_t* counters;  // [2] units handed out, CTAs done: zero between calls
+  int32_t* status;    // [kMaxCtas]
+  int batch, num_q_heads, num_kv_heads, group, total_q, total_k, causal;
+  int tile_tokens;    // T: tokens of a 128-row tile
+  float scale_log2;   // sm_scale * log2(e)
+  long long v_row_stride, v_head_stride, out_row_stride, out_head_stride;
+};
+
+cudaError_t launch_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                           const CUtensorMap& tm_v, const PrefillParams& p, int dtype, int ctas,
+                           cudaStream_t stream);
 cudaError_t launch_rows(bool append, const RowsParams& p, cudaStream_t stream);
 cudaError_t launch_plan(const int32_t* context_lens, int batch, int num_kv_heads,
                         int max_blocks_per_seq, int n_max, int min_pages_per_cta,
