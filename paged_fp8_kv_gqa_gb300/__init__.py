@@ -191,12 +191,15 @@ def make_shape(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tenso
                merge_mode: int = 0, kv_dtype: str = "e5m2", kv_layout: str = "hnd") -> XqaShape:
     """Shape descriptor from q [B, Hq, D] (or [B, T, Hq, D] for T new tokens per
     sequence), block_tables [B, MBS] and k_cache [NB, Hkv, BS, D] (kv_layout
-    "hnd") or [NB, BS, Hkv, D] ("nhd")."""
+    "hnd") or [NB, BS, Hkv, D] ("nhd"); for kv_dtype "e2m1" [NB, Hkv, 1152]."""
     if q.dim() == 4:
         b, t_new, hq, d = q.shape
     else:
         (b, hq, d), t_new = q.shape, 1
-    if kv_layout == "hnd":
+    if kv_dtype == "e2m1":
+        nb, hkv, bs = _cache_dims(k_cache, kv_dtype, kv_layout)
+        d2 = 128
+    elif kv_layout == "hnd":
         nb, hkv, bs, d2 = k_cache.shape
     else:
         nb, bs, hkv, d2 = k_cache.shape

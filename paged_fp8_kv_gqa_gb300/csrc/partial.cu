@@ -221,6 +221,46 @@ struct PageRegs {
   uint4 vx, vy, vz, vw;      // V tokens 2c, 2c+1, 2c+8, 2c+9, dims [16g, 16g+16)
 };
 
+// 4 bits: a lane's K dims [32c, 32c+32) are 16 code bytes and two scales of a
+// token, its V dims [16g, 16g+16) are 8 code bytes and one scale. The slice is not
+// swizzled; MMA row (and contraction index) r stands for token r ^ (r >> 1 & 1), so
+// that 8 lanes of a K load cover 128 contiguous bytes and the four tokens of a V
+// load lie in both halves of the banks (2-way conflicts instead of 4-way).
+struct PageRegs4 {
+  uint4 ka, kb;             // K codes, tokens tok(g) and tok(g) + 8
+  uint32_t ksa, ksb;        // their scales: two E4M3 codes each
+  uint2 vx, vy, vz, vw;     // V codes, tokens tok(2c), tok(2c+1) and both + 8
+  uint32_t vsx, vsy, vsz, vsw;
+};
+__device__ __forceinline__ int row_token4(int r) { return r ^ ((r >> 1) & 1); }
+
+template <int kFmt>
+struct PageOf {
+  using Regs = PageRegs;
+};
+template <>
+struct PageOf<XQA_KV_E2M1> {
+  using Regs = PageRegs4;
+};
+
+__device__ __forceinline__ PageRegs4 load_page4(const uint8_t* ks, const uint8_t* vs, int g, int c) {
+  PageRegs4 r;
+  const int tg = row_token4(g), ta = row_token4(2 * c), tb = ta ^ 1;
+  r.ka = lds128(ks + tg * 64 + 16 * c);
+  r.kb = lds128(ks + (tg + 8) * 64 + 16 * c);
+  r.ksa = lds_u16(ks + kCodeBytes4 + tg * 8 + 2 * c);
+  r.ksb = lds_u16(ks + kCodeBytes4 + (tg + 8) * 8 + 2 * c);
+  r.vx = lds64(vs + ta * 64 + 8 * g);
+  r.vy = lds64(vs + tb * 64 + 8 * g);
+  r.vz = lds64(vs + (ta + 8) * 64 + 8 * g);
+  r.vw = lds64(vs + (tb + 8) * 64 + 8 * g);
+  r.vsx = lds_u8(vs + kCodeBytes4 + ta * 8 + g);
+  r.vsy = lds_u8(vs + kCodeBytes4 + tb * 8 + g);
+  r.vsz = lds_u8(vs + kCodeBytes4 + (ta + 8) * 8 + g);
+  r.vsw = lds_u8(vs + kCodeBytes4 + (tb + 8) * 8 + g);
+  return r;
+}
+
 // Shared loads of one stage (swizzled 16-byte chunks, conflict-free).
 __device__ __forceinline__ PageRegs load_page(const uint8_t* ks, const uint8_t* vs, int g, int c) {
   PageRegs r;
@@ -252,7 +292,8 @@ struct SegLimits {
 // fragments are converted once and shared by all tiles. With two pages the two
 // independent chains interleave and hide each other's fixed latencies.
 template <int kFmt, int NP, int NT, bool kMulti>
-__device__ __forceinline__ void process_pages(WarpState<NT>& st, const PageRegs (&r)[NP],
+__device__ __forceinline__ void process_pages(WarpState<NT>& st,
+                                              const typename PageOf<kFmt>::Regs (&r)[NP],
                                               const uint32_t (&qf)[NT][16], const int (&tok0)[NP],
                                               const int (&nvalid)[NP], const SegLimits<NT>& sl,
                                               float scale_log2, int g, int c) {
@@ -260,25 +301,50 @@ __device__ __forceinline__ void process_pages(WarpState<NT>& st, const PageRegs 
   float s[NP][NT][4];
 #pragma unroll
   for (int pi = 0; pi < NP; ++pi) {
-    const uint32_t kr0[8] = {r[pi].ka0.x, r[pi].ka0.y, r[pi].ka0.z, r[pi].ka0.w,
-                             r[pi].ka1.x, r[pi].ka1.y, r[pi].ka1.z, r[pi].ka1.w};
-    const uint32_t kr1[8] = {r[pi].kb0.x, r[pi].kb0.y, r[pi].kb0.z, r[pi].kb0.w,
-                             r[pi].kb1.x, r[pi].kb1.y, r[pi].kb1.z, r[pi].kb1.w};
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int k = 0; k < 4; ++k) s[pi][j][k] = 0.f;
+    if constexpr (kFmt == XQA_KV_E2M1) {
+      // values s * code in fp16, exact: 2 x 4 significant bits, 2^-10 .. 2688
+      const uint32_t ka[4] = {r[pi].ka.x, r[pi].ka.y, r[pi].ka.z, r[pi].ka.w};
+      const uint32_t kb[4] = {r[pi].kb.x, r[pi].kb.y, r[pi].kb.z, r[pi].kb.w};
+      const uint32_t sa = e4m3x2_to_f16x2(r[pi].ksa), sb = e4m3x2_to_f16x2(r[pi].ksb);
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
-      const uint32_t a0 = KvConv<kFmt>::k_lo(kr0[kk]), a1 = KvConv<kFmt>::k_lo(kr1[kk]);
-      const uint32_t a2 = KvConv<kFmt>::k_hi(kr0[kk]), a3 = KvConv<kFmt>::k_hi(kr1[kk]);
+      for (int w = 0; w < 4; ++w) {  // dims 32c + 8w .. + 8
+        const uint32_t sel = w < 2 ? 0x1010u : 0x3232u;
+        const uint32_t fa = prmt(sa, sa, sel), fb = prmt(sb, sb, sel);
+        uint32_t xa[4], xb[4];
+        e2m1x8_to_f16x2(ka[w], xa);
+        e2m1x8_to_f16x2(kb[w], xb);
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        mma_16816(s[pi][j], a0, a1, a2, a3, qf[j][2 * kk], qf[j][2 * kk + 1]);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a0 = hmul2(xa[2 * h], fa), a1 = hmul2(xb[2 * h], fb);
+          const uint32_t a2 = hmul2(xa[2 * h + 1], fa), a3 = hmul2(xb[2 * h + 1], fb);
+          const int kk = 2 * w + h;
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            mma_16816(s[pi][j], a0, a1, a2, a3, qf[j][2 * kk], qf[j][2 * kk + 1]);
+        }
+      }
+    } else {
+      const uint32_t kr0[8] = {r[pi].ka0.x, r[pi].ka0.y, r[pi].ka0.z, r[pi].ka0.w,
+                               r[pi].ka1.x, r[pi].ka1.y, r[pi].ka1.z, r[pi].ka1.w};
+      const uint32_t kr1[8] = {r[pi].kb0.x, r[pi].kb0.y, r[pi].kb0.z, r[pi].kb0.w,
+                               r[pi].kb1.x, r[pi].kb1.y, r[pi].kb1.z, r[pi].kb1.w};
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t a0 = KvConv<kFmt>::k_lo(kr0[kk]), a1 = KvConv<kFmt>::k_lo(kr1[kk]);
+        const uint32_t a2 = KvConv<kFmt>::k_hi(kr0[kk]), a3 = KvConv<kFmt>::k_hi(kr1[kk]);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          mma_16816(s[pi][j], a0, a1, a2, a3, qf[j][2 * kk], qf[j][2 * kk + 1]);
+      }
     }
   }
 
   // ---- online softmax (log2 domain), one update for all NP pages ----
+  const int tg = kFmt == XQA_KV_E2M1 ? row_token4(g) : g;  // token of this lane's first row
   float t[NP][NT][4];
   float mx[NT][2];
 #pragma unroll
@@ -286,15 +352,15 @@ __device__ __forceinline__ void process_pages(WarpState<NT>& st, const PageRegs 
 #pragma unroll
   for (int pi = 0; pi < NP; ++pi) {
     const bool masked = tok0[pi] + kBlockSize - 1 > sl.min_lim;
-    const int r0 = tok0[pi] + g, r1 = tok0[pi] + g + 8;
+    const int r0 = tok0[pi] + tg, r1 = tok0[pi] + tg + 8;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) t[pi][j][k] = s[pi][j][k] * scale_log2;
       if (!kMulti) {  // one new token: every column's limit is ctx - 1
         if (nvalid[pi] < kBlockSize) {
-          if (g >= nvalid[pi]) t[pi][j][0] = t[pi][j][1] = -INFINITY;
-          if (g + 8 >= nvalid[pi]) t[pi][j][2] = t[pi][j][3] = -INFINITY;
+          if (tg >= nvalid[pi]) t[pi][j][0] = t[pi][j][1] = -INFINITY;
+          if (tg + 8 >= nvalid[pi]) t[pi][j][2] = t[pi][j][3] = -INFINITY;
         }
       } else if (masked) {
         if (r0 > sl.lim[j][0]) t[pi][j][0] = -INFINITY;
@@ -348,25 +414,85 @@ __device__ __forceinline__ void process_pages(WarpState<NT>& st, const PageRegs 
     }
 
     // ---- O^T += V^T * P^T for every tile ----
-    uint4 vx = r[pi].vx, vy = r[pi].vy, vz = r[pi].vz, vw = r[pi].vw;
-    if (nvalid[pi] < kBlockSize) {  // zero V rows past the context (0 * NaN would poison O)
-      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-      if (2 * c >= nvalid[pi]) vx = z;
-      if (2 * c + 1 >= nvalid[pi]) vy = z;
-      if (2 * c + 8 >= nvalid[pi]) vz = z;
-      if (2 * c + 9 >= nvalid[pi]) vw = z;
-    }
-    const uint32_t X[4] = {vx.x, vx.y, vx.z, vx.w}, Y[4] = {vy.x, vy.y, vy.z, vy.w};
-    const uint32_t Z[4] = {vz.x, vz.y, vz.z, vz.w}, W[4] = {vw.x, vw.y, vw.z, vw.w};
+    if constexpr (kFmt == XQA_KV_E2M1) {
+      uint2 vx = r[pi].vx, vy = r[pi].vy, vz = r[pi].vz, vw = r[pi].vw;
+      uint32_t sx = r[pi].vsx, sy = r[pi].vsy, sz = r[pi].vsz, sw = r[pi].vsw;
+      if (nvalid[pi] < kBlockSize) {  // zero V past the context, scales too
+        const uint2 z = make_uint2(0u, 0u);
+        const int ta = row_token4(2 * c), tb = ta ^ 1;
+        if (ta >= nvalid[pi]) vx = z, sx = 0u;
+        if (tb >= nvalid[pi]) vy = z, sy = 0u;
+        if (ta + 8 >= nvalid[pi]) vz = z, sz = 0u;
+        if (tb + 8 >= nvalid[pi]) vw = z, sw = 0u;
+      }
+      if constexpr (kMulti) {
+        // a NaN scale of a token that some column does not see: its values are
+        // taken as 0 and the columns that do see it get the NaN
+        if (tok0[pi] + kBlockSize - 1 > sl.min_lim) {
+          const int ta = row_token4(2 * c), tb = ta ^ 1;
+          uint32_t nan_at = 0;  // tokens of the page, this lane's four
+          if ((sx & 0x7fu) == 0x7fu) sx = 0u, nan_at |= 1u << ta;
+          if ((sy & 0x7fu) == 0x7fu) sy = 0u, nan_at |= 1u << tb;
+          if ((sz & 0x7fu) == 0x7fu) sz = 0u, nan_at |= 256u << ta;
+          if ((sw & 0x7fu) == 0x7fu) sw = 0u, nan_at |= 256u << tb;
+          nan_at |= __shfl_xor_sync(kFull, nan_at, 1);
+          nan_at |= __shfl_xor_sync(kFull, nan_at, 2);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      uint32_t xy[4], zw[4];  // {x_k, y_k}: tokens 2c, 2c+1 / 2c+8, 2c+9 at dim byte k
-      KvConv<kFmt>::v_pairs(X[u], Y[u], xy);
-      KvConv<kFmt>::v_pairs(Z[u], W[u], zw);
+          for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        mma_16816(st.o[j][2 * u], xy[0], xy[1], zw[0], zw[1], pb0[j], pb1[j]);
-        mma_16816(st.o[j][2 * u + 1], xy[2], xy[3], zw[2], zw[3], pb0[j], pb1[j]);
+            for (int e = 0; e < 2; ++e) {
+              const int seen = sl.lim[j][e] - tok0[pi] + 1;  // tokens of the page column e sees
+              const uint32_t m = seen >= 16 ? 0xffffu : seen <= 0 ? 0u : (1u << seen) - 1u;
+              if (nan_at & m) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  st.o[j][i][e] = st.o[j][i][e + 2] = __int_as_float(0x7fc00000);
+              }
+            }
+        }
+      }
+      const uint32_t fxy = e4m3x2_to_f16x2(sx | sy << 8), fzw = e4m3x2_to_f16x2(sz | sw << 8);
+      const uint32_t X[2] = {vx.x, vx.y}, Y[2] = {vy.x, vy.y};
+      const uint32_t Z[2] = {vz.x, vz.y}, W[2] = {vw.x, vw.y};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        // bytes {x, y} of one dim: even dims from the low nibbles, odd from the high
+        constexpr uint32_t kLow = 0x0f0f0f0fu;
+        uint32_t xe[4], xo[4], ze[4], zo[4];
+        e2m1x8_to_f16x2((X[u] & kLow) | ((Y[u] << 4) & ~kLow), xe);
+        e2m1x8_to_f16x2(((X[u] >> 4) & kLow) | (Y[u] & ~kLow), xo);
+        e2m1x8_to_f16x2((Z[u] & kLow) | ((W[u] << 4) & ~kLow), ze);
+        e2m1x8_to_f16x2(((Z[u] >> 4) & kLow) | (W[u] & ~kLow), zo);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // dims 16g + 8u + 2k, + 1
+          const uint32_t a0 = hmul2(xe[k], fxy), a1 = hmul2(xo[k], fxy);
+          const uint32_t a2 = hmul2(ze[k], fzw), a3 = hmul2(zo[k], fzw);
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            mma_16816(st.o[j][4 * u + k], a0, a1, a2, a3, pb0[j], pb1[j]);
+        }
+      }
+    } else {
+      uint4 vx = r[pi].vx, vy = r[pi].vy, vz = r[pi].vz, vw = r[pi].vw;
+      if (nvalid[pi] < kBlockSize) {  // zero V rows past the context (0 * NaN would poison O)
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        if (2 * c >= nvalid[pi]) vx = z;
+        if (2 * c + 1 >= nvalid[pi]) vy = z;
+        if (2 * c + 8 >= nvalid[pi]) vz = z;
+        if (2 * c + 9 >= nvalid[pi]) vw = z;
+      }
+      const uint32_t X[4] = {vx.x, vx.y, vx.z, vx.w}, Y[4] = {vy.x, vy.y, vy.z, vy.w};
+      const uint32_t Z[4] = {vz.x, vz.y, vz.z, vz.w}, W[4] = {vw.x, vw.y, vw.z, vw.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint32_t xy[4], zw[4];  // {x_k, y_k}: tokens 2c, 2c+1 / 2c+8, 2c+9 at dim byte k
+        KvConv<kFmt>::v_pairs(X[u], Y[u], xy);
+        KvConv<kFmt>::v_pairs(Z[u], W[u], zw);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma_16816(st.o[j][2 * u], xy[0], xy[1], zw[0], zw[1], pb0[j], pb1[j]);
+          mma_16816(st.o[j][2 * u + 1], xy[2], xy[3], zw[2], zw[3], pb0[j], pb1[j]);
+        }
       }
     }
 #pragma unroll
@@ -495,11 +621,11 @@ __device__ __forceinline__ void merge_segments(const PartialParams& p, const int
 
 // Static shared state of one partial CTA (the ring, the merge buffers and the
 // segment caches live in dynamic shared memory).
-template <int NT>
+template <int NT, int kDepth>
 struct CtaShared {
   static constexpr int kBufs = PartialGeom<NT>::kMergeBufs;
-  uint64_t full_bar[kStages];  // one per ring slot: the slot's K and V pages landed
-  int stage_bad[kStages];      // the slot's page had a block id outside [0, NB)
+  uint64_t full_bar[kDepth];  // one per ring slot: the slot's K and V pages landed
+  int stage_bad[kDepth];      // the slot's page had a block id outside [0, NB)
   int abort_flag;              // a wait ran out of time: stop issuing, drain
   int scan_warp[kWarps], scan_warp_cost[kWarps];
   int scan_carry, scan_carry_cost;
@@ -568,9 +694,10 @@ struct RangeView {
 // the rows of empty segments, and this CTA's range on the cost line. Also
 // initialises the ring barriers and waits for the kernels before this one on
 // the stream. Returns false when this CTA holds no page.
-template <int NT>
+template <int kFmt, int NT>
 __device__ __forceinline__ bool setup_range(const PartialParams& p, const CUtensorMap* tm_k,
-                                            const CUtensorMap* tm_v, CtaShared<NT>& sh,
+                                            const CUtensorMap* tm_v,
+                                            CtaShared<NT, Ring<kFmt>::kDepth>& sh,
                                             const CtaSmem<NT>& sm, RangeView& rv) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
@@ -581,7 +708,7 @@ __device__ __forceinline__ bool setup_range(const PartialParams& p, const CUtens
   const int32_t* cc;
   int total, n;
   if (tid == 0) {  // before the wait: nothing here reads or writes global memory
-    for (int i = 0; i < kStages; ++i) mbar_init(&sh.full_bar[i], 1);
+    for (int i = 0; i < Ring<kFmt>::kDepth; ++i) mbar_init(&sh.full_bar[i], 1);
     sh.abort_flag = 0;
     sh.npend = 0;
     sh.cta_status = XQA_OK;
@@ -590,8 +717,10 @@ __device__ __forceinline__ bool setup_range(const PartialParams& p, const CUtens
     sh.first_stamped = 0;
 #endif
     fence_mbar_init();
-    prefetch_tensormap(tm_k);
-    prefetch_tensormap(tm_v);
+    if constexpr (kFmt != XQA_KV_E2M1) {
+      prefetch_tensormap(tm_k);
+      prefetch_tensormap(tm_v);
+    }
   }
   // Also before the wait, and only a hint: the first pages this CTA index
   // streamed in the previous call (usually the same pages), fetched into L2
@@ -600,7 +729,13 @@ __device__ __forceinline__ bool setup_range(const PartialParams& p, const CUtens
   // the tensor fetches nothing).
   if (p.hints != nullptr && tid < kHintPages) {
     const int y = ld_relaxed_gpu(p.hints + (size_t)cta * kHintPages + tid);
-    if (y >= 0) {
+    if constexpr (kFmt == XQA_KV_E2M1) {
+      const uint32_t slice = (uint32_t)y / kBlockSize;  // any word: only slices of the pool
+      if (y >= 0 && slice < (uint32_t)p.num_blocks * (uint32_t)p.num_kv_heads) {
+        bulk_prefetch(p.k_pool + (size_t)slice * kSliceBytes4, kSliceBytes4);
+        bulk_prefetch(p.v_pool + (size_t)slice * kSliceBytes4, kSliceBytes4);
+      }
+    } else if (y >= 0) {
       if (p.kv_layout == XQA_LAYOUT_HND) {
         tma_prefetch_2d(tm_k, 0, y);
         tma_prefetch_2d(tm_v, 0, y);
@@ -791,8 +926,8 @@ __device__ __forceinline__ bool setup_range(const PartialParams& p, const CUtens
 // first and the last page of the range's first and last segment (two 64-bit
 // divisions each), which the end of the range needs for the merge tickets and
 // the final merge and would otherwise compute on its critical path.
-template <int NT>
-__device__ __forceinline__ void piece_owners(CtaShared<NT>& sh, const RangeView& rv) {
+template <class Sh>
+__device__ __forceinline__ void piece_owners(Sh& sh, const RangeView& rv) {
   const long long line = sh.cost_line;
   const int s_last = find_segment(rv.segs, rv.s_first, rv.s_hi + 1, rv.cend - 1);
 #pragma unroll 1
@@ -807,20 +942,24 @@ __device__ __forceinline__ void piece_owners(CtaShared<NT>& sh, const RangeView&
 // Lane 0 of a warp: the two TMA loads (K and V slice of one page) into ring
 // slot `slot`, completing on its barrier; a page with a bad block id is
 // flagged instead (the slot's barrier completes without data).
-template <int NT>
+template <int kFmt, class Sh>
 __device__ __forceinline__ void issue_page(const PartialParams& p, const CUtensorMap* tm_k,
-                                           const CUtensorMap* tm_v, CtaShared<NT>& sh,
+                                           const CUtensorMap* tm_v, Sh& sh,
                                            uint8_t* stages, int slot, int y, int bad, int sg,
                                            uint64_t policy) {
-  uint8_t* st = stages + slot * kStageBytes;
+  uint8_t* st = stages + slot * Ring<kFmt>::kStage;
   sh.stage_bad[slot] = bad;
   fence_proxy_async_smem();  // this slot's earlier shared reads come before the TMA writes
   if (bad) {
     record_status(&sh.cta_status, XQA_ERR_BAD_BLOCK_ID);
     mbar_arrive(&sh.full_bar[slot]);
   } else {
-    mbar_arrive_expect_tx(&sh.full_bar[slot], kStageBytes);
-    if (p.kv_layout == XQA_LAYOUT_HND) {
+    mbar_arrive_expect_tx(&sh.full_bar[slot], Ring<kFmt>::kStage);
+    if constexpr (kFmt == XQA_KV_E2M1) {
+      const size_t at = (size_t)(y / kBlockSize) * kSliceBytes4;  // y: as in an HND pool
+      bulk_load(st, p.k_pool + at, kSliceBytes4, &sh.full_bar[slot], policy);
+      bulk_load(st + kSliceBytes4, p.v_pool + at, kSliceBytes4, &sh.full_bar[slot], policy);
+    } else if (p.kv_layout == XQA_LAYOUT_HND) {
       tma_load_2d(st, tm_k, &sh.full_bar[slot], 0, y, policy);
       tma_load_2d(st + kPageBytes, tm_v, &sh.full_bar[slot], 0, y, policy);
     } else {  // NHD: box (128 dims, 1 kv head, 16 tokens) at (0, kvh, page*16)
@@ -838,7 +977,8 @@ __device__ __forceinline__ void issue_page(const PartialParams& p, const CUtenso
 // token within the sequence. A wait that runs out marks the warp's segment
 // state poisoned and the CTA aborted.
 template <int kFmt, int NT, bool kMulti, typename Refill>
-__device__ __forceinline__ void consume_pages(const PartialParams& p, CtaShared<NT>& sh,
+__device__ __forceinline__ void consume_pages(const PartialParams& p,
+                                              CtaShared<NT, Ring<kFmt>::kDepth>& sh,
                                               const uint8_t* stages, int slot0, uint32_t ph0,
                                               int slot1, uint32_t ph1, bool pair, int t0, int t1,
                                               int ctx, WarpState<NT>& st,
@@ -862,12 +1002,18 @@ __device__ __forceinline__ void consume_pages(const PartialParams& p, CtaShared<
     stamp(3);
   }
 #endif
-  const uint8_t* stg0 = stages + slot0 * kStageBytes;
-  const uint8_t* stg1 = stages + slot1 * kStageBytes;
+  using Regs = typename PageOf<kFmt>::Regs;
+  const uint8_t* stg0 = stages + slot0 * Ring<kFmt>::kStage;
+  const uint8_t* stg1 = stages + slot1 * Ring<kFmt>::kStage;
   const bool bad0 = sh.stage_bad[slot0] != 0, bad1 = pair && sh.stage_bad[slot1] != 0;
-  PageRegs regs[2];
-  regs[0] = load_page(stg0, stg0 + kPageBytes, g, c);
-  if (pair) regs[1] = load_page(stg1, stg1 + kPageBytes, g, c);
+  Regs regs[2];
+  if constexpr (kFmt == XQA_KV_E2M1) {
+    regs[0] = load_page4(stg0, stg0 + kSliceBytes4, g, c);
+    if (pair) regs[1] = load_page4(stg1, stg1 + kSliceBytes4, g, c);
+  } else {
+    regs[0] = load_page(stg0, stg0 + kPageBytes, g, c);
+    if (pair) regs[1] = load_page(stg1, stg1 + kPageBytes, g, c);
+  }
   // The pages are in registers: refill their slots with the pages kStages
   // ahead right away (warp-uniform decision), before the math.
   if (!__any_sync(kFull, *abort != 0)) {
@@ -881,12 +1027,12 @@ __device__ __forceinline__ void consume_pages(const PartialParams& p, CtaShared<
   } else {
     if (bad0 || bad1) poisoned = 1;
     if (!bad0) {
-      const PageRegs one[1] = {regs[0]};
+      const Regs one[1] = {regs[0]};
       const int tk[1] = {t0}, nv[1] = {nv0};
       process_pages<kFmt, 1, NT, kMulti>(st, one, qf, tk, nv, sl, scale_log2, g, c);
     }
     if (pair && !bad1) {
-      const PageRegs one[1] = {regs[1]};
+      const Regs one[1] = {regs[1]};
       const int tk[1] = {t1}, nv[1] = {nv1};
       process_pages<kFmt, 1, NT, kMulti>(st, one, qf, tk, nv, sl, scale_log2, g, c);
     }
@@ -912,8 +1058,8 @@ __device__ __forceinline__ SegLimits<NT> seg_limits(const PartialParams& p, int 
 // Merge of one buffered segment by all threads (column col, dims dq..dq+3):
 // the 8 warps' (m, l, O) combine in shared memory; a segment owned whole is
 // normalised and written as fp16, a split piece goes to partial slot cta + s.
-template <int NT>
-__device__ __forceinline__ void merge_buffer(const PartialParams& p, CtaShared<NT>& sh,
+template <int NT, class Sh>
+__device__ __forceinline__ void merge_buffer(const PartialParams& p, Sh& sh,
                                              const float* merge_bufs, int mb, int ncols,
                                              float v_scale) {
   using Geom = PartialGeom<NT>;
@@ -979,7 +1125,8 @@ __device__ __forceinline__ void merge_buffer(const PartialParams& p, CtaShared<N
 // warps when the buffer is next reused or at the end of the range.
 template <int kFmt, int NT, bool kMulti>
 __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUtensorMap* tm_k,
-                                               const CUtensorMap* tm_v, CtaShared<NT>& sh,
+                                               const CUtensorMap* tm_v,
+                                               CtaShared<NT, Ring<kFmt>::kDepth>& sh,
                                                const CtaSmem<NT>& sm, const RangeView& rv,
                                                float scale_log2, float v_scale, uint64_t policy,
                                                WarpState<NT>& st, uint32_t (&qf)[NT][16],
@@ -988,6 +1135,7 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
   using Geom = PartialGeom<NT>;
   constexpr int kCols = Geom::kCols;
   constexpr int kBufs = Geom::kMergeBufs;
+  constexpr int kDepth = Ring<kFmt>::kDepth;
   constexpr bool kPrefetchQ = NT == 1;  // registers: two-tile kernels load Q per segment
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -1020,14 +1168,14 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
     const int y = __shfl_sync(kFull, cur.y, k - cur_base);
     const int bad = __shfl_sync(kFull, cur.bad, k - cur_base);
     const int sg = __shfl_sync(kFull, cur.seg, k - cur_base);
-    const int slot = (warp + kWarps * k) % kStages;
+    const int slot = (warp + kWarps * k) % kDepth;
     __syncwarp();  // all lanes' reads of this slot's previous page are done
-    if (lane == 0) issue_page<NT>(p, tm_k, tm_v, sh, sm.stages, slot, y, bad, sg, policy);
+    if (lane == 0) issue_page<kFmt>(p, tm_k, tm_v, sh, sm.stages, slot, y, bad, sg, policy);
     __syncwarp();
   };
 #pragma unroll 1
-  for (int i = 0; i < kLookahead; ++i) issue_next();
-  if (warp == kWarps - 1 && lane == 0) piece_owners<NT>(sh, rv);
+  for (int i = 0; i < kDepth / kWarps; ++i) issue_next();
+  if (warp == kWarps - 1 && lane == 0) piece_owners(sh, rv);
 
   int s = s_first;
   int q0 = 0;
@@ -1060,8 +1208,8 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
     for (int q = q0 + ((warp - q0 % kWarps) + kWarps) % kWarps; q < qe; q += 2 * kWarps) {
       const bool pair = q + kWarps < qe;
       const int j0 = cbeg + q - sb;  // page index within the sequence
-      consume_pages<kFmt, NT, kMulti>(p, sh, sm.stages, q % kStages, (q / kStages) & 1,
-                                      (q + kWarps) % kStages, ((q + kWarps) / kStages) & 1, pair,
+      consume_pages<kFmt, NT, kMulti>(p, sh, sm.stages, q % kDepth, (q / kDepth) & 1,
+                                      (q + kWarps) % kDepth, ((q + kWarps) / kDepth) & 1, pair,
                                       j0 * kBlockSize, (j0 + kWarps) * kBlockSize, ctx, st, qf,
                                       sl, scale_log2, g, c, lane, poisoned, issue_next);
     }
@@ -1232,8 +1380,8 @@ __device__ __forceinline__ void merge_staged(const PartialParams& p, uint8_t* st
 // call. A CTA that aborted (its ring may still receive page copies) writes
 // NaN rows instead. Out of line: the code of the page loop does not depend
 // on it.
-template <int NT>
-__device__ __noinline__ void merge_shared(const PartialParams& p, CtaShared<NT>& sh,
+template <int NT, class Sh>
+__device__ __noinline__ void merge_shared(const PartialParams& p, Sh& sh,
                                           uint8_t* stage, float v_scale) {
   const int tid = threadIdx.x, warp = tid >> 5;
   const int ncols = p.group * p.q_len;
@@ -1275,8 +1423,9 @@ __device__ __noinline__ void merge_shared(const PartialParams& p, CtaShared<NT>&
 // would). The tickets are device-wide atomic round trips taken once per piece
 // after the whole range, so no mid-range segment boundary stalls the CTA on
 // them. Last, after an abort, the copies still in flight are waited for.
-template <int NT>
-__device__ __forceinline__ void finish_range(const PartialParams& p, CtaShared<NT>& sh,
+template <int kFmt, int NT>
+__device__ __forceinline__ void finish_range(const PartialParams& p,
+                                             CtaShared<NT, Ring<kFmt>::kDepth>& sh,
                                              const CtaSmem<NT>& sm, const RangeView& rv,
                                              float v_scale, int issued, int kseg) {
   constexpr int kCols = PartialGeom<NT>::kCols;
@@ -1399,12 +1548,13 @@ __device__ __forceinline__ void finish_range(const PartialParams& p, CtaShared<N
   if (sh.abort_flag) {
     int never = 0;
     volatile int* no_abort = &never;
-    // only the last kLookahead issued pages can still be in flight: every
+    // only the last kDepth / kWarps issued pages can still be in flight: every
     // earlier one was waited for before its slot was reissued
-    const int first = issued > kLookahead ? issued - kLookahead : 0;
+    constexpr int kDepth = Ring<kFmt>::kDepth;
+    const int first = issued > kDepth / kWarps ? issued - kDepth / kWarps : 0;
     for (int k = first; k < issued; ++k) {
       const int q = warp + kWarps * k;
-      const bool ok = mbar_wait_bounded(&sh.full_bar[q % kStages], (q / kStages) & 1, no_abort);
+      const bool ok = mbar_wait_bounded(&sh.full_bar[q % kDepth], (q / kDepth) & 1, no_abort);
       if (!__all_sync(kFull, ok)) {
         if ((threadIdx.x & 31) == 0) atomicExch(&sh.cta_status, XQA_ERR_DRAIN_TIMEOUT);
         break;
@@ -1415,8 +1565,8 @@ __device__ __forceinline__ void finish_range(const PartialParams& p, CtaShared<N
 
 // Every CTA of the launch writes its status word once, at exit (the words of
 // one call need no reset: the next call overwrites all it reads).
-template <int NT>
-__device__ __forceinline__ void publish_status(const PartialParams& p, CtaShared<NT>& sh) {
+template <class Sh>
+__device__ __forceinline__ void publish_status(const PartialParams& p, Sh& sh) {
   __syncthreads();
   stamp(7);
   if (threadIdx.x == 0) p.status[blockIdx.x] = sh.cta_status;
@@ -1429,13 +1579,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     partial_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const PartialParams p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) CtaShared<NT> sh;
+  __shared__ __align__(8) CtaShared<NT, Ring<kFmt>::kDepth> sh;
   griddep_launch_dependents();  // a dependent next kernel waits for this grid itself
   stamp(0);
   const CtaSmem<NT> sm = carve_smem<NT>(smem_raw);
   RangeView rv;
-  if (!setup_range<NT>(p, &tm_k, &tm_v, sh, sm, rv)) {
-    publish_status<NT>(p, sh);
+  if (!setup_range<kFmt, NT>(p, &tm_k, &tm_v, sh, sm, rv)) {
+    publish_status(p, sh);
     return;
   }
   // per-tensor scales: host values, or device scalars read when the kernel
@@ -1452,8 +1602,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int kseg = 0;    // segments of this range handed to the merge buffers
   cta_mode_range<kFmt, NT, kMulti>(p, &tm_k, &tm_v, sh, sm, rv, scale_log2, v_scale, policy, st, qf,
                                    qf_next, q_next_seg, issued, kseg);
-  finish_range<NT>(p, sh, sm, rv, v_scale, issued, kseg);
-  publish_status<NT>(p, sh);
+  finish_range<kFmt, NT>(p, sh, sm, rv, v_scale, issued, kseg);
+  publish_status(p, sh);
 }
 
 // The same kernel with a second way to work a range (warp mode): when the
@@ -1470,15 +1620,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const PartialParams p) {
   static_assert(NT == 1, "warp mode holds one column tile");
   constexpr bool kPrefetchQ = true;
+  constexpr int kDepth = Ring<kFmt>::kDepth, kAhead = kDepth / kWarps;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) CtaShared<NT> sh;
+  __shared__ __align__(8) CtaShared<NT, Ring<kFmt>::kDepth> sh;
   griddep_launch_dependents();  // a dependent next kernel waits for this grid itself
   stamp(0);
   const int ncols = p.group * p.q_len;
   const CtaSmem<NT> sm = carve_smem<NT>(smem_raw);
   RangeView rv;
-  if (!setup_range<NT>(p, &tm_k, &tm_v, sh, sm, rv)) {
-    publish_status<NT>(p, sh);
+  if (!setup_range<kFmt, NT>(p, &tm_k, &tm_v, sh, sm, rv)) {
+    publish_status(p, sh);
     return;
   }
   const float k_scale = p.k_scale_ptr ? __ldg(p.k_scale_ptr) : p.k_scale;
@@ -1561,9 +1712,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int bad = __shfl_sync(kFull, wcur.bad, ioff);
           ++ioff;
           const int k = issued++;
-          const int slot = (warp + kWarps * k) % kStages;
+          const int slot = (warp + kWarps * k) % kDepth;
           __syncwarp();  // all lanes' reads of this slot's previous page are done
-          if (lane == 0) issue_page<NT>(p, &tm_k, &tm_v, sh, sm.stages, slot, y, bad, wcur.seg, policy);
+          if (lane == 0) issue_page<kFmt>(p, &tm_k, &tm_v, sh, sm.stages, slot, y, bad, wcur.seg, policy);
           __syncwarp();
           return;
         }
@@ -1575,8 +1726,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
 #pragma unroll 1
-    for (int i = 0; i < kLookahead; ++i) issue_next_w();
-    if (warp == kWarps - 1 && lane == 0) piece_owners<NT>(sh, rv);
+    for (int i = 0; i < kAhead; ++i) issue_next_w();
+    if (warp == kWarps - 1 && lane == 0) piece_owners(sh, rv);
 
     int k = 0;  // this warp's running page index (ring slot and phase)
     for (int j = next_piece(warp); j < nsr; j = next_piece(j + kWarps)) {
@@ -1605,9 +1756,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int o = 0; o < len; o += 2) {
         const bool pair = o + 1 < len;
         const int t0 = (pb + o - sb) * kBlockSize;
-        consume_pages<kFmt, NT, kMulti>(p, sh, sm.stages, (warp + kWarps * k) % kStages,
-                                        (k / kLookahead) & 1, (warp + kWarps * (k + 1)) % kStages,
-                                        ((k + 1) / kLookahead) & 1, pair, t0, t0 + kBlockSize, ctx,
+        consume_pages<kFmt, NT, kMulti>(p, sh, sm.stages, (warp + kWarps * k) % kDepth,
+                                        (k / kAhead) & 1, (warp + kWarps * (k + 1)) % kDepth,
+                                        ((k + 1) / kAhead) & 1, pair, t0, t0 + kBlockSize, ctx,
                                         st, qf, sl, scale_log2, g, c, lane, poisoned, issue_next_w);
         k += pair ? 2 : 1;
       }
@@ -1649,9 +1800,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  finish_range<NT>(p, sh, sm, rv, v_scale, issued, kseg);
-  publish_status<NT>(p, sh);
+  finish_range<kFmt, NT>(p, sh, sm, rv, v_scale, issued, kseg);
+  publish_status(p, sh);
 }
+
+namespace {
+
+// The instance of one format: several columns need two tiles, one-tile shapes with
+// enough segments the warp-capable kernel.
+template <int kFmt>
+cudaError_t launch_format(const cudaLaunchConfig_t& cfg, bool wm, int nt, bool multi,
+                          const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                          const PartialParams& p) {
+  if (wm)
+    return multi ? cudaLaunchKernelEx(&cfg, partial_kernel_wm<kFmt, 1, true>, tm_k, tm_v, p)
+                 : cudaLaunchKernelEx(&cfg, partial_kernel_wm<kFmt, 1, false>, tm_k, tm_v, p);
+  if (nt == 2) return cudaLaunchKernelEx(&cfg, partial_kernel<kFmt, 2, true>, tm_k, tm_v, p);
+  return multi ? cudaLaunchKernelEx(&cfg, partial_kernel<kFmt, 1, true>, tm_k, tm_v, p)
+               : cudaLaunchKernelEx(&cfg, partial_kernel<kFmt, 1, false>, tm_k, tm_v, p);
+}
+
+}  // namespace
 
 cudaError_t launch_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                            const PartialParams& p, int n_max, cudaStream_t stream) {
@@ -1676,37 +1845,34 @@ cudaError_t launch_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
   // CTA take the warp-capable kernel
   const bool multi = p.q_len > 1;
   const bool wm = nt == 1 && (long long)p.batch * p.num_kv_heads >= (long long)kWarpModeMinPieces * n_max;
-  if (wm) {
-    if (p.kv_dtype == XQA_KV_E4M3)
-      return multi ? cudaLaunchKernelEx(&cfg, partial_kernel_wm<XQA_KV_E4M3, 1, true>, tm_k, tm_v, p)
-                   : cudaLaunchKernelEx(&cfg, partial_kernel_wm<XQA_KV_E4M3, 1, false>, tm_k, tm_v, p);
-    return multi ? cudaLaunchKernelEx(&cfg, partial_kernel_wm<XQA_KV_E5M2, 1, true>, tm_k, tm_v, p)
-                 : cudaLaunchKernelEx(&cfg, partial_kernel_wm<XQA_KV_E5M2, 1, false>, tm_k, tm_v, p);
+  switch (p.kv_dtype) {
+    case XQA_KV_E2M1: return launch_format<XQA_KV_E2M1>(cfg, wm, nt, multi, tm_k, tm_v, p);
+    case XQA_KV_E4M3: return launch_format<XQA_KV_E4M3>(cfg, wm, nt, multi, tm_k, tm_v, p);
+    default: return launch_format<XQA_KV_E5M2>(cfg, wm, nt, multi, tm_k, tm_v, p);
   }
-  if (p.kv_dtype == XQA_KV_E4M3) {
-    if (nt == 2) return cudaLaunchKernelEx(&cfg, partial_kernel<XQA_KV_E4M3, 2, true>, tm_k, tm_v, p);
-    return multi ? cudaLaunchKernelEx(&cfg, partial_kernel<XQA_KV_E4M3, 1, true>, tm_k, tm_v, p)
-                 : cudaLaunchKernelEx(&cfg, partial_kernel<XQA_KV_E4M3, 1, false>, tm_k, tm_v, p);
-  }
-  if (nt == 2) return cudaLaunchKernelEx(&cfg, partial_kernel<XQA_KV_E5M2, 2, true>, tm_k, tm_v, p);
-  return multi ? cudaLaunchKernelEx(&cfg, partial_kernel<XQA_KV_E5M2, 1, true>, tm_k, tm_v, p)
-               : cudaLaunchKernelEx(&cfg, partial_kernel<XQA_KV_E5M2, 1, false>, tm_k, tm_v, p);
 }
 
-cudaError_t set_partial_attributes() {
+namespace {
+
+template <int kFmt>
+cudaError_t set_format_attributes() {
   const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
   const int s1 = PartialGeom<1>::kSmem, s2 = PartialGeom<2>::kSmem;
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(partial_kernel<XQA_KV_E5M2, 1, false>, a, s1)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(partial_kernel<XQA_KV_E5M2, 1, true>, a, s1)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(partial_kernel<XQA_KV_E5M2, 2, true>, a, s2)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(partial_kernel<XQA_KV_E4M3, 1, false>, a, s1)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(partial_kernel<XQA_KV_E4M3, 1, true>, a, s1)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(partial_kernel<XQA_KV_E4M3, 2, true>, a, s2)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(partial_kernel_wm<XQA_KV_E5M2, 1, false>, a, s1)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(partial_kernel_wm<XQA_KV_E5M2, 1, true>, a, s1)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(partial_kernel_wm<XQA_KV_E4M3, 1, false>, a, s1)) != cudaSuccess) return e;
-  return cudaFuncSetAttribute(partial_kernel_wm<XQA_KV_E4M3, 1, true>, a, s1);
+  if ((e = cudaFuncSetAttribute(partial_kernel<kFmt, 1, false>, a, s1)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(partial_kernel<kFmt, 1, true>, a, s1)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(partial_kernel<kFmt, 2, true>, a, s2)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(partial_kernel_wm<kFmt, 1, false>, a, s1)) != cudaSuccess) return e;
+  return cudaFuncSetAttribute(partial_kernel_wm<kFmt, 1, true>, a, s1);
+}
+
+}  // namespace
+
+cudaError_t set_partial_attributes() {
+  cudaError_t e;
+  if ((e = set_format_attributes<XQA_KV_E5M2>()) != cudaSuccess) return e;
+  if ((e = set_format_attributes<XQA_KV_E4M3>()) != cudaSuccess) return e;
+  return set_format_attributes<XQA_KV_E2M1>();
 }
 
 }  // namespace xqa

@@ -46,8 +46,11 @@ xqa_status_t resolve(const xqa_shape_t* s, Resolved* r) {
   if (s->max_blocks_per_seq < 1 || s->num_blocks < 1) return XQA_ERR_SHAPE;
   if (s->max_ctas < 0 || s->min_pages_per_cta < 0) return XQA_ERR_SHAPE;
   if (s->merge_mode != 0 && s->merge_mode != 1) return XQA_ERR_SHAPE;
-  if (s->kv_dtype != XQA_KV_E5M2 && s->kv_dtype != XQA_KV_E4M3) return XQA_ERR_SHAPE;
-  if (s->kv_layout != XQA_LAYOUT_HND && s->kv_layout != XQA_LAYOUT_NHD) return XQA_ERR_SHAPE;
+  if (s->kv_dtype != XQA_KV_E5M2 && s->kv_dtype != XQA_KV_E4M3 && s->kv_dtype != XQA_KV_E2M1)
+    return XQA_ERR_SHAPE;
+  if (s->kv_layout != XQA_LAYOUT_HND &&
+      (s->kv_layout != XQA_LAYOUT_NHD || s->kv_dtype == XQA_KV_E2M1))
+    return XQA_ERR_SHAPE;
   const int q_len = s->q_len > 0 ? s->q_len : 1;
   if (s->q_len < 0 || group * q_len > xqa::kMaxCols) return XQA_ERR_SHAPE;
   // int32 index arithmetic on the device: pool rows, total pages, segments
@@ -211,9 +214,11 @@ xqa_status_t attend_partial_impl(const void* q, const uint8_t* k_cache, const ui
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
     return XQA_ERR_ALIGN;
   if ((st = ensure_device_setup()) != XQA_OK) return st;
-  alignas(64) CUtensorMap tm_k, tm_v;
-  if ((st = encode_pool_map(&tm_k, k_cache, r)) != XQA_OK) return st;
-  if ((st = encode_pool_map(&tm_v, v_cache, r)) != XQA_OK) return st;
+  alignas(64) CUtensorMap tm_k = {}, tm_v = {};
+  if (r.kv_dtype != XQA_KV_E2M1) {  // 4-bit slices are plain contiguous copies
+    if ((st = encode_pool_map(&tm_k, k_cache, r)) != XQA_OK) return st;
+    if ((st = encode_pool_map(&tm_v, v_cache, r)) != XQA_OK) return st;
+  }
   uint8_t* base = reinterpret_cast<uint8_t*>(workspace);
   xqa::PartialParams p;
   p.q = reinterpret_cast<const __half*>(q);
@@ -248,6 +253,8 @@ xqa_status_t attend_partial_impl(const void* q, const uint8_t* k_cache, const ui
   p.v_scale = v_scale;
   p.k_scale_ptr = k_scale_ptr;
   p.v_scale_ptr = v_scale_ptr;
+  p.k_pool = k_cache;
+  p.v_pool = v_cache;
   cudaError_t e = xqa::launch_partial(tm_k, tm_v, p, r.n_max, (cudaStream_t)stream);
   return e == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
 }

@@ -51,6 +51,22 @@ constexpr int kGroup4 = 16;
 constexpr int kCodeBytes4 = kBlockSize * kHeadDim / 2;
 constexpr int kSliceBytes4 = kCodeBytes4 + kBlockSize * (kHeadDim / kGroup4);
 static_assert(kSliceBytes4 == XQA_E2M1_SLICE_BYTES, "slice size in the header");
+// The partial kernel's page ring by format: bytes of a (page, kv head) slice, of a
+// stage (K and V slice), stages (a multiple of kWarps). The 4-bit ring holds 56
+// stages in the same 128 KB.
+template <int kFmt>
+struct Ring {
+  static constexpr int kPage = kPageBytes;
+  static constexpr int kStage = kStageBytes;
+  static constexpr int kDepth = kStages;
+};
+template <>
+struct Ring<XQA_KV_E2M1> {
+  static constexpr int kPage = kSliceBytes4;
+  static constexpr int kStage = 2 * kSliceBytes4;
+  static constexpr int kDepth = 56;
+  static_assert(kDepth % kWarps == 0 && kDepth * kStage <= kStages * kStageBytes, "ring");
+};
 constexpr int kDefaultMinPagesPerCta = 16;
 // Split rule cost line: every non-empty segment costs kSegCost page units on
 // top of its pages (a segment switch inside a CTA, and the split-piece merge
@@ -272,6 +288,46 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z),
       "l"(policy)
       : "memory");
+}
+
+// Contiguous bulk copy into shared memory, completing on `bar` (16-byte aligned
+// addresses, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar,
+                                          uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1], %2, [%3], %4;" ::"r"(smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
+}
+
+// L2 prefetch of a contiguous run (aligned as for bulk_load).
+__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ uint2 lds64(const uint8_t* p) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(smem_addr(p)));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t lds_u16(const uint8_t* p) {
+  unsigned short v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(smem_addr(p)));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t lds_u8(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(smem_addr(p)));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
 __device__ __forceinline__ uint4 lds128(const uint8_t* p) {

@@ -31,6 +31,8 @@ struct PartialParams {
   float k_scale, v_scale;    // per-tensor scales (used when the pointers are null)
   const float* k_scale_ptr;  // optional device scalars, read when the kernel runs
   const float* v_scale_ptr;
+  const uint8_t* k_pool;     // the caches (4-bit: read by plain bulk copies)
+  const uint8_t* v_pool;
 };
 
 struct CombineParams {
