@@ -15,6 +15,7 @@ The names mirror the C ABI declared in ``include/xqa.h``:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -171,8 +172,8 @@ def _check(code: int, where: str) -> None:
 
 
 def _stream_handle(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # torch.cuda.current_stream() without the Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream)
 
 
@@ -318,23 +319,29 @@ def xqa_dequant_e4m3(codes: torch.Tensor, scale: float = 1.0, with_f32: bool = T
     return _dequant("xqa_dequant_e4m3", codes, scale, with_f32, stream)
 
 
-def _device_stream(stream, *tensors) -> int:
-    """Handle of ``stream`` (default: the current one). The library works on the
-    current device, so the stream and every tensor must be there."""
+def _device_stream(stream):
+    """(current device, handle of ``stream`` or of its current stream). The
+    library works on the current device: the stream must be there, and every
+    tensor (checked where its pointer is taken)."""
+    dev = torch.cuda.current_device()
     if stream is None:
-        stream = torch.cuda.current_stream()
-    elif stream.device_index != torch.cuda.current_device():
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
         raise ValueError("the stream belongs to another device than the current one")
-    for t in tensors:
-        if t is not None and t.device.index != stream.device_index:
-            raise ValueError(f"a tensor is on {t.device}, the current device is "
-                             f"cuda:{stream.device_index}")
-    return int(stream.cuda_stream)
+    return dev, int(stream.cuda_stream)
+
+
+def _on(t: torch.Tensor, dtype, dev: int, name: str) -> int:
+    """Pointer of a contiguous tensor of ``dtype`` on device ``dev``."""
+    ptr = _cuda(t, dtype, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    return ptr
 
 
 def _heads(t: torch.Tensor, name: str, dtype=None):
-    """Pointer, row stride and head stride of a [rows, heads, 128] view whose
-    last dim is contiguous (strides of dims of size 1 play no part)."""
+    """(row stride, head stride) of a [rows, heads, 128] CUDA view whose last
+    dim is contiguous (strides of dims of size 1 play no part)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in ROW_DTYPES or (dtype is not None and t.dtype != dtype):
@@ -342,14 +349,16 @@ def _heads(t: torch.Tensor, name: str, dtype=None):
     if t.dim() != 3:
         raise ValueError(f"{name} must be [rows, heads, head_dim], got {tuple(t.shape)}")
     n, h, d = t.shape
-    if t.numel() == 0:
-        return t.data_ptr(), h * d, d
+    if n == 0 or h == 0:
+        return h * d, d
     rs, hs, es = t.stride()
-    hs = hs if h > 1 else d
-    rs = rs if n > 1 else h * d
-    if (d > 1 and es != 1) or rs <= 0 or hs <= 0:
+    if h == 1:
+        hs = d
+    if n == 1:
+        rs = h * d
+    if (es != 1 and d > 1) or rs <= 0 or hs <= 0:
         raise ValueError(f"{name}: the last dim must be contiguous and no stride may be 0")
-    return t.data_ptr(), rs, hs
+    return rs, hs
 
 
 def _cache_dims(cache: torch.Tensor, kv_dtype: str, kv_layout: str):
@@ -366,39 +375,50 @@ def _cache_dims(cache: torch.Tensor, kv_dtype: str, kv_layout: str):
     return (nb, a, b) if kv_layout == "hnd" else (nb, b, a)
 
 
-def _scale_args(k_scale, v_scale):
-    """(k value, v value, k pointer, v pointer): floats, or CUDA tensors of one element."""
-    val, ptr = [], []
-    for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        dev = isinstance(s, torch.Tensor)
-        if dev and s.numel() != 1:
-            raise ValueError(f"{name} must have one element")
-        ptr.append(_cuda(s, torch.float32, name) if dev else None)
-        val.append(0.0 if dev else float(s))
-    return (*val, *ptr)
+def _scale_arg(s, dev: int, name: str):
+    """(value, pointer) of a scale: a float, or a CUDA tensor of one element."""
+    if not isinstance(s, torch.Tensor):
+        return float(s), None
+    if s.numel() != 1:
+        raise ValueError(f"{name} must have one element")
+    return 0.0, _on(s, torch.float32, dev, name)
+
+
+@functools.lru_cache(maxsize=256)
+def _rows_descriptor(*fields) -> XqaRows:
+    return XqaRows(*fields)
 
 
 def _move_rows(fn_name, k, v, cu_seqlens, k_cache, v_cache, block_tables, context_lens, k_scale,
                v_scale, kv_dtype, kv_layout, status, stream):
-    kp, krs, khs = _heads(k, "k")
-    vp, vrs, vhs = _heads(v, "v", k.dtype)
+    dev, handle = _device_stream(stream)
+    krs, khs = _heads(k, "k")
+    vrs, vhs = _heads(v, "v", k.dtype)
     nb, hkv, bs = _cache_dims(k_cache, kv_dtype, kv_layout)
+    n, h, d = k.shape
     b = context_lens.numel()
-    if (v.shape != k.shape or v_cache.shape != k_cache.shape or k.shape[1] != hkv
-            or k.shape[2] != 128 or block_tables.dim() != 2 or block_tables.shape[0] != b
+    if (v.shape != k.shape or v_cache.shape != k_cache.shape or h != hkv or d != 128
+            or block_tables.dim() != 2 or block_tables.shape[0] != b
             or cu_seqlens.numel() != b + 1):
         raise ValueError("inconsistent rows / cache / block_tables / cu_seqlens shapes")
-    rows = XqaRows(b, hkv, 128, bs, block_tables.shape[1], nb, k.shape[0], KV_DTYPES[kv_dtype],
-                   KV_LAYOUTS[kv_layout], ROW_DTYPES[k.dtype], krs, khs, vrs, vhs)
-    caches = (_cuda(k_cache, torch.uint8, "k_cache"), _cuda(v_cache, torch.uint8, "v_cache"))
-    a, c = ((kp, vp), caches) if fn_name == "xqa_append" else (caches, (kp, vp))
-    _check(getattr(load_library(), fn_name)(
-        *a, _cuda(cu_seqlens, torch.int32, "cu_seqlens"),
-        _cuda(block_tables, torch.int32, "block_tables"),
-        _cuda(context_lens, torch.int32, "context_lens"), *_scale_args(k_scale, v_scale), *c,
-        ctypes.byref(rows), None if status is None else _cuda(status, torch.int32, "status"),
-        _device_stream(stream, k, v, k_cache, v_cache, cu_seqlens, block_tables, context_lens,
-                       status)), fn_name)
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError(f"k and v must be on the current device, cuda:{dev}")
+    rows = _rows_descriptor(b, hkv, 128, bs, block_tables.shape[1], nb, n, KV_DTYPES[kv_dtype],
+                            KV_LAYOUTS[kv_layout], ROW_DTYPES[k.dtype], krs, khs, vrs, vhs)
+    kp, vp = k.data_ptr(), v.data_ptr()
+    kc = _on(k_cache, torch.uint8, dev, "k_cache")
+    vc = _on(v_cache, torch.uint8, dev, "v_cache")
+    ks, ksp = _scale_arg(k_scale, dev, "k_scale")
+    vs, vsp = _scale_arg(v_scale, dev, "v_scale")
+    a = (kp, vp, kc, vc) if fn_name == "xqa_append" else (kc, vc, kp, vp)
+    code = getattr(load_library(), fn_name)(
+        a[0], a[1], _on(cu_seqlens, torch.int32, dev, "cu_seqlens"),
+        _on(block_tables, torch.int32, dev, "block_tables"),
+        _on(context_lens, torch.int32, dev, "context_lens"), ks, vs, ksp, vsp, a[2], a[3],
+        ctypes.byref(rows), None if status is None else _on(status, torch.int32, dev, "status"),
+        handle)
+    if code:
+        raise XqaError(code, fn_name)
 
 
 def xqa_append(k, v, cu_seqlens, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale,
@@ -441,15 +461,18 @@ def make_prefill_shape(q, k, v, cu_seqlens_q, causal: bool = True, sm_scale: flo
     [total_k, Hkv, 128] (fp16 or bf16; views whose last dim is contiguous are
     fine) and cu_seqlens_q [B+1]. It holds for every call with tensors of these
     shapes, types and strides (out: contiguous unless given)."""
-    _, qr, qh = _heads(q, "q")
-    _, kr, kh = _heads(k, "k", q.dtype)
-    _, vr, vh = _heads(v, "v", q.dtype)
-    if k.shape != v.shape or k.shape[2] != q.shape[2]:
-        raise ValueError("inconsistent q / k / v shapes")
-    orow, oh = (0, 0) if out is None else _heads(out, "out", q.dtype)[1:]
+    side = _prefill_strides(q, k, v)
+    orow, oh = (0, 0) if out is None else _heads(out, "out", q.dtype)
     return XqaPrefillShape(cu_seqlens_q.numel() - 1, q.shape[1], k.shape[1], q.shape[2],
                            q.shape[0], k.shape[0], ROW_DTYPES[q.dtype], int(bool(causal)),
-                           float(sm_scale), int(max_ctas), qr, qh, kr, kh, vr, vh, orow, oh)
+                           float(sm_scale), int(max_ctas), *side, orow, oh)
+
+
+def _prefill_strides(q, k, v):
+    side = _heads(q, "q") + _heads(k, "k", q.dtype) + _heads(v, "v", q.dtype)
+    if k.shape != v.shape or k.shape[2] != q.shape[2]:
+        raise ValueError("inconsistent q / k / v shapes")
+    return side
 
 
 def xqa_prefill_workspace_size(shape: XqaPrefillShape) -> int:
@@ -476,43 +499,45 @@ def xqa_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=None, lse=None, wo
     (fp32 [total_q, Hq], optional) receives the log-sum-exp. Returns ``out``;
     rows that see nothing are zero, rows behind the last sequence are not
     written."""
-    made = shape is None
-    if made:
+    dev, handle = _device_stream(stream)
+    if shape is None:
         shape = make_prefill_shape(q, k, v, cu_seqlens_q, causal, sm_scale, max_ctas, out)
+    else:
+        s = shape
+        if _prefill_strides(q, k, v) != (s.q_row_stride, s.q_head_stride, s.k_row_stride,
+                                         s.k_head_stride, s.v_row_stride, s.v_head_stride) or (
+                s.total_q, s.num_q_heads, s.head_dim, s.total_k, s.num_kv_heads, s.dtype) != (
+                *q.shape, k.shape[0], k.shape[1], ROW_DTYPES[q.dtype]):
+            raise ValueError("q, k, v do not match the shape descriptor")
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if shape.out_row_stride not in (0, q.shape[1] * q.shape[2]) or (
+                shape.out_head_stride not in (0, q.shape[2])):
+            raise ValueError("the shape descriptor names strides of out: pass out")
+    elif out.shape != q.shape or _heads(out, "out", q.dtype) != (
+            shape.out_row_stride or shape.num_q_heads * 128, shape.out_head_stride or 128):
+        raise ValueError("out does not match q or the shape descriptor")
     if workspace is None:
         workspace = alloc_prefill_workspace(shape, q.device)
-    qp, qr, qh = _heads(q, "q")
-    kp, kr, kh = _heads(k, "k", q.dtype)
-    vp, vr, vh = _heads(v, "v", q.dtype)
-    op, orow, oh = _heads(out, "out", q.dtype)
-    s = shape
-    if not made and (
-            (s.total_q, s.num_q_heads, s.head_dim) != q.shape or q.dtype not in ROW_DTYPES
-            or ROW_DTYPES[q.dtype] != s.dtype
-            or (s.q_row_stride, s.q_head_stride, s.k_row_stride, s.k_head_stride, s.v_row_stride,
-                s.v_head_stride) != (qr, qh, kr, kh, vr, vh)):
-        raise ValueError("q, k, v do not match the shape descriptor")
-    if ((s.total_k, s.num_kv_heads, s.head_dim) != k.shape or k.shape != v.shape
-            or out.shape != q.shape
-            or (s.out_row_stride or s.num_q_heads * 128, s.out_head_stride or 128) != (orow, oh)):
-        raise ValueError("k, v or out do not match the shape descriptor")
-    if cu_seqlens_q.numel() != s.batch + 1 or cu_seqlens_k.numel() != s.batch + 1:
+    if cu_seqlens_q.numel() != shape.batch + 1 or cu_seqlens_k.numel() != shape.batch + 1:
         raise ValueError("cu_seqlens_q and cu_seqlens_k must have batch + 1 entries")
     lp = None
     if lse is not None:
-        lp = _cuda(lse, torch.float32, "lse")
+        lp = _on(lse, torch.float32, dev, "lse")
         if lse.shape != q.shape[:2]:
             raise ValueError("lse must be [total_q, num_q_heads]")
-    _check(load_library().xqa_prefill(
-        qp, kp, vp, _cuda(cu_seqlens_q, torch.int32, "cu_seqlens_q"),
-        _cuda(cu_seqlens_k, torch.int32, "cu_seqlens_k"), op, lp, ctypes.byref(shape),
-        _cuda(workspace, torch.uint8, "workspace"), workspace.numel(),
-        _device_stream(stream, q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, workspace)),
-        "xqa_prefill")
+    for x in (q, k, v, out):
+        if x.get_device() != dev:
+            raise ValueError(f"q, k, v and out must be on the current device, cuda:{dev}")
+    code = load_library().xqa_prefill(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _on(cu_seqlens_q, torch.int32, dev, "cu_seqlens_q"),
+        _on(cu_seqlens_k, torch.int32, dev, "cu_seqlens_k"), out.data_ptr(), lp,
+        ctypes.byref(shape), _on(workspace, torch.uint8, dev, "workspace"), workspace.numel(),
+        handle)
+    if code:
+        raise XqaError(code, "xqa_prefill")
     return out
 
 

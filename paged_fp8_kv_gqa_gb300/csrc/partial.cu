@@ -119,8 +119,9 @@ __device__ __forceinline__ void stamp_after(int, int) {}
 
 namespace {
 
+template <class G>
 __device__ __forceinline__ void consumer_bar() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(G::kThreads) : "memory");
 }
 
 // Largest s in [lo, nseg) with seg_start[s] <= page, given seg_start[lo] <= page
@@ -142,6 +143,7 @@ struct PageBatch {
   int seg;  // segment of the page
 };
 
+template <int kWarps>
 __device__ __forceinline__ PageBatch load_batch(const PartialParams& p, const int32_t* segs,
                                                 int s_first, int nseg, int cbeg, int npages,
                                                 int warp, int base, int lane) {
@@ -621,11 +623,11 @@ __device__ __forceinline__ void merge_segments(const PartialParams& p, const int
 
 // Static shared state of one partial CTA (the ring, the merge buffers and the
 // segment caches live in dynamic shared memory).
-template <int NT, int kDepth>
+template <class G>
 struct CtaShared {
-  static constexpr int kBufs = PartialGeom<NT>::kMergeBufs;
-  uint64_t full_bar[kDepth];  // one per ring slot: the slot's K and V pages landed
-  int stage_bad[kDepth];      // the slot's page had a block id outside [0, NB)
+  static constexpr int kBufs = G::kMergeBufs, kWarps = G::kWarps;
+  uint64_t full_bar[G::kStages];  // one per ring slot: the slot's K and V pages landed
+  int stage_bad[G::kStages];      // the slot's page had a block id outside [0, NB)
   int abort_flag;              // a wait ran out of time: stop issuing, drain
   int scan_warp[kWarps], scan_warp_cost[kWarps];
   int scan_carry, scan_carry_cost;
@@ -655,7 +657,6 @@ struct CtaShared {
 // Dynamic shared memory of a partial CTA: the 1024-byte aligned ring of
 // kStages (K, V) page slots, then the merge buffers and the three segment
 // caches (segment starts, context lengths, cost-line prefix).
-template <int NT>
 struct CtaSmem {
   uint8_t* stages;
   float* merge_bufs;
@@ -664,14 +665,14 @@ struct CtaSmem {
   int32_t* cc_cache;
 };
 
-template <int NT>
-__device__ __forceinline__ CtaSmem<NT> carve_smem(uint8_t* smem_raw) {
-  CtaSmem<NT> m;
+template <class G>
+__device__ __forceinline__ CtaSmem carve_smem(uint8_t* smem_raw) {
+  CtaSmem m;
   m.stages = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  m.merge_bufs = reinterpret_cast<float*>(m.stages + kStages * kStageBytes);
+  m.merge_bufs = reinterpret_cast<float*>(m.stages + G::kStages * G::kStage);
   m.seg_cache = reinterpret_cast<int32_t*>(m.merge_bufs +
-                                           PartialGeom<NT>::kMergeBufs * PartialGeom<NT>::kMergeBufFloats);
+                                           G::kMergeBufs * G::kMergeBufFloats);
   m.ctx_cache = m.seg_cache + kSegCache;  // context length per sequence
   m.cc_cache = m.ctx_cache + kSegCache;   // cost-line prefix per segment
   return m;
@@ -694,11 +695,12 @@ struct RangeView {
 // the rows of empty segments, and this CTA's range on the cost line. Also
 // initialises the ring barriers and waits for the kernels before this one on
 // the stream. Returns false when this CTA holds no page.
-template <int kFmt, int NT>
+template <class G>
 __device__ __forceinline__ bool setup_range(const PartialParams& p, const CUtensorMap* tm_k,
                                             const CUtensorMap* tm_v,
-                                            CtaShared<NT, Ring<kFmt>::kDepth>& sh,
-                                            const CtaSmem<NT>& sm, RangeView& rv) {
+                                            CtaShared<G>& sh,
+                                            const CtaSmem& sm, RangeView& rv) {
+  constexpr int kFmt = G::kFmt, kWarps = G::kWarps, kThreads = G::kThreads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
   const int nseg = p.batch * p.num_kv_heads;
@@ -708,7 +710,7 @@ __device__ __forceinline__ bool setup_range(const PartialParams& p, const CUtens
   const int32_t* cc;
   int total, n;
   if (tid == 0) {  // before the wait: nothing here reads or writes global memory
-    for (int i = 0; i < Ring<kFmt>::kDepth; ++i) mbar_init(&sh.full_bar[i], 1);
+    for (int i = 0; i < G::kStages; ++i) mbar_init(&sh.full_bar[i], 1);
     sh.abort_flag = 0;
     sh.npend = 0;
     sh.cta_status = XQA_OK;
@@ -942,19 +944,20 @@ __device__ __forceinline__ void piece_owners(Sh& sh, const RangeView& rv) {
 // Lane 0 of a warp: the two TMA loads (K and V slice of one page) into ring
 // slot `slot`, completing on its barrier; a page with a bad block id is
 // flagged instead (the slot's barrier completes without data).
-template <int kFmt, class Sh>
+template <class G>
 __device__ __forceinline__ void issue_page(const PartialParams& p, const CUtensorMap* tm_k,
-                                           const CUtensorMap* tm_v, Sh& sh,
+                                           const CUtensorMap* tm_v, CtaShared<G>& sh,
                                            uint8_t* stages, int slot, int y, int bad, int sg,
                                            uint64_t policy) {
-  uint8_t* st = stages + slot * Ring<kFmt>::kStage;
+  constexpr int kFmt = G::kFmt;
+  uint8_t* st = stages + slot * G::kStage;
   sh.stage_bad[slot] = bad;
   fence_proxy_async_smem();  // this slot's earlier shared reads come before the TMA writes
   if (bad) {
     record_status(&sh.cta_status, XQA_ERR_BAD_BLOCK_ID);
     mbar_arrive(&sh.full_bar[slot]);
   } else {
-    mbar_arrive_expect_tx(&sh.full_bar[slot], Ring<kFmt>::kStage);
+    mbar_arrive_expect_tx(&sh.full_bar[slot], G::kStage);
     if constexpr (kFmt == XQA_KV_E2M1) {
       const size_t at = (size_t)(y / kBlockSize) * kSliceBytes4;  // y: as in an HND pool
       bulk_load(st, p.k_pool + at, kSliceBytes4, &sh.full_bar[slot], policy);
@@ -976,15 +979,16 @@ __device__ __forceinline__ void issue_page(const PartialParams& p, const CUtenso
 // math on the pages whose block ids were good. t0 / t1 are the pages' first
 // token within the sequence. A wait that runs out marks the warp's segment
 // state poisoned and the CTA aborted.
-template <int kFmt, int NT, bool kMulti, typename Refill>
+template <class G, bool kMulti, typename Refill>
 __device__ __forceinline__ void consume_pages(const PartialParams& p,
-                                              CtaShared<NT, Ring<kFmt>::kDepth>& sh,
+                                              CtaShared<G>& sh,
                                               const uint8_t* stages, int slot0, uint32_t ph0,
                                               int slot1, uint32_t ph1, bool pair, int t0, int t1,
-                                              int ctx, WarpState<NT>& st,
-                                              const uint32_t (&qf)[NT][16],
-                                              const SegLimits<NT>& sl, float scale_log2, int g,
+                                              int ctx, WarpState<G::kTiles>& st,
+                                              const uint32_t (&qf)[G::kTiles][16],
+                                              const SegLimits<G::kTiles>& sl, float scale_log2, int g,
                                               int c, int lane, int& poisoned, Refill&& refill) {
+  constexpr int kFmt = G::kFmt, NT = G::kTiles;
   volatile int* abort = &sh.abort_flag;
   bool ready = mbar_wait_bounded(&sh.full_bar[slot0], ph0, abort);
   if (pair) ready = ready && mbar_wait_bounded(&sh.full_bar[slot1], ph1, abort);
@@ -1003,8 +1007,8 @@ __device__ __forceinline__ void consume_pages(const PartialParams& p,
   }
 #endif
   using Regs = typename PageOf<kFmt>::Regs;
-  const uint8_t* stg0 = stages + slot0 * Ring<kFmt>::kStage;
-  const uint8_t* stg1 = stages + slot1 * Ring<kFmt>::kStage;
+  const uint8_t* stg0 = stages + slot0 * G::kStage;
+  const uint8_t* stg1 = stages + slot1 * G::kStage;
   const bool bad0 = sh.stage_bad[slot0] != 0, bad1 = pair && sh.stage_bad[slot1] != 0;
   Regs regs[2];
   if constexpr (kFmt == XQA_KV_E2M1) {
@@ -1058,20 +1062,19 @@ __device__ __forceinline__ SegLimits<NT> seg_limits(const PartialParams& p, int 
 // Merge of one buffered segment by all threads (column col, dims dq..dq+3):
 // the 8 warps' (m, l, O) combine in shared memory; a segment owned whole is
 // normalised and written as fp16, a split piece goes to partial slot cta + s.
-template <int NT, class Sh>
-__device__ __forceinline__ void merge_buffer(const PartialParams& p, Sh& sh,
+template <class G>
+__device__ __forceinline__ void merge_buffer(const PartialParams& p, CtaShared<G>& sh,
                                              const float* merge_bufs, int mb, int ncols,
                                              float v_scale) {
-  using Geom = PartialGeom<NT>;
-  constexpr int kCols = Geom::kCols;
+  constexpr int kCols = G::kCols, kWarps = G::kWarps;
   const int tid = threadIdx.x;
   const int ms = sh.buf_seg[mb];
   const bool mwhole = sh.buf_whole[mb] != 0;
   int any_poison = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) any_poison |= sh.buf_poison[mb][w];
-  const float* base = merge_bufs + mb * Geom::kMergeBufFloats;
-  const float* bm = base + Geom::kScratchFloats;
+  const float* base = merge_bufs + mb * G::kMergeBufFloats;
+  const float* bm = base + G::kScratchFloats;
   const float* bl = bm + kWarps * kCols;
   const int dq = (tid & 31) * 4;  // 0..124
 #pragma unroll
@@ -1123,19 +1126,19 @@ __device__ __forceinline__ void merge_buffer(const PartialParams& p, Sh& sh,
 // range (two at a time), keeping kLookahead of them in flight; at the end of
 // each segment every warp hands its (m, l, O) to a merge buffer, merged across
 // warps when the buffer is next reused or at the end of the range.
-template <int kFmt, int NT, bool kMulti>
+template <class G, bool kMulti>
 __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUtensorMap* tm_k,
                                                const CUtensorMap* tm_v,
-                                               CtaShared<NT, Ring<kFmt>::kDepth>& sh,
-                                               const CtaSmem<NT>& sm, const RangeView& rv,
+                                               CtaShared<G>& sh,
+                                               const CtaSmem& sm, const RangeView& rv,
                                                float scale_log2, float v_scale, uint64_t policy,
-                                               WarpState<NT>& st, uint32_t (&qf)[NT][16],
-                                               uint32_t (&qf_next)[NT][16], int& q_next_seg,
+                                               WarpState<G::kTiles>& st,
+                                               uint32_t (&qf)[G::kTiles][16],
+                                               uint32_t (&qf_next)[G::kTiles][16], int& q_next_seg,
                                                int& issued, int& kseg) {
-  using Geom = PartialGeom<NT>;
-  constexpr int kCols = Geom::kCols;
-  constexpr int kBufs = Geom::kMergeBufs;
-  constexpr int kDepth = Ring<kFmt>::kDepth;
+  constexpr int NT = G::kTiles, kWarps = G::kWarps, kStages = G::kStages;
+  constexpr int kCols = G::kCols;
+  constexpr int kBufs = G::kMergeBufs;
   constexpr bool kPrefetchQ = NT == 1;  // registers: two-tile kernels load Q per segment
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -1147,8 +1150,8 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
   // ---- this warp's loads: owned page k is CTA-local page warp + 8k ----
   const int owned = npages > warp ? (npages - warp + kWarps - 1) / kWarps : 0;
   stamp(14);
-  PageBatch cur = load_batch(p, segs, s_first, s_hi + 1, cbeg, npages, warp, 0, lane);
-  PageBatch nxt = load_batch(p, segs, s_first, s_hi + 1, cbeg, npages, warp, 32, lane);
+  PageBatch cur = load_batch<kWarps>(p, segs, s_first, s_hi + 1, cbeg, npages, warp, 0, lane);
+  PageBatch nxt = load_batch<kWarps>(p, segs, s_first, s_hi + 1, cbeg, npages, warp, 32, lane);
   stamp_after(11, cur.y ^ nxt.y);
   if (p.hints != nullptr && lane < 2) {  // this warp's first pair, for the next call's prefetch
     const int row = p.kv_layout == XQA_LAYOUT_HND
@@ -1163,18 +1166,18 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
     if (k >= cur_base + 32) {
       cur = nxt;
       cur_base += 32;
-      nxt = load_batch(p, segs, s_first, s_hi + 1, cbeg, npages, warp, cur_base + 32, lane);
+      nxt = load_batch<kWarps>(p, segs, s_first, s_hi + 1, cbeg, npages, warp, cur_base + 32, lane);
     }
     const int y = __shfl_sync(kFull, cur.y, k - cur_base);
     const int bad = __shfl_sync(kFull, cur.bad, k - cur_base);
     const int sg = __shfl_sync(kFull, cur.seg, k - cur_base);
-    const int slot = (warp + kWarps * k) % kDepth;
+    const int slot = (warp + kWarps * k) % kStages;
     __syncwarp();  // all lanes' reads of this slot's previous page are done
-    if (lane == 0) issue_page<kFmt>(p, tm_k, tm_v, sh, sm.stages, slot, y, bad, sg, policy);
+    if (lane == 0) issue_page<G>(p, tm_k, tm_v, sh, sm.stages, slot, y, bad, sg, policy);
     __syncwarp();
   };
 #pragma unroll 1
-  for (int i = 0; i < kDepth / kWarps; ++i) issue_next();
+  for (int i = 0; i < G::kLookahead; ++i) issue_next();
   if (warp == kWarps - 1 && lane == 0) piece_owners(sh, rv);
 
   int s = s_first;
@@ -1208,8 +1211,8 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
     for (int q = q0 + ((warp - q0 % kWarps) + kWarps) % kWarps; q < qe; q += 2 * kWarps) {
       const bool pair = q + kWarps < qe;
       const int j0 = cbeg + q - sb;  // page index within the sequence
-      consume_pages<kFmt, NT, kMulti>(p, sh, sm.stages, q % kDepth, (q / kDepth) & 1,
-                                      (q + kWarps) % kDepth, ((q + kWarps) / kDepth) & 1, pair,
+      consume_pages<G, kMulti>(p, sh, sm.stages, q % kStages, (q / kStages) & 1,
+                                      (q + kWarps) % kStages, ((q + kWarps) / kStages) & 1, pair,
                                       j0 * kBlockSize, (j0 + kWarps) * kBlockSize, ctx, st, qf,
                                       sl, scale_log2, g, c, lane, poisoned, issue_next);
     }
@@ -1219,13 +1222,13 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
     // buffers a range of at most two segments never stops mid-way) ----
     const int buf = kseg % kBufs;
     if (kseg >= kBufs) {
-      consumer_bar();
-      merge_buffer<NT>(p, sh, sm.merge_bufs, buf, ncols, v_scale);
-      consumer_bar();
+      consumer_bar<G>();
+      merge_buffer<G>(p, sh, sm.merge_bufs, buf, ncols, v_scale);
+      consumer_bar<G>();
     }
     {
-      float* base = sm.merge_bufs + buf * Geom::kMergeBufFloats;
-      float* bm = base + Geom::kScratchFloats;
+      float* base = sm.merge_bufs + buf * G::kMergeBufFloats;
+      float* bm = base + G::kScratchFloats;
       float* bl = bm + kWarps * kCols;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
@@ -1267,12 +1270,12 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
 // piece's maximum for its row with lane-parallel loads issued with the first
 // gather. The sums run in piece order with the combine kernel's arithmetic
 // (bitwise equal results).
-template <int NT>
+template <class G>
 __device__ __forceinline__ void merge_staged(const PartialParams& p, uint8_t* stage, int s,
                                              int ilo, int ihi, int row0, int rstride,
                                              float v_scale) {
-  constexpr int kCap = kStages * kStageBytes +
-                       PartialGeom<NT>::kMergeBufs * PartialGeom<NT>::kMergeBufFloats * 4;
+  constexpr int NT = G::kTiles, kWarps = G::kWarps, kThreads = G::kThreads;
+  constexpr int kCap = G::kStages * G::kStage + G::kMergeBufs * G::kMergeBufFloats * 4;
   constexpr int kGatherLoads = 16;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, dq = lane * 4;
   const int ncols = p.group * p.q_len;
@@ -1380,8 +1383,8 @@ __device__ __forceinline__ void merge_staged(const PartialParams& p, uint8_t* st
 // call. A CTA that aborted (its ring may still receive page copies) writes
 // NaN rows instead. Out of line: the code of the page loop does not depend
 // on it.
-template <int NT, class Sh>
-__device__ __noinline__ void merge_shared(const PartialParams& p, Sh& sh,
+template <class G>
+__device__ __noinline__ void merge_shared(const PartialParams& p, CtaShared<G>& sh,
                                           uint8_t* stage, float v_scale) {
   const int tid = threadIdx.x, warp = tid >> 5;
   const int ncols = p.group * p.q_len;
@@ -1401,9 +1404,9 @@ __device__ __noinline__ void merge_shared(const PartialParams& p, Sh& sh,
     if (nh > 1 && seen && tid == 0) rel_old = atomicAdd(&p.tickets[ilo], kTicketRelease);
     if (!seen && tid == 0) record_status(&sh.cta_status, XQA_ERR_DEVICE_TIMEOUT);
     if (seen && (word & kTicketPoisonMask) == 0 && !aborted) {
-      merge_staged<NT>(p, stage, s, ilo, ihi, rank, nh, v_scale);
+      merge_staged<G>(p, stage, s, ilo, ihi, rank, nh, v_scale);
     } else {
-      for (int col = rank + nh * warp; col < ncols; col += nh * kWarps) {
+      for (int col = rank + nh * warp; col < ncols; col += nh * G::kWarps) {
         const float nan = __int_as_float(0x7fc00000);
         store_half4(p.out + col_row(p, s, col) * kHeadDim + (tid & 31) * 4, nan, nan, nan, nan);
       }
@@ -1423,17 +1426,18 @@ __device__ __noinline__ void merge_shared(const PartialParams& p, Sh& sh,
 // would). The tickets are device-wide atomic round trips taken once per piece
 // after the whole range, so no mid-range segment boundary stalls the CTA on
 // them. Last, after an abort, the copies still in flight are waited for.
-template <int kFmt, int NT>
+template <class G>
 __device__ __forceinline__ void finish_range(const PartialParams& p,
-                                             CtaShared<NT, Ring<kFmt>::kDepth>& sh,
-                                             const CtaSmem<NT>& sm, const RangeView& rv,
+                                             CtaShared<G>& sh,
+                                             const CtaSmem& sm, const RangeView& rv,
                                              float v_scale, int issued, int kseg) {
-  constexpr int kCols = PartialGeom<NT>::kCols;
-  constexpr int kBufs = PartialGeom<NT>::kMergeBufs;
+  constexpr int NT = G::kTiles, kWarps = G::kWarps, kStages = G::kStages;
+  constexpr int kCols = G::kCols;
+  constexpr int kBufs = G::kMergeBufs;
   constexpr int kAlone = NT == 1 ? kWidePieces : kFewPieces;  // pieces the last merges alone
   const int tid = threadIdx.x, warp = tid >> 5;
   const int ncols = p.group * p.q_len;
-  consumer_bar();
+  consumer_bar<G>();
   stamp(4);
   // In-kernel merge: the arrival tickets of the range's split segments (its
   // first and last; thread e takes segment e) that are merged by arrival
@@ -1448,14 +1452,14 @@ __device__ __forceinline__ void finish_range(const PartialParams& p,
       arrived = atomicAdd(&p.tickets[sh.own_ilo[tid]], 1);
   }
   for (int k = kseg > kBufs ? kseg - kBufs : 0; k < kseg; ++k)
-    merge_buffer<NT>(p, sh, sm.merge_bufs, k % kBufs, ncols, v_scale);
+    merge_buffer<G>(p, sh, sm.merge_bufs, k % kBufs, ncols, v_scale);
   if (tid < 2) sh.arrived[tid] = arrived;
-  consumer_bar();
+  consumer_bar<G>();
   stamp(5);
 
   const int npend = sh.npend;
   if (npend > 0) {
-    consumer_bar();  // all of this CTA's partial-slot writes precede the written counts
+    consumer_bar<G>();  // all of this CTA's partial-slot writes precede the written counts
     if (tid < npend) {
       // A split segment's tickets are the words of the CTA holding its first
       // page (unique in a call). Each piece raises the written count by 1,
@@ -1514,7 +1518,7 @@ __device__ __forceinline__ void finish_range(const PartialParams& p,
       sh.pend_bad[tid] = bad;
       sh.pend_rank[tid] = rank;
     }
-    consumer_bar();
+    consumer_bar<G>();
     stamp(6);
     int m0 = 0, m1 = 0, b0 = 0, b1 = 0, nm = 0;  // the segments this CTA completes alone
     for (int i = 0; i < npend; ++i) {
@@ -1536,7 +1540,7 @@ __device__ __forceinline__ void finish_range(const PartialParams& p,
         merge_segments<NT == 1>(p, ms, mbad, milo, mihi, nm, col, (tid & 31) * 4, v_scale);
     if (sh.pend_rank[0] >= 0 || (npend > 1 && sh.pend_rank[1] >= 0)) {
       __syncthreads();  // the merge buffers and every warp's last pages are read
-      merge_shared<NT>(p, sh, sm.stages, v_scale);
+      merge_shared<G>(p, sh, sm.stages, v_scale);
     }
   }
 
@@ -1548,13 +1552,12 @@ __device__ __forceinline__ void finish_range(const PartialParams& p,
   if (sh.abort_flag) {
     int never = 0;
     volatile int* no_abort = &never;
-    // only the last kDepth / kWarps issued pages can still be in flight: every
+    // only the last kLookahead issued pages can still be in flight: every
     // earlier one was waited for before its slot was reissued
-    constexpr int kDepth = Ring<kFmt>::kDepth;
-    const int first = issued > kDepth / kWarps ? issued - kDepth / kWarps : 0;
+    const int first = issued > G::kLookahead ? issued - G::kLookahead : 0;
     for (int k = first; k < issued; ++k) {
       const int q = warp + kWarps * k;
-      const bool ok = mbar_wait_bounded(&sh.full_bar[q % kDepth], (q / kDepth) & 1, no_abort);
+      const bool ok = mbar_wait_bounded(&sh.full_bar[q % kStages], (q / kStages) & 1, no_abort);
       if (!__all_sync(kFull, ok)) {
         if ((threadIdx.x & 31) == 0) atomicExch(&sh.cta_status, XQA_ERR_DRAIN_TIMEOUT);
         break;
@@ -1575,16 +1578,17 @@ __device__ __forceinline__ void publish_status(const PartialParams& p, Sh& sh) {
 }  // namespace
 
 template <int kFmt, int NT, bool kMulti>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(PartialGeom<kFmt, NT>::kThreads, 1)
     partial_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const PartialParams p) {
+  using G = PartialGeom<kFmt, NT>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) CtaShared<NT, Ring<kFmt>::kDepth> sh;
+  __shared__ __align__(8) CtaShared<G> sh;
   griddep_launch_dependents();  // a dependent next kernel waits for this grid itself
   stamp(0);
-  const CtaSmem<NT> sm = carve_smem<NT>(smem_raw);
+  const CtaSmem sm = carve_smem<G>(smem_raw);
   RangeView rv;
-  if (!setup_range<kFmt, NT>(p, &tm_k, &tm_v, sh, sm, rv)) {
+  if (!setup_range<G>(p, &tm_k, &tm_v, sh, sm, rv)) {
     publish_status(p, sh);
     return;
   }
@@ -1600,9 +1604,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   int q_next_seg = -1;
   int issued = 0;  // this warp's pages whose loads have been issued
   int kseg = 0;    // segments of this range handed to the merge buffers
-  cta_mode_range<kFmt, NT, kMulti>(p, &tm_k, &tm_v, sh, sm, rv, scale_log2, v_scale, policy, st, qf,
+  cta_mode_range<G, kMulti>(p, &tm_k, &tm_v, sh, sm, rv, scale_log2, v_scale, policy, st, qf,
                                    qf_next, q_next_seg, issued, kseg);
-  finish_range<kFmt, NT>(p, sh, sm, rv, v_scale, issued, kseg);
+  finish_range<G>(p, sh, sm, rv, v_scale, issued, kseg);
   publish_status(p, sh);
 }
 
@@ -1615,20 +1619,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 // shapes with many segments per CTA (batches of many short sequences): the
 // mode test and the warp-mode code slow the page loop of CTA-mode ranges.
 template <int kFmt, int NT, bool kMulti>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(PartialGeom<kFmt, NT>::kThreads, 1)
     partial_kernel_wm(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const PartialParams p) {
   static_assert(NT == 1, "warp mode holds one column tile");
+  using G = PartialGeom<kFmt, NT>;
   constexpr bool kPrefetchQ = true;
-  constexpr int kDepth = Ring<kFmt>::kDepth, kAhead = kDepth / kWarps;
+  constexpr int kWarps = G::kWarps, kThreads = G::kThreads, kStages = G::kStages;
+  constexpr int kAhead = G::kLookahead;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) CtaShared<NT, Ring<kFmt>::kDepth> sh;
+  __shared__ __align__(8) CtaShared<G> sh;
   griddep_launch_dependents();  // a dependent next kernel waits for this grid itself
   stamp(0);
   const int ncols = p.group * p.q_len;
-  const CtaSmem<NT> sm = carve_smem<NT>(smem_raw);
+  const CtaSmem sm = carve_smem<G>(smem_raw);
   RangeView rv;
-  if (!setup_range<kFmt, NT>(p, &tm_k, &tm_v, sh, sm, rv)) {
+  if (!setup_range<G>(p, &tm_k, &tm_v, sh, sm, rv)) {
     publish_status(p, sh);
     return;
   }
@@ -1662,7 +1668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (!warp_mode) {
-    cta_mode_range<kFmt, NT, kMulti>(p, &tm_k, &tm_v, sh, sm, rv, scale_log2, v_scale, policy, st,
+    cta_mode_range<G, kMulti>(p, &tm_k, &tm_v, sh, sm, rv, scale_log2, v_scale, policy, st,
                                      qf, qf_next, q_next_seg, issued, kseg);
   } else {
     // ---- warp mode: this warp's pieces are the range's segments j = warp,
@@ -1712,9 +1718,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int bad = __shfl_sync(kFull, wcur.bad, ioff);
           ++ioff;
           const int k = issued++;
-          const int slot = (warp + kWarps * k) % kDepth;
+          const int slot = (warp + kWarps * k) % kStages;
           __syncwarp();  // all lanes' reads of this slot's previous page are done
-          if (lane == 0) issue_page<kFmt>(p, &tm_k, &tm_v, sh, sm.stages, slot, y, bad, wcur.seg, policy);
+          if (lane == 0) issue_page<G>(p, &tm_k, &tm_v, sh, sm.stages, slot, y, bad, wcur.seg, policy);
           __syncwarp();
           return;
         }
@@ -1756,8 +1762,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int o = 0; o < len; o += 2) {
         const bool pair = o + 1 < len;
         const int t0 = (pb + o - sb) * kBlockSize;
-        consume_pages<kFmt, NT, kMulti>(p, sh, sm.stages, (warp + kWarps * k) % kDepth,
-                                        (k / kAhead) & 1, (warp + kWarps * (k + 1)) % kDepth,
+        consume_pages<G, kMulti>(p, sh, sm.stages, (warp + kWarps * k) % kStages,
+                                        (k / kAhead) & 1, (warp + kWarps * (k + 1)) % kStages,
                                         ((k + 1) / kAhead) & 1, pair, t0, t0 + kBlockSize, ctx,
                                         st, qf, sl, scale_log2, g, c, lane, poisoned, issue_next_w);
         k += pair ? 2 : 1;
@@ -1800,7 +1806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  finish_range<kFmt, NT>(p, sh, sm, rv, v_scale, issued, kseg);
+  finish_range<G>(p, sh, sm, rv, v_scale, issued, kseg);
   publish_status(p, sh);
 }
 
@@ -1809,9 +1815,13 @@ namespace {
 // The instance of one format: several columns need two tiles, one-tile shapes with
 // enough segments the warp-capable kernel.
 template <int kFmt>
-cudaError_t launch_format(const cudaLaunchConfig_t& cfg, bool wm, int nt, bool multi,
+cudaError_t launch_format(cudaLaunchConfig_t cfg, bool wm, int nt, bool multi,
                           const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                           const PartialParams& p) {
+  using G1 = PartialGeom<kFmt, 1>;
+  using G2 = PartialGeom<kFmt, 2>;
+  cfg.blockDim = dim3(nt == 1 ? G1::kThreads : G2::kThreads);
+  cfg.dynamicSmemBytes = nt == 1 ? G1::kSmem : G2::kSmem;
   if (wm)
     return multi ? cudaLaunchKernelEx(&cfg, partial_kernel_wm<kFmt, 1, true>, tm_k, tm_v, p)
                  : cudaLaunchKernelEx(&cfg, partial_kernel_wm<kFmt, 1, false>, tm_k, tm_v, p);
@@ -1832,8 +1842,6 @@ cudaError_t launch_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
   const int nt = (p.group * p.q_len + 7) / 8;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)n_max);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = nt == 1 ? PartialGeom<1>::kSmem : PartialGeom<2>::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1857,7 +1865,7 @@ namespace {
 template <int kFmt>
 cudaError_t set_format_attributes() {
   const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  const int s1 = PartialGeom<1>::kSmem, s2 = PartialGeom<2>::kSmem;
+  const int s1 = PartialGeom<kFmt, 1>::kSmem, s2 = PartialGeom<kFmt, 2>::kSmem;
   cudaError_t e;
   if ((e = cudaFuncSetAttribute(partial_kernel<kFmt, 1, false>, a, s1)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(partial_kernel<kFmt, 1, true>, a, s1)) != cudaSuccess) return e;

@@ -20,30 +20,9 @@ constexpr int kBlockSize = 16;
 // 8-wide MMA tiles (so G <= 16: G = 16 takes both tiles for one new token).
 constexpr int kMaxCols = 16;
 constexpr int kPageBytes = kBlockSize * kHeadDim;             // one (page, kv head) slice: 2048 B
-constexpr int kStageBytes = 2 * kPageBytes;                   // K slice + V slice
-constexpr int kWarps = 8;                                     // every warp loads and computes
-constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 32;                                   // smem ring depth (multiple of kWarps)
-constexpr int kLookahead = kStages / kWarps;                  // pages in flight per warp
 constexpr int kScratchStride = kHeadDim + 4;                  // floats per (warp, head) merge row
 constexpr int kSegCache = 2048;  // seg_start (and context length) entries kept in smem
 
-// Per-instance geometry of the partial kernel with NT MMA column tiles
-// (8 * NT columns = new token x head): merge buffers hold every warp's O rows,
-// then m[warp][col], l[warp][col]. One-tile kernels keep two buffers (merges
-// deferred), two-tile kernels one (their buffer is twice as large).
-template <int NT>
-struct PartialGeom {
-  static constexpr int kCols = 8 * NT;
-  static constexpr int kScratchFloats = kWarps * kCols * kScratchStride;
-  static constexpr int kMergeBufFloats = kScratchFloats + 2 * kWarps * kCols;
-  static constexpr int kMergeBufs = NT == 1 ? 2 : 1;
-  static constexpr int kSmem = 1024 /* alignment slack for the 1024-B swizzle atom */ +
-                               kStages * kStageBytes + kMergeBufs * kMergeBufFloats * 4 +
-                               kSegCache * 4 /* segment starts */ + kSegCache * 4 /* lengths */ +
-                               kSegCache * 4 /* cost prefix */;
-  static_assert(kSmem <= 227 * 1024, "shared memory budget");
-};
 // 4-bit cache: a (page, kv head) slice is 16 tokens x 64 code bytes (dim 2i in
 // the low nibble of byte i), then 16 tokens x 8 E4M3 scales, one for each group
 // of 16 dims.
@@ -51,21 +30,31 @@ constexpr int kGroup4 = 16;
 constexpr int kCodeBytes4 = kBlockSize * kHeadDim / 2;
 constexpr int kSliceBytes4 = kCodeBytes4 + kBlockSize * (kHeadDim / kGroup4);
 static_assert(kSliceBytes4 == XQA_E2M1_SLICE_BYTES, "slice size in the header");
-// The partial kernel's page ring by format: bytes of a (page, kv head) slice, of a
-// stage (K and V slice), stages (a multiple of kWarps). The 4-bit ring holds 56
-// stages in the same 128 KB.
-template <int kFmt>
-struct Ring {
-  static constexpr int kPage = kPageBytes;
-  static constexpr int kStage = kStageBytes;
-  static constexpr int kDepth = kStages;
-};
-template <>
-struct Ring<XQA_KV_E2M1> {
-  static constexpr int kPage = kSliceBytes4;
-  static constexpr int kStage = 2 * kSliceBytes4;
-  static constexpr int kDepth = 56;
-  static_assert(kDepth % kWarps == 0 && kDepth * kStage <= kStages * kStageBytes, "ring");
+// Per-instance geometry of the partial kernel: cache format and NT MMA column
+// tiles (8 * NT columns = new token x head). Every warp loads and computes; the
+// ring's depth is a multiple of the warps. Merge buffers hold every warp's O rows,
+// then m[warp][col], l[warp][col]. One-tile FP8 kernels keep two buffers (merges
+// deferred), two-tile kernels one (their buffer is twice as large).
+template <int kFmtV, int NT>
+struct PartialGeom {
+  static constexpr int kFmt = kFmtV;
+  static constexpr int kTiles = NT;
+  static constexpr bool kFour = kFmt == XQA_KV_E2M1;
+  static constexpr int kWarps = 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kStage = kFour ? 2 * kSliceBytes4 : 2 * kPageBytes;  // K slice + V slice
+  static constexpr int kStages = kFour ? 56 : 32;                           // ring depth
+  static constexpr int kLookahead = kStages / kWarps;                       // pages in flight per warp
+  static constexpr int kCols = 8 * NT;
+  static constexpr int kScratchFloats = kWarps * kCols * kScratchStride;
+  static constexpr int kMergeBufFloats = kScratchFloats + 2 * kWarps * kCols;
+  static constexpr int kMergeBufs = NT == 1 ? 2 : 1;
+  static constexpr int kSmem = 1024 /* alignment slack for the 1024-B swizzle atom */ +
+                               kStages * kStage + kMergeBufs * kMergeBufFloats * 4 +
+                               kSegCache * 4 /* segment starts */ + kSegCache * 4 /* lengths */ +
+                               kSegCache * 4 /* cost prefix */;
+  static_assert(kStages % kWarps == 0, "a warp's slots are its own");
+  static_assert(kSmem <= 226 * 1024, "shared memory budget (the rest: static)");
 };
 constexpr int kDefaultMinPagesPerCta = 16;
 // Split rule cost line: every non-empty segment costs kSegCost page units on
