@@ -26,8 +26,8 @@
 // weight, the size of the rounding of out itself.
 //
 // Warps: 0-3 and 4-7 softmax of row tile 0 and 1 (a thread owns a row), 8-11
-// epilogue, 12 tensor core, 13 units and TMA loads, 14-15 the masked V tiles
-// (below). TMEM: S0, S1 (P over them), O0, O1: 4 x 128 columns.
+// epilogue, 12 and 14 tensor core (row tile 0 and 1), 13 units and TMA loads, 15
+// the masked V tiles (below). TMEM: S0, S1 (P over them), O0, O1: 4 x 128 columns.
 //
 // Hidden values do not leak: a weight of exactly 0 times an infinity or NaN
 // would be NaN, so in V tiles that some row of the unit sees in part, rows past
@@ -53,7 +53,7 @@ constexpr int kPrefillThreads = 512;
 constexpr float kNoRowMax = -1e30f;              // as in the decode kernel
 constexpr float kLazyMax = 8.0f;                 // log2 units
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kUnitReaders = 15;  // 8 softmax, 4 epilogue, 1 tensor-core, 2 V warps
+constexpr int kUnitReaders = 15;  // 8 softmax, 4 epilogue, 2 tensor-core, 1 V warp
 
 // One unit of work, written by the loading warp.
 struct Unit {
@@ -74,7 +74,8 @@ struct Shared {
   uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
   uint64_t q_full, q_empty;
   uint64_t v_clean[kKvStages];   // the stage's V tile may be used (masked tiles only)
-  uint64_t s_full[2], p_full[2]; // S ready / P written
+  uint64_t s_full[2];            // S ready
+  uint64_t p_full[2][2];         // the first / second 64 keys of P written
   uint64_t o_full[2], o_free[2]; // O complete / read by the epilogue
   uint64_t stat_full[2], stat_free[2];
   uint64_t drain;
@@ -158,6 +159,26 @@ __device__ __forceinline__ void tmem_wait_ld() {
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Two 32-bit values in one register pair, and their packed arithmetic.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void split2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 // Shared-memory matrix descriptors, 128-byte swizzle (layout 2), version 1.
@@ -354,92 +375,87 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
   }
 }
 
-// ---- warp 12: the products ----
+// ---- warps 12, 14: the products of row tile 0, 1 ----
 template <int kType>
-__device__ __forceinline__ void tensor_role(const Ctx& c) {
+__device__ __forceinline__ void tensor_role(const Ctx& c, int s) {
   Shared& sh = c.sh;
   const int lane = threadIdx.x & 31;
   const uint32_t id_qk = instr_desc<kType>(false), id_pv = instr_desc<kType>(true);
-  const uint32_t q_addr = smem_addr(c.tiles);
-  int kv = 0, units_with_work = 0;
-  uint32_t cleaned = 0;     // phase of v_clean, one bit per stage
-  int np[2] = {0, 0};       // P tiles consumed
-  int no[2] = {0, 0};       // O tiles started
-  auto qk = [&](int s, int st) {
-    if (lane == 0) {
-      const uint32_t a = q_addr + s * kTileBytes, b = smem_addr(c.kv(st));
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t off = (k >> 2) * kHalfBytes + (k & 3) * 32;
-        tc_mma_ss(c.tmem + s * kTile, desc_k_major(a + off), desc_k_major(b + off), id_qk, k > 0);
-      }
-      tc_commit(&sh.s_full[s]);
-    }
-  };
+  const uint32_t q_addr = smem_addr(c.tiles) + s * kTileBytes;
+  const uint32_t s_tmem = c.tmem + s * kTile, o_tmem = c.tmem + 256 + s * kTile;
+  int kv = 0, units_with_work = 0, np = 0, no = 0;
+  uint32_t cleaned = 0;  // phase of v_clean, one bit per stage
   for (int i = 0;; ++i) {
     Unit u;
     if (!c.get_unit(i, u)) return;
     c.free_unit(i);
-    const int n = max(u.n[0], u.n[1]);
+    const int n = max(u.n[0], u.n[1]), mine = s == 0 ? u.n[0] : u.n[1];
     if (n == 0) continue;
     if (!c.wait(&sh.q_full, units_with_work & 1)) return;
     ++units_with_work;
-    int st = kv % kKvStages;
-    if (!c.wait(&sh.kv_full[st], (kv / kKvStages) & 1)) return;
-    tc_fence_after();
+    // tiles K(n-1), V(n-1), K(n-2), ...: S of tile j - 1 is made after P of tile j,
+    // which lies over S, is used
+    for (int j = n - 1; j >= 0; --j, kv += 2) {
+      const int sk = kv % kKvStages, sv = (kv + 1) % kKvStages;
+      if (!c.wait(&sh.kv_full[sk], (kv / kKvStages) & 1)) return;
+      tc_fence_after();
+      if (lane == 0) {
+        if (j < mine) {
+          const uint32_t b = smem_addr(c.kv(sk));
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-      if (u.n[s] == n) qk(s, st);
-    if (lane == 0) {
-      tc_commit(&sh.kv_empty[st]);
-      if (n == 1) tc_commit(&sh.q_empty);
-    }
-    ++kv;
-    for (int j = n - 1; j >= 0; --j) {
-      const int sv = kv % kKvStages, sk = (kv + 1) % kKvStages;
-      if (!c.wait(&sh.kv_full[sv], (kv / kKvStages) & 1)) return;
-      if ((j + 1) * kTile > u.hidden) {  // masked: after the V warps are done with it
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t off = (k >> 2) * kHalfBytes + (k & 3) * 32;
+            tc_mma_ss(s_tmem, desc_k_major(q_addr + off), desc_k_major(b + off), id_qk, k > 0);
+          }
+          tc_commit(&sh.s_full[s]);
+          tc_commit(&sh.kv_empty[sk]);
+        } else {
+          mbar_arrive(&sh.kv_empty[sk]);
+        }
+        if (j == 0) tc_commit(&sh.q_empty);
+      }
+      __syncwarp();
+      if (!c.wait(&sh.kv_full[sv], ((kv + 1) / kKvStages) & 1)) return;
+      if ((j + 1) * kTile > u.hidden) {  // masked: after the V warp is done with it
         if (!c.wait(&sh.v_clean[sv], (cleaned >> sv) & 1)) return;
         cleaned ^= 1u << sv;
       }
-      if (j > 0 && !c.wait(&sh.kv_full[sk], ((kv + 1) / kKvStages) & 1)) return;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (j < u.n[s]) {
-          if (!c.wait(&sh.p_full[s], np[s] & 1)) return;
-          ++np[s];
-          const bool start = j == u.n[s] - 1;
-          if (start) {
-            if (no[s] > 0 && !c.wait(&sh.o_free[s], (no[s] - 1) & 1)) return;
-            ++no[s];
-          }
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t b = smem_addr(c.kv(sv));
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc_mma_ts(c.tmem + 256 + s * kTile, c.tmem + s * kTile + 8 * k,
-                        desc_mn_major(b + k * 2048), id_pv, !start || k > 0);
-            if (j == 0) tc_commit(&sh.o_full[s]);
-          }
-        }
-        if (j > 0 && j - 1 < u.n[s]) qk(s, sk);
+      if (j >= mine) {
+        c.arrive(&sh.kv_empty[sv]);
+        continue;
       }
+      const bool start = j == mine - 1;
+      if (start) {
+        if (no > 0 && !c.wait(&sh.o_free[s], (no - 1) & 1)) return;
+        ++no;
+      }
+      const uint32_t b = smem_addr(c.kv(sv));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // as P's halves are written
+        if (!c.wait(&sh.p_full[s][h], np & 1)) return;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 4 * h; k < 4 * h + 4; ++k)
+            tc_mma_ts(o_tmem, s_tmem + 8 * k, desc_mn_major(b + k * 2048), id_pv, !start || k > 0);
+        }
+        __syncwarp();
+      }
+      ++np;
       if (lane == 0) {
         tc_commit(&sh.kv_empty[sv]);
-        if (j > 0) tc_commit(&sh.kv_empty[sk]);
-        if (j == 1) tc_commit(&sh.q_empty);
+        if (j == 0) tc_commit(&sh.o_full[s]);
       }
-      kv += j > 0 ? 2 : 1;
+      __syncwarp();
     }
   }
 }
 
-// ---- warps 14, 15: V tiles that some row of the unit sees in part ----
+// ---- warp 15: V tiles that some row of the unit sees in part ----
 template <int kType>
 __device__ __forceinline__ void clean_role(const Ctx& c) {
   Shared& sh = c.sh;
-  const int t = threadIdx.x & 63;  // 64 threads
+  const int t = threadIdx.x & 31;
   const uint32_t exp_mask = kType == XQA_F16 ? 0x7c00u : 0x7f80u;
   int kv = 0;
   for (int i = 0;; ++i) {
@@ -454,7 +470,7 @@ __device__ __forceinline__ void clean_role(const Ctx& c) {
         const int from = max(0, u.hidden - j * kTile);     // first row some token does not see
         const int past = min(kTile, u.len_k - j * kTile);  // first row past the sequence
         uint4* rows = reinterpret_cast<uint4*>(c.kv(st));
-        for (int x = from * 8 + t; x < kTile * 8; x += 64) {
+        for (int x = from * 8 + t; x < kTile * 8; x += 32) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint4& cell = rows[h * (kHalfBytes / 16) + x];
@@ -543,11 +559,16 @@ __device__ __forceinline__ void softmax_role(const Ctx& c, int s) {
         for (int k = 0; k < kTile; ++k)
           if (k >= lim) r[k] = 0xff800000u;  // -inf
       }
-      float mx[4];
+      float mx[4];  // three-operand maxima
 #pragma unroll
       for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(r[k]);
 #pragma unroll
-      for (int k = 4; k < kTile; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(r[k]));
+      for (int k = 4; k < kTile - 4; k += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(r[k + e])), __uint_as_float(r[k + 4 + e]));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(r[kTile - 4 + e]));
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
       const bool moves = top > m + kLazyMax;
       if (j < n - 1) {
@@ -569,24 +590,28 @@ __device__ __forceinline__ void softmax_role(const Ctx& c, int s) {
         }
       }
       if (moves) m = top;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t sc2 = f32x2(sc, sc), m2 = f32x2(-m, -m);
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t pk[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
-          const float a = ex2(__fmaf_rn(__uint_as_float(r[64 * h + 2 * k]), sc, -m));
-          const float b = ex2(__fmaf_rn(__uint_as_float(r[64 * h + 2 * k + 1]), sc, -m));
-          sum[(2 * k) & 3] += a;
-          sum[(2 * k + 1) & 3] += b;
+          float a, b;
+          split2(fma2(f32x2(__uint_as_float(r[64 * h + 2 * k]), __uint_as_float(r[64 * h + 2 * k + 1])), sc2, m2), a, b);
+          a = ex2(a);
+          b = ex2(b);
+          sum[k & 1] = add2(sum[k & 1], f32x2(a, b));
           pk[k] = pack2<kType>(a, b);
         }
         tmem_st32(s_addr + 32 * h, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        c.arrive(&sh.p_full[s][h]);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_wait_st();
-      tc_fence_before();
-      c.arrive(&sh.p_full[s]);
+      float la, lb;
+      split2(add2(sum[0], sum[1]), la, lb);
+      l += la + lb;
       ++ns;
     }
     if (nstat > 0 && !c.wait(&sh.stat_free[s], (nstat - 1) & 1)) return;
@@ -694,24 +719,25 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKvStages; ++i) {
       mbar_init(&sh.kv_full[i], 1);
-      mbar_init(&sh.kv_empty[i], 3);  // the tensor-core warp and the two V warps
-      mbar_init(&sh.v_clean[i], 2);
+      mbar_init(&sh.kv_empty[i], 3);  // the tensor-core warps and the V warp
+      mbar_init(&sh.v_clean[i], 1);
     }
     for (int i = 0; i < kUnitSlots; ++i) {
       mbar_init(&sh.unit_full[i], 1);
       mbar_init(&sh.unit_empty[i], kUnitReaders);
     }
     mbar_init(&sh.q_full, 1);
-    mbar_init(&sh.q_empty, 1);
+    mbar_init(&sh.q_empty, 2);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh.s_full[s], 1);
-      mbar_init(&sh.p_full[s], 4);
+      mbar_init(&sh.p_full[s][0], 4);
+      mbar_init(&sh.p_full[s][1], 4);
       mbar_init(&sh.o_full[s], 1);
       mbar_init(&sh.o_free[s], 4);
       mbar_init(&sh.stat_full[s], 4);
       mbar_init(&sh.stat_free[s], 4);
     }
-    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.drain, 2);
     sh.abort_flag = 0;
     sh.status = aligned ? XQA_OK : XQA_ERR_LAUNCH;
     fence_mbar_init();
@@ -732,7 +758,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     __syncwarp();
     if (warp >= 12) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-      if (warp == 12) tensor_role<kType>(c);
+      if (warp == 12 || warp == 14) tensor_role<kType>(c, (warp - 12) >> 1);
       else if (warp == 13) load_role(c, &tm_q, &tm_k, &tm_v, kv_issued, q_issued);
       else clean_role<kType>(c);
     } else if (warp >= 8) {
@@ -746,10 +772,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   __syncwarp();
   // Products and their arrivals, and after an abort copies, may be in flight:
   // they end before the CTA's shared memory and TMEM are given up.
-  if (aligned && (warp == 12 || warp == 13)) {
+  if (aligned && warp >= 12 && warp <= 14) {
     int never = 0;
     bool ok = true;
-    if (warp == 12) {
+    if (warp != 13) {
       if ((threadIdx.x & 31) == 0) tc_commit(&sh.drain);
       __syncwarp();
       ok = mbar_wait_bounded(&sh.drain, 0, &never);
