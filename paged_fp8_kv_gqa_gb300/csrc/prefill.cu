@@ -381,8 +381,14 @@ __device__ __forceinline__ void tensor_role(const Ctx& c, int s) {
   Shared& sh = c.sh;
   const int lane = threadIdx.x & 31;
   const uint32_t id_qk = instr_desc<kType>(false), id_pv = instr_desc<kType>(true);
-  const uint32_t q_addr = smem_addr(c.tiles) + s * kTileBytes;
-  const uint32_t s_tmem = c.tmem + s * kTile, o_tmem = c.tmem + 256 + s * kTile;
+  // descriptors and addresses are warp-uniform and stay in uniform registers: built
+  // per product by one lane, they cost more than the product (180 cycles against 64)
+  const uint32_t tiles = __shfl_sync(kAll, smem_addr(c.tiles), 0);
+  const uint32_t tmem = __shfl_sync(kAll, c.tmem, 0);
+  const uint64_t q_desc = desc_k_major(tiles + s * kTileBytes);
+  const uint64_t k_desc = desc_k_major(tiles + 2 * kTileBytes);   // stage 0 of the ring
+  const uint64_t v_desc = desc_mn_major(tiles + 2 * kTileBytes);
+  const uint32_t s_tmem = tmem + s * kTile, o_tmem = tmem + 256 + s * kTile;
   int kv = 0, units_with_work = 0, np = 0, no = 0;
   uint32_t cleaned = 0;  // phase of v_clean, one bit per stage
   for (int i = 0;; ++i) {
@@ -401,11 +407,11 @@ __device__ __forceinline__ void tensor_role(const Ctx& c, int s) {
       tc_fence_after();
       if (lane == 0) {
         if (j < mine) {
-          const uint32_t b = smem_addr(c.kv(sk));
+          const uint64_t b = k_desc + sk * (kTileBytes >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const uint32_t off = (k >> 2) * kHalfBytes + (k & 3) * 32;
-            tc_mma_ss(s_tmem, desc_k_major(q_addr + off), desc_k_major(b + off), id_qk, k > 0);
+            const uint32_t off = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+            tc_mma_ss(s_tmem, q_desc + off, b + off, id_qk, k > 0);
           }
           tc_commit(&sh.s_full[s]);
           tc_commit(&sh.kv_empty[sk]);
@@ -429,7 +435,7 @@ __device__ __forceinline__ void tensor_role(const Ctx& c, int s) {
         if (no > 0 && !c.wait(&sh.o_free[s], (no - 1) & 1)) return;
         ++no;
       }
-      const uint32_t b = smem_addr(c.kv(sv));
+      const uint64_t b = v_desc + sv * (kTileBytes >> 4);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // as P's halves are written
         if (!c.wait(&sh.p_full[s][h], np & 1)) return;
@@ -437,7 +443,7 @@ __device__ __forceinline__ void tensor_role(const Ctx& c, int s) {
         if (lane == 0) {
 #pragma unroll
           for (int k = 4 * h; k < 4 * h + 4; ++k)
-            tc_mma_ts(o_tmem, s_tmem + 8 * k, desc_mn_major(b + k * 2048), id_pv, !start || k > 0);
+            tc_mma_ts(o_tmem, s_tmem + 8 * k, b + k * (2048 >> 4), id_pv, !start || k > 0);
         }
         __syncwarp();
       }
@@ -713,7 +719,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   float* stats = reinterpret_cast<float*>(smem + kSmemTiles);
   Shared& sh = *reinterpret_cast<Shared*>(smem + kSmemTiles + kSmemStats);
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0);  // known to be warp-uniform
   const bool aligned = (smem_addr(smem) & 1023u) == 0;  // as the swizzle needs
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
