@@ -26,8 +26,8 @@
 // weight, the size of the rounding of out itself.
 //
 // Warps: 0-3 and 4-7 softmax of row tile 0 and 1 (a thread owns a row), 8-11
-// epilogue, 12 and 14 tensor core (row tile 0 and 1), 13 units and TMA loads, 15
-// the masked V tiles (below). TMEM: S0, S1 (P over them), O0, O1: 4 x 128 columns.
+// epilogue, 12 tensor core, 13 units and TMA loads, 14-15 the masked V tiles
+// (below). TMEM: S0, S1 (P over them), O0, O1: 4 x 128 columns.
 //
 // Hidden values do not leak: a weight of exactly 0 times an infinity or NaN
 // would be NaN, so in V tiles that some row of the unit sees in part, rows past
@@ -53,7 +53,7 @@ constexpr int kPrefillThreads = 512;
 constexpr float kNoRowMax = -1e30f;              // as in the decode kernel
 constexpr float kLazyMax = 8.0f;                 // log2 units
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kUnitReaders = 15;  // 8 softmax, 4 epilogue, 2 tensor-core, 1 V warp
+constexpr int kUnitReaders = 15;  // 8 softmax, 4 epilogue, 1 tensor-core, 2 V warps
 
 // One unit of work, written by the loading warp.
 struct Unit {
@@ -375,9 +375,9 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
   }
 }
 
-// ---- warps 12, 14: the products of row tile 0, 1 ----
+// ---- warp 12: the products ----
 template <int kType>
-__device__ __forceinline__ void tensor_role(const Ctx& c, int s) {
+__device__ __forceinline__ void tensor_role(const Ctx& c) {
   Shared& sh = c.sh;
   const int lane = threadIdx.x & 31;
   const uint32_t id_qk = instr_desc<kType>(false), id_pv = instr_desc<kType>(true);
@@ -385,83 +385,98 @@ __device__ __forceinline__ void tensor_role(const Ctx& c, int s) {
   // per product by one lane, they cost more than the product (180 cycles against 64)
   const uint32_t tiles = __shfl_sync(kAll, smem_addr(c.tiles), 0);
   const uint32_t tmem = __shfl_sync(kAll, c.tmem, 0);
-  const uint64_t q_desc = desc_k_major(tiles + s * kTileBytes);
+  const uint64_t q_desc = desc_k_major(tiles);
   const uint64_t k_desc = desc_k_major(tiles + 2 * kTileBytes);   // stage 0 of the ring
   const uint64_t v_desc = desc_mn_major(tiles + 2 * kTileBytes);
-  const uint32_t s_tmem = tmem + s * kTile, o_tmem = tmem + 256 + s * kTile;
-  int kv = 0, units_with_work = 0, np = 0, no = 0;
-  uint32_t cleaned = 0;  // phase of v_clean, one bit per stage
+  int kv = 0, units_with_work = 0;
+  int np[2] = {0, 0}, no[2] = {0, 0};  // P tiles used, O tiles started
+  uint32_t cleaned = 0;                // phase of v_clean, one bit per stage
+  auto qk = [&](int s, int st) {       // one lane
+    const uint64_t a = q_desc + s * (kTileBytes >> 4), b = k_desc + st * (kTileBytes >> 4);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t off = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+      tc_mma_ss(tmem + s * kTile, a + off, b + off, id_qk, k > 0);
+    }
+    tc_commit(&sh.s_full[s]);
+  };
   for (int i = 0;; ++i) {
     Unit u;
     if (!c.get_unit(i, u)) return;
     c.free_unit(i);
-    const int n = max(u.n[0], u.n[1]), mine = s == 0 ? u.n[0] : u.n[1];
+    const int n = max(u.n[0], u.n[1]);
     if (n == 0) continue;
     if (!c.wait(&sh.q_full, units_with_work & 1)) return;
     ++units_with_work;
-    // tiles K(n-1), V(n-1), K(n-2), ...: S of tile j - 1 is made after P of tile j,
-    // which lies over S, is used
-    for (int j = n - 1; j >= 0; --j, kv += 2) {
-      const int sk = kv % kKvStages, sv = (kv + 1) % kKvStages;
-      if (!c.wait(&sh.kv_full[sk], (kv / kKvStages) & 1)) return;
-      tc_fence_after();
-      if (lane == 0) {
-        if (j < mine) {
-          const uint64_t b = k_desc + sk * (kTileBytes >> 4);
+    int sk = kv % kKvStages;
+    if (!c.wait(&sh.kv_full[sk], (kv / kKvStages) & 1)) return;
+    tc_fence_after();
+    if (lane == 0) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t off = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
-            tc_mma_ss(s_tmem, q_desc + off, b + off, id_qk, k > 0);
-          }
-          tc_commit(&sh.s_full[s]);
-          tc_commit(&sh.kv_empty[sk]);
-        } else {
-          mbar_arrive(&sh.kv_empty[sk]);
-        }
-        if (j == 0) tc_commit(&sh.q_empty);
-      }
-      __syncwarp();
-      if (!c.wait(&sh.kv_full[sv], ((kv + 1) / kKvStages) & 1)) return;
-      if ((j + 1) * kTile > u.hidden) {  // masked: after the V warp is done with it
+      for (int s = 0; s < 2; ++s)
+        if (u.n[s] == n) qk(s, sk);
+      tc_commit(&sh.kv_empty[sk]);
+      if (n == 1) tc_commit(&sh.q_empty);
+    }
+    __syncwarp();
+    ++kv;
+    // The row tiles in turn: O += P V of tile j, then S of tile j - 1 (which takes
+    // the place of P). The order is fixed, so the tiles settle half a period apart
+    // and one's softmax runs under the other's products.
+    for (int j = n - 1; j >= 0; --j) {
+      const int sv = kv % kKvStages;
+      sk = (kv + 1) % kKvStages;
+      if (!c.wait(&sh.kv_full[sv], (kv / kKvStages) & 1)) return;
+      if ((j + 1) * kTile > u.hidden) {  // masked: after the V warps are done with it
         if (!c.wait(&sh.v_clean[sv], (cleaned >> sv) & 1)) return;
         cleaned ^= 1u << sv;
       }
-      if (j >= mine) {
-        c.arrive(&sh.kv_empty[sv]);
-        continue;
-      }
-      const bool start = j == mine - 1;
-      if (start) {
-        if (no > 0 && !c.wait(&sh.o_free[s], (no - 1) & 1)) return;
-        ++no;
-      }
-      const uint64_t b = v_desc + sv * (kTileBytes >> 4);
+      if (j > 0 && !c.wait(&sh.kv_full[sk], ((kv + 1) / kKvStages) & 1)) return;
+      const uint64_t vb = v_desc + sv * (kTileBytes >> 4);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {  // as P's halves are written
-        if (!c.wait(&sh.p_full[s][h], np & 1)) return;
-        tc_fence_after();
-        if (lane == 0) {
+      for (int s = 0; s < 2; ++s) {
+        if (j < u.n[s]) {
+          const bool start = j == u.n[s] - 1;
+          if (start) {
+            if (no[s] > 0 && !c.wait(&sh.o_free[s], (no[s] - 1) & 1)) return;
+            ++no[s];
+          }
 #pragma unroll
-          for (int k = 4 * h; k < 4 * h + 4; ++k)
-            tc_mma_ts(o_tmem, s_tmem + 8 * k, b + k * (2048 >> 4), id_pv, !start || k > 0);
+          for (int h = 0; h < 2; ++h) {  // as P's halves are written
+            if (!c.wait(&sh.p_full[s][h], np[s] & 1)) return;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+              for (int k = 4 * h; k < 4 * h + 4; ++k)
+                tc_mma_ts(tmem + 256 + s * kTile, tmem + s * kTile + 8 * k, vb + k * (2048 >> 4),
+                          id_pv, !start || k > 0);
+              if (h == 1 && j > 0) qk(s, sk);
+              if (h == 1 && j == 0) tc_commit(&sh.o_full[s]);
+            }
+            __syncwarp();
+          }
+          ++np[s];
+        } else if (j > 0 && j - 1 < u.n[s]) {
+          if (lane == 0) qk(s, sk);  // the row tile's first
+          __syncwarp();
         }
-        __syncwarp();
       }
-      ++np;
       if (lane == 0) {
         tc_commit(&sh.kv_empty[sv]);
-        if (j == 0) tc_commit(&sh.o_full[s]);
+        if (j > 0) tc_commit(&sh.kv_empty[sk]);
+        if (j == 1) tc_commit(&sh.q_empty);
       }
       __syncwarp();
+      kv += j > 0 ? 2 : 1;
     }
   }
 }
 
-// ---- warp 15: V tiles that some row of the unit sees in part ----
+// ---- warps 14, 15: V tiles that some row of the unit sees in part ----
 template <int kType>
 __device__ __forceinline__ void clean_role(const Ctx& c) {
   Shared& sh = c.sh;
-  const int t = threadIdx.x & 31;
+  const int t = threadIdx.x & 63;  // 64 threads
   const uint32_t exp_mask = kType == XQA_F16 ? 0x7c00u : 0x7f80u;
   int kv = 0;
   for (int i = 0;; ++i) {
@@ -476,7 +491,7 @@ __device__ __forceinline__ void clean_role(const Ctx& c) {
         const int from = max(0, u.hidden - j * kTile);     // first row some token does not see
         const int past = min(kTile, u.len_k - j * kTile);  // first row past the sequence
         uint4* rows = reinterpret_cast<uint4*>(c.kv(st));
-        for (int x = from * 8 + t; x < kTile * 8; x += 32) {
+        for (int x = from * 8 + t; x < kTile * 8; x += 64) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint4& cell = rows[h * (kHalfBytes / 16) + x];
@@ -725,15 +740,15 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKvStages; ++i) {
       mbar_init(&sh.kv_full[i], 1);
-      mbar_init(&sh.kv_empty[i], 3);  // the tensor-core warps and the V warp
-      mbar_init(&sh.v_clean[i], 1);
+      mbar_init(&sh.kv_empty[i], 3);  // the tensor-core warp and the V warps
+      mbar_init(&sh.v_clean[i], 2);
     }
     for (int i = 0; i < kUnitSlots; ++i) {
       mbar_init(&sh.unit_full[i], 1);
       mbar_init(&sh.unit_empty[i], kUnitReaders);
     }
     mbar_init(&sh.q_full, 1);
-    mbar_init(&sh.q_empty, 2);
+    mbar_init(&sh.q_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh.s_full[s], 1);
       mbar_init(&sh.p_full[s][0], 4);
@@ -743,7 +758,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       mbar_init(&sh.stat_full[s], 4);
       mbar_init(&sh.stat_free[s], 4);
     }
-    mbar_init(&sh.drain, 2);
+    mbar_init(&sh.drain, 1);
     sh.abort_flag = 0;
     sh.status = aligned ? XQA_OK : XQA_ERR_LAUNCH;
     fence_mbar_init();
@@ -764,7 +779,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     __syncwarp();
     if (warp >= 12) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-      if (warp == 12 || warp == 14) tensor_role<kType>(c, (warp - 12) >> 1);
+      if (warp == 12) tensor_role<kType>(c);
       else if (warp == 13) load_role(c, &tm_q, &tm_k, &tm_v, kv_issued, q_issued);
       else clean_role<kType>(c);
     } else if (warp >= 8) {
@@ -778,10 +793,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   __syncwarp();
   // Products and their arrivals, and after an abort copies, may be in flight:
   // they end before the CTA's shared memory and TMEM are given up.
-  if (aligned && warp >= 12 && warp <= 14) {
+  if (aligned && (warp == 12 || warp == 13)) {
     int never = 0;
     bool ok = true;
-    if (warp != 13) {
+    if (warp == 12) {
       if ((threadIdx.x & 31) == 0) tc_commit(&sh.drain);
       __syncwarp();
       ok = mbar_wait_bounded(&sh.drain, 0, &never);
