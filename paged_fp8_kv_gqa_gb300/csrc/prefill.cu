@@ -53,6 +53,7 @@ constexpr int kPrefillThreads = 512;
 constexpr float kNoRowMax = -1e30f;              // as in the decode kernel
 constexpr float kLazyMax = 8.0f;                 // log2 units
 constexpr unsigned kAll = 0xffffffffu;
+constexpr uint32_t kWaitClocks = 2000000000u;    // about 1 s
 constexpr int kUnitReaders = 15;  // 8 softmax, 4 epilogue, 1 tensor-core, 2 V warps
 
 // One unit of work, written by the loading warp.
@@ -72,7 +73,7 @@ struct Unit {
 struct Shared {
   uint64_t kv_full[kKvStages], kv_empty[kKvStages];
   uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
-  uint64_t q_full, q_empty;
+  uint64_t q_full[2], q_empty[2];
   uint64_t v_clean[kKvStages];   // the stage's V tile may be used (masked tiles only)
   uint64_t s_full[2];            // S ready
   uint64_t p_full[2][2];         // the first / second 64 keys of P written
@@ -224,6 +225,13 @@ __device__ __forceinline__ void tma_load_kv(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
 // What every warp role works on.
 struct Ctx {
   const PrefillParams& p;
@@ -234,15 +242,16 @@ struct Ctx {
 
   __device__ __forceinline__ uint8_t* kv(int stage) const { return tiles + (2 + stage) * kTileBytes; }
 
-  // Warp-uniform bounded wait; false ends the role (the CTA is aborted).
+  // Warp-uniform wait, for about a second at most; false ends the role (the CTA is
+  // aborted). Short: the roles wait in many places and share an instruction cache.
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
-    const bool ok = mbar_wait_bounded(bar, parity, &sh.abort_flag);
-    if (__all_sync(kAll, ok)) return true;
-    if ((threadIdx.x & 31) == 0) {
-      *(volatile int*)&sh.abort_flag = 1;
-      record_status(&sh.status, XQA_ERR_DEVICE_TIMEOUT);
-    }
-    __syncwarp();
+    if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+    volatile int* abort = &sh.abort_flag;
+    const uint32_t t0 = (uint32_t)clock();
+    do {
+      if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+    } while (__all_sync(kAll, !*abort && (uint32_t)clock() - t0 < kWaitClocks));
+    *abort = 1;
     return false;
   }
   __device__ __forceinline__ bool get_unit(int i, Unit& u) const {
@@ -262,7 +271,7 @@ struct Ctx {
 // ---- warp 13: the units of this CTA and their TMA loads ----
 __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
                                           const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                                          int& kv_issued, int& q_issued) {
+                                          int& kv_issued, int (&q_issued)[2]) {
   const PrefillParams& p = c.p;
   Shared& sh = c.sh;
   const int lane = threadIdx.x & 31;
@@ -343,132 +352,177 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
     next = __shfl_sync(kAll, next, 0);
     const int n = max(w.n[0], w.n[1]);
     if (n == 0) continue;
-    if (q_issued > 0 && !c.wait(&sh.q_empty, (q_issued - 1) & 1)) return;
-    if (lane == 0) {
-      const int box = p.group * p.tile_tokens * 128;  // bytes of a half tile
-      mbar_arrive_expect_tx(&sh.q_full, 4 * box);
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
+    if (lane < 4)  // into L2 while the unit before still uses Q's place
+      tma_prefetch_4d(tm_q, 64 * (lane & 1), 0, w.head, w.q_row + (lane >> 1) * p.tile_tokens);
+    for (int t = 0; t < 2 * n; ++t) {  // K(n-1), Q, V(n-1), K(n-2), V(n-2), ...
+      const int st = kv_issued % kKvStages, j = n - 1 - (t >> 1);
+      if (kv_issued >= kKvStages && !c.wait(&sh.kv_empty[st], (kv_issued / kKvStages - 1) & 1))
+        return;
+      if (lane == 0) {
+        const CUtensorMap* tm = (t & 1) ? tm_v : tm_k;
+        mbar_arrive_expect_tx(&sh.kv_full[st], kTileBytes);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          tma_load_4d(c.tiles + s * kTileBytes + h * kHalfBytes, tm_q, &sh.q_full, 64 * h, 0,
-                      w.head, w.q_row + s * p.tile_tokens);
-    }
-    ++q_issued;
-    for (int j = n - 1; j >= 0; --j) {
-#pragma unroll 1
-      for (int v = 0; v < 2; ++v) {
-        const int st = kv_issued % kKvStages;
-        if (kv_issued >= kKvStages && !c.wait(&sh.kv_empty[st], (kv_issued / kKvStages - 1) & 1))
-          return;
+          tma_load_kv(c.kv(st) + h * kHalfBytes, tm, &sh.kv_full[st], 64 * h, w.head,
+                      w.k_row + j * kTile);
+      }
+      ++kv_issued;
+      if (t > 0) continue;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (w.n[s] == 0) continue;
+        if (q_issued[s] > 0 && !c.wait(&sh.q_empty[s], (q_issued[s] - 1) & 1)) return;
         if (lane == 0) {
-          const CUtensorMap* tm = v ? tm_v : tm_k;
-          mbar_arrive_expect_tx(&sh.kv_full[st], kTileBytes);
+          const int box = p.group * p.tile_tokens * 128;  // bytes of a half tile
+          mbar_arrive_expect_tx(&sh.q_full[s], 2 * box);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            tma_load_kv(c.kv(st) + h * kHalfBytes, tm, &sh.kv_full[st], 64 * h, w.head,
-                        w.k_row + j * kTile);
+            tma_load_4d(c.tiles + s * kTileBytes + h * kHalfBytes, tm_q, &sh.q_full[s], 64 * h, 0,
+                        w.head, w.q_row + s * p.tile_tokens);
         }
-        ++kv_issued;
+        ++q_issued[s];
       }
     }
   }
 }
 
+// A value that is the same in every lane, told to the compiler.
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+  return (uint64_t)__shfl_sync(kAll, (uint32_t)(v >> 32), 0) << 32 |
+         __shfl_sync(kAll, (uint32_t)v, 0);
+}
+
+// One lane of the (converged) warp. Products and copies are issued by it: the
+// compiler then knows that a single thread runs and keeps descriptors and addresses
+// in uniform registers; under `lane == 0` each product costs more to issue than to
+// execute (1 x 16384: 1775 us against 1420).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---- warp 12: the products ----
+// The row tiles in turn: O += P V of tile j, then S of the next tile (j - 1, or the
+// next unit's first), which takes the place of P. The order is fixed, so the row
+// tiles settle half a period apart and one's softmax runs under the other's
+// products; it runs on across units, so a new unit starts without a gap. The code is
+// kept short: it runs once a tile between the softmax warps' long loops and is
+// fetched anew each time (products cut to the keys that a diagonal tile's rows see
+// saved less than their code cost: 1 x 16384 1500 us against 1403, ragged prompts
+// 205 against 190).
 template <int kType>
 __device__ __forceinline__ void tensor_role(const Ctx& c) {
   Shared& sh = c.sh;
-  const int lane = threadIdx.x & 31;
-  const uint32_t id_qk = instr_desc<kType>(false), id_pv = instr_desc<kType>(true);
-  // descriptors and addresses are warp-uniform and stay in uniform registers: built
-  // per product by one lane, they cost more than the product (180 cycles against 64)
   const uint32_t tiles = __shfl_sync(kAll, smem_addr(c.tiles), 0);
   const uint32_t tmem = __shfl_sync(kAll, c.tmem, 0);
   const uint64_t q_desc = desc_k_major(tiles);
-  const uint64_t k_desc = desc_k_major(tiles + 2 * kTileBytes);   // stage 0 of the ring
+  const uint64_t k_desc = desc_k_major(tiles + 2 * kTileBytes);  // stage 0 of the ring
   const uint64_t v_desc = desc_mn_major(tiles + 2 * kTileBytes);
-  int kv = 0, units_with_work = 0;
-  int np[2] = {0, 0}, no[2] = {0, 0};  // P tiles used, O tiles started
-  uint32_t cleaned = 0;                // phase of v_clean, one bit per stage
-  auto qk = [&](int s, int st) {       // one lane
-    const uint64_t a = q_desc + s * (kTileBytes >> 4), b = k_desc + st * (kTileBytes >> 4);
+  int i = -1;
+  auto next_unit = [&](int (&n)[2], int& hidden) {  // the next one with work
+    do {
+      Unit w;
+      if (!c.get_unit(++i, w)) return false;
+      c.free_unit(i);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t off = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
-      tc_mma_ss(tmem + s * kTile, a + off, b + off, id_qk, k > 0);
-    }
-    tc_commit(&sh.s_full[s]);
+      for (int s = 0; s < 2; ++s) n[s] = __shfl_sync(kAll, w.n[s], 0);  // uniform
+      hidden = __shfl_sync(kAll, w.hidden, 0);
+    } while (max(n[0], n[1]) == 0);
+    return true;
   };
-  for (int i = 0;; ++i) {
-    Unit u;
-    if (!c.get_unit(i, u)) return;
-    c.free_unit(i);
-    const int n = max(u.n[0], u.n[1]);
-    if (n == 0) continue;
-    if (!c.wait(&sh.q_full, units_with_work & 1)) return;
-    ++units_with_work;
-    int sk = kv % kKvStages;
-    if (!c.wait(&sh.kv_full[sk], (kv / kKvStages) & 1)) return;
-    tc_fence_after();
-    if (lane == 0) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (u.n[s] == n) qk(s, sk);
-      tc_commit(&sh.kv_empty[sk]);
-      if (n == 1) tc_commit(&sh.q_empty);
-    }
-    __syncwarp();
-    ++kv;
-    // The row tiles in turn: O += P V of tile j, then S of tile j - 1 (which takes
-    // the place of P). The order is fixed, so the tiles settle half a period apart
-    // and one's softmax runs under the other's products.
-    for (int j = n - 1; j >= 0; --j) {
-      const int sv = kv % kKvStages;
-      sk = (kv + 1) % kKvStages;
-      if (!c.wait(&sh.kv_full[sv], (kv / kKvStages) & 1)) return;
-      if ((j + 1) * kTile > u.hidden) {  // masked: after the V warps are done with it
-        if (!c.wait(&sh.v_clean[sv], (cleaned >> sv) & 1)) return;
-        cleaned ^= 1u << sv;
+  // tiles of the current unit (row tile s has n[s]) and of the next; before the first
+  // unit, an empty one
+  int n[2] = {0, 0}, hidden = 0, n2[2], hidden2;
+  if (!next_unit(n2, hidden2)) return;
+  bool more = true, begin = true;
+  int j = 0;                // tile of the V slot
+  int sv = 0, sk = 0;       // ring slots of this round's V and K tile
+  uint32_t pv = 0, pk = 0;  // their phases
+  // phases, a bit for each row tile (p: two, o: of a barrier never waited for) or stage
+  uint32_t ph_q = 0, ph_p = 0, ph_o = 3, ph_clean = 0;
+  for (;;) {
+    // V tile j of the current unit (none in the first round), then a K tile: j - 1, or
+    // the next unit's first
+    if (!begin) {
+      if (!c.wait(&sh.kv_full[sv], pv)) return;
+      if ((j + 1) * kTile > hidden) {  // masked: after the V warps are done with it
+        if (!c.wait(&sh.v_clean[sv], ph_clean >> sv & 1)) return;
+        ph_clean ^= 1u << sv;
       }
-      if (j > 0 && !c.wait(&sh.kv_full[sk], ((kv + 1) / kKvStages) & 1)) return;
-      const uint64_t vb = v_desc + sv * (kTileBytes >> 4);
+      if (j == 0) {
+        more = next_unit(n2, hidden2);
+        if (!more && *(volatile int*)&sh.abort_flag) return;
+      }
+      sk = sv + 1 == kKvStages ? 0 : sv + 1;
+      pk = sk == 0 ? pv ^ 1 : pv;
+    }
+    const bool cross = j == 0;         // the K tile is the next unit's
+    const bool next = !cross || more;  // there is one
+    if (next && !c.wait(&sh.kv_full[sk], pk)) return;
+    const int nk = cross ? max(n2[0], n2[1]) : 0;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (j < u.n[s]) {
-          const bool start = j == u.n[s] - 1;
-          if (start) {
-            if (no[s] > 0 && !c.wait(&sh.o_free[s], (no[s] - 1) & 1)) return;
-            ++no[s];
+    for (int s = 0; s < 2; ++s) {
+      const uint32_t s_tmem = tmem + s * kTile, o_tmem = s_tmem + 256;
+      if (!begin && j < n[s]) {
+        const bool start = j == n[s] - 1;
+        if (start) {
+          if (!c.wait(&sh.o_free[s], ph_o >> s & 1)) return;
+          ph_o ^= 1u << s;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // as P's halves are written
+          const uint32_t bit = 2 * s + h;
+          if (!c.wait(&sh.p_full[s][h], ph_p >> bit & 1)) return;
+          ph_p ^= 1u << bit;
+          tc_fence_after();
+          const uint64_t vb = v_desc + sv * (kTileBytes >> 4) + h * (4 * 2048 >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc_mma_ts(o_tmem, s_tmem + 32 * h + 8 * k, vb + k * (2048 >> 4),
+                        instr_desc<kType>(true), !start || h + k > 0);
           }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {  // as P's halves are written
-            if (!c.wait(&sh.p_full[s][h], np[s] & 1)) return;
-            tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
-              for (int k = 4 * h; k < 4 * h + 4; ++k)
-                tc_mma_ts(tmem + 256 + s * kTile, tmem + s * kTile + 8 * k, vb + k * (2048 >> 4),
-                          id_pv, !start || k > 0);
-              if (h == 1 && j > 0) qk(s, sk);
-              if (h == 1 && j == 0) tc_commit(&sh.o_full[s]);
-            }
-            __syncwarp();
-          }
-          ++np[s];
-        } else if (j > 0 && j - 1 < u.n[s]) {
-          if (lane == 0) qk(s, sk);  // the row tile's first
           __syncwarp();
         }
+        if (cross && elect_one()) tc_commit(&sh.o_full[s]);
+        __syncwarp();
       }
-      if (lane == 0) {
-        tc_commit(&sh.kv_empty[sv]);
-        if (j > 0) tc_commit(&sh.kv_empty[sk]);
-        if (j == 1) tc_commit(&sh.q_empty);
+      // S: tile j - 1, or the next unit's first; the row tile's first waits for its Q
+      if (!(cross ? more && n2[s] == nk : j - 1 < n[s])) continue;
+      if (cross || j == n[s]) {
+        if (!c.wait(&sh.q_full[s], ph_q >> s & 1)) return;
+        ph_q ^= 1u << s;
+      }
+      tc_fence_after();
+      const uint64_t a = q_desc + s * (kTileBytes >> 4), b = k_desc + sk * (kTileBytes >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t off = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+          tc_mma_ss(s_tmem, a + off, b + off, instr_desc<kType>(false), k > 0);
+        }
+        tc_commit(&sh.s_full[s]);
+        if (cross ? nk == 1 : j == 1) tc_commit(&sh.q_empty[s]);
       }
       __syncwarp();
-      kv += j > 0 ? 2 : 1;
     }
+    if (elect_one()) {
+      if (!begin) tc_commit(&sh.kv_empty[sv]);
+      if (next) tc_commit(&sh.kv_empty[sk]);
+    }
+    __syncwarp();
+    if (!next) return;
+    sv = sk + 1 == kKvStages ? 0 : sk + 1;
+    pv = sv == 0 ? pk ^ 1 : pk;
+    if (cross) {  // on to the next unit
+      n[0] = n2[0], n[1] = n2[1], hidden = hidden2;
+      j = nk;
+      begin = false;
+    }
+    --j;
   }
 }
 
@@ -747,9 +801,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       mbar_init(&sh.unit_full[i], 1);
       mbar_init(&sh.unit_empty[i], kUnitReaders);
     }
-    mbar_init(&sh.q_full, 1);
-    mbar_init(&sh.q_empty, 1);
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&sh.q_full[s], 1);
+      mbar_init(&sh.q_empty[s], 1);
       mbar_init(&sh.s_full[s], 1);
       mbar_init(&sh.p_full[s][0], 4);
       mbar_init(&sh.p_full[s][1], 4);
@@ -773,7 +827,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   __syncthreads();
   tc_fence_after();
   griddep_wait();  // inputs are read, and outputs written, after the kernels before this one
-  int kv_issued = 0, q_issued = 0;
+  int kv_issued = 0, q_issued[2] = {0, 0};
   if (aligned) {
     const Ctx c{p, sh, smem, stats, sh.tmem};
     __syncwarp();
@@ -797,13 +851,15 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     int never = 0;
     bool ok = true;
     if (warp == 12) {
-      if ((threadIdx.x & 31) == 0) tc_commit(&sh.drain);
+      if (elect_one()) tc_commit(&sh.drain);
       __syncwarp();
       ok = mbar_wait_bounded(&sh.drain, 0, &never);
     } else if (*(volatile int*)&sh.abort_flag) {
       for (int k = max(0, kv_issued - kKvStages); k < kv_issued; ++k)
         ok = mbar_wait_bounded(&sh.kv_full[k % kKvStages], (k / kKvStages) & 1, &never) && ok;
-      if (q_issued > 0) ok = mbar_wait_bounded(&sh.q_full, (q_issued - 1) & 1, &never) && ok;
+      for (int s = 0; s < 2; ++s)
+        if (q_issued[s] > 0)
+          ok = mbar_wait_bounded(&sh.q_full[s], (q_issued[s] - 1) & 1, &never) && ok;
     }
     if (!ok) atomicExch(&sh.status, XQA_ERR_DRAIN_TIMEOUT);
     __syncwarp();
@@ -813,6 +869,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   tc_fence_after();
   if (warp == 12) tmem_dealloc(sh.tmem, 512);
   if (threadIdx.x == 0) {
+    if (sh.abort_flag) record_status(&sh.status, XQA_ERR_DEVICE_TIMEOUT);
     p.status[blockIdx.x] = sh.status;
     if (blockIdx.x == 0) p.header[0] = gridDim.x;
     // the last CTA leaves the counters at zero for the next call
