@@ -542,36 +542,34 @@ __device__ __forceinline__ void clean_role(const Ctx& c) {
       const int st = kv % kKvStages, j = n - 1 - (k >> 1);
       if (!c.wait(&sh.kv_full[st], (kv / kKvStages) & 1)) return;
       if ((k & 1) && (j + 1) * kTile > u.hidden) {
-        const int from = max(0, u.hidden - j * kTile);     // first row some token does not see
         const int past = min(kTile, u.len_k - j * kTile);  // first row past the sequence
-        uint4* rows = reinterpret_cast<uint4*>(c.kv(st));
-        for (int x = from * 8 + t; x < kTile * 8; x += 64) {
+        const int from = max(0, u.hidden - j * kTile);     // first row some token does not see
+        uint4* rows = reinterpret_cast<uint4*>(c.kv(st));  // 8 chunks of 16 bytes a row and half
+        // the largest magnitude, both halves of a word at once: one test for all
+        uint32_t top = 0;
+        for (int x = from * 8 + t; x < past * 8; x += 64) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint4& cell = rows[h * (kHalfBytes / 16) + x];
-            if ((x >> 3) >= past) {
-              cell = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint32_t w[4] = {cell.x, cell.y, cell.z, cell.w};
-            bool hit = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if ((w[e] & exp_mask) == exp_mask) {
-                w[e] &= 0xffff0000u;
-                hit = true;
-              }
-              if ((w[e] & exp_mask << 16) == exp_mask << 16) {
-                w[e] &= 0x0000ffffu;
-                hit = true;
-              }
-            }
-            if (hit) {
-              cell = make_uint4(w[0], w[1], w[2], w[3]);
-              found = true;
-            }
+            const uint4 w = rows[h * (kHalfBytes / 16) + x];
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                         __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
           }
         }
+        if ((top & 0xffffu) >= exp_mask || top >> 16 >= exp_mask) {
+          found = true;
+          for (int x = from * 8 + t; x < past * 8; x += 64)
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e) {  // the words of both halves
+              uint32_t* w = reinterpret_cast<uint32_t*>(rows + (e >> 2) * (kHalfBytes / 16) + x) + (e & 3);
+              uint32_t v = *w;
+              if ((v & exp_mask) == exp_mask) v &= 0xffff0000u;
+              if ((v & exp_mask << 16) == exp_mask << 16) v &= 0x0000ffffu;
+              *w = v;
+            }
+        }
+        for (int x = past * 8 + t; x < kTile * 8; x += 64)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) rows[h * (kHalfBytes / 16) + x] = make_uint4(0, 0, 0, 0);
         if (found) *(volatile int*)&sh.not_finite[i % kUnitSlots] = 1;
         fence_proxy_async_smem();  // before the tensor core reads the tile
         c.arrive(&sh.v_clean[st]);
@@ -629,10 +627,14 @@ __device__ __forceinline__ void softmax_role(const Ctx& c, int s) {
       for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32 * q, r + 32 * q);
       tmem_wait_ld();
       if ((j + 1) * kTile > clear) {
-        const int lim = vis - j * kTile;
+        const int lim = vis - j * kTile, lo = __reduce_min_sync(kAll, lim);
 #pragma unroll
-        for (int k = 0; k < kTile; ++k)
-          if (k >= lim) r[k] = 0xff800000u;  // -inf
+        for (int q = 0; q < 4; ++q) {
+          if (32 * q + 32 <= lo) continue;  // the warp's rows see these
+#pragma unroll
+          for (int k = 32 * q; k < 32 * q + 32; ++k)
+            if (k >= lim) r[k] = 0xff800000u;  // -inf
+        }
       }
       float mx[4];  // three-operand maxima
 #pragma unroll
