@@ -354,7 +354,7 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
     if (n == 0) continue;
     if (lane < 4)  // into L2 while the unit before still uses Q's place
       tma_prefetch_4d(tm_q, 64 * (lane & 1), 0, w.head, w.q_row + (lane >> 1) * p.tile_tokens);
-    for (int t = 0; t < 2 * n; ++t) {  // K(n-1), Q, V(n-1), K(n-2), V(n-2), ...
+    for (int t = 0; t < 2 * n; ++t) {  // K(n-1), V(n-1), Q, K(n-2), V(n-2), ...
       const int st = kv_issued % kKvStages, j = n - 1 - (t >> 1);
       if (kv_issued >= kKvStages && !c.wait(&sh.kv_empty[st], (kv_issued / kKvStages - 1) & 1))
         return;
@@ -367,7 +367,7 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
                       w.k_row + j * kTile);
       }
       ++kv_issued;
-      if (t > 0) continue;
+      if (t != 1) continue;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (w.n[s] == 0) continue;
