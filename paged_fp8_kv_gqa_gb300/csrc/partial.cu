@@ -949,7 +949,6 @@ __device__ __forceinline__ void issue_page(const PartialParams& p, const CUtenso
                                            const CUtensorMap* tm_v, CtaShared<G>& sh,
                                            uint8_t* stages, int slot, int y, int bad, int sg,
                                            uint64_t policy) {
-  constexpr int kFmt = G::kFmt;
   uint8_t* st = stages + slot * G::kStage;
   sh.stage_bad[slot] = bad;
   fence_proxy_async_smem();  // this slot's earlier shared reads come before the TMA writes
@@ -958,11 +957,7 @@ __device__ __forceinline__ void issue_page(const PartialParams& p, const CUtenso
     mbar_arrive(&sh.full_bar[slot]);
   } else {
     mbar_arrive_expect_tx(&sh.full_bar[slot], G::kStage);
-    if constexpr (kFmt == XQA_KV_E2M1) {
-      const size_t at = (size_t)(y / kBlockSize) * kSliceBytes4;  // y: as in an HND pool
-      bulk_load(st, p.k_pool + at, kSliceBytes4, &sh.full_bar[slot], policy);
-      bulk_load(st + kSliceBytes4, p.v_pool + at, kSliceBytes4, &sh.full_bar[slot], policy);
-    } else if (p.kv_layout == XQA_LAYOUT_HND) {
+    if (p.kv_layout == XQA_LAYOUT_HND) {
       tma_load_2d(st, tm_k, &sh.full_bar[slot], 0, y, policy);
       tma_load_2d(st + kPageBytes, tm_v, &sh.full_bar[slot], 0, y, policy);
     } else {  // NHD: box (128 dims, 1 kv head, 16 tokens) at (0, kvh, page*16)
@@ -1006,18 +1001,12 @@ __device__ __forceinline__ void consume_pages(const PartialParams& p,
     stamp(3);
   }
 #endif
-  using Regs = typename PageOf<kFmt>::Regs;
   const uint8_t* stg0 = stages + slot0 * G::kStage;
   const uint8_t* stg1 = stages + slot1 * G::kStage;
   const bool bad0 = sh.stage_bad[slot0] != 0, bad1 = pair && sh.stage_bad[slot1] != 0;
-  Regs regs[2];
-  if constexpr (kFmt == XQA_KV_E2M1) {
-    regs[0] = load_page4(stg0, stg0 + kSliceBytes4, g, c);
-    if (pair) regs[1] = load_page4(stg1, stg1 + kSliceBytes4, g, c);
-  } else {
-    regs[0] = load_page(stg0, stg0 + kPageBytes, g, c);
-    if (pair) regs[1] = load_page(stg1, stg1 + kPageBytes, g, c);
-  }
+  PageRegs regs[2];
+  regs[0] = load_page(stg0, stg0 + kPageBytes, g, c);
+  if (pair) regs[1] = load_page(stg1, stg1 + kPageBytes, g, c);
   // The pages are in registers: refill their slots with the pages kStages
   // ahead right away (warp-uniform decision), before the math.
   if (!__any_sync(kFull, *abort != 0)) {
@@ -1031,15 +1020,117 @@ __device__ __forceinline__ void consume_pages(const PartialParams& p,
   } else {
     if (bad0 || bad1) poisoned = 1;
     if (!bad0) {
-      const Regs one[1] = {regs[0]};
+      const PageRegs one[1] = {regs[0]};
       const int tk[1] = {t0}, nv[1] = {nv0};
       process_pages<kFmt, 1, NT, kMulti>(st, one, qf, tk, nv, sl, scale_log2, g, c);
     }
     if (pair && !bad1) {
-      const Regs one[1] = {regs[1]};
+      const PageRegs one[1] = {regs[1]};
       const int tk[1] = {t1}, nv[1] = {nv1};
       process_pages<kFmt, 1, NT, kMulti>(st, one, qf, tk, nv, sl, scale_log2, g, c);
     }
+  }
+}
+
+// ---- 4 bits: half the bytes of a page for the same arithmetic, so the page loop is
+// bound by instructions. Its ring is kept in registers: a warp's next slot to fill
+// and to use, their phases, and which of its slots hold a bad page.
+struct WarpRing {
+  int fill, use;       // of the warp's own slots (slot = warp + kWarps * index)
+  uint32_t phase;      // of the slot to use
+  uint32_t bad;        // bit per own slot
+};
+
+// One lane of the warp; tells the compiler that a single thread runs, so the copies'
+// operands stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Fills the warp's next slot with slice `slice` (-1: a bad block id; the slot is
+// flagged and its barrier completes without data). Warp-uniform arguments.
+template <class G>
+__device__ __forceinline__ void fill_slot4(const PartialParams& p, CtaShared<G>& sh,
+                                           uint8_t* stages, WarpRing& ring, int warp, int slice,
+                                           uint64_t policy) {
+  const int slot = warp + G::kWarps * ring.fill;
+  const uint32_t bit = 1u << ring.fill;
+  ring.bad = slice < 0 ? ring.bad | bit : ring.bad & ~bit;
+  ring.fill = ring.fill + 1 == G::kLookahead ? 0 : ring.fill + 1;
+  if (elect_one()) {
+    uint64_t* bar = &sh.full_bar[slot];
+    fence_proxy_async_smem();  // this slot's earlier shared reads come before the copies
+    if (slice < 0) {
+      record_status(&sh.cta_status, XQA_ERR_BAD_BLOCK_ID);
+      mbar_arrive(bar);
+    } else {
+      uint8_t* st = stages + slot * G::kStage;
+      const size_t at = (size_t)slice * kSliceBytes4;
+      mbar_arrive_expect_tx(bar, G::kStage);
+      bulk_load(st, p.k_pool + at, kSliceBytes4, bar, policy);
+      bulk_load(st + kSliceBytes4, p.v_pool + at, kSliceBytes4, bar, policy);
+    }
+  }
+  __syncwarp();
+}
+
+// consume_pages for the 4-bit ring: the warp's next one or two pages.
+template <class G, bool kMulti, typename Refill>
+__device__ __forceinline__ void consume_pages4(CtaShared<G>& sh, const uint8_t* stages,
+                                               WarpRing& ring, int warp, bool pair, int t0, int t1,
+                                               int ctx, WarpState<G::kTiles>& st,
+                                               const uint32_t (&qf)[G::kTiles][16],
+                                               const SegLimits<G::kTiles>& sl, float scale_log2,
+                                               int g, int c, int lane, int& poisoned,
+                                               Refill&& refill) {
+  constexpr int NT = G::kTiles;
+  PageRegs4 regs[2];
+  uint32_t bad = 0;
+  bool ready = true;
+  auto take = [&](PageRegs4& r, int i) {  // wait for the next slot and move it into registers
+    const int slot = warp + G::kWarps * ring.use;
+    uint64_t* bar = &sh.full_bar[slot];
+    if (!__all_sync(kFull, mbar_try_wait(bar, ring.phase)))
+      ready = __all_sync(kFull, mbar_wait_bounded(bar, ring.phase, &sh.abort_flag)) && ready;
+    const uint8_t* page = stages + slot * G::kStage;
+    r = load_page4(page, page + kSliceBytes4, g, c);
+    bad |= (ring.bad >> ring.use & 1u) << i;
+    ring.use += 1;
+    if (ring.use == G::kLookahead) {
+      ring.use = 0;
+      ring.phase ^= 1u;
+    }
+  };
+  take(regs[0], 0);
+  if (pair) take(regs[1], 1);
+  if (!ready) {
+    poisoned = 1;
+    if (lane == 0) {
+      *(volatile int*)&sh.abort_flag = 1;
+      record_status(&sh.cta_status, XQA_ERR_DEVICE_TIMEOUT);
+    }
+    __syncwarp();
+    return;
+  }
+  __syncwarp();  // every lane's reads of the slots are done
+  refill(pair ? 2 : 1);
+  const int nv0 = min(kBlockSize, ctx - t0), nv1 = min(kBlockSize, ctx - t1);
+  if (pair && bad == 0) {
+    const int tk[2] = {t0, t1}, nv[2] = {nv0, nv1};
+    process_pages<XQA_KV_E2M1, 2, NT, kMulti>(st, regs, qf, tk, nv, sl, scale_log2, g, c);
+    return;
+  }
+  if (bad) poisoned = 1;
+#pragma unroll 1
+  for (int i = 0; i < (pair ? 2 : 1); ++i) {
+    if (bad >> i & 1) continue;
+    const PageRegs4 one[1] = {i == 0 ? regs[0] : regs[1]};
+    const int tk[1] = {i == 0 ? t0 : t1}, nv[1] = {i == 0 ? nv0 : nv1};
+    process_pages<XQA_KV_E2M1, 1, NT, kMulti>(st, one, qf, tk, nv, sl, scale_log2, g, c);
   }
 }
 
@@ -1160,6 +1251,7 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
     p.hints[(size_t)blockIdx.x * kHintPages + 2 * warp + lane] = lane < owned && !cur.bad ? row : -1;
   }
   int cur_base = 0;
+  WarpRing ring{0, 0, 0, 0};  // 4 bits only
   auto issue_next = [&]() {
     if (issued >= owned) return;
     const int k = issued++;
@@ -1167,6 +1259,11 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
       cur = nxt;
       cur_base += 32;
       nxt = load_batch<kWarps>(p, segs, s_first, s_hi + 1, cbeg, npages, warp, cur_base + 32, lane);
+    }
+    if constexpr (G::kFour) {
+      const int slice = __shfl_sync(kFull, cur.bad ? -1 : cur.y / kBlockSize, k - cur_base);
+      fill_slot4<G>(p, sh, sm.stages, ring, warp, slice, policy);
+      return;
     }
     const int y = __shfl_sync(kFull, cur.y, k - cur_base);
     const int bad = __shfl_sync(kFull, cur.bad, k - cur_base);
@@ -1211,6 +1308,14 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
     for (int q = q0 + ((warp - q0 % kWarps) + kWarps) % kWarps; q < qe; q += 2 * kWarps) {
       const bool pair = q + kWarps < qe;
       const int j0 = cbeg + q - sb;  // page index within the sequence
+      if constexpr (G::kFour)
+        consume_pages4<G, kMulti>(sh, sm.stages, ring, warp, pair, j0 * kBlockSize,
+                                  (j0 + kWarps) * kBlockSize, ctx, st, qf, sl, scale_log2, g, c,
+                                  lane, poisoned, [&](int n) {
+                                    issue_next();
+                                    if (n == 2) issue_next();
+                                  });
+      else
       consume_pages<G, kMulti>(p, sh, sm.stages, q % kStages, (q / kStages) & 1,
                                       (q + kWarps) % kStages, ((q + kWarps) / kStages) & 1, pair,
                                       j0 * kBlockSize, (j0 + kWarps) * kBlockSize, ctx, st, qf,
@@ -1709,11 +1814,19 @@ __global__ void __launch_bounds__(PartialGeom<kFmt, NT>::kThreads, 1)
     int ij = next_piece(warp), ioff = 0;  // the piece being issued, its next page
     int ij_next = next_piece(ij + kWarps);
     PageBatch wcur = fetch(ij), wnxt = fetch(ij_next);
+    WarpRing ring{0, 0, 0, 0};  // 4 bits only
     auto issue_next_w = [&]() {
       while (ij < nsr) {
         int pb, len;
         piece(ij, pb, len);
         if (ioff < len) {
+          if constexpr (G::kFour) {
+            const int slice = __shfl_sync(kFull, wcur.bad ? -1 : wcur.y / kBlockSize, ioff);
+            ++ioff;
+            ++issued;
+            fill_slot4<G>(p, sh, sm.stages, ring, warp, slice, policy);
+            return;
+          }
           const int y = __shfl_sync(kFull, wcur.y, ioff);
           const int bad = __shfl_sync(kFull, wcur.bad, ioff);
           ++ioff;
@@ -1762,6 +1875,13 @@ __global__ void __launch_bounds__(PartialGeom<kFmt, NT>::kThreads, 1)
       for (int o = 0; o < len; o += 2) {
         const bool pair = o + 1 < len;
         const int t0 = (pb + o - sb) * kBlockSize;
+        if constexpr (G::kFour)
+          consume_pages4<G, kMulti>(sh, sm.stages, ring, warp, pair, t0, t0 + kBlockSize, ctx, st,
+                                    qf, sl, scale_log2, g, c, lane, poisoned, [&](int n) {
+                                      issue_next_w();
+                                      if (n == 2) issue_next_w();
+                                    });
+        else
         consume_pages<G, kMulti>(p, sh, sm.stages, (warp + kWarps * k) % kStages,
                                         (k / kAhead) & 1, (warp + kWarps * (k + 1)) % kStages,
                                         ((k + 1) / kAhead) & 1, pair, t0, t0 + kBlockSize, ctx,
