@@ -124,6 +124,11 @@ __device__ __forceinline__ void consumer_bar() {
   asm volatile("bar.sync 1, %0;" ::"n"(G::kThreads) : "memory");
 }
 
+// Barrier of two neighbouring warps (names 2 .. 9).
+__device__ __forceinline__ void team_bar(int team) {
+  asm volatile("bar.sync %0, 64;" ::"r"(team + 2) : "memory");
+}
+
 // Largest s in [lo, nseg) with seg_start[s] <= page, given seg_start[lo] <= page
 // < seg_start[nseg]. `seg_start` may point to shared or global memory.
 __device__ __forceinline__ int find_segment(const int32_t* seg_start, int lo, int nseg, int page) {
@@ -311,11 +316,14 @@ __device__ __forceinline__ void process_pages(WarpState<NT>& st,
       // values s * code in fp16, exact: 2 x 4 significant bits, 2^-10 .. 2688
       const uint32_t ka[4] = {r[pi].ka.x, r[pi].ka.y, r[pi].ka.z, r[pi].ka.w};
       const uint32_t kb[4] = {r[pi].kb.x, r[pi].kb.y, r[pi].kb.z, r[pi].kb.w};
-      const uint32_t sa = e4m3x2_to_f16x2(r[pi].ksa), sb = e4m3x2_to_f16x2(r[pi].ksb);
+      const uint32_t ua = e4m3x2_to_f16x2(r[pi].ksa), ub = e4m3x2_to_f16x2(r[pi].ksb);
+      const __half2 sa = *reinterpret_cast<const __half2*>(&ua);
+      const __half2 sb = *reinterpret_cast<const __half2*>(&ub);
 #pragma unroll
       for (int w = 0; w < 4; ++w) {  // dims 32c + 8w .. + 8
-        const uint32_t sel = w < 2 ? 0x1010u : 0x3232u;
-        const uint32_t fa = prmt(sa, sa, sel), fb = prmt(sb, sb, sel);
+        // one scale for both halves: an operand's half, not a permutation of its own
+        const __half2 fa = w < 2 ? __low2half2(sa) : __high2half2(sa);
+        const __half2 fb = w < 2 ? __low2half2(sb) : __high2half2(sb);
         uint32_t xa[4], xb[4];
         e2m1x8_to_f16x2(ka[w], xa);
         e2m1x8_to_f16x2(kb[w], xb);
@@ -1033,12 +1041,13 @@ __device__ __forceinline__ void consume_pages(const PartialParams& p,
 }
 
 // ---- 4 bits: half the bytes of a page for the same arithmetic, so the page loop is
-// bound by instructions. Its ring is kept in registers: a warp's next slot to fill
-// and to use, their phases, and which of its slots hold a bad page.
+// bound by instructions. The ring's state is in registers: the slot to fill and the
+// slot to use, its phase, and which of the slots hold a bad page. A warp's slots lie
+// side by side.
 struct WarpRing {
-  int fill, use;       // of the warp's own slots (slot = warp + kWarps * index)
-  uint32_t phase;      // of the slot to use
-  uint32_t bad;        // bit per own slot
+  int fill, use;   // of the warp's own slots
+  uint32_t phase;  // of the slot to use
+  uint32_t bad;    // bit per own slot
 };
 
 // One lane of the warp; tells the compiler that a single thread runs, so the copies'
@@ -1057,7 +1066,7 @@ template <class G>
 __device__ __forceinline__ void fill_slot4(const PartialParams& p, CtaShared<G>& sh,
                                            uint8_t* stages, WarpRing& ring, int warp, int slice,
                                            uint64_t policy) {
-  const int slot = warp + G::kWarps * ring.fill;
+  const int slot = warp * G::kLookahead + ring.fill;
   const uint32_t bit = 1u << ring.fill;
   ring.bad = slice < 0 ? ring.bad | bit : ring.bad & ~bit;
   ring.fill = ring.fill + 1 == G::kLookahead ? 0 : ring.fill + 1;
@@ -1078,7 +1087,8 @@ __device__ __forceinline__ void fill_slot4(const PartialParams& p, CtaShared<G>&
   __syncwarp();
 }
 
-// consume_pages for the 4-bit ring: the warp's next one or two pages.
+// The warp's next page, or its next two: wait, move into registers, refill the slots,
+// then the arithmetic. t0, t1: first token of the pages.
 template <class G, bool kMulti, typename Refill>
 __device__ __forceinline__ void consume_pages4(CtaShared<G>& sh, const uint8_t* stages,
                                                WarpRing& ring, int warp, bool pair, int t0, int t1,
@@ -1088,11 +1098,11 @@ __device__ __forceinline__ void consume_pages4(CtaShared<G>& sh, const uint8_t* 
                                                int g, int c, int lane, int& poisoned,
                                                Refill&& refill) {
   constexpr int NT = G::kTiles;
-  PageRegs4 regs[2];
+  PageRegs4 regs[G::kPairs ? 2 : 1];
   uint32_t bad = 0;
   bool ready = true;
   auto take = [&](PageRegs4& r, int i) {  // wait for the next slot and move it into registers
-    const int slot = warp + G::kWarps * ring.use;
+    const int slot = warp * G::kLookahead + ring.use;
     uint64_t* bar = &sh.full_bar[slot];
     if (!__all_sync(kFull, mbar_try_wait(bar, ring.phase)))
       ready = __all_sync(kFull, mbar_wait_bounded(bar, ring.phase, &sh.abort_flag)) && ready;
@@ -1106,7 +1116,7 @@ __device__ __forceinline__ void consume_pages4(CtaShared<G>& sh, const uint8_t* 
     }
   };
   take(regs[0], 0);
-  if (pair) take(regs[1], 1);
+  if (G::kPairs && pair) take(regs[G::kPairs ? 1 : 0], 1);
   if (!ready) {
     poisoned = 1;
     if (lane == 0) {
@@ -1117,18 +1127,21 @@ __device__ __forceinline__ void consume_pages4(CtaShared<G>& sh, const uint8_t* 
     return;
   }
   __syncwarp();  // every lane's reads of the slots are done
-  refill(pair ? 2 : 1);
+  refill();
+  if (G::kPairs && pair) refill();
   const int nv0 = min(kBlockSize, ctx - t0), nv1 = min(kBlockSize, ctx - t1);
-  if (pair && bad == 0) {
-    const int tk[2] = {t0, t1}, nv[2] = {nv0, nv1};
-    process_pages<XQA_KV_E2M1, 2, NT, kMulti>(st, regs, qf, tk, nv, sl, scale_log2, g, c);
-    return;
+  if constexpr (G::kPairs) {
+    if (pair && bad == 0) {
+      const int tk[2] = {t0, t1}, nv[2] = {nv0, nv1};
+      process_pages<XQA_KV_E2M1, 2, NT, kMulti>(st, regs, qf, tk, nv, sl, scale_log2, g, c);
+      return;
+    }
   }
   if (bad) poisoned = 1;
 #pragma unroll 1
-  for (int i = 0; i < (pair ? 2 : 1); ++i) {
+  for (int i = 0; i < (G::kPairs && pair ? 2 : 1); ++i) {
     if (bad >> i & 1) continue;
-    const PageRegs4 one[1] = {i == 0 ? regs[0] : regs[1]};
+    const PageRegs4 one[1] = {i == 0 || !G::kPairs ? regs[0] : regs[G::kPairs ? 1 : 0]};
     const int tk[1] = {i == 0 ? t0 : t1}, nv[1] = {i == 0 ? nv0 : nv1};
     process_pages<XQA_KV_E2M1, 1, NT, kMulti>(st, one, qf, tk, nv, sl, scale_log2, g, c);
   }
@@ -1230,7 +1243,7 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
   constexpr int NT = G::kTiles, kWarps = G::kWarps, kStages = G::kStages;
   constexpr int kCols = G::kCols;
   constexpr int kBufs = G::kMergeBufs;
-  constexpr bool kPrefetchQ = NT == 1;  // registers: two-tile kernels load Q per segment
+  constexpr bool kPrefetchQ = NT == 1 && !G::kFour;  // registers: two-tile kernels load Q per segment
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   const int ncols = p.group * p.q_len;
@@ -1244,7 +1257,7 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
   PageBatch cur = load_batch<kWarps>(p, segs, s_first, s_hi + 1, cbeg, npages, warp, 0, lane);
   PageBatch nxt = load_batch<kWarps>(p, segs, s_first, s_hi + 1, cbeg, npages, warp, 32, lane);
   stamp_after(11, cur.y ^ nxt.y);
-  if (p.hints != nullptr && lane < 2) {  // this warp's first pair, for the next call's prefetch
+  if (p.hints != nullptr && lane < 2 && (kWarps <= kHintPages / 2 || warp < kHintPages / 2)) {  // this warp's first pair, for the next call's prefetch
     const int row = p.kv_layout == XQA_LAYOUT_HND
                         ? cur.y
                         : (cur.y / kBlockSize * p.num_kv_heads + cur.seg % p.num_kv_heads) * kBlockSize;
@@ -1252,18 +1265,28 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
   }
   int cur_base = 0;
   WarpRing ring{0, 0, 0, 0};  // 4 bits only
-  auto issue_next = [&]() {
-    if (issued >= owned) return;
+  auto next_slice = [&]() {   // 4 bits: the warp's next page to load
+    if (issued >= owned) return -2;
     const int k = issued++;
     if (k >= cur_base + 32) {
       cur = nxt;
       cur_base += 32;
       nxt = load_batch<kWarps>(p, segs, s_first, s_hi + 1, cbeg, npages, warp, cur_base + 32, lane);
     }
+    return __shfl_sync(kFull, cur.bad ? -1 : cur.y / kBlockSize, k - cur_base);
+  };
+  auto issue_next = [&]() {
     if constexpr (G::kFour) {
-      const int slice = __shfl_sync(kFull, cur.bad ? -1 : cur.y / kBlockSize, k - cur_base);
-      fill_slot4<G>(p, sh, sm.stages, ring, warp, slice, policy);
+      const int slice = next_slice();
+      if (slice != -2) fill_slot4<G>(p, sh, sm.stages, ring, warp, slice, policy);
       return;
+    }
+    if (issued >= owned) return;
+    const int k = issued++;
+    if (k >= cur_base + 32) {
+      cur = nxt;
+      cur_base += 32;
+      nxt = load_batch<kWarps>(p, segs, s_first, s_hi + 1, cbeg, npages, warp, cur_base + 32, lane);
     }
     const int y = __shfl_sync(kFull, cur.y, k - cur_base);
     const int bad = __shfl_sync(kFull, cur.bad, k - cur_base);
@@ -1304,22 +1327,25 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
     reset_state<NT>(st);
     int poisoned = 0;
 
-    // this warp's pages of the segment (q, and q + kWarps when pairing)
-    for (int q = q0 + ((warp - q0 % kWarps) + kWarps) % kWarps; q < qe; q += 2 * kWarps) {
-      const bool pair = q + kWarps < qe;
-      const int j0 = cbeg + q - sb;  // page index within the sequence
-      if constexpr (G::kFour)
-        consume_pages4<G, kMulti>(sh, sm.stages, ring, warp, pair, j0 * kBlockSize,
-                                  (j0 + kWarps) * kBlockSize, ctx, st, qf, sl, scale_log2, g, c,
-                                  lane, poisoned, [&](int n) {
-                                    issue_next();
-                                    if (n == 2) issue_next();
-                                  });
-      else
-      consume_pages<G, kMulti>(p, sh, sm.stages, q % kStages, (q / kStages) & 1,
-                                      (q + kWarps) % kStages, ((q + kWarps) / kStages) & 1, pair,
-                                      j0 * kBlockSize, (j0 + kWarps) * kBlockSize, ctx, st, qf,
-                                      sl, scale_log2, g, c, lane, poisoned, issue_next);
+    const int qw = q0 + ((warp - q0 % kWarps) + kWarps) % kWarps;  // this warp's first page
+    if constexpr (G::kFour) {
+      constexpr int kNp = G::kPairs ? 2 : 1;
+      for (int q = qw; q < qe; q += kNp * kWarps) {
+        const int t0 = (cbeg + q - sb) * kBlockSize;
+        consume_pages4<G, kMulti>(sh, sm.stages, ring, warp, q + kWarps < qe, t0,
+                                  t0 + kWarps * kBlockSize, ctx, st, qf, sl, scale_log2, g, c,
+                                  lane, poisoned, issue_next);
+      }
+    } else {
+      // this warp's pages of the segment (q, and q + kWarps when pairing)
+      for (int q = qw; q < qe; q += 2 * kWarps) {
+        const bool pair = q + kWarps < qe;
+        const int j0 = cbeg + q - sb;  // page index within the sequence
+        consume_pages<G, kMulti>(p, sh, sm.stages, q % kStages, (q / kStages) & 1,
+                                 (q + kWarps) % kStages, ((q + kWarps) / kStages) & 1, pair,
+                                 j0 * kBlockSize, (j0 + kWarps) * kBlockSize, ctx, st, qf, sl,
+                                 scale_log2, g, c, lane, poisoned, issue_next);
+      }
     }
 
     // ---- hand this segment's per-warp state to a merge buffer; a CTA-wide
@@ -1662,7 +1688,9 @@ __device__ __forceinline__ void finish_range(const PartialParams& p,
     const int first = issued > G::kLookahead ? issued - G::kLookahead : 0;
     for (int k = first; k < issued; ++k) {
       const int q = warp + kWarps * k;
-      const bool ok = mbar_wait_bounded(&sh.full_bar[q % kStages], (q / kStages) & 1, no_abort);
+      const int slot = G::kFour ? warp * G::kLookahead + k % G::kLookahead : q % kStages;
+      const uint32_t phase = (G::kFour ? k / G::kLookahead : q / kStages) & 1;
+      const bool ok = mbar_wait_bounded(&sh.full_bar[slot], phase, no_abort);
       if (!__all_sync(kFull, ok)) {
         if ((threadIdx.x & 31) == 0) atomicExch(&sh.cta_status, XQA_ERR_DRAIN_TIMEOUT);
         break;
@@ -1729,7 +1757,7 @@ __global__ void __launch_bounds__(PartialGeom<kFmt, NT>::kThreads, 1)
                       const PartialParams p) {
   static_assert(NT == 1, "warp mode holds one column tile");
   using G = PartialGeom<kFmt, NT>;
-  constexpr bool kPrefetchQ = true;
+  constexpr bool kPrefetchQ = !G::kFour;
   constexpr int kWarps = G::kWarps, kThreads = G::kThreads, kStages = G::kStages;
   constexpr int kAhead = G::kLookahead;
   extern __shared__ uint8_t smem_raw[];
@@ -1779,14 +1807,28 @@ __global__ void __launch_bounds__(PartialGeom<kFmt, NT>::kThreads, 1)
     // ---- warp mode: this warp's pieces are the range's segments j = warp,
     // warp + 8, ... (j counted from s_first; empty ones skipped). A piece's
     // block ids are fetched one per lane; the next piece's when the current
-    // one starts issuing.
+    // one starts issuing. 4 bits: two neighbouring warps share a piece, half its
+    // pages each (with a warp for a piece 9 of the 16 warps had none at 256 x 512).
+    constexpr int kShare = G::kFour ? 2 : 1;
+    constexpr int kBoxFloats = 1056;  // O, (m, l) of four lanes, bad-page flag
+    static_assert(kShare == 1 || kWarps / 2 * kBoxFloats <= G::kMergeBufFloats, "boxes");
+    constexpr int kTeams = kWarps / kShare;
+    const int team = warp / kShare, half = warp % kShare;
     auto piece = [&](int j, int& pb, int& len) {
       const int sg = s_first + j;
       pb = max(segs[sg], cbeg);
       len = min(segs[sg + 1], cend) - pb;
     };
-    auto next_piece = [&](int j) {  // the first non-empty piece among j, j + 8, ...
-      for (; j < nsr; j += kWarps) {
+    auto part = [&](int j, int& pb, int& len) {  // this warp's pages of a piece
+      piece(j, pb, len);
+      if (kShare == 2) {
+        const int first = (len + 1) / 2;
+        pb += half ? first : 0;
+        len = half ? len - first : first;
+      }
+    };
+    auto next_piece = [&](int j) {  // the first non-empty piece among j, j + kTeams, ...
+      for (; j < nsr; j += kTeams) {
         int pb, len;
         piece(j, pb, len);
         if (len > 0) break;
@@ -1797,7 +1839,7 @@ __global__ void __launch_bounds__(PartialGeom<kFmt, NT>::kThreads, 1)
       PageBatch r{0, 0, 0};
       if (j < nsr) {
         int pb, len;
-        piece(j, pb, len);
+        part(j, pb, len);
         const int sg = s_first + j;
         r.seg = sg;
         if (lane < len) {
@@ -1811,22 +1853,36 @@ __global__ void __launch_bounds__(PartialGeom<kFmt, NT>::kThreads, 1)
       }
       return r;
     };
-    int ij = next_piece(warp), ioff = 0;  // the piece being issued, its next page
-    int ij_next = next_piece(ij + kWarps);
+    int ij = next_piece(team), ioff = 0;  // the piece being issued, its next page
+    int ij_next = next_piece(ij + kTeams);
     PageBatch wcur = fetch(ij), wnxt = fetch(ij_next);
     WarpRing ring{0, 0, 0, 0};  // 4 bits only
-    auto issue_next_w = [&]() {
+    auto next_slice_w = [&]() {  // 4 bits: the warp's next page to load
       while (ij < nsr) {
         int pb, len;
-        piece(ij, pb, len);
+        part(ij, pb, len);
         if (ioff < len) {
-          if constexpr (G::kFour) {
-            const int slice = __shfl_sync(kFull, wcur.bad ? -1 : wcur.y / kBlockSize, ioff);
-            ++ioff;
-            ++issued;
-            fill_slot4<G>(p, sh, sm.stages, ring, warp, slice, policy);
-            return;
-          }
+          ++issued;
+          return __shfl_sync(kFull, wcur.bad ? -1 : wcur.y / kBlockSize, ioff++);
+        }
+        ij = ij_next;
+        ioff = 0;
+        wcur = wnxt;
+        ij_next = next_piece(ij + kTeams);
+        wnxt = fetch(ij_next);
+      }
+      return -2;
+    };
+    auto issue_next_w = [&]() {
+      if constexpr (G::kFour) {
+        const int slice = next_slice_w();
+        if (slice != -2) fill_slot4<G>(p, sh, sm.stages, ring, warp, slice, policy);
+        return;
+      }
+      while (ij < nsr) {
+        int pb, len;
+        part(ij, pb, len);
+        if (ioff < len) {
           const int y = __shfl_sync(kFull, wcur.y, ioff);
           const int bad = __shfl_sync(kFull, wcur.bad, ioff);
           ++ioff;
@@ -1840,7 +1896,7 @@ __global__ void __launch_bounds__(PartialGeom<kFmt, NT>::kThreads, 1)
         ij = ij_next;
         ioff = 0;
         wcur = wnxt;
-        ij_next = next_piece(ij + kWarps);
+        ij_next = next_piece(ij + kTeams);
         wnxt = fetch(ij_next);
       }
     };
@@ -1849,10 +1905,10 @@ __global__ void __launch_bounds__(PartialGeom<kFmt, NT>::kThreads, 1)
     if (warp == kWarps - 1 && lane == 0) piece_owners(sh, rv);
 
     int k = 0;  // this warp's running page index (ring slot and phase)
-    for (int j = next_piece(warp); j < nsr; j = next_piece(j + kWarps)) {
+    for (int j = next_piece(team); j < nsr; j = next_piece(j + kTeams)) {
       const int s = s_first + j;
       int pb, len;
-      piece(j, pb, len);
+      part(j, pb, len);
       const int sb = segs[s], se = segs[s + 1];
       const bool whole = (sb >= cbeg) && (se <= cend);
       const int ctx = rv.ctxs[s / p.num_kv_heads];
@@ -1863,7 +1919,7 @@ __global__ void __launch_bounds__(PartialGeom<kFmt, NT>::kThreads, 1)
         load_q<NT>(p, s, g, c, qf);
       }
       if (kPrefetchQ) {  // Q of this warp's next piece
-        const int jn = next_piece(j + kWarps);
+        const int jn = next_piece(j + kTeams);
         if (jn < nsr) {
           q_next_seg = s_first + jn;
           load_q<NT>(p, q_next_seg, g, c, qf_next);
@@ -1872,21 +1928,59 @@ __global__ void __launch_bounds__(PartialGeom<kFmt, NT>::kThreads, 1)
       const SegLimits<NT> sl = seg_limits<NT>(p, ctx, ncols, c);
       reset_state<NT>(st);
       int poisoned = 0;
-      for (int o = 0; o < len; o += 2) {
-        const bool pair = o + 1 < len;
-        const int t0 = (pb + o - sb) * kBlockSize;
-        if constexpr (G::kFour)
-          consume_pages4<G, kMulti>(sh, sm.stages, ring, warp, pair, t0, t0 + kBlockSize, ctx, st,
-                                    qf, sl, scale_log2, g, c, lane, poisoned, [&](int n) {
-                                      issue_next_w();
-                                      if (n == 2) issue_next_w();
-                                    });
-        else
-        consume_pages<G, kMulti>(p, sh, sm.stages, (warp + kWarps * k) % kStages,
-                                        (k / kAhead) & 1, (warp + kWarps * (k + 1)) % kStages,
-                                        ((k + 1) / kAhead) & 1, pair, t0, t0 + kBlockSize, ctx,
-                                        st, qf, sl, scale_log2, g, c, lane, poisoned, issue_next_w);
-        k += pair ? 2 : 1;
+      if constexpr (G::kFour) {
+        constexpr int kNp = G::kPairs ? 2 : 1;
+        for (int o = 0; o < len; o += kNp) {
+          const int t0 = (pb + o - sb) * kBlockSize;
+          consume_pages4<G, kMulti>(sh, sm.stages, ring, warp, o + 1 < len, t0, t0 + kBlockSize,
+                                    ctx, st, qf, sl, scale_log2, g, c, lane, poisoned,
+                                    issue_next_w);
+        }
+      } else {
+        for (int o = 0; o < len; o += 2) {
+          const bool pair = o + 1 < len;
+          const int t0 = (pb + o - sb) * kBlockSize;
+          consume_pages<G, kMulti>(p, sh, sm.stages, (warp + kWarps * k) % kStages,
+                                   (k / kAhead) & 1, (warp + kWarps * (k + 1)) % kStages,
+                                   ((k + 1) / kAhead) & 1, pair, t0, t0 + kBlockSize, ctx, st, qf,
+                                   sl, scale_log2, g, c, lane, poisoned, issue_next_w);
+          k += pair ? 2 : 1;
+        }
+      }
+      if constexpr (kShare == 2) {
+        // the second warp's state joins the first's, lane by lane, through shared
+        // memory (the merge buffers are free in this mode)
+        float* box = sm.merge_bufs + team * kBoxFloats;
+        if (half) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) box[(4 * i + e) * 32 + lane] = st.o[0][i][e];
+          if (g == 0)
+            *reinterpret_cast<float4*>(box + 1024 + 4 * c) =
+                make_float4(st.m[0][0], st.m[0][1], st.l[0][0], st.l[0][1]);
+          if (lane == 0) box[1040] = poisoned ? 1.f : 0.f;
+        }
+        team_bar(team);
+        if (!half) {
+          const float4 ml = *reinterpret_cast<const float4*>(box + 1024 + 4 * c);
+          const float om[2] = {ml.x, ml.y}, ol[2] = {ml.z, ml.w};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float nm = fmaxf(st.m[0][e], om[e]);
+            const float a = ex2(st.m[0][e] - nm), b = ex2(om[e] - nm);
+            st.m[0][e] = nm;
+            st.l[0][e] = st.l[0][e] * a + ol[e] * b;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              st.o[0][i][e] = st.o[0][i][e] * a + box[(4 * i + e) * 32 + lane] * b;
+              st.o[0][i][e + 2] = st.o[0][i][e + 2] * a + box[(4 * i + e + 2) * 32 + lane] * b;
+            }
+          }
+          if (box[1040] != 0.f) poisoned = 1;
+        }
+        team_bar(team);  // read before the next piece's state is written
+        if (half) continue;
       }
       // ---- the piece's (m, l, O) straight from this warp's registers: lane
       // (g, c) holds dims 16g + 2i (+1) of columns 2c, 2c + 1 ----
