@@ -1050,16 +1050,6 @@ struct WarpRing {
   uint32_t bad;    // bit per own slot
 };
 
-// One lane of the warp; tells the compiler that a single thread runs, so the copies'
-// operands stay in uniform registers.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
 // Fills the warp's next slot with slice `slice` (-1: a bad block id; the slot is
 // flagged and its barrier completes without data). Warp-uniform arguments.
 template <class G>

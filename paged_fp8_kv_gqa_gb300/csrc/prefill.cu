@@ -162,26 +162,6 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Two 32-bit values in one register pair, and their packed arithmetic.
-__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ void split2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // Shared-memory matrix descriptors, 128-byte swizzle (layout 2), version 1.
 // K-major (Q, K): rows of 128 bytes, 8-row groups 1024 bytes apart.
 // MN-major (V, whose dims are contiguous): 64 dims x 8 tokens per group, groups
@@ -392,24 +372,14 @@ __device__ __forceinline__ uint64_t uniform(uint64_t v) {
          __shfl_sync(kAll, (uint32_t)v, 0);
 }
 
-// One lane of the (converged) warp. Products and copies are issued by it: the
-// compiler then knows that a single thread runs and keeps descriptors and addresses
-// in uniform registers; under `lane == 0` each product costs more to issue than to
-// execute (1 x 16384: 1775 us against 1420).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
 // ---- warp 12: the products ----
 // The row tiles in turn: O += P V of tile j, then S of the next tile (j - 1, or the
 // next unit's first), which takes the place of P. The order is fixed, so the row
 // tiles settle half a period apart and one's softmax runs under the other's
-// products; it runs on across units, so a new unit starts without a gap. The code is
-// kept short: it runs once a tile between the softmax warps' long loops and is
+// products; it runs on across units, so a new unit starts without a gap. Products are
+// issued by an elected lane, whose operands stay in uniform registers: under `lane ==
+// 0` each cost more to issue than to execute (1 x 16384: 1775 us against 1420). The
+// code is kept short: it runs once a tile between the softmax warps' long loops and is
 // fetched anew each time (products cut to the keys that a diagonal tile's rows see
 // saved less than their code cost: 1 x 16384 1500 us against 1403, ragged prompts
 // 205 against 190).

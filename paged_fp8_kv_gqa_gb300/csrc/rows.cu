@@ -31,35 +31,53 @@ namespace {
 constexpr int kRowThreads = 128;
 constexpr int kLanesPerRow = 8;  // threads of one (row, kv head): 16 dims each
 
-// Quotients by one divisor t > 0: q0 = x r with r = RN(1/t), then one
-// correction q0 + (x - q0 t) r (Markstein, "Computation of elementary functions
-// on the IBM RISC System/6000 processor", 1990): exact whenever x / t is
-// representable, so ties are seen as ties. Quotients past 2^20 saturate in
-// every format and are left as they are (infinities and NaN among them).
+// Quotients by one divisor t >= 0, as in IEEE division: q0 = x r with r = RN(1/t),
+// then one correction q0 - (q0 t - x) r (Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990): exact whenever x / t is
+// representable, so ties are seen as ties; in this form a zero keeps its sign. A
+// divisor that is a power of two needs no correction. t = 0 gives zeros.
 struct Divisor {
   float t, r;
-  bool slow;  // 1 / t or the correction could leave the normal range
+  bool exact;  // x r is x / t
+  bool slow;   // 1 / t or the correction could leave the normal range
 };
 
 __device__ __forceinline__ Divisor make_divisor(float t) {
   Divisor d;
   d.t = t;
-  d.r = __frcp_rn(t);
-  d.slow = !(t >= 0x1p-60f && t <= 0x1p60f);
+  d.r = t > 0.f ? __frcp_rn(t) : 0.f;
+  d.exact = (__float_as_uint(t) & 0x7fffffu) == 0;
+  d.slow = t > 0.f && !(t >= 0x1p-60f && t <= 0x1p60f);
   return d;
 }
 
-__device__ __forceinline__ float divide(float x, const Divisor& d) {
-  if (d.slow) return __fdiv_rn(x, d.t);
-  const float q0 = x * d.r;
-  const float q = __fmaf_rn(__fmaf_rn(-q0, d.t, x), d.r, q0);
-  return fabsf(q0) < 0x1p20f ? copysignf(q, x) : q0;  // the correction turns -0 into +0
-}
-
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
+// The quotients of a thread's 16 values; amax: their largest magnitude. Quotients
+// past 2^20 (infinities and NaN among them: they saturate in every format) go by
+// plain division too.
+__device__ __forceinline__ void divide(const uint64_t (&x)[8], float amax, const Divisor& d,
+                                       float (&q)[16]) {
+  if (!d.slow && amax * d.r < 0x1p20f) {
+    const uint64_t r2 = f32x2(d.r, d.r);
+    if (d.exact) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) split2(mul2(x[i], r2), q[2 * i], q[2 * i + 1]);
+    } else {
+      const uint64_t t2 = f32x2(d.t, d.t), m2 = f32x2(-d.r, -d.r);
+      constexpr uint64_t kSigns = 0x8000000080000000ull;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t q0 = mul2(x[i], r2);
+        split2(fma2(fma2(q0, t2, x[i] ^ kSigns), m2, q0), q[2 * i], q[2 * i + 1]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      split2(x[i], q[2 * i], q[2 * i + 1]);
+      q[2 * i] = d.t > 0.f ? __fdiv_rn(q[2 * i], d.t) : copysignf(0.f, q[2 * i]);
+      q[2 * i + 1] = d.t > 0.f ? __fdiv_rn(q[2 * i + 1], d.t) : copysignf(0.f, q[2 * i + 1]);
+    }
+  }
 }
 
 // Two fp32 -> two codes, the first in the low bits.
@@ -87,20 +105,25 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float* x) {
   return d;
 }
 
+// A thread's 16 values in 32 bits, in pairs; returns the largest magnitude (NaN if
+// there is one): 15-bit patterns order like the magnitudes they stand for.
 template <int kType>
-__device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float (&x)[16]) {
+__device__ __forceinline__ float unpack16(const uint4& a, const uint4& b, uint64_t (&x)[8]) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
+    top = __vmaxu2(top, w[i] & 0x7fff7fffu);
     if (kType == XQA_F16) {
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
+      x[i] = f32x2(f.x, f.y);
     } else {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      x[i] = f32x2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
   }
+  const uint32_t m = max(top & 0xffffu, top >> 16);
+  return kType == XQA_F16 ? __half2float(__ushort_as_half((unsigned short)m))
+                          : __uint_as_float(m << 16);
 }
 
 template <int kType>
@@ -159,28 +182,22 @@ __device__ __forceinline__ RowPlace find_row(const RowsParams& p, int row, int h
 template <int kFmt, int kType>
 __device__ __forceinline__ void store_codes(uint8_t* cache, long long at, int part, const uint4& a,
                                             const uint4& b, float scale) {
-  float x[16];
-  unpack16<kType>(a, b, x);
+  uint64_t x[8];
+  const float amax = unpack16<kType>(a, b, x);
+  float q[16];
   if (kFmt != XQA_KV_E2M1) {
-    const Divisor d = make_divisor(scale);
+    divide(x, amax, make_divisor(scale), q);
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      w[i] = cvt_fp8x2<kFmt>(divide(x[4 * i], d), divide(x[4 * i + 1], d)) |
-             cvt_fp8x2<kFmt>(divide(x[4 * i + 2], d), divide(x[4 * i + 3], d)) << 16;
+      w[i] = cvt_fp8x2<kFmt>(q[4 * i], q[4 * i + 1]) |
+             cvt_fp8x2<kFmt>(q[4 * i + 2], q[4 * i + 3]) << 16;
     *reinterpret_cast<uint4*>(cache + at * kHeadDim + 16 * part) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(x[i]));
     const uint32_t s8 = cvt_fp8x2<XQA_KV_E4M3>(__fdiv_rn(__fdiv_rn(amax, scale), 6.f), 0.f) & 0xffu;
     const uint32_t sh = e4m3x2_to_f16x2(s8);
     const float s = __low2float(*reinterpret_cast<const __half2*>(&sh));
-    const Divisor d = make_divisor(s * scale);
-    float q[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i)  // a group whose s is 0 (or NaN) holds zeros
-      q[i] = d.t > 0.f ? divide(x[i], d) : copysignf(0.f, x[i]);
+    divide(x, amax, make_divisor(s * scale), q);  // s of 0: zeros
     uint8_t* slice = cache + (at / kBlockSize) * kSliceBytes4;
     const int token = (int)(at % kBlockSize);
     *reinterpret_cast<uint2*>(slice + token * (kHeadDim / 2) + 8 * part) =
@@ -216,7 +233,11 @@ __device__ __forceinline__ void load_values(const uint8_t* cache, long long at, 
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-    o[i] = pack16<kType>((f.x * s) * scale, (f.y * s) * scale);
+    uint64_t v = f32x2(f.x, f.y);
+    if (kFmt == XQA_KV_E2M1) v = mul2(v, f32x2(s, s));  // exact
+    float lo, hi;
+    split2(mul2(v, f32x2(scale, scale)), lo, hi);
+    o[i] = pack16<kType>(lo, hi);
   }
   out[0] = make_uint4(o[0], o[1], o[2], o[3]);
   out[1] = make_uint4(o[4], o[5], o[6], o[7]);
