@@ -14,11 +14,12 @@
 //
 // Both move bytes and compute little: 256 B on the 16-bit side of a (row, kv
 // head) and 128 B (72 B in 4 bits) on the cache side, for K and V each. Eight
-// threads take one (row, kv head): 16 dims each, so a thread's part of an FP8
-// row is one 16-byte access and of a 4-bit row exactly one scale group, and no
-// value crosses threads. A thread does K and V of its row together: the walk
-// from row to cache slot (a search in cu_seqlens, a length, a table entry) is
-// paid once, with four 16-byte loads in flight.
+// threads take one (row, kv head): thread p the dims [8p, 8p+8) and [64+8p, 64+8p+8),
+// so that every access of the eight is one contiguous run of whole sectors (16 dims
+// side by side would write each sector of a packed row in two halves). A 4-bit scale
+// group is shared by two neighbouring threads. A thread does K and V of its row
+// together: the walk from row to cache slot (a search in cu_seqlens, a length, a table
+// entry) is paid once, with four 16-byte loads in flight.
 #include <cuda_bf16.h>
 
 #include "xqa_device.cuh"
@@ -29,7 +30,7 @@ namespace xqa {
 namespace {
 
 constexpr int kRowThreads = 128;
-constexpr int kLanesPerRow = 8;  // threads of one (row, kv head): 16 dims each
+constexpr int kLanesPerRow = 8;  // threads of one (row, kv head)
 
 // Quotients by one divisor t >= 0, as in IEEE division: q0 = x r with r = RN(1/t),
 // then one correction q0 - (q0 t - x) r (Markstein, "Computation of elementary
@@ -51,28 +52,28 @@ __device__ __forceinline__ Divisor make_divisor(float t) {
   return d;
 }
 
-// The quotients of a thread's 16 values; amax: their largest magnitude. Quotients
-// past 2^20 (infinities and NaN among them: they saturate in every format) go by
-// plain division too.
-__device__ __forceinline__ void divide(const uint64_t (&x)[8], float amax, const Divisor& d,
-                                       float (&q)[16]) {
+// The quotients of a thread's 8 neighbouring values; amax: their largest magnitude.
+// Quotients past 2^20 (infinities and NaN among them: they saturate in every format)
+// go by plain division too.
+__device__ __forceinline__ void divide(const uint64_t (&x)[4], float amax, const Divisor& d,
+                                       float (&q)[8]) {
   if (!d.slow && amax * d.r < 0x1p20f) {
     const uint64_t r2 = f32x2(d.r, d.r);
     if (d.exact) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) split2(mul2(x[i], r2), q[2 * i], q[2 * i + 1]);
+      for (int i = 0; i < 4; ++i) split2(mul2(x[i], r2), q[2 * i], q[2 * i + 1]);
     } else {
       const uint64_t t2 = f32x2(d.t, d.t), m2 = f32x2(-d.r, -d.r);
       constexpr uint64_t kSigns = 0x8000000080000000ull;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const uint64_t q0 = mul2(x[i], r2);
         split2(fma2(fma2(q0, t2, x[i] ^ kSigns), m2, q0), q[2 * i], q[2 * i + 1]);
       }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       split2(x[i], q[2 * i], q[2 * i + 1]);
       q[2 * i] = d.t > 0.f ? __fdiv_rn(q[2 * i], d.t) : copysignf(0.f, q[2 * i]);
       q[2 * i + 1] = d.t > 0.f ? __fdiv_rn(q[2 * i + 1], d.t) : copysignf(0.f, q[2 * i + 1]);
@@ -105,14 +106,14 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float* x) {
   return d;
 }
 
-// A thread's 16 values in 32 bits, in pairs; returns the largest magnitude (NaN if
-// there is one): 15-bit patterns order like the magnitudes they stand for.
+// 8 neighbouring values in 32 bits, in pairs; returns the 15-bit pattern of the
+// largest magnitude (the patterns order like the magnitudes, infinities and NaN last).
 template <int kType>
-__device__ __forceinline__ float unpack16(const uint4& a, const uint4& b, uint64_t (&x)[8]) {
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ uint32_t unpack8(const uint4& a, uint64_t (&x)[4]) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     top = __vmaxu2(top, w[i] & 0x7fff7fffu);
     if (kType == XQA_F16) {
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
@@ -121,9 +122,13 @@ __device__ __forceinline__ float unpack16(const uint4& a, const uint4& b, uint64
       x[i] = f32x2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
   }
-  const uint32_t m = max(top & 0xffffu, top >> 16);
-  return kType == XQA_F16 ? __half2float(__ushort_as_half((unsigned short)m))
-                          : __uint_as_float(m << 16);
+  return max(top & 0xffffu, top >> 16);
+}
+
+template <int kType>
+__device__ __forceinline__ float magnitude(uint32_t pattern) {
+  return kType == XQA_F16 ? __half2float(__ushort_as_half((unsigned short)pattern))
+                          : __uint_as_float(pattern << 16);
 }
 
 template <int kType>
@@ -179,68 +184,90 @@ __device__ __forceinline__ RowPlace find_row(const RowsParams& p, int row, int h
   return r;
 }
 
+// One thread's dims [8 part, 8 part + 8) (a) and 64 on (b) of one row. The threads of
+// a row come here together.
 template <int kFmt, int kType>
 __device__ __forceinline__ void store_codes(uint8_t* cache, long long at, int part, const uint4& a,
                                             const uint4& b, float scale) {
-  uint64_t x[8];
-  const float amax = unpack16<kType>(a, b, x);
-  float q[16];
-  if (kFmt != XQA_KV_E2M1) {
-    divide(x, amax, make_divisor(scale), q);
-    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = cvt_fp8x2<kFmt>(q[4 * i], q[4 * i + 1]) |
-             cvt_fp8x2<kFmt>(q[4 * i + 2], q[4 * i + 3]) << 16;
-    *reinterpret_cast<uint4*>(cache + at * kHeadDim + 16 * part) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-    const uint32_t s8 = cvt_fp8x2<XQA_KV_E4M3>(__fdiv_rn(__fdiv_rn(amax, scale), 6.f), 0.f) & 0xffu;
-    const uint32_t sh = e4m3x2_to_f16x2(s8);
-    const float s = __low2float(*reinterpret_cast<const __half2*>(&sh));
-    divide(x, amax, make_divisor(s * scale), q);  // s of 0: zeros
-    uint8_t* slice = cache + (at / kBlockSize) * kSliceBytes4;
-    const int token = (int)(at % kBlockSize);
-    *reinterpret_cast<uint2*>(slice + token * (kHeadDim / 2) + 8 * part) =
-        make_uint2(cvt_e2m1x8(q), cvt_e2m1x8(q + 8));
-    slice[kCodeBytes4 + token * (kHeadDim / kGroup4) + part] = (uint8_t)s8;
+  for (int h = 0; h < 2; ++h) {
+    uint64_t x[4];
+    uint32_t top = unpack8<kType>(h ? b : a, x);
+    float q[8];
+    if (kFmt != XQA_KV_E2M1) {
+      divide(x, magnitude<kType>(top), make_divisor(scale), q);
+      uint32_t w[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        w[i] = cvt_fp8x2<kFmt>(q[4 * i], q[4 * i + 1]) |
+               cvt_fp8x2<kFmt>(q[4 * i + 2], q[4 * i + 3]) << 16;
+      *reinterpret_cast<uint2*>(cache + at * kHeadDim + 64 * h + 8 * part) = make_uint2(w[0], w[1]);
+    } else {
+      const unsigned eight = 0xffu << (threadIdx.x & 24);
+      top = max(top, __shfl_xor_sync(eight, top, 1));  // the group's other half
+      const float amax = magnitude<kType>(top);
+      const uint32_t s8 = cvt_fp8x2<XQA_KV_E4M3>(__fdiv_rn(__fdiv_rn(amax, scale), 6.f), 0.f) & 0xffu;
+      const uint32_t sh = e4m3x2_to_f16x2(s8);
+      const float s = __low2float(*reinterpret_cast<const __half2*>(&sh));
+      divide(x, amax, make_divisor(s * scale), q);  // s of 0: zeros
+      uint8_t* slice = cache + (at / kBlockSize) * kSliceBytes4;
+      const int token = (int)(at % kBlockSize);
+      *reinterpret_cast<uint32_t*>(slice + token * (kHeadDim / 2) + 32 * h + 4 * part) = cvt_e2m1x8(q);
+      // the four scales of this half row in one store
+      uint32_t sw = s8 << 8 * (part >> 1);
+      sw |= __shfl_xor_sync(eight, sw, 2);
+      sw |= __shfl_xor_sync(eight, sw, 4);
+      if (part == 0)
+        *reinterpret_cast<uint32_t*>(slice + kCodeBytes4 + token * (kHeadDim / kGroup4) + 4 * h) = sw;
+    }
   }
 }
 
 template <int kFmt, int kType>
 __device__ __forceinline__ void load_values(const uint8_t* cache, long long at, int part,
                                             float scale, uint4 (&out)[2]) {
-  uint32_t h[8];  // the codes' values in pairs, fp16 (exact)
-  float s = 1.f;
+  uint2 c[2];
+  uint32_t s8[2] = {0, 0};
   if (kFmt != XQA_KV_E2M1) {
-    const uint4 c = __ldg(reinterpret_cast<const uint4*>(cache + at * kHeadDim + 16 * part));
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[2 * i] = KvConv<kFmt == XQA_KV_E2M1 ? XQA_KV_E4M3 : kFmt>::k_lo(w[i]);
-      h[2 * i + 1] = KvConv<kFmt == XQA_KV_E2M1 ? XQA_KV_E4M3 : kFmt>::k_hi(w[i]);
-    }
+    for (int h = 0; h < 2; ++h)
+      c[h] = __ldg(reinterpret_cast<const uint2*>(cache + at * kHeadDim + 64 * h + 8 * part));
   } else {
     const uint8_t* slice = cache + (at / kBlockSize) * kSliceBytes4;
     const int token = (int)(at % kBlockSize);
-    const uint2 c = __ldg(reinterpret_cast<const uint2*>(slice + token * (kHeadDim / 2) + 8 * part));
-    const uint32_t sh =
-        e4m3x2_to_f16x2(__ldg(slice + kCodeBytes4 + token * (kHeadDim / kGroup4) + part));
-    s = __low2float(*reinterpret_cast<const __half2*>(&sh));
-    e2m1x8_to_f16x2(c.x, h);
-    e2m1x8_to_f16x2(c.y, h + 4);
-  }
-  uint32_t o[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-    uint64_t v = f32x2(f.x, f.y);
-    if (kFmt == XQA_KV_E2M1) v = mul2(v, f32x2(s, s));  // exact
-    float lo, hi;
-    split2(mul2(v, f32x2(scale, scale)), lo, hi);
-    o[i] = pack16<kType>(lo, hi);
+    for (int h = 0; h < 2; ++h) {
+      c[h].x = __ldg(reinterpret_cast<const uint32_t*>(slice + token * (kHeadDim / 2) + 32 * h + 4 * part));
+      s8[h] = __ldg(slice + kCodeBytes4 + token * (kHeadDim / kGroup4) + 4 * h + (part >> 1));
+    }
   }
-  out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[4];  // the codes' values in pairs, fp16 (exact)
+    float s = 1.f;
+    if (kFmt != XQA_KV_E2M1) {
+      using Conv = KvConv<kFmt == XQA_KV_E2M1 ? XQA_KV_E4M3 : kFmt>;
+      v[0] = Conv::k_lo(c[h].x);
+      v[1] = Conv::k_hi(c[h].x);
+      v[2] = Conv::k_lo(c[h].y);
+      v[3] = Conv::k_hi(c[h].y);
+    } else {
+      const uint32_t sh = e4m3x2_to_f16x2(s8[h]);
+      s = __low2float(*reinterpret_cast<const __half2*>(&sh));
+      e2m1x8_to_f16x2(c[h].x, v);
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
+      uint64_t y = f32x2(f.x, f.y);
+      if (kFmt == XQA_KV_E2M1) y = mul2(y, f32x2(s, s));  // exact
+      float lo, hi;
+      split2(mul2(y, f32x2(scale, scale)), lo, hi);
+      o[i] = pack16<kType>(lo, hi);
+    }
+    out[h] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
 }
 
 template <int kFmt, int kType, bool kAppend>
@@ -252,15 +279,15 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsParams p) {
   if (u >= (long long)p.num_rows * p.num_kv_heads) return;
   const int row = (int)((uint32_t)u / (uint32_t)p.num_kv_heads);
   const int head = (int)u - row * p.num_kv_heads;
-  const long long ko = row * p.k_row_stride + head * p.k_head_stride + 16 * part;
-  const long long vo = row * p.v_row_stride + head * p.v_head_stride + 16 * part;
+  const long long ko = row * p.k_row_stride + head * p.k_head_stride + 8 * part;
+  const long long vo = row * p.v_row_stride + head * p.v_head_stride + 8 * part;
   uint4* k = reinterpret_cast<uint4*>(p.k + ko);
   uint4* v = reinterpret_cast<uint4*>(p.v + vo);
   const float k_scale = p.k_scale_ptr ? __ldg(p.k_scale_ptr) : p.k_scale;
   const float v_scale = p.v_scale_ptr ? __ldg(p.v_scale_ptr) : p.v_scale;
   if (kAppend) {
     // in flight while the slot is looked up; rows of no sequence are readable too
-    const uint4 k0 = __ldg(k), k1 = __ldg(k + 1), v0 = __ldg(v), v1 = __ldg(v + 1);
+    const uint4 k0 = __ldg(k), k1 = __ldg(k + 8), v0 = __ldg(v), v1 = __ldg(v + 8);
     const RowPlace r = find_row(p, row, head);
     if (r.state != 1) return;
     store_codes<kFmt, kType>(p.k_cache, r.at, part, k0, k1, k_scale);
@@ -277,9 +304,9 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsParams p) {
       a[0] = a[1] = b[0] = b[1] = make_uint4(nan, nan, nan, nan);
     }
     k[0] = a[0];
-    k[1] = a[1];
+    k[8] = a[1];
     v[0] = b[0];
-    v[1] = b[1];
+    v[8] = b[1];
   }
 }
 
