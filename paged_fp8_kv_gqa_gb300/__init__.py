@@ -333,10 +333,11 @@ def _device_stream(stream):
 
 def _on(t: torch.Tensor, dtype, dev: int, name: str) -> int:
     """Pointer of a contiguous tensor of ``dtype`` on device ``dev``."""
-    ptr = _cuda(t, dtype, name)
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-    return ptr
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _cuda(t, dtype, name)  # raises with the reason, if it is not the device
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
 def _heads(t: torch.Tensor, name: str, dtype=None):
