@@ -29,6 +29,11 @@
 // epilogue, 12 tensor core, 13 units and TMA loads, 14-15 the masked V tiles
 // (below). TMEM: S0, S1 (P over them), O0, O1: 4 x 128 columns.
 //
+// Few units and many keys (a prompt of some tokens that goes on after thousands):
+// the unit's keys are cut into pieces, one for each CTA, which leave (O, m, l) in 32
+// bits in the workspace; the piece that is written last joins them. No CTA waits for
+// another.
+//
 // Hidden values do not leak: a weight of exactly 0 times an infinity or NaN
 // would be NaN, so in V tiles that some row of the unit sees in part, rows past
 // the sequence are zeroed in shared memory, and values that are not finite are
@@ -53,6 +58,7 @@ constexpr int kPrefillThreads = 512;
 constexpr float kNoRowMax = -1e30f;              // as in the decode kernel
 constexpr float kLazyMax = 8.0f;                 // log2 units
 constexpr unsigned kAll = 0xffffffffu;
+constexpr int kMaxPieces = kPrefillMaxPieces;
 constexpr uint32_t kWaitClocks = 2000000000u;    // about 1 s
 constexpr int kUnitReaders = 15;  // 8 softmax, 4 epilogue, 1 tensor-core, 2 V warps
 
@@ -68,6 +74,7 @@ struct Unit {
   int vis0;      // keys the unit's first token sees (causal: one more per token)
   int n[2];      // KV tiles row tile 0 / 1 sees (0: no tokens, or nothing to see)
   int hidden;    // first key hidden from some token (tiles past it are masked)
+  int slot;      // place of this piece's (O, m, l); -1: the unit is one piece
 };
 
 struct Shared {
@@ -83,6 +90,7 @@ struct Shared {
   Unit unit[kUnitSlots];
   int not_finite[kUnitSlots];    // the unit's masked V tiles held infinities or NaN
   int abort_flag, status;
+  int joins;                     // this CTA's piece was the last: 1, or -1 if one failed
   uint32_t tmem;
 };
 
@@ -249,6 +257,7 @@ struct Ctx {
 };
 
 // ---- warp 13: the units of this CTA and their TMA loads ----
+template <bool kCut>
 __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
                                           const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                                           int& kv_issued, int (&q_issued)[2]) {
@@ -264,7 +273,7 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
   int q0 = 0, len_q = 0, mine = 0, incl = 0;
   int next = blockIdx.x;
   for (int i = 0;; ++i) {
-    const int u = next;
+    const int u = kCut ? next / p.pieces : next;
     while (base < p.batch && u >= first + total) {  // the chunk that holds unit u
       first += total;
       base += 32;
@@ -288,7 +297,10 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
     }
     const int slot = i % kUnitSlots;
     if (i >= kUnitSlots && !c.wait(&sh.unit_empty[slot], (i / kUnitSlots - 1) & 1)) return;
-    if (base >= p.batch) {  // none left
+    // in pieces: one a CTA (there are CTAs for all, unless offsets overlap)
+    const bool over = kCut && i > 0;
+    if (base >= p.batch || over) {  // none left
+      if (base < p.batch) record_status(&sh.status, XQA_ERR_BAD_OFFSETS);
       if (lane == 0) {
         sh.unit[slot].end = 1;
         mbar_arrive(&sh.unit_full[slot]);
@@ -315,6 +327,18 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
     w.len_k = w.bad ? 0 : k1 - k0;
     // keys seen by the first token; clamped where it is used
     w.vis0 = p.causal ? w.len_k - s_len + tok0 + 1 : w.len_k;
+    w.slot = -1;
+    if (kCut) {  // the piece's keys, as if they were all
+      w.slot = next;
+      const int piece = next - u * p.pieces;
+      const int last = p.causal ? min(w.len_k, w.vis0 + w.tokens - 1) : w.len_k;
+      const int tiles = last > 0 ? (last - 1) / kTile + 1 : 0;
+      const int from = tiles * piece / p.pieces * kTile;
+      const int to = min(w.len_k, tiles * (piece + 1) / p.pieces * kTile);
+      w.k_row += from;
+      w.len_k = to - from;
+      w.vis0 = p.causal ? w.vis0 - from : w.len_k;
+    }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int toks = min(p.tile_tokens, w.tokens - s * p.tile_tokens);
@@ -670,7 +694,7 @@ __device__ __forceinline__ void softmax_role(const Ctx& c, int s) {
 }
 
 // ---- warps 8-11: normalise and write ----
-template <int kType>
+template <int kType, bool kCut>
 __device__ __forceinline__ void epilogue_role(const Ctx& c) {
   const PrefillParams& p = c.p;
   Shared& sh = c.sh;
@@ -687,6 +711,10 @@ __device__ __forceinline__ void epilogue_role(const Ctx& c) {
       const long long at = (long long)u.q_row + rp.token;
       const int h = u.head * p.group + rp.head;
       uint16_t* out = p.out + at * p.out_row_stride + h * p.out_head_stride;
+      if (kCut && u.n[s] == 0) {
+        p.piece_ml[(u.slot * 2 + s) * kTile + row] = make_float2(kNoRowMax, 0.f);
+        continue;
+      }
       if (u.n[s] == 0) {  // no tokens, or tokens that see nothing
         if (rp.valid) {
           const uint32_t f = !u.bad ? 0u : kType == XQA_F16 ? 0x7fff7fffu : 0x7fc07fc0u;
@@ -733,7 +761,15 @@ __device__ __forceinline__ void epilogue_role(const Ctx& c) {
             }
           }
         }
-        if (rp.valid) {
+        if (kCut) {  // as it is: [32 chunks of 4 dims][128 rows]
+          float4* po = p.piece_o + ((size_t)(u.slot * 2 + s) * 32 + 8 * q) * kTile + row;
+          if (rp.valid) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              po[k * kTile] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                          __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+          }
+        } else if (rp.valid) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t w[4];
@@ -745,7 +781,8 @@ __device__ __forceinline__ void epilogue_role(const Ctx& c) {
           }
         }
       }
-      if (p.lse && rp.valid)
+      if (kCut) p.piece_ml[(u.slot * 2 + s) * kTile + row] = ml;
+      else if (p.lse && rp.valid)
         p.lse[at * p.num_q_heads + h] =
             ml.y == 0.f ? -INFINITY : (ml.x + __log2f(ml.y)) * 0.6931471805599453f;
     }
@@ -753,7 +790,88 @@ __device__ __forceinline__ void epilogue_role(const Ctx& c) {
   }
 }
 
+// ---- warps 0-7, after the roles: the unit's pieces joined by the last of them. A CTA
+// has at most one piece (its unit 0).
 template <int kType>
+__device__ __forceinline__ void join_pieces(const Ctx& c) {
+  const PrefillParams& p = c.p;
+  Shared& sh = c.sh;
+  // every (O, m, l) of this CTA's piece is written (the epilogue warps arrive)
+  asm volatile("bar.sync 1, 384;" ::: "memory");
+  const Unit u = sh.unit[0];
+  if (u.end) return;  // no piece
+  const int unit = u.slot / p.pieces;
+  if (threadIdx.x == 0) {
+    const bool failed = *(volatile int*)&sh.abort_flag != 0;
+    __threadfence();
+    const int old = atom_add_acq_rel_gpu(p.tickets + unit, failed ? 1 + kTicketPoison : 1);
+    const bool last = (old & kTicketCountMask) == p.pieces - 1;
+    sh.joins = !last ? 0 : failed || (old & kTicketPoisonMask) ? -1 : 1;
+    if (last) p.tickets[unit] = 0;  // for the next call
+  }
+  asm volatile("bar.sync 2, 256;" ::: "memory");
+  const int joins = sh.joins;
+  if (joins == 0) return;
+  const size_t first = (size_t)unit * p.pieces * 2;  // its piece k, row tile s: first + 2 k + s
+  const bool bad = joins < 0 || u.bad;
+  const int rows = u.tokens * p.group;  // <= 256
+  // threads of a row: 256 / (rows rounded up to 32, 64, 128 or 256), its dims shared
+  // out among them
+  const int span = rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+  const int r = threadIdx.x & (span - 1), chunks = span / 8;  // chunks of 4 dims for each
+  const int c0 = threadIdx.x / span * chunks;
+  if (r >= rows) return;
+  const int t = r / p.group, g = r - t * p.group, h = u.head * p.group + g;
+  const int s = t >= p.tile_tokens ? 1 : 0, row = r - s * p.tile_tokens * p.group;
+  const long long at = (long long)u.q_row + t;
+  float w[kMaxPieces], top = -INFINITY, sum = 0.f;
+  float2 ml[kMaxPieces];
+#pragma unroll
+  for (int k = 0; k < kMaxPieces; ++k)
+    ml[k] = k < p.pieces ? __ldcg(p.piece_ml + (first + 2 * k + s) * kTile + row)
+                         : make_float2(kNoRowMax, 0.f);
+#pragma unroll
+  for (int k = 0; k < kMaxPieces; ++k)
+    if (ml[k].y != 0.f) top = fmaxf(top, ml[k].x);
+#pragma unroll
+  for (int k = 0; k < kMaxPieces; ++k) {
+    w[k] = ml[k].y != 0.f ? ex2(ml[k].x - top) : 0.f;
+    if (w[k] != 0.f) sum += w[k] * ml[k].y;
+  }
+  const float nan = __int_as_float(0x7fc00000);
+  const float rl = bad ? nan : sum == 0.f ? 0.f : 1.f / sum;
+  uint16_t* out = p.out + at * p.out_row_stride + h * p.out_head_stride + 4 * c0;
+  const float4* po = p.piece_o + ((first + s) * 32 + c0) * kTile + row;
+#pragma unroll 1
+  for (int q = 0; q < chunks; q += 4) {  // 16 dims, every piece's in flight at once
+    float4 v[kMaxPieces][4];
+#pragma unroll
+    for (int k = 0; k < kMaxPieces; ++k)
+      if (w[k] != 0.f)  // (a piece without keys has written none)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k][e] = __ldcg(po + ((size_t)k * 64 + q + e) * kTile);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kMaxPieces; ++k)
+        if (w[k] != 0.f) {
+          a.x += w[k] * v[k][e].x;
+          a.y += w[k] * v[k][e].y;
+          a.z += w[k] * v[k][e].z;
+          a.w += w[k] * v[k][e].w;
+        }
+      reinterpret_cast<uint2*>(out)[q + e] =
+          make_uint2(pack2<kType>(a.x * rl, a.y * rl), pack2<kType>(a.z * rl, a.w * rl));
+    }
+  }
+  if (p.lse && c0 == 0)
+    p.lse[at * p.num_q_heads + h] =
+        bad ? nan : sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.6931471805599453f;
+}
+
+// kCut: units are cut into pieces (p.pieces > 1).
+template <int kType, bool kCut>
 __global__ void __launch_bounds__(kPrefillThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const PrefillParams p) {
@@ -785,6 +903,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       mbar_init(&sh.stat_free[s], 4);
     }
     mbar_init(&sh.drain, 1);
+    sh.unit[0].end = 1;  // until there is one
     sh.abort_flag = 0;
     sh.status = aligned ? XQA_OK : XQA_ERR_LAUNCH;
     fence_mbar_init();
@@ -806,14 +925,20 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     if (warp >= 12) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
       if (warp == 12) tensor_role<kType>(c);
-      else if (warp == 13) load_role(c, &tm_q, &tm_k, &tm_v, kv_issued, q_issued);
+      else if (warp == 13) load_role<kCut>(c, &tm_q, &tm_k, &tm_v, kv_issued, q_issued);
       else clean_role<kType>(c);
     } else if (warp >= 8) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-      epilogue_role<kType>(c);
+      epilogue_role<kType, kCut>(c);
+      if (kCut) {
+        __syncwarp();
+        asm volatile("bar.arrive 1, 384;" ::: "memory");
+      }
     } else {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
       softmax_role<kType>(c, warp >> 2);
+      __syncwarp();
+      if (kCut) join_pieces<kType>(c);
     }
   }
   __syncwarp();
@@ -868,14 +993,21 @@ cudaError_t launch_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return dtype == XQA_F16 ? cudaLaunchKernelEx(&cfg, prefill_kernel<XQA_F16>, tm_q, tm_k, tm_v, p)
-                          : cudaLaunchKernelEx(&cfg, prefill_kernel<XQA_BF16>, tm_q, tm_k, tm_v, p);
+  const bool cut = p.pieces > 1;
+  if (dtype == XQA_F16)
+    return cut ? cudaLaunchKernelEx(&cfg, prefill_kernel<XQA_F16, true>, tm_q, tm_k, tm_v, p)
+               : cudaLaunchKernelEx(&cfg, prefill_kernel<XQA_F16, false>, tm_q, tm_k, tm_v, p);
+  return cut ? cudaLaunchKernelEx(&cfg, prefill_kernel<XQA_BF16, true>, tm_q, tm_k, tm_v, p)
+             : cudaLaunchKernelEx(&cfg, prefill_kernel<XQA_BF16, false>, tm_q, tm_k, tm_v, p);
 }
 
 cudaError_t set_prefill_attributes() {
   const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  const cudaError_t e = cudaFuncSetAttribute(prefill_kernel<XQA_F16>, a, kPrefillSmem);
-  return e != cudaSuccess ? e : cudaFuncSetAttribute(prefill_kernel<XQA_BF16>, a, kPrefillSmem);
+  cudaError_t e;
+  if ((e = cudaFuncSetAttribute(prefill_kernel<XQA_F16, false>, a, kPrefillSmem)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(prefill_kernel<XQA_F16, true>, a, kPrefillSmem)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(prefill_kernel<XQA_BF16, false>, a, kPrefillSmem)) != cudaSuccess) return e;
+  return cudaFuncSetAttribute(prefill_kernel<XQA_BF16, true>, a, kPrefillSmem);
 }
 
 }  // namespace xqa

@@ -302,8 +302,10 @@ bool row_strides(const xqa_rows_t& s, int64_t row, int64_t head, bool written, l
 }
 
 // The regions of a prefill workspace: those of a decode workspace in front of
-// its first-page hints (header, tickets, status words).
+// its first-page hints (header, tickets, status words), then, where units are cut
+// into pieces, each piece's O (256 rows x 128) and (m, l) in 32 bits.
 constexpr size_t kPrefillWorkspaceBytes = 12544;
+constexpr size_t kPieceFloats = 256 * (kHeadDim + 2);
 
 struct Side {  // a strided [rows, heads, 128] tensor
   long long rs, hs;
@@ -325,9 +327,25 @@ bool prefill_side(int rows, int heads, int64_t row, int64_t head, bool written, 
 
 struct PrefillResolved {
   Side q, k, v, out;
-  int group, ctas;
+  int group, ctas, pieces;
   float sm_scale;
+  size_t bytes;
 };
+
+// Pieces of a unit's keys. Units that leave half of the CTAs idle are cut, into pieces
+// of four 128-key tiles at least. A tile takes 1.1 to 1.6 us, writing and joining the
+// pieces about 7 us: 1 x 64 queries over 8256 keys (32/4 heads) 102 us whole, 40 in 8
+// pieces; 2 x 30 over 3030 (32/8) 34 and 21.5; 1 x 16 over 1016 (8/1) 15.0 and 15.4, and
+// stays whole. The lengths are on the device: the average stands for them.
+int prefill_pieces(const xqa_prefill_shape_t& s, long long units, int ctas) {
+  if (units < 1 || units > ctas / 2) return 1;
+  const long long seqs = s.batch < s.total_q ? s.batch : s.total_q;
+  const long long tiles = s.total_k / seqs / 128;
+  long long n = tiles / 4;
+  if (n > ctas / units) n = ctas / units;
+  if (n > xqa::kPrefillMaxPieces) n = xqa::kPrefillMaxPieces;
+  return n < 2 || tiles * (n - 1) < 7 * n ? 1 : (int)n;
+}
 
 xqa_status_t resolve_prefill(const xqa_prefill_shape_t* s, PrefillResolved* r) {
   if (!s) return XQA_ERR_NULL;
@@ -364,7 +382,10 @@ xqa_status_t resolve_prefill(const xqa_prefill_shape_t* s, PrefillResolved* r) {
     r->ctas = sms;
   }
   if (r->ctas > xqa::kMaxCtas) r->ctas = xqa::kMaxCtas;
-  if (r->ctas > units) r->ctas = units > 0 ? (int)units : 1;
+  r->pieces = prefill_pieces(*s, units, r->ctas);
+  if (r->ctas > units * r->pieces) r->ctas = units > 0 ? (int)(units * r->pieces) : 1;
+  r->bytes = kPrefillWorkspaceBytes;
+  if (r->pieces > 1) r->bytes += (size_t)r->ctas * kPieceFloats * sizeof(float);
   return XQA_OK;
 }
 
@@ -535,7 +556,7 @@ xqa_status_t xqa_prefill_workspace_size(const xqa_prefill_shape_t* shape, size_t
   static_assert(kPrefillWorkspaceBytes >=
                     4 * xqa::kHeaderWords + 8 * (size_t)xqa::kMaxCtas + 4 * (size_t)xqa::kMaxCtas,
                 "header, tickets and status words");
-  *bytes = kPrefillWorkspaceBytes;
+  *bytes = r.bytes;
   return XQA_OK;
 }
 
@@ -551,7 +572,7 @@ xqa_status_t xqa_prefill(const void* q, const void* k, const void* v, const int3
   if (!q || !out || !cu_seqlens_q || !cu_seqlens_k || !workspace || (keys && (!k || !v)))
     return XQA_ERR_NULL;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return XQA_ERR_ALIGN;
-  if (workspace_bytes < kPrefillWorkspaceBytes) return XQA_ERR_WORKSPACE;
+  if (workspace_bytes < r.bytes) return XQA_ERR_WORKSPACE;
   if (!aligned16(q) || !aligned16(out) || (keys && (!aligned16(k) || !aligned16(v))))
     return XQA_ERR_ALIGN;
   if ((st = ensure_device_setup()) != XQA_OK) return st;
@@ -584,6 +605,11 @@ xqa_status_t xqa_prefill(const void* q, const void* k, const void* v, const int3
   p.total_q = shape->total_q;
   p.total_k = shape->total_k;
   p.causal = shape->causal;
+  p.pieces = r.pieces;
+  p.tickets = reinterpret_cast<int32_t*>(base + lay.ticket_off);
+  p.piece_o = reinterpret_cast<float4*>(base + kPrefillWorkspaceBytes);
+  p.piece_ml = reinterpret_cast<float2*>(base + kPrefillWorkspaceBytes +
+                                         (size_t)r.ctas * 256 * kHeadDim * sizeof(float));
   p.tile_tokens = tokens;
   p.scale_log2 = (float)((double)r.sm_scale * 1.4426950408889634);
   p.v_row_stride = r.v.rs;

@@ -65,6 +65,8 @@ struct RowsParams {
   const float* v_scale_ptr;
 };
 
+constexpr int kPrefillMaxPieces = 8;
+
 struct PrefillParams {
   const int32_t* cu_q;  // [batch + 1]
   const int32_t* cu_k;
@@ -76,6 +78,11 @@ struct PrefillParams {
   int32_t* status;    // [kMaxCtas]
   int batch, num_q_heads, num_kv_heads, group, total_q, total_k, causal;
   int tile_tokens;    // T: tokens of a 128-row tile
+  int pieces;         // a unit's keys are cut into so many (1: not at all); with more
+                      // than 1 there are at least as many CTAs as pieces of all units
+  int32_t* tickets;   // pieces written, by unit: zero between calls
+  float4* piece_o;    // [units * pieces][2][32 chunks of 4 dims][128 rows]
+  float2* piece_ml;   // [units * pieces][2][128]
   float scale_log2;   // sm_scale * log2(e)
   long long v_row_stride, v_head_stride, out_row_stride, out_head_stride;
 };

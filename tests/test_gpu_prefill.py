@@ -147,6 +147,97 @@ def test_units_of_many_sequences(max_ctas):
     c.check(c.run(max_ctas=max_ctas))
 
 
+SPLIT = [([5], [3000]), ([1], [9001]), ([1, 30], [5000, 2]), ([16, 0, 40], [2500, 100, 4000]),
+         ([3, 17], [4100, 900]), ([40], [5000])]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lq,lk", SPLIT)
+def test_few_queries_over_many_keys(lq, lk, causal, dtype):
+    # units cut along the keys, pieces joined by the last CTA of a unit; among them
+    # sequences with fewer tiles than pieces
+    for hq, hkv in ((12, 4), (8, 1), (2, 2)):
+        c = Call(lq, lk, hq=hq, hkv=hkv, seed=sum(lk), dtype=dtype, pad=2)
+        out = c.run(causal)
+        assert c.ws.numel() > 16384  # the pieces' place
+        c.check(out, causal)
+        assert not bool(c.ws[64:64 + 8 * 1024].any())  # the units' counts back at zero
+        assert torch.equal(c.run(causal), out)
+
+
+def test_pieces_with_hidden_and_visible_infinities():
+    for at in (10, 2900, 2996, 2998):
+        c = Call([5, 4], [3000, 1800], hq=8, hkv=2, seed=at)
+        for val in (float("nan"), float("inf")):
+            c.v[at, 1, 77] = val
+            c.check(c.run())
+        c = Call([5, 4], [3000, 1800], hq=8, hkv=2, seed=at)
+        assert c.run() is not None and c.ws.numel() > 16384
+        ref = c.run()
+        c.k[at] = float("nan")
+        out = c.run()
+        assert c.ws.numel() > 16384
+        first = max(0, at - 2995)
+        assert bool(torch.isnan(out[first:5]).all())
+        keep = [*range(first), *range(5, 9)]
+        assert torch.equal(out[keep], ref[keep])
+    c = Call([6], [2000], hq=4, hkv=2, seed=5)     # logits that move the maximum between pieces
+    c.q.abs_()
+    c.k.copy_(c.k[c.k[:, 0].float().sum(-1).argsort()] * 2)
+    c.check(c.run())
+
+
+def test_pieces_in_a_graph_with_other_lengths_and_bad_offsets():
+    c = Call([9, 7], [3000, 2000], hq=8, hkv=2, seed=31)
+    want = c.run()
+    assert c.ws.numel() > 16384
+    out = torch.zeros_like(want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(3):
+            xqa.xqa_prefill(c.q, c.k, c.v, c.cq, c.ck, out=out, workspace=c.ws, shape=c.shape)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    good_q, good_k = c.cq.clone(), c.ck.clone()
+    c.cq.copy_(offsets([1, 15]))
+    c.ck.copy_(offsets([4990, 10]))
+    g.replay()
+    torch.cuda.synchronize()
+    w, _, big = plain(c.q, c.k, c.v, [1, 15], [4990, 10], True)
+    compare(out, w, big, c.t)
+    # bad key offsets: NaN rows; overlapping query offsets: reported, nothing out of place
+    c.cq.copy_(good_q)
+    c.ck.copy_(torch.tensor([0, 3000, 5001], dtype=torch.int32))
+    g.replay()
+    torch.cuda.synchronize()
+    assert xqa.xqa_read_status(c.ws) == xqa.XQA_ERR_BAD_OFFSETS
+    assert torch.equal(out[:9], want[:9]) and bool(torch.isnan(out[9:]).all())
+    for bad in ([0, 16, 0], [0, 16, 16], [3, 2, 1]):
+        c.cq.copy_(torch.tensor(bad, dtype=torch.int32))
+        g.replay()
+    c.cq.copy_(good_q)
+    c.ck.copy_(good_k)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and xqa.xqa_read_status(c.ws) == xqa.XQA_OK
+
+
+def test_two_calls_in_pieces_at_once():
+    a, b = Call([5], [40000], hq=8, hkv=2, seed=41), Call([8, 8], [9000, 12000], hq=8, hkv=2, seed=42)
+    wa, wb = a.run(), b.run()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        oa, ob = torch.empty_like(wa), torch.empty_like(wb)
+        for s in (s1, s2):
+            s.wait_stream(torch.cuda.current_stream())
+        xqa.xqa_prefill(a.q, a.k, a.v, a.cq, a.ck, out=oa, workspace=a.ws, shape=a.shape, stream=s1)
+        xqa.xqa_prefill(b.q, b.k, b.v, b.cq, b.ck, out=ob, workspace=b.ws, shape=b.shape, stream=s2)
+        torch.cuda.synchronize()
+        assert torch.equal(oa, wa) and torch.equal(ob, wb)
+
+
 def test_one_long_prompt():
     c = Call([5000], hq=4, hkv=1, dtype="bf16", seed=6)
     c.check(c.run())
