@@ -97,7 +97,8 @@ typedef struct xqa_shape {
   float sm_scale;             /* softmax scale; <= 0 selects 1/sqrt(D) */
   int32_t max_ctas;           /* upper bound on split-KV CTAs; 0 = SM count;
                                  values above 1024 are taken as 1024 */
-  int32_t min_pages_per_cta;  /* planner lower bound on pages per CTA; 0 = 16 */
+  int32_t min_pages_per_cta;  /* planner lower bound on pages per CTA; 0 = 16
+                                 (XQA_KV_E2M1: at most max_blocks_per_seq) */
   int32_t merge_mode;         /* how segments split over several CTAs are merged:
                                  0 = inside the partial kernel (default), by the
                                  last CTA to finish one, or for a segment of
