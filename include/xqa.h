@@ -107,8 +107,9 @@ typedef struct xqa_shape {
                                  the rows (when max_ctas <= SM count, so that
                                  every CTA is resident at once);
                                  1 = by the separate combine kernel (xqa_combine) */
-  int32_t kv_dtype;           /* XQA_KV_E5M2 (0, default) or XQA_KV_E4M3 */
-  int32_t kv_layout;          /* XQA_LAYOUT_HND (0, default) or XQA_LAYOUT_NHD */
+  int32_t kv_dtype;           /* XQA_KV_E5M2 (0, default), XQA_KV_E4M3 or XQA_KV_E2M1 */
+  int32_t kv_layout;          /* XQA_LAYOUT_HND (0, default) or, with the 8-bit
+                                 formats, XQA_LAYOUT_NHD */
   int32_t q_len;              /* T: new tokens per sequence; 0 or 1 = single-token
                                  decode. With T > 1, q and out are [B, T, Hq, D],
                                  context_lens count the T new tokens (their K/V
@@ -132,7 +133,7 @@ xqa_status_t xqa_kernels_per_call(const xqa_shape_t* shape, int32_t* kernels);
  *   k_cache       device, FP8 codes (shape->kv_dtype) in the shape->kv_layout
  *                 layout: [NB, Hkv, BS, D] (HND: one (page, kv head) slice is
  *                 BS*D = 2048 contiguous bytes) or [NB, BS, Hkv, D] (NHD),
- *                 16-byte aligned
+ *                 16-byte aligned; XQA_KV_E2M1: 1152-byte slices (see above)
  *   v_cache       device, same layout as k_cache
  *   block_tables  device, int32 [B, MBS]; entry j of row b is the physical page
  *                 of tokens [16j, 16j+16) of sequence b; entries at or past

@@ -14,6 +14,7 @@ The names mirror the C ABI declared in ``include/xqa.h``:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -257,10 +258,12 @@ def xqa_decode(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale
     if shape is None:
         shape = make_shape(q, k_cache, block_tables, sm_scale, max_ctas, min_pages_per_cta,
                            kv_dtype=kv_dtype, kv_layout=kv_layout)
-    if out is None:
-        out = torch.empty_like(q)
-    if workspace is None:
-        workspace = alloc_workspace(shape, q.device)
+    if out is None or workspace is None:
+        with _allocating(stream):
+            if out is None:
+                out = torch.empty_like(q)
+            if workspace is None:
+                workspace = alloc_workspace(shape, q.device)
     a = _decode_args(q, k_cache, v_cache, block_tables, context_lens, out, workspace, shape)
     lib = load_library()
     if isinstance(k_scale, torch.Tensor) or isinstance(v_scale, torch.Tensor):
@@ -317,6 +320,12 @@ def xqa_dequant_e5m2(codes: torch.Tensor, scale: float = 1.0, with_f32: bool = T
 def xqa_dequant_e4m3(codes: torch.Tensor, scale: float = 1.0, with_f32: bool = True, stream=None):
     """Exact E4M3 dequantisation: (fp16 bit patterns as int16 tensor, fp32 scaled or None)."""
     return _dequant("xqa_dequant_e4m3", codes, scale, with_f32, stream)
+
+
+def _allocating(stream):
+    """Context in which the binding allocates what a call on ``stream`` writes: the
+    memory (and the zero fill of a workspace) belongs to that stream."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _device_stream(stream):
@@ -447,8 +456,9 @@ def xqa_gather(k_cache, v_cache, block_tables, context_lens, cu_seqlens, num_row
         raise ValueError("pass both k and v, or neither")
     if k is None:
         hkv = _cache_dims(k_cache, kv_dtype, kv_layout)[1]
-        k = torch.empty((int(num_rows), hkv, 128), dtype=dtype, device=k_cache.device)
-        v = torch.empty_like(k)
+        with _allocating(stream):
+            k = torch.empty((int(num_rows), hkv, 128), dtype=dtype, device=k_cache.device)
+            v = torch.empty_like(k)
     elif k.shape[0] != num_rows:
         raise ValueError("k and v must have num_rows rows")
     _move_rows("xqa_gather", k, v, cu_seqlens, k_cache, v_cache, block_tables, context_lens,
@@ -513,7 +523,8 @@ def xqa_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=None, lse=None, wo
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        with _allocating(stream):
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if shape.out_row_stride not in (0, q.shape[1] * q.shape[2]) or (
                 shape.out_head_stride not in (0, q.shape[2])):
             raise ValueError("the shape descriptor names strides of out: pass out")
@@ -521,7 +532,8 @@ def xqa_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=None, lse=None, wo
             shape.out_row_stride or shape.num_q_heads * 128, shape.out_head_stride or 128):
         raise ValueError("out does not match q or the shape descriptor")
     if workspace is None:
-        workspace = alloc_prefill_workspace(shape, q.device)
+        with _allocating(stream):
+            workspace = alloc_prefill_workspace(shape, q.device)
     if cu_seqlens_q.numel() != shape.batch + 1 or cu_seqlens_k.numel() != shape.batch + 1:
         raise ValueError("cu_seqlens_q and cu_seqlens_k must have batch + 1 entries")
     lp = None

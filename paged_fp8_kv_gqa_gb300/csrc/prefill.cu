@@ -55,7 +55,10 @@ constexpr int kTileBytes = 2 * kHalfBytes;       // a Q, K or V tile
 constexpr int kKvStages = 5;
 constexpr int kUnitSlots = 3;
 constexpr int kPrefillThreads = 512;
-constexpr float kNoRowMax = -1e30f;              // as in the decode kernel
+// Running maximum before any visible key: finite, so that 2^(-inf - m) is 0, and
+// below the logits of the types' largest values.
+constexpr float kNoRowMax = -3e38f;
+constexpr float kExactMax = 4194304.f;  // 2^22: half a step of smaller m is at most 1/4
 constexpr float kLazyMax = 8.0f;                 // log2 units
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kMaxPieces = kPrefillMaxPieces;
@@ -390,12 +393,6 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
   }
 }
 
-// A value that is the same in every lane, told to the compiler.
-__device__ __forceinline__ uint64_t uniform(uint64_t v) {
-  return (uint64_t)__shfl_sync(kAll, (uint32_t)(v >> 32), 0) << 32 |
-         __shfl_sync(kAll, (uint32_t)v, 0);
-}
-
 // ---- warp 12: the products ----
 // The row tiles in turn: O += P V of tile j, then S of the next tile (j - 1, or the
 // next unit's first), which takes the place of P. The order is fixed, so the row
@@ -435,7 +432,7 @@ __device__ __forceinline__ void tensor_role(const Ctx& c) {
   int j = 0;                // tile of the V slot
   int sv = 0, sk = 0;       // ring slots of this round's V and K tile
   uint32_t pv = 0, pk = 0;  // their phases
-  // phases, a bit for each row tile (p: two, o: of a barrier never waited for) or stage
+  // phases, a bit for each row tile (P: two) or stage; O is free before its first use
   uint32_t ph_q = 0, ph_p = 0, ph_o = 3, ph_clean = 0;
   for (;;) {
     // V tile j of the current unit (none in the first round), then a K tile: j - 1, or
@@ -612,7 +609,7 @@ __device__ __forceinline__ void softmax_role(const Ctx& c, int s) {
     if (n == 0) continue;
     // keys that every token of this row tile sees
     const int clear = p.causal ? min(u.len_k, u.vis0 + s * p.tile_tokens) : u.len_k;
-    float m = kNoRowMax, l = 0.f;
+    float m = kNoRowMax, m_raw = 0.f, l = 0.f;  // m_raw: m before the scale
     for (int j = n - 1; j >= 0; --j) {
       if (!c.wait(&sh.s_full[s], ns & 1)) return;
       tc_fence_after();
@@ -640,14 +637,23 @@ __device__ __forceinline__ void softmax_role(const Ctx& c, int s) {
           mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(r[k + e])), __uint_as_float(r[k + 4 + e]));
 #pragma unroll
       for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(r[kTile - 4 + e]));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+      const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), top = raw * sc;
       const bool moves = top > m + kLazyMax;
-      if (j < n - 1) {
-        // O holds something: rows whose maximum moves are rescaled (the product
-        // that last wrote O was issued before the one that made this S)
-        const bool scale_o = moves && m != kNoRowMax;
+      // O holds something: rows whose maximum moves are rescaled (the product that last
+      // wrote O was issued before the one that made this S)
+      const bool scale_o = moves && m != kNoRowMax;
+      const float old = m;
+      if (moves) m = top, m_raw = raw;
+      uint64_t m2 = f32x2(-m, -m);
+      // s * sc - m is rounded once, m before: at the maximum itself up to half a step of
+      // m is left, a factor of the whole row that the division by l takes out again, but
+      // 2^128 and more once m is large. There the maximum is subtracted first. Each row
+      // by its own: its result does not depend on its neighbours, of which those without
+      // a token hold anything.
+      const bool exact = fabsf(m) > kExactMax && m != kNoRowMax && vis > 0;
+      if (__any_sync(kAll, scale_o || exact)) {
         if (__any_sync(kAll, scale_o)) {
-          const float a = scale_o ? ex2(m - top) : 1.f;
+          const float a = scale_o ? ex2(old - top) : 1.f;
           l *= a;
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
@@ -659,9 +665,12 @@ __device__ __forceinline__ void softmax_role(const Ctx& c, int s) {
             tmem_st32(o_addr + 32 * q, o);
           }
         }
+        const float minus = exact ? m_raw : 0.f;
+#pragma unroll
+        for (int k = 0; k < kTile; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) - minus);
+        if (exact) m2 = 0;
       }
-      if (moves) m = top;
-      const uint64_t sc2 = f32x2(sc, sc), m2 = f32x2(-m, -m);
+      const uint64_t sc2 = f32x2(sc, sc);
       uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {

@@ -391,6 +391,59 @@ def test_graph_replay_streams_and_determinism():
     compare(out, n, big, c.t)
 
 
+@pytest.mark.parametrize("dtype,q,k", [("bf16", 1e18, -1e16), ("bf16", 1e18, 1e16),
+                                       ("fp16", 6e4, -6e4), ("fp16", 6e4, 6e4)])
+def test_large_logits_are_a_softmax_like_any_other(dtype, q, k):
+    # equal logits, near 1e36 with bf16 and 4e11 with fp16: means of the values
+    c = Call([40], hq=2, hkv=1, dtype=dtype, seed=21)
+    c.q.fill_(q)
+    c.k.fill_(k)
+    out = c.run()
+    mean = c.v.double().cumsum(0) / torch.arange(1, 41, device="cuda").view(-1, 1, 1)
+    u = torch.finfo(out.dtype).eps / 2
+    assert float((out.double() - mean).abs().max()) <= 1.05 * u * 2 * float(c.v.abs().max()) + 1e-6
+
+
+@pytest.mark.parametrize("hq,hkv", [(6, 2), (7, 1)])
+def test_rows_do_not_depend_on_their_neighbours(hq, hkv):
+    # a token with large logits beside others, whose rows come out as without it
+    c = Call([60, 30], hq=hq, hkv=hkv, dtype="bf16", seed=25)
+    want = c.run()
+    c.q[20] *= 1e25
+    got = c.run()
+    assert torch.equal(got[:20], want[:20]) and torch.equal(got[21:], want[21:])
+    assert bool(torch.isfinite(got[20]).all()) and not torch.equal(got[20], want[20])
+
+
+def test_another_stream_without_a_workspace():
+    c = Call([70, 200], seed=22)
+    want = c.run()
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        side.wait_stream(torch.cuda.current_stream())
+        got = xqa.xqa_prefill(c.q, c.k, c.v, c.cq, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(got, want)
+
+
+def test_one_workspace_for_prompt_attention_and_decode():
+    # alternately, also where units are cut into pieces; the counts and tickets stay zero
+    a, b = Call([300], seed=23), Call([4], [5000], seed=24)
+    wa, wb = a.run(), b.run()
+    k = torch.randint(0, 60, (300, 2, 16, 128), dtype=torch.uint8, device="cuda")
+    bt = torch.randperm(300, device="cuda").to(torch.int32).view(2, 150)
+    lens = torch.tensor([2400, 900], dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 8, 128, device="cuda").half()
+    shape = xqa.make_shape(q, k, bt)
+    ws = torch.zeros(max(xqa.xqa_workspace_size(shape), b.ws.numel()), dtype=torch.uint8, device="cuda")
+    want = xqa.xqa_decode(q, k, k, bt, lens, 1.0, 1.0, workspace=ws, shape=shape).clone()
+    for _ in range(3):
+        for c, w in ((a, wa), (b, wb)):
+            got = xqa.xqa_prefill(c.q, c.k, c.v, c.cq, c.ck, workspace=ws, shape=c.shape)
+            assert torch.equal(got, w)
+            assert torch.equal(xqa.xqa_decode(q, k, k, bt, lens, 1.0, 1.0, workspace=ws, shape=shape), want)
+
+
 def test_two_calls_at_once_with_their_own_workspaces():
     a, b = Call([900], seed=16), Call([64, 700], seed=17)
     wa, wb = a.run(), b.run()
