@@ -325,7 +325,7 @@ def xqa_dequant_e4m3(codes: torch.Tensor, scale: float = 1.0, with_f32: bool = T
 def _allocating(stream):
     """Context in which the binding allocates what a call on ``stream`` writes: the
     memory (and the zero fill of a workspace) belongs to that stream."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext()
 
 
 def _device_stream(stream):

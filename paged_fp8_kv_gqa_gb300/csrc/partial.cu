@@ -1247,7 +1247,8 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
   PageBatch cur = load_batch<kWarps>(p, segs, s_first, s_hi + 1, cbeg, npages, warp, 0, lane);
   PageBatch nxt = load_batch<kWarps>(p, segs, s_first, s_hi + 1, cbeg, npages, warp, 32, lane);
   stamp_after(11, cur.y ^ nxt.y);
-  if (p.hints != nullptr && lane < 2 && (kWarps <= kHintPages / 2 || warp < kHintPages / 2)) {  // this warp's first pair, for the next call's prefetch
+  // this warp's first pair, for the next call's prefetch
+  if (p.hints != nullptr && lane < 2 && (kWarps <= kHintPages / 2 || warp < kHintPages / 2)) {
     const int row = p.kv_layout == XQA_LAYOUT_HND
                         ? cur.y
                         : (cur.y / kBlockSize * p.num_kv_heads + cur.seg % p.num_kv_heads) * kBlockSize;

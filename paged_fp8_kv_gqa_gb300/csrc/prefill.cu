@@ -22,8 +22,13 @@
 // exceeds it by more than 8 (log2), so O is rescaled seldom (P <= 2^8 stays
 // exact enough: its rounding is relative); O and the row sum l stay in 32 bits,
 // l sums the unrounded P. P is rounded to the inputs' type because a tcgen05
-// product has both operands in 16 bits: 2^-9 (bf16) or 2^-12 (fp16) of each
+// product has both operands in 16 bits: at most 2^-8 (bf16) or 2^-11 (fp16) of each
 // weight, the size of the rounding of out itself.
+//
+// Measured (32/4 heads): 1 x 16384 tokens bf16 1.39 ms, 1580 TFLOP/s of visible pairs,
+// 0.83 of a library product's rate; 16 prompts of 190 to 2048 tokens fp16 166 us, 0.61:
+// a tenth of the tiles is hidden, and a unit of 6 tiles starts and ends its two chains
+// of dependent products and softmax anew (about 2 us of its 11).
 //
 // Warps: 0-3 and 4-7 softmax of row tile 0 and 1 (a thread owns a row), 8-11
 // epilogue, 12 tensor core, 13 units and TMA loads, 14-15 the masked V tiles
@@ -164,6 +169,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], " XQA_LIST32 ";" ::XQA_I8(r, 0),
       XQA_I8(r, 8), XQA_I8(r, 16), XQA_I8(r, 24), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+      "%10, %11, %12, %13, %14, %15};" ::XQA_I8(r, 0),
+      XQA_I8(r, 8), "r"(addr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() {
@@ -591,6 +603,11 @@ __device__ __forceinline__ int visible(const PrefillParams& p, const Unit& u, co
 }
 
 // ---- warps 0-7: softmax of row tile s; a thread owns a row ----
+// Small loops over 32 keys that read S from TMEM again, rather than a row of registers
+// and straight code: all roles share the instruction caches, and the roles that run once
+// a tile or a unit fetched their code anew (16 ragged prompts 182 us with rows in
+// registers and keys masked there, 168 so; 1 x 16384 1405 and 1395; a prompt of 37
+// tokens 7.7 and 8.0: its time is these loops' latency).
 template <int kType>
 __device__ __forceinline__ void softmax_role(const Ctx& c, int s) {
   const PrefillParams& p = c.p;
@@ -613,30 +630,32 @@ __device__ __forceinline__ void softmax_role(const Ctx& c, int s) {
     for (int j = n - 1; j >= 0; --j) {
       if (!c.wait(&sh.s_full[s], ns & 1)) return;
       tc_fence_after();
-      uint32_t r[kTile];
+      if ((j + 1) * kTile > clear) {  // keys that a row does not see: -inf
+        const int lim = vis - j * kTile;
+#pragma unroll 1
+        for (int q = max(0, __reduce_min_sync(kAll, lim)) >> 5; q < 4; ++q) {
+          uint32_t r[32];
+          tmem_ld32(s_addr + 32 * q, r);
+          tmem_wait_ld();
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32 * q, r + 32 * q);
-      tmem_wait_ld();
-      if ((j + 1) * kTile > clear) {
-        const int lim = vis - j * kTile, lo = __reduce_min_sync(kAll, lim);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (32 * q + 32 <= lo) continue;  // the warp's rows see these
-#pragma unroll
-          for (int k = 32 * q; k < 32 * q + 32; ++k)
-            if (k >= lim) r[k] = 0xff800000u;  // -inf
+          for (int k = 0; k < 32; ++k)
+            if (32 * q + k >= lim) r[k] = 0xff800000u;
+          tmem_st32(s_addr + 32 * q, r);
         }
+        tmem_wait_st();
       }
-      float mx[4];  // three-operand maxima
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // three-operand maxima
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t r[32];
+        tmem_ld32(s_addr + 32 * q, r);
+        tmem_wait_ld();
 #pragma unroll
-      for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(r[k]);
+        for (int k = 0; k < 32; k += 8)
 #pragma unroll
-      for (int k = 4; k < kTile - 4; k += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(r[k + e])), __uint_as_float(r[k + 4 + e]));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(r[kTile - 4 + e]));
+          for (int e = 0; e < 4; ++e)
+            mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(r[k + e])), __uint_as_float(r[k + 4 + e]));
+      }
       const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), top = raw * sc;
       const bool moves = top > m + kLazyMax;
       // O holds something: rows whose maximum moves are rescaled (the product that last
@@ -651,43 +670,48 @@ __device__ __forceinline__ void softmax_role(const Ctx& c, int s) {
       // by its own: its result does not depend on its neighbours, of which those without
       // a token hold anything.
       const bool exact = fabsf(m) > kExactMax && m != kNoRowMax && vis > 0;
-      if (__any_sync(kAll, scale_o || exact)) {
-        if (__any_sync(kAll, scale_o)) {
-          const float a = scale_o ? ex2(old - top) : 1.f;
-          l *= a;
+      if (__any_sync(kAll, scale_o)) {
+        const float a = scale_o ? ex2(old - top) : 1.f;
+        l *= a;
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t o[32];
-            tmem_ld32(o_addr + 32 * q, o);
-            tmem_wait_ld();
+        for (int q = 0; q < 4; ++q) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + 32 * q, o);
+          tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-            tmem_st32(o_addr + 32 * q, o);
-          }
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+          tmem_st32(o_addr + 32 * q, o);
         }
-        const float minus = exact ? m_raw : 0.f;
-#pragma unroll
-        for (int k = 0; k < kTile; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) - minus);
-        if (exact) m2 = 0;
       }
+      const bool any_exact = __any_sync(kAll, exact);
+      const float minus = exact ? m_raw : 0.f;
+      if (exact) m2 = 0;
       const uint64_t sc2 = f32x2(sc, sc);
       uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {  // P of 32 keys over S of keys that are read already
+        uint32_t r[32], pk[16];
+        tmem_ld32(s_addr + 32 * q, r);
+        tmem_wait_ld();
+        if (any_exact) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[32];
+          for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) - minus);
+        }
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
+        for (int k = 0; k < 16; ++k) {
           float a, b;
-          split2(fma2(f32x2(__uint_as_float(r[64 * h + 2 * k]), __uint_as_float(r[64 * h + 2 * k + 1])), sc2, m2), a, b);
+          split2(fma2(f32x2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), sc2, m2), a, b);
           a = ex2(a);
           b = ex2(b);
           sum[k & 1] = add2(sum[k & 1], f32x2(a, b));
           pk[k] = pack2<kType>(a, b);
         }
-        tmem_st32(s_addr + 32 * h, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        c.arrive(&sh.p_full[s][h]);
+        tmem_st16(s_addr + 16 * q, pk);
+        if (q & 1) {
+          tmem_wait_st();
+          tc_fence_before();
+          c.arrive(&sh.p_full[s][q >> 1]);
+        }
       }
       float la, lb;
       split2(add2(sum[0], sum[1]), la, lb);
@@ -702,7 +726,30 @@ __device__ __forceinline__ void softmax_role(const Ctx& c, int s) {
   }
 }
 
+// One round of a 4 x 4 transpose among four lanes, of the 16-byte units of w: lanes kBit
+// apart trade the units that differ in that bit of their number.
+template <int kBit>
+__device__ __forceinline__ void trade(uint32_t (&w)[16]) {
+  const bool up = threadIdx.x & kBit;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (u & kBit) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t &lo = w[4 * u + e], &hi = w[4 * (u + kBit) + e];
+      const uint32_t got = __shfl_xor_sync(kAll, up ? lo : hi, kBit);
+      if (up) lo = got;
+      else hi = got;
+    }
+  }
+}
+
 // ---- warps 8-11: normalise and write ----
+// A thread has a row of O. Before a store, four lanes trade their 16-byte units, so that
+// the four write 64 contiguous bytes of one row: a store of 32 rows' units kept the next
+// unit's first product waiting for O (prompts on prefixes 161 us, 157 so; 1 x 16384 1409
+// and 1395). More dims at a time free O earlier, but their code costs more than it saves
+// (ragged prompts 182 to 191 us).
 template <int kType, bool kCut>
 __device__ __forceinline__ void epilogue_role(const Ctx& c) {
   const PrefillParams& p = c.p;
@@ -744,6 +791,15 @@ __device__ __forceinline__ void epilogue_role(const Ctx& c) {
       const bool patch = *(volatile int*)&sh.not_finite[i % kUnitSlots] != 0;
       const int vis = visible(p, u, rp);
       const float rl = ml.y == 0.f ? 0.f : 1.f / ml.y;  // a row that sees nothing: 0
+      uint16_t* dst[4];  // this lane's unit of the four lanes' rows
+      if (!kCut) {
+        const unsigned long long mine = rp.valid ? reinterpret_cast<unsigned long long>(out) : 0ull;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const unsigned long long a = __shfl_sync(kAll, mine, (threadIdx.x & 28) + k);
+          dst[k] = a ? reinterpret_cast<uint16_t*>(a) + 8 * (threadIdx.x & 3) : nullptr;
+        }
+      }
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
         uint32_t o[32];
@@ -778,16 +834,22 @@ __device__ __forceinline__ void epilogue_role(const Ctx& c) {
               po[k * kTile] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
                                           __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
           }
-        } else if (rp.valid) {
+        } else {
+          uint32_t w[16];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack2<kType>(__uint_as_float(o[8 * k + 2 * e]) * rl,
-                                  __uint_as_float(o[8 * k + 2 * e + 1]) * rl);
-            reinterpret_cast<uint4*>(out + 32 * q)[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int k = 0; k < 16; ++k) {
+            float a, b;
+            split2(mul2(f32x2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), f32x2(rl, rl)),
+                   a, b);
+            w[k] = pack2<kType>(a, b);
           }
+          trade<1>(w);
+          trade<2>(w);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (dst[k])
+              *reinterpret_cast<uint4*>(dst[k] + 32 * q) =
+                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         }
       }
       if (kCut) p.piece_ml[(u.slot * 2 + s) * kTile + row] = ml;
@@ -937,14 +999,18 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       else if (warp == 13) load_role<kCut>(c, &tm_q, &tm_k, &tm_v, kv_issued, q_issued);
       else clean_role<kType>(c);
     } else if (warp >= 8) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+      if (kCut) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+      else asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
       epilogue_role<kType, kCut>(c);
       if (kCut) {
         __syncwarp();
         asm volatile("bar.arrive 1, 384;" ::: "memory");
       }
     } else {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+      // the join of pieces holds 8 x 16 dims; the sums of the shares, 256 x 192 + 128 x 80
+      // and 256 x 144 + 128 x 128, with 128 x 48, stay within the 65,536 of the launch
+      if (kCut) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+      else asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
       softmax_role<kType>(c, warp >> 2);
       __syncwarp();
       if (kCut) join_pieces<kType>(c);
