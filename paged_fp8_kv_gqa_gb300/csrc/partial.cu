@@ -12,7 +12,7 @@
 // (long-scoreboard stalls at low occupancy, section "Starting bottleneck"); on
 // sm_103a this kernel keeps kStages pages in flight per SM instead.
 //
-// Every one of the 8 warps both loads and computes. Warp w owns the CTA-local
+// Every one of the 8 warps (FP8; 4 bits below) both loads and computes. Warp w owns the CTA-local
 // pages w, w+8, w+16, ... and the ring slots w, w+8, w+16, w+24 they map to
 // (slot = page % kStages). It keeps kLookahead of its pages in flight: once a
 // page is in registers it issues the two TMA loads (K and V slice, 2048 B each,
@@ -54,6 +54,13 @@
 // segment table in shared memory a decode step is this one launch, which may
 // become resident while the previous kernel on the stream still runs and
 // waits for it before reading any input.
+//
+// 4-bit caches (E2M1 codes, an E4M3 scale for 16 dims; 1152-byte slices, copied whole and
+// not swizzled): the same steps on half the bytes, each value multiplied by its scale in
+// fp16, where the product is exact. That arithmetic bounds the loop (issue slots, not
+// memory), so one-tile kernels run 16 warps a page at a time, with the ring's state in
+// registers, and two neighbouring warps share a piece in warp mode. 16 x 17.8k tokens,
+// 32/4 heads: 44.5 us, 3750 GB/s of codes and scales, 0.56 of the copy rate.
 //
 // Contraction-index permutation: the MMA result does not depend on how the
 // contraction index is laid out, as long as both operands use the same layout.
@@ -1701,8 +1708,8 @@ __device__ __forceinline__ void publish_status(const PartialParams& p, Sh& sh) {
 
 }  // namespace
 
-template <int kFmt, int NT, bool kMulti>
-__global__ void __launch_bounds__(PartialGeom<kFmt, NT>::kThreads, 1)
+template <int kFmt, int NT, bool kMulti, int kThreads = PartialGeom<kFmt, NT>::kThreads>
+__global__ void __launch_bounds__(kThreads, 1)
     partial_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const PartialParams p) {
   using G = PartialGeom<kFmt, NT>;
@@ -1742,14 +1749,14 @@ __global__ void __launch_bounds__(PartialGeom<kFmt, NT>::kThreads, 1)
 // per segment; other ranges are worked in CTA mode as above. Launched only for
 // shapes with many segments per CTA (batches of many short sequences): the
 // mode test and the warp-mode code slow the page loop of CTA-mode ranges.
-template <int kFmt, int NT, bool kMulti>
-__global__ void __launch_bounds__(PartialGeom<kFmt, NT>::kThreads, 1)
+template <int kFmt, int NT, bool kMulti, int kThreads = PartialGeom<kFmt, NT>::kThreads>
+__global__ void __launch_bounds__(kThreads, 1)
     partial_kernel_wm(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const PartialParams p) {
   static_assert(NT == 1, "warp mode holds one column tile");
   using G = PartialGeom<kFmt, NT>;
   constexpr bool kPrefetchQ = !G::kFour;
-  constexpr int kWarps = G::kWarps, kThreads = G::kThreads, kStages = G::kStages;
+  constexpr int kWarps = G::kWarps, kStages = G::kStages;
   constexpr int kAhead = G::kLookahead;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) CtaShared<G> sh;
