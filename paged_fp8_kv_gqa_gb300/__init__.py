@@ -401,9 +401,9 @@ def _rows_descriptor(*fields) -> XqaRows:
 
 def _move_rows(fn_name, k, v, cu_seqlens, k_cache, v_cache, block_tables, context_lens, k_scale,
                v_scale, kv_dtype, kv_layout, status, stream):
-    dev, handle = _device_stream(stream)
-    krs, khs = _heads(k, "k")
+    krs, khs = _heads(k, "k")  # CPU tensors are refused before CUDA is asked
     vrs, vhs = _heads(v, "v", k.dtype)
+    dev, handle = _device_stream(stream)
     nb, hkv, bs = _cache_dims(k_cache, kv_dtype, kv_layout)
     n, h, d = k.shape
     b = context_lens.numel()
@@ -510,7 +510,6 @@ def xqa_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=None, lse=None, wo
     (fp32 [total_q, Hq], optional) receives the log-sum-exp. Returns ``out``;
     rows that see nothing are zero, rows behind the last sequence are not
     written."""
-    dev, handle = _device_stream(stream)
     if shape is None:
         shape = make_prefill_shape(q, k, v, cu_seqlens_q, causal, sm_scale, max_ctas, out)
     else:
@@ -520,6 +519,7 @@ def xqa_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=None, lse=None, wo
                 s.total_q, s.num_q_heads, s.head_dim, s.total_k, s.num_kv_heads, s.dtype) != (
                 *q.shape, k.shape[0], k.shape[1], ROW_DTYPES[q.dtype]):
             raise ValueError("q, k, v do not match the shape descriptor")
+    dev, handle = _device_stream(stream)  # CPU tensors are refused before CUDA is asked
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
     if out is None:

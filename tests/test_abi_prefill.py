@@ -3,6 +3,7 @@ call; the addresses are never dereferenced)."""
 import ctypes
 
 import pytest
+import torch
 
 import paged_fp8_kv_gqa_gb300 as xqa
 from paged_fp8_kv_gqa_gb300 import build
@@ -61,3 +62,9 @@ def test_pointer_refusals(lib):
     assert call(lib, shape(), nbytes=xqa.xqa_prefill_workspace_size(shape()) - 1) == xqa.XQA_ERR_WORKSPACE
     assert call(lib, shape(total_q=0), q=0, out=0) == xqa.XQA_OK  # nothing to do
     assert xqa.xqa_status_string(xqa.XQA_ERR_BAD_OFFSETS) != "unknown status"
+
+
+def test_binding_refuses_cpu_tensors_before_the_library():
+    x = torch.zeros(3, 2, 128, dtype=torch.float16)
+    with pytest.raises(ValueError, match="CUDA"):
+        xqa.xqa_prefill(x, x, x, torch.zeros(2, dtype=torch.int32))
