@@ -757,21 +757,22 @@ __device__ __forceinline__ void epilogue_role(const Ctx& c) {
   const int row = threadIdx.x & 127;
   const uint32_t lane_base = c.tmem + ((uint32_t)(row & ~31) << 16);
   const uint32_t exp_mask = kType == XQA_F16 ? 0x7c00u : 0x7f80u;
-  int done[2] = {0, 0};
+  uint32_t ph = 0;  // a bit for each row tile
   for (int i = 0;; ++i) {
     Unit u;
     if (!c.get_unit(i, u)) return;
-#pragma unroll
+#pragma unroll 1
     for (int s = 0; s < 2; ++s) {
       const RowPos rp = row_pos(p, u, s, row);
+      const int n_s = s ? u.n[1] : u.n[0];
       const long long at = (long long)u.q_row + rp.token;
       const int h = u.head * p.group + rp.head;
       uint16_t* out = p.out + at * p.out_row_stride + h * p.out_head_stride;
-      if (kCut && u.n[s] == 0) {
+      if (kCut && n_s == 0) {
         p.piece_ml[(u.slot * 2 + s) * kTile + row] = make_float2(kNoRowMax, 0.f);
         continue;
       }
-      if (u.n[s] == 0) {  // no tokens, or tokens that see nothing
+      if (n_s == 0) {  // no tokens, or tokens that see nothing
         if (rp.valid) {
           const uint32_t f = !u.bad ? 0u : kType == XQA_F16 ? 0x7fff7fffu : 0x7fc07fc0u;
 #pragma unroll 1
@@ -781,11 +782,11 @@ __device__ __forceinline__ void epilogue_role(const Ctx& c) {
         }
         continue;
       }
-      if (!c.wait(&sh.stat_full[s], done[s] & 1)) return;
+      if (!c.wait(&sh.stat_full[s], ph >> s & 1)) return;
       const float2 ml = reinterpret_cast<const float2*>(c.stats)[s * kTile + row];
       c.arrive(&sh.stat_free[s]);
-      if (!c.wait(&sh.o_full[s], done[s] & 1)) return;
-      ++done[s];
+      if (!c.wait(&sh.o_full[s], ph >> s & 1)) return;
+      ph ^= 1u << s;
       tc_fence_after();
       // infinities and NaN of masked V tiles (zeroed there), for rows that see them
       const bool patch = *(volatile int*)&sh.not_finite[i % kUnitSlots] != 0;
