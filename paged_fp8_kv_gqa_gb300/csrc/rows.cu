@@ -270,29 +270,40 @@ __device__ __forceinline__ void load_values(const uint8_t* cache, long long at, 
   }
 }
 
-template <int kFmt, int kType, bool kAppend>
+// kHeads: neighbouring kv heads that a thread takes (append only, see launch_format).
+template <int kFmt, int kType, bool kAppend, int kHeads>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsParams p) {
   griddep_launch_dependents();
   const long long u = ((long long)blockIdx.x * kRowThreads + threadIdx.x) / kLanesPerRow;
   const int part = threadIdx.x % kLanesPerRow;
   griddep_wait();  // every input may come from the kernels before this one
-  if (u >= (long long)p.num_rows * p.num_kv_heads) return;
-  const int row = (int)((uint32_t)u / (uint32_t)p.num_kv_heads);
-  const int head = (int)u - row * p.num_kv_heads;
-  const long long ko = row * p.k_row_stride + head * p.k_head_stride + 8 * part;
-  const long long vo = row * p.v_row_stride + head * p.v_head_stride + 8 * part;
-  uint4* k = reinterpret_cast<uint4*>(p.k + ko);
-  uint4* v = reinterpret_cast<uint4*>(p.v + vo);
+  const int per_row = p.num_kv_heads / kHeads;  // a multiple, see launch_format
+  if (u >= (long long)p.num_rows * per_row) return;
+  const int row = (int)((uint32_t)u / (uint32_t)per_row);
+  const int head = ((int)u - row * per_row) * kHeads;
+  const uint16_t* kp = p.k + row * p.k_row_stride + head * p.k_head_stride + 8 * part;
+  const uint16_t* vp = p.v + row * p.v_row_stride + head * p.v_head_stride + 8 * part;
   const float k_scale = p.k_scale_ptr ? __ldg(p.k_scale_ptr) : p.k_scale;
   const float v_scale = p.v_scale_ptr ? __ldg(p.v_scale_ptr) : p.v_scale;
-  if (kAppend) {
+  if constexpr (kAppend) {
     // in flight while the slot is looked up; rows of no sequence are readable too
-    const uint4 k0 = __ldg(k), k1 = __ldg(k + 8), v0 = __ldg(v), v1 = __ldg(v + 8);
+    uint4 x[kHeads][4];
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+      const uint4* k = reinterpret_cast<const uint4*>(kp + h * p.k_head_stride);
+      const uint4* v = reinterpret_cast<const uint4*>(vp + h * p.v_head_stride);
+      x[h][0] = __ldg(k), x[h][1] = __ldg(k + 8), x[h][2] = __ldg(v), x[h][3] = __ldg(v + 8);
+    }
     const RowPlace r = find_row(p, row, head);
     if (r.state != 1) return;
-    store_codes<kFmt, kType>(p.k_cache, r.at, part, k0, k1, k_scale);
-    store_codes<kFmt, kType>(p.v_cache, r.at, part, v0, v1, v_scale);
+    const int next = p.kv_layout == XQA_LAYOUT_HND ? kBlockSize : 1;  // the next head's row
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+      store_codes<kFmt, kType>(p.k_cache, r.at + h * next, part, x[h][0], x[h][1], k_scale);
+      store_codes<kFmt, kType>(p.v_cache, r.at + h * next, part, x[h][2], x[h][3], v_scale);
+    }
   } else {
+    static_assert(kHeads == 1, "gather");
     const RowPlace r = find_row(p, row, head);
     if (r.state == 0) return;
     uint4 a[2], b[2];
@@ -303,6 +314,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsParams p) {
       const uint32_t nan = kType == XQA_F16 ? 0x7fff7fffu : 0x7fc07fc0u;
       a[0] = a[1] = b[0] = b[1] = make_uint4(nan, nan, nan, nan);
     }
+    uint4* k = reinterpret_cast<uint4*>(const_cast<uint16_t*>(kp));
+    uint4* v = reinterpret_cast<uint4*>(const_cast<uint16_t*>(vp));
     k[0] = a[0];
     k[8] = a[1];
     v[0] = b[0];
@@ -310,21 +323,40 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsParams p) {
   }
 }
 
+template <int kFmt, int kType, bool kAppend, int kHeads>
+cudaError_t launch(cudaLaunchConfig_t cfg, const RowsParams& p) {
+  const long long threads = (long long)p.num_rows * (p.num_kv_heads / kHeads) * kLanesPerRow;
+  cfg.gridDim = dim3((unsigned)((threads + kRowThreads - 1) / kRowThreads));
+  return cudaLaunchKernelEx(&cfg, rows_kernel<kFmt, kType, kAppend, kHeads>, p);
+}
+
+// FP8 rows of many tokens are appended two heads to a thread: twice the loads in flight
+// for one lookup. 4 heads: 48.6k tokens 28.1 us with one head, 26.0 with two (5750 GB/s),
+// 8192 tokens 6.2 and 5.7; fewer leave SMs idle: 4096 tokens 3.7 and 4.5, 256 2.2 and
+// 2.6. An odd head would have a thread of its own (3 heads, 16384 tokens: 10.2 and 10.5).
+// 4-bit rows and gather hold more registers for each head and lose (append and gather of
+// 4-bit rows 50.5 and 53.5 us, gather of 30k FP8 tokens 12.0 and 13.9).
+constexpr long long kPairFrom = 1ll << 15;  // (row, kv head) pairs
+
 template <bool kAppend, int kType>
-cudaError_t launch(int fmt, const cudaLaunchConfig_t& cfg, const RowsParams& p) {
+cudaError_t launch_format(int fmt, const cudaLaunchConfig_t& cfg, const RowsParams& p) {
+  if constexpr (kAppend) {
+    if (fmt != XQA_KV_E2M1 && p.num_kv_heads % 2 == 0 &&
+        (long long)p.num_rows * p.num_kv_heads >= kPairFrom)
+      return fmt == XQA_KV_E5M2 ? launch<XQA_KV_E5M2, kType, true, 2>(cfg, p)
+                                : launch<XQA_KV_E4M3, kType, true, 2>(cfg, p);
+  }
   switch (fmt) {
-    case XQA_KV_E5M2: return cudaLaunchKernelEx(&cfg, rows_kernel<XQA_KV_E5M2, kType, kAppend>, p);
-    case XQA_KV_E4M3: return cudaLaunchKernelEx(&cfg, rows_kernel<XQA_KV_E4M3, kType, kAppend>, p);
-    default: return cudaLaunchKernelEx(&cfg, rows_kernel<XQA_KV_E2M1, kType, kAppend>, p);
+    case XQA_KV_E5M2: return launch<XQA_KV_E5M2, kType, kAppend, 1>(cfg, p);
+    case XQA_KV_E4M3: return launch<XQA_KV_E4M3, kType, kAppend, 1>(cfg, p);
+    default: return launch<XQA_KV_E2M1, kType, kAppend, 1>(cfg, p);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_rows(bool append, const RowsParams& p, cudaStream_t stream) {
-  const long long threads = (long long)p.num_rows * p.num_kv_heads * kLanesPerRow;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((threads + kRowThreads - 1) / kRowThreads));
   cfg.blockDim = dim3(kRowThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -333,10 +365,10 @@ cudaError_t launch_rows(bool append, const RowsParams& p, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (append)
-    return p.dtype == XQA_F16 ? launch<true, XQA_F16>(p.kv_dtype, cfg, p)
-                              : launch<true, XQA_BF16>(p.kv_dtype, cfg, p);
-  return p.dtype == XQA_F16 ? launch<false, XQA_F16>(p.kv_dtype, cfg, p)
-                            : launch<false, XQA_BF16>(p.kv_dtype, cfg, p);
+    return p.dtype == XQA_F16 ? launch_format<true, XQA_F16>(p.kv_dtype, cfg, p)
+                              : launch_format<true, XQA_BF16>(p.kv_dtype, cfg, p);
+  return p.dtype == XQA_F16 ? launch_format<false, XQA_F16>(p.kv_dtype, cfg, p)
+                            : launch_format<false, XQA_BF16>(p.kv_dtype, cfg, p);
 }
 
 }  // namespace xqa

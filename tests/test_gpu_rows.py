@@ -342,3 +342,31 @@ def test_cache_past_4_gb():
         a, _ = xqa.xqa_gather(cache, cache, table, lens, cu, 20, 1.0, 1.0, kv_dtype=kv_dtype)
         assert float((a - k).abs().max()) <= 0.17 * float(k.abs().max())
         del cache
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("kv_dtype,kv_layout", FORMATS)
+@pytest.mark.parametrize("hkv", [4, 2, 5])
+def test_many_rows_are_those_of_few(kv_dtype, kv_layout, dtype, hkv):
+    # one call over many rows (two heads to a thread where they are even) writes the bytes
+    # of calls over a sequence each, views with strides and bad entries among them
+    new = [28000 // hkv, 8000 // hkv, 50]
+    r = Rows(new, [new[0] + 77, new[1], 66], hkv, kv_dtype, kv_layout, dtype=dtype, seed=5, pad=3)
+    r.bt[1, 3] = r.nb + 5
+    wide = torch.zeros(r.k.shape[0], 3 * hkv, 128, dtype=r.k.dtype, device="cuda")
+    wide[:, hkv:2 * hkv], wide[:, 2 * hkv:] = r.k, r.v
+    k, v, cu, lens, bt = wide[:, hkv:2 * hkv], wide[:, 2 * hkv:], r.cu, r.lens, r.bt
+    r.k, r.v = k, v
+    r.append(0.3, 0.7)
+    assert int(r.status[0]) == xqa.XQA_ERR_BAD_BLOCK_ID
+    many = r.kc.clone(), r.vc.clone()
+    r.kc.fill_(POISON)
+    r.vc.fill_(POISON)
+    at = 0
+    for b, n in enumerate(new):
+        r.k, r.v = k[at:at + n], v[at:at + n]
+        r.cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        r.lens, r.bt = lens[b:b + 1].contiguous(), bt[b:b + 1].contiguous()
+        r.append(0.3, 0.7)
+        at += n
+    assert torch.equal(r.kc, many[0]) and torch.equal(r.vc, many[1])
