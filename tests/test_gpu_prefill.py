@@ -415,6 +415,24 @@ def test_rows_do_not_depend_on_their_neighbours(hq, hkv):
     assert bool(torch.isfinite(got[20]).all()) and not torch.equal(got[20], want[20])
 
 
+@pytest.mark.parametrize("lk", [160, 1700])
+def test_rows_past_32_bit_offsets(lk):
+    # views whose rows lie 2^23 or 2^24 elements apart: the last ones past 2^31 elements,
+    # in whole units and in units cut along the keys
+    c = Call([150, 3], [lk, 20], hq=4, hkv=2, seed=26)
+    want = c.run()
+    n = max(153, lk + 20)
+    big = torch.empty(n << 24 if lk < 1000 else n << 23, dtype=torch.float16, device="cuda").view(n, -1)
+    q = big[:153, :512].view(153, 4, 128)
+    out = big[:153, 512:1024].view(153, 4, 128)
+    k = big[:lk + 20, 1024:1280].view(-1, 2, 128)
+    v = big[:lk + 20, 1280:1536].view(-1, 2, 128)
+    q.copy_(c.q), k.copy_(c.k), v.copy_(c.v)
+    assert int(k.stride(0)) * (lk + 19) > 2**31
+    xqa.xqa_prefill(q, k, v, c.cq, c.ck, out=out)
+    assert torch.equal(out, want)
+
+
 def test_another_stream_without_a_workspace():
     c = Call([70, 200], seed=22)
     want = c.run()

@@ -112,3 +112,19 @@ def test_a_captured_step_of_append_and_decode():
         ck, cv = s.cached()
         want, _, big = plain(q, ck, cv, [1, 1], s.lens, True)
         compare(out, want, big + want.abs().amax(-1), torch.float16)
+
+
+def test_gather_and_decode_on_another_stream():
+    # outputs and workspaces that the binding allocates belong to the call's stream: the
+    # zero fill of a workspace comes before the kernel that counts in it
+    s = Server([900, 30], 20, "e4m3", "hnd", seed=8)
+    s.append(s.rows(930, HKV), s.rows(930, HKV), [900, 30])
+    q, cu, lens = s.rows(2, HQ), offsets(s.lens), s.context()
+    want, (wk, wv) = s.decode(q), s.cached()
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        side.wait_stream(torch.cuda.current_stream())
+        got = xqa.xqa_decode(q, s.kc, s.vc, s.bt, lens, s.ks, s.vs, kv_dtype="e4m3", stream=side)
+        k, v = xqa.xqa_gather(s.kc, s.vc, s.bt, lens, cu, 930, s.ks, s.vs, kv_dtype="e4m3", stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(got, want) and torch.equal(k, wk) and torch.equal(v, wv)
