@@ -251,10 +251,10 @@ def xqa_decode(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale
                sm_scale: float = 0.0, max_ctas: int = 0, min_pages_per_cta: int = 0,
                kv_dtype: str = "e5m2", kv_layout: str = "hnd"):
     """One decode step. Tensors: q fp16 [B,Hq,D]; k/v_cache uint8 FP8 codes
-    [NB,Hkv,16,D] (or [NB,16,Hkv,D] for kv_layout "nhd"); block_tables int32
-    [B,MBS]; context_lens int32 [B]. k_scale / v_scale are floats, or float32
-    CUDA tensors of one element (read on the device: xqa_decode_device_scales).
-    Returns ``out`` fp16 [B,Hq,D]."""
+    [NB,Hkv,16,D] (or [NB,16,Hkv,D] for kv_layout "nhd"), for kv_dtype "e2m1"
+    4-bit slices [NB,Hkv,1152]; block_tables int32 [B,MBS]; context_lens int32
+    [B]. k_scale / v_scale are floats, or float32 CUDA tensors of one element
+    (read on the device: xqa_decode_device_scales). Returns ``out`` fp16 [B,Hq,D]."""
     if shape is None:
         shape = make_shape(q, k_cache, block_tables, sm_scale, max_ctas, min_pages_per_cta,
                            kv_dtype=kv_dtype, kv_layout=kv_layout)
