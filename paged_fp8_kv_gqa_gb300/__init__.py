@@ -64,6 +64,7 @@ KV_LAYOUTS = {"hnd": 0, "nhd": 1}
 #: bytes of a (page, kv head) slice of a 4-bit cache (XQA_E2M1_SLICE_BYTES)
 E2M1_SLICE_BYTES = 1152
 ROW_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+_F16, _U8, _I32 = torch.float16, torch.uint8, torch.int32
 
 
 class XqaShape(ctypes.Structure):
@@ -121,6 +122,8 @@ _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
 _SHAPE = ctypes.POINTER(XqaShape)
+_DIMS_AT, _CAUSAL_AT = XqaPrefillShape.num_q_heads.offset, XqaPrefillShape.causal.offset
+_STRIDES_AT, _OUT_AT = XqaPrefillShape.q_row_stride.offset, XqaPrefillShape.out_row_stride.offset
 _ROWS = ctypes.POINTER(XqaRows)
 _PREFILL = ctypes.POINTER(XqaPrefillShape)
 _SIGS = {
@@ -235,7 +238,19 @@ def alloc_workspace(shape: XqaShape, device=None) -> torch.Tensor:
 
 
 def _decode_args(q, k_cache, v_cache, block_tables, context_lens, out, workspace, shape):
-    return (
+    try:  # the usual call, without a function call for each tensor
+        if (q.dtype is _F16 and q.is_cuda and q.is_contiguous()
+                and k_cache.dtype is _U8 and k_cache.is_cuda and k_cache.is_contiguous()
+                and v_cache.dtype is _U8 and v_cache.is_cuda and v_cache.is_contiguous()
+                and block_tables.dtype is _I32 and block_tables.is_cuda and block_tables.is_contiguous()
+                and context_lens.dtype is _I32 and context_lens.is_cuda and context_lens.is_contiguous()
+                and out.dtype is _F16 and out.is_cuda and out.is_contiguous()
+                and workspace.dtype is _U8 and workspace.is_cuda and workspace.is_contiguous()):
+            return (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+                    context_lens.data_ptr(), out.data_ptr(), workspace.data_ptr())
+    except AttributeError:
+        pass
+    return (  # raises with the reason
         _cuda(q, torch.float16, "q"),
         _cuda(k_cache, torch.uint8, "k_cache"),
         _cuda(v_cache, torch.uint8, "v_cache"),
@@ -258,7 +273,9 @@ def xqa_decode(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale
     if shape is None:
         shape = make_shape(q, k_cache, block_tables, sm_scale, max_ctas, min_pages_per_cta,
                            kv_dtype=kv_dtype, kv_layout=kv_layout)
-    if out is None or workspace is None:
+    if out is None and workspace is not None and stream is None:
+        out = torch.empty_like(q)
+    elif out is None or workspace is None:
         with _allocating(stream):
             if out is None:
                 out = torch.empty_like(q)
@@ -322,10 +339,13 @@ def xqa_dequant_e4m3(codes: torch.Tensor, scale: float = 1.0, with_f32: bool = T
     return _dequant("xqa_dequant_e4m3", codes, scale, with_f32, stream)
 
 
+_NO_CONTEXT = contextlib.nullcontext()
+
+
 def _allocating(stream):
     """Context in which the binding allocates what a call on ``stream`` writes: the
     memory (and the zero fill of a workspace) belongs to that stream."""
-    return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext()
+    return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else _NO_CONTEXT
 
 
 def _device_stream(stream):
@@ -356,12 +376,16 @@ def _heads(t: torch.Tensor, name: str, dtype=None):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in ROW_DTYPES or (dtype is not None and t.dtype != dtype):
         raise ValueError(f"{name} must have dtype {dtype or 'float16 or bfloat16'}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [rows, heads, head_dim], got {tuple(t.shape)}")
-    n, h, d = t.shape
+    return _head_strides(t.shape, t.stride(), name)
+
+
+def _head_strides(shape, stride, name: str):
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [rows, heads, head_dim], got {tuple(shape)}")
+    n, h, d = shape
     if n == 0 or h == 0:
         return h * d, d
-    rs, hs, es = t.stride()
+    rs, hs, es = stride
     if h == 1:
         hs = d
     if n == 1:
@@ -373,13 +397,17 @@ def _heads(t: torch.Tensor, name: str, dtype=None):
 
 def _cache_dims(cache: torch.Tensor, kv_dtype: str, kv_layout: str):
     """(num_blocks, num_kv_heads, block_size) of a cache tensor."""
+    return _cache_shape(cache.shape, kv_dtype, kv_layout)
+
+
+def _cache_shape(shape, kv_dtype: str, kv_layout: str):
     if kv_dtype == "e2m1":
-        if cache.dim() != 3 or cache.shape[2] != E2M1_SLICE_BYTES or kv_layout != "hnd":
+        if len(shape) != 3 or shape[2] != E2M1_SLICE_BYTES or kv_layout != "hnd":
             raise ValueError("an e2m1 cache is [num_blocks, num_kv_heads, 1152], kv_layout 'hnd'")
-        return cache.shape[0], cache.shape[1], 16
-    if cache.dim() != 4:
+        return shape[0], shape[1], 16
+    if len(shape) != 4:
         raise ValueError("an FP8 cache has four dims")
-    nb, a, b, d = cache.shape
+    nb, a, b, d = shape
     if d != 128:
         raise ValueError("head_dim must be 128")
     return (nb, a, b) if kv_layout == "hnd" else (nb, b, a)
@@ -394,39 +422,69 @@ def _scale_arg(s, dev: int, name: str):
     return 0.0, _on(s, torch.float32, dev, name)
 
 
-@functools.lru_cache(maxsize=256)
-def _rows_descriptor(*fields) -> XqaRows:
-    return XqaRows(*fields)
+@functools.lru_cache(maxsize=1024)
+def _rows_descriptor(k_shape, k_stride, v_shape, v_stride, kc_shape, vc_shape, bt_shape, n_lens,
+                     n_cu, dtype, kv_dtype, kv_layout) -> XqaRows:
+    """The descriptor of calls with tensors of these shapes and strides, checked."""
+    krs, khs = _head_strides(k_shape, k_stride, "k")
+    vrs, vhs = _head_strides(v_shape, v_stride, "v")
+    nb, hkv, bs = _cache_shape(kc_shape, kv_dtype, kv_layout)
+    n, h, d = k_shape
+    if (v_shape != k_shape or vc_shape != kc_shape or h != hkv or d != 128
+            or len(bt_shape) != 2 or bt_shape[0] != n_lens or n_cu != n_lens + 1):
+        raise ValueError("inconsistent rows / cache / block_tables / cu_seqlens shapes")
+    if dtype not in ROW_DTYPES:
+        raise ValueError(f"k must have dtype float16 or bfloat16, got {dtype}")
+    return XqaRows(n_lens, hkv, 128, bs, bt_shape[1], nb, n, KV_DTYPES[kv_dtype],
+                   KV_LAYOUTS[kv_layout], ROW_DTYPES[dtype], krs, khs, vrs, vhs)
+
+
+def _refuse_rows(k, v, cu_seqlens, k_cache, v_cache, block_tables, context_lens, stream):
+    """Raises with the first reason to refuse a call of _move_rows."""
+    _heads(k, "k")  # CPU tensors before CUDA is asked
+    _heads(v, "v", k.dtype)
+    dev, _ = _device_stream(stream)
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError(f"k and v must be on the current device, cuda:{dev}")
+    for x, dtype, name in ((k_cache, _U8, "k_cache"), (v_cache, _U8, "v_cache"),
+                           (cu_seqlens, _I32, "cu_seqlens"), (block_tables, _I32, "block_tables"),
+                           (context_lens, _I32, "context_lens")):
+        _on(x, dtype, dev, name)
+    raise ValueError("invalid arguments")
 
 
 def _move_rows(fn_name, k, v, cu_seqlens, k_cache, v_cache, block_tables, context_lens, k_scale,
                v_scale, kv_dtype, kv_layout, status, stream):
-    krs, khs = _heads(k, "k")  # CPU tensors are refused before CUDA is asked
-    vrs, vhs = _heads(v, "v", k.dtype)
-    dev, handle = _device_stream(stream)
-    nb, hkv, bs = _cache_dims(k_cache, kv_dtype, kv_layout)
-    n, h, d = k.shape
-    b = context_lens.numel()
-    if (v.shape != k.shape or v_cache.shape != k_cache.shape or h != hkv or d != 128
-            or block_tables.dim() != 2 or block_tables.shape[0] != b
-            or cu_seqlens.numel() != b + 1):
-        raise ValueError("inconsistent rows / cache / block_tables / cu_seqlens shapes")
-    if k.get_device() != dev or v.get_device() != dev:
-        raise ValueError(f"k and v must be on the current device, cuda:{dev}")
-    rows = _rows_descriptor(b, hkv, 128, bs, block_tables.shape[1], nb, n, KV_DTYPES[kv_dtype],
-                            KV_LAYOUTS[kv_layout], ROW_DTYPES[k.dtype], krs, khs, vrs, vhs)
-    kp, vp = k.data_ptr(), v.data_ptr()
-    kc = _on(k_cache, torch.uint8, dev, "k_cache")
-    vc = _on(v_cache, torch.uint8, dev, "v_cache")
-    ks, ksp = _scale_arg(k_scale, dev, "k_scale")
-    vs, vsp = _scale_arg(v_scale, dev, "v_scale")
-    a = (kp, vp, kc, vc) if fn_name == "xqa_append" else (kc, vc, kp, vp)
-    code = getattr(load_library(), fn_name)(
-        a[0], a[1], _on(cu_seqlens, torch.int32, dev, "cu_seqlens"),
-        _on(block_tables, torch.int32, dev, "block_tables"),
-        _on(context_lens, torch.int32, dev, "context_lens"), ks, vs, ksp, vsp, a[2], a[3],
-        ctypes.byref(rows), None if status is None else _on(status, torch.int32, dev, "status"),
-        handle)
+    rows = None
+    try:  # the usual call, without a function call for each tensor
+        dev, dtype = k.get_device(), k.dtype
+        if (dev >= 0 and v.dtype is dtype and v.get_device() == dev
+                and k_cache.dtype is _U8 and k_cache.get_device() == dev and k_cache.is_contiguous()
+                and v_cache.dtype is _U8 and v_cache.get_device() == dev and v_cache.is_contiguous()
+                and cu_seqlens.dtype is _I32 and cu_seqlens.get_device() == dev
+                and cu_seqlens.is_contiguous()
+                and block_tables.dtype is _I32 and block_tables.get_device() == dev
+                and block_tables.is_contiguous()
+                and context_lens.dtype is _I32 and context_lens.get_device() == dev
+                and context_lens.is_contiguous() and torch._C._cuda_getDevice() == dev):
+            rows = _rows_descriptor(k.shape, k.stride(), v.shape, v.stride(), k_cache.shape,
+                                    v_cache.shape, block_tables.shape, context_lens.numel(),
+                                    cu_seqlens.numel(), dtype, kv_dtype, kv_layout)
+    except AttributeError:
+        pass
+    if rows is None:
+        _refuse_rows(k, v, cu_seqlens, k_cache, v_cache, block_tables, context_lens, stream)
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _device_stream(stream)[1]
+    ks, ksp = (k_scale, None) if type(k_scale) is float else _scale_arg(k_scale, dev, "k_scale")
+    vs, vsp = (v_scale, None) if type(v_scale) is float else _scale_arg(v_scale, dev, "v_scale")
+    kp, vp, kc, vc = k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
+    if fn_name == "xqa_append":
+        fn = load_library().xqa_append
+    else:
+        fn, kp, vp, kc, vc = load_library().xqa_gather, kc, vc, kp, vp
+    code = fn(kp, vp, cu_seqlens.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), ks, vs,
+              ksp, vsp, kc, vc, ctypes.byref(rows),
+              None if status is None else _on(status, _I32, dev, "status"), handle)
     if code:
         raise XqaError(code, fn_name)
 
@@ -456,7 +514,7 @@ def xqa_gather(k_cache, v_cache, block_tables, context_lens, cu_seqlens, num_row
         raise ValueError("pass both k and v, or neither")
     if k is None:
         hkv = _cache_dims(k_cache, kv_dtype, kv_layout)[1]
-        with _allocating(stream):
+        with _allocating(stream) if stream is not None else _NO_CONTEXT:
             k = torch.empty((int(num_rows), hkv, 128), dtype=dtype, device=k_cache.device)
             v = torch.empty_like(k)
     elif k.shape[0] != num_rows:
@@ -486,6 +544,22 @@ def _prefill_strides(q, k, v):
     return side
 
 
+@functools.lru_cache(maxsize=1024)
+def _prefill_fields(q_shape, q_stride, k_shape, k_stride, v_shape, v_stride, dtype) -> tuple:
+    """(what a descriptor for tensors of these shapes and strides holds from num_q_heads to
+    dtype, and as strides; its strides of a contiguous out, written out or 0)."""
+    side = (_head_strides(q_shape, q_stride, "q") + _head_strides(k_shape, k_stride, "k")
+            + _head_strides(v_shape, v_stride, "v"))
+    if k_shape != v_shape or k_shape[2] != q_shape[2] or dtype not in ROW_DTYPES:
+        raise ValueError("inconsistent q / k / v shapes")
+    rs, hs = q_shape[1] * q_shape[2], q_shape[2]
+    s = bytes(XqaPrefillShape(0, q_shape[1], k_shape[1], q_shape[2], q_shape[0], k_shape[0],
+                              ROW_DTYPES[dtype], 0, 0.0, 0, *side, 0, 0))
+    outs = frozenset(bytes(XqaPrefillShape(out_row_stride=a, out_head_stride=b))[_OUT_AT:]
+                     for a in (0, rs) for b in (0, hs))
+    return s[_DIMS_AT:_CAUSAL_AT], s[_STRIDES_AT:_OUT_AT], outs
+
+
 def xqa_prefill_workspace_size(shape: XqaPrefillShape) -> int:
     n = _SZ(0)
     _check(load_library().xqa_prefill_workspace_size(ctypes.byref(shape), ctypes.byref(n)),
@@ -500,6 +574,18 @@ def alloc_prefill_workspace(shape: XqaPrefillShape, device=None) -> torch.Tensor
                        device=device or "cuda")
 
 
+def _refuse_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, stream):
+    """Raises with the first reason to refuse a call of xqa_prefill."""
+    _prefill_strides(q, k, v)  # CPU tensors before CUDA is asked
+    dev, _ = _device_stream(stream)
+    for x in (q, k, v):
+        if x.get_device() != dev:
+            raise ValueError(f"q, k, v and out must be on the current device, cuda:{dev}")
+    _on(cu_seqlens_q, _I32, dev, "cu_seqlens_q")
+    _on(cu_seqlens_k, _I32, dev, "cu_seqlens_k")
+    raise ValueError("invalid arguments")
+
+
 def xqa_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=None, lse=None, workspace=None,
                 shape: XqaPrefillShape | None = None, stream=None, causal: bool = True,
                 sm_scale: float = 0.0, max_ctas: int = 0):
@@ -512,43 +598,52 @@ def xqa_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=None, lse=None, wo
     written."""
     if shape is None:
         shape = make_prefill_shape(q, k, v, cu_seqlens_q, causal, sm_scale, max_ctas, out)
-    else:
-        s = shape
-        if _prefill_strides(q, k, v) != (s.q_row_stride, s.q_head_stride, s.k_row_stride,
-                                         s.k_head_stride, s.v_row_stride, s.v_head_stride) or (
-                s.total_q, s.num_q_heads, s.head_dim, s.total_k, s.num_kv_heads, s.dtype) != (
-                *q.shape, k.shape[0], k.shape[1], ROW_DTYPES[q.dtype]):
-            raise ValueError("q, k, v do not match the shape descriptor")
-    dev, handle = _device_stream(stream)  # CPU tensors are refused before CUDA is asked
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
+    outs = None
+    try:  # the usual call, without a function call for each tensor
+        dev, dtype = q.get_device(), q.dtype
+        if (dev >= 0 and k.dtype is dtype and k.get_device() == dev
+                and v.dtype is dtype and v.get_device() == dev
+                and cu_seqlens_q.dtype is _I32 and cu_seqlens_q.get_device() == dev
+                and cu_seqlens_q.is_contiguous()
+                and cu_seqlens_k.dtype is _I32 and cu_seqlens_k.get_device() == dev
+                and cu_seqlens_k.is_contiguous() and torch._C._cuda_getDevice() == dev):
+            dims, strides, outs = _prefill_fields(q.shape, q.stride(), k.shape, k.stride(), v.shape,
+                                                  v.stride(), dtype)
+    except AttributeError:
+        pass
+    if outs is None:
+        _refuse_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, stream)
+    held = bytes(shape)
+    if held[_DIMS_AT:_CAUSAL_AT] != dims or held[_STRIDES_AT:_OUT_AT] != strides:
+        raise ValueError("q, k, v do not match the shape descriptor")
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _device_stream(stream)[1]
     if out is None:
-        with _allocating(stream):
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if shape.out_row_stride not in (0, q.shape[1] * q.shape[2]) or (
-                shape.out_head_stride not in (0, q.shape[2])):
+        if held[_OUT_AT:] not in outs:
             raise ValueError("the shape descriptor names strides of out: pass out")
-    elif out.shape != q.shape or _heads(out, "out", q.dtype) != (
+        with _allocating(stream) if stream is not None else _NO_CONTEXT:
+            out = torch.empty(q.shape, dtype=dtype, device=q.device)
+    elif out.shape != q.shape or _heads(out, "out", dtype) != (
             shape.out_row_stride or shape.num_q_heads * 128, shape.out_head_stride or 128):
         raise ValueError("out does not match q or the shape descriptor")
+    elif out.get_device() != dev:
+        raise ValueError(f"q, k, v and out must be on the current device, cuda:{dev}")
     if workspace is None:
         with _allocating(stream):
             workspace = alloc_prefill_workspace(shape, q.device)
-    if cu_seqlens_q.numel() != shape.batch + 1 or cu_seqlens_k.numel() != shape.batch + 1:
+    n = shape.batch + 1
+    if cu_seqlens_q.numel() != n or cu_seqlens_k.numel() != n:
         raise ValueError("cu_seqlens_q and cu_seqlens_k must have batch + 1 entries")
     lp = None
     if lse is not None:
         lp = _on(lse, torch.float32, dev, "lse")
         if lse.shape != q.shape[:2]:
             raise ValueError("lse must be [total_q, num_q_heads]")
-    for x in (q, k, v, out):
-        if x.get_device() != dev:
-            raise ValueError(f"q, k, v and out must be on the current device, cuda:{dev}")
     code = load_library().xqa_prefill(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), _on(cu_seqlens_q, torch.int32, dev, "cu_seqlens_q"),
-        _on(cu_seqlens_k, torch.int32, dev, "cu_seqlens_k"), out.data_ptr(), lp,
-        ctypes.byref(shape), _on(workspace, torch.uint8, dev, "workspace"), workspace.numel(),
-        handle)
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
+        out.data_ptr(), lp, ctypes.byref(shape), _on(workspace, _U8, dev, "workspace"),
+        workspace.numel(), handle)
     if code:
         raise XqaError(code, "xqa_prefill")
     return out

@@ -442,7 +442,7 @@ __device__ __forceinline__ void tensor_role(const Ctx& c) {
   if (!next_unit(n2, hidden2)) return;
   bool more = true, begin = true;
   int j = 0;                // tile of the V slot
-  int sv = 0, sk = 0;       // ring slots of this round's V and K tile
+  int sv = 0, sk = 0;       // ring slots of the V and the K tile in turn
   uint32_t pv = 0, pk = 0;  // their phases
   // phases, a bit for each row tile (P: two) or stage; O is free before its first use
   uint32_t ph_q = 0, ph_p = 0, ph_o = 3, ph_clean = 0;
