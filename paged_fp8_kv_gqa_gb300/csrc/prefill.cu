@@ -409,7 +409,10 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
 // The row tiles in turn: O += P V of tile j, then S of the next tile (j - 1, or the
 // next unit's first), which takes the place of P. The order is fixed, so the row
 // tiles settle half a period apart and one's softmax runs under the other's
-// products; it runs on across units, so a new unit starts without a gap. Products are
+// products; it runs on across units, so a new unit starts without a gap. At a unit's last
+// tile it looks at the next unit only: the ones behind it may be published no earlier than
+// the epilogue is done with this one, whose products are not issued yet. A unit without
+// tiles there ends the run, and the search for the next with some comes after. Products are
 // issued by an elected lane, whose operands stay in uniform registers: under `lane ==
 // 0` each cost more to issue than to execute (1 x 16384: 1775 us against 1420). The
 // code is kept short: it runs once a tile between the softmax warps' long loops and is
@@ -425,21 +428,17 @@ __device__ __forceinline__ void tensor_role(const Ctx& c) {
   const uint64_t k_desc = desc_k_major(tiles + 2 * kTileBytes);  // stage 0 of the ring
   const uint64_t v_desc = desc_mn_major(tiles + 2 * kTileBytes);
   int i = -1;
-  auto next_unit = [&](int (&n)[2], int& hidden) {  // the next one with work
-    do {
-      Unit w;
-      if (!c.get_unit(++i, w)) return false;
-      c.free_unit(i);
+  // tiles of the current unit (row tile s has n[s]) and of the one after it
+  int n[2] = {0, 0}, hidden = 0, n2[2], hidden2 = 0;
+  auto next_unit = [&]() {
+    Unit w;
+    if (!c.get_unit(++i, w)) return false;
+    c.free_unit(i);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) n[s] = __shfl_sync(kAll, w.n[s], 0);  // uniform
-      hidden = __shfl_sync(kAll, w.hidden, 0);
-    } while (max(n[0], n[1]) == 0);
+    for (int s = 0; s < 2; ++s) n2[s] = __shfl_sync(kAll, w.n[s], 0);  // uniform
+    hidden2 = __shfl_sync(kAll, w.hidden, 0);
     return true;
   };
-  // tiles of the current unit (row tile s has n[s]) and of the next; before the first
-  // unit, an empty one
-  int n[2] = {0, 0}, hidden = 0, n2[2], hidden2;
-  if (!next_unit(n2, hidden2)) return;
   bool more = true, begin = true;
   int j = 0;                // tile of the V slot
   int sv = 0, sk = 0;       // ring slots of the V and the K tile in turn
@@ -447,25 +446,29 @@ __device__ __forceinline__ void tensor_role(const Ctx& c) {
   // phases, a bit for each row tile (P: two) or stage; O is free before its first use
   uint32_t ph_q = 0, ph_p = 0, ph_o = 3, ph_clean = 0;
   for (;;) {
-    // V tile j of the current unit (none in the first round), then a K tile: j - 1, or
+    // V tile j of the current unit (none in a run's first round), then a K tile: j - 1, or
     // the next unit's first
-    if (!begin) {
+    if (begin) {  // no product is outstanding: past units without tiles
+      do {
+        if (!next_unit()) return;
+      } while (max(n2[0], n2[1]) == 0);
+    } else {
       if (!c.wait(&sh.kv_full[sv], pv)) return;
       if ((j + 1) * kTile > hidden) {  // masked: after the V warps are done with it
         if (!c.wait(&sh.v_clean[sv], ph_clean >> sv & 1)) return;
         ph_clean ^= 1u << sv;
       }
       if (j == 0) {
-        more = next_unit(n2, hidden2);
+        more = next_unit();
         if (!more && *(volatile int*)&sh.abort_flag) return;
       }
       sk = sv + 1 == kKvStages ? 0 : sv + 1;
       pk = sk == 0 ? pv ^ 1 : pv;
     }
-    const bool cross = j == 0;         // the K tile is the next unit's
-    const bool next = !cross || more;  // there is one
-    if (next && !c.wait(&sh.kv_full[sk], pk)) return;
+    const bool cross = j == 0;  // the K tile is the next unit's
     const int nk = cross ? max(n2[0], n2[1]) : 0;
+    const bool next = !cross || (more && nk > 0);  // there is one
+    if (next && !c.wait(&sh.kv_full[sk], pk)) return;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const uint32_t s_tmem = tmem + s * kTile, o_tmem = s_tmem + 256;
@@ -494,7 +497,7 @@ __device__ __forceinline__ void tensor_role(const Ctx& c) {
         __syncwarp();
       }
       // S: tile j - 1, or the next unit's first; the row tile's first waits for its Q
-      if (!(cross ? more && n2[s] == nk : j - 1 < n[s])) continue;
+      if (!(cross ? next && n2[s] == nk : j - 1 < n[s])) continue;
       if (cross || j == n[s]) {
         if (!c.wait(&sh.q_full[s], ph_q >> s & 1)) return;
         ph_q ^= 1u << s;
@@ -517,7 +520,11 @@ __device__ __forceinline__ void tensor_role(const Ctx& c) {
       if (next) tc_commit(&sh.kv_empty[sk]);
     }
     __syncwarp();
-    if (!next) return;
+    if (!next) {
+      if (!more) return;
+      begin = true;
+      continue;
+    }
     sv = sk + 1 == kKvStages ? 0 : sk + 1;
     pv = sv == 0 ? pk ^ 1 : pk;
     if (cross) {  // on to the next unit

@@ -1,0 +1,49 @@
+"""xqa_prefill where one CTA works through units with and without keys (see test_gpu_prefill
+for the bounds)."""
+import pytest
+import torch
+
+import paged_fp8_kv_gqa_gb300 as xqa
+from test_gpu_prefill import Call
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("max_ctas", [1, 2, 0])
+@pytest.mark.parametrize("lq,lk", [([40, 7, 9, 20, 50], [40, 0, 0, 0, 50]),
+                                   ([300, 200, 100, 1], [300, 0, 0, 0]),
+                                   ([1, 2, 3, 4, 5, 6, 7, 8], [0, 0, 9, 0, 0, 0, 0, 700]),
+                                   ([900], [30]), ([700, 5, 640], [129, 0, 260])])
+def test_units_without_keys_between_units_with_keys(lq, lk, max_ctas, causal):
+    # sequences without keys, and causal rows in front of the first key: every CTA meets runs
+    # of such units after, before and between those with work
+    for hq, hkv in ((8, 2), (6, 1)):
+        c = Call(lq, lk, hq=hq, hkv=hkv, seed=sum(lk), dtype="bf16" if hkv == 1 else "fp16")
+        out = c.run(causal, max_ctas=max_ctas)
+        c.check(out, causal)
+        assert torch.equal(c.run(causal, max_ctas=max_ctas), out)
+
+
+def test_many_more_queries_than_keys():
+    c = Call([8192], [128], hq=32, hkv=4, seed=3, dtype="bf16")
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("max_ctas", [1, 3])
+def test_bad_key_offsets_between_good_sequences(max_ctas):
+    lens = [70, 40, 30, 300, 20]
+    c = Call(lens, hq=8, hkv=2, seed=4)
+    want = c.run(max_ctas=max_ctas)
+    good = c.ck.clone()
+    c.ck[2:4] = torch.tensor([-1, -1], dtype=torch.int32)  # sequences 1, 2 and 3
+    lse = torch.zeros_like(c.lse)
+    out = torch.full_like(want, 9.0)
+    xqa.xqa_prefill(c.q, c.k, c.v, c.cq, c.ck, out=out, lse=lse, workspace=c.ws, shape=c.shape)
+    assert xqa.xqa_read_status(c.ws) == xqa.XQA_ERR_BAD_OFFSETS
+    lost = slice(70, 440)
+    assert bool(torch.isnan(out[lost]).all()) and bool(torch.isnan(lse[lost]).all())
+    for keep in (slice(0, 70), slice(440, 460)):
+        assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], c.lse[keep])
+    xqa.xqa_prefill(c.q, c.k, c.v, c.cq, good, out=out, workspace=c.ws, shape=c.shape)
+    assert torch.equal(out, want) and xqa.xqa_read_status(c.ws) == xqa.XQA_OK
