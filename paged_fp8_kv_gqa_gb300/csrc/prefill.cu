@@ -912,9 +912,11 @@ __device__ __forceinline__ void join_pieces(const Ctx& c) {
 #pragma unroll
   for (int k = 0; k < kMaxPieces; ++k)
     if (ml[k].y != 0.f) top = fmaxf(top, ml[k].x);
+  // A piece with keys keeps the least weight there is: the infinities and NaN in its O and l
+  // (keys of NaN alone leave its maximum at kNoRowMax) are the row's, however small it is.
 #pragma unroll
   for (int k = 0; k < kMaxPieces; ++k) {
-    w[k] = ml[k].y != 0.f ? ex2(ml[k].x - top) : 0.f;
+    w[k] = ml[k].y != 0.f ? fmaxf(ex2(ml[k].x - top), 0x1p-149f) : 0.f;
     if (w[k] != 0.f) sum += w[k] * ml[k].y;
   }
   const float nan = __int_as_float(0x7fc00000);

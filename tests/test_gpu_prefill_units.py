@@ -1,10 +1,12 @@
-"""xqa_prefill where one CTA works through units with and without keys (see test_gpu_prefill
-for the bounds)."""
+"""xqa_prefill where one CTA works through units with and without keys, and where a row has
+infinities or NaN in one piece of its keys (see test_gpu_prefill for the bounds)."""
+import math
+
 import pytest
 import torch
 
 import paged_fp8_kv_gqa_gb300 as xqa
-from test_gpu_prefill import Call
+from test_gpu_prefill import Call, plain
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +49,49 @@ def test_bad_key_offsets_between_good_sequences(max_ctas):
         assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], c.lse[keep])
     xqa.xqa_prefill(c.q, c.k, c.v, c.cq, good, out=out, workspace=c.ws, shape=c.shape)
     assert torch.equal(out, want) and xqa.xqa_read_status(c.ws) == xqa.XQA_OK
+
+
+def same_specials(a, b):
+    """NaN in the same places, equal infinities."""
+    assert torch.equal(torch.isnan(a), torch.isnan(b))
+    inf = torch.isinf(b)
+    assert torch.equal(torch.isinf(a), inf) and torch.equal(a[inf].double(), b[inf].double())
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("at", [[256], [0, 256], range(128), range(128, 256), [100]])
+def test_a_piece_of_nan_keys_makes_its_rows_nan(at, causal, dtype):
+    # the second sequence's three tiles are a piece each, the last one of a single key; its
+    # rows that see a NaN key are NaN, whole or in pieces
+    for hq, hkv in ((8, 2), (5, 1)):
+        c = Call([3, 2], [4000, 257], hq=hq, hkv=hkv, seed=7, dtype=dtype)
+        for i in at:
+            c.k[4000 + i] = math.nan
+        out = c.run(causal)
+        assert c.ws.numel() > 16384  # in pieces
+        lse = c.lse.clone()
+        sees = causal and list(at) == [256]  # then the first of the two rows sees none of them
+        assert bool(torch.isnan(out[3 + sees:]).all()) and bool(torch.isnan(lse[3 + sees:]).all())
+        assert bool(torch.isfinite(out[:3 + sees]).all()) and bool(torch.isfinite(lse[:3 + sees]).all())
+        one = c.run(causal, max_ctas=1)
+        assert c.ws.numel() < 16384  # whole
+        same_specials(out, one)
+        same_specials(lse, c.lse)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("val", [math.inf, -math.inf, math.nan])
+def test_infinities_in_a_piece_of_little_weight(val, causal):
+    # the last key's logits lie about 300 below the others: its weight is a number in 64 bits,
+    # not in 32, and its value reaches every row that sees it
+    c = Call([3, 2], [4000, 257], hq=8, hkv=2, seed=8)
+    c.q[3:] = 1.0
+    c.k[4000 + 256] = -300 * math.sqrt(128) / 128
+    c.v[4000 + 256, :, 9] = val
+    out = c.run(causal)
+    assert c.ws.numel() > 16384
+    c.check(out, causal)
+    want, _, _ = plain(c.q, c.k, c.v, c.lq, c.lk, causal)
+    assert int((~torch.isfinite(want)).sum()) == 8 * (1 if causal else 2)
+    same_specials(out, want)
