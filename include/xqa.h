@@ -260,7 +260,8 @@ typedef struct xqa_rows {
  * holds zeros, and one that has a NaN reads back as NaN throughout. Two rows must not
  * name the same cache slot. One kernel, no host synchronisation, no workspace; may be
  * captured into a CUDA graph. A host scale that is not finite or not above 0 is
- * refused (XQA_ERR_VALUE). */
+ * refused (XQA_ERR_VALUE). A device scale is known to the kernel alone and divides as
+ * it is, as IEEE division does: by 0, FP8 codes saturate (a NaN where x is 0). */
 xqa_status_t xqa_append(const void* k, const void* v, const int32_t* cu_seqlens,
                         const int32_t* block_tables, const int32_t* context_lens, float k_scale,
                         float v_scale, const float* k_scale_dev, const float* v_scale_dev,

@@ -32,23 +32,26 @@ namespace {
 constexpr int kRowThreads = 128;
 constexpr int kLanesPerRow = 8;  // threads of one (row, kv head)
 
-// Quotients by one divisor t >= 0, as in IEEE division: q0 = x r with r = RN(1/t),
+// Quotients by one divisor t, as in IEEE division: q0 = x r with r = RN(1/t),
 // then one correction q0 - (q0 t - x) r (Markstein, "Computation of elementary
 // functions on the IBM RISC System/6000 processor", 1990): exact whenever x / t is
 // representable, so ties are seen as ties; in this form a zero keeps its sign. A
-// divisor that is a power of two needs no correction. t = 0 gives zeros.
+// divisor that is a power of two needs no correction. Other divisors than those of
+// 2^-60 to 2^60 (a scale on the device may be 0, negative or NaN) divide plainly.
 struct Divisor {
   float t, r;
   bool exact;  // x r is x / t
   bool slow;   // 1 / t or the correction could leave the normal range
+  bool zeros;  // zeros in place of the quotients
 };
 
-__device__ __forceinline__ Divisor make_divisor(float t) {
+__device__ __forceinline__ Divisor make_divisor(float t, bool zeros = false) {
   Divisor d;
   d.t = t;
-  d.r = t > 0.f ? __frcp_rn(t) : 0.f;
-  d.exact = (__float_as_uint(t) & 0x7fffffu) == 0;
-  d.slow = t > 0.f && !(t >= 0x1p-60f && t <= 0x1p60f);
+  d.r = zeros ? 0.f : __frcp_rn(t);
+  d.exact = zeros || (__float_as_uint(t) & 0x7fffffu) == 0;
+  d.slow = !zeros && !(t >= 0x1p-60f && t <= 0x1p60f);
+  d.zeros = zeros;
   return d;
 }
 
@@ -75,8 +78,8 @@ __device__ __forceinline__ void divide(const uint64_t (&x)[4], float amax, const
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       split2(x[i], q[2 * i], q[2 * i + 1]);
-      q[2 * i] = d.t > 0.f ? __fdiv_rn(q[2 * i], d.t) : copysignf(0.f, q[2 * i]);
-      q[2 * i + 1] = d.t > 0.f ? __fdiv_rn(q[2 * i + 1], d.t) : copysignf(0.f, q[2 * i + 1]);
+      q[2 * i] = d.zeros ? copysignf(0.f, q[2 * i]) : __fdiv_rn(q[2 * i], d.t);
+      q[2 * i + 1] = d.zeros ? copysignf(0.f, q[2 * i + 1]) : __fdiv_rn(q[2 * i + 1], d.t);
     }
   }
 }
@@ -209,7 +212,7 @@ __device__ __forceinline__ void store_codes(uint8_t* cache, long long at, int pa
       const uint32_t s8 = cvt_fp8x2<XQA_KV_E4M3>(__fdiv_rn(__fdiv_rn(amax, scale), 6.f), 0.f) & 0xffu;
       const uint32_t sh = e4m3x2_to_f16x2(s8);
       const float s = __low2float(*reinterpret_cast<const __half2*>(&sh));
-      divide(x, amax, make_divisor(s * scale), q);  // s of 0: zeros
+      divide(x, amax, make_divisor(s * scale, !(fabsf(s) > 0.f)), q);  // s of 0 or NaN: zeros
       uint8_t* slice = cache + (at / kBlockSize) * kSliceBytes4;
       const int token = (int)(at % kBlockSize);
       *reinterpret_cast<uint32_t*>(slice + token * (kHeadDim / 2) + 32 * h + 4 * part) = cvt_e2m1x8(q);
