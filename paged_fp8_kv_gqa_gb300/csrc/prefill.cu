@@ -296,8 +296,8 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
       if (base >= p.batch) break;
       q0 = len_q = mine = 0;
       if (base + lane < p.batch) {
-        q0 = __ldg(p.cu_q + base + lane);
-        const int q1 = __ldg(p.cu_q + base + lane + 1);
+        q0 = p.cu_q[base + lane];
+        const int q1 = p.cu_q[base + lane + 1];
         if (q0 >= 0 && q1 >= q0 && q1 <= p.total_q) len_q = q1 - q0;
         else record_status(&sh.status, XQA_ERR_BAD_OFFSETS);
         mine = (int)(((long long)len_q + per_unit - 1) / per_unit) * p.num_kv_heads;
@@ -330,7 +330,7 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
     const int pairs = s_mine / p.num_kv_heads;
     const int pair = pairs - 1 - local / p.num_kv_heads;
     const int head = local - local / p.num_kv_heads * p.num_kv_heads;
-    const int k0 = __ldg(p.cu_k + base + src), k1 = __ldg(p.cu_k + base + src + 1);
+    const int k0 = p.cu_k[base + src], k1 = p.cu_k[base + src + 1];
     Unit w;
     w.end = 0;
     w.bad = (k0 < 0 || k1 < k0 || k1 > p.total_k) ? 1 : 0;

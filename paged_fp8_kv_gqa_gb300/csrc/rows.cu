@@ -154,13 +154,13 @@ __device__ __forceinline__ RowPlace find_row(const RowsParams& p, int row, int h
   int lo = 0, hi = p.batch;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(p.cu_seqlens + mid) <= row) lo = mid;
+    if (p.cu_seqlens[mid] <= row) lo = mid;
     else hi = mid - 1;
   }
   if (lo >= p.batch) return r;
-  const int beg = __ldg(p.cu_seqlens + lo), end = __ldg(p.cu_seqlens + lo + 1);
+  const int beg = p.cu_seqlens[lo], end = p.cu_seqlens[lo + 1];
   if (row < beg || row >= end) return r;
-  const int ctx = __ldg(p.context_lens + lo);
+  const int ctx = p.context_lens[lo];
   const long long pos = (long long)ctx - ((long long)end - row);
   // every row of a sequence with a bad length is bad, not only those in front
   // of its first token
@@ -171,8 +171,7 @@ __device__ __forceinline__ RowPlace find_row(const RowsParams& p, int row, int h
       atomicCAS(p.status, XQA_OK, XQA_ERR_CTX_TOO_LONG);
     return r;
   }
-  const int id =
-      __ldg(p.block_tables + (size_t)lo * p.max_blocks_per_seq + (size_t)(pos / kBlockSize));
+  const int id = p.block_tables[(size_t)lo * p.max_blocks_per_seq + (size_t)(pos / kBlockSize)];
   if (id < 0 || id >= p.num_blocks) {
     r.state = -1;
     if (p.status && head == 0 && (threadIdx.x & (kLanesPerRow - 1)) == 0)
@@ -234,14 +233,14 @@ __device__ __forceinline__ void load_values(const uint8_t* cache, long long at, 
   if (kFmt != XQA_KV_E2M1) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      c[h] = __ldg(reinterpret_cast<const uint2*>(cache + at * kHeadDim + 64 * h + 8 * part));
+      c[h] = *reinterpret_cast<const uint2*>(cache + at * kHeadDim + 64 * h + 8 * part);
   } else {
     const uint8_t* slice = cache + (at / kBlockSize) * kSliceBytes4;
     const int token = (int)(at % kBlockSize);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      c[h].x = __ldg(reinterpret_cast<const uint32_t*>(slice + token * (kHeadDim / 2) + 32 * h + 4 * part));
-      s8[h] = __ldg(slice + kCodeBytes4 + token * (kHeadDim / kGroup4) + 4 * h + (part >> 1));
+      c[h].x = *reinterpret_cast<const uint32_t*>(slice + token * (kHeadDim / 2) + 32 * h + 4 * part);
+      s8[h] = slice[kCodeBytes4 + token * (kHeadDim / kGroup4) + 4 * h + (part >> 1)];
     }
   }
 #pragma unroll
@@ -279,15 +278,19 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsParams p) {
   griddep_launch_dependents();
   const long long u = ((long long)blockIdx.x * kRowThreads + threadIdx.x) / kLanesPerRow;
   const int part = threadIdx.x % kLanesPerRow;
-  griddep_wait();  // every input may come from the kernels before this one
+  // Every input may come from the kernels before this one, and some of its sectors may lie
+  // in this SM's cache since one of those read them: it may run on the SM after this kernel
+  // became resident and before another wrote them. So the loads behind the wait are plain
+  // ones: the read-only path promises nothing for bytes that change meanwhile.
+  griddep_wait();
   const int per_row = p.num_kv_heads / kHeads;  // a multiple, see launch_format
   if (u >= (long long)p.num_rows * per_row) return;
   const int row = (int)((uint32_t)u / (uint32_t)per_row);
   const int head = ((int)u - row * per_row) * kHeads;
   const uint16_t* kp = p.k + row * p.k_row_stride + head * p.k_head_stride + 8 * part;
   const uint16_t* vp = p.v + row * p.v_row_stride + head * p.v_head_stride + 8 * part;
-  const float k_scale = p.k_scale_ptr ? __ldg(p.k_scale_ptr) : p.k_scale;
-  const float v_scale = p.v_scale_ptr ? __ldg(p.v_scale_ptr) : p.v_scale;
+  const float k_scale = p.k_scale_ptr ? *p.k_scale_ptr : p.k_scale;
+  const float v_scale = p.v_scale_ptr ? *p.v_scale_ptr : p.v_scale;
   if constexpr (kAppend) {
     // in flight while the slot is looked up; rows of no sequence are readable too
     uint4 x[kHeads][4];
@@ -295,7 +298,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsParams p) {
     for (int h = 0; h < kHeads; ++h) {
       const uint4* k = reinterpret_cast<const uint4*>(kp + h * p.k_head_stride);
       const uint4* v = reinterpret_cast<const uint4*>(vp + h * p.v_head_stride);
-      x[h][0] = __ldg(k), x[h][1] = __ldg(k + 8), x[h][2] = __ldg(v), x[h][3] = __ldg(v + 8);
+      x[h][0] = k[0], x[h][1] = k[8], x[h][2] = v[0], x[h][3] = v[8];
     }
     const RowPlace r = find_row(p, row, head);
     if (r.state != 1) return;
