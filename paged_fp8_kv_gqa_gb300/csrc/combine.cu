@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineParams 
   const bool bad = p.tickets[ilo] >= kTicketPoison;
   __syncthreads();  // every thread has read the ticket before it is cleared
   if (threadIdx.x == 0) p.tickets[ilo] = 0;
-  const float v_scale = p.v_scale_ptr ? __ldg(p.v_scale_ptr) : p.v_scale;
+  const float v_scale = p.v_scale_ptr ? *p.v_scale_ptr : p.v_scale;
   for (int col = threadIdx.x >> 5; col < ncols; col += kCombineThreads / 32) {
     __half* o = p.out + combine_row(p, s, col) * kHeadDim + dq;
     if (bad) {

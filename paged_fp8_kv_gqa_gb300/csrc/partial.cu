@@ -167,7 +167,7 @@ __device__ __forceinline__ PageBatch load_batch(const PartialParams& p, const in
     if (base == 0) stamp_after(15, s);
     const int b = s / p.num_kv_heads, kvh = s - b * p.num_kv_heads;
     const int j = pg - segs[s];
-    const int id = __ldg(&p.block_tables[(size_t)b * p.max_blocks_per_seq + j]);
+    const int id = p.block_tables[(size_t)b * p.max_blocks_per_seq + j];
     r.bad = (id < 0 || id >= p.num_blocks) ? 1 : 0;
     r.y = r.bad ? 0 : (p.kv_layout == XQA_LAYOUT_HND ? (id * p.num_kv_heads + kvh) : id) * kBlockSize;
     r.seg = s;
@@ -195,7 +195,7 @@ __device__ __forceinline__ void load_q(const PartialParams& p, int s, int g, int
       const uint4* qp = reinterpret_cast<const uint4*>(p.q + col_row(p, s, col) * kHeadDim + 32 * c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint4 v = __ldg(qp + i);
+        const uint4 v = qp[i];
         qf[j][4 * i] = v.x;
         qf[j][4 * i + 1] = v.y;
         qf[j][4 * i + 2] = v.z;
@@ -777,7 +777,7 @@ __device__ __forceinline__ bool setup_range(const PartialParams& p, const CUtens
       const int b = base + tid;
       int pages = 0;
       if (b < p.batch) {
-        const int ctx = __ldg(&p.context_lens[b]);
+        const int ctx = p.context_lens[b];
         if (base == 0) stamp_after(10, ctx);
         sm.ctx_cache[b] = ctx;
         pages = (ctx < 0 || (long long)ctx > max_ctx) ? 0 : (ctx + kBlockSize - 1) / kBlockSize;
@@ -850,7 +850,7 @@ __device__ __forceinline__ bool setup_range(const PartialParams& p, const CUtens
     const long long max_ctx = (long long)p.max_blocks_per_seq * kBlockSize;
     for (int s = cta * kWarps + warp; s < nseg; s += gridDim.x * kWarps) {
       if (segs[s] != segs[s + 1]) continue;
-      const int ctx = __ldg(&p.context_lens[s / p.num_kv_heads]);
+      const int ctx = p.context_lens[s / p.num_kv_heads];
       const bool bad = ctx < 0 || (long long)ctx > max_ctx;
       const float v = bad ? __int_as_float(0x7fc00000) : 0.0f;
       if (bad && lane == 0) record_status(&sh.cta_status, XQA_ERR_CTX_TOO_LONG);
@@ -923,7 +923,7 @@ __device__ __forceinline__ bool setup_range(const PartialParams& p, const CUtens
         sm.seg_cache[i] = segs[s_first + i];
         if (i < wn) sm.cc_cache[i] = cc[s_first + i];
       }
-      for (int i = tid; i < wb; i += kThreads) sm.ctx_cache[i] = __ldg(&p.context_lens[b_first + i]);
+      for (int i = tid; i < wb; i += kThreads) sm.ctx_cache[i] = p.context_lens[b_first + i];
       __syncthreads();
       segs = sm.seg_cache - s_first;
       cc = sm.cc_cache - s_first;
@@ -1725,8 +1725,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // per-tensor scales: host values, or device scalars read when the kernel
   // runs (after the wait in setup_range, like every input)
-  const float k_scale = p.k_scale_ptr ? __ldg(p.k_scale_ptr) : p.k_scale;
-  const float v_scale = p.v_scale_ptr ? __ldg(p.v_scale_ptr) : p.v_scale;
+  const float k_scale = p.k_scale_ptr ? *p.k_scale_ptr : p.k_scale;
+  const float v_scale = p.v_scale_ptr ? *p.v_scale_ptr : p.v_scale;
   const float scale_log2 = static_cast<float>(p.qk_scale_base * static_cast<double>(k_scale));
   const uint64_t policy = l2_evict_first_policy();
 
@@ -1769,8 +1769,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     publish_status(p, sh);
     return;
   }
-  const float k_scale = p.k_scale_ptr ? __ldg(p.k_scale_ptr) : p.k_scale;
-  const float v_scale = p.v_scale_ptr ? __ldg(p.v_scale_ptr) : p.v_scale;
+  const float k_scale = p.k_scale_ptr ? *p.k_scale_ptr : p.k_scale;
+  const float v_scale = p.v_scale_ptr ? *p.v_scale_ptr : p.v_scale;
   const float scale_log2 = static_cast<float>(p.qk_scale_base * static_cast<double>(k_scale));
   const uint64_t policy = l2_evict_first_policy();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1844,7 +1844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane < len) {
           const int bb = sg / p.num_kv_heads, kvh = sg - bb * p.num_kv_heads;
           const int id =
-              __ldg(&p.block_tables[(size_t)bb * p.max_blocks_per_seq + (pb + lane - segs[sg])]);
+              p.block_tables[(size_t)bb * p.max_blocks_per_seq + (pb + lane - segs[sg])];
           r.bad = (id < 0 || id >= p.num_blocks) ? 1 : 0;
           r.y = r.bad ? 0
                       : (p.kv_layout == XQA_LAYOUT_HND ? (id * p.num_kv_heads + kvh) : id) * kBlockSize;

@@ -1,8 +1,10 @@
-"""Gather, append and gather again behind one another in one stream: each call sees what the
-one before it wrote, although its threads may be resident while earlier calls still run."""
+"""Calls behind one another in one stream (gather, append and gather again; decode on the rows
+of the decode before): each call sees what the one before it wrote, although its threads may
+be resident while earlier calls still run."""
 import pytest
 import torch
 
+import paged_fp8_kv_gqa_gb300 as xqa
 from test_gpu_rows import FORMATS, Rows
 
 pytestmark = pytest.mark.gpu
@@ -64,3 +66,26 @@ def test_a_row_that_was_gathered_is_appended():
         y.append(0.5, 0.5)
     b.gather(530, 0.5, 0.5, k=rows[0], v=rows[1])
     assert torch.equal(rows[0], want[0]) and torch.equal(rows[1], want[1])
+
+
+@pytest.mark.parametrize("kv_dtype", ["e5m2", "e2m1"])
+@pytest.mark.parametrize("ctx", [[20], [300, 17, 1000]])
+def test_decode_reads_the_rows_of_the_decode_before(ctx, kv_dtype):
+    r = Rows(ctx, ctx, 2, kv_dtype, "hnd", seed=4)
+    r.append()
+    q = torch.randn(len(ctx), 8, 128, device="cuda").half()
+    shape = xqa.make_shape(q, r.kc, r.bt, kv_dtype=kv_dtype)
+    ws = xqa.alloc_workspace(shape)
+
+    def run(wait):
+        a, b = q.clone(), torch.empty_like(q)
+        for _ in range(10):
+            xqa.xqa_decode(a, r.kc, r.vc, r.bt, r.lens, 1.0, 1.0, out=b, workspace=ws, shape=shape)
+            wait()
+            a, b = b, a
+        torch.cuda.synchronize()
+        return a
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(3):
+        assert torch.equal(run(lambda: None), want)
