@@ -178,7 +178,7 @@ def _check(code: int, where: str) -> None:
 def _stream_handle(stream) -> int:
     if stream is None:  # torch.cuda.current_stream() without the Stream object
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    return int(stream.cuda_stream)
+    return _device_stream(stream)[1]
 
 
 def _cuda(t: torch.Tensor, dtype, name: str) -> int:
@@ -237,28 +237,63 @@ def alloc_workspace(shape: XqaShape, device=None) -> torch.Tensor:
     return torch.zeros(xqa_workspace_size(shape), dtype=torch.uint8, device=device or "cuda")
 
 
-def _decode_args(q, k_cache, v_cache, block_tables, context_lens, out, workspace, shape):
+@functools.lru_cache(maxsize=1024)
+def _decode_fits(shape: bytes, q, k_cache, v_cache, block_tables, n_lens: int, n_out) -> bool:
+    """Raises unless tensors of these shapes are what the descriptor says (n_out: elements of
+    out, None if it is like q)."""
+    s = XqaShape.from_buffer_copy(shape)
+    if s.kv_dtype == KV_DTYPES["e2m1"]:
+        page = (s.num_kv_heads, E2M1_SLICE_BYTES)
+    elif s.kv_layout == KV_LAYOUTS["nhd"]:
+        page = (s.block_size, s.num_kv_heads, s.head_dim)
+    else:
+        page = (s.num_kv_heads, s.block_size, s.head_dim)
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if c[1:] != page or c[0] < s.num_blocks:
+            raise ValueError(f"{name} is {tuple(c)}, the shape descriptor says {(s.num_blocks, *page)}")
+    n = s.batch * max(s.q_len, 1) * s.num_q_heads * s.head_dim
+    if q[-2:] != (s.num_q_heads, s.head_dim) or q.numel() != n or n_out not in (n, None):
+        raise ValueError("q or out does not match the shape descriptor")
+    if len(block_tables) != 2 or block_tables[0] < s.batch or block_tables[1] != s.max_blocks_per_seq:
+        raise ValueError("block_tables does not match the shape descriptor")
+    if n_lens < s.batch:
+        raise ValueError("context_lens has fewer entries than sequences")
+    return True
+
+
+def _decode_args(q, k_cache, v_cache, block_tables, context_lens, out, workspace, shape,
+                 static=False, fresh=False):
+    """Pointers of a decode call's tensors, checked (static: a call without a workspace;
+    fresh: out was allocated like q just now)."""
     try:  # the usual call, without a function call for each tensor
-        if (q.dtype is _F16 and q.is_cuda and q.is_contiguous()
-                and k_cache.dtype is _U8 and k_cache.is_cuda and k_cache.is_contiguous()
-                and v_cache.dtype is _U8 and v_cache.is_cuda and v_cache.is_contiguous()
-                and block_tables.dtype is _I32 and block_tables.is_cuda and block_tables.is_contiguous()
-                and context_lens.dtype is _I32 and context_lens.is_cuda and context_lens.is_contiguous()
-                and out.dtype is _F16 and out.is_cuda and out.is_contiguous()
-                and workspace.dtype is _U8 and workspace.is_cuda and workspace.is_contiguous()):
+        dev = q.get_device()
+        if (dev >= 0 and q.dtype is _F16 and q.is_contiguous()
+                and k_cache.dtype is _U8 and k_cache.get_device() == dev and k_cache.is_contiguous()
+                and v_cache.dtype is _U8 and v_cache.get_device() == dev and v_cache.is_contiguous()
+                and block_tables.dtype is _I32 and block_tables.get_device() == dev
+                and block_tables.is_contiguous()
+                and context_lens.dtype is _I32 and context_lens.get_device() == dev
+                and context_lens.is_contiguous()
+                and (fresh or (out.dtype is _F16 and out.get_device() == dev and out.is_contiguous()))
+                and (static or (workspace.dtype is _U8 and workspace.get_device() == dev
+                                and workspace.is_contiguous()))
+                and torch._C._cuda_getDevice() == dev
+                and _decode_fits(bytes(shape), q.shape, k_cache.shape, v_cache.shape,
+                                 block_tables.shape, context_lens.numel(),
+                                 None if fresh else out.numel())):
             return (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-                    context_lens.data_ptr(), out.data_ptr(), workspace.data_ptr())
+                    context_lens.data_ptr(), out.data_ptr(), None if static else workspace.data_ptr())
     except AttributeError:
         pass
-    return (  # raises with the reason
-        _cuda(q, torch.float16, "q"),
-        _cuda(k_cache, torch.uint8, "k_cache"),
-        _cuda(v_cache, torch.uint8, "v_cache"),
-        _cuda(block_tables, torch.int32, "block_tables"),
-        _cuda(context_lens, torch.int32, "context_lens"),
-        _cuda(out, torch.float16, "out"),
-        _cuda(workspace, torch.uint8, "workspace"),
-    )
+    named = [(q, _F16, "q"), (k_cache, _U8, "k_cache"), (v_cache, _U8, "v_cache"),
+             (block_tables, _I32, "block_tables"), (context_lens, _I32, "context_lens"),
+             (out, _F16, "out")] + [(workspace, _U8, "workspace")] * (not static)
+    for t, dtype, name in named:  # the reason; CPU tensors before CUDA is asked
+        _cuda(t, dtype, name)
+    dev = torch.cuda.current_device()
+    for t, dtype, name in named:
+        _on(t, dtype, dev, name)
+    raise ValueError("invalid arguments")
 
 
 def xqa_decode(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale,
@@ -273,7 +308,8 @@ def xqa_decode(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale
     if shape is None:
         shape = make_shape(q, k_cache, block_tables, sm_scale, max_ctas, min_pages_per_cta,
                            kv_dtype=kv_dtype, kv_layout=kv_layout)
-    if out is None and workspace is not None and stream is None:
+    fresh = out is None
+    if fresh and workspace is not None and stream is None:
         out = torch.empty_like(q)
     elif out is None or workspace is None:
         with _allocating(stream):
@@ -281,22 +317,30 @@ def xqa_decode(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale
                 out = torch.empty_like(q)
             if workspace is None:
                 workspace = alloc_workspace(shape, q.device)
-    a = _decode_args(q, k_cache, v_cache, block_tables, context_lens, out, workspace, shape)
+    a = _decode_args(q, k_cache, v_cache, block_tables, context_lens, out, workspace, shape,
+                     fresh=fresh)
     lib = load_library()
-    if isinstance(k_scale, torch.Tensor) or isinstance(v_scale, torch.Tensor):
-        ks = _cuda(k_scale, torch.float32, "k_scale")
-        vs = _cuda(v_scale, torch.float32, "v_scale")
+    # the tensors are on the current device
+    handle = (torch._C._cuda_getCurrentRawStream(q.get_device()) if stream is None
+              else _stream_handle(stream))
+    if not (type(k_scale) is type(v_scale) is float) and (
+            isinstance(k_scale, torch.Tensor) or isinstance(v_scale, torch.Tensor)):
+        ks, vs = (_on(x, torch.float32, q.get_device(), name)
+                  for x, name in ((k_scale, "k_scale"), (v_scale, "v_scale")))
         _check(lib.xqa_decode_device_scales(a[0], a[1], a[2], a[3], a[4], ks, vs, a[5],
                                             ctypes.byref(shape), a[6], workspace.numel(),
-                                            _stream_handle(stream)), "xqa_decode_device_scales")
+                                            handle), "xqa_decode_device_scales")
         return out
-    _check(lib.xqa_decode(a[0], a[1], a[2], a[3], a[4], float(k_scale), float(v_scale), a[5],
-                          ctypes.byref(shape), a[6], workspace.numel(), _stream_handle(stream)),
-           "xqa_decode")
+    code = lib.xqa_decode(a[0], a[1], a[2], a[3], a[4], float(k_scale), float(v_scale), a[5],
+                          ctypes.byref(shape), a[6], workspace.numel(), handle)
+    if code:
+        raise XqaError(code, "xqa_decode")
     return out
 
 
 def xqa_plan(context_lens, workspace, shape: XqaShape, stream=None) -> None:
+    if context_lens.numel() < shape.batch:
+        raise ValueError("context_lens has fewer entries than sequences")
     _check(load_library().xqa_plan(_cuda(context_lens, torch.int32, "context_lens"),
                                    ctypes.byref(shape), _cuda(workspace, torch.uint8, "workspace"),
                                    workspace.numel(), _stream_handle(stream)), "xqa_plan")
@@ -312,6 +356,8 @@ def xqa_attend_partial(q, k_cache, v_cache, block_tables, context_lens, k_scale,
 
 
 def xqa_combine(context_lens, v_scale, out, workspace, shape: XqaShape, stream=None) -> None:
+    if out.numel() != shape.batch * max(shape.q_len, 1) * shape.num_q_heads * shape.head_dim:
+        raise ValueError("out does not match the shape descriptor")
     _check(load_library().xqa_combine(_cuda(context_lens, torch.int32, "context_lens"),
                                       float(v_scale), _cuda(out, torch.float16, "out"),
                                       ctypes.byref(shape),
@@ -689,14 +735,8 @@ def xqa_decode_static_workspace(q, k_cache, v_cache, block_tables, context_lens,
                            merge_mode, kv_dtype=kv_dtype, kv_layout=kv_layout)
     if out is None:
         out = torch.empty_like(q)
-    ptrs = (
-        _cuda(q, torch.float16, "q"),
-        _cuda(k_cache, torch.uint8, "k_cache"),
-        _cuda(v_cache, torch.uint8, "v_cache"),
-        _cuda(block_tables, torch.int32, "block_tables"),
-        _cuda(context_lens, torch.int32, "context_lens"),
-        _cuda(out, torch.float16, "out"),
-    )
+    ptrs = _decode_args(q, k_cache, v_cache, block_tables, context_lens, out, None, shape,
+                        static=True)
     _check(load_library().xqa_decode_static_workspace(
         ptrs[0], ptrs[1], ptrs[2], ptrs[3], ptrs[4], float(k_scale), float(v_scale), ptrs[5],
         ctypes.byref(shape), _stream_handle(stream)), "xqa_decode_static_workspace")
