@@ -292,13 +292,16 @@ xqa_status_t combine_impl(const int32_t* context_lens, float v_scale, const floa
   return e == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
 }
 
+// Offsets of n rows or heads, and the sums of two such, in 64 bits of bytes.
+bool offsets_fit(long long n, long long stride) { return stride <= (1ll << 60) / (n > 1 ? n : 1); }
+
 // Row / head stride of one side of xqa_append / xqa_gather (0: contiguous).
 bool row_strides(const xqa_rows_t& s, int64_t row, int64_t head, bool written, long long* rs,
                  long long* hs) {
   *hs = head != 0 ? head : kHeadDim;
   *rs = row != 0 ? row : (long long)s.num_kv_heads * kHeadDim;
   if (*hs < 0 || *rs < 0 || *hs % 8 != 0 || *rs % 8 != 0) return false;
-  if (*rs >= (1ll << 40) || *hs >= (1ll << 40)) return false;  // 64-bit offsets of 2^31 rows
+  if (!offsets_fit(s.num_rows, *rs) || !offsets_fit(s.num_kv_heads, *hs)) return false;
   if (!written) return true;
   // heads and rows that are written must not overlap one another
   if ((s.num_kv_heads > 1 && *hs < kHeadDim) || (s.num_rows > 1 && *rs < kHeadDim)) return false;
@@ -324,6 +327,7 @@ bool prefill_side(int rows, int heads, int64_t row, int64_t head, bool written, 
   if (rows <= 1) s->rs = (long long)heads * kHeadDim;
   if (s->hs < 0 || s->rs < 0 || s->hs % 8 != 0 || s->rs % 8 != 0) return false;
   if (s->rs >= (1ll << 38) || s->hs >= (1ll << 38) / heads) return false;  // tensor map: 2^40 bytes
+  if (!offsets_fit(rows, s->rs)) return false;
   if (!written) return true;
   if ((heads > 1 && s->hs < kHeadDim) || (rows > 1 && s->rs < kHeadDim)) return false;
   return s->rs >= (heads - 1) * s->hs + kHeadDim ||
