@@ -67,7 +67,10 @@ constexpr float kExactMax = 4194304.f;  // 2^22: half a step of smaller m is at 
 constexpr float kLazyMax = 8.0f;                 // log2 units
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kMaxPieces = kPrefillMaxPieces;
-constexpr uint32_t kWaitClocks = 2000000000u;    // about 1 s
+// Limit of a wait: about 1 s in units of 2^16 clocks. A role may have to wait for a whole
+// unit, so a unit of many tiles raises it by as much for every 2^16 of them (0.09 s of work
+// at 1.3 us a tile).
+constexpr uint32_t kWaitLimit = 2000000000u >> 16;
 constexpr int kUnitReaders = 15;  // 8 softmax, 4 epilogue, 1 tensor-core, 2 V warps
 
 // One unit of work, written by the loading warp.
@@ -97,7 +100,8 @@ struct Shared {
   uint64_t drain;
   Unit unit[kUnitSlots];
   int not_finite[kUnitSlots];    // the unit's masked V tiles held infinities or NaN
-  int abort_flag, status;
+  int status;
+  uint32_t wait_limit;           // of every wait; 0: the CTA is aborted
   int joins;                     // this CTA's piece was the last: 1, or -1 if one failed
   uint32_t tmem;
 };
@@ -245,17 +249,20 @@ struct Ctx {
 
   __device__ __forceinline__ uint8_t* kv(int stage) const { return tiles + (2 + stage) * kTileBytes; }
 
-  // Warp-uniform wait, for about a second at most; false ends the role (the CTA is
-  // aborted). Short: the roles wait in many places and share an instruction cache.
+  // Warp-uniform wait within the CTA's limit; false ends the role (the CTA is aborted).
+  // Short: the roles wait in many places and share an instruction cache.
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
     if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
-    volatile int* abort = &sh.abort_flag;
-    const uint32_t t0 = (uint32_t)clock();
+    volatile uint32_t* limit = &sh.wait_limit;
+    const uint32_t t0 = (uint32_t)(clock64() >> 16);
     do {
       if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
-    } while (__all_sync(kAll, !*abort && (uint32_t)clock() - t0 < kWaitClocks));
-    *abort = 1;
+    } while (__all_sync(kAll, (uint32_t)(clock64() >> 16) - t0 < *limit));
+    *limit = 0;
     return false;
+  }
+  __device__ __forceinline__ bool aborted() const {
+    return *(volatile uint32_t*)&sh.wait_limit == 0;
   }
   __device__ __forceinline__ bool get_unit(int i, Unit& u) const {
     const int slot = i % kUnitSlots;
@@ -364,6 +371,11 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
     if (lane == 0) {
       sh.unit[slot] = w;
       sh.not_finite[slot] = 0;
+      if (const uint32_t more = max(w.n[0], w.n[1]) >> 16) {  // (an abort stays one)
+        const uint32_t limit = *(volatile uint32_t*)&sh.wait_limit;
+        if (limit != 0 && limit < (1 + more) * kWaitLimit)
+          atomicCAS(&sh.wait_limit, limit, (1 + more) * kWaitLimit);
+      }
       mbar_arrive(&sh.unit_full[slot]);
       if (w.bad) record_status(&sh.status, XQA_ERR_BAD_OFFSETS);
       next = gridDim.x + atomicAdd(p.counters, 1);
@@ -460,7 +472,7 @@ __device__ __forceinline__ void tensor_role(const Ctx& c) {
       }
       if (j == 0) {
         more = next_unit();
-        if (!more && *(volatile int*)&sh.abort_flag) return;
+        if (!more && c.aborted()) return;
       }
       sk = sv + 1 == kKvStages ? 0 : sv + 1;
       pk = sk == 0 ? pv ^ 1 : pv;
@@ -881,7 +893,7 @@ __device__ __forceinline__ void join_pieces(const Ctx& c) {
   if (u.end) return;  // no piece
   const int unit = u.slot / p.pieces;
   if (threadIdx.x == 0) {
-    const bool failed = *(volatile int*)&sh.abort_flag != 0;
+    const bool failed = c.aborted();
     __threadfence();
     const int old = atom_add_acq_rel_gpu(p.tickets + unit, failed ? 1 + kTicketPoison : 1);
     const bool last = (old & kTicketCountMask) == p.pieces - 1;
@@ -985,7 +997,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     }
     mbar_init(&sh.drain, 1);
     sh.unit[0].end = 1;  // until there is one
-    sh.abort_flag = 0;
+    sh.wait_limit = kWaitLimit;
     sh.status = aligned ? XQA_OK : XQA_ERR_LAUNCH;
     fence_mbar_init();
   }
@@ -1036,7 +1048,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       if (elect_one()) tc_commit(&sh.drain);
       __syncwarp();
       ok = mbar_wait_bounded(&sh.drain, 0, &never);
-    } else if (*(volatile int*)&sh.abort_flag) {
+    } else if (*(volatile uint32_t*)&sh.wait_limit == 0) {
       for (int k = max(0, kv_issued - kKvStages); k < kv_issued; ++k)
         ok = mbar_wait_bounded(&sh.kv_full[k % kKvStages], (k / kKvStages) & 1, &never) && ok;
       for (int s = 0; s < 2; ++s)
@@ -1051,7 +1063,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   tc_fence_after();
   if (warp == 12) tmem_dealloc(sh.tmem, 512);
   if (threadIdx.x == 0) {
-    if (sh.abort_flag) record_status(&sh.status, XQA_ERR_DEVICE_TIMEOUT);
+    if (sh.wait_limit == 0) record_status(&sh.status, XQA_ERR_DEVICE_TIMEOUT);
     p.status[blockIdx.x] = sh.status;
     if (blockIdx.x == 0) p.header[0] = gridDim.x;
     // the last CTA leaves the counters at zero for the next call

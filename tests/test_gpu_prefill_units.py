@@ -95,3 +95,24 @@ def test_infinities_in_a_piece_of_little_weight(val, causal):
     want, _, _ = plain(c.q, c.k, c.v, c.lq, c.lk, causal)
     assert int((~torch.isfinite(want)).sum()) == 8 * (1 if causal else 2)
     same_specials(out, want)
+
+
+def test_a_unit_that_takes_longer_than_a_wait():
+    # 2^27 keys (34 GB) for one CTA, 1.4 s of work: every role waits for as long as the others
+    # get on. Equal weights, 2^20 values of 1: the sums are
+    # exact, out is rounded twice (32 bits, then fp16)
+    n = 2**27
+    k = torch.zeros(n, 1, 128, dtype=torch.float16, device="cuda")
+    k[2**26:2**26 + 2**20] = 1.0
+    q = torch.zeros(3, 2, 128, dtype=torch.float16, device="cuda")
+    cq, ck = (torch.tensor([0, x], dtype=torch.int32, device="cuda") for x in (3, n))
+    shape = xqa.make_prefill_shape(q, k, k, cq, causal=False, max_ctas=1)
+    ws = xqa.alloc_prefill_workspace(shape)
+    out, lse = torch.zeros_like(q), torch.zeros(3, 2, device="cuda")
+    xqa.xqa_prefill(q, k, k, cq, ck, out=out, lse=lse, workspace=ws, shape=shape)
+    status = xqa.xqa_read_status(ws)
+    del k
+    torch.cuda.empty_cache()
+    assert status == xqa.XQA_OK
+    assert float((out.double() * n / 2**20 - 1).abs().max()) <= 2.0**-11 + 2.0**-22
+    assert float((lse.double() - math.log(n)).abs().max()) <= 2.0**-18 * (1 + math.log(n))
