@@ -326,8 +326,9 @@ xqa_status_t xqa_prefill_workspace_size(const xqa_prefill_shape_t* shape, size_t
  * shape->dtype for the second product, out is rounded once. What a query does not see
  * does not reach its row, infinities and NaN included. Rows of q and out behind
  * cu_seqlens_q[B] are left alone. A sequence whose offsets are bad
- * (XQA_ERR_BAD_OFFSETS, see xqa_read_status) is skipped; if only its key offsets are,
- * its rows are NaN. One kernel, no host synchronisation; may be captured into a CUDA
+ * (XQA_ERR_BAD_OFFSETS, see xqa_read_status) is skipped, and where offsets descend so
+ * that sequences overlap, some behind them may be; if only its key offsets are bad, its
+ * rows are NaN. One kernel, no host synchronisation; may be captured into a CUDA
  * graph. */
 xqa_status_t xqa_prefill(const void* q, const void* k, const void* v, const int32_t* cu_seqlens_q,
                          const int32_t* cu_seqlens_k, void* out, float* lse,

@@ -319,8 +319,9 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
     }
     const int slot = i % kUnitSlots;
     if (i >= kUnitSlots && !c.wait(&sh.unit_empty[slot], (i / kUnitSlots - 1) & 1)) return;
-    // in pieces: one a CTA (there are CTAs for all, unless offsets overlap)
-    const bool over = kCut && i > 0;
+    // Offsets that ascend have max_units units at most, and in pieces one a CTA; sequences that
+    // overlap may have any number (the call's time would grow with batch times rows).
+    const bool over = u >= p.max_units || (kCut && i > 0);
     if (base >= p.batch || over) {  // none left
       if (base < p.batch) record_status(&sh.status, XQA_ERR_BAD_OFFSETS);
       if (lane == 0) {

@@ -336,7 +336,7 @@ bool prefill_side(int rows, int heads, int64_t row, int64_t head, bool written, 
 
 struct PrefillResolved {
   Side q, k, v, out;
-  int group, ctas, pieces;
+  int group, ctas, pieces, units;
   float sm_scale;
   size_t bytes;
 };
@@ -382,6 +382,7 @@ xqa_status_t resolve_prefill(const xqa_prefill_shape_t* s, PrefillResolved* r) {
   const long long tokens = 2 * (128 / r->group);
   const long long seqs = s->batch < s->total_q ? s->batch : s->total_q;
   const long long units = (s->total_q / tokens + seqs) * s->num_kv_heads;
+  r->units = (int)units;  // <= 2^28: rows x heads < 2^27
   r->ctas = s->max_ctas;
   if (r->ctas == 0) {
     int dev = 0, sms = 0;
@@ -620,6 +621,7 @@ xqa_status_t xqa_prefill(const void* q, const void* k, const void* v, const int3
   p.piece_ml = reinterpret_cast<float2*>(base + kPrefillWorkspaceBytes +
                                          (size_t)r.ctas * 256 * kHeadDim * sizeof(float));
   p.tile_tokens = tokens;
+  p.max_units = r.units;
   p.scale_log2 = (float)((double)r.sm_scale * 1.4426950408889634);
   p.v_row_stride = r.v.rs;
   p.v_head_stride = r.v.hs;

@@ -78,6 +78,7 @@ struct PrefillParams {
   int32_t* status;    // [kMaxCtas]
   int batch, num_q_heads, num_kv_heads, group, total_q, total_k, causal;
   int tile_tokens;    // T: tokens of a 128-row tile
+  int max_units;      // of offsets that ascend
   int pieces;         // a unit's keys are cut into so many (1: not at all); with more
                       // than 1 there are at least as many CTAs as pieces of all units
   int32_t* tickets;   // pieces written, by unit: zero between calls

@@ -51,6 +51,26 @@ def test_bad_key_offsets_between_good_sequences(max_ctas):
     assert torch.equal(out, want) and xqa.xqa_read_status(c.ws) == xqa.XQA_OK
 
 
+@pytest.mark.parametrize("max_ctas", [1, 0])
+def test_offsets_that_overlap_end_with_an_error(max_ctas):
+    # 0, 200, 0, 200, ..., 240: every other sequence is the first one again; as many units as
+    # ascending offsets can have are worked off, which leaves out the last sequence
+    c = Call([200, 40], hq=8, hkv=2, seed=5)
+    want = c.run(max_ctas=max_ctas)
+    cu = (torch.arange(601, device="cuda") % 2 * 200).to(torch.int32)
+    cu[600] = 240
+    shape = xqa.make_prefill_shape(c.q, c.k, c.v, cu, max_ctas=max_ctas)
+    ws = xqa.alloc_prefill_workspace(shape)
+    for _ in range(2):
+        out = torch.full_like(want, 7.0)
+        xqa.xqa_prefill(c.q, c.k, c.v, cu, cu, out=out, workspace=ws, shape=shape)
+        assert xqa.xqa_read_status(ws) == xqa.XQA_ERR_BAD_OFFSETS
+        assert torch.equal(out[:200], want[:200]) and bool((out[200:] == 7.0).all())
+        assert not bool(ws[16:64].any())  # counters back at zero
+    xqa.xqa_prefill(c.q, c.k, c.v, c.cq, c.ck, out=out, workspace=ws)
+    assert torch.equal(out, want) and xqa.xqa_read_status(ws) == xqa.XQA_OK
+
+
 def same_specials(a, b):
     """NaN in the same places, equal infinities."""
     assert torch.equal(torch.isnan(a), torch.isnan(b))
