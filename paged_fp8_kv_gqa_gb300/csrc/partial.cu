@@ -12,9 +12,9 @@
 // (long-scoreboard stalls at low occupancy, section "Starting bottleneck"); on
 // sm_103a this kernel keeps kStages pages in flight per SM instead.
 //
-// Every one of the 8 warps (FP8; 4 bits below) both loads and computes. Warp w owns the CTA-local
-// pages w, w+8, w+16, ... and the ring slots w, w+8, w+16, w+24 they map to
-// (slot = page % kStages). It keeps kLookahead of its pages in flight: once a
+// Every one of the kWarps warps (8 with FP8 caches; 4 bits below) both loads and computes.
+// Warp w owns the CTA-local pages w, w + kWarps, w + 2 kWarps, ... and the ring slots they
+// map to (slot = page % kStages; FP8: w, w+8, w+16, w+24). It keeps kLookahead of its pages in flight: once a
 // page is in registers it issues the two TMA loads (K and V slice, 2048 B each,
 // 128-byte swizzle) of its page q + kStages into the slot just freed, so no
 // empty-slot barrier is needed and TMA issue is spread over all warps. Block ids
@@ -37,7 +37,7 @@
 //   - O^T[128 x 8] += V^T * P^T with 8 MMAs per tile (V converted once for all
 //     tiles) plus one MMA against ones for the row sums l (so l sums exactly
 //     the fp16 P used for O).
-// A warp takes its pages two at a time, interleaving two independent
+// A warp takes its pages two at a time (kPairs), interleaving two independent
 // dependency chains (two-tile kernels load Q per segment instead of
 // prefetching it, to stay within 255 registers). At the end of a segment each
 // warp hands its (m, l, O) to a shared merge buffer and moves on; the buffered
@@ -1161,7 +1161,7 @@ __device__ __forceinline__ SegLimits<NT> seg_limits(const PartialParams& p, int 
 }
 
 // Merge of one buffered segment by all threads (column col, dims dq..dq+3):
-// the 8 warps' (m, l, O) combine in shared memory; a segment owned whole is
+// the warps' (m, l, O) combine in shared memory; a segment owned whole is
 // normalised and written as fp16, a split piece goes to partial slot cta + s.
 template <class G>
 __device__ __forceinline__ void merge_buffer(const PartialParams& p, CtaShared<G>& sh,
@@ -1223,8 +1223,8 @@ __device__ __forceinline__ void merge_buffer(const PartialParams& p, CtaShared<G
   }
 }
 
-// CTA mode: warp w takes the CTA-local pages w, w + 8, w + 16, ... of the
-// range (two at a time), keeping kLookahead of them in flight; at the end of
+// CTA mode: warp w takes the CTA-local pages w, w + kWarps, w + 2 kWarps, ... of the
+// range (two at a time with kPairs), keeping kLookahead of them in flight; at the end of
 // each segment every warp hands its (m, l, O) to a merge buffer, merged across
 // warps when the buffer is next reused or at the end of the range.
 template <class G, bool kMulti>
@@ -1248,13 +1248,13 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
   const int cbeg = rv.cbeg, cend = rv.cend, npages = rv.npages;
   const int s_first = rv.s_first, s_hi = rv.s_hi;
 
-  // ---- this warp's loads: owned page k is CTA-local page warp + 8k ----
+  // ---- this warp's loads: owned page k is CTA-local page warp + kWarps * k ----
   const int owned = npages > warp ? (npages - warp + kWarps - 1) / kWarps : 0;
   stamp(14);
   PageBatch cur = load_batch<kWarps>(p, segs, s_first, s_hi + 1, cbeg, npages, warp, 0, lane);
   PageBatch nxt = load_batch<kWarps>(p, segs, s_first, s_hi + 1, cbeg, npages, warp, 32, lane);
   stamp_after(11, cur.y ^ nxt.y);
-  // this warp's first pair, for the next call's prefetch
+  // this warp's first two pages, for the next call's prefetch (of 16 warps, the first 8's)
   if (p.hints != nullptr && lane < 2 && (kWarps <= kHintPages / 2 || warp < kHintPages / 2)) {
     const int row = p.kv_layout == XQA_LAYOUT_HND
                         ? cur.y
@@ -1392,7 +1392,7 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
 // Merge of the rows row0, row0 + rstride, ... (< G * q_len) of a good split
 // segment too large for merge_segments, by every thread of the CTA. The
 // pieces' rows and their (m, l) words are gathered into shared memory (the
-// page ring and the merge buffers, free once the range is done) by all 256
+// page ring and the merge buffers, free once the range is done) by all
 // threads, kGatherLoads 16-byte loads in flight per thread, as many pieces per
 // batch as fit; then warp w sums the CTA's rows w and w + kWarps over the
 // pieces (lane: dims 4 * lane .. 4 * lane + 3). Each warp reads every
@@ -1743,10 +1743,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The same kernel with a second way to work a range (warp mode): when the
 // range touches at least kWarpModeMinPieces segment pieces of at most
-// kWarpModePages pages each, whole pieces go to single warps (round-robin over
-// the range's segments, a static rule), each warp accumulates its piece alone
-// and writes it from registers, with no merge across warps and no CTA barrier
-// per segment; other ranges are worked in CTA mode as above. Launched only for
+// kWarpModePages pages each (4 bits: twice as many), whole pieces go to single
+// warps, in 4 bits to two neighbouring ones (round-robin over the range's
+// segments, a static rule). Each warp or pair of them accumulates its piece
+// alone and writes it from registers, with no merge beyond that and no CTA
+// barrier per segment; other ranges are worked in CTA mode as above. Launched only for
 // shapes with many segments per CTA (batches of many short sequences): the
 // mode test and the warp-mode code slow the page loop of CTA-mode ranges.
 template <int kFmt, int NT, bool kMulti, int kThreads = PartialGeom<kFmt, NT>::kThreads>
@@ -1787,7 +1788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int kseg = 0;    // pieces handed to the merge buffers
 
   // ---- mode: at least kWarpModeMinPieces pieces, none longer than
-  // kWarpModePages pages -> warp mode; otherwise CTA mode ----
+  // kWarpModePages pages (4 bits: twice as many) -> warp mode; otherwise CTA mode ----
   const int nsr = find_segment(segs, s_first, rv.s_hi + 1, cend - 1) - s_first + 1;  // segments touched
   bool warp_mode = false;
   if (nsr >= kWarpModeMinPieces && nsr <= kThreads) {
@@ -1803,8 +1804,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     cta_mode_range<G, kMulti>(p, &tm_k, &tm_v, sh, sm, rv, scale_log2, v_scale, policy, st,
                                      qf, qf_next, q_next_seg, issued, kseg);
   } else {
-    // ---- warp mode: this warp's pieces are the range's segments j = warp,
-    // warp + 8, ... (j counted from s_first; empty ones skipped). A piece's
+    // ---- warp mode: this warp's pieces are the range's segments j = team,
+    // team + kTeams, ... (j counted from s_first; empty ones skipped). A piece's
     // block ids are fetched one per lane; the next piece's when the current
     // one starts issuing. 4 bits: two neighbouring warps share a piece, half its
     // pages each (with a warp for a piece 9 of the 16 warps had none at 256 x 512).

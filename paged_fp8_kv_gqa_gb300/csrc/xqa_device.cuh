@@ -129,7 +129,7 @@ static_assert(kMaxCtas * (long long)kTicketPoison < kTicketRelease, "poison bits
 constexpr int kMergeHelpers = 8;
 static_assert(kMergeHelpers * (long long)kTicketRelease <= 0x7fffffffLL + 1, "release bits overflow");
 constexpr int kHeaderWords = 16;
-// Pages of a CTA's range (each warp's first pair) that the CTA records for the
+// Pages of a CTA's range (its first 8 warps' first two) that the CTA records for the
 // next call, as (block id * Hkv + kv head) * 16: that call's CTA of the same
 // index prefetches them into L2 while it waits for the kernels before it (a
 // hint: consecutive calls, e.g. the layers of one decode step, cut the same
