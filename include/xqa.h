@@ -288,8 +288,8 @@ typedef struct xqa_prefill_shape {
   int32_t num_q_heads;  /* Hq, a multiple of Hkv; G = Hq / Hkv <= 128 */
   int32_t num_kv_heads; /* Hkv */
   int32_t head_dim;     /* D = 128 */
-  int32_t total_q;      /* rows of q and out (>= 0) */
-  int32_t total_k;      /* rows of k and v (>= 0) */
+  int32_t total_q;      /* rows of q and out (>= 0, total_q * Hq < 2^27) */
+  int32_t total_k;      /* rows of k and v (>= 0, <= 2^31 - 512) */
   int32_t dtype;        /* XQA_F16 or XQA_BF16: q, k, v and out */
   int32_t causal;       /* 1: query i of a sequence sees keys 0 .. len_k - len_q + i
                            (the last query sees every key); 0: every key */

@@ -401,7 +401,7 @@ def _device_stream(stream):
     dev = torch.cuda.current_device()
     if stream is None:
         return dev, torch._C._cuda_getCurrentRawStream(dev)
-    if stream.device_index != dev:
+    if getattr(stream, "device_index", dev) != dev:  # (any object with a cuda_stream will do)
         raise ValueError("the stream belongs to another device than the current one")
     return dev, int(stream.cuda_stream)
 
@@ -641,7 +641,10 @@ def xqa_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=None, lse=None, wo
     of a sequence sees all its keys and each one before it one key less. ``lse``
     (fp32 [total_q, Hq], optional) receives the log-sum-exp. Returns ``out``;
     rows that see nothing are zero, rows behind the last sequence are not
-    written."""
+    written. Errors that only the device sees (bad offsets, a wait that ran out)
+    are in the workspace: pass one and call xqa_read_status on it to learn of
+    them. Without ``workspace`` the call allocates one and drops it, status
+    included."""
     if shape is None:
         shape = make_prefill_shape(q, k, v, cu_seqlens_q, causal, sm_scale, max_ctas, out)
     if cu_seqlens_k is None:

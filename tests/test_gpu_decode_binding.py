@@ -42,3 +42,22 @@ def test_refusals(kv_dtype):
     xqa.xqa_decode(**{**good, "context_lens": torch.cat([lens, lens]), "block_tables": torch.cat([bt, bt])}, workspace=ws)
     torch.cuda.synchronize()
     assert bool((out == 0.0).all()) and xqa.xqa_read_status(ws) == xqa.XQA_OK
+
+
+def test_any_object_with_a_stream_handle():
+    class Handle:
+        def __init__(self, s):
+            self.cuda_stream = s.cuda_stream
+
+    q = torch.randn(1, 8, 128, device="cuda").half()
+    k = torch.randint(0, 100, (3, 2, 16, 128), dtype=torch.uint8, device="cuda")
+    bt = torch.arange(3, dtype=torch.int32, device="cuda").view(1, 3)
+    lens = torch.tensor([40], dtype=torch.int32, device="cuda")
+    shape = xqa.make_shape(q, k, bt)
+    ws, out = xqa.alloc_workspace(shape), torch.zeros_like(q)
+    want = xqa.xqa_decode(q, k, k, bt, lens, 1.0, 1.0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    xqa.xqa_decode(q, k, k, bt, lens, 1.0, 1.0, out=out, workspace=ws, shape=shape, stream=Handle(side))
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out, want) and xqa.xqa_read_status(ws, stream=Handle(side)) == xqa.XQA_OK
