@@ -26,7 +26,7 @@
 // weight, the size of the rounding of out itself.
 //
 // Measured (32/4 heads): 1 x 16384 tokens bf16 1.39 ms, 1580 TFLOP/s of visible pairs,
-// 0.83 of a library product's rate; 16 prompts of 190 to 2048 tokens fp16 164 us, 0.62:
+// 0.83 of a library product's rate; 16 prompts of 190 to 2048 tokens fp16 164 to 167 us, 0.61:
 // a tenth of the tiles is hidden, and a unit of 6 tiles starts and ends its two chains
 // of dependent products and softmax anew (about 2 us of its 11).
 //

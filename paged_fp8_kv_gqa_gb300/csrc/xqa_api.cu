@@ -69,7 +69,8 @@ xqa_status_t resolve(const xqa_shape_t* s, Resolved* r) {
   r->min_pages = s->min_pages_per_cta > 0 ? s->min_pages_per_cta : xqa::kDefaultMinPagesPerCta;
   // 4 bits: tables shorter than the default share of a CTA hold segments of a few pages;
   // one CTA for many of them would spend its time on segment switches (4 sequences of
-  // up to 30 tokens, 8 kv heads: 25.1 us with 16 pages, 7.8 with 2)
+  // up to 30 tokens, 8 kv heads: 25.1 us with 16 pages, 7.8 with 2). A wider table keeps
+  // the default: the lengths are on the device
   if (s->kv_dtype == XQA_KV_E2M1 && s->min_pages_per_cta == 0 && r->min_pages > r->mbs)
     r->min_pages = r->mbs;
   r->merge_mode = s->merge_mode;
