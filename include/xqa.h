@@ -115,7 +115,9 @@ typedef struct xqa_shape {
                                  context_lens count the T new tokens (their K/V
                                  already in the cache) and new token i attends
                                  causally to tokens 0 .. ctx_b - T + i (none if
-                                 negative: a zero row) */
+                                 negative: a zero row). 8-bit formats: values of the
+                                 new tokens are to be finite (one that is not reaches
+                                 the new tokens before it too) */
 } xqa_shape_t;
 
 /* Bytes of device workspace xqa_decode needs for `shape` on the current

@@ -285,14 +285,9 @@ def _decode_args(q, k_cache, v_cache, block_tables, context_lens, out, workspace
                     context_lens.data_ptr(), out.data_ptr(), None if static else workspace.data_ptr())
     except AttributeError:
         pass
-    named = [(q, _F16, "q"), (k_cache, _U8, "k_cache"), (v_cache, _U8, "v_cache"),
-             (block_tables, _I32, "block_tables"), (context_lens, _I32, "context_lens"),
-             (out, _F16, "out")] + [(workspace, _U8, "workspace")] * (not static)
-    for t, dtype, name in named:  # the reason; CPU tensors before CUDA is asked
-        _cuda(t, dtype, name)
-    dev = torch.cuda.current_device()
-    for t, dtype, name in named:
-        _on(t, dtype, dev, name)
+    _on_current((q, _F16, "q"), (k_cache, _U8, "k_cache"), (v_cache, _U8, "v_cache"),  # the reason
+                (block_tables, _I32, "block_tables"), (context_lens, _I32, "context_lens"),
+                (out, _F16, "out"), *([] if static else [(workspace, _U8, "workspace")]))
     raise ValueError("invalid arguments")
 
 
@@ -338,12 +333,20 @@ def xqa_decode(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale
     return out
 
 
+def _on_current(*named) -> list:
+    """Pointers of (tensor, dtype, name) on the current device."""
+    for t, dtype, name in named:  # CPU tensors before CUDA is asked
+        _cuda(t, dtype, name)
+    dev = torch.cuda.current_device()
+    return [_on(t, dtype, dev, name) for t, dtype, name in named]
+
+
 def xqa_plan(context_lens, workspace, shape: XqaShape, stream=None) -> None:
+    lens, ws = _on_current((context_lens, _I32, "context_lens"), (workspace, _U8, "workspace"))
     if context_lens.numel() < shape.batch:
         raise ValueError("context_lens has fewer entries than sequences")
-    _check(load_library().xqa_plan(_cuda(context_lens, torch.int32, "context_lens"),
-                                   ctypes.byref(shape), _cuda(workspace, torch.uint8, "workspace"),
-                                   workspace.numel(), _stream_handle(stream)), "xqa_plan")
+    _check(load_library().xqa_plan(lens, ctypes.byref(shape), ws, workspace.numel(),
+                                   _stream_handle(stream)), "xqa_plan")
 
 
 def xqa_attend_partial(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, out,
@@ -356,12 +359,11 @@ def xqa_attend_partial(q, k_cache, v_cache, block_tables, context_lens, k_scale,
 
 
 def xqa_combine(context_lens, v_scale, out, workspace, shape: XqaShape, stream=None) -> None:
+    o, lens, ws = _on_current((out, _F16, "out"), (context_lens, _I32, "context_lens"),
+                              (workspace, _U8, "workspace"))
     if out.numel() != shape.batch * max(shape.q_len, 1) * shape.num_q_heads * shape.head_dim:
         raise ValueError("out does not match the shape descriptor")
-    _check(load_library().xqa_combine(_cuda(context_lens, torch.int32, "context_lens"),
-                                      float(v_scale), _cuda(out, torch.float16, "out"),
-                                      ctypes.byref(shape),
-                                      _cuda(workspace, torch.uint8, "workspace"),
+    _check(load_library().xqa_combine(lens, float(v_scale), o, ctypes.byref(shape), ws,
                                       workspace.numel(), _stream_handle(stream)), "xqa_combine")
 
 

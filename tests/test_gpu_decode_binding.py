@@ -34,8 +34,11 @@ def test_refusals(kv_dtype):
                 xqa.xqa_decode(**{**a, "shape": xqa.make_shape(q, k, bt, kv_dtype=kv_dtype)})
     with pytest.raises(ValueError):
         xqa.xqa_attend_partial(**good, workspace=None)
-    with pytest.raises(ValueError):
-        xqa.xqa_plan(lens[:1], ws, shape)
+    for call in (lambda: xqa.xqa_plan(lens[:1], ws, shape), lambda: xqa.xqa_plan(None, ws, shape),
+                 lambda: xqa.xqa_combine(lens, 1.0, out[:1], ws, shape),
+                 lambda: xqa.xqa_combine(lens, 1.0, None, ws, shape)):
+        with pytest.raises(ValueError):
+            call()
     torch.cuda.synchronize()
     assert bool((out == 3.0).all())
     xqa.xqa_decode(**good, workspace=ws)
