@@ -131,8 +131,8 @@ def _lengths(case):
         return _ints(4, n, case["min_new"], case["max_new"]), _ints(5, n, 0, case["max_ctx"])
     if case["op"] == "release":
         return [0] * n, _ints(6, n, 0, case["max_ctx"])
-    return (_ints(1, n, case["min_new"], case["max_new"]),
-            _ints(2, n, case["min_ctx"], case["max_ctx"]))
+    new = _ints(1, n, case["min_new"], case["max_new"])
+    return new, [max(a, b) for a, b in zip(new, _ints(2, n, case["min_ctx"], case["max_ctx"]))]
 
 
 def _ending(case):
