@@ -44,19 +44,15 @@
 // the sequence are zeroed in shared memory, and values that are not finite are
 // zeroed and their rows' sums patched in the epilogue (only for tokens that see
 // them). A hidden key only makes its own column of S, which is replaced.
-#include <cuda_bf16.h>
 #include <math.h>
 
-#include "xqa_device.cuh"
+#include "xqa_tcgen05.cuh"
 #include "xqa_launch.h"
 
 namespace xqa {
 
 namespace {
 
-constexpr int kTile = 128;                       // rows of a row tile, keys of a KV tile
-constexpr int kHalfBytes = kTile * 128;          // 128 rows x 64 dims of 16 bits
-constexpr int kTileBytes = 2 * kHalfBytes;       // a Q, K or V tile
 constexpr int kKvStages = 5;
 constexpr int kUnitSlots = 3;
 constexpr int kPrefillThreads = 512;
@@ -65,7 +61,6 @@ constexpr int kPrefillThreads = 512;
 constexpr float kNoRowMax = -3e38f;
 constexpr float kExactMax = 4194304.f;  // 2^22: half a step of smaller m is at most 1/4
 constexpr float kLazyMax = 8.0f;                 // log2 units
-constexpr unsigned kAll = 0xffffffffu;
 constexpr int kMaxPieces = kPrefillMaxPieces;
 // Limit of a wait: about 1 s in units of 2^16 clocks. A role may have to wait for a whole
 // unit, so a unit of many tiles raises it by as much for every 2^16 of them (0.09 s of work
@@ -111,133 +106,6 @@ constexpr int kSmemStats = 2 * kTile * 2 * 4;  // (m, l) of every row
 constexpr int kPrefillSmem = kSmemTiles + kSmemStats + 1024;
 static_assert(sizeof(Shared) <= 1024, "shared state");
 static_assert(kPrefillSmem <= 227 * 1024, "shared memory budget");
-
-// ---- tcgen05 ----
-__device__ __forceinline__ void tmem_alloc(uint32_t* dst, int cols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                   smem_addr(dst)),
-               "r"(cols)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t addr, int cols) {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_addr(bar))
-      : "memory");
-}
-// D (+)= A B, both operands in shared memory
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                          bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((int)add)
-      : "memory");
-}
-// D (+)= A B, A in TMEM
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                          bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((int)add)
-      : "memory");
-}
-
-#define XQA_R8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), \
-    "=r"(a[i + 4]), "=r"(a[i + 5]), "=r"(a[i + 6]), "=r"(a[i + 7])
-#define XQA_I8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), \
-    "r"(a[i + 5]), "r"(a[i + 6]), "r"(a[i + 7])
-#define XQA_LIST32                                                                            \
-  "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, " \
-  "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}"
-
-// 32 columns of this thread's TMEM lane (its row)
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 " XQA_LIST32 ", [%32];"
-               : XQA_R8(r, 0), XQA_R8(r, 8), XQA_R8(r, 16), XQA_R8(r, 24)
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], " XQA_LIST32 ";" ::XQA_I8(r, 0),
-      XQA_I8(r, 8), XQA_I8(r, 16), XQA_I8(r, 24), "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
-      "%10, %11, %12, %13, %14, %15};" ::XQA_I8(r, 0),
-      XQA_I8(r, 8), "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// Shared-memory matrix descriptors, 128-byte swizzle (layout 2), version 1.
-// K-major (Q, K): rows of 128 bytes, 8-row groups 1024 bytes apart.
-// MN-major (V, whose dims are contiguous): 64 dims x 8 tokens per group, groups
-// of 8 tokens 1024 bytes apart, the second 64 dims kHalfBytes on.
-__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-__device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)(kHalfBytes >> 4) << 16 |
-         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-// Instruction descriptor: fp32 accumulator, fp16 or bf16 operands, M = N = 128.
-template <int kType>
-__device__ __forceinline__ constexpr uint32_t instr_desc(bool b_mn_major) {
-  return 1u << 4 | (uint32_t)(kType == XQA_BF16) << 7 | (uint32_t)(kType == XQA_BF16) << 10 |
-         (uint32_t)b_mn_major << 16 | (uint32_t)(kTile >> 3) << 17 | (uint32_t)(kTile >> 4) << 24;
-}
-
-template <int kType>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if (kType == XQA_F16) return pack_half2(lo, hi);
-  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
-                                            int y, int z, int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_kv(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
-                                            int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int x, int y, int z, int w) {
-  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(z), "r"(w)
-               : "memory");
-}
 
 // What every warp role works on.
 struct Ctx {
@@ -743,24 +611,6 @@ __device__ __forceinline__ void softmax_role(const Ctx& c, int s) {
     float2* st = reinterpret_cast<float2*>(c.stats) + s * kTile + row;
     *st = make_float2(m, l);
     c.arrive(&sh.stat_full[s]);
-  }
-}
-
-// One round of a 4 x 4 transpose among four lanes, of the 16-byte units of w: lanes kBit
-// apart trade the units that differ in that bit of their number.
-template <int kBit>
-__device__ __forceinline__ void trade(uint32_t (&w)[16]) {
-  const bool up = threadIdx.x & kBit;
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    if (u & kBit) continue;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint32_t &lo = w[4 * u + e], &hi = w[4 * (u + kBit) + e];
-      const uint32_t got = __shfl_xor_sync(kAll, up ? lo : hi, kBit);
-      if (up) lo = got;
-      else hi = got;
-    }
   }
 }
 
