@@ -337,6 +337,76 @@ xqa_status_t xqa_prefill(const void* q, const void* k, const void* v, const int3
                          const xqa_prefill_shape_t* shape, void* workspace,
                          size_t workspace_bytes, void* stream);
 
+/* Problem dimensions of xqa_extend. Strides are in elements, multiples of 8 (16 bytes); 0
+ * selects the contiguous value (Hq * 128 between rows, 128 between heads), so q may be a
+ * view of a projection. */
+typedef struct xqa_extend_shape {
+  int32_t batch;              /* B: sequences, >= 1 */
+  int32_t num_q_heads;        /* Hq, a multiple of Hkv; G = Hq / Hkv <= 128 */
+  int32_t num_kv_heads;       /* Hkv */
+  int32_t head_dim;           /* D = 128 */
+  int32_t block_size;         /* BS = 16 tokens per page */
+  int32_t max_blocks_per_seq; /* MBS: row length of block_tables (<= 2^26) */
+  int32_t num_blocks;         /* NB: pages in the K (and V) pool */
+  int32_t total_q;            /* rows of q and out (>= 0, total_q * Hq < 2^27) */
+  int32_t dtype;              /* XQA_F16 or XQA_BF16: q and out */
+  int32_t kv_dtype;           /* XQA_KV_E5M2, XQA_KV_E4M3 or XQA_KV_E2M1 */
+  int32_t kv_layout;          /* XQA_LAYOUT_HND or (8-bit formats) XQA_LAYOUT_NHD */
+  int32_t causal;             /* 1: query i of a sequence's n sees its tokens 0 ..
+                                 ctx - n + i; 0: every one */
+  float sm_scale;             /* softmax scale; <= 0 selects 1/sqrt(D) */
+  int32_t max_ctas;           /* upper bound on CTAs; 0 = SM count */
+  int64_t q_row_stride, q_head_stride;
+  int64_t out_row_stride, out_head_stride;
+} xqa_extend_shape_t;
+
+/* Bytes of device workspace xqa_extend needs for `shape`. Host only. */
+xqa_status_t xqa_extend_workspace_size(const xqa_extend_shape_t* shape, size_t* bytes);
+
+/* Attention of chunks of new tokens over the paged cache: any number of new tokens for
+ * each sequence, from one to a whole prompt, their keys and values already in the cache
+ * (xqa_append), read there as they lie.
+ *
+ *   q             device, shape->dtype [total_q, Hq, 128] (strided), 16-byte aligned,
+ *                 packed by sequence
+ *   k_cache, v_cache  device, as for xqa_decode, 16-byte aligned
+ *   block_tables  device, int32 [B, MBS], as for xqa_decode
+ *   context_lens  device, int32 [B]: tokens of each sequence, the new ones counted
+ *   cu_seqlens    device, int32 [B+1], ascending: sequence b's rows of q and out (none
+ *                 for a sequence that has no part in the call)
+ *   k_scale, v_scale  per-tensor scales; k_scale_dev / v_scale_dev, when not NULL, point
+ *                 to one device float each, read when the kernel runs
+ *   out           device, [total_q, Hq, 128] (strided), 16-byte aligned
+ *   lse           device, fp32 [total_q, Hq] contiguous, or NULL: the natural logarithm of
+ *                 the row's sum of exponentials
+ *   workspace     device, >= xqa_extend_workspace_size bytes, 256-byte aligned, zero-filled
+ *                 once before its first use; every completed call leaves it ready for the
+ *                 next (a call that reports XQA_ERR_DEVICE_TIMEOUT or
+ *                 XQA_ERR_DRAIN_TIMEOUT does not). A decode or prompt workspace of at
+ *                 least that size may serve too. Concurrent calls must not share one
+ *
+ * out[i, h] = sum_t softmax_t(sm_scale * k_scale * <q[i, h], K_t>) * v_scale * V_t over
+ * the tokens that query i sees. A row that sees none (a context shorter than the new
+ * tokens) is zero, its lse -inf. Codes are taken exactly; products accumulate in 32 bits,
+ * the softmax is in 32 bits, its weights are rounded to shape->dtype for the second
+ * product, out is rounded once. What a query does not see does not reach its row,
+ * infinities and NaN included. Rows behind cu_seqlens[B] are left alone. Results do not
+ * depend on what else is in the batch beyond the order of 32-bit sums (where a long
+ * sequence is cut into pieces).
+ *
+ * Errors that only the device sees (xqa_read_status): XQA_ERR_BAD_BLOCK_ID (the rows that
+ * see a token of the page are NaN), XQA_ERR_CTX_TOO_LONG (the sequence's rows are NaN),
+ * XQA_ERR_BAD_OFFSETS (the sequence is skipped; where offsets descend so that sequences
+ * overlap beyond total_q rows, all are), XQA_ERR_VALUE (a device k_scale that is not
+ * finite or not above 0: all rows are NaN). A host scale of that kind is refused. One
+ * kernel, no host synchronisation; may be captured into a CUDA graph. */
+xqa_status_t xqa_extend(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                        const int32_t* block_tables, const int32_t* context_lens,
+                        const int32_t* cu_seqlens, float k_scale, float v_scale,
+                        const float* k_scale_dev, const float* v_scale_dev, void* out, float* lse,
+                        const xqa_extend_shape_t* shape, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
 /* Self-check of the device-side failure detection: launches one CTA whose
  * threads wait, through the same bounded mbarrier wait the attention kernel
  * uses, on a barrier that nothing ever arrives at. After budget_ns

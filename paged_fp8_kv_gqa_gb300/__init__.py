@@ -10,7 +10,8 @@ The names mirror the C ABI declared in ``include/xqa.h``:
 ``xqa_combine``, ``xqa_decode_device_scales``, ``xqa_dequant_e5m2``,
 ``xqa_dequant_e4m3``, ``xqa_read_status``, ``xqa_read_plan``, ``xqa_status_string``,
 ``xqa_decode_static_workspace``, ``xqa_kernels_per_call``, ``xqa_append``,
-``xqa_gather``, ``xqa_prefill``, ``xqa_prefill_workspace_size``.
+``xqa_gather``, ``xqa_prefill``, ``xqa_prefill_workspace_size``, ``xqa_extend``,
+``xqa_extend_workspace_size``.
 """
 from __future__ import annotations
 
@@ -57,6 +58,8 @@ EXPORTED = (
     "xqa_gather",
     "xqa_prefill",
     "xqa_prefill_workspace_size",
+    "xqa_extend",
+    "xqa_extend_workspace_size",
 )
 
 KV_DTYPES = {"e5m2": 0, "e4m3": 1, "e2m1": 4}
@@ -110,6 +113,17 @@ class XqaPrefillShape(ctypes.Structure):
         "v_head_stride", "out_row_stride", "out_head_stride")]
 
 
+class XqaExtendShape(ctypes.Structure):
+    """Mirror of ``xqa_extend_shape_t``."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "num_q_heads", "num_kv_heads", "head_dim", "block_size", "max_blocks_per_seq",
+        "num_blocks", "total_q", "dtype", "kv_dtype", "kv_layout", "causal")]
+    _fields_ += [("sm_scale", ctypes.c_float), ("max_ctas", ctypes.c_int32)]
+    _fields_ += [(n, ctypes.c_int64) for n in (
+        "q_row_stride", "q_head_stride", "out_row_stride", "out_head_stride")]
+
+
 class XqaError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = int(code)
@@ -126,6 +140,7 @@ _DIMS_AT, _CAUSAL_AT = XqaPrefillShape.num_q_heads.offset, XqaPrefillShape.causa
 _STRIDES_AT, _OUT_AT = XqaPrefillShape.q_row_stride.offset, XqaPrefillShape.out_row_stride.offset
 _ROWS = ctypes.POINTER(XqaRows)
 _PREFILL = ctypes.POINTER(XqaPrefillShape)
+_EXTEND = ctypes.POINTER(XqaExtendShape)
 _SIGS = {
     "xqa_workspace_size": [_SHAPE, ctypes.POINTER(_SZ)],
     "xqa_decode": [_P, _P, _P, _P, _P, _F, _F, _P, _SHAPE, _P, _SZ, _P],
@@ -143,6 +158,8 @@ _SIGS = {
     "xqa_kernels_per_call": [_SHAPE, ctypes.POINTER(ctypes.c_int32)],
     "xqa_prefill": [_P, _P, _P, _P, _P, _P, _P, _PREFILL, _P, _SZ, _P],
     "xqa_prefill_workspace_size": [_PREFILL, ctypes.POINTER(_SZ)],
+    "xqa_extend": [_P, _P, _P, _P, _P, _P, _F, _F, _P, _P, _P, _P, _EXTEND, _P, _SZ, _P],
+    "xqa_extend_workspace_size": [_EXTEND, ctypes.POINTER(_SZ)],
     "xqa_append": [_P, _P, _P, _P, _P, _F, _F, _P, _P, _P, _P, _ROWS, _P, _P],
     "xqa_gather": [_P, _P, _P, _P, _P, _F, _F, _P, _P, _P, _P, _ROWS, _P, _P],
 }
@@ -697,6 +714,128 @@ def xqa_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=None, lse=None, wo
         workspace.numel(), handle)
     if code:
         raise XqaError(code, "xqa_prefill")
+    return out
+
+
+def make_extend_shape(q, k_cache, block_tables, causal: bool = True, sm_scale: float = 0.0,
+                      max_ctas: int = 0, kv_dtype: str = "e5m2", kv_layout: str = "hnd",
+                      out=None) -> XqaExtendShape:
+    """Shape descriptor of xqa_extend from q [total_q, Hq, 128] (fp16 or bf16; a view whose
+    last dim is contiguous is fine), k_cache as for xqa_decode and block_tables [B, MBS].
+    It holds for every call with tensors of these shapes, types and strides (out:
+    contiguous unless given)."""
+    qs = _heads(q, "q")
+    orow, oh = (0, 0) if out is None else _heads(out, "out", q.dtype)
+    nb, hkv, bs = _cache_dims(k_cache, kv_dtype, kv_layout)
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [batch, max_blocks_per_seq]")
+    return XqaExtendShape(block_tables.shape[0], q.shape[1], hkv, q.shape[2], bs,
+                          block_tables.shape[1], nb, q.shape[0], ROW_DTYPES[q.dtype],
+                          KV_DTYPES[kv_dtype], KV_LAYOUTS[kv_layout], int(bool(causal)),
+                          float(sm_scale), int(max_ctas), *qs, orow, oh)
+
+
+def xqa_extend_workspace_size(shape: XqaExtendShape) -> int:
+    n = _SZ(0)
+    _check(load_library().xqa_extend_workspace_size(ctypes.byref(shape), ctypes.byref(n)),
+           "xqa_extend_workspace_size")
+    return int(n.value)
+
+
+def alloc_extend_workspace(shape: XqaExtendShape, device=None) -> torch.Tensor:
+    """A zero-filled uint8 device buffer of xqa_extend_workspace_size bytes; every call
+    leaves it ready for the next."""
+    return torch.zeros(xqa_extend_workspace_size(shape), dtype=torch.uint8, device=device or "cuda")
+
+
+@functools.lru_cache(maxsize=1024)
+def _extend_fits(shape: bytes, q_shape, q_stride, dtype, k_cache, v_cache, block_tables,
+                 n_lens: int, n_cu: int) -> bool:
+    """Raises unless tensors of these shapes are what the descriptor says; whether a
+    contiguous out is what it says too."""
+    s = XqaExtendShape.from_buffer_copy(shape)
+    names = {v: k for k, v in KV_DTYPES.items()}, {v: k for k, v in KV_LAYOUTS.items()}
+    rs, hs = _head_strides(q_shape, q_stride, "q")
+    if (dtype not in ROW_DTYPES or ROW_DTYPES[dtype] != s.dtype
+            or tuple(q_shape) != (s.total_q, s.num_q_heads, s.head_dim)
+            or rs != (s.q_row_stride or s.num_q_heads * 128) or hs != (s.q_head_stride or 128)):
+        raise ValueError("q does not match the shape descriptor")
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        nb, hkv, bs = _cache_shape(c, names[0][s.kv_dtype], names[1][s.kv_layout])
+        if (hkv, bs) != (s.num_kv_heads, s.block_size) or nb < s.num_blocks or c != k_cache:
+            raise ValueError(f"{name} does not match the shape descriptor")
+    if tuple(block_tables) != (s.batch, s.max_blocks_per_seq):
+        raise ValueError("block_tables does not match the shape descriptor")
+    if n_lens != s.batch or n_cu != s.batch + 1:
+        raise ValueError("context_lens must have batch entries, cu_seqlens batch + 1")
+    return s.out_row_stride in (0, s.num_q_heads * 128) and s.out_head_stride in (0, 128)
+
+
+def xqa_extend(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, k_scale, v_scale,
+               out=None, lse=None, workspace=None, shape: XqaExtendShape | None = None, stream=None,
+               causal: bool = True, sm_scale: float = 0.0, max_ctas: int = 0,
+               kv_dtype: str = "e5m2", kv_layout: str = "hnd"):
+    """Attention of chunks of new tokens over the paged cache. q: fp16 or bf16 [total_q, Hq,
+    128], packed by sequence through cu_seqlens int32 [B+1]; the chunk's own keys and values
+    are in the cache already (xqa_append), and context_lens int32 [B] counts them. Query i
+    of a sequence's n sees its tokens 0 .. context_len - n + i (all of them without
+    ``causal``). Caches, block_tables and scales as for xqa_decode. ``lse`` (fp32 [total_q,
+    Hq], optional) receives the log-sum-exp. Returns ``out``; rows that see nothing are
+    zero, rows behind the last sequence are not written. Errors that only the device sees
+    are in the workspace (xqa_read_status); without ``workspace`` the call allocates one
+    and drops it, status included."""
+    if shape is None:
+        shape = make_extend_shape(q, k_cache, block_tables, causal, sm_scale, max_ctas, kv_dtype,
+                                  kv_layout, out)
+    plain_out = None
+    try:  # the usual call, without a function call for each tensor
+        dev, dtype = q.get_device(), q.dtype
+        if (dev >= 0 and k_cache.dtype is _U8 and k_cache.get_device() == dev and k_cache.is_contiguous()
+                and v_cache.dtype is _U8 and v_cache.get_device() == dev and v_cache.is_contiguous()
+                and block_tables.dtype is _I32 and block_tables.get_device() == dev
+                and block_tables.is_contiguous()
+                and context_lens.dtype is _I32 and context_lens.get_device() == dev
+                and context_lens.is_contiguous()
+                and cu_seqlens.dtype is _I32 and cu_seqlens.get_device() == dev
+                and cu_seqlens.is_contiguous() and torch._C._cuda_getDevice() == dev):
+            plain_out = _extend_fits(bytes(shape), q.shape, q.stride(), dtype, k_cache.shape,
+                                     v_cache.shape, block_tables.shape, context_lens.numel(),
+                                     cu_seqlens.numel())
+    except AttributeError:
+        pass
+    if plain_out is None:
+        _heads(q, "q")
+        _on_current((k_cache, _U8, "k_cache"), (v_cache, _U8, "v_cache"),
+                    (block_tables, _I32, "block_tables"), (context_lens, _I32, "context_lens"),
+                    (cu_seqlens, _I32, "cu_seqlens"))
+        raise ValueError("q must be on the current device")
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _device_stream(stream)[1]
+    if out is None:
+        if not plain_out:
+            raise ValueError("the shape descriptor names strides of out: pass out")
+        with _allocating(stream) if stream is not None else _NO_CONTEXT:
+            out = torch.empty(q.shape, dtype=dtype, device=q.device)
+    elif out.shape != q.shape or _heads(out, "out", dtype) != (
+            shape.out_row_stride or shape.num_q_heads * 128, shape.out_head_stride or 128):
+        raise ValueError("out does not match q or the shape descriptor")
+    elif out.get_device() != dev:
+        raise ValueError(f"q and out must be on the current device, cuda:{dev}")
+    if workspace is None:
+        with _allocating(stream):
+            workspace = alloc_extend_workspace(shape, q.device)
+    lp = None
+    if lse is not None:
+        lp = _on(lse, torch.float32, dev, "lse")
+        if lse.shape != q.shape[:2]:
+            raise ValueError("lse must be [total_q, num_q_heads]")
+    ks, ksp = (k_scale, None) if type(k_scale) is float else _scale_arg(k_scale, dev, "k_scale")
+    vs, vsp = (v_scale, None) if type(v_scale) is float else _scale_arg(v_scale, dev, "v_scale")
+    code = load_library().xqa_extend(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), cu_seqlens.data_ptr(), ks, vs, ksp, vsp, out.data_ptr(), lp,
+        ctypes.byref(shape), _on(workspace, _U8, dev, "workspace"), workspace.numel(), handle)
+    if code:
+        raise XqaError(code, "xqa_extend")
     return out
 
 

@@ -1,0 +1,1213 @@
+// extend.cu — attention of a chunk of new tokens over the paged cache (xqa_extend).
+//
+//   out[i, h] = sum_t softmax_t(sm_scale k_scale <q[i, h], K_t>) v_scale V_t,
+//   t < ctx, and for causal calls t <= ctx - n + i (i of the sequence's n queries, t its
+//   cached tokens, the chunk's own among them); a row that sees nothing is zero.
+//
+// Prompt attention's mathematics (a running maximum and sum over 128-key tiles, products
+// on tcgen05, two 128-row tiles worked in turn) on keys and values that are read as they
+// lie in the cache: 8 or 4 bits, 16-token pages in any order. Six warps turn each tile's
+// codes into the queries' 16-bit type in shared memory; every code's value (times its
+// group's scale in a 4-bit cache) is exact there, so the products are those of the cached
+// values, and the tensor's scales are applied in 32 bits (to the logits, to out).
+//
+// Work: a unit is 2 x T consecutive tokens of one sequence and the G heads of one kv head,
+// T = floor(128 / G). The units lie on a line, each as long as the keys it sees plus a
+// constant, and every CTA takes an equal share of the line: long sequences are cut
+// anywhere, at 128-key tiles, without the host knowing a length. A unit cut into pieces
+// leaves (O, m, l) of each in 32 bits in the workspace; the CTA that is last to write a
+// piece joins them. No CTA waits for another.
+//
+// A unit of at most T tokens fills one row tile only; both chains of product, softmax
+// and product then work on it, on every other key tile each, and are joined in the
+// epilogue.
+//
+// Warps: 0-3 and 4-7 softmax of chain 0 and 1 (a thread owns a row), 8-11 epilogue, 12
+// tensor core, 13 units and copies, 14-19 codes to 16-bit values. TMEM: S0, S1 (P over
+// them), O0, O1: 4 x 128 columns.
+//
+// Hidden values do not leak: see prompt attention; here rows past the sequence and values
+// that are not finite are zeroed as they are converted. A page whose table entry is out of
+// range has keys of NaN: the rows that see it are NaN, the others are not touched.
+#include <math.h>
+
+#include "xqa_tcgen05.cuh"
+#include "xqa_launch.h"
+
+namespace xqa {
+
+namespace {
+
+constexpr int kKvStages = 3;    // 16-bit K or V tiles
+constexpr int kUnitSlots = 3;
+constexpr int kExtendThreads = 640;  // whole groups of four warps, as their register split needs
+constexpr int kConvertWarps = 6;
+constexpr int kTilePages = kTile / kBlockSize;
+constexpr float kNoRowMax = -3e38f;     // as in prompt attention
+constexpr float kExactMax = 4194304.f;
+constexpr float kLazyMax = 8.0f;
+constexpr uint32_t kWaitLimit = 2000000000u >> 16;  // about 1 s in units of 2^16 clocks
+constexpr int kUnitReaders = 13 + kConvertWarps;  // 8 softmax, 4 epilogue, 1 tensor-core
+constexpr int kRawBytes = 4 * kTile * kHeadDim;  // the ring of codes
+
+template <int kFmt>
+struct Raw {
+  static constexpr int kSlice = kFmt == XQA_KV_E2M1 ? kSliceBytes4 : kPageBytes;
+  static constexpr int kBytes = kTilePages * kSlice;  // codes of a tile
+  static constexpr int kStages = kRawBytes / kBytes;  // 4, or 7 of 4 bits
+};
+
+struct Unit {
+  int end;       // 1: no more units
+  int bad;       // 1: NaN rows (a bad length or scale)
+  int seq;
+  int q_row;     // first token's row in q and out
+  int tokens;    // 1 .. 2 T
+  int head;      // kv head
+  int page0;     // first page of the piece within the sequence's table row
+  int len_k;     // keys of the piece, from the first of page0
+  int vis0;      // keys the first token sees (causal: one more per token)
+  int n[2];      // KV tiles row tile 0 / 1 sees
+  int split;     // 1: both chains work on row tile 0
+  int hidden;    // first key hidden from some token
+  int slot;      // place of this piece's (O, m, l); -1: the unit is one piece
+  int first;     // CTA of the unit's first piece
+  int pieces;
+};
+
+struct Shared {
+  uint64_t raw_full[7], raw_empty[7];
+  uint64_t kv_full[kKvStages], kv_empty[kKvStages];
+  uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2];
+  uint64_t p_full[2][2];
+  uint64_t o_full[2], o_free[2];
+  uint64_t stat_full[2], stat_free[2];
+  uint64_t drain;
+  Unit unit[kUnitSlots];
+  int not_finite[kUnitSlots];
+  int bad_pages[7];              // of the codes' stage, a bit for each page
+  int status;
+  uint32_t wait_limit;           // of every wait; 0: the CTA is aborted
+  int joins;
+  uint32_t tmem;
+  // the line (block-wide scan)
+  long long scan[32];
+  long long total, start_at;     // length of the line; where the first sequence begins
+  int start_seq, ctas;           // ctas: that share the line
+};
+
+constexpr int kSmemTiles = (2 + kKvStages) * kTileBytes;
+constexpr int kSmemStats = 2 * kTile * 2 * 4;
+constexpr int kExtendSmem = kSmemTiles + kRawBytes + kSmemStats + 1024;
+static_assert(sizeof(Shared) <= 1024, "shared state");
+static_assert(kExtendSmem <= 227 * 1024, "shared memory budget");
+
+// ---- the line of work ----
+// A sequence of n tokens: np = ceil(n / 2T) units for each kv head; unit i is
+// kUnitCost + base + min(step (i + 1), rows) long, the keys that its last token sees and a
+// constant for its start and end (in keys).
+constexpr int kUnitCost = 128;
+struct Seq {
+  int q0, n, ctx;  // ctx: -1 if the length is invalid
+};
+struct Cost {
+  int np;
+  long long base;
+  int step, rows;
+  __device__ __forceinline__ long long upto(int i) const {  // cost of the units before i
+    return i * (kUnitCost + base) + (long long)step * ((long long)i * (i + 1) / 2);
+  }
+  __device__ __forceinline__ long long unit(int i) const {
+    return kUnitCost + base + min((long long)step * (i + 1), (long long)rows);
+  }
+  __device__ __forceinline__ long long head() const { return np == 0 ? 0 : upto(np - 1) + unit(np - 1); }
+};
+
+__device__ __forceinline__ Seq read_seq(const ExtendParams& p, int b, int* status) {
+  Seq s;
+  s.q0 = p.cu_q[b];
+  const int q1 = p.cu_q[b + 1];
+  s.ctx = p.context_lens[b];
+  s.n = 0;
+  if (s.q0 >= 0 && q1 >= s.q0 && q1 <= p.total_q) s.n = q1 - s.q0;
+  else record_status(status, XQA_ERR_BAD_OFFSETS);
+  if (s.ctx < 0 || s.ctx > (long long)p.max_blocks_per_seq * kBlockSize) {
+    s.ctx = -1;
+    if (s.n > 0) record_status(status, XQA_ERR_CTX_TOO_LONG);
+  }
+  return s;
+}
+
+__device__ __forceinline__ Cost seq_cost(const ExtendParams& p, const Seq& s) {
+  Cost c;
+  const int per = 2 * p.tile_tokens;
+  c.np = (int)(((long long)s.n + per - 1) / per);
+  const bool causal = p.causal && s.ctx >= 0;
+  c.base = causal ? max(0, s.ctx - s.n) : max(0, s.ctx);
+  c.step = causal ? per : 0;
+  c.rows = causal ? s.n : 0;
+  return c;
+}
+
+// Block-wide exclusive scan; every thread calls it.
+__device__ __forceinline__ long long scan_all(long long v, Shared& sh, long long& sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long incl = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long x = __shfl_up_sync(kAll, incl, off);
+    if (lane >= off) incl += x;
+  }
+  if (lane == 31) sh.scan[warp] = incl;
+  __syncthreads();
+  long long before = 0;
+  sum = 0;
+  for (int w = 0; w < kExtendThreads / 32; ++w) {
+    if (w == warp) before = sum;
+    sum += sh.scan[w];
+  }
+  __syncthreads();
+  return before + incl - v;
+}
+
+struct Ctx {
+  const ExtendParams& p;
+  Shared& sh;
+  uint8_t* tiles;  // Q0, Q1, then the 16-bit ring
+  uint8_t* raw;
+  float* stats;    // [2][128][2]
+  uint32_t tmem;
+
+  __device__ __forceinline__ uint8_t* kv(int stage) const { return tiles + (2 + stage) * kTileBytes; }
+
+  // Warp-uniform wait within the CTA's limit; false ends the role (the CTA is aborted).
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
+    if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+    volatile uint32_t* limit = &sh.wait_limit;
+    const uint32_t t0 = (uint32_t)(clock64() >> 16);
+    do {
+      if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+    } while (__all_sync(kAll, (uint32_t)(clock64() >> 16) - t0 < *limit));
+    *limit = 0;
+    return false;
+  }
+  __device__ __forceinline__ bool get_unit(int i, Unit& u) const {
+    const int slot = i % kUnitSlots;
+    if (!wait(&sh.unit_full[slot], (i / kUnitSlots) & 1)) return false;
+    u = sh.unit[slot];
+    return !u.end;
+  }
+  __device__ __forceinline__ void arrive(uint64_t* bar) const {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  }
+  __device__ __forceinline__ void free_unit(int i) const { arrive(&sh.unit_empty[i % kUnitSlots]); }
+};
+
+// The order in which a unit's tiles pass through the rings: the first `lag` K tiles, then V
+// and the K tile `lag` below it in turn (lag: 1, or 2 where the chains take turns).
+struct TileOrder {
+  int n, lag;
+  __device__ __forceinline__ TileOrder(const Unit& u) : n(max(u.n[0], u.n[1])), lag(u.split ? 2 : 1) {}
+  // tile of item t (0 .. 2 n - 1), and whether it is V's
+  __device__ __forceinline__ int at(int t, bool& is_v) const {
+    const int u = t - lag;
+    if (u < 0) {
+      is_v = false;
+      return n - 1 - t;
+    }
+    const int both = 2 * (n - lag);
+    is_v = u >= both || (u & 1) == 0;
+    return u >= both ? lag - 1 - (u - both) : n - 1 - (u >> 1) - (is_v ? 0 : lag);
+  }
+};
+
+// Page ids of a table row, read 32 at a time by a whole warp, one group ahead (tiles are
+// taken from the last to the first).
+struct PageIds {
+  const int32_t* row;
+  int pages, group, cur, next;
+  __device__ __forceinline__ int read(int g) const {
+    const int i = g * 32 + (threadIdx.x & 31);
+    return g >= 0 && i < pages ? row[i] : -1;
+  }
+  __device__ __forceinline__ void start(const int32_t* r, int n, int tile) {
+    row = r;
+    pages = n;
+    group = tile >> 2;
+    cur = read(group);
+    next = read(group - 1);
+  }
+  // id of page `lane & 7` of a tile (the same or a lower one than before)
+  __device__ __forceinline__ int of(int tile) {
+    if (tile >> 2 != group) {
+      group = tile >> 2;
+      cur = next;
+      next = read(group - 1);
+    }
+    return __shfl_sync(kAll, cur, (tile & 3) * 8 + (threadIdx.x & 7));
+  }
+};
+
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// ---- warp 13: the units of this CTA, their queries and codes ----
+template <int kFmt>
+__device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
+                                          const CUtensorMap* tm_k, const CUtensorMap* tm_v, bool bad_scale,
+                                          int& raw_issued, int& q_issued) {
+  const ExtendParams& p = c.p;
+  Shared& sh = c.sh;
+  constexpr int kStages = Raw<kFmt>::kStages;
+  const int lane = threadIdx.x & 31;
+  const int per = 2 * p.tile_tokens;
+  const long long share = sh.total / sh.ctas, extra = sh.total % sh.ctas;
+  const int cta = blockIdx.x;
+  const long long lo = cta * share + min((long long)cta, extra);
+  const long long hi = lo + share + (cta < extra ? 1 : 0);
+  auto owner = [&](long long x) {  // CTA of a position of the line
+    const long long large = extra * (share + 1);
+    return (int)(x < large ? x / (share + 1) : extra + (x - large) / share);
+  };
+  int base = sh.start_seq & ~31, b = sh.start_seq;  // sequences base .. base + 31, one a lane
+  Seq mine;
+  auto read_chunk = [&]() {
+    mine.q0 = mine.n = 0;
+    mine.ctx = 0;
+    if (base + lane < p.batch) mine = read_seq(p, base + lane, &sh.status);
+  };
+  long long at = sh.start_at;  // where sequence b begins
+  if (lo < hi) read_chunk();
+  Seq s;
+  Cost cost;
+  auto pick = [&]() {
+    s.q0 = __shfl_sync(kAll, mine.q0, b - base);
+    s.n = __shfl_sync(kAll, mine.n, b - base);
+    s.ctx = __shfl_sync(kAll, mine.ctx, b - base);
+    cost = seq_cost(p, s);
+  };
+  int head = 0, pair = 0;
+  long long pos = lo;
+  if (lo < hi) {  // the unit that holds lo
+    pick();
+    const long long one = cost.head();
+    head = (int)((lo - at) / one);
+    const long long rem = lo - at - head * one;
+    int a = 0, z = cost.np - 1;  // the last unit that begins at or before rem
+    while (a < z) {
+      const int m = (a + z + 1) >> 1;
+      if (cost.upto(m) <= rem) a = m;
+      else z = m - 1;
+    }
+    pair = a;
+    at += head * one;  // now: where this head begins
+  }
+  for (int i = 0;; ++i) {
+    const int slot = i % kUnitSlots;
+    if (i >= kUnitSlots && !c.wait(&sh.unit_empty[slot], (i / kUnitSlots - 1) & 1)) return;
+    if (pos >= hi) {
+      if (lane == 0) {
+        sh.unit[slot].end = 1;
+        mbar_arrive(&sh.unit_full[slot]);
+      }
+      return;
+    }
+    const long long u0 = at + cost.upto(pair), len = cost.unit(pair);
+    const long long x0 = max(lo, u0) - u0, x1 = min(hi, u0 + len) - u0;
+    Unit w;
+    w.end = 0;
+    w.bad = s.ctx < 0 || bad_scale;
+    w.seq = b;
+    const int tok0 = pair * per;
+    w.q_row = s.q0 + tok0;
+    w.tokens = min(per, s.n - tok0);
+    w.head = head;
+    int len_k = w.bad ? 0 : s.ctx;
+    int vis0 = p.causal ? len_k - s.n + tok0 + 1 : len_k;
+    const int last = p.causal ? min(len_k, vis0 + w.tokens - 1) : len_k;
+    const int tiles = last > 0 ? (last - 1) / kTile + 1 : 0;
+    w.slot = -1;
+    w.first = cta;
+    w.pieces = 1;
+    int t0 = 0, t1 = tiles;
+    if (x0 > 0 || x1 < len) {
+      w.first = owner(u0);
+      w.pieces = owner(u0 + len - 1) - w.first + 1;
+      w.slot = 2 * cta + (x0 > 0 ? 0 : 1);
+      auto tile_of = [&](long long x) {
+        return (int)min((long long)tiles, max(0ll, (x - kUnitCost + kTile / 2) / kTile));
+      };
+      if (x0 > 0) t0 = tile_of(x0);
+      if (x1 < len) t1 = tile_of(x1);
+    }
+    w.page0 = t0 * kTilePages;
+    w.len_k = max(0, min(len_k, t1 * kTile) - t0 * kTile);
+    w.vis0 = p.causal ? vis0 - t0 * kTile : w.len_k;
+    int used = 0;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int toks = min(p.tile_tokens, w.tokens - r * p.tile_tokens);
+      const int seen = p.causal ? min(w.len_k, w.vis0 + r * p.tile_tokens + toks - 1) : w.len_k;
+      w.n[r] = toks > 0 && seen > 0 ? (seen - 1) / kTile + 1 : 0;
+      used += w.n[r] > 0;
+    }
+    w.split = w.tokens <= p.tile_tokens && w.n[0] >= 2;
+    if (w.split) w.n[1] = w.n[0];
+    w.hidden = max(0, min(w.vis0, w.len_k));
+    if (lane == 0) {
+      sh.unit[slot] = w;
+      sh.not_finite[slot] = 0;
+      if (const uint32_t more = max(w.n[0], w.n[1]) >> 16) {  // (an abort stays one)
+        const uint32_t limit = *(volatile uint32_t*)&sh.wait_limit;
+        if (limit != 0 && limit < (1 + more) * kWaitLimit)
+          atomicCAS(&sh.wait_limit, limit, (1 + more) * kWaitLimit);
+      }
+      mbar_arrive(&sh.unit_full[slot]);
+    }
+    const TileOrder order(w);
+    if (order.n > 0) {
+      const int32_t* table = p.block_tables + (size_t)b * p.max_blocks_per_seq + w.page0;
+      const int pages = (w.len_k + kBlockSize - 1) / kBlockSize;
+      PageIds k_ids, v_ids;
+      k_ids.start(table, pages, order.n - 1);
+      v_ids.start(table, pages, order.n - 1);
+      if (q_issued > 0 && !c.wait(&sh.q_empty, (q_issued - 1) & 1)) return;
+      if (lane == 0) {
+        const int half = p.group * p.tile_tokens * 128;  // bytes of a half tile
+        const int row_tiles = w.split ? 1 : used;        // tile 0 alone, or both, or tile 1 alone
+        mbar_arrive_expect_tx(&sh.q_full, 2 * half * row_tiles);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (w.n[r] == 0 || (w.split && r == 1)) continue;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            tma_load_4d(c.tiles + r * kTileBytes + h * kHalfBytes, tm_q, &sh.q_full, 64 * h, 0,
+                        w.head, w.q_row + r * p.tile_tokens);
+        }
+      }
+      ++q_issued;
+      for (int t = 0; t < 2 * order.n; ++t) {
+        bool is_v;
+        const int j = order.at(t, is_v);
+        const int st = raw_issued % kStages;
+        const int id = is_v ? v_ids.of(j) : k_ids.of(j);
+        if (raw_issued >= kStages && !c.wait(&sh.raw_empty[st], (raw_issued / kStages - 1) & 1))
+          return;
+        const bool want = lane < kTilePages && j * kTilePages + lane < pages;
+        const bool good = want && (uint32_t)id < (uint32_t)p.num_blocks;
+        const uint32_t n_good = __popc(__ballot_sync(kAll, good));
+        const uint32_t n_bad = __ballot_sync(kAll, want && !good);
+        if (lane == 0) {
+          sh.bad_pages[st] = n_bad;
+          if (n_bad) record_status(&sh.status, XQA_ERR_BAD_BLOCK_ID);
+          mbar_arrive_expect_tx(&sh.raw_full[st], n_good * Raw<kFmt>::kSlice);
+        }
+        __syncwarp();
+        if (good) {
+          uint8_t* dst = c.raw + st * Raw<kFmt>::kBytes + lane * Raw<kFmt>::kSlice;
+          if (kFmt != XQA_KV_E2M1 && p.kv_layout == XQA_LAYOUT_NHD)
+            tma_load_kv(dst, is_v ? tm_v : tm_k, &sh.raw_full[st], 0, w.head, id * kBlockSize);
+          else
+            bulk_copy(dst, (is_v ? p.v_pool : p.k_pool) +
+                               ((size_t)id * p.num_kv_heads + w.head) * Raw<kFmt>::kSlice,
+                      Raw<kFmt>::kSlice, &sh.raw_full[st]);
+        }
+        __syncwarp();
+        ++raw_issued;
+      }
+    }
+    // on to the next unit
+    pos = u0 + len;
+    if (++pair < cost.np) continue;
+    pair = 0;
+    at = pos;
+    if (++head < p.num_kv_heads || pos >= hi) continue;
+    head = 0;
+    for (;;) {  // the next sequence with tokens (there is one: the line goes on)
+      const uint32_t some = __ballot_sync(kAll, mine.n > 0 && base + lane > b);
+      if (some) {
+        b = base + __ffs(some) - 1;
+        break;
+      }
+      base += 32;
+      if (base >= p.batch) return;  // cannot be
+      b = base - 1;
+      read_chunk();
+    }
+    pick();
+  }
+}
+
+// ---- warp 12: the products ----
+// The chains in turn, as in prompt attention: O += P V of a tile, then S of the chain's next
+// tile over P.
+template <int kType>
+__device__ __forceinline__ void tensor_role(const Ctx& c) {
+  Shared& sh = c.sh;
+  const uint32_t tiles = __shfl_sync(kAll, smem_addr(c.tiles), 0);
+  const uint32_t tmem = __shfl_sync(kAll, c.tmem, 0);
+  const uint64_t q_desc = desc_k_major(tiles);
+  const uint64_t k_desc = desc_k_major(tiles + 2 * kTileBytes);
+  const uint64_t v_desc = desc_mn_major(tiles + 2 * kTileBytes);
+  int item = 0, units = 0;
+  uint32_t ph_p = 0, ph_o = 3;
+  // a tile of the ring in turn: its stage, once it is there
+  auto stage = [&](int it) { return it % kKvStages; };
+  auto arrived = [&](int it) { return c.wait(&sh.kv_full[it % kKvStages], (it / kKvStages) & 1); };
+  for (int i = 0;; ++i) {
+    Unit w;
+    if (!c.get_unit(i, w)) return;
+    c.free_unit(i);
+    const int n0 = __shfl_sync(kAll, w.n[0], 0), n1 = __shfl_sync(kAll, w.n[1], 0);
+    const int split = __shfl_sync(kAll, w.split, 0);
+    const int n = max(n0, n1), lag = 1 + split;
+    if (n == 0) continue;
+    if (!c.wait(&sh.q_full, units & 1)) return;
+    ++units;
+    auto score = [&](int s, int st) {  // S of chain s
+      const uint64_t a = q_desc + (split ? 0 : s) * (kTileBytes >> 4);
+      const uint64_t b = k_desc + st * (kTileBytes >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t off = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+          tc_mma_ss(tmem + s * kTile, a + off, b + off, instr_desc<kType>(false), k > 0);
+        }
+        tc_commit(&sh.s_full[s]);
+      }
+      __syncwarp();
+    };
+    for (int t = 0; t < lag; ++t, ++item) {  // the first K tiles
+      if (!arrived(item)) return;
+      tc_fence_after();
+#pragma unroll 1
+      for (int s = 0; s < 2; ++s)
+        if (split ? s == t : (s ? n1 : n0) == n) score(s, stage(item));
+      if (elect_one()) tc_commit(&sh.kv_empty[stage(item)]);
+      __syncwarp();
+    }
+    if (n == lag && elect_one()) tc_commit(&sh.q_empty);
+    __syncwarp();
+    for (int j = n - 1; j >= 0; --j) {
+      const int vi = item++;
+      const bool next = j >= lag;
+      const int ki = next ? item++ : 0;
+      if (!arrived(vi)) return;
+      if (next && !arrived(ki)) return;
+#pragma unroll 1
+      for (int s = 0; s < 2; ++s) {
+        const int ns = s ? n1 : n0;
+        if (split && ((n - 1 - j) & 1) != s) continue;
+        if (j < ns) {
+          const bool start = split ? j >= n - 2 : j == ns - 1;
+          if (start) {
+            if (!c.wait(&sh.o_free[s], ph_o >> s & 1)) return;
+            ph_o ^= 1u << s;
+          }
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {  // as P's halves are written
+            const uint32_t bit = 2 * s + h;
+            if (!c.wait(&sh.p_full[s][h], ph_p >> bit & 1)) return;
+            ph_p ^= 1u << bit;
+            tc_fence_after();
+            const uint64_t vb = v_desc + stage(vi) * (kTileBytes >> 4) + h * (4 * 2048 >> 4);
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc_mma_ts(tmem + 256 + s * kTile, tmem + s * kTile + 32 * h + 8 * k,
+                          vb + k * (2048 >> 4), instr_desc<kType>(true), !start || h + k > 0);
+            }
+            __syncwarp();
+          }
+          if (j < lag && elect_one()) tc_commit(&sh.o_full[s]);
+          __syncwarp();
+        }
+        if (next && j - lag < ns) score(s, stage(ki));
+      }
+      if (elect_one()) {
+        tc_commit(&sh.kv_empty[stage(vi)]);
+        if (next) tc_commit(&sh.kv_empty[stage(ki)]);
+        if (j == lag) tc_commit(&sh.q_empty);
+      }
+      __syncwarp();
+    }
+  }
+}
+
+// ---- warps 14-19: codes to 16-bit values ----
+// 16 neighbouring dims of a token, as 8 pairs.
+template <int kType>
+__device__ __forceinline__ uint32_t half2_as(uint32_t h) {  // exact: at most 6 significant bits
+  if (kType == XQA_F16) return h;
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack2<XQA_BF16>(f.x, f.y);
+}
+template <int kFmt, int kType>
+__device__ __forceinline__ void convert16(const uint8_t* page, int row, int group, uint32_t (&o)[8]) {
+  if constexpr (kFmt == XQA_KV_E2M1) {
+    const uint2 w = lds64(page + row * (kHeadDim / 2) + 8 * group);
+    const uint32_t s8 = lds_u8(page + kCodeBytes4 + row * (kHeadDim / kGroup4) + group);
+    const uint32_t sc = e4m3x2_to_f16x2(s8 | s8 << 8);
+    e2m1x8_to_f16x2(w.x, o);
+    e2m1x8_to_f16x2(w.y, o + 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = half2_as<kType>(hmul2(o[i], sc));
+  } else {
+    const uint4 w = lds128(page + row * kHeadDim + 16 * group);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[2 * i] = half2_as<kType>(KvConv<kFmt>::k_lo(x[i]));
+      o[2 * i + 1] = half2_as<kType>(KvConv<kFmt>::k_hi(x[i]));
+    }
+  }
+}
+
+template <int kFmt, int kType>
+__device__ __forceinline__ void convert_role(const Ctx& c) {
+  Shared& sh = c.sh;
+  constexpr int kStages = Raw<kFmt>::kStages;
+  const int warp = (threadIdx.x >> 5) - 14, lane = threadIdx.x & 31;
+  const uint32_t exp_mask = kType == XQA_F16 ? 0x7c00u : 0x7f80u;
+  // Eight lanes take the first 64 dims of one token and the last 64 of its neighbour, the
+  // next eight the other halves: whole 128-byte runs are read, and a store's 16-byte
+  // chunks, which the swizzle would pair up within one token, fall into different banks.
+  const int half = lane >> 2 & 1, group = 4 * half + (lane & 3);
+  const int row_in4 = 2 * (lane >> 4) + (half ^ (lane >> 3 & 1));
+  int item = 0;
+  for (int i = 0;; ++i) {
+    Unit u;
+    if (!c.get_unit(i, u)) return;
+    const TileOrder order(u);
+    bool found = false;
+    for (int t = 0; t < 2 * order.n; ++t, ++item) {
+      bool is_v;
+      const int j = order.at(t, is_v);
+      const int rs = item % kStages, st = item % kKvStages;
+      if (!c.wait(&sh.raw_full[rs], (item / kStages) & 1)) return;
+      if (item >= kKvStages && !c.wait(&sh.kv_empty[st], (item / kKvStages - 1) & 1)) return;
+      const uint8_t* raw = c.raw + rs * Raw<kFmt>::kBytes;
+      uint8_t* dst = c.kv(st) + half * kHalfBytes;
+      const int bad = *(volatile int*)&sh.bad_pages[rs];
+      const bool masked = is_v && (j + 1) * kTile > u.hidden;
+      auto store = [&](int row, const uint32_t (&o)[8]) {
+        uint8_t* d = dst + row * 128;
+        *reinterpret_cast<uint4*>(d + ((2 * (group & 3)) ^ (row & 7)) * 16) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(d + ((2 * (group & 3) + 1) ^ (row & 7)) * 16) =
+            make_uint4(o[4], o[5], o[6], o[7]);
+      };
+      if (masked || bad) {
+        const int past = u.len_k - j * kTile, from = u.hidden - j * kTile;
+#pragma unroll 1
+        for (int r4 = warp; r4 < kTile / 4; r4 += kConvertWarps) {
+          const int row = r4 * 4 + row_in4;
+          uint32_t o[8];
+          convert16<kFmt, kType>(raw + (row >> 4) * Raw<kFmt>::kSlice, row & 15, group, o);
+          const bool none = bad >> (row >> 4) & 1;
+          const bool zero = is_v && (none || row >= past);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if (zero) o[k] = 0;
+            else if (none) o[k] = 0x7fff7fffu;  // NaN in both types
+            else if (masked && row >= from) {
+              if ((o[k] & exp_mask) == exp_mask) o[k] &= 0xffff0000u, found = true;
+              if ((o[k] & exp_mask << 16) == exp_mask << 16) o[k] &= 0x0000ffffu, found = true;
+            }
+          }
+          store(row, o);
+        }
+        if (found) *(volatile int*)&sh.not_finite[i % kUnitSlots] = 1;
+      } else {
+#pragma unroll 2
+        for (int r4 = warp; r4 < kTile / 4; r4 += kConvertWarps) {
+          const int row = r4 * 4 + row_in4;
+          uint32_t o[8];
+          convert16<kFmt, kType>(raw + (row >> 4) * Raw<kFmt>::kSlice, row & 15, group, o);
+          store(row, o);
+        }
+      }
+      fence_proxy_async_smem();  // before the tensor core reads the tile
+      c.arrive(&sh.kv_full[st]);
+      c.arrive(&sh.raw_empty[rs]);
+    }
+    c.free_unit(i);
+  }
+}
+
+struct RowPos {
+  int token;  // within the unit
+  int head;   // within the group
+  bool valid;
+};
+__device__ __forceinline__ RowPos row_pos(const ExtendParams& p, const Unit& u, int r, int row) {
+  RowPos x;
+  const int t = row / p.group;
+  x.head = row - t * p.group;
+  x.token = r * p.tile_tokens + t;
+  x.valid = t < p.tile_tokens && x.token < u.tokens;
+  return x;
+}
+__device__ __forceinline__ int visible(const ExtendParams& p, const Unit& u, const RowPos& r) {
+  if (!r.valid) return 0;
+  return p.causal ? max(0, min(u.len_k, u.vis0 + r.token)) : u.len_k;
+}
+
+// ---- warps 0-7: softmax of chain s; a thread owns a row (as in prompt attention) ----
+template <int kType>
+__device__ __forceinline__ void softmax_role(const Ctx& c, int s, float sc) {
+  const ExtendParams& p = c.p;
+  Shared& sh = c.sh;
+  const int row = threadIdx.x & 127;
+  const uint32_t lane_base = c.tmem + ((uint32_t)(row & ~31) << 16);
+  const uint32_t s_addr = lane_base + s * kTile, o_addr = lane_base + 256 + s * kTile;
+  int ns = 0, nstat = 0;
+  for (int i = 0;; ++i) {
+    Unit u;
+    if (!c.get_unit(i, u)) return;
+    const int r = u.split ? 0 : s;  // row tile
+    const RowPos rp = row_pos(p, u, r, row);
+    const int vis = visible(p, u, rp);
+    c.free_unit(i);
+    const int n = s == 0 ? u.n[0] : u.n[1];
+    if (n == 0) continue;
+    const bool idle = !__any_sync(kAll, rp.valid);  // no row of this warp is a token's
+    // keys that every token of this row tile sees
+    const int clear = p.causal ? min(u.len_k, u.vis0 + r * p.tile_tokens) : u.len_k;
+    float m = kNoRowMax, m_raw = 0.f, l = 0.f;  // m_raw: m before the scale
+    for (int j = u.split ? n - 1 - s : n - 1; j >= 0; j -= 1 + u.split) {
+      if (!c.wait(&sh.s_full[s], ns & 1)) return;
+      ++ns;
+      tc_fence_after();
+      if (idle) {  // P is what S left there: rows that nobody reads
+        tc_fence_before();
+        c.arrive(&sh.p_full[s][0]);
+        c.arrive(&sh.p_full[s][1]);
+        continue;
+      }
+      if ((j + 1) * kTile > clear) {  // keys that a row does not see: -inf
+        const int lim = vis - j * kTile;
+#pragma unroll 1
+        for (int q = max(0, __reduce_min_sync(kAll, lim)) >> 5; q < 4; ++q) {
+          uint32_t v[32];
+          tmem_ld32(s_addr + 32 * q, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (32 * q + k >= lim) v[k] = 0xff800000u;
+          tmem_st32(s_addr + 32 * q, v);
+        }
+        tmem_wait_st();
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t v[32];
+        tmem_ld32(s_addr + 32 * q, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; k += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(v[k + e])), __uint_as_float(v[k + 4 + e]));
+      }
+      const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), top = raw * sc;
+      const bool moves = top > m + kLazyMax;
+      const bool scale_o = moves && m != kNoRowMax;
+      const float old = m;
+      if (moves) m = top, m_raw = raw;
+      uint64_t m2 = f32x2(-m, -m);
+      // large maxima are subtracted before the scale (see prompt attention)
+      const bool exact = fabsf(m) > kExactMax && m != kNoRowMax && vis > 0;
+      if (__any_sync(kAll, scale_o)) {
+        const float a = scale_o ? ex2(old - top) : 1.f;
+        l *= a;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + 32 * q, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+          tmem_st32(o_addr + 32 * q, o);
+        }
+      }
+      const bool any_exact = __any_sync(kAll, exact);
+      const float minus = exact ? m_raw : 0.f;
+      if (exact) m2 = 0;
+      const uint64_t sc2 = f32x2(sc, sc);
+      uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {  // P of 32 keys over S of keys that are read already
+        uint32_t v[32], pk[16];
+        tmem_ld32(s_addr + 32 * q, v);
+        tmem_wait_ld();
+        if (any_exact) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) - minus);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          float a, b;
+          split2(fma2(f32x2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sc2, m2), a, b);
+          a = ex2(a);
+          b = ex2(b);
+          sum[k & 1] = add2(sum[k & 1], f32x2(a, b));
+          pk[k] = pack2<kType>(a, b);
+        }
+        tmem_st16(s_addr + 16 * q, pk);
+        if (q & 1) {
+          tmem_wait_st();
+          tc_fence_before();
+          c.arrive(&sh.p_full[s][q >> 1]);
+        }
+      }
+      float la, lb;
+      split2(add2(sum[0], sum[1]), la, lb);
+      l += la + lb;
+    }
+    if (nstat > 0 && !c.wait(&sh.stat_free[s], (nstat - 1) & 1)) return;
+    ++nstat;
+    float2* st = reinterpret_cast<float2*>(c.stats) + s * kTile + row;
+    *st = make_float2(m, l);
+    c.arrive(&sh.stat_full[s]);
+  }
+}
+
+// Value (before the tensor's scale) of one cached V element if it is not finite, else 0.
+template <int kFmt>
+__device__ __noinline__ float not_finite_value(const uint8_t* slice, long long token_stride, int slot,
+                                               int dim) {
+  uint32_t h;
+  if constexpr (kFmt == XQA_KV_E2M1) {
+    const uint32_t s8 = slice[kCodeBytes4 + slot * (kHeadDim / kGroup4) + dim / kGroup4];
+    h = e4m3x2_to_f16x2(s8);
+  } else {
+    const uint32_t code = slice[slot * token_stride + dim];
+    h = KvConv<kFmt>::k_lo(code);
+  }
+  return (h & 0x7c00u) == 0x7c00u ? __half2float(__ushort_as_half((unsigned short)h)) : 0.f;
+}
+
+// ---- warps 8-11: normalise and write, or leave a piece and join ----
+template <int kType>
+__device__ __noinline__ void join_pieces(const Ctx& c, const Unit& u, float v_scale);
+
+template <int kFmt, int kType>
+__device__ __forceinline__ void epilogue_role(const Ctx& c, float v_scale) {
+  const ExtendParams& p = c.p;
+  Shared& sh = c.sh;
+  const int row = threadIdx.x & 127;
+  const uint32_t lane_base = c.tmem + ((uint32_t)(row & ~31) << 16);
+  uint32_t ph = 0;  // a bit for each chain
+  for (int i = 0;; ++i) {
+    Unit u;
+    if (!c.get_unit(i, u)) return;
+    const bool piece = u.slot >= 0;
+#pragma unroll 1
+    for (int s = 0; s < 2; ++s) {
+      if (u.split && s == 1) break;
+      const RowPos rp = row_pos(p, u, s, row);
+      const int n_s = s ? u.n[1] : u.n[0];
+      const long long at = (long long)u.q_row + rp.token;
+      const int h = u.head * p.group + rp.head;
+      uint16_t* out = p.out + at * p.out_row_stride + h * p.out_head_stride;
+      const size_t place = (size_t)(u.slot * 2 + s);
+      if (n_s == 0) {  // no tokens, or tokens that see nothing
+        if (piece) p.piece_ml[place * kTile + row] = make_float2(kNoRowMax, 0.f);
+        else if (rp.valid) {
+          const uint32_t f = !u.bad ? 0u : kType == XQA_F16 ? 0x7fff7fffu : 0x7fc07fc0u;
+#pragma unroll 1
+          for (int k = 0; k < kHeadDim / 8; ++k)
+            reinterpret_cast<uint4*>(out)[k] = make_uint4(f, f, f, f);
+          if (p.lse) p.lse[at * p.num_q_heads + h] = u.bad ? __int_as_float(0x7fc00000) : -INFINITY;
+        }
+        continue;
+      }
+      // the chain's (m, l), or both chains' and their weights
+      float2 ml;
+      float w0 = 1.f, w1 = 0.f;
+      if (!c.wait(&sh.stat_full[s], ph >> s & 1)) return;
+      ml = reinterpret_cast<const float2*>(c.stats)[s * kTile + row];
+      c.arrive(&sh.stat_free[s]);
+      if (u.split) {
+        if (!c.wait(&sh.stat_full[1], ph >> 1 & 1)) return;
+        const float2 b = reinterpret_cast<const float2*>(c.stats)[kTile + row];
+        c.arrive(&sh.stat_free[1]);
+        const float m = ml.y == 0.f ? b.x : b.y == 0.f ? ml.x : fmaxf(ml.x, b.x);
+        // a chain with keys keeps the least weight there is: its infinities and NaN are the row's
+        w0 = ml.y != 0.f ? fmaxf(ex2(ml.x - m), 0x1p-149f) : 0.f;
+        w1 = b.y != 0.f ? fmaxf(ex2(b.x - m), 0x1p-149f) : 0.f;
+        ml = make_float2(m, (ml.y != 0.f ? w0 * ml.y : 0.f) + (b.y != 0.f ? w1 * b.y : 0.f));
+        if (!c.wait(&sh.o_full[1], ph >> 1 & 1)) return;
+        ph ^= 2u;
+      }
+      if (!c.wait(&sh.o_full[s], ph >> s & 1)) return;
+      ph ^= 1u << s;
+      tc_fence_after();
+      const bool patch = *(volatile int*)&sh.not_finite[i % kUnitSlots] != 0;
+      const int vis = visible(p, u, rp);
+      const float rl = ml.y == 0.f ? 0.f : v_scale / ml.y;
+      uint16_t* dst[4];  // this lane's 16 bytes of four lanes' rows
+      const unsigned long long mine = rp.valid ? reinterpret_cast<unsigned long long>(out) : 0ull;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const unsigned long long a = __shfl_sync(kAll, mine, (threadIdx.x & 28) + k);
+        dst[k] = a ? reinterpret_cast<uint16_t*>(a) + 8 * (threadIdx.x & 3) : nullptr;
+      }
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t o[32];
+        __syncwarp();  // rows part ways below
+        tmem_ld32(lane_base + 256 + s * kTile + 32 * q, o);
+        tmem_wait_ld();
+        if (u.split) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t o1[16];
+            tmem_ld16(lane_base + 256 + kTile + 32 * q + 16 * e, o1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float a = w0 != 0.f ? w0 * __uint_as_float(o[16 * e + k]) : 0.f;
+              const float b = w1 != 0.f ? w1 * __uint_as_float(o1[k]) : 0.f;
+              o[16 * e + k] = __float_as_uint(a + b);
+            }
+          }
+        }
+        if (q == 3) {  // O is read
+          tc_fence_before();
+          c.arrive(&sh.o_free[s]);
+          if (u.split) c.arrive(&sh.o_free[1]);
+        }
+        if (patch) {  // infinities and NaN that were zeroed, for rows that see them
+          const int32_t* table = p.block_tables + (size_t)u.seq * p.max_blocks_per_seq + u.page0;
+#pragma unroll 1
+          for (int key = u.hidden; key < vis; ++key) {
+            const int id = table[key / kBlockSize];
+            if ((uint32_t)id >= (uint32_t)p.num_blocks) continue;
+            const bool nhd = kFmt != XQA_KV_E2M1 && p.kv_layout == XQA_LAYOUT_NHD;
+            const uint8_t* slice =
+                p.v_pool + (nhd ? ((size_t)id * kBlockSize * p.num_kv_heads + u.head) * kHeadDim
+                                : ((size_t)id * p.num_kv_heads + u.head) * Raw<kFmt>::kSlice);
+            const long long stride = nhd ? (long long)p.num_kv_heads * kHeadDim : kHeadDim;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              o[k] = __float_as_uint(__uint_as_float(o[k]) +
+                                     not_finite_value<kFmt>(slice, stride, key % kBlockSize, 32 * q + k));
+          }
+        }
+        if (piece) {  // as it is: [32 chunks of 4 dims][128 rows]
+          float4* po = p.piece_o + (place * 32 + 8 * q) * kTile + row;
+          if (rp.valid) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              po[k * kTile] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                          __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+          }
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float a, b;
+            split2(mul2(f32x2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), f32x2(rl, rl)),
+                   a, b);
+            w[k] = pack2<kType>(a, b);
+          }
+          trade<1>(w);
+          trade<2>(w);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (dst[k])
+              *reinterpret_cast<uint4*>(dst[k] + 32 * q) =
+                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        }
+      }
+      if (piece) p.piece_ml[place * kTile + row] = ml;
+      else if (p.lse && rp.valid)
+        p.lse[at * p.num_q_heads + h] =
+            ml.y == 0.f ? -INFINITY : (ml.x + __log2f(ml.y)) * 0.6931471805599453f;
+    }
+    if (piece) {
+      __threadfence();
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if ((threadIdx.x & 127) == 0) {
+        const int old = atom_add_acq_rel_gpu(p.tickets + u.first, 1);
+        sh.joins = old == u.pieces - 1;
+        if (old == u.pieces - 1) p.tickets[u.first] = 0;  // for the next call
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (*(volatile int*)&sh.joins) join_pieces<kType>(c, u, v_scale);
+    }
+    c.free_unit(i);
+  }
+}
+
+// The pieces of a unit, by the epilogue warps of the CTA that wrote the last one.
+template <int kType>
+__device__ __noinline__ void join_pieces(const Ctx& c, const Unit& u, float v_scale) {
+  const ExtendParams& p = c.p;
+  __threadfence();
+  const float nan = __int_as_float(0x7fc00000);
+#pragma unroll 1
+  for (int s = 0; s < 2; ++s) {
+    const int tokens = min(p.tile_tokens, u.tokens - s * p.tile_tokens);
+    if (tokens <= 0) break;
+    const int rows = tokens * p.group;  // <= 128
+    // threads of a row: 128 / span, its dims shared out among them
+    const int span = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    const int row = threadIdx.x & (span - 1), chunks = span / 4;
+    const int c0 = (threadIdx.x & 127) / span * chunks;
+    if (row >= rows) continue;
+    const int t = row / p.group, g = row - t * p.group, h = u.head * p.group + g;
+    const long long at = (long long)u.q_row + s * p.tile_tokens + t;
+    // piece k is in slot 1 of the first CTA, slot 0 of the others
+    auto place = [&](int k) { return (size_t)(4 * (u.first + k) + (k == 0 ? 2 : 0) + s); };
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < u.pieces; ++k) {
+      const float2 ml = __ldcg(p.piece_ml + place(k) * kTile + row);
+      if (ml.y != 0.f) top = fmaxf(top, ml.x);
+    }
+#pragma unroll 4
+    for (int k = 0; k < u.pieces; ++k) {
+      const float2 ml = __ldcg(p.piece_ml + place(k) * kTile + row);
+      // (a piece with keys keeps the least weight there is)
+      if (ml.y != 0.f) sum += fmaxf(ex2(ml.x - top), 0x1p-149f) * ml.y;
+    }
+    const float rl = u.bad ? nan : sum == 0.f ? 0.f : v_scale / sum;
+    uint16_t* out = p.out + at * p.out_row_stride + h * p.out_head_stride;
+#pragma unroll 1
+    for (int q = c0; q < c0 + chunks; q += 4) {  // 16 dims
+      float4 acc[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+      for (int k = 0; k < u.pieces; ++k) {
+        const float2 ml = __ldcg(p.piece_ml + place(k) * kTile + row);
+        if (ml.y == 0.f) continue;  // without keys: it has written no O
+        const float w = fmaxf(ex2(ml.x - top), 0x1p-149f);
+        const float4* po = p.piece_o + (place(k) * 32 + q) * kTile + row;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 v = __ldcg(po + (size_t)e * kTile);
+          acc[e].x += w * v.x;
+          acc[e].y += w * v.y;
+          acc[e].z += w * v.z;
+          acc[e].w += w * v.w;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        reinterpret_cast<uint2*>(out)[q + e] = make_uint2(pack2<kType>(acc[e].x * rl, acc[e].y * rl),
+                                                          pack2<kType>(acc[e].z * rl, acc[e].w * rl));
+    }
+    if (p.lse && c0 == 0)
+      p.lse[at * p.num_q_heads + h] =
+          u.bad ? nan : sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.6931471805599453f;
+  }
+}
+
+template <int kFmt, int kType>
+__global__ void __launch_bounds__(kExtendThreads, 1)
+    extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const ExtendParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* raw = smem + kSmemTiles;
+  float* stats = reinterpret_cast<float*>(raw + kRawBytes);
+  Shared& sh = *reinterpret_cast<Shared*>(raw + kRawBytes + kSmemStats);
+  const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0);  // known to be warp-uniform
+  const bool aligned = (smem_addr(smem) & 1023u) == 0;  // as the swizzle needs
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Raw<kFmt>::kStages; ++i) {
+      mbar_init(&sh.raw_full[i], 1);
+      mbar_init(&sh.raw_empty[i], kConvertWarps);
+    }
+    for (int i = 0; i < kKvStages; ++i) {
+      mbar_init(&sh.kv_full[i], kConvertWarps);
+      mbar_init(&sh.kv_empty[i], 1);
+    }
+    for (int i = 0; i < kUnitSlots; ++i) {
+      mbar_init(&sh.unit_full[i], 1);
+      mbar_init(&sh.unit_empty[i], kUnitReaders);
+    }
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sh.s_full[s], 1);
+      mbar_init(&sh.p_full[s][0], 4);
+      mbar_init(&sh.p_full[s][1], 4);
+      mbar_init(&sh.o_full[s], 1);
+      mbar_init(&sh.o_free[s], 4);
+      mbar_init(&sh.stat_full[s], 4);
+      mbar_init(&sh.stat_free[s], 4);
+    }
+    mbar_init(&sh.drain, 1);
+    sh.wait_limit = kWaitLimit;
+    sh.status = aligned ? XQA_OK : XQA_ERR_LAUNCH;
+    sh.start_seq = 0;
+    sh.start_at = 0;
+    fence_mbar_init();
+  }
+  if (warp == 13 && (threadIdx.x & 31) == 0) {
+    prefetch_tensormap(&tm_q);
+    if (kFmt != XQA_KV_E2M1 && p.kv_layout == XQA_LAYOUT_NHD) {
+      prefetch_tensormap(&tm_k);
+      prefetch_tensormap(&tm_v);
+    }
+  }
+  if (warp == 12) tmem_alloc(&sh.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_wait();  // inputs are read, and outputs written, after the kernels before this one
+  // the line's length, and the sequence that holds this CTA's first position
+  long long total = 0, rows = 0;
+  int ctas = 1;
+  for (int b0 = 0; b0 < p.batch; b0 += kExtendThreads) {
+    const int b = b0 + threadIdx.x;
+    Seq s{0, 0, 0};
+    if (b < p.batch) s = read_seq(p, b, &sh.status);
+    long long sum;
+    scan_all(seq_cost(p, s).head() * p.num_kv_heads, sh, sum);
+    total += sum;
+    scan_all(s.n, sh, sum);
+    rows += sum;
+  }
+  // sequences that overlap (offsets that descend) could have any number of units
+  if (rows > p.total_q) total = 0;
+  if (total > 0) ctas = (int)min((long long)gridDim.x, max(1ll, total / kExtendMinShare));
+  const long long share = total / ctas, extra = total % ctas;
+  const long long lo = blockIdx.x * share + min((long long)blockIdx.x, extra);
+  const bool works = total > 0 && blockIdx.x < ctas;
+  if (works) {
+    long long before = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += kExtendThreads) {
+      const int b = b0 + threadIdx.x;
+      Seq s{0, 0, 0};
+      if (b < p.batch) s = read_seq(p, b, &sh.status);
+      const long long mine = seq_cost(p, s).head() * p.num_kv_heads;
+      long long sum;
+      const long long excl = before + scan_all(mine, sh, sum);
+      if (excl <= lo && lo < excl + mine) sh.start_seq = b, sh.start_at = excl;
+      before += sum;
+      if (lo < before) break;
+    }
+  }
+  if (threadIdx.x == 0) {
+    sh.total = total;
+    sh.ctas = ctas;
+  }
+  __syncthreads();
+  const float ks = p.k_scale_ptr ? *p.k_scale_ptr : p.k_scale;
+  const float vs = p.v_scale_ptr ? *p.v_scale_ptr : p.v_scale;
+  const float sc = (float)(p.qk_scale_base * (double)ks);
+  const bool bad_scale = !(sc > 0.f && sc < INFINITY);
+  if (bad_scale && works && threadIdx.x == 0) record_status(&sh.status, XQA_ERR_VALUE);
+  int raw_issued = 0, q_issued = 0;
+  if (aligned && works) {
+    const Ctx c{p, sh, smem, raw, stats, sh.tmem};
+    __syncwarp();
+    // 256 x 136 + 128 x 96 + 256 x 56 are the launch's 640 x 96
+    if (warp >= 12) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      if (warp == 12) tensor_role<kType>(c);
+      else if (warp == 13) load_role<kFmt>(c, &tm_q, &tm_k, &tm_v, bad_scale, raw_issued, q_issued);
+      else convert_role<kFmt, kType>(c);
+    } else if (warp >= 8) {
+      epilogue_role<kFmt, kType>(c, vs);
+    } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+      softmax_role<kType>(c, warp >> 2, sc);
+    }
+  }
+  __syncwarp();
+  // Products and their arrivals, and after an abort copies, may be in flight: they end
+  // before the CTA's shared memory and TMEM are given up.
+  if (aligned && (warp == 12 || warp == 13)) {
+    int never = 0;
+    bool ok = true;
+    if (warp == 12) {
+      if (elect_one()) tc_commit(&sh.drain);
+      __syncwarp();
+      ok = mbar_wait_bounded(&sh.drain, 0, &never);
+    } else if (*(volatile uint32_t*)&sh.wait_limit == 0) {
+      constexpr int kStages = Raw<kFmt>::kStages;
+      for (int k = max(0, raw_issued - kStages); k < raw_issued; ++k)
+        ok = mbar_wait_bounded(&sh.raw_full[k % kStages], (k / kStages) & 1, &never) && ok;
+      if (q_issued > 0) ok = mbar_wait_bounded(&sh.q_full, (q_issued - 1) & 1, &never) && ok;
+    }
+    if (!ok) atomicExch(&sh.status, XQA_ERR_DRAIN_TIMEOUT);
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(sh.tmem, 512);
+  if (threadIdx.x == 0) {
+    if (sh.wait_limit == 0) record_status(&sh.status, XQA_ERR_DEVICE_TIMEOUT);
+    p.status[blockIdx.x] = sh.status;
+    if (blockIdx.x == 0) p.header[0] = gridDim.x;
+  }
+}
+
+template <int kFmt, int kType>
+cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                   const ExtendParams& p, const cudaLaunchConfig_t& cfg) {
+  return cudaLaunchKernelEx(&cfg, extend_kernel<kFmt, kType>, tm_q, tm_k, tm_v, p);
+}
+
+template <int kFmt, int kType>
+cudaError_t set_attribute() {
+  return cudaFuncSetAttribute(extend_kernel<kFmt, kType>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kExtendSmem);
+}
+
+}  // namespace
+
+cudaError_t launch_extend(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                          const ExtendParams& p, int dtype, int ctas, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kExtendThreads);
+  cfg.dynamicSmemBytes = kExtendSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const bool f16 = dtype == XQA_F16;
+  switch (p.kv_dtype) {
+    case XQA_KV_E5M2:
+      return f16 ? launch<XQA_KV_E5M2, XQA_F16>(tm_q, tm_k, tm_v, p, cfg)
+                 : launch<XQA_KV_E5M2, XQA_BF16>(tm_q, tm_k, tm_v, p, cfg);
+    case XQA_KV_E4M3:
+      return f16 ? launch<XQA_KV_E4M3, XQA_F16>(tm_q, tm_k, tm_v, p, cfg)
+                 : launch<XQA_KV_E4M3, XQA_BF16>(tm_q, tm_k, tm_v, p, cfg);
+    default:
+      return f16 ? launch<XQA_KV_E2M1, XQA_F16>(tm_q, tm_k, tm_v, p, cfg)
+                 : launch<XQA_KV_E2M1, XQA_BF16>(tm_q, tm_k, tm_v, p, cfg);
+  }
+}
+
+cudaError_t set_extend_attributes() {
+  cudaError_t e;
+  if ((e = set_attribute<XQA_KV_E5M2, XQA_F16>()) != cudaSuccess) return e;
+  if ((e = set_attribute<XQA_KV_E5M2, XQA_BF16>()) != cudaSuccess) return e;
+  if ((e = set_attribute<XQA_KV_E4M3, XQA_F16>()) != cudaSuccess) return e;
+  if ((e = set_attribute<XQA_KV_E4M3, XQA_BF16>()) != cudaSuccess) return e;
+  if ((e = set_attribute<XQA_KV_E2M1, XQA_F16>()) != cudaSuccess) return e;
+  return set_attribute<XQA_KV_E2M1, XQA_BF16>();
+}
+
+}  // namespace xqa

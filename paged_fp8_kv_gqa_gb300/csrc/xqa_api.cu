@@ -16,6 +16,7 @@
 namespace xqa {
 cudaError_t set_partial_attributes();
 cudaError_t set_prefill_attributes();
+cudaError_t set_extend_attributes();
 }
 
 namespace {
@@ -112,7 +113,8 @@ xqa_status_t ensure_device_setup() {
   if (dev < 0 || dev >= kMaxDevices) return XQA_ERR_DEVICE;
   if (g_attrs_set[dev].load(std::memory_order_acquire) == 0) {
     if (xqa::set_partial_attributes() != cudaSuccess ||
-        xqa::set_prefill_attributes() != cudaSuccess)
+        xqa::set_prefill_attributes() != cudaSuccess ||
+        xqa::set_extend_attributes() != cudaSuccess)
       return XQA_ERR_LAUNCH;
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -421,6 +423,80 @@ xqa_status_t encode_rows_map(CUtensorMap* map, const void* base, const Side& s, 
   return res == CUDA_SUCCESS ? XQA_OK : XQA_ERR_LAUNCH;
 }
 
+// What the calls over caches ask of a cache's dimensions and format.
+bool cache_fits(int batch, int hkv, int head_dim, int block_size, int mbs, int nb, int kv_dtype,
+                int kv_layout) {
+  if (head_dim != kHeadDim || block_size != kBlockSize || batch < 1 || batch == 0x7fffffff ||
+      hkv < 1 || mbs < 1 || nb < 1)
+    return false;
+  if (kv_dtype != XQA_KV_E5M2 && kv_dtype != XQA_KV_E4M3 && kv_dtype != XQA_KV_E2M1) return false;
+  if (kv_layout != XQA_LAYOUT_HND && (kv_layout != XQA_LAYOUT_NHD || kv_dtype == XQA_KV_E2M1))
+    return false;
+  return (long long)nb * hkv < (1ll << 31) / kBlockSize;  // int32 rows of the pool
+}
+
+struct ExtendResolved {
+  Side q, out;
+  int group, ctas;
+  float sm_scale;
+  size_t bytes;
+};
+
+xqa_status_t resolve_extend(const xqa_extend_shape_t* s, ExtendResolved* r) {
+  if (!s) return XQA_ERR_NULL;
+  if (!cache_fits(s->batch, s->num_kv_heads, s->head_dim, s->block_size, s->max_blocks_per_seq,
+                  s->num_blocks, s->kv_dtype, s->kv_layout))
+    return XQA_ERR_SHAPE;
+  if (s->num_q_heads < 1 || s->num_q_heads % s->num_kv_heads != 0 || s->total_q < 0 || s->max_ctas < 0)
+    return XQA_ERR_SHAPE;
+  if (s->dtype != XQA_F16 && s->dtype != XQA_BF16) return XQA_ERR_SHAPE;
+  if (s->causal != 0 && s->causal != 1) return XQA_ERR_SHAPE;
+  r->group = s->num_q_heads / s->num_kv_heads;
+  if (r->group > 128) return XQA_ERR_SHAPE;  // a 128-row tile holds whole tokens
+  // int32 rows, keys and units on the device
+  if ((long long)s->total_q * s->num_q_heads >= (1ll << 27) || s->batch > (1 << 24) ||
+      s->num_q_heads > (1 << 20) || s->max_blocks_per_seq > (1 << 26))
+    return XQA_ERR_SHAPE;
+  if (!prefill_side(s->total_q, s->num_q_heads, s->q_row_stride, s->q_head_stride, false, &r->q) ||
+      !prefill_side(s->total_q, s->num_q_heads, s->out_row_stride, s->out_head_stride, true,
+                    &r->out))
+    return XQA_ERR_SHAPE;
+  r->sm_scale = s->sm_scale > 0.f ? s->sm_scale : (float)(1.0 / sqrt((double)kHeadDim));
+  if (!isfinite(r->sm_scale)) return XQA_ERR_SHAPE;
+  r->ctas = s->max_ctas;
+  if (r->ctas == 0) {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return XQA_ERR_DEVICE;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+      return XQA_ERR_DEVICE;
+    r->ctas = sms;
+  }
+  if (r->ctas > xqa::kMaxCtas) r->ctas = xqa::kMaxCtas;
+  // no more than the longest line of these dimensions has shares for
+  const long long seqs = s->batch < s->total_q ? s->batch : s->total_q;
+  const long long units = (s->total_q / (2 * (128 / r->group)) + seqs) * s->num_kv_heads;
+  const long long line = units * (128 + (long long)s->max_blocks_per_seq * kBlockSize);
+  if (r->ctas > line / xqa::kExtendMinShare)
+    r->ctas = line < xqa::kExtendMinShare ? 1 : (int)(line / xqa::kExtendMinShare);
+  r->bytes = kPrefillWorkspaceBytes + (size_t)r->ctas * 2 * kPieceFloats * sizeof(float);
+  return XQA_OK;
+}
+
+// Token-major pools: x = D, y = kv head, z = token row; a box is a page's 16 rows of one head.
+xqa_status_t encode_nhd_map(CUtensorMap* map, const uint8_t* pool, int hkv, int nb) {
+  cuuint32_t estr[3] = {1, 1, 1};
+  cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)hkv, (cuuint64_t)nb * kBlockSize};
+  cuuint64_t strides[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)hkv * kHeadDim};
+  cuuint32_t box[3] = {(cuuint32_t)kHeadDim, 1, (cuuint32_t)kBlockSize};
+  const CUresult res = g_encode.load(std::memory_order_acquire)(
+      map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(pool), dims, strides, box, estr,
+      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return res == CUDA_SUCCESS ? XQA_OK : XQA_ERR_LAUNCH;
+}
+
+bool good_scale(float s, const float* dev) { return dev || (s > 0.f && isfinite(s)); }
+
 xqa_status_t rows_impl(bool append, void* k, void* v, const int32_t* cu_seqlens,
                        const int32_t* block_tables, const int32_t* context_lens, float k_scale,
                        float v_scale, const float* k_scale_dev, const float* v_scale_dev,
@@ -630,6 +706,81 @@ xqa_status_t xqa_prefill(const void* q, const void* k, const void* v, const int3
   p.out_head_stride = r.out.hs;
   const cudaError_t e =
       xqa::launch_prefill(tm_q, tm_k, tm_v, p, shape->dtype, r.ctas, (cudaStream_t)stream);
+  return e == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
+}
+
+xqa_status_t xqa_extend_workspace_size(const xqa_extend_shape_t* shape, size_t* bytes) {
+  if (!bytes) return XQA_ERR_NULL;
+  ExtendResolved r;
+  const xqa_status_t st = resolve_extend(shape, &r);
+  if (st != XQA_OK) return st;
+  *bytes = r.bytes;
+  return XQA_OK;
+}
+
+xqa_status_t xqa_extend(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                        const int32_t* block_tables, const int32_t* context_lens,
+                        const int32_t* cu_seqlens, float k_scale, float v_scale,
+                        const float* k_scale_dev, const float* v_scale_dev, void* out, float* lse,
+                        const xqa_extend_shape_t* shape, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  ExtendResolved r;
+  xqa_status_t st = resolve_extend(shape, &r);
+  if (st != XQA_OK) return st;
+  if (!good_scale(k_scale, k_scale_dev) || !good_scale(v_scale, v_scale_dev)) return XQA_ERR_VALUE;
+  if (shape->total_q == 0) return XQA_OK;
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !cu_seqlens || !out || !workspace)
+    return XQA_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return XQA_ERR_ALIGN;
+  if (workspace_bytes < r.bytes) return XQA_ERR_WORKSPACE;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+    return XQA_ERR_ALIGN;
+  if ((st = ensure_device_setup()) != XQA_OK) return st;
+  const int tokens = 128 / r.group;
+  alignas(64) CUtensorMap tm_q, tm_k = {}, tm_v = {};
+  if ((st = encode_rows_map(&tm_q, q, r.q, shape->total_q, shape->num_kv_heads, r.group, tokens,
+                            shape->dtype, true)) != XQA_OK)
+    return st;
+  if (shape->kv_layout == XQA_LAYOUT_NHD &&
+      ((st = encode_nhd_map(&tm_k, k_cache, shape->num_kv_heads, shape->num_blocks)) != XQA_OK ||
+       (st = encode_nhd_map(&tm_v, v_cache, shape->num_kv_heads, shape->num_blocks)) != XQA_OK))
+    return st;
+  const xqa::WsLayout lay = xqa::ws_layout(0, 0);
+  uint8_t* base = reinterpret_cast<uint8_t*>(workspace);
+  xqa::ExtendParams p;
+  p.cu_q = cu_seqlens;
+  p.context_lens = context_lens;
+  p.block_tables = block_tables;
+  p.k_pool = k_cache;
+  p.v_pool = v_cache;
+  p.out = reinterpret_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.header = ws_i32(workspace);
+  p.tickets = reinterpret_cast<int32_t*>(base + lay.ticket_off);
+  p.status = reinterpret_cast<int32_t*>(base + lay.status_off);
+  p.piece_o = reinterpret_cast<float4*>(base + kPrefillWorkspaceBytes);
+  p.piece_ml = reinterpret_cast<float2*>(base + kPrefillWorkspaceBytes +
+                                         (size_t)r.ctas * 2 * 256 * kHeadDim * sizeof(float));
+  p.batch = shape->batch;
+  p.num_q_heads = shape->num_q_heads;
+  p.num_kv_heads = shape->num_kv_heads;
+  p.group = r.group;
+  p.total_q = shape->total_q;
+  p.causal = shape->causal;
+  p.max_blocks_per_seq = shape->max_blocks_per_seq;
+  p.num_blocks = shape->num_blocks;
+  p.kv_dtype = shape->kv_dtype;
+  p.kv_layout = shape->kv_layout;
+  p.tile_tokens = tokens;
+  p.qk_scale_base = (double)r.sm_scale * 1.4426950408889634;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.k_scale_ptr = k_scale_dev;
+  p.v_scale_ptr = v_scale_dev;
+  p.out_row_stride = r.out.rs;
+  p.out_head_stride = r.out.hs;
+  const cudaError_t e =
+      xqa::launch_extend(tm_q, tm_k, tm_v, p, shape->dtype, r.ctas, (cudaStream_t)stream);
   return e == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
 }
 

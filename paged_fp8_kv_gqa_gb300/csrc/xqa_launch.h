@@ -88,6 +88,35 @@ struct PrefillParams {
   long long v_row_stride, v_head_stride, out_row_stride, out_head_stride;
 };
 
+// The least share of the line of work (extend.cu: keys seen, summed over the units) that a
+// CTA takes; fewer CTAs work on shorter lines.
+constexpr int kExtendMinShare = 640;
+
+struct ExtendParams {
+  const int32_t* cu_q;  // [batch + 1]
+  const int32_t* context_lens;
+  const int32_t* block_tables;
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  uint16_t* out;
+  float* lse;         // optional [total_q, Hq]
+  int32_t* header;    // workspace header (CTAs launched)
+  int32_t* tickets;   // pieces written, by the CTA of a unit's first: zero between calls
+  int32_t* status;    // [kMaxCtas]
+  float4* piece_o;    // [CTAs][2][2 row tiles][32 chunks of 4 dims][128 rows]
+  float2* piece_ml;   // [CTAs][2][2][128]
+  int batch, num_q_heads, num_kv_heads, group, total_q, causal;
+  int max_blocks_per_seq, num_blocks, kv_dtype, kv_layout;
+  int tile_tokens;    // T: tokens of a 128-row tile
+  double qk_scale_base;      // sm_scale * log2(e); the logit scale is this * k_scale
+  float k_scale, v_scale;    // per-tensor scales (used when the pointers are null)
+  const float* k_scale_ptr;
+  const float* v_scale_ptr;
+  long long out_row_stride, out_head_stride;
+};
+
+cudaError_t launch_extend(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                          const ExtendParams& p, int dtype, int ctas, cudaStream_t stream);
 cudaError_t launch_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                            const CUtensorMap& tm_v, const PrefillParams& p, int dtype, int ctas,
                            cudaStream_t stream);
