@@ -61,7 +61,8 @@ typedef enum xqa_status {
   XQA_ERR_DEVICE_TIMEOUT = 18,  /* a pipeline or merge-ticket wait exceeded its time budget */
   XQA_ERR_DRAIN_TIMEOUT = 19,   /* after a timeout, a copy was still in flight when its
                                    CTA exited: the device state is not to be trusted */
-  XQA_ERR_BAD_OFFSETS = 20      /* cu_seqlens descending, negative or past the rows */
+  XQA_ERR_BAD_OFFSETS = 20,     /* cu_seqlens descending, negative or past the rows */
+  XQA_ERR_NO_PAGES = 21         /* no free page is left (or no room among the free pages) */
 } xqa_status_t;
 
 /* KV cache code formats (xqa_shape_t.kv_dtype). */
@@ -406,6 +407,148 @@ xqa_status_t xqa_extend(const void* q, const uint8_t* k_cache, const uint8_t* v_
                         const float* k_scale_dev, const float* v_scale_dev, void* out, float* lse,
                         const xqa_extend_shape_t* shape, void* workspace, size_t workspace_bytes,
                         void* stream);
+
+/* Pages of sequences that grow and end. The pool's free pages are a stack, free_pages[0 ..
+ * num_free). */
+typedef struct xqa_pages {
+  int32_t batch;              /* B: sequences (places for them), 1 .. 16384 */
+  int32_t block_size;         /* BS = 16 tokens per page */
+  int32_t max_blocks_per_seq; /* MBS: row length of block_tables (< 2^27) */
+  int32_t num_blocks;         /* NB: pages in the pool, entries of free_pages (< 2^27) */
+  int32_t num_rows;           /* entries of slots and positions (< 2^30): the most new tokens
+                                 that a call may assign; not used by xqa_release_pages */
+} xqa_pages_t;
+
+/* A step's block tables, offsets, slots and positions from the tokens that each sequence
+ * gains.
+ *
+ *   new_tokens    device, int32 [B]: tokens that sequence b gains, 0 for none
+ *   context_lens  device, int32 [B]: its tokens before
+ *   block_tables  device, int32 [B, MBS]: entries ceil(c / 16) .. ceil((c + n) / 16) - 1 of
+ *                 row b are written, the others left as they are
+ *   free_pages    device, int32 [NB]; num_free: device, int32 [1]. Pages are taken from the
+ *                 stack's end, sequence after sequence, each one's in the order of its table
+ *   new_lens      device, int32 [B]: tokens after the step; may be context_lens
+ *   new_free      device, int32 [1]: pages left; may be num_free
+ *   cu_seqlens    device, int32 [B+1]: offsets of the new tokens' rows
+ *   slots         device, int32 [num_rows], or NULL: page * 16 + position % 16 of each new
+ *                 token; -1 in rows behind the last one
+ *   positions     device, int32 [num_rows], or NULL: its position in the sequence, or -1
+ *   device_status device int32 or NULL: receives the first of these errors if it holds
+ *                 XQA_OK. A sequence that meets one gains nothing in this call, the others
+ *                 do: XQA_ERR_CTX_TOO_LONG (a negative number or length, or more than MBS *
+ *                 16 tokens), XQA_ERR_BAD_OFFSETS (its rows would pass num_rows; so would
+ *                 every later one's with new tokens), XQA_ERR_NO_PAGES (the stack has too few
+ *                 pages for it and those before it; later ones that need no page are
+ *                 served). XQA_ERR_BAD_BLOCK_ID: a page outside [0, NB) in the stack or the
+ *                 table; entries are written as they are, slots as -1
+ *
+ * What the next calls take: block_tables and new_lens as context_lens for all of them,
+ * cu_seqlens for xqa_append, xqa_page_bounds and xqa_extend. One kernel, no host
+ * synchronisation, no workspace; may be captured into a CUDA graph. */
+xqa_status_t xqa_assign_pages(const int32_t* new_tokens, const int32_t* context_lens,
+                              int32_t* block_tables, const int32_t* free_pages,
+                              const int32_t* num_free, int32_t* new_lens, int32_t* new_free,
+                              int32_t* cu_seqlens, int32_t* slots, int32_t* positions,
+                              const xqa_pages_t* pages, int32_t* device_status, void* stream);
+
+/* Pages of ended sequences back onto the stack: those of every b with done[b] != 0, in the
+ * order of b and of its table, and new_lens[b] = 0 (context_lens[b] where done[b] is 0).
+ *
+ *   done          device, uint8 [B]
+ *   block_tables  device, int32 [B, MBS]; not written: entries past a length are never read
+ *   new_lens, new_free  as for xqa_assign_pages; free_pages[num_free ..] is written
+ *   device_status as for xqa_assign_pages: XQA_ERR_BAD_BLOCK_ID (an entry outside [0, NB):
+ *                 it is left out), XQA_ERR_CTX_TOO_LONG (a length below 0 or above MBS * 16:
+ *                 none of the sequence's pages goes back), XQA_ERR_NO_PAGES (more than NB
+ *                 pages would be free: those past NB are dropped)
+ * A page must not go back twice. One kernel, no host synchronisation, no workspace; may be
+ * captured into a CUDA graph. */
+xqa_status_t xqa_release_pages(const uint8_t* done, const int32_t* context_lens,
+                               const int32_t* block_tables, int32_t* free_pages,
+                               const int32_t* num_free, int32_t* new_lens, int32_t* new_free,
+                               const xqa_pages_t* pages, int32_t* device_status, void* stream);
+
+/* Bytes of a (page, kv head) slice of the bounds: 128 upper bounds (int8), 128 lower bounds
+ * (int8), the exponent e (int8), 15 zeros. For every token t of the page that is in use
+ * and every dim d: lower[d] * 2^e <= key[t][d] <= upper[d] * 2^e, the key before k_scale,
+ * with 2^(e+6) <= max |key| < 2^(e+7) over the slice (e = 0 where all keys are 0) and the
+ * bounds rounded away from the keys to whole numbers. e = -128, bounds 0: a key is not
+ * finite. */
+#define XQA_BOUNDS_BYTES 272
+
+/* Bounds of the pages that a step's new tokens touched, computed anew from all their tokens.
+ *
+ *   k_cache, block_tables, context_lens, cu_seqlens  as for xqa_append, after it
+ *   bounds        device, uint8 [NB, Hkv, XQA_BOUNDS_BYTES], 16-byte aligned
+ *   rows          dimensions as for xqa_append; dtype and strides play no part
+ *   device_status device int32 or NULL: as for xqa_append; pages that it would not write
+ *                 keep their bounds
+ * One kernel, no host synchronisation, no workspace; may be captured into a CUDA graph. */
+xqa_status_t xqa_page_bounds(const uint8_t* k_cache, const int32_t* block_tables,
+                             const int32_t* context_lens, const int32_t* cu_seqlens,
+                             uint8_t* bounds, const xqa_rows_t* rows, int32_t* device_status,
+                             void* stream);
+
+/* Problem dimensions of xqa_select. */
+typedef struct xqa_select_shape {
+  int32_t batch;              /* B: sequences, >= 1 */
+  int32_t num_q_heads;        /* Hq, a multiple of Hkv; G = Hq / Hkv <= 16 */
+  int32_t num_kv_heads;       /* Hkv */
+  int32_t head_dim;           /* D = 128 */
+  int32_t block_size;         /* BS = 16 tokens per page */
+  int32_t max_blocks_per_seq; /* MBS: row length of block_tables */
+  int32_t num_blocks;         /* NB: pages in the pool */
+  int32_t max_pages;          /* K: row length of selected */
+  int32_t first_pages;        /* a sequence's first pages that are always taken, >= 0 */
+  int32_t last_pages;         /* its last ones, >= 1 (the new token's page among them);
+                                 first_pages + last_pages <= max_pages */
+  int32_t max_ctas;           /* upper bound on CTAs; 0 = 4 per SM */
+} xqa_select_shape_t;
+
+/* Bytes of device workspace xqa_select needs for `shape`. Host only. */
+xqa_status_t xqa_select_workspace_size(const xqa_select_shape_t* shape, size_t* bytes);
+
+/* The pages that each sequence's new token is to read, for each kv head: all of them if
+ * there are at most K, else the first and last ones and of the others those with the
+ * highest scores, the lower page first among equal ones.
+ *
+ *   q             device, fp16 [B, Hq, 128], contiguous, 16-byte aligned
+ *   bounds        device, as xqa_page_bounds writes them, up to date for every page of the
+ *                 sequences
+ *   block_tables, context_lens  device, as for xqa_decode
+ *   selected      device, int32 [B, Hkv, K]: pages (ids of the pool) in the order of the
+ *                 sequence, -1 behind the last
+ *   selected_lens device, int32 [B, Hkv]: tokens in them; what xqa_decode_selected takes
+ *   workspace     device, >= xqa_select_workspace_size bytes, 256-byte aligned, zero-filled
+ *                 once before its first use; every completed call leaves it ready for the
+ *                 next. Not one that other calls use, nor one of another shape
+ *
+ * score(page) = 2^e * sum_d (A_d * upper_d + B_d * lower_d), where A_d (B_d) is the sum of
+ * the positive (negative) q8_gd over the G heads, q8 = q / 2^f rounded to nearest even, f
+ * the whole number with 2^(f+5) <= max |q| < 2^(f+6) over the group's finite values (others
+ * count as 0). The sum is in whole numbers and exact: a choice does not depend on the split
+ * of the work or on the batch. Pages whose keys are not finite come before all scores, and
+ * so do those whose id is outside [0, NB) (XQA_ERR_BAD_BLOCK_ID, see xqa_read_status):
+ * xqa_decode_selected then meets them. A length below 0 or above MBS * 16
+ * (XQA_ERR_CTX_TOO_LONG) gives selected_lens -1. One kernel, no host synchronisation; may
+ * be captured into a CUDA graph. */
+xqa_status_t xqa_select(const void* q, const uint8_t* bounds, const int32_t* block_tables,
+                        const int32_t* context_lens, int32_t* selected, int32_t* selected_lens,
+                        const xqa_select_shape_t* shape, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* xqa_decode over a table of its own for each (sequence, kv head): selected, int32 [B, Hkv,
+ * K] with K = shape->max_blocks_per_seq, and selected_lens, int32 [B, Hkv], in place of
+ * block_tables and context_lens (all pages but the last of a row are full). One new token
+ * for each sequence (q_len 0 or 1); several go as so many sequences. k_scale_dev and
+ * v_scale_dev: both NULL, or both pointers to one device float. Everything else is as for
+ * xqa_decode, the workspace included. */
+xqa_status_t xqa_decode_selected(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                 const int32_t* selected, const int32_t* selected_lens,
+                                 float k_scale, float v_scale, const float* k_scale_dev,
+                                 const float* v_scale_dev, void* out, const xqa_shape_t* shape,
+                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /* Self-check of the device-side failure detection: launches one CTA whose
  * threads wait, through the same bounded mbarrier wait the attention kernel

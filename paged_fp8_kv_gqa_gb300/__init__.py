@@ -11,7 +11,9 @@ The names mirror the C ABI declared in ``include/xqa.h``:
 ``xqa_dequant_e4m3``, ``xqa_read_status``, ``xqa_read_plan``, ``xqa_status_string``,
 ``xqa_decode_static_workspace``, ``xqa_kernels_per_call``, ``xqa_append``,
 ``xqa_gather``, ``xqa_prefill``, ``xqa_prefill_workspace_size``, ``xqa_extend``,
-``xqa_extend_workspace_size``.
+``xqa_extend_workspace_size``, ``xqa_assign_pages``, ``xqa_release_pages``,
+``xqa_page_bounds``, ``xqa_select``, ``xqa_select_workspace_size``,
+``xqa_decode_selected``.
 """
 from __future__ import annotations
 
@@ -37,6 +39,7 @@ XQA_ERR_CTX_TOO_LONG = 17
 XQA_ERR_DEVICE_TIMEOUT = 18
 XQA_ERR_DRAIN_TIMEOUT = 19
 XQA_ERR_BAD_OFFSETS = 20
+XQA_ERR_NO_PAGES = 21
 
 #: C symbols the library exports (kept in step with include/xqa.h).
 EXPORTED = (
@@ -60,12 +63,20 @@ EXPORTED = (
     "xqa_prefill_workspace_size",
     "xqa_extend",
     "xqa_extend_workspace_size",
+    "xqa_assign_pages",
+    "xqa_release_pages",
+    "xqa_page_bounds",
+    "xqa_select",
+    "xqa_select_workspace_size",
+    "xqa_decode_selected",
 )
 
 KV_DTYPES = {"e5m2": 0, "e4m3": 1, "e2m1": 4}
 KV_LAYOUTS = {"hnd": 0, "nhd": 1}
 #: bytes of a (page, kv head) slice of a 4-bit cache (XQA_E2M1_SLICE_BYTES)
 E2M1_SLICE_BYTES = 1152
+#: bytes of a (page, kv head) slice of the bounds (XQA_BOUNDS_BYTES)
+BOUNDS_BYTES = 272
 ROW_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 _F16, _U8, _I32 = torch.float16, torch.uint8, torch.int32
 
@@ -124,6 +135,21 @@ class XqaExtendShape(ctypes.Structure):
         "q_row_stride", "q_head_stride", "out_row_stride", "out_head_stride")]
 
 
+class XqaPages(ctypes.Structure):
+    """Mirror of ``xqa_pages_t``."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "block_size", "max_blocks_per_seq", "num_blocks", "num_rows")]
+
+
+class XqaSelectShape(ctypes.Structure):
+    """Mirror of ``xqa_select_shape_t``."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "num_q_heads", "num_kv_heads", "head_dim", "block_size", "max_blocks_per_seq",
+        "num_blocks", "max_pages", "first_pages", "last_pages", "max_ctas")]
+
+
 class XqaError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = int(code)
@@ -141,6 +167,8 @@ _STRIDES_AT, _OUT_AT = XqaPrefillShape.q_row_stride.offset, XqaPrefillShape.out_
 _ROWS = ctypes.POINTER(XqaRows)
 _PREFILL = ctypes.POINTER(XqaPrefillShape)
 _EXTEND = ctypes.POINTER(XqaExtendShape)
+_PAGES = ctypes.POINTER(XqaPages)
+_SELECT = ctypes.POINTER(XqaSelectShape)
 _SIGS = {
     "xqa_workspace_size": [_SHAPE, ctypes.POINTER(_SZ)],
     "xqa_decode": [_P, _P, _P, _P, _P, _F, _F, _P, _SHAPE, _P, _SZ, _P],
@@ -160,6 +188,12 @@ _SIGS = {
     "xqa_prefill_workspace_size": [_PREFILL, ctypes.POINTER(_SZ)],
     "xqa_extend": [_P, _P, _P, _P, _P, _P, _F, _F, _P, _P, _P, _P, _EXTEND, _P, _SZ, _P],
     "xqa_extend_workspace_size": [_EXTEND, ctypes.POINTER(_SZ)],
+    "xqa_assign_pages": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _PAGES, _P, _P],
+    "xqa_release_pages": [_P, _P, _P, _P, _P, _P, _P, _PAGES, _P, _P],
+    "xqa_page_bounds": [_P, _P, _P, _P, _P, _ROWS, _P, _P],
+    "xqa_select": [_P, _P, _P, _P, _P, _P, _SELECT, _P, _SZ, _P],
+    "xqa_select_workspace_size": [_SELECT, ctypes.POINTER(_SZ)],
+    "xqa_decode_selected": [_P, _P, _P, _P, _P, _F, _F, _P, _P, _P, _SHAPE, _P, _SZ, _P],
     "xqa_append": [_P, _P, _P, _P, _P, _F, _F, _P, _P, _P, _P, _ROWS, _P, _P],
     "xqa_gather": [_P, _P, _P, _P, _P, _F, _F, _P, _P, _P, _P, _ROWS, _P, _P],
 }
@@ -836,6 +870,300 @@ def xqa_extend(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, k_sc
         ctypes.byref(shape), _on(workspace, _U8, dev, "workspace"), workspace.numel(), handle)
     if code:
         raise XqaError(code, "xqa_extend")
+    return out
+
+
+_BOOL = torch.bool
+
+
+@functools.lru_cache(maxsize=1024)
+def _pages_descriptor(n_lens: int, bt_shape, n_free: int, n_first: int, num_rows: int, *single) -> XqaPages:
+    """The descriptor of calls with tensors of these sizes, checked (n_first: entries of
+    new_tokens or done; single: sizes that have to be 1, B or B + 1 with what they have to be)."""
+    if len(bt_shape) != 2 or bt_shape[0] != n_lens or n_first != n_lens:
+        raise ValueError("inconsistent context_lens / block_tables / new_tokens or done")
+    for have, want in zip(single[::2], single[1::2]):
+        if have != want:
+            raise ValueError(f"a tensor has {have} entries where {want} are needed")
+    return XqaPages(n_lens, 16, bt_shape[1], n_free, num_rows)
+
+
+def _all_i32(dev: int, *tensors) -> bool:
+    for t in tensors:
+        if not (t.dtype is _I32 and t.get_device() == dev and t.is_contiguous()):
+            return False
+    return True
+
+
+def xqa_assign_pages(new_tokens, context_lens, block_tables, free_pages, num_free, num_rows: int,
+                     new_lens=None, new_free=None, cu_seqlens=None, slots=None, positions=None,
+                     status=None, stream=None):
+    """Give a step's new tokens their pages. new_tokens, context_lens: int32 [B];
+    block_tables: int32 [B, MBS], written where a sequence gets a page; free_pages: int32
+    [NB], of which the first ``num_free`` (int32 CUDA tensor of one element) are a stack of
+    free pages. context_lens and num_free become what they are after the step, or stay if
+    ``new_lens`` and ``new_free`` are passed. Returns (cu_seqlens [B+1], slots [num_rows],
+    positions [num_rows]), int32: the new tokens' offsets, and for each the slot page * 16 +
+    position % 16 and the position (-1 in rows behind the last). A sequence that cannot be
+    served gains nothing; ``status`` (int32 CUDA tensor, optional) receives the first error
+    of that kind."""
+    new_lens = context_lens if new_lens is None else new_lens
+    new_free = num_free if new_free is None else new_free
+    pages = None
+    try:  # the usual call, without a function call for each tensor
+        dev = context_lens.get_device()
+        if dev >= 0 and torch._C._cuda_getDevice() == dev and _all_i32(
+                dev, new_tokens, context_lens, block_tables, free_pages, num_free, new_lens, new_free):
+            n, num_rows = context_lens.numel(), int(num_rows)
+            if num_rows < 0:
+                raise ValueError("num_rows must not be negative")
+            with _allocating(stream) if stream is not None else _NO_CONTEXT:
+                if cu_seqlens is None:
+                    cu_seqlens = torch.empty(n + 1, dtype=_I32, device=context_lens.device)
+                if slots is None:
+                    slots = torch.empty(num_rows, dtype=_I32, device=context_lens.device)
+                if positions is None:
+                    positions = torch.empty(num_rows, dtype=_I32, device=context_lens.device)
+            if _all_i32(dev, cu_seqlens, slots, positions):
+                pages = _pages_descriptor(n, block_tables.shape, free_pages.numel(), new_tokens.numel(),
+                                          num_rows, num_free.numel(), 1, new_free.numel(), 1,
+                                          new_lens.numel(), n, cu_seqlens.numel(), n + 1,
+                                          slots.numel(), num_rows, positions.numel(), num_rows)
+    except AttributeError:
+        pass
+    if pages is None:
+        _on_current(*[(t, _I32, name) for t, name in (
+            (new_tokens, "new_tokens"), (context_lens, "context_lens"), (block_tables, "block_tables"),
+            (free_pages, "free_pages"), (num_free, "num_free"), (new_lens, "new_lens"),
+            (new_free, "new_free"), (cu_seqlens, "cu_seqlens"), (slots, "slots"),
+            (positions, "positions")) if t is not None or name not in ("cu_seqlens", "slots", "positions")])
+        raise ValueError("invalid arguments")
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _device_stream(stream)[1]
+    code = load_library().xqa_assign_pages(
+        new_tokens.data_ptr(), context_lens.data_ptr(), block_tables.data_ptr(), free_pages.data_ptr(),
+        num_free.data_ptr(), new_lens.data_ptr(), new_free.data_ptr(), cu_seqlens.data_ptr(),
+        slots.data_ptr(), positions.data_ptr(), ctypes.byref(pages),
+        None if status is None else _on(status, _I32, dev, "status"), handle)
+    if code:
+        raise XqaError(code, "xqa_assign_pages")
+    return cu_seqlens, slots, positions
+
+
+def xqa_release_pages(done, context_lens, block_tables, free_pages, num_free, new_lens=None,
+                      new_free=None, status=None, stream=None) -> None:
+    """Put the pages of ended sequences back: those of every b with ``done[b]`` (bool or uint8
+    [B]) go onto the stack free_pages[:num_free], and its length becomes 0. Other arguments
+    as for xqa_assign_pages."""
+    new_lens = context_lens if new_lens is None else new_lens
+    new_free = num_free if new_free is None else new_free
+    pages = None
+    try:  # the usual call, without a function call for each tensor
+        dev = context_lens.get_device()
+        if (dev >= 0 and torch._C._cuda_getDevice() == dev
+                and (done.dtype is _BOOL or done.dtype is _U8) and done.get_device() == dev
+                and done.is_contiguous()
+                and _all_i32(dev, context_lens, block_tables, free_pages, num_free, new_lens, new_free)):
+            n = context_lens.numel()
+            pages = _pages_descriptor(n, block_tables.shape, free_pages.numel(), done.numel(), 0,
+                                      num_free.numel(), 1, new_free.numel(), 1, new_lens.numel(), n)
+    except AttributeError:
+        pass
+    if pages is None:
+        _on_current(*[(t, _I32, name) for t, name in (
+            (context_lens, "context_lens"), (block_tables, "block_tables"), (free_pages, "free_pages"),
+            (num_free, "num_free"), (new_lens, "new_lens"), (new_free, "new_free"))])
+        _on_current((done, _U8, "done"))
+        raise ValueError("invalid arguments")
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _device_stream(stream)[1]
+    code = load_library().xqa_release_pages(
+        done.data_ptr(), context_lens.data_ptr(), block_tables.data_ptr(), free_pages.data_ptr(),
+        num_free.data_ptr(), new_lens.data_ptr(), new_free.data_ptr(), ctypes.byref(pages),
+        None if status is None else _on(status, _I32, dev, "status"), handle)
+    if code:
+        raise XqaError(code, "xqa_release_pages")
+
+
+def alloc_bounds(k_cache, kv_dtype: str = "e5m2", kv_layout: str = "hnd") -> torch.Tensor:
+    """A zero-filled uint8 buffer [num_blocks, Hkv, 272] for the bounds of k_cache's pages."""
+    nb, hkv, _ = _cache_dims(k_cache, kv_dtype, kv_layout)
+    return torch.zeros((nb, hkv, BOUNDS_BYTES), dtype=_U8, device=k_cache.device)
+
+
+@functools.lru_cache(maxsize=1024)
+def _bounds_descriptor(kc_shape, bounds_shape, bt_shape, n_lens: int, n_cu: int, num_rows: int,
+                       kv_dtype, kv_layout) -> XqaRows:
+    nb, hkv, bs = _cache_shape(kc_shape, kv_dtype, kv_layout)
+    if (tuple(bounds_shape) != (nb, hkv, BOUNDS_BYTES) or len(bt_shape) != 2 or bt_shape[0] != n_lens
+            or n_cu != n_lens + 1):
+        raise ValueError("inconsistent k_cache / bounds / block_tables / cu_seqlens shapes")
+    return XqaRows(n_lens, hkv, 128, bs, bt_shape[1], nb, num_rows, KV_DTYPES[kv_dtype],
+                   KV_LAYOUTS[kv_layout])
+
+
+def xqa_page_bounds(k_cache, block_tables, context_lens, cu_seqlens, num_rows: int, bounds,
+                    kv_dtype: str = "e5m2", kv_layout: str = "hnd", status=None, stream=None) -> None:
+    """Bring ``bounds`` (uint8 [NB, Hkv, 272], see alloc_bounds) up to date for the pages that a
+    step's new tokens touched: after xqa_append, with its cu_seqlens and context_lens.
+    ``num_rows``: rows of that call (cu_seqlens[-1] or more)."""
+    rows = None
+    try:  # the usual call, without a function call for each tensor
+        dev = k_cache.get_device()
+        if (dev >= 0 and torch._C._cuda_getDevice() == dev and k_cache.dtype is _U8
+                and k_cache.is_contiguous() and bounds.dtype is _U8 and bounds.get_device() == dev
+                and bounds.is_contiguous() and _all_i32(dev, block_tables, context_lens, cu_seqlens)):
+            rows = _bounds_descriptor(k_cache.shape, bounds.shape, block_tables.shape,
+                                      context_lens.numel(), cu_seqlens.numel(), int(num_rows), kv_dtype,
+                                      kv_layout)
+    except AttributeError:
+        pass
+    if rows is None:
+        _on_current((k_cache, _U8, "k_cache"), (bounds, _U8, "bounds"), (block_tables, _I32, "block_tables"),
+                    (context_lens, _I32, "context_lens"), (cu_seqlens, _I32, "cu_seqlens"))
+        raise ValueError("invalid arguments")
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _device_stream(stream)[1]
+    code = load_library().xqa_page_bounds(
+        k_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), cu_seqlens.data_ptr(),
+        bounds.data_ptr(), ctypes.byref(rows), None if status is None else _on(status, _I32, dev, "status"),
+        handle)
+    if code:
+        raise XqaError(code, "xqa_page_bounds")
+
+
+def make_select_shape(q, bounds, block_tables, max_pages: int, first_pages: int = 1,
+                      last_pages: int = 1, max_ctas: int = 0) -> XqaSelectShape:
+    """Shape descriptor of xqa_select from q [B, Hq, 128], bounds [NB, Hkv, 272] and
+    block_tables [B, MBS]. It holds for every call with tensors of these shapes."""
+    if q.dim() != 3 or bounds.dim() != 3 or block_tables.dim() != 2:
+        raise ValueError("q must be [B, Hq, 128], bounds [NB, Hkv, 272], block_tables [B, MBS]")
+    if block_tables.shape[0] != q.shape[0] or bounds.shape[2] != BOUNDS_BYTES:
+        raise ValueError("inconsistent q / bounds / block_tables shapes")
+    return XqaSelectShape(q.shape[0], q.shape[1], bounds.shape[1], q.shape[2], 16,
+                          block_tables.shape[1], bounds.shape[0], int(max_pages), int(first_pages),
+                          int(last_pages), int(max_ctas))
+
+
+def xqa_select_workspace_size(shape: XqaSelectShape) -> int:
+    n = _SZ(0)
+    _check(load_library().xqa_select_workspace_size(ctypes.byref(shape), ctypes.byref(n)),
+           "xqa_select_workspace_size")
+    return int(n.value)
+
+
+def alloc_select_workspace(shape: XqaSelectShape, device=None) -> torch.Tensor:
+    """A zero-filled uint8 device buffer of xqa_select_workspace_size bytes; every call
+    leaves it ready for the next."""
+    return torch.zeros(xqa_select_workspace_size(shape), dtype=torch.uint8, device=device or "cuda")
+
+
+@functools.lru_cache(maxsize=1024)
+def _select_fits(shape: bytes, q, bounds, block_tables, n_lens: int, selected, selected_lens) -> bool:
+    """Raises unless tensors of these shapes are what the descriptor says."""
+    s = XqaSelectShape.from_buffer_copy(shape)
+    if (tuple(q) != (s.batch, s.num_q_heads, s.head_dim)
+            or tuple(bounds) != (s.num_blocks, s.num_kv_heads, BOUNDS_BYTES)
+            or tuple(block_tables) != (s.batch, s.max_blocks_per_seq) or n_lens != s.batch):
+        raise ValueError("q, bounds, block_tables or context_lens do not match the shape descriptor")
+    if (tuple(selected) != (s.batch, s.num_kv_heads, s.max_pages)
+            or tuple(selected_lens) != (s.batch, s.num_kv_heads)):
+        raise ValueError("selected must be [B, Hkv, max_pages], selected_lens [B, Hkv]")
+    return True
+
+
+def xqa_select(q, bounds, block_tables, context_lens, max_pages: int = 0, first_pages: int = 1,
+               last_pages: int = 1, selected=None, selected_lens=None, workspace=None,
+               shape: XqaSelectShape | None = None, stream=None):
+    """Choose the pages that each sequence's new token reads, for each kv head. q: fp16 [B, Hq,
+    128]; bounds: uint8 [NB, Hkv, 272] (xqa_page_bounds); block_tables int32 [B, MBS];
+    context_lens int32 [B]. Of a sequence with more than ``max_pages`` pages the first
+    ``first_pages`` and last ``last_pages`` are taken, and of the others those with the
+    highest scores (see include/xqa.h). Returns (selected int32 [B, Hkv, max_pages], -1
+    behind the last page, and selected_lens int32 [B, Hkv]) for xqa_decode_selected."""
+    if shape is None:
+        shape = make_select_shape(q, bounds, block_tables, max_pages, first_pages, last_pages)
+    fits = False
+    try:  # the usual call, without a function call for each tensor
+        dev = q.get_device()
+        if (dev >= 0 and torch._C._cuda_getDevice() == dev and q.dtype is _F16 and q.is_contiguous()
+                and bounds.dtype is _U8 and bounds.get_device() == dev and bounds.is_contiguous()
+                and _all_i32(dev, block_tables, context_lens)):
+            with _allocating(stream) if stream is not None else _NO_CONTEXT:
+                if selected is None:
+                    selected = torch.empty((shape.batch, shape.num_kv_heads, max(shape.max_pages, 0)),
+                                           dtype=_I32, device=q.device)
+                if selected_lens is None:
+                    selected_lens = torch.empty((shape.batch, shape.num_kv_heads), dtype=_I32,
+                                                device=q.device)
+                if workspace is None:
+                    workspace = alloc_select_workspace(shape, q.device)
+            fits = _all_i32(dev, selected, selected_lens) and _select_fits(
+                bytes(shape), q.shape, bounds.shape, block_tables.shape, context_lens.numel(),
+                selected.shape, selected_lens.shape)
+    except AttributeError:
+        pass
+    if not fits:
+        _on_current((q, _F16, "q"), (bounds, _U8, "bounds"), (block_tables, _I32, "block_tables"),
+                    (context_lens, _I32, "context_lens"),
+                    *[(t, _I32, n) for t, n in ((selected, "selected"), (selected_lens, "selected_lens"))
+                      if t is not None])
+        raise ValueError("invalid arguments")
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _device_stream(stream)[1]
+    code = load_library().xqa_select(
+        q.data_ptr(), bounds.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+        selected.data_ptr(), selected_lens.data_ptr(), ctypes.byref(shape),
+        _on(workspace, _U8, dev, "workspace"), workspace.numel(), handle)
+    if code:
+        raise XqaError(code, "xqa_select")
+    return selected, selected_lens
+
+
+def make_selected_shape(q, k_cache, selected, sm_scale: float = 0.0, max_ctas: int = 0,
+                        min_pages_per_cta: int = 0, merge_mode: int = 0, kv_dtype: str = "e5m2",
+                        kv_layout: str = "hnd") -> XqaShape:
+    """Shape descriptor of xqa_decode_selected from q [B, Hq, 128], k_cache and selected [B,
+    Hkv, K]; for alloc_workspace too."""
+    if selected.dim() != 3 or q.dim() != 3:
+        raise ValueError("q must be [B, Hq, 128], selected [B, Hkv, K]")
+    shape = make_shape(q, k_cache, selected[:, 0], sm_scale, max_ctas, min_pages_per_cta, merge_mode,
+                       kv_dtype, kv_layout)
+    if selected.shape[1] != shape.num_kv_heads:
+        raise ValueError("selected must have a row for each kv head")
+    return shape
+
+
+def xqa_decode_selected(q, k_cache, v_cache, selected, selected_lens, k_scale, v_scale, out=None,
+                        workspace=None, shape: XqaShape | None = None, stream=None,
+                        sm_scale: float = 0.0, max_ctas: int = 0, min_pages_per_cta: int = 0,
+                        kv_dtype: str = "e5m2", kv_layout: str = "hnd"):
+    """xqa_decode over a table of its own for each (sequence, kv head): selected int32 [B, Hkv,
+    K] and selected_lens int32 [B, Hkv] (xqa_select) in place of block_tables and
+    context_lens. q: fp16 [B, Hq, 128]. Returns ``out``, like q."""
+    if shape is None:
+        shape = make_selected_shape(q, k_cache, selected, sm_scale, max_ctas, min_pages_per_cta,
+                                    kv_dtype=kv_dtype, kv_layout=kv_layout)
+    if selected.dim() != 3 or tuple(selected.shape) != (shape.batch, shape.num_kv_heads,
+                                                        shape.max_blocks_per_seq):
+        raise ValueError("selected does not match the shape descriptor")
+    if tuple(selected_lens.shape) != (shape.batch, shape.num_kv_heads):
+        raise ValueError("selected_lens must be [B, Hkv]")
+    fresh = out is None
+    if out is None or workspace is None:
+        with _allocating(stream) if stream is not None else _NO_CONTEXT:
+            if out is None:
+                out = torch.empty_like(q)
+            if workspace is None:
+                workspace = alloc_workspace(shape, q.device)
+    a = _decode_args(q, k_cache, v_cache, selected.view(-1, selected.shape[2]),
+                     selected_lens, out, workspace, shape, fresh=fresh)
+    dev = q.get_device()
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
+    ks, ksp = (k_scale, None) if type(k_scale) is float else _scale_arg(k_scale, dev, "k_scale")
+    vs, vsp = (v_scale, None) if type(v_scale) is float else _scale_arg(v_scale, dev, "v_scale")
+    if (ksp is None) != (vsp is None):
+        raise ValueError("k_scale and v_scale must both be numbers, or both CUDA tensors")
+    code = load_library().xqa_decode_selected(a[0], a[1], a[2], a[3], a[4], ks, vs, ksp, vsp, a[5],
+                                              ctypes.byref(shape), a[6], workspace.numel(), handle)
+    if code:
+        raise XqaError(code, "xqa_decode_selected")
     return out
 
 

@@ -155,6 +155,12 @@ struct PageBatch {
   int seg;  // segment of the page
 };
 
+// Head of segment s within the cache. (Tables of a kv head's own, xqa_decode_selected, make
+// each (sequence, kv head) a sequence of one head; the cache has cache_heads all the same.)
+__device__ __forceinline__ int cache_head(const PartialParams& p, int s) {
+  return s - s / p.cache_heads * p.cache_heads;
+}
+
 template <int kWarps>
 __device__ __forceinline__ PageBatch load_batch(const PartialParams& p, const int32_t* segs,
                                                 int s_first, int nseg, int cbeg, int npages,
@@ -165,11 +171,11 @@ __device__ __forceinline__ PageBatch load_batch(const PartialParams& p, const in
     const int pg = cbeg + q;
     const int s = find_segment(segs, s_first, nseg, pg);
     if (base == 0) stamp_after(15, s);
-    const int b = s / p.num_kv_heads, kvh = s - b * p.num_kv_heads;
+    const int b = s / p.num_kv_heads, kvh = cache_head(p, s);
     const int j = pg - segs[s];
     const int id = p.block_tables[(size_t)b * p.max_blocks_per_seq + j];
     r.bad = (id < 0 || id >= p.num_blocks) ? 1 : 0;
-    r.y = r.bad ? 0 : (p.kv_layout == XQA_LAYOUT_HND ? (id * p.num_kv_heads + kvh) : id) * kBlockSize;
+    r.y = r.bad ? 0 : (p.kv_layout == XQA_LAYOUT_HND ? (id * p.cache_heads + kvh) : id) * kBlockSize;
     r.seg = s;
   }
   return r;
@@ -748,7 +754,7 @@ __device__ __forceinline__ bool setup_range(const PartialParams& p, const CUtens
     const int y = ld_relaxed_gpu(p.hints + (size_t)cta * kHintPages + tid);
     if constexpr (kFmt == XQA_KV_E2M1) {
       const uint32_t slice = (uint32_t)y / kBlockSize;  // any word: only slices of the pool
-      if (y >= 0 && slice < (uint32_t)p.num_blocks * (uint32_t)p.num_kv_heads) {
+      if (y >= 0 && slice < (uint32_t)p.num_blocks * (uint32_t)p.cache_heads) {
         bulk_prefetch(p.k_pool + (size_t)slice * kSliceBytes4, kSliceBytes4);
         bulk_prefetch(p.v_pool + (size_t)slice * kSliceBytes4, kSliceBytes4);
       }
@@ -757,7 +763,7 @@ __device__ __forceinline__ bool setup_range(const PartialParams& p, const CUtens
         tma_prefetch_2d(tm_k, 0, y);
         tma_prefetch_2d(tm_v, 0, y);
       } else {  // NHD: box (128 dims, 1 kv head, 16 tokens) at (0, kvh, page * 16)
-        const int row = y / kBlockSize, id = row / p.num_kv_heads, kvh = row - id * p.num_kv_heads;
+        const int row = y / kBlockSize, id = row / p.cache_heads, kvh = row - id * p.cache_heads;
         tma_prefetch_3d(tm_k, 0, kvh, id * kBlockSize);
         tma_prefetch_3d(tm_v, 0, kvh, id * kBlockSize);
       }
@@ -976,7 +982,7 @@ __device__ __forceinline__ void issue_page(const PartialParams& p, const CUtenso
       tma_load_2d(st, tm_k, &sh.full_bar[slot], 0, y, policy);
       tma_load_2d(st + kPageBytes, tm_v, &sh.full_bar[slot], 0, y, policy);
     } else {  // NHD: box (128 dims, 1 kv head, 16 tokens) at (0, kvh, page*16)
-      const int kvh = sg - (sg / p.num_kv_heads) * p.num_kv_heads;
+      const int kvh = cache_head(p, sg);
       tma_load_3d(st, tm_k, &sh.full_bar[slot], 0, kvh, y, policy);
       tma_load_3d(st + kPageBytes, tm_v, &sh.full_bar[slot], 0, kvh, y, policy);
     }
@@ -1258,7 +1264,7 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
   if (p.hints != nullptr && lane < 2 && (kWarps <= kHintPages / 2 || warp < kHintPages / 2)) {
     const int row = p.kv_layout == XQA_LAYOUT_HND
                         ? cur.y
-                        : (cur.y / kBlockSize * p.num_kv_heads + cur.seg % p.num_kv_heads) * kBlockSize;
+                        : (cur.y / kBlockSize * p.cache_heads + cache_head(p, cur.seg)) * kBlockSize;
     p.hints[(size_t)blockIdx.x * kHintPages + 2 * warp + lane] = lane < owned && !cur.bad ? row : -1;
   }
   int cur_base = 0;
@@ -1843,12 +1849,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int sg = s_first + j;
         r.seg = sg;
         if (lane < len) {
-          const int bb = sg / p.num_kv_heads, kvh = sg - bb * p.num_kv_heads;
+          const int bb = sg / p.num_kv_heads, kvh = cache_head(p, sg);
           const int id =
               p.block_tables[(size_t)bb * p.max_blocks_per_seq + (pb + lane - segs[sg])];
           r.bad = (id < 0 || id >= p.num_blocks) ? 1 : 0;
           r.y = r.bad ? 0
-                      : (p.kv_layout == XQA_LAYOUT_HND ? (id * p.num_kv_heads + kvh) : id) * kBlockSize;
+                      : (p.kv_layout == XQA_LAYOUT_HND ? (id * p.cache_heads + kvh) : id) * kBlockSize;
         }
       }
       return r;

@@ -1,0 +1,438 @@
+// select.cu — the pages worth reading: bounds of each page's keys (xqa_page_bounds) and the
+// choice of a few pages for each sequence and kv head from them (xqa_select).
+//
+// Bounds. For the tokens t of a (page, kv head) and every dim d, in whole steps of one
+// power of two for the slice:
+//
+//   2^e: the largest |k| lies in [2^(e+6), 2^(e+7))      (so it is at most 127 steps)
+//   hi_d = ceil(max_t k_td / 2^e),  lo_d = floor(min_t k_td / 2^e)
+//
+// 128 + 128 + 1 bytes, padded to 272, in place of 2048 codes. No key lies outside them.
+//
+// Score. With the group's queries in whole steps, q8 = rint(q / 2^f), |q8| <= 64, the
+// largest logits that keys within a page's bounds can have, summed over the group, are
+//
+//   2^f 2^e sum_d (A_d hi_d + B_d lo_d),   A_d = sum_g max(q8_gd, 0), B_d = sum_g min(q8_gd, 0)
+//
+// (a positive q wants the upper bound, a negative one the lower), so a group costs as much
+// as one head. At most 128 x 16 x 64 x 127 < 2^24 in whole numbers: the sum is exact in any
+// order, so a choice depends neither on the split of the work nor on the batch, and ties are
+// ties. 2^f is common to all pages of a choice and left out.
+//
+// Both are bound by bytes: 2048 + 272 (1152 + 272 in 4 bits) for a slice's bounds, 272 for a
+// score, against 4096 for a page's keys and values.
+#include "xqa_device.cuh"
+#include "xqa_launch.h"
+
+namespace xqa {
+
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kBoundsBytes = XQA_BOUNDS_BYTES;
+constexpr int kNotFinite = -128;  // exponent of a slice with an infinity or NaN
+
+__device__ __forceinline__ void raise(int32_t* status, int code) {
+  if (status) atomicCAS(status, XQA_OK, code);
+}
+
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 .. 127
+// floor(log2 x) of a normal x > 0
+__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
+
+__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
+  const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+__device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
+  const __half2 m = __hmin2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+// ---------------------------------------------------------------------------
+// bounds: a warp takes one kv head of the pages that `rows_per` consecutive new rows
+// touch. Eight lanes hold the 128 dims of a token, 16 each, so a warp reads four tokens at
+// a time and each lane keeps the largest and smallest of four tokens.
+// ---------------------------------------------------------------------------
+constexpr int kBoundsThreads = 128;
+
+// 16 neighbouring dims of a token as 8 half2 (exact: see the formats).
+template <int kFmt>
+__device__ __forceinline__ void key16(const uint8_t* slice, size_t token_stride, int t, int c,
+                                      uint32_t (&o)[8]) {
+  if constexpr (kFmt == XQA_KV_E2M1) {
+    const uint2 w = *reinterpret_cast<const uint2*>(slice + t * (kHeadDim / 2) + 8 * c);
+    const uint32_t s8 = slice[kCodeBytes4 + t * (kHeadDim / kGroup4) + c];
+    const uint32_t sc = e4m3x2_to_f16x2(s8 | s8 << 8);
+    e2m1x8_to_f16x2(w.x, o);
+    e2m1x8_to_f16x2(w.y, o + 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = hmul2(o[i], sc);
+  } else {
+    const uint4 w = *reinterpret_cast<const uint4*>(slice + t * token_stride + 16 * c);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[2 * i] = KvConv<kFmt>::k_lo(x[i]);
+      o[2 * i + 1] = KvConv<kFmt>::k_hi(x[i]);
+    }
+  }
+}
+
+template <int kFmt>
+__device__ __forceinline__ void bound_slice(const BoundsParams& p, int page, int head, int fill) {
+  const int lane = threadIdx.x & 31, c = lane & 7, t0 = lane >> 3;
+  const bool nhd = kFmt != XQA_KV_E2M1 && p.kv_layout == XQA_LAYOUT_NHD;
+  const size_t stride = nhd ? (size_t)p.num_kv_heads * kHeadDim : kHeadDim;
+  const uint8_t* slice =
+      p.k_cache + (nhd ? ((size_t)page * kBlockSize * p.num_kv_heads + head) * kHeadDim
+                       : ((size_t)page * p.num_kv_heads + head) *
+                             (kFmt == XQA_KV_E2M1 ? (size_t)kSliceBytes4 : (size_t)kPageBytes));
+  uint32_t hi[8], lo[8], top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) hi[i] = 0xfc00fc00u, lo[i] = 0x7c007c00u;  // -inf, inf
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int t = 4 * s + t0;
+    if (t >= fill) continue;
+    uint32_t k[8];
+    key16<kFmt>(slice, stride, t, c, k);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      hi[i] = hmax2(hi[i], k[i]);
+      lo[i] = hmin2(lo[i], k[i]);
+      top = __vmaxu2(top, k[i] & 0x7fff7fffu);  // magnitudes order like their patterns
+    }
+  }
+#pragma unroll
+  for (int off = 8; off < 32; off <<= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      hi[i] = hmax2(hi[i], __shfl_xor_sync(kAll, hi[i], off));
+      lo[i] = hmin2(lo[i], __shfl_xor_sync(kAll, lo[i], off));
+    }
+  const uint32_t big = __reduce_max_sync(kAll, max(top & 0xffffu, top >> 16));
+  int e = 0;
+  if (big >= 0x7c00u) e = kNotFinite;
+  else if (big > 0) e = exponent(__half2float(__ushort_as_half((unsigned short)big))) - 6;
+  // lanes 0-7 write the upper bounds, 8-15 the lower ones, lane 16 the exponent
+  uint4 out = make_uint4(0, 0, 0, 0);
+  uint32_t* w = &out.x;
+  if (lane < 16 && e != kNotFinite) {
+    const float step = pow2(-e);  // |e| <= 22
+    const bool upper = lane < 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t v = upper ? hi[i] : lo[i];
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+      const float a = f.x * step, b = f.y * step;  // exact
+      const int x = (int)(upper ? ceilf(a) : floorf(a)), y = (int)(upper ? ceilf(b) : floorf(b));
+      w[i >> 1] |= ((uint32_t)(x & 255) | (uint32_t)(y & 255) << 8) << (16 * (i & 1));
+    }
+  }
+  if (lane == 16) out.x = (uint32_t)(e & 255);
+  if (lane <= 16)
+    *reinterpret_cast<uint4*>(p.bounds + ((size_t)page * p.num_kv_heads + head) * kBoundsBytes +
+                              16 * lane) = out;
+}
+
+template <int kFmt>
+__global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsParams p, int rows_per) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const long long unit = (long long)blockIdx.x * (kBoundsThreads / 32) + (threadIdx.x >> 5);
+  const long long r0 = unit / p.num_kv_heads * rows_per;
+  const int head = (int)(unit % p.num_kv_heads);
+  if (r0 >= p.num_rows) return;
+  // a row a lane: is it its page's first new one, and which page is that
+  int page = -1, fill = 0;
+  const long long r = r0 + lane;
+  if (lane < rows_per && r < p.num_rows && r >= p.cu_seqlens[0] && r < p.cu_seqlens[p.batch]) {
+    int lo = 0, hi = p.batch - 1;  // last sequence that begins at or before r
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (p.cu_seqlens[m] <= r) lo = m;
+      else hi = m - 1;
+    }
+    const int q0 = p.cu_seqlens[lo], q1 = p.cu_seqlens[lo + 1], ctx = p.context_lens[lo];
+    if (r >= q0 && r < q1) {
+      if (ctx < 0 || ctx < (long long)q1 - q0 || ctx > (long long)p.max_blocks_per_seq * kBlockSize) {
+        raise(p.status, XQA_ERR_CTX_TOO_LONG);
+      } else {
+        const int pos = ctx - (int)(q1 - r);
+        if (r == q0 || pos % kBlockSize == 0) {
+          const int j = pos / kBlockSize;
+          page = p.block_tables[(size_t)lo * p.max_blocks_per_seq + j];
+          fill = min(kBlockSize, ctx - j * kBlockSize);
+          if ((uint32_t)page >= (uint32_t)p.num_blocks) {
+            raise(p.status, XQA_ERR_BAD_BLOCK_ID);
+            page = -1;
+          }
+        }
+      }
+    }
+  }
+  for (uint32_t some = __ballot_sync(kAll, page >= 0); some; some &= some - 1) {
+    const int src = __ffs(some) - 1;
+    bound_slice<kFmt>(p, __shfl_sync(kAll, page, src), head, __shfl_sync(kAll, fill, src));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the choice: a CTA scores a chunk of a segment's pages (segment: sequence and kv head); the
+// one that is last to finish a segment's chunks takes its best pages.
+// ---------------------------------------------------------------------------
+constexpr int kSelectThreads = 256;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr uint32_t kKeyAlways = 0xffffffffu, kKeyFirst = 0xfffffffeu;  // above every score's
+
+// Orders like the score.
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ int dp2_lo(uint32_t a, uint32_t b, int c) {  // a: 2 x 16, b: bytes 0, 1
+  int d;
+  asm("dp2a.lo.s32.s32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ int dp2_hi(uint32_t a, uint32_t b, int c) {  // bytes 2, 3
+  int d;
+  asm("dp2a.hi.s32.s32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
+struct SelectShared {
+  short ab[2][kHeadDim];  // A, B
+  uint32_t amax[kSelectWarps];
+  int count[kSelectWarps][2];
+  int total;
+  int last;
+  int status;
+};
+
+// A and B of a segment's queries into shared memory.
+__device__ __forceinline__ void group_query(const SelectParams& p, int seg, SelectShared& sh) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const uint16_t* q = p.q + (size_t)seg * p.group * kHeadDim;  // [B, Hkv, G, 128]
+  uint32_t top = 0;  // magnitudes order like their patterns; those that are not finite count as 0
+  for (int i = tid; i < p.group * kHeadDim; i += kSelectThreads) {
+    const uint32_t m = q[i] & 0x7fffu;
+    if (m < 0x7c00u) top = max(top, m);
+  }
+  top = __reduce_max_sync(kAll, top);
+  if (lane == 0) sh.amax[tid >> 5] = top;
+  __syncthreads();
+  for (int w = 0; w < kSelectWarps; ++w) top = max(top, sh.amax[w]);
+  const int f = top > 0 ? exponent(__half2float(__ushort_as_half((unsigned short)top))) - 5 : 0;
+  const float step = pow2(-f);
+  if (tid < kHeadDim) {
+    int a = 0, b = 0;
+    for (int g = 0; g < p.group; ++g) {
+      const uint32_t v = q[g * kHeadDim + tid];
+      if ((v & 0x7c00u) == 0x7c00u) continue;
+      const int x = (int)rintf(__half2float(__ushort_as_half((unsigned short)v)) * step);
+      a += max(x, 0);
+      b += min(x, 0);
+    }
+    sh.ab[0][tid] = (short)a;
+    sh.ab[1][tid] = (short)b;
+  }
+  __syncthreads();
+}
+
+// Keys of a segment's pages from .. to - 1.
+__device__ __forceinline__ void score_pages(const SelectParams& p, int seg, int pages, int from, int to,
+                                            SelectShared& sh, uint32_t* keys) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 7, at = lane >> 3;
+  const int b = seg / p.num_kv_heads, head = seg - b * p.num_kv_heads;
+  const int32_t* table = p.block_tables + (size_t)b * p.max_blocks_per_seq;
+  uint32_t qa[8], qb[8];  // dims 16 c .. 16 c + 15, in pairs
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    qa[i] = reinterpret_cast<const uint32_t*>(sh.ab[0])[8 * c + i];
+    qb[i] = reinterpret_cast<const uint32_t*>(sh.ab[1])[8 * c + i];
+  }
+  for (int j0 = from + 32 * warp; j0 < to; j0 += 32 * kSelectWarps) {  // 32 pages, four at a time
+    const int id = j0 + lane < to ? table[j0 + lane] : 0;
+    const bool good = (uint32_t)id < (uint32_t)p.num_blocks;
+    if (!good) record_status(&sh.status, XQA_ERR_BAD_BLOCK_ID);
+    uint32_t key = 0;
+#pragma unroll 4
+    for (int s = 0; s < 8; ++s) {
+      const int page = __shfl_sync(kAll, good ? id : 0, 4 * s + at);
+      const uint8_t* bd = p.bounds + ((size_t)page * p.num_kv_heads + head) * kBoundsBytes;
+      const uint4 hi = *reinterpret_cast<const uint4*>(bd + 16 * c);
+      const uint4 lo = *reinterpret_cast<const uint4*>(bd + kHeadDim + 16 * c);
+      const int e = (int)(signed char)bd[2 * kHeadDim];
+      int sum = 0;
+      sum = dp2_lo(qa[0], hi.x, sum), sum = dp2_hi(qa[1], hi.x, sum);
+      sum = dp2_lo(qa[2], hi.y, sum), sum = dp2_hi(qa[3], hi.y, sum);
+      sum = dp2_lo(qa[4], hi.z, sum), sum = dp2_hi(qa[5], hi.z, sum);
+      sum = dp2_lo(qa[6], hi.w, sum), sum = dp2_hi(qa[7], hi.w, sum);
+      sum = dp2_lo(qb[0], lo.x, sum), sum = dp2_hi(qb[1], lo.x, sum);
+      sum = dp2_lo(qb[2], lo.y, sum), sum = dp2_hi(qb[3], lo.y, sum);
+      sum = dp2_lo(qb[4], lo.z, sum), sum = dp2_hi(qb[5], lo.z, sum);
+      sum = dp2_lo(qb[6], lo.w, sum), sum = dp2_hi(qb[7], lo.w, sum);
+#pragma unroll
+      for (int off = 1; off < 8; off <<= 1) sum += __shfl_xor_sync(kAll, sum, off);
+      const uint32_t k = e == kNotFinite ? kKeyFirst : key_of((float)sum * pow2(max(e, -126)));
+      const uint32_t mine = __shfl_sync(kAll, k, (lane & 3) * 8);  // page 4 s + (lane & 3)
+      if (lane >> 2 == s) key = mine;
+    }
+    const int j = j0 + lane;
+    if (!good) key = kKeyFirst;  // is met, and reported, by whoever reads it
+    if (j < p.first_pages || j >= pages - p.last_pages) key = kKeyAlways;
+    if (j < to) keys[j] = key;
+  }
+}
+
+// Block-wide sum; every thread calls it.
+__device__ __forceinline__ int sum_all(int v, SelectShared& sh) {
+  v = __reduce_add_sync(kAll, v);
+  if ((threadIdx.x & 31) == 0) sh.count[threadIdx.x >> 5][0] = v;
+  __syncthreads();
+  int s = 0;
+#pragma unroll
+  for (int w = 0; w < kSelectWarps; ++w) s += sh.count[w][0];
+  __syncthreads();
+  return s;
+}
+
+// The `take` largest of n keys, the lowest index first among equal ones, as ascending indices.
+__device__ __forceinline__ void take_pages(const SelectParams& p, int seg, int n, int take,
+                                           const uint32_t* keys, SelectShared& sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // the take-th largest key, bit by bit: the largest t that at least `take` keys reach
+  uint32_t t = 0;
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t probe = t | 1u << bit;
+    int c = 0;
+    for (int i = tid; i < n; i += kSelectThreads) c += keys[i] >= probe;
+    if (sum_all(c, sh) >= take) t = probe;
+  }
+  int c = 0;
+  for (int i = tid; i < n; i += kSelectThreads) c += keys[i] > t;
+  const int ties = take - sum_all(c, sh);  // of the keys equal to t, the first so many
+  // each warp writes those of a run of keys, behind the ones of the warps before it
+  const int run = ((n + kSelectWarps - 1) / kSelectWarps + 31) & ~31;
+  const int from = min(n, warp * run), to = min(n, from + run);
+  int above = 0, equal = 0;
+  for (int i0 = from; i0 < to; i0 += 32) {
+    const uint32_t k = i0 + lane < to ? keys[i0 + lane] : 0;
+    above += __popc(__ballot_sync(kAll, i0 + lane < to && k > t));
+    equal += __popc(__ballot_sync(kAll, i0 + lane < to && k == t));
+  }
+  if (lane == 0) sh.count[warp][0] = above, sh.count[warp][1] = equal;
+  __syncthreads();
+  int at = 0, eq = 0;
+  for (int w = 0; w < warp; ++w) at += sh.count[w][0], eq += sh.count[w][1];
+  at += min(eq, ties);
+  const int b = seg / p.num_kv_heads;
+  const int32_t* table = p.block_tables + (size_t)b * p.max_blocks_per_seq;
+  int32_t* out = p.selected + (size_t)seg * p.max_pages;
+  for (int i0 = from; i0 < to; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t k = i < to ? keys[i] : 0;
+    const unsigned eqs = __ballot_sync(kAll, i < to && k == t);
+    const unsigned below = (1u << lane) - 1;
+    const bool mine = i < to && (k > t || (k == t && eq + __popc(eqs & below) < ties));
+    const unsigned some = __ballot_sync(kAll, mine);
+    if (mine) out[at + __popc(some & below)] = table[i];
+    at += __popc(some);
+    eq += __popc(eqs);
+  }
+}
+
+__global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectParams p) {
+  __shared__ __align__(16) SelectShared sh;
+  griddep_launch_dependents();
+  const int tid = threadIdx.x;
+  if (tid == 0) sh.status = XQA_OK;
+  __syncthreads();
+  griddep_wait();
+  const long long units = (long long)p.batch * p.num_kv_heads * p.chunks;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const int seg = (int)(u / p.chunks), chunk = (int)(u - (long long)seg * p.chunks);
+    const int ctx = p.context_lens[seg / p.num_kv_heads];
+    const bool bad = ctx < 0 || ctx > (long long)p.max_blocks_per_seq * kBlockSize;
+    const int pages = bad ? 0 : (ctx + kBlockSize - 1) / kBlockSize;
+    const int take = min(pages, p.max_pages);
+    const int from = chunk * p.chunk_pages;
+    if (chunk > 0 && (pages <= p.max_pages || from >= pages)) continue;
+    int32_t* out = p.selected + (size_t)seg * p.max_pages;
+    if (chunk == 0) {  // what does not depend on a score
+      for (int i = take + tid; i < p.max_pages; i += kSelectThreads) out[i] = -1;
+      if (tid == 0) {
+        p.selected_lens[seg] = bad ? -1 : ctx - (pages - take) * kBlockSize;
+        if (bad) record_status(&sh.status, XQA_ERR_CTX_TOO_LONG);
+      }
+    }
+    if (pages <= p.max_pages) {  // all of them
+      const int32_t* table = p.block_tables + (size_t)(seg / p.num_kv_heads) * p.max_blocks_per_seq;
+      for (int i = tid; i < pages; i += kSelectThreads) {
+        const int id = table[i];
+        out[i] = id;
+        if ((uint32_t)id >= (uint32_t)p.num_blocks) record_status(&sh.status, XQA_ERR_BAD_BLOCK_ID);
+      }
+      continue;
+    }
+    uint32_t* keys = p.keys + (size_t)seg * p.max_blocks_per_seq;
+    group_query(p, seg, sh);
+    score_pages(p, seg, pages, from, min(pages, from + p.chunk_pages), sh, keys);
+    const int chunks = (pages + p.chunk_pages - 1) / p.chunk_pages;
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      const int old = atom_add_acq_rel_gpu(p.tickets + seg, 1);
+      sh.last = old == chunks - 1;
+      if (sh.last) p.tickets[seg] = 0;  // for the next call
+      __threadfence();
+    }
+    __syncthreads();
+    if (sh.last) take_pages(p, seg, pages, take, keys, sh);
+    __syncthreads();
+  }
+  __syncthreads();
+  if (tid == 0) {
+    p.status[blockIdx.x] = sh.status;
+    if (blockIdx.x == 0) p.header[0] = gridDim.x;
+  }
+}
+
+template <class... Args>
+cudaError_t launch(void (*kernel)(Args...), int ctas, int threads, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace
+
+cudaError_t launch_bounds(const BoundsParams& p, cudaStream_t stream) {
+  // a row a warp while they are few (a decode step's are all pages of their own), else 16:
+  // of a prompt's rows, those of one or two pages
+  const int rows_per = p.num_rows <= 4096 ? 1 : kBlockSize;
+  const long long units = ((long long)p.num_rows + rows_per - 1) / rows_per * p.num_kv_heads;
+  const int ctas = (int)((units + kBoundsThreads / 32 - 1) / (kBoundsThreads / 32));
+  switch (p.kv_dtype) {
+    case XQA_KV_E2M1: return launch(bounds_kernel<XQA_KV_E2M1>, ctas, kBoundsThreads, stream, p, rows_per);
+    case XQA_KV_E4M3: return launch(bounds_kernel<XQA_KV_E4M3>, ctas, kBoundsThreads, stream, p, rows_per);
+    default: return launch(bounds_kernel<XQA_KV_E5M2>, ctas, kBoundsThreads, stream, p, rows_per);
+  }
+}
+
+cudaError_t launch_select(const SelectParams& p, int ctas, cudaStream_t stream) {
+  return launch(select_kernel, ctas, kSelectThreads, stream, p);
+}
+
+}  // namespace xqa

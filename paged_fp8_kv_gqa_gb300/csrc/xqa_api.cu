@@ -17,6 +17,7 @@ namespace xqa {
 cudaError_t set_partial_attributes();
 cudaError_t set_prefill_attributes();
 cudaError_t set_extend_attributes();
+cudaError_t set_pages_attributes();
 }
 
 namespace {
@@ -114,7 +115,8 @@ xqa_status_t ensure_device_setup() {
   if (g_attrs_set[dev].load(std::memory_order_acquire) == 0) {
     if (xqa::set_partial_attributes() != cudaSuccess ||
         xqa::set_prefill_attributes() != cudaSuccess ||
-        xqa::set_extend_attributes() != cudaSuccess)
+        xqa::set_extend_attributes() != cudaSuccess ||
+        xqa::set_pages_attributes() != cudaSuccess)
       return XQA_ERR_LAUNCH;
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -213,7 +215,8 @@ xqa_status_t attend_partial_impl(const void* q, const uint8_t* k_cache, const ui
                                  const int32_t* block_tables, const int32_t* context_lens,
                                  float k_scale, float v_scale, const float* k_scale_ptr,
                                  const float* v_scale_ptr, void* out, const xqa_shape_t* shape,
-                                 void* workspace, size_t workspace_bytes, void* stream) {
+                                 void* workspace, size_t workspace_bytes, void* stream,
+                                 bool per_head = false) {
   if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out) return XQA_ERR_NULL;
   Resolved r;
   xqa_status_t st = resolve(shape, &r);
@@ -247,9 +250,12 @@ xqa_status_t attend_partial_impl(const void* q, const uint8_t* k_cache, const ui
   // CTAs that wait for one another's merge tickets need the whole grid
   // resident at once: one CTA per SM, so no more CTAs than SMs
   p.merge_helpers = r.n_max <= device_sms() ? xqa::kMergeHelpers : 1;
-  p.batch = r.batch;
-  p.num_q_heads = r.hq;
-  p.num_kv_heads = r.hkv;
+  // tables of a kv head's own: each (sequence, kv head) is a sequence of one kv head, its q
+  // and out rows where they were
+  p.batch = per_head ? r.nseg : r.batch;
+  p.num_q_heads = per_head ? r.group : r.hq;
+  p.num_kv_heads = per_head ? 1 : r.hkv;
+  p.cache_heads = r.hkv;
   p.group = r.group;
   p.max_blocks_per_seq = r.mbs;
   p.num_blocks = r.nb;
@@ -269,7 +275,7 @@ xqa_status_t attend_partial_impl(const void* q, const uint8_t* k_cache, const ui
 
 xqa_status_t combine_impl(const int32_t* context_lens, float v_scale, const float* v_scale_ptr,
                           void* out, const xqa_shape_t* shape, void* workspace,
-                          size_t workspace_bytes, void* stream) {
+                          size_t workspace_bytes, void* stream, bool per_head = false) {
   if (!context_lens || !out) return XQA_ERR_NULL;
   Resolved r;
   xqa_status_t st = resolve(shape, &r);
@@ -285,8 +291,8 @@ xqa_status_t combine_impl(const int32_t* context_lens, float v_scale, const floa
   p.seg_cc = reinterpret_cast<const int32_t*>(base + r.ws.seg_cc_off);
   p.tickets = reinterpret_cast<int32_t*>(base + r.ws.ticket_off);
   p.partials = reinterpret_cast<const float*>(base + r.ws.partials_off);
-  p.num_q_heads = r.hq;
-  p.num_kv_heads = r.hkv;
+  p.num_q_heads = per_head ? r.group : r.hq;
+  p.num_kv_heads = per_head ? 1 : r.hkv;
   p.group = r.group;
   p.q_len = r.q_len;
   p.v_scale = v_scale;
@@ -493,6 +499,67 @@ xqa_status_t encode_nhd_map(CUtensorMap* map, const uint8_t* pool, int hkv, int 
       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return res == CUDA_SUCCESS ? XQA_OK : XQA_ERR_LAUNCH;
+}
+
+struct SelectResolved {
+  int group, ctas, chunks, chunk_pages;
+  size_t ticket_off, keys_off, bytes;
+};
+
+xqa_status_t resolve_select(const xqa_select_shape_t* s, SelectResolved* r) {
+  if (!s) return XQA_ERR_NULL;
+  if (!cache_fits(s->batch, s->num_kv_heads, s->head_dim, s->block_size, s->max_blocks_per_seq,
+                  s->num_blocks, XQA_KV_E5M2, XQA_LAYOUT_HND))
+    return XQA_ERR_SHAPE;
+  if (s->num_q_heads < 1 || s->num_q_heads % s->num_kv_heads != 0 || s->max_ctas < 0)
+    return XQA_ERR_SHAPE;
+  r->group = s->num_q_heads / s->num_kv_heads;
+  if (r->group > xqa::kMaxCols) return XQA_ERR_SHAPE;
+  if (s->max_pages < 1 || s->first_pages < 0 || s->last_pages < 1 ||
+      s->first_pages > s->max_pages - s->last_pages)
+    return XQA_ERR_SHAPE;
+  // int32 segments, table entries and selected pages
+  const long long nseg = (long long)s->batch * s->num_kv_heads;
+  if (nseg >= (1ll << 31) / s->max_blocks_per_seq || nseg >= (1ll << 31) / s->max_pages ||
+      nseg * r->group >= (1ll << 31) / kHeadDim || s->max_blocks_per_seq > (1 << 26))
+    return XQA_ERR_SHAPE;
+  r->ctas = s->max_ctas;
+  if (r->ctas == 0) {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return XQA_ERR_DEVICE;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+      return XQA_ERR_DEVICE;
+    r->ctas = 4 * sms;
+  }
+  if (r->ctas > xqa::kMaxCtas) r->ctas = xqa::kMaxCtas;
+  // chunks of 256 pages (32 to a warp) at least, about one for each CTA
+  const long long pages = nseg * s->max_blocks_per_seq;
+  const long long chunk = ((pages / r->ctas + 255) / 256 > 0 ? (pages / r->ctas + 255) / 256 : 1) * 256;
+  r->chunk_pages = (int)chunk;
+  r->chunks = (int)((s->max_blocks_per_seq + chunk - 1) / chunk);
+  if (nseg * r->chunks < r->ctas) r->ctas = (int)(nseg * r->chunks);
+  r->ticket_off = kPrefillWorkspaceBytes;
+  r->keys_off = (r->ticket_off + 4 * (size_t)nseg + 255) & ~(size_t)255;
+  r->bytes = r->keys_off + 4 * (size_t)pages;
+  return XQA_OK;
+}
+
+// Checks of the calls over pages of sequences; fills what they share.
+xqa_status_t resolve_pages(const xqa_pages_t* s, xqa::PagesParams* p) {
+  if (!s) return XQA_ERR_NULL;
+  if (s->block_size != kBlockSize || s->batch < 1 || s->batch > xqa::kMaxPagesBatch ||
+      s->max_blocks_per_seq < 1 || s->num_blocks < 1 || s->num_rows < 0)
+    return XQA_ERR_SHAPE;
+  // int32 positions, slots and table entries
+  if (s->num_blocks >= (1 << 27) || s->max_blocks_per_seq >= (1 << 27) ||
+      (long long)s->batch * s->max_blocks_per_seq >= (1ll << 31) || s->num_rows >= (1 << 30))
+    return XQA_ERR_SHAPE;
+  *p = xqa::PagesParams{};
+  p->batch = s->batch;
+  p->max_blocks_per_seq = s->max_blocks_per_seq;
+  p->num_blocks = s->num_blocks;
+  p->num_rows = s->num_rows;
+  return XQA_OK;
 }
 
 bool good_scale(float s, const float* dev) { return dev || (s > 0.f && isfinite(s)); }
@@ -784,6 +851,157 @@ xqa_status_t xqa_extend(const void* q, const uint8_t* k_cache, const uint8_t* v_
   return e == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
 }
 
+xqa_status_t xqa_assign_pages(const int32_t* new_tokens, const int32_t* context_lens,
+                              int32_t* block_tables, const int32_t* free_pages,
+                              const int32_t* num_free, int32_t* new_lens, int32_t* new_free,
+                              int32_t* cu_seqlens, int32_t* slots, int32_t* positions,
+                              const xqa_pages_t* pages, int32_t* device_status, void* stream) {
+  xqa::PagesParams p;
+  xqa_status_t st = resolve_pages(pages, &p);
+  if (st != XQA_OK) return st;
+  if (!new_tokens || !context_lens || !block_tables || !free_pages || !num_free || !new_lens ||
+      !new_free || !cu_seqlens)
+    return XQA_ERR_NULL;
+  if ((st = ensure_device_setup()) != XQA_OK) return st;
+  p.new_tokens = new_tokens;
+  p.context_lens = context_lens;
+  p.block_tables = block_tables;
+  p.free_pages = const_cast<int32_t*>(free_pages);
+  p.num_free = num_free;
+  p.new_lens = new_lens;
+  p.new_free = new_free;
+  p.cu_seqlens = cu_seqlens;
+  p.slots = slots;
+  p.positions = positions;
+  p.status = device_status;
+  return xqa::launch_assign(p, (cudaStream_t)stream) == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
+}
+
+xqa_status_t xqa_release_pages(const uint8_t* done, const int32_t* context_lens,
+                               const int32_t* block_tables, int32_t* free_pages,
+                               const int32_t* num_free, int32_t* new_lens, int32_t* new_free,
+                               const xqa_pages_t* pages, int32_t* device_status, void* stream) {
+  xqa::PagesParams p;
+  xqa_status_t st = resolve_pages(pages, &p);
+  if (st != XQA_OK) return st;
+  if (!done || !context_lens || !block_tables || !free_pages || !num_free || !new_lens || !new_free)
+    return XQA_ERR_NULL;
+  if ((st = ensure_device_setup()) != XQA_OK) return st;
+  p.done = done;
+  p.context_lens = context_lens;
+  p.block_tables = const_cast<int32_t*>(block_tables);
+  p.free_pages = free_pages;
+  p.num_free = num_free;
+  p.new_lens = new_lens;
+  p.new_free = new_free;
+  p.status = device_status;
+  return xqa::launch_release(p, (cudaStream_t)stream) == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
+}
+
+xqa_status_t xqa_page_bounds(const uint8_t* k_cache, const int32_t* block_tables,
+                             const int32_t* context_lens, const int32_t* cu_seqlens,
+                             uint8_t* bounds, const xqa_rows_t* rows, int32_t* device_status,
+                             void* stream) {
+  if (!rows) return XQA_ERR_NULL;
+  const xqa_rows_t& s = *rows;
+  if (!cache_fits(s.batch, s.num_kv_heads, s.head_dim, s.block_size, s.max_blocks_per_seq,
+                  s.num_blocks, s.kv_dtype, s.kv_layout) ||
+      s.num_rows < 0 || (long long)s.num_rows * s.num_kv_heads >= (1ll << 31))
+    return XQA_ERR_SHAPE;
+  if (s.num_rows == 0) return XQA_OK;
+  if (!k_cache || !block_tables || !context_lens || !cu_seqlens || !bounds) return XQA_ERR_NULL;
+  if (!aligned16(k_cache) || !aligned16(bounds)) return XQA_ERR_ALIGN;
+  xqa::BoundsParams p;
+  p.k_cache = k_cache;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.cu_seqlens = cu_seqlens;
+  p.bounds = bounds;
+  p.status = device_status;
+  p.batch = s.batch;
+  p.num_kv_heads = s.num_kv_heads;
+  p.max_blocks_per_seq = s.max_blocks_per_seq;
+  p.num_blocks = s.num_blocks;
+  p.num_rows = s.num_rows;
+  p.kv_dtype = s.kv_dtype;
+  p.kv_layout = s.kv_layout;
+  return xqa::launch_bounds(p, (cudaStream_t)stream) == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
+}
+
+xqa_status_t xqa_select_workspace_size(const xqa_select_shape_t* shape, size_t* bytes) {
+  if (!bytes) return XQA_ERR_NULL;
+  SelectResolved r;
+  const xqa_status_t st = resolve_select(shape, &r);
+  if (st != XQA_OK) return st;
+  *bytes = r.bytes;
+  return XQA_OK;
+}
+
+xqa_status_t xqa_select(const void* q, const uint8_t* bounds, const int32_t* block_tables,
+                        const int32_t* context_lens, int32_t* selected, int32_t* selected_lens,
+                        const xqa_select_shape_t* shape, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  SelectResolved r;
+  const xqa_status_t st = resolve_select(shape, &r);
+  if (st != XQA_OK) return st;
+  if (!q || !bounds || !block_tables || !context_lens || !selected || !selected_lens || !workspace)
+    return XQA_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return XQA_ERR_ALIGN;
+  if (workspace_bytes < r.bytes) return XQA_ERR_WORKSPACE;
+  if (!aligned16(q) || !aligned16(bounds)) return XQA_ERR_ALIGN;
+  const xqa::WsLayout lay = xqa::ws_layout(0, 0);
+  uint8_t* base = reinterpret_cast<uint8_t*>(workspace);
+  xqa::SelectParams p;
+  p.q = reinterpret_cast<const uint16_t*>(q);
+  p.bounds = bounds;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.selected = selected;
+  p.selected_lens = selected_lens;
+  p.header = ws_i32(workspace);
+  p.status = reinterpret_cast<int32_t*>(base + lay.status_off);
+  p.tickets = reinterpret_cast<int32_t*>(base + r.ticket_off);
+  p.keys = reinterpret_cast<uint32_t*>(base + r.keys_off);
+  p.batch = shape->batch;
+  p.num_kv_heads = shape->num_kv_heads;
+  p.group = r.group;
+  p.max_blocks_per_seq = shape->max_blocks_per_seq;
+  p.num_blocks = shape->num_blocks;
+  p.max_pages = shape->max_pages;
+  p.first_pages = shape->first_pages;
+  p.last_pages = shape->last_pages;
+  p.chunks = r.chunks;
+  p.chunk_pages = r.chunk_pages;
+  return xqa::launch_select(p, r.ctas, (cudaStream_t)stream) == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
+}
+
+xqa_status_t xqa_decode_selected(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                 const int32_t* selected, const int32_t* selected_lens,
+                                 float k_scale, float v_scale, const float* k_scale_dev,
+                                 const float* v_scale_dev, void* out, const xqa_shape_t* shape,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !k_cache || !v_cache || !selected || !selected_lens || !out) return XQA_ERR_NULL;
+  if ((k_scale_dev == nullptr) != (v_scale_dev == nullptr)) return XQA_ERR_NULL;
+  Resolved r;
+  xqa_status_t st = resolve(shape, &r);
+  if (st != XQA_OK) return st;
+  if (r.q_len != 1) return XQA_ERR_SHAPE;
+  if ((st = check_workspace(r, workspace, workspace_bytes)) != XQA_OK) return st;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+    return XQA_ERR_ALIGN;
+  if ((st = ensure_device_setup()) != XQA_OK) return st;
+  if (needs_planner(r) &&
+      xqa::launch_plan(selected_lens, r.nseg, 1, r.mbs, r.n_max, r.min_pages, ws_i32(workspace),
+                       (cudaStream_t)stream) != cudaSuccess)
+    return XQA_ERR_LAUNCH;
+  if ((st = attend_partial_impl(q, k_cache, v_cache, selected, selected_lens, k_scale, v_scale,
+                                k_scale_dev, v_scale_dev, out, shape, workspace, workspace_bytes,
+                                stream, true)) != XQA_OK)
+    return st;
+  return combine_impl(selected_lens, v_scale, v_scale_dev, out, shape, workspace, workspace_bytes,
+                      stream, true);
+}
+
 xqa_status_t xqa_append(const void* k, const void* v, const int32_t* cu_seqlens,
                         const int32_t* block_tables, const int32_t* context_lens, float k_scale,
                         float v_scale, const float* k_scale_dev, const float* v_scale_dev,
@@ -877,6 +1095,7 @@ const char* xqa_status_string(xqa_status_t status) {
     case XQA_ERR_DEVICE_TIMEOUT: return "device: pipeline wait exceeded its time budget";
     case XQA_ERR_DRAIN_TIMEOUT:
       return "device: a copy was still in flight when its CTA gave up; device state not trusted";
+    case XQA_ERR_NO_PAGES: return "device: the free pages ran out, or their number cannot be";
     case XQA_ERR_BAD_OFFSETS: return "device: cu_seqlens descending, negative or past the rows";
   }
   return "unknown status";

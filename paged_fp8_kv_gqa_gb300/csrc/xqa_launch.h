@@ -21,6 +21,8 @@ struct PartialParams {
   float* partials;     // [(n_max + nseg) * kSlotFloats]
   int32_t* hints;      // [kMaxCtas * kHintPages] first pages of each CTA's range (null: none)
   int batch, num_q_heads, num_kv_heads, group, max_blocks_per_seq, num_blocks;
+  int cache_heads;           // kv heads of the cache (num_kv_heads, unless every kv head has
+                             // a table of its own: then num_kv_heads is 1)
   int q_len;                 // new tokens per sequence (q, out: [B, q_len, Hq, D])
   int n_max, min_pages;      // split rule inputs (same values the planner got)
   int fused_merge;           // 1: the last CTA of a split segment merges it
@@ -117,6 +119,58 @@ struct ExtendParams {
 
 cudaError_t launch_extend(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                           const ExtendParams& p, int dtype, int ctas, cudaStream_t stream);
+// xqa_assign_pages and xqa_release_pages.
+constexpr int kMaxPagesBatch = 16384;          // sequences: three words each in shared memory
+constexpr int kMaxReleasePieces = 48 * 1024;   // pieces of tables: a word each
+
+struct PagesParams {
+  const int32_t* new_tokens;    // assign
+  const uint8_t* done;          // release
+  const int32_t* context_lens;
+  int32_t* block_tables;        // release: read only
+  int32_t* free_pages;          // assign: read only
+  const int32_t* num_free;
+  int32_t* new_lens;
+  int32_t* new_free;
+  int32_t* cu_seqlens;
+  int32_t* slots;               // optional
+  int32_t* positions;           // optional
+  int32_t* status;              // optional: first error of the call
+  int batch, max_blocks_per_seq, num_blocks, num_rows;
+};
+
+// xqa_page_bounds.
+struct BoundsParams {
+  const uint8_t* k_cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* cu_seqlens;
+  uint8_t* bounds;
+  int32_t* status;
+  int batch, num_kv_heads, max_blocks_per_seq, num_blocks, num_rows, kv_dtype, kv_layout;
+};
+
+// xqa_select.
+struct SelectParams {
+  const uint16_t* q;  // [B, Hq, 128] fp16
+  const uint8_t* bounds;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  int32_t* selected;       // [B * Hkv, max_pages]
+  int32_t* selected_lens;  // [B * Hkv]
+  int32_t* header;         // workspace header (CTAs launched)
+  int32_t* status;         // [kMaxCtas]
+  int32_t* tickets;        // [B * Hkv] chunks scored: zero between calls
+  uint32_t* keys;          // [B * Hkv, MBS]
+  int batch, num_kv_heads, group, max_blocks_per_seq, num_blocks;
+  int max_pages, first_pages, last_pages;
+  int chunks, chunk_pages;
+};
+
+cudaError_t launch_assign(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_release(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_bounds(const BoundsParams& p, cudaStream_t stream);
+cudaError_t launch_select(const SelectParams& p, int ctas, cudaStream_t stream);
 cudaError_t launch_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                            const CUtensorMap& tm_v, const PrefillParams& p, int dtype, int ctas,
                            cudaStream_t stream);
