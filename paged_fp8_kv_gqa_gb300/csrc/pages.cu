@@ -29,38 +29,44 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kPageThreads = 512;
-constexpr int kWarps = kPageThreads / 32;
+constexpr int kClusterCtas = 8;  // the largest portable cluster
+constexpr int kSmallThreads = 256, kLargeThreads = 1024;
 constexpr unsigned kAll = 0xffffffffu;
 
 __device__ __forceinline__ void raise(int32_t* status, int code) {
   if (status) atomicCAS(status, XQA_OK, code);
 }
 
-// Block-wide exclusive scan of two sums at once; sums: those of all threads.
+// Block-wide exclusive scan of two sums at once; sums: those of all threads. Every warp scans
+// the warps' sums for itself.
 struct Two {
   long long rows;
   int pages;
 };
-__device__ __forceinline__ Two scan2(Two v, Two* warp_sums, Two& sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Two incl = v;
+__device__ __forceinline__ Two warp_scan2(Two v) {  // inclusive
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const long long r = __shfl_up_sync(kAll, incl.rows, off);
-    const int p = __shfl_up_sync(kAll, incl.pages, off);
-    if (lane >= off) incl.rows += r, incl.pages += p;
+    const long long r = __shfl_up_sync(kAll, v.rows, off);
+    const int p = __shfl_up_sync(kAll, v.pages, off);
+    if (lane >= off) v.rows += r, v.pages += p;
   }
+  return v;
+}
+template <int kThreads>
+__device__ __forceinline__ Two scan2(Two v, Two* warp_sums, Two& sums) {
+  constexpr int kWarps = kThreads / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Two incl = warp_scan2(v);
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
-  Two before{0, 0};
-  sums = Two{0, 0};
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) before = sums;
-    sums.rows += warp_sums[w].rows;
-    sums.pages += warp_sums[w].pages;
-  }
+  const Two w = warp_scan2(lane < kWarps ? warp_sums[lane] : Two{0, 0});
+  sums.rows = __shfl_sync(kAll, w.rows, 31);
+  sums.pages = __shfl_sync(kAll, w.pages, 31);
+  Two before;
+  before.rows = __shfl_sync(kAll, w.rows, max(warp - 1, 0));
+  before.pages = __shfl_sync(kAll, w.pages, max(warp - 1, 0));
+  if (warp == 0) before = Two{0, 0};
   __syncthreads();
   return Two{before.rows + incl.rows - v.rows, before.pages + incl.pages - v.pages};
 }
@@ -78,6 +84,13 @@ __device__ __forceinline__ int last_at_most(const int* a, int n, int x) {
   return lo;
 }
 
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Height of the stack, 0 if the word cannot be one.
 __device__ __forceinline__ int stack_height(const PagesParams& p) {
   const int f = *p.num_free;
@@ -86,24 +99,22 @@ __device__ __forceinline__ int stack_height(const PagesParams& p) {
   return 0;
 }
 
-template <bool kCluster>
-__global__ void __launch_bounds__(kPageThreads) assign_kernel(const PagesParams p) {
+template <int kThreads, bool kCluster>
+__global__ void __launch_bounds__(kThreads) assign_kernel(const PagesParams p) {
   extern __shared__ int smem[];
   int* row0 = smem;                // [batch + 1] first row of each sequence
   int* page0 = row0 + p.batch + 1; // [batch + 1] pages taken before it
   int* old = page0 + p.batch + 1;  // [batch] tokens before the step
-  __shared__ Two sums[kWarps];
+  __shared__ Two sums[kThreads / 32];
   __shared__ int height;
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x;
-  if (tid == 0) height = stack_height(p);
-  __syncthreads();
-  const int free_now = height;
+  if (tid == 0) height = stack_height(p);  // (read behind the first scan)
   Two before{0, 0};
   long long rows = 0;  // served so far
   int taken = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += kPageThreads) {
+  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
     const int b = b0 + tid;
     int n = 0, c = 0;
     if (b < p.batch) {
@@ -117,21 +128,21 @@ __global__ void __launch_bounds__(kPageThreads) assign_kernel(const PagesParams 
     }
     const int need = n > 0 ? pages_of(c + n) - pages_of(c) : 0;
     Two all;
-    const Two at = scan2(Two{n, need}, sums, all);
+    const Two at = scan2<kThreads>(Two{n, need}, sums, all);
     // Refused: rows past the caller's, pages past the stack. Both only begin at some
     // sequence and stay, so the pages of those that are served have no gaps.
     bool refused = false;
     if (n > 0 && before.rows + at.rows + n > p.num_rows) {
       refused = true;
       raise(p.status, XQA_ERR_BAD_OFFSETS);
-    } else if (need > 0 && (long long)before.pages + at.pages + need > free_now) {
+    } else if (need > 0 && (long long)before.pages + at.pages + need > height) {
       refused = true;
       raise(p.status, XQA_ERR_NO_PAGES);
     }
     const int served = refused ? 0 : n;
     if (__syncthreads_or(refused)) {  // rows and pages of those that are left
       Two left;
-      const Two now = scan2(Two{served, refused ? 0 : need}, sums, left);
+      const Two now = scan2<kThreads>(Two{served, refused ? 0 : need}, sums, left);
       if (b < p.batch) {
         row0[b] = (int)(rows + now.rows);
         page0[b] = taken + now.pages;
@@ -155,8 +166,9 @@ __global__ void __launch_bounds__(kPageThreads) assign_kernel(const PagesParams 
   }
   if (kCluster) cg::this_cluster().sync();  // every CTA has read what is written below
   else __syncthreads();
+  const int free_now = height;
   const int ctas = kCluster ? gridDim.x : 1;
-  const int first = blockIdx.x * kPageThreads + tid, stride = ctas * kPageThreads;
+  const int first = blockIdx.x * kThreads + tid, stride = ctas * kThreads;
   for (int b = first; b <= p.batch; b += stride) {
     p.cu_seqlens[b] = row0[b];
     if (b < p.batch) p.new_lens[b] = old[b] + (row0[b + 1] - row0[b]);
@@ -169,134 +181,152 @@ __global__ void __launch_bounds__(kPageThreads) assign_kernel(const PagesParams 
     if ((uint32_t)id >= (uint32_t)p.num_blocks) raise(p.status, XQA_ERR_BAD_BLOCK_ID);
   }
   if (!p.slots && !p.positions) return;
-  // four rows to a thread: one search, one 16-byte write
+  // four rows to a thread: one search, four table entries asked for at once, 16-byte writes
   for (int r0 = 4 * first; r0 < p.num_rows; r0 += 4 * stride) {
-    int slot[4], pos[4];
     int b = r0 < rows ? last_at_most(row0, p.batch, r0) : 0;
-    int page = -1, id = -1;  // the last one looked up
+    int pos[4], id[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int r = r0 + k;
-      slot[k] = pos[k] = -1;
+      pos[k] = id[k] = -1;
       if (r >= rows) continue;
-      if (r >= row0[b + 1]) {
-        do ++b;
-        while (r >= row0[b + 1]);
-        page = -1;
-      }
-      pos[k] = old[b] + (r - row0[b]);
-      if (!p.slots) continue;
-      const int j = pos[k] / kBlockSize;
-      if (j != page) {
-        page = j;
-        const int fresh = j - pages_of(old[b]);  // its table entry is being written
-        id = fresh < 0 ? p.block_tables[(size_t)b * p.max_blocks_per_seq + j]
-                       : p.free_pages[free_now - 1 - (page0[b] + fresh)];
-        if ((uint32_t)id >= (uint32_t)p.num_blocks) {
-          raise(p.status, XQA_ERR_BAD_BLOCK_ID);
-          id = -1;
-        }
-      }
-      slot[k] = id < 0 ? -1 : id * kBlockSize + pos[k] % kBlockSize;
+      while (r >= row0[b + 1]) ++b;
+      const int c = old[b];
+      pos[k] = c + (r - row0[b]);
+      const int j = pos[k] / kBlockSize, fresh = j - pages_of(c);  // fresh: its entry is being written
+      const int32_t* entry = fresh < 0 ? p.block_tables + (size_t)b * p.max_blocks_per_seq + j
+                                       : p.free_pages + (free_now - 1 - (page0[b] + fresh));
+      if (p.slots) id[k] = *entry;
     }
     auto write = [&](int32_t* dst, const int (&v)[4]) {
       if (!dst) return;
       if (r0 + 4 <= p.num_rows && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
         *reinterpret_cast<int4*>(dst + r0) = make_int4(v[0], v[1], v[2], v[3]);
       } else {
+#pragma unroll
         for (int k = 0; k < 4; ++k)
           if (r0 + k < p.num_rows) dst[r0 + k] = v[k];
       }
     };
-    write(p.slots, slot);
     write(p.positions, pos);
+    if (!p.slots) continue;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (pos[k] < 0) continue;
+      if ((uint32_t)id[k] < (uint32_t)p.num_blocks) id[k] = id[k] * kBlockSize + pos[k] % kBlockSize;
+      else id[k] = -1, raise(p.status, XQA_ERR_BAD_BLOCK_ID);
+    }
+    write(p.slots, id);
   }
 }
 
-// Table entries are taken in pieces of `piece` pages, a warp to a piece: the valid ones are
-// counted, every CTA of the cluster is told, and after a scan they are written.
-template <bool kCluster>
-__global__ void __launch_bounds__(kPageThreads) release_kernel(const PagesParams p, int piece,
-                                                               int pieces_per_seq) {
-  extern __shared__ int smem[];  // [batch * pieces_per_seq] valid entries, then those before
+// The entries that go back form one list, sequence after sequence, of which every warp takes
+// an equal run: it counts the valid ones, every CTA of the cluster is told, and behind a scan of
+// the warps' counts they are written.
+constexpr int kPerLane = 8;  // entries of a lane in flight at once
+template <int kThreads, bool kCluster>
+__global__ void __launch_bounds__(kThreads) release_kernel(const PagesParams p) {
+  extern __shared__ int smem[];
+  int* first = smem;                  // [batch + 1] entries before each sequence's
+  int* lens = first + p.batch + 1;    // [batch] new lengths
+  constexpr int kWarps = kThreads / 32;
   __shared__ Two sums[kWarps];
+  __shared__ int count[kClusterCtas * kWarps];
   __shared__ int height;
   griddep_launch_dependents();
+  if (kCluster) cluster_arrive();  // (this CTA runs: its memory is there)
   griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31;
   const int ctas = kCluster ? gridDim.x : 1;
-  const int warp0 = blockIdx.x * kWarps + (tid >> 5), warps = ctas * kWarps;
-  const int items = p.batch * pieces_per_seq;
+  const int warp = blockIdx.x * kWarps + (tid >> 5), warps = ctas * kWarps;
   if (tid == 0) height = stack_height(p);
-  auto range = [&](int item, int& b, int& from, int& to) {  // table entries of a piece
-    b = item / pieces_per_seq;
-    from = (item - b * pieces_per_seq) * piece;
-    to = 0;
-    if (!p.done[b]) return;
-    const int c = p.context_lens[b];
-    if (c < 0 || c > (long long)p.max_blocks_per_seq * kBlockSize) {
-      raise(p.status, XQA_ERR_CTX_TOO_LONG);
-      return;
+  int entries = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+    const int b = b0 + tid;
+    int pages = 0;
+    if (b < p.batch) {
+      const bool ends = p.done[b] != 0;
+      const int c = p.context_lens[b];
+      const bool bad = c < 0 || c > (long long)p.max_blocks_per_seq * kBlockSize;
+      if (ends && bad) raise(p.status, XQA_ERR_CTX_TOO_LONG);
+      pages = ends && !bad ? pages_of(c) : 0;
+      lens[b] = ends ? 0 : c;
     }
-    to = min(from + piece, pages_of(c));
-  };
-  if (kCluster) cg::this_cluster().sync();  // every CTA of the cluster runs: its memory is there
-  for (int item = warp0; item < items; item += warps) {
-    int b, from, to, count = 0;
-    range(item, b, from, to);
-    const int32_t* row = p.block_tables + (size_t)b * p.max_blocks_per_seq;
-#pragma unroll 4
-    for (int j = from + lane; j < to; j += 32) {
-      const bool good = (uint32_t)row[j] < (uint32_t)p.num_blocks;
-      count += good;
-      if (!good) raise(p.status, XQA_ERR_BAD_BLOCK_ID);
-    }
-    count = __reduce_add_sync(kAll, count);
-    if (kCluster) {
-      if (lane < ctas) *cg::this_cluster().map_shared_rank(smem + item, lane) = count;
-    } else if (lane == 0) {
-      smem[item] = count;
-    }
-  }
-  if (kCluster) cg::this_cluster().sync();
-  else __syncthreads();
-  const int free_now = height;
-  long long total = 0;
-  for (int i0 = 0; i0 < items; i0 += kPageThreads) {
-    const int i = i0 + tid;
     Two all;
-    const Two at = scan2(Two{i < items ? smem[i] : 0, 0}, sums, all);
-    if (i < items) smem[i] = (int)min(total + at.rows, (long long)p.num_blocks);
-    total += all.rows;
+    const Two at = scan2<kThreads>(Two{0, pages}, sums, all);
+    if (b < p.batch) first[b] = entries + at.pages;
+    entries += all.pages;
   }
+  if (tid == 0) first[p.batch] = entries;
   __syncthreads();
-  if (free_now + total > p.num_blocks && tid == 0) raise(p.status, XQA_ERR_NO_PAGES);
-  for (int item = warp0; item < items; item += warps) {
-    int b, from, to;
-    range(item, b, from, to);
-    const int32_t* row = p.block_tables + (size_t)b * p.max_blocks_per_seq;
-    int at = free_now + smem[item];
-    for (int j0 = from; j0 < to; j0 += 32) {
-      const int id = j0 + lane < to ? row[j0 + lane] : -1;
-      const unsigned good = __ballot_sync(kAll, (uint32_t)id < (uint32_t)p.num_blocks);
-      const int mine = at + __popc(good & ((1u << lane) - 1));
-      if ((good >> lane & 1) && mine < p.num_blocks) p.free_pages[mine] = id;
-      at += __popc(good);
+  const int run = (int)(((long long)entries + 32 * warps - 1) / (32 * warps) * 32);
+  const int from = (int)min((long long)warp * run, (long long)entries), to = min(from + run, entries);
+  // A lane's entries ascend: its sequence is looked for again only where one ends.
+  struct At {
+    const int32_t* row;  // row[i]: the table's entry of list entry i < next
+    int next;
+  };
+  auto read = [&](int i0, At& at, int (&id)[kPerLane]) {  // entries i0 + 32 e + lane; -1 past the run
+#pragma unroll
+    for (int e = 0; e < kPerLane; ++e) {
+      const int i = i0 + 32 * e + lane;
+      id[e] = -1;
+      if (i >= to) continue;
+      if (i >= at.next) {
+        const int b = last_at_most(first, p.batch, i);
+        at.row = p.block_tables + ((long long)b * p.max_blocks_per_seq - first[b]);
+        at.next = first[b + 1];
+      }
+      id[e] = at.row[i];
+    }
+  };
+  int good = 0, id[kPerLane];
+  At place{nullptr, 0};
+  for (int i0 = from; i0 < to; i0 += 32 * kPerLane) {
+    read(i0, place, id);
+#pragma unroll
+    for (int e = 0; e < kPerLane; ++e) {
+      const bool ok = (uint32_t)id[e] < (uint32_t)p.num_blocks;
+      good += ok;
+      if (!ok && i0 + 32 * e + lane < to) raise(p.status, XQA_ERR_BAD_BLOCK_ID);
     }
   }
-  // the lengths: each sequence's only after the last read of it, by any CTA
-  if (kCluster) cg::this_cluster().sync();
-  else __syncthreads();
-  for (int b = blockIdx.x * kPageThreads + tid; b < p.batch; b += ctas * kPageThreads)
-    p.new_lens[b] = p.done[b] ? 0 : p.context_lens[b];
+  good = __reduce_add_sync(kAll, good);
+  if (kCluster) {
+    cluster_wait();
+    if (lane < ctas) *cg::this_cluster().map_shared_rank(count + warp, lane) = good;
+    cg::this_cluster().sync();  // every count is there, and every CTA has read the lengths
+  } else {
+    if (lane == 0) count[warp] = good;
+    __syncthreads();
+  }
+  const int free_now = height;
+  Two all;
+  const Two mine = scan2<kThreads>(Two{tid < warps ? count[tid] : 0, 0}, sums, all);
+  if (tid < warps) count[tid] = (int)mine.rows;
+  __syncthreads();
+  if (free_now + all.rows > p.num_blocks && tid == 0) raise(p.status, XQA_ERR_NO_PAGES);
+  for (int b = blockIdx.x * kThreads + tid; b < p.batch; b += ctas * kThreads) p.new_lens[b] = lens[b];
   if (blockIdx.x == 0 && tid == 0)
-    *p.new_free = (int)min(free_now + total, (long long)p.num_blocks);
+    *p.new_free = (int)min(free_now + all.rows, (long long)p.num_blocks);
+  long long at = (long long)free_now + count[warp];
+  place.next = 0;
+  for (int i0 = from; i0 < to; i0 += 32 * kPerLane) {
+    if (run > 32 * kPerLane) read(i0, place, id);  // (one round's are still there)
+#pragma unroll
+    for (int e = 0; e < kPerLane; ++e) {
+      const unsigned some = __ballot_sync(kAll, (uint32_t)id[e] < (uint32_t)p.num_blocks);
+      const long long slot = at + __popc(some & ((1u << lane) - 1));
+      if ((some >> lane & 1) && slot < p.num_blocks) p.free_pages[slot] = id[e];
+      at += __popc(some);
+    }
+  }
 }
 
-cudaLaunchConfig_t config(int ctas, size_t smem, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
+cudaLaunchConfig_t config(int ctas, int threads, size_t smem, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kPageThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -309,40 +339,41 @@ cudaLaunchConfig_t config(int ctas, size_t smem, cudaStream_t stream, cudaLaunch
   return cfg;
 }
 
-constexpr int kClusterCtas = 8;  // the largest portable cluster
-
 }  // namespace
 
-// One CTA where it has a few rounds of rows or entries, else the cluster.
+// A small CTA where one round of it takes every sequence and row, a large one where it has few
+// rows or pages to write, else the cluster. Step of 16 tokens: 4.7 us in 256 threads, 6.4 in
+// 1024 (a barrier of 32 warps at each turn).
 cudaError_t launch_assign(const PagesParams& p, cudaStream_t stream) {
-  const int ctas = p.num_rows <= 4 * 4 * kPageThreads ? 1 : kClusterCtas;
+  const bool small = p.batch <= kSmallThreads && p.num_rows <= 4 * kSmallThreads;
+  const int ctas = p.num_rows <= 4 * kLargeThreads ? 1 : kClusterCtas;
   const size_t smem = sizeof(int) * (3 * (size_t)p.batch + 2);
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = config(ctas, smem, stream, attr);
-  return ctas > 1 ? cudaLaunchKernelEx(&cfg, assign_kernel<true>, p)
-                  : cudaLaunchKernelEx(&cfg, assign_kernel<false>, p);
+  const cudaLaunchConfig_t cfg = config(ctas, small ? kSmallThreads : kLargeThreads, smem, stream, attr);
+  if (small) return cudaLaunchKernelEx(&cfg, assign_kernel<kSmallThreads, false>, p);
+  return ctas > 1 ? cudaLaunchKernelEx(&cfg, assign_kernel<kLargeThreads, true>, p)
+                  : cudaLaunchKernelEx(&cfg, assign_kernel<kLargeThreads, false>, p);
 }
 
+// (how many pages go back is known to the device alone: the tables' width stands for it)
 cudaError_t launch_release(const PagesParams& p, cudaStream_t stream) {
-  int piece = 512;
-  while (((long long)p.max_blocks_per_seq + piece - 1) / piece * p.batch > kMaxReleasePieces) piece *= 2;
-  const int per_seq = (p.max_blocks_per_seq + piece - 1) / piece;
-  const int items = per_seq * p.batch;
-  const int ctas = items <= 4 * kWarps ? 1 : kClusterCtas;
+  const bool small = p.batch <= kSmallThreads &&
+                     (long long)p.batch * p.max_blocks_per_seq <= 32ll * kPerLane * (kSmallThreads / 32);
+  const size_t smem = sizeof(int) * (2 * (size_t)p.batch + 1);
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = config(ctas, sizeof(int) * (size_t)items, stream, attr);
-  return ctas > 1 ? cudaLaunchKernelEx(&cfg, release_kernel<true>, p, piece, per_seq)
-                  : cudaLaunchKernelEx(&cfg, release_kernel<false>, p, piece, per_seq);
+  const cudaLaunchConfig_t cfg = config(small ? 1 : kClusterCtas, small ? kSmallThreads : kLargeThreads,
+                                        smem, stream, attr);
+  return small ? cudaLaunchKernelEx(&cfg, release_kernel<kSmallThreads, false>, p)
+               : cudaLaunchKernelEx(&cfg, release_kernel<kLargeThreads, true>, p);
 }
 
 cudaError_t set_pages_attributes() {
   const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  const int assign = sizeof(int) * (3 * kMaxPagesBatch + 2), release = sizeof(int) * kMaxReleasePieces;
+  const int assign = sizeof(int) * (3 * kMaxPagesBatch + 2), release = sizeof(int) * (2 * kMaxPagesBatch + 1);
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(assign_kernel<true>, a, assign)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(assign_kernel<false>, a, assign)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(release_kernel<true>, a, release)) != cudaSuccess) return e;
-  return cudaFuncSetAttribute(release_kernel<false>, a, release);
+  if ((e = cudaFuncSetAttribute(assign_kernel<kLargeThreads, true>, a, assign)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(assign_kernel<kLargeThreads, false>, a, assign)) != cudaSuccess) return e;
+  return cudaFuncSetAttribute(release_kernel<kLargeThreads, true>, a, release);
 }
 
 }  // namespace xqa

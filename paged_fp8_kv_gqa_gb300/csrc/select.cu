@@ -204,163 +204,318 @@ __device__ __forceinline__ int dp2_hi(uint32_t a, uint32_t b, int c) {  // bytes
   return d;
 }
 
+constexpr int kBins = 2048;
+constexpr int kKeysInSmem = 8192;  // of a segment of up to 131072 tokens
+
+constexpr int kWarpPages = 16;  // pages of a warp at a time: all their loads in flight at once
+constexpr int kQueryParts = kSelectThreads / kHeadDim;
+
+static_assert(kWarpPages * kSelectWarps == kSelectPages, "pages of a CTA at a time");
+
 struct SelectShared {
-  short ab[2][kHeadDim];  // A, B
+  alignas(16) uint32_t keys[kKeysInSmem];
+  int bins[kBins];
+  alignas(16) uint32_t ab[kQueryParts][kHeadDim];  // A (low half), B of some of the heads
   uint32_t amax[kSelectWarps];
-  int count[kSelectWarps][2];
-  int total;
+  int count[kSelectWarps][3];
+  uint32_t edge[kSelectWarps][2];
+  int bin, above, size;  // the bin that holds the key in question; keys above it, in it
+  uint32_t some[32], t;  // its keys, where they are few; the key
+  int num_some, ties;
   int last;
   int status;
 };
 
-// A and B of a segment's queries into shared memory.
-__device__ __forceinline__ void group_query(const SelectParams& p, int seg, SelectShared& sh) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  const uint16_t* q = p.q + (size_t)seg * p.group * kHeadDim;  // [B, Hkv, G, 128]
-  uint32_t top = 0;  // magnitudes order like their patterns; those that are not finite count as 0
-  for (int i = tid; i < p.group * kHeadDim; i += kSelectThreads) {
-    const uint32_t m = q[i] & 0x7fffu;
+// Keys of a segment's pages from .. to - 1 (id: the table's entry of the warp's first page +
+// lane; q: element tid + 512 k of the group's queries).
+constexpr int kQueryLoads = kMaxCols * kHeadDim / kSelectThreads;
+__device__ __forceinline__ void score_pages(const SelectParams& p, int seg, int pages, int from, int to,
+                                            int id, const uint32_t (&q)[kQueryLoads],
+                                            SelectShared& sh, uint32_t* keys) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 7, at = lane >> 3;
+  const int b = seg / p.num_kv_heads, head = seg - b * p.num_kv_heads;
+  const int32_t* table = p.block_tables + (size_t)b * p.max_blocks_per_seq;
+  // magnitudes order like their patterns; those that are not finite count as 0
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < kQueryLoads; ++k) {
+    const uint32_t m = q[k] & 0x7fffu;
     if (m < 0x7c00u) top = max(top, m);
   }
   top = __reduce_max_sync(kAll, top);
-  if (lane == 0) sh.amax[tid >> 5] = top;
+  if (lane == 0) sh.amax[warp] = top;
   __syncthreads();
+#pragma unroll
   for (int w = 0; w < kSelectWarps; ++w) top = max(top, sh.amax[w]);
   const int f = top > 0 ? exponent(__half2float(__ushort_as_half((unsigned short)top))) - 5 : 0;
   const float step = pow2(-f);
-  if (tid < kHeadDim) {
-    int a = 0, b = 0;
-    for (int g = 0; g < p.group; ++g) {
-      const uint32_t v = q[g * kHeadDim + tid];
-      if ((v & 0x7c00u) == 0x7c00u) continue;
-      const int x = (int)rintf(__half2float(__ushort_as_half((unsigned short)v)) * step);
-      a += max(x, 0);
-      b += min(x, 0);
-    }
-    sh.ab[0][tid] = (short)a;
-    sh.ab[1][tid] = (short)b;
-  }
-  __syncthreads();
-}
-
-// Keys of a segment's pages from .. to - 1.
-__device__ __forceinline__ void score_pages(const SelectParams& p, int seg, int pages, int from, int to,
-                                            SelectShared& sh, uint32_t* keys) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 7, at = lane >> 3;
-  const int b = seg / p.num_kv_heads, head = seg - b * p.num_kv_heads;
-  const int32_t* table = p.block_tables + (size_t)b * p.max_blocks_per_seq;
-  uint32_t qa[8], qb[8];  // dims 16 c .. 16 c + 15, in pairs
+  int a = 0, n = 0;  // positive, negative
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    qa[i] = reinterpret_cast<const uint32_t*>(sh.ab[0])[8 * c + i];
-    qb[i] = reinterpret_cast<const uint32_t*>(sh.ab[1])[8 * c + i];
+  for (int k = 0; k < kQueryLoads; ++k) {
+    if ((q[k] & 0x7c00u) == 0x7c00u) continue;
+    const int x = (int)rintf(__half2float(__ushort_as_half((unsigned short)q[k])) * step);
+    a += max(x, 0);
+    n += min(x, 0);
   }
-  for (int j0 = from + 32 * warp; j0 < to; j0 += 32 * kSelectWarps) {  // 32 pages, four at a time
-    const int id = j0 + lane < to ? table[j0 + lane] : 0;
-    const bool good = (uint32_t)id < (uint32_t)p.num_blocks;
+  sh.ab[tid / kHeadDim][tid % kHeadDim] = (uint32_t)(a & 0xffff) | (uint32_t)n << 16;
+  __syncthreads();
+  uint32_t qa[8], qb[8];  // A and B of dims 16 c .. 16 c + 15, in pairs
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int r = 0; r < kQueryParts; ++r) {
+      const uint4 x = *reinterpret_cast<const uint4*>(&sh.ab[r][16 * c + 4 * i]);
+      v.x = __vadd2(v.x, x.x), v.y = __vadd2(v.y, x.y), v.z = __vadd2(v.z, x.z), v.w = __vadd2(v.w, x.w);
+    }
+    qa[2 * i] = prmt(v.x, v.y, 0x5410u), qa[2 * i + 1] = prmt(v.z, v.w, 0x5410u);
+    qb[2 * i] = prmt(v.x, v.y, 0x7632u), qb[2 * i + 1] = prmt(v.z, v.w, 0x7632u);
+  }
+  for (int j0 = from + kWarpPages * warp; j0 < to; j0 += kWarpPages * kSelectWarps) {
+    if (j0 > from + kWarpPages * warp) id = lane < kWarpPages && j0 + lane < to ? table[j0 + lane] : 0;
+    const bool mine = lane < kWarpPages && j0 + lane < to;
+    const bool good = !mine || (uint32_t)id < (uint32_t)p.num_blocks;
     if (!good) record_status(&sh.status, XQA_ERR_BAD_BLOCK_ID);
-    uint32_t key = 0;
-#pragma unroll 4
-    for (int s = 0; s < 8; ++s) {
-      const int page = __shfl_sync(kAll, good ? id : 0, 4 * s + at);
+    const int page0 = mine && good ? id : 0;
+    uint4 hi[kWarpPages / 4], lo[kWarpPages / 4];
+    int e[kWarpPages / 4];
+#pragma unroll
+    for (int s = 0; s < kWarpPages / 4; ++s) {
+      const int page = __shfl_sync(kAll, page0, 4 * s + at);
       const uint8_t* bd = p.bounds + ((size_t)page * p.num_kv_heads + head) * kBoundsBytes;
-      const uint4 hi = *reinterpret_cast<const uint4*>(bd + 16 * c);
-      const uint4 lo = *reinterpret_cast<const uint4*>(bd + kHeadDim + 16 * c);
-      const int e = (int)(signed char)bd[2 * kHeadDim];
+      hi[s] = *reinterpret_cast<const uint4*>(bd + 16 * c);
+      lo[s] = *reinterpret_cast<const uint4*>(bd + kHeadDim + 16 * c);
+      e[s] = (int)(signed char)bd[2 * kHeadDim];
+    }
+    uint32_t key = 0;
+#pragma unroll
+    for (int s = 0; s < kWarpPages / 4; ++s) {
       int sum = 0;
-      sum = dp2_lo(qa[0], hi.x, sum), sum = dp2_hi(qa[1], hi.x, sum);
-      sum = dp2_lo(qa[2], hi.y, sum), sum = dp2_hi(qa[3], hi.y, sum);
-      sum = dp2_lo(qa[4], hi.z, sum), sum = dp2_hi(qa[5], hi.z, sum);
-      sum = dp2_lo(qa[6], hi.w, sum), sum = dp2_hi(qa[7], hi.w, sum);
-      sum = dp2_lo(qb[0], lo.x, sum), sum = dp2_hi(qb[1], lo.x, sum);
-      sum = dp2_lo(qb[2], lo.y, sum), sum = dp2_hi(qb[3], lo.y, sum);
-      sum = dp2_lo(qb[4], lo.z, sum), sum = dp2_hi(qb[5], lo.z, sum);
-      sum = dp2_lo(qb[6], lo.w, sum), sum = dp2_hi(qb[7], lo.w, sum);
+      sum = dp2_lo(qa[0], hi[s].x, sum), sum = dp2_hi(qa[1], hi[s].x, sum);
+      sum = dp2_lo(qa[2], hi[s].y, sum), sum = dp2_hi(qa[3], hi[s].y, sum);
+      sum = dp2_lo(qa[4], hi[s].z, sum), sum = dp2_hi(qa[5], hi[s].z, sum);
+      sum = dp2_lo(qa[6], hi[s].w, sum), sum = dp2_hi(qa[7], hi[s].w, sum);
+      sum = dp2_lo(qb[0], lo[s].x, sum), sum = dp2_hi(qb[1], lo[s].x, sum);
+      sum = dp2_lo(qb[2], lo[s].y, sum), sum = dp2_hi(qb[3], lo[s].y, sum);
+      sum = dp2_lo(qb[4], lo[s].z, sum), sum = dp2_hi(qb[5], lo[s].z, sum);
+      sum = dp2_lo(qb[6], lo[s].w, sum), sum = dp2_hi(qb[7], lo[s].w, sum);
 #pragma unroll
       for (int off = 1; off < 8; off <<= 1) sum += __shfl_xor_sync(kAll, sum, off);
-      const uint32_t k = e == kNotFinite ? kKeyFirst : key_of((float)sum * pow2(max(e, -126)));
-      const uint32_t mine = __shfl_sync(kAll, k, (lane & 3) * 8);  // page 4 s + (lane & 3)
-      if (lane >> 2 == s) key = mine;
+      const uint32_t k = e[s] == kNotFinite ? kKeyFirst : key_of((float)sum * pow2(max(e[s], -126)));
+      const uint32_t got = __shfl_sync(kAll, k, (lane & 3) * 8);  // page 4 s + (lane & 3)
+      if (lane >> 2 == s) key = got;
     }
     const int j = j0 + lane;
     if (!good) key = kKeyFirst;  // is met, and reported, by whoever reads it
     if (j < p.first_pages || j >= pages - p.last_pages) key = kKeyAlways;
-    if (j < to) keys[j] = key;
+    if (mine) keys[j] = key;
   }
-}
-
-// Block-wide sum; every thread calls it.
-__device__ __forceinline__ int sum_all(int v, SelectShared& sh) {
-  v = __reduce_add_sync(kAll, v);
-  if ((threadIdx.x & 31) == 0) sh.count[threadIdx.x >> 5][0] = v;
-  __syncthreads();
-  int s = 0;
-#pragma unroll
-  for (int w = 0; w < kSelectWarps; ++w) s += sh.count[w][0];
-  __syncthreads();
-  return s;
 }
 
 // The `take` largest of n keys, the lowest index first among equal ones, as ascending indices.
+//
+// The take-th largest key t by a histogram over the keys' range, whose bin that holds it is
+// the next range: the range shrinks by a factor of 2048 a round, and as it is the keys' own
+// (not their leading bits, which scores of one sequence share) its bins fill evenly. Bit by
+// bit (32 rounds of counting) the choice of 128 of 1100 pages x 64 took 23.8 us, so 8.
 __device__ __forceinline__ void take_pages(const SelectParams& p, int seg, int n, int take,
-                                           const uint32_t* keys, SelectShared& sh) {
+                                           const uint32_t* from_chunks, SelectShared& sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // the take-th largest key, bit by bit: the largest t that at least `take` keys reach
-  uint32_t t = 0;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t probe = t | 1u << bit;
-    int c = 0;
-    for (int i = tid; i < n; i += kSelectThreads) c += keys[i] >= probe;
-    if (sum_all(c, sh) >= take) t = probe;
+  const uint32_t* keys = from_chunks;
+  // smallest and largest score, and how many pages come before all of them
+  uint32_t low = 0xffffffffu, high = 0;
+  int always = 0, special = 0;
+  const bool staged = n <= kKeysInSmem;
+  constexpr int kAtOnce = 4;  // 16-byte loads of a thread in flight (rows of keys are 16-byte aligned)
+  for (int i0 = 0; i0 < n; i0 += 4 * kAtOnce * kSelectThreads) {
+    uint4 k[kAtOnce];
+#pragma unroll
+    for (int e = 0; e < kAtOnce; ++e) {
+      const int i = i0 + 4 * (e * kSelectThreads + tid);
+      k[e] = i < n ? __ldcg(reinterpret_cast<const uint4*>(from_chunks + i)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int e = 0; e < kAtOnce; ++e) {
+      const int i = i0 + 4 * (e * kSelectThreads + tid);
+      if (i >= n) continue;
+      if (staged) *reinterpret_cast<uint4*>(sh.keys + i) = k[e];
+      const uint32_t w[4] = {k[e].x, k[e].y, k[e].z, k[e].w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (i + x >= n) continue;
+        if (w[x] >= kKeyFirst) {
+          special += 1;
+          always += w[x] == kKeyAlways;
+        } else {
+          low = min(low, w[x]);
+          high = max(high, w[x]);
+        }
+      }
+    }
   }
-  int c = 0;
-  for (int i = tid; i < n; i += kSelectThreads) c += keys[i] > t;
-  const int ties = take - sum_all(c, sh);  // of the keys equal to t, the first so many
-  // each warp writes those of a run of keys, behind the ones of the warps before it
+  if (staged) keys = sh.keys;
+  special = __reduce_add_sync(kAll, special);
+  always = __reduce_add_sync(kAll, always);
+  low = __reduce_min_sync(kAll, low);
+  high = __reduce_max_sync(kAll, high);
+  if (lane == 0) {
+    sh.count[warp][0] = special;
+    sh.count[warp][1] = always;
+    sh.edge[warp][0] = low;
+    sh.edge[warp][1] = high;
+  }
+  __syncthreads();
+  special = always = 0;
+#pragma unroll
+  for (int w = 0; w < kSelectWarps; ++w) {
+    special += sh.count[w][0];
+    always += sh.count[w][1];
+    low = min(low, sh.edge[w][0]);
+    high = max(high, sh.edge[w][1]);
+  }
+  uint32_t t = kKeyFirst;    // the take-th largest key
+  int ties = take - always;  // of the keys equal to it, the first so many
+  if (special < take) {
+    int want = take - special;  // the want-th largest of [low, high]
+    for (;;) {
+      const int bits = 32 - __clz(high - low);
+      const int shift = bits > 11 ? bits - 11 : 0;
+      for (int i = tid; i < n; i += kSelectThreads) {
+        const uint32_t k = keys[i];
+        if (k >= low && k <= high) atomicAdd(&sh.bins[(k - low) >> shift], 1);
+      }
+      __syncthreads();
+      // bins from the top: 8 to a thread, thread 0 the highest; left at zero for the next
+      constexpr int kPer = kBins / kSelectThreads;
+      int mine[kPer], sum = 0;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        int& bin = sh.bins[kBins - 1 - (tid * kPer + e)];
+        sum += mine[e] = bin;
+        bin = 0;
+      }
+      int incl = sum;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_up_sync(kAll, incl, off);
+        if (lane >= off) incl += x;
+      }
+      if (lane == 31) sh.count[warp][2] = incl;
+      __syncthreads();
+      int above = incl - sum;
+      for (int w = 0; w < warp; ++w) above += sh.count[w][2];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        if (above < want && above + mine[e] >= want) {
+          sh.bin = kBins - 1 - (tid * kPer + e);
+          sh.above = above;
+          sh.size = mine[e];
+          sh.num_some = 0;
+        }
+        above += mine[e];
+      }
+      __syncthreads();
+      want -= sh.above;
+      const uint32_t start = low + ((uint32_t)sh.bin << shift);
+      if (shift == 0) {
+        t = start;
+        ties = want;
+        break;
+      }
+      high = min(high, start + ((1u << shift) - 1));
+      low = start;
+      if (sh.size > 32) continue;
+      // few are left: a warp ranks them
+      for (int i = tid; i < n; i += kSelectThreads) {
+        const uint32_t k = keys[i];
+        if (k >= low && k <= high) sh.some[atomicAdd(&sh.num_some, 1)] = k;
+      }
+      __syncthreads();
+      if (warp == 0) {
+        const bool in = lane < sh.size;
+        const uint32_t k = in ? sh.some[lane] : 0u;
+        int larger = 0, equal = 0;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const uint32_t x = __shfl_sync(kAll, k, e);
+          larger += e < sh.size && x > k;
+          equal += e < sh.size && x == k;
+        }
+        if (in && larger < want && larger + equal >= want) sh.t = k, sh.ties = want - larger;
+      }
+      __syncthreads();
+      t = sh.t;
+      ties = sh.ties;
+      break;
+    }
+  }
+  __syncthreads();
+  // each warp writes those of a run of keys, behind the ones of the warps before it: their
+  // indices first, so that no table entry is waited for on the way
   const int run = ((n + kSelectWarps - 1) / kSelectWarps + 31) & ~31;
   const int from = min(n, warp * run), to = min(n, from + run);
   int above = 0, equal = 0;
   for (int i0 = from; i0 < to; i0 += 32) {
     const uint32_t k = i0 + lane < to ? keys[i0 + lane] : 0;
-    above += __popc(__ballot_sync(kAll, i0 + lane < to && k > t));
-    equal += __popc(__ballot_sync(kAll, i0 + lane < to && k == t));
+    above += i0 + lane < to && k > t;
+    equal += i0 + lane < to && k == t;
   }
+  above = __reduce_add_sync(kAll, above);
+  equal = __reduce_add_sync(kAll, equal);
   if (lane == 0) sh.count[warp][0] = above, sh.count[warp][1] = equal;
   __syncthreads();
   int at = 0, eq = 0;
   for (int w = 0; w < warp; ++w) at += sh.count[w][0], eq += sh.count[w][1];
   at += min(eq, ties);
-  const int b = seg / p.num_kv_heads;
-  const int32_t* table = p.block_tables + (size_t)b * p.max_blocks_per_seq;
   int32_t* out = p.selected + (size_t)seg * p.max_pages;
+  int* list = take <= kBins ? sh.bins : out;
   for (int i0 = from; i0 < to; i0 += 32) {
     const int i = i0 + lane;
     const uint32_t k = i < to ? keys[i] : 0;
     const unsigned eqs = __ballot_sync(kAll, i < to && k == t);
-    const unsigned below = (1u << lane) - 1;
-    const bool mine = i < to && (k > t || (k == t && eq + __popc(eqs & below) < ties));
+    const unsigned before = (1u << lane) - 1;
+    const bool mine = i < to && (k > t || (k == t && eq + __popc(eqs & before) < ties));
     const unsigned some = __ballot_sync(kAll, mine);
-    if (mine) out[at + __popc(some & below)] = table[i];
+    if (mine) list[at + __popc(some & before)] = i;
     at += __popc(some);
     eq += __popc(eqs);
   }
+  __syncthreads();
+  const int32_t* table = p.block_tables + (size_t)(seg / p.num_kv_heads) * p.max_blocks_per_seq;
+  for (int i = tid; i < take; i += kSelectThreads) {
+    const int j = list[i];
+    if (list == sh.bins) sh.bins[i] = 0;
+    out[i] = table[j];
+  }
 }
 
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kSelectThreads, kSelectCtas) select_kernel(const SelectParams p) {
   __shared__ __align__(16) SelectShared sh;
   griddep_launch_dependents();
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   if (tid == 0) sh.status = XQA_OK;
+  for (int i = tid; i < kBins; i += kSelectThreads) sh.bins[i] = 0;
   __syncthreads();
   griddep_wait();
   const long long units = (long long)p.batch * p.num_kv_heads * p.chunks;
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
     const int seg = (int)(u / p.chunks), chunk = (int)(u - (long long)seg * p.chunks);
+    const int from = chunk * p.chunk_pages;
+    // what the scores need, asked for before the length says whether they are needed (the
+    // table's row is as long as it may be)
+    const int32_t* table = p.block_tables + (size_t)(seg / p.num_kv_heads) * p.max_blocks_per_seq;
+    const int first = from + kWarpPages * (tid >> 5) + lane;
+    const int id = lane < kWarpPages && first < p.max_blocks_per_seq ? table[first] : 0;
+    uint32_t q[kQueryLoads];
+#pragma unroll
+    for (int k = 0; k < kQueryLoads; ++k) {
+      const int i = tid + k * kSelectThreads;
+      q[k] = i < p.group * kHeadDim ? p.q[(size_t)seg * p.group * kHeadDim + i] : 0u;  // [B, Hkv, G, 128]
+    }
     const int ctx = p.context_lens[seg / p.num_kv_heads];
     const bool bad = ctx < 0 || ctx > (long long)p.max_blocks_per_seq * kBlockSize;
     const int pages = bad ? 0 : (ctx + kBlockSize - 1) / kBlockSize;
     const int take = min(pages, p.max_pages);
-    const int from = chunk * p.chunk_pages;
     if (chunk > 0 && (pages <= p.max_pages || from >= pages)) continue;
     int32_t* out = p.selected + (size_t)seg * p.max_pages;
     if (chunk == 0) {  // what does not depend on a score
@@ -371,7 +526,6 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
       }
     }
     if (pages <= p.max_pages) {  // all of them
-      const int32_t* table = p.block_tables + (size_t)(seg / p.num_kv_heads) * p.max_blocks_per_seq;
       for (int i = tid; i < pages; i += kSelectThreads) {
         const int id = table[i];
         out[i] = id;
@@ -379,9 +533,8 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
       }
       continue;
     }
-    uint32_t* keys = p.keys + (size_t)seg * p.max_blocks_per_seq;
-    group_query(p, seg, sh);
-    score_pages(p, seg, pages, from, min(pages, from + p.chunk_pages), sh, keys);
+    uint32_t* keys = p.keys + (size_t)seg * p.key_stride;
+    score_pages(p, seg, pages, from, min(pages, from + p.chunk_pages), id, q, sh, keys);
     const int chunks = (pages + p.chunk_pages - 1) / p.chunk_pages;
     __threadfence();
     __syncthreads();

@@ -502,7 +502,7 @@ xqa_status_t encode_nhd_map(CUtensorMap* map, const uint8_t* pool, int hkv, int 
 }
 
 struct SelectResolved {
-  int group, ctas, chunks, chunk_pages;
+  int group, ctas, chunks, chunk_pages, key_stride;
   size_t ticket_off, keys_off, bytes;
 };
 
@@ -529,18 +529,20 @@ xqa_status_t resolve_select(const xqa_select_shape_t* s, SelectResolved* r) {
     if (cudaGetDevice(&dev) != cudaSuccess) return XQA_ERR_DEVICE;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
       return XQA_ERR_DEVICE;
-    r->ctas = 4 * sms;
+    r->ctas = xqa::kSelectCtas * sms;
   }
   if (r->ctas > xqa::kMaxCtas) r->ctas = xqa::kMaxCtas;
-  // chunks of 256 pages (32 to a warp) at least, about one for each CTA
+  // about one chunk for each CTA, in whole rounds of its warps
   const long long pages = nseg * s->max_blocks_per_seq;
-  const long long chunk = ((pages / r->ctas + 255) / 256 > 0 ? (pages / r->ctas + 255) / 256 : 1) * 256;
+  long long chunk = (pages / r->ctas + xqa::kSelectPages - 1) / xqa::kSelectPages * xqa::kSelectPages;
+  if (chunk < xqa::kSelectPages) chunk = xqa::kSelectPages;
   r->chunk_pages = (int)chunk;
   r->chunks = (int)((s->max_blocks_per_seq + chunk - 1) / chunk);
   if (nseg * r->chunks < r->ctas) r->ctas = (int)(nseg * r->chunks);
   r->ticket_off = kPrefillWorkspaceBytes;
   r->keys_off = (r->ticket_off + 4 * (size_t)nseg + 255) & ~(size_t)255;
-  r->bytes = r->keys_off + 4 * (size_t)pages;
+  r->key_stride = (s->max_blocks_per_seq + 3) & ~3;
+  r->bytes = r->keys_off + 4 * (size_t)nseg * r->key_stride;
   return XQA_OK;
 }
 
@@ -972,6 +974,7 @@ xqa_status_t xqa_select(const void* q, const uint8_t* bounds, const int32_t* blo
   p.last_pages = shape->last_pages;
   p.chunks = r.chunks;
   p.chunk_pages = r.chunk_pages;
+  p.key_stride = r.key_stride;
   return xqa::launch_select(p, r.ctas, (cudaStream_t)stream) == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
 }
 

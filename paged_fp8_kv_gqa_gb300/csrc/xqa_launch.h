@@ -121,7 +121,6 @@ cudaError_t launch_extend(const CUtensorMap& tm_q, const CUtensorMap& tm_k, cons
                           const ExtendParams& p, int dtype, int ctas, cudaStream_t stream);
 // xqa_assign_pages and xqa_release_pages.
 constexpr int kMaxPagesBatch = 16384;          // sequences: three words each in shared memory
-constexpr int kMaxReleasePieces = 48 * 1024;   // pieces of tables: a word each
 
 struct PagesParams {
   const int32_t* new_tokens;    // assign
@@ -150,7 +149,9 @@ struct BoundsParams {
   int batch, num_kv_heads, max_blocks_per_seq, num_blocks, num_rows, kv_dtype, kv_layout;
 };
 
-// xqa_select.
+// xqa_select. CTAs that fit an SM at once (its launch bounds) and pages that a CTA scores at
+// a time: 16 for each of its 8 warps.
+constexpr int kSelectCtas = 3, kSelectPages = 128;
 struct SelectParams {
   const uint16_t* q;  // [B, Hq, 128] fp16
   const uint8_t* bounds;
@@ -161,7 +162,8 @@ struct SelectParams {
   int32_t* header;         // workspace header (CTAs launched)
   int32_t* status;         // [kMaxCtas]
   int32_t* tickets;        // [B * Hkv] chunks scored: zero between calls
-  uint32_t* keys;          // [B * Hkv, MBS]
+  uint32_t* keys;          // [B * Hkv, key_stride]
+  int key_stride;          // MBS, a multiple of 4
   int batch, num_kv_heads, group, max_blocks_per_seq, num_blocks;
   int max_pages, first_pages, last_pages;
   int chunks, chunk_pages;
