@@ -29,7 +29,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kClusterCtas = 8;  // the largest portable cluster
+constexpr int kClusterCtas = 16;  // (more than 8: where a GPC has them, as an sm_103 has)
 constexpr int kSmallThreads = 256, kLargeThreads = 1024;
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -372,6 +372,9 @@ cudaError_t set_pages_attributes() {
   const int assign = sizeof(int) * (3 * kMaxPagesBatch + 2), release = sizeof(int) * (2 * kMaxPagesBatch + 1);
   cudaError_t e;
   if ((e = cudaFuncSetAttribute(assign_kernel<kLargeThreads, true>, a, assign)) != cudaSuccess) return e;
+  const cudaFuncAttribute any = cudaFuncAttributeNonPortableClusterSizeAllowed;
+  if ((e = cudaFuncSetAttribute(assign_kernel<kLargeThreads, true>, any, 1)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(release_kernel<kLargeThreads, true>, any, 1)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(assign_kernel<kLargeThreads, false>, a, assign)) != cudaSuccess) return e;
   return cudaFuncSetAttribute(release_kernel<kLargeThreads, true>, a, release);
 }

@@ -271,8 +271,9 @@ __device__ __forceinline__ void score_pages(const SelectParams& p, int seg, int 
     qa[2 * i] = prmt(v.x, v.y, 0x5410u), qa[2 * i + 1] = prmt(v.z, v.w, 0x5410u);
     qb[2 * i] = prmt(v.x, v.y, 0x7632u), qb[2 * i + 1] = prmt(v.z, v.w, 0x7632u);
   }
-  for (int j0 = from + kWarpPages * warp; j0 < to; j0 += kWarpPages * kSelectWarps) {
-    if (j0 > from + kWarpPages * warp) id = lane < kWarpPages && j0 + lane < to ? table[j0 + lane] : 0;
+  constexpr int kStep = kWarpPages * kSelectWarps;
+  for (int j0 = from + kWarpPages * warp; j0 < to; j0 += kStep) {
+    const int next = lane < kWarpPages && j0 + kStep + lane < to ? table[j0 + kStep + lane] : 0;
     const bool mine = lane < kWarpPages && j0 + lane < to;
     const bool good = !mine || (uint32_t)id < (uint32_t)p.num_blocks;
     if (!good) record_status(&sh.status, XQA_ERR_BAD_BLOCK_ID);
@@ -309,7 +310,12 @@ __device__ __forceinline__ void score_pages(const SelectParams& p, int seg, int 
     if (!good) key = kKeyFirst;  // is met, and reported, by whoever reads it
     if (j < p.first_pages || j >= pages - p.last_pages) key = kKeyAlways;
     if (mine) keys[j] = key;
+    id = next;
   }
+}
+
+__device__ __forceinline__ void sum_above(int& both, uint32_t k, uint32_t t) {
+  both += k > t ? 1 : k == t ? 1 << 16 : 0;
 }
 
 // The `take` largest of n keys, the lowest index first among equal ones, as ascending indices.
@@ -318,42 +324,29 @@ __device__ __forceinline__ void score_pages(const SelectParams& p, int seg, int 
 // the next range: the range shrinks by a factor of 2048 a round, and as it is the keys' own
 // (not their leading bits, which scores of one sequence share) its bins fill evenly. Bit by
 // bit (32 rounds of counting) the choice of 128 of 1100 pages x 64 took 23.8 us, so 8.
+template <bool kInSmem>
 __device__ __forceinline__ void take_pages(const SelectParams& p, int seg, int n, int take,
-                                           const uint32_t* from_chunks, SelectShared& sh) {
+                                           const uint32_t* global, SelectShared& sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t* keys = from_chunks;
+  const uint32_t* keys = kInSmem ? sh.keys : global;
   // smallest and largest score, and how many pages come before all of them
   uint32_t low = 0xffffffffu, high = 0;
   int always = 0, special = 0;
-  const bool staged = n <= kKeysInSmem;
-  constexpr int kAtOnce = 4;  // 16-byte loads of a thread in flight (rows of keys are 16-byte aligned)
-  for (int i0 = 0; i0 < n; i0 += 4 * kAtOnce * kSelectThreads) {
-    uint4 k[kAtOnce];
+  for (int i = 4 * tid; i < n; i += 4 * kSelectThreads) {  // (rows of keys are 16-byte aligned)
+    const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+    const uint32_t w[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-    for (int e = 0; e < kAtOnce; ++e) {
-      const int i = i0 + 4 * (e * kSelectThreads + tid);
-      k[e] = i < n ? __ldcg(reinterpret_cast<const uint4*>(from_chunks + i)) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int e = 0; e < kAtOnce; ++e) {
-      const int i = i0 + 4 * (e * kSelectThreads + tid);
-      if (i >= n) continue;
-      if (staged) *reinterpret_cast<uint4*>(sh.keys + i) = k[e];
-      const uint32_t w[4] = {k[e].x, k[e].y, k[e].z, k[e].w};
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        if (i + x >= n) continue;
-        if (w[x] >= kKeyFirst) {
-          special += 1;
-          always += w[x] == kKeyAlways;
-        } else {
-          low = min(low, w[x]);
-          high = max(high, w[x]);
-        }
+    for (int x = 0; x < 4; ++x) {
+      if (i + x >= n) continue;
+      if (w[x] >= kKeyFirst) {
+        special += 1;
+        always += w[x] == kKeyAlways;
+      } else {
+        low = min(low, w[x]);
+        high = max(high, w[x]);
       }
     }
   }
-  if (staged) keys = sh.keys;
   special = __reduce_add_sync(kAll, special);
   always = __reduce_add_sync(kAll, always);
   low = __reduce_min_sync(kAll, low);
@@ -452,33 +445,51 @@ __device__ __forceinline__ void take_pages(const SelectParams& p, int seg, int n
   __syncthreads();
   // each warp writes those of a run of keys, behind the ones of the warps before it: their
   // indices first, so that no table entry is waited for on the way
-  const int run = ((n + kSelectWarps - 1) / kSelectWarps + 31) & ~31;
+  // (four keys to a lane; keys past n count as none)
+  const int run = ((n + kSelectWarps - 1) / kSelectWarps + 127) & ~127;
   const int from = min(n, warp * run), to = min(n, from + run);
-  int above = 0, equal = 0;
-  for (int i0 = from; i0 < to; i0 += 32) {
-    const uint32_t k = i0 + lane < to ? keys[i0 + lane] : 0;
-    above += i0 + lane < to && k > t;
-    equal += i0 + lane < to && k == t;
+  auto four = [&](int i, uint32_t (&k)[4]) {
+    const uint4 v = i < to ? *reinterpret_cast<const uint4*>(keys + i) : make_uint4(0, 0, 0, 0);
+    k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+  };
+  int both = 0;  // keys above t in the low half, equal to it in the high one
+  for (int i0 = from; i0 < to; i0 += 128) {
+    uint32_t k[4];
+    four(i0 + 4 * lane, k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (i0 + 4 * lane + e < to) sum_above(both, k[e], t);
   }
-  above = __reduce_add_sync(kAll, above);
-  equal = __reduce_add_sync(kAll, equal);
+  int above = __reduce_add_sync(kAll, both & 0xffff), equal = __reduce_add_sync(kAll, both >> 16);
   if (lane == 0) sh.count[warp][0] = above, sh.count[warp][1] = equal;
   __syncthreads();
   int at = 0, eq = 0;
   for (int w = 0; w < warp; ++w) at += sh.count[w][0], eq += sh.count[w][1];
-  at += min(eq, ties);
   int32_t* out = p.selected + (size_t)seg * p.max_pages;
   int* list = take <= kBins ? sh.bins : out;
-  for (int i0 = from; i0 < to; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t k = i < to ? keys[i] : 0;
-    const unsigned eqs = __ballot_sync(kAll, i < to && k == t);
-    const unsigned before = (1u << lane) - 1;
-    const bool mine = i < to && (k > t || (k == t && eq + __popc(eqs & before) < ties));
-    const unsigned some = __ballot_sync(kAll, mine);
-    if (mine) list[at + __popc(some & before)] = i;
-    at += __popc(some);
-    eq += __popc(eqs);
+  for (int i0 = from; i0 < to; i0 += 128) {  // at, eq: keys above and equal before i0
+    uint32_t k[4];
+    four(i0 + 4 * lane, k);
+    int mine = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (i0 + 4 * lane + e < to) sum_above(mine, k[e], t);
+    int incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(kAll, incl, off);
+      if (lane >= off) incl += x;
+    }
+    const int before = incl - mine, all = __shfl_sync(kAll, incl, 31);
+    int a = at + (before & 0xffff), q = eq + (before >> 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (i0 + 4 * lane + e >= to) continue;
+      if (k[e] > t) list[a++ + min(q, ties)] = i0 + 4 * lane + e;
+      else if (k[e] == t && q++ < ties) list[a + q - 1] = i0 + 4 * lane + e;
+    }
+    at += all & 0xffff;
+    eq += all >> 16;
   }
   __syncthreads();
   const int32_t* table = p.block_tables + (size_t)(seg / p.num_kv_heads) * p.max_blocks_per_seq;
@@ -533,19 +544,38 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectCtas) select_kernel(con
       }
       continue;
     }
-    uint32_t* keys = p.keys + (size_t)seg * p.key_stride;
-    score_pages(p, seg, pages, from, min(pages, from + p.chunk_pages), id, q, sh, keys);
+    // a segment of one chunk keeps its keys here
     const int chunks = (pages + p.chunk_pages - 1) / p.chunk_pages;
-    __threadfence();
+    uint32_t* keys = chunks == 1 && pages <= kKeysInSmem ? sh.keys : p.keys + (size_t)seg * p.key_stride;
+    score_pages(p, seg, pages, from, min(pages, from + p.chunk_pages), id, q, sh, keys);
     __syncthreads();
-    if (tid == 0) {
-      const int old = atom_add_acq_rel_gpu(p.tickets + seg, 1);
+    if (tid == 0) {  // (releases what the barrier has put before it)
+      const int old = chunks == 1 ? 0 : atom_add_acq_rel_gpu(p.tickets + seg, 1);
       sh.last = old == chunks - 1;
-      if (sh.last) p.tickets[seg] = 0;  // for the next call
-      __threadfence();
+      if (sh.last && chunks > 1) p.tickets[seg] = 0;  // for the next call
     }
     __syncthreads();
-    if (sh.last) take_pages(p, seg, pages, take, keys, sh);
+    if (sh.last) {
+      if (pages > kKeysInSmem) {
+        take_pages<false>(p, seg, pages, take, keys, sh);
+      } else {
+        if (chunks > 1) {  // as many 16-byte loads of a thread in flight as there are
+          constexpr int kAtOnce = kKeysInSmem / 4 / kSelectThreads;
+          uint4 k[kAtOnce];
+#pragma unroll
+          for (int e = 0; e < kAtOnce; ++e) {
+            const int i = 4 * (e * kSelectThreads + tid);
+            if (i < pages) k[e] = __ldcg(reinterpret_cast<const uint4*>(keys + i));
+          }
+#pragma unroll
+          for (int e = 0; e < kAtOnce; ++e) {
+            const int i = 4 * (e * kSelectThreads + tid);
+            if (i < pages) *reinterpret_cast<uint4*>(sh.keys + i) = k[e];
+          }
+        }
+        take_pages<true>(p, seg, pages, take, nullptr, sh);
+      }
+    }
     __syncthreads();
   }
   __syncthreads();

@@ -532,10 +532,11 @@ xqa_status_t resolve_select(const xqa_select_shape_t* s, SelectResolved* r) {
     r->ctas = xqa::kSelectCtas * sms;
   }
   if (r->ctas > xqa::kMaxCtas) r->ctas = xqa::kMaxCtas;
-  // about one chunk for each CTA, in whole rounds of its warps
-  const long long pages = nseg * s->max_blocks_per_seq;
-  long long chunk = (pages / r->ctas + xqa::kSelectPages - 1) / xqa::kSelectPages * xqa::kSelectPages;
-  if (chunk < xqa::kSelectPages) chunk = xqa::kSelectPages;
+  // As many chunks of a segment as leave no CTA a second one, in whole rounds of a CTA's
+  // warps (256 segments of 1024 pages in two chunks each, a few CTAs with two: 30.6 us)
+  const long long split = r->ctas / nseg > 1 ? r->ctas / nseg : 1;
+  long long chunk = (s->max_blocks_per_seq + split - 1) / split;
+  chunk = (chunk + xqa::kSelectPages - 1) / xqa::kSelectPages * xqa::kSelectPages;
   r->chunk_pages = (int)chunk;
   r->chunks = (int)((s->max_blocks_per_seq + chunk - 1) / chunk);
   if (nseg * r->chunks < r->ctas) r->ctas = (int)(nseg * r->chunks);
