@@ -399,8 +399,8 @@ xqa_status_t xqa_extend_workspace_size(const xqa_extend_shape_t* shape, size_t* 
  * see a token of the page are NaN), XQA_ERR_CTX_TOO_LONG (the sequence's rows are NaN),
  * XQA_ERR_BAD_OFFSETS (the sequence is skipped; where offsets descend so that sequences
  * overlap beyond total_q rows, all are), XQA_ERR_VALUE (a device k_scale that is not
- * finite or not above 0: all rows are NaN). A host scale of that kind is refused. One
- * kernel, no host synchronisation; may be captured into a CUDA graph. */
+ * finite or not above 0: all rows are NaN). A host scale of that kind is refused. Two
+ * kernels, no host synchronisation; may be captured into a CUDA graph. */
 xqa_status_t xqa_extend(const void* q, const uint8_t* k_cache, const uint8_t* v_cache,
                         const int32_t* block_tables, const int32_t* context_lens,
                         const int32_t* cu_seqlens, float k_scale, float v_scale,

@@ -15,8 +15,9 @@
 // T = floor(128 / G). The units lie on a line, each as long as the keys it sees plus a
 // constant, and every CTA takes an equal share of the line: long sequences are cut
 // anywhere, at 128-key tiles, without the host knowing a length. A unit cut into pieces
-// leaves (O, m, l) of each in 32 bits in the workspace; the CTA that is last to write a
-// piece joins them. No CTA waits for another.
+// leaves (O, m, l) of each in 32 bits in the workspace, and a second, small kernel joins
+// them with the whole GPU. (Joined by the CTA that wrote a unit's last piece, 32 tokens over
+// 131072 took 1340 us, 16 x 32 over 2048 85 us.)
 //
 // A unit of at most T tokens fills one row tile only; both chains of product, softmax
 // and product then work on it, on every other key tile each, and are joined in the
@@ -71,8 +72,6 @@ struct Unit {
   int split;     // 1: both chains work on row tile 0
   int hidden;    // first key hidden from some token
   int slot;      // place of this piece's (O, m, l); -1: the unit is one piece
-  int first;     // CTA of the unit's first piece
-  int pieces;
 };
 
 struct Shared {
@@ -90,7 +89,6 @@ struct Shared {
   int bad_pages[7];              // of the codes' stage, a bit for each page
   int status;
   uint32_t wait_limit;           // of every wait; 0: the CTA is aborted
-  int joins;
   uint32_t tmem;
   // the line (block-wide scan)
   long long scan[32];
@@ -284,6 +282,7 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
     mine.ctx = 0;
     if (base + lane < p.batch) mine = read_seq(p, base + lane, &sh.status);
   };
+  SplitUnit split_unit{0, 0, 0, 0, 0};  // the one whose first piece is this CTA's
   long long at = sh.start_at;  // where sequence b begins
   if (lo < hi) read_chunk();
   Seq s;
@@ -315,6 +314,7 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
     if (i >= kUnitSlots && !c.wait(&sh.unit_empty[slot], (i / kUnitSlots - 1) & 1)) return;
     if (pos >= hi) {
       if (lane == 0) {
+        p.split[cta] = split_unit;
         sh.unit[slot].end = 1;
         mbar_arrive(&sh.unit_full[slot]);
       }
@@ -335,13 +335,16 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
     const int last = p.causal ? min(len_k, vis0 + w.tokens - 1) : len_k;
     const int tiles = last > 0 ? (last - 1) / kTile + 1 : 0;
     w.slot = -1;
-    w.first = cta;
-    w.pieces = 1;
     int t0 = 0, t1 = tiles;
     if (x0 > 0 || x1 < len) {
-      w.first = owner(u0);
-      w.pieces = owner(u0 + len - 1) - w.first + 1;
       w.slot = 2 * cta + (x0 > 0 ? 0 : 1);
+      if (x0 == 0) {  // its other pieces are those of the next CTAs
+        split_unit.pieces = owner(u0 + len - 1) - cta + 1;
+        split_unit.q_row = w.q_row;
+        split_unit.tokens = w.tokens;
+        split_unit.head = head;
+        split_unit.bad = w.bad;
+      }
       auto tile_of = [&](long long x) {
         return (int)min((long long)tiles, max(0ll, (x - kUnitCost + kTile / 2) / kTile));
       };
@@ -501,7 +504,6 @@ __device__ __forceinline__ void tensor_role(const Ctx& c) {
       const bool next = j >= lag;
       const int ki = next ? item++ : 0;
       if (!arrived(vi)) return;
-      if (next && !arrived(ki)) return;
 #pragma unroll 1
       for (int s = 0; s < 2; ++s) {
         const int ns = s ? n1 : n0;
@@ -530,11 +532,17 @@ __device__ __forceinline__ void tensor_role(const Ctx& c) {
           if (j < lag && elect_one()) tc_commit(&sh.o_full[s]);
           __syncwarp();
         }
-        if (next && j - lag < ns) score(s, stage(ki));
+        // V's place is free behind its last product, while K's is being used
+        if ((split || s == 1) && elect_one()) tc_commit(&sh.kv_empty[stage(vi)]);
+        __syncwarp();
+        if (next && j - lag < ns) {
+          if (!arrived(ki)) return;
+          tc_fence_after();
+          score(s, stage(ki));
+        }
       }
-      if (elect_one()) {
-        tc_commit(&sh.kv_empty[stage(vi)]);
-        if (next) tc_commit(&sh.kv_empty[stage(ki)]);
+      if (next && elect_one()) {
+        tc_commit(&sh.kv_empty[stage(ki)]);
         if (j == lag) tc_commit(&sh.q_empty);
       }
       __syncwarp();
@@ -550,19 +558,38 @@ __device__ __forceinline__ uint32_t half2_as(uint32_t h) {  // exact: at most 6 
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
   return pack2<XQA_BF16>(f.x, f.y);
 }
-template <int kFmt, int kType>
-__device__ __forceinline__ void convert16(const uint8_t* page, int row, int group, uint32_t (&o)[8]) {
+template <int kFmt>
+struct Codes16 {
+  uint4 w;
+};
+template <>
+struct Codes16<XQA_KV_E2M1> {
+  uint2 w;
+  uint32_t s8;  // the group's scale
+};
+// Codes of dims 16 group .. 16 group + 15 of a tile's token `row`.
+template <int kFmt>
+__device__ __forceinline__ Codes16<kFmt> read16(const uint8_t* raw, int row, int group) {
+  Codes16<kFmt> c;
   if constexpr (kFmt == XQA_KV_E2M1) {
-    const uint2 w = lds64(page + row * (kHeadDim / 2) + 8 * group);
-    const uint32_t s8 = lds_u8(page + kCodeBytes4 + row * (kHeadDim / kGroup4) + group);
-    const uint32_t sc = e4m3x2_to_f16x2(s8 | s8 << 8);
-    e2m1x8_to_f16x2(w.x, o);
-    e2m1x8_to_f16x2(w.y, o + 4);
+    const uint8_t* page = raw + (row >> 4) * kSliceBytes4;
+    c.w = lds64(page + (row & 15) * (kHeadDim / 2) + 8 * group);
+    c.s8 = lds_u8(page + kCodeBytes4 + (row & 15) * (kHeadDim / kGroup4) + group);
+  } else {
+    c.w = lds128(raw + row * kHeadDim + 16 * group);
+  }
+  return c;
+}
+template <int kFmt, int kType>
+__device__ __forceinline__ void convert16(const Codes16<kFmt>& c, uint32_t (&o)[8]) {
+  if constexpr (kFmt == XQA_KV_E2M1) {
+    const uint32_t sc = e4m3x2_to_f16x2(c.s8 | c.s8 << 8);
+    e2m1x8_to_f16x2(c.w.x, o);
+    e2m1x8_to_f16x2(c.w.y, o + 4);
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = half2_as<kType>(hmul2(o[i], sc));
   } else {
-    const uint4 w = lds128(page + row * kHeadDim + 16 * group);
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    const uint32_t x[4] = {c.w.x, c.w.y, c.w.z, c.w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       o[2 * i] = half2_as<kType>(KvConv<kFmt>::k_lo(x[i]));
@@ -598,20 +625,22 @@ __device__ __forceinline__ void convert_role(const Ctx& c) {
       uint8_t* dst = c.kv(st) + half * kHalfBytes;
       const int bad = *(volatile int*)&sh.bad_pages[rs];
       const bool masked = is_v && (j + 1) * kTile > u.hidden;
+      // rows row0, row0 + 4 kConvertWarps, ...: a multiple of 8 apart, so that the swizzle is
+      // the same for all of a thread's rows
+      constexpr int kStep = 4 * kConvertWarps, kTurns = (kTile + kStep - 1) / kStep;
+      static_assert(kStep % 8 == 0, "swizzle");
+      const int row0 = 4 * warp + row_in4;
+      const uint32_t swz0 = ((2 * (group & 3)) ^ (row0 & 7)) * 16, swz1 = swz0 ^ 16;
       auto store = [&](int row, const uint32_t (&o)[8]) {
-        uint8_t* d = dst + row * 128;
-        *reinterpret_cast<uint4*>(d + ((2 * (group & 3)) ^ (row & 7)) * 16) =
-            make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(d + ((2 * (group & 3) + 1) ^ (row & 7)) * 16) =
-            make_uint4(o[4], o[5], o[6], o[7]);
+        *reinterpret_cast<uint4*>(dst + row * 128 + swz0) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + row * 128 + swz1) = make_uint4(o[4], o[5], o[6], o[7]);
       };
       if (masked || bad) {
         const int past = u.len_k - j * kTile, from = u.hidden - j * kTile;
 #pragma unroll 1
-        for (int r4 = warp; r4 < kTile / 4; r4 += kConvertWarps) {
-          const int row = r4 * 4 + row_in4;
+        for (int row = row0; row < kTile; row += kStep) {
           uint32_t o[8];
-          convert16<kFmt, kType>(raw + (row >> 4) * Raw<kFmt>::kSlice, row & 15, group, o);
+          convert16<kFmt, kType>(read16<kFmt>(raw, row, group), o);
           const bool none = bad >> (row >> 4) & 1;
           const bool zero = is_v && (none || row >= past);
 #pragma unroll
@@ -627,12 +656,16 @@ __device__ __forceinline__ void convert_role(const Ctx& c) {
         }
         if (found) *(volatile int*)&sh.not_finite[i % kUnitSlots] = 1;
       } else {
-#pragma unroll 2
-        for (int r4 = warp; r4 < kTile / 4; r4 += kConvertWarps) {
-          const int row = r4 * 4 + row_in4;
+        Codes16<kFmt> w[kTurns];  // every read of the tile before the first use
+#pragma unroll
+        for (int k = 0; k < kTurns; ++k)
+          if (row0 + k * kStep < kTile) w[k] = read16<kFmt>(raw, row0 + k * kStep, group);
+#pragma unroll
+        for (int k = 0; k < kTurns; ++k) {
+          if (row0 + k * kStep >= kTile) continue;
           uint32_t o[8];
-          convert16<kFmt, kType>(raw + (row >> 4) * Raw<kFmt>::kSlice, row & 15, group, o);
-          store(row, o);
+          convert16<kFmt, kType>(w[k], o);
+          store(row0 + k * kStep, o);
         }
       }
       fence_proxy_async_smem();  // before the tensor core reads the tile
@@ -797,10 +830,7 @@ __device__ __noinline__ float not_finite_value(const uint8_t* slice, long long t
   return (h & 0x7c00u) == 0x7c00u ? __half2float(__ushort_as_half((unsigned short)h)) : 0.f;
 }
 
-// ---- warps 8-11: normalise and write, or leave a piece and join ----
-template <int kType>
-__device__ __noinline__ void join_pieces(const Ctx& c, const Unit& u, float v_scale);
-
+// ---- warps 8-11: normalise and write, or leave a piece ----
 template <int kFmt, int kType>
 __device__ __forceinline__ void epilogue_role(const Ctx& c, float v_scale) {
   const ExtendParams& p = c.p;
@@ -905,13 +935,21 @@ __device__ __forceinline__ void epilogue_role(const Ctx& c, float v_scale) {
                                      not_finite_value<kFmt>(slice, stride, key % kBlockSize, 32 * q + k));
           }
         }
-        if (piece) {  // as it is: [32 chunks of 4 dims][128 rows]
-          float4* po = p.piece_o + (place * 32 + 8 * q) * kTile + row;
-          if (rp.valid) {
+        if (piece) {  // as it is, a row of 128 values after the other, in runs of 64 bytes
+          const int rows = min(p.tile_tokens, u.tokens - s * p.tile_tokens) * p.group;
+          float* po = p.piece_o + (place * kTile + (row & ~3)) * kHeadDim + 32 * q + 4 * (row & 3);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              po[k * kTile] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                          __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+          for (int e = 0; e < 2; ++e) {
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) w[k] = o[16 * e + k];
+            trade<1>(w);
+            trade<2>(w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if ((row & ~3) + k < rows)
+                *reinterpret_cast<uint4*>(po + k * kHeadDim + 16 * e) =
+                    make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
           }
         } else {
           uint32_t w[16];
@@ -936,83 +974,7 @@ __device__ __forceinline__ void epilogue_role(const Ctx& c, float v_scale) {
         p.lse[at * p.num_q_heads + h] =
             ml.y == 0.f ? -INFINITY : (ml.x + __log2f(ml.y)) * 0.6931471805599453f;
     }
-    if (piece) {
-      __threadfence();
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      if ((threadIdx.x & 127) == 0) {
-        const int old = atom_add_acq_rel_gpu(p.tickets + u.first, 1);
-        sh.joins = old == u.pieces - 1;
-        if (old == u.pieces - 1) p.tickets[u.first] = 0;  // for the next call
-      }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (*(volatile int*)&sh.joins) join_pieces<kType>(c, u, v_scale);
-    }
     c.free_unit(i);
-  }
-}
-
-// The pieces of a unit, by the epilogue warps of the CTA that wrote the last one.
-template <int kType>
-__device__ __noinline__ void join_pieces(const Ctx& c, const Unit& u, float v_scale) {
-  const ExtendParams& p = c.p;
-  __threadfence();
-  const float nan = __int_as_float(0x7fc00000);
-#pragma unroll 1
-  for (int s = 0; s < 2; ++s) {
-    const int tokens = min(p.tile_tokens, u.tokens - s * p.tile_tokens);
-    if (tokens <= 0) break;
-    const int rows = tokens * p.group;  // <= 128
-    // threads of a row: 128 / span, its dims shared out among them
-    const int span = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    const int row = threadIdx.x & (span - 1), chunks = span / 4;
-    const int c0 = (threadIdx.x & 127) / span * chunks;
-    if (row >= rows) continue;
-    const int t = row / p.group, g = row - t * p.group, h = u.head * p.group + g;
-    const long long at = (long long)u.q_row + s * p.tile_tokens + t;
-    // piece k is in slot 1 of the first CTA, slot 0 of the others
-    auto place = [&](int k) { return (size_t)(4 * (u.first + k) + (k == 0 ? 2 : 0) + s); };
-    float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < u.pieces; ++k) {
-      const float2 ml = __ldcg(p.piece_ml + place(k) * kTile + row);
-      if (ml.y != 0.f) top = fmaxf(top, ml.x);
-    }
-#pragma unroll 4
-    for (int k = 0; k < u.pieces; ++k) {
-      const float2 ml = __ldcg(p.piece_ml + place(k) * kTile + row);
-      // (a piece with keys keeps the least weight there is)
-      if (ml.y != 0.f) sum += fmaxf(ex2(ml.x - top), 0x1p-149f) * ml.y;
-    }
-    const float rl = u.bad ? nan : sum == 0.f ? 0.f : v_scale / sum;
-    uint16_t* out = p.out + at * p.out_row_stride + h * p.out_head_stride;
-#pragma unroll 1
-    for (int q = c0; q < c0 + chunks; q += 4) {  // 16 dims
-      float4 acc[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-      for (int k = 0; k < u.pieces; ++k) {
-        const float2 ml = __ldcg(p.piece_ml + place(k) * kTile + row);
-        if (ml.y == 0.f) continue;  // without keys: it has written no O
-        const float w = fmaxf(ex2(ml.x - top), 0x1p-149f);
-        const float4* po = p.piece_o + (place(k) * 32 + q) * kTile + row;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 v = __ldcg(po + (size_t)e * kTile);
-          acc[e].x += w * v.x;
-          acc[e].y += w * v.y;
-          acc[e].z += w * v.z;
-          acc[e].w += w * v.w;
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        reinterpret_cast<uint2*>(out)[q + e] = make_uint2(pack2<kType>(acc[e].x * rl, acc[e].y * rl),
-                                                          pack2<kType>(acc[e].z * rl, acc[e].w * rl));
-    }
-    if (p.lse && c0 == 0)
-      p.lse[at * p.num_q_heads + h] =
-          u.bad ? nan : sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.6931471805599453f;
   }
 }
 
@@ -1154,9 +1116,129 @@ __global__ void __launch_bounds__(kExtendThreads, 1)
   tc_fence_after();
   if (warp == 12) tmem_dealloc(sh.tmem, 512);
   if (threadIdx.x == 0) {
+    if (!works) p.split[blockIdx.x] = SplitUnit{0, 0, 0, 0, 0};
     if (sh.wait_limit == 0) record_status(&sh.status, XQA_ERR_DEVICE_TIMEOUT);
     p.status[blockIdx.x] = sh.status;
     if (blockIdx.x == 0) p.header[0] = gridDim.x;
+  }
+}
+
+// ---- the join of split units' pieces ----
+// A warp has a row, 4 dims a lane; the pieces' (m, l) are read a piece a lane. Up to
+// kWarpPieces pieces are one warp's work; of more, the block's warps take equal runs, each
+// with its own maximum, and join once more through shared memory.
+constexpr int kJoinBlocks = 4;  // for each CTA of the kernel before
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kWarpPieces = 8;
+
+struct Row {  // O, m, l of a row (O: this lane's 4 dims)
+  float4 o;
+  float m, l;
+};
+__device__ __forceinline__ void add_row(Row& a, const Row& b) {
+  if (b.l == 0.f) return;  // without keys: its O was not written
+  const float m = a.l == 0.f ? b.m : fmaxf(a.m, b.m);
+  // a piece with keys keeps the least weight there is: its infinities and NaN are the row's
+  const float wa = a.l == 0.f ? 0.f : fmaxf(ex2(a.m - m), 0x1p-149f), wb = fmaxf(ex2(b.m - m), 0x1p-149f);
+  a.o.x = (wa == 0.f ? 0.f : wa * a.o.x) + wb * b.o.x;
+  a.o.y = (wa == 0.f ? 0.f : wa * a.o.y) + wb * b.o.y;
+  a.o.z = (wa == 0.f ? 0.f : wa * a.o.z) + wb * b.o.z;
+  a.o.w = (wa == 0.f ? 0.f : wa * a.o.w) + wb * b.o.w;
+  a.l = (wa == 0.f ? 0.f : wa * a.l) + wb * b.l;
+  a.m = m;
+}
+
+template <int kType>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const ExtendParams p, int ctas) {
+  __shared__ int first[kMaxCtas + 1];  // work items before each CTA's split unit
+  __shared__ float4 part_o[kJoinWarps][32];
+  __shared__ float2 part_ml[kJoinWarps];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // an item: eight rows, a warp each, or a row of many pieces
+  auto items = [&](const SplitUnit& u) {
+    const int rows = u.tokens * p.group;
+    return u.pieces < 2 ? 0 : u.pieces <= kWarpPieces ? (rows + kJoinWarps - 1) / kJoinWarps : rows;
+  };
+  int total = 0;
+  for (int c0 = 0; c0 < ctas; c0 += kJoinThreads) {
+    const int c = c0 + tid;
+    int n = 0;
+    if (c < ctas) n = items(p.split[c]);
+    int incl = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(kAll, incl, off);
+      if (lane >= off) incl += x;
+    }
+    __shared__ int sums[kJoinWarps];
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int before = total;
+    for (int w = 0; w < kJoinWarps; ++w) {
+      if (w < warp) before += sums[w];
+      total += sums[w];
+    }
+    if (c < ctas) first[c] = before + incl - n;
+    __syncthreads();
+  }
+  if (tid == 0) first[ctas] = total;
+  __syncthreads();
+  const float vs = p.v_scale_ptr ? *p.v_scale_ptr : p.v_scale;
+  for (int item = blockIdx.x; item < total; item += gridDim.x) {
+    int lo = 0, hi = ctas - 1;  // the last unit that begins at or before the item
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (first[m] <= item) lo = m;
+      else hi = m - 1;
+    }
+    const SplitUnit u = p.split[lo];
+    const bool many = u.pieces > kWarpPieces;
+    const int at = item - first[lo], r = many ? at : at * kJoinWarps + warp;
+    const int rows = u.tokens * p.group;
+    const bool valid = r < rows;
+    const int t = min(r, rows - 1) / p.group, g = min(r, rows - 1) - t * p.group;
+    const int s = t >= p.tile_tokens;
+    const int row = (t - s * p.tile_tokens) * p.group + g;
+    // piece k is in slot 1 of the first CTA, slot 0 of the others
+    auto place = [&](int k) {
+      return ((size_t)(4 * (lo + k) + (k == 0 ? 2 : 0) + s)) * kTile + row;
+    };
+    Row sum{make_float4(0.f, 0.f, 0.f, 0.f), kNoRowMax, 0.f};
+    const int per = many ? (u.pieces + kJoinWarps - 1) / kJoinWarps : u.pieces;
+    const int k0 = many ? warp * per : 0, k1 = min(u.pieces, k0 + per);
+    for (int k = k0; k < k1; k += 8) {  // eight pieces' rows in flight
+      const float2 ml = lane < 8 && k + lane < k1 ? __ldcg(p.piece_ml + place(k + lane))
+                                                  : make_float2(kNoRowMax, 0.f);
+      float4 o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k + e < k1)
+          o[e] = __ldcg(reinterpret_cast<const float4*>(p.piece_o + place(k + e) * kHeadDim) + lane);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        add_row(sum, Row{o[e], __shfl_sync(kAll, ml.x, e), __shfl_sync(kAll, ml.y, e)});
+    }
+    if (many) {
+      __syncthreads();  // the item before is read
+      part_o[warp][lane] = sum.o;
+      if (lane == 0) part_ml[warp] = make_float2(sum.m, sum.l);
+      __syncthreads();
+      if (warp != 0) continue;
+      for (int w = 1; w < kJoinWarps; ++w) add_row(sum, Row{part_o[w][lane], part_ml[w].x, part_ml[w].y});
+    }
+    if (!valid) continue;
+    const float nan = __int_as_float(0x7fc00000);
+    const float rl = u.bad ? nan : sum.l == 0.f ? 0.f : vs / sum.l;
+    const long long q = (long long)u.q_row + t;
+    const int h = u.head * p.group + g;
+    reinterpret_cast<uint2*>(p.out + q * p.out_row_stride + h * p.out_head_stride)[lane] =
+        make_uint2(pack2<kType>(sum.o.x * rl, sum.o.y * rl), pack2<kType>(sum.o.z * rl, sum.o.w * rl));
+    if (p.lse && lane == 0)
+      p.lse[q * p.num_q_heads + h] =
+          u.bad ? nan : sum.l == 0.f ? -INFINITY : (sum.m + __log2f(sum.l)) * 0.6931471805599453f;
   }
 }
 
@@ -1187,17 +1269,26 @@ cudaError_t launch_extend(const CUtensorMap& tm_q, const CUtensorMap& tm_k, cons
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const bool f16 = dtype == XQA_F16;
+  cudaError_t e;
   switch (p.kv_dtype) {
     case XQA_KV_E5M2:
-      return f16 ? launch<XQA_KV_E5M2, XQA_F16>(tm_q, tm_k, tm_v, p, cfg)
-                 : launch<XQA_KV_E5M2, XQA_BF16>(tm_q, tm_k, tm_v, p, cfg);
+      e = f16 ? launch<XQA_KV_E5M2, XQA_F16>(tm_q, tm_k, tm_v, p, cfg)
+              : launch<XQA_KV_E5M2, XQA_BF16>(tm_q, tm_k, tm_v, p, cfg);
+      break;
     case XQA_KV_E4M3:
-      return f16 ? launch<XQA_KV_E4M3, XQA_F16>(tm_q, tm_k, tm_v, p, cfg)
-                 : launch<XQA_KV_E4M3, XQA_BF16>(tm_q, tm_k, tm_v, p, cfg);
+      e = f16 ? launch<XQA_KV_E4M3, XQA_F16>(tm_q, tm_k, tm_v, p, cfg)
+              : launch<XQA_KV_E4M3, XQA_BF16>(tm_q, tm_k, tm_v, p, cfg);
+      break;
     default:
-      return f16 ? launch<XQA_KV_E2M1, XQA_F16>(tm_q, tm_k, tm_v, p, cfg)
-                 : launch<XQA_KV_E2M1, XQA_BF16>(tm_q, tm_k, tm_v, p, cfg);
+      e = f16 ? launch<XQA_KV_E2M1, XQA_F16>(tm_q, tm_k, tm_v, p, cfg)
+              : launch<XQA_KV_E2M1, XQA_BF16>(tm_q, tm_k, tm_v, p, cfg);
   }
+  if (e != cudaSuccess || ctas == 1) return e;  // (one CTA has nothing to share)
+  cfg.gridDim = dim3((unsigned)(ctas * kJoinBlocks));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  return f16 ? cudaLaunchKernelEx(&cfg, join_kernel<XQA_F16>, p, ctas)
+             : cudaLaunchKernelEx(&cfg, join_kernel<XQA_BF16>, p, ctas);
 }
 
 cudaError_t set_extend_attributes() {

@@ -445,7 +445,7 @@ struct ExtendResolved {
   Side q, out;
   int group, ctas;
   float sm_scale;
-  size_t bytes;
+  size_t pieces_off, bytes;
 };
 
 xqa_status_t resolve_extend(const xqa_extend_shape_t* s, ExtendResolved* r) {
@@ -484,7 +484,8 @@ xqa_status_t resolve_extend(const xqa_extend_shape_t* s, ExtendResolved* r) {
   const long long line = units * (128 + (long long)s->max_blocks_per_seq * kBlockSize);
   if (r->ctas > line / xqa::kExtendMinShare)
     r->ctas = line < xqa::kExtendMinShare ? 1 : (int)(line / xqa::kExtendMinShare);
-  r->bytes = kPrefillWorkspaceBytes + (size_t)r->ctas * 2 * kPieceFloats * sizeof(float);
+  r->pieces_off = (kPrefillWorkspaceBytes + (size_t)r->ctas * sizeof(xqa::SplitUnit) + 255) & ~(size_t)255;
+  r->bytes = r->pieces_off + (size_t)r->ctas * 2 * kPieceFloats * sizeof(float);
   return XQA_OK;
 }
 
@@ -826,10 +827,10 @@ xqa_status_t xqa_extend(const void* q, const uint8_t* k_cache, const uint8_t* v_
   p.out = reinterpret_cast<uint16_t*>(out);
   p.lse = lse;
   p.header = ws_i32(workspace);
-  p.tickets = reinterpret_cast<int32_t*>(base + lay.ticket_off);
   p.status = reinterpret_cast<int32_t*>(base + lay.status_off);
-  p.piece_o = reinterpret_cast<float4*>(base + kPrefillWorkspaceBytes);
-  p.piece_ml = reinterpret_cast<float2*>(base + kPrefillWorkspaceBytes +
+  p.split = reinterpret_cast<xqa::SplitUnit*>(base + kPrefillWorkspaceBytes);
+  p.piece_o = reinterpret_cast<float*>(base + r.pieces_off);
+  p.piece_ml = reinterpret_cast<float2*>(base + r.pieces_off +
                                          (size_t)r.ctas * 2 * 256 * kHeadDim * sizeof(float));
   p.batch = shape->batch;
   p.num_q_heads = shape->num_q_heads;

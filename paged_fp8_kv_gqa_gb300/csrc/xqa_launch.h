@@ -94,6 +94,11 @@ struct PrefillParams {
 // CTA takes; fewer CTAs work on shorter lines.
 constexpr int kExtendMinShare = 640;
 
+// A unit of tokens whose keys several CTAs share; pieces < 2: none.
+struct SplitUnit {
+  int pieces, q_row, tokens, head, bad;
+};
+
 struct ExtendParams {
   const int32_t* cu_q;  // [batch + 1]
   const int32_t* context_lens;
@@ -103,9 +108,9 @@ struct ExtendParams {
   uint16_t* out;
   float* lse;         // optional [total_q, Hq]
   int32_t* header;    // workspace header (CTAs launched)
-  int32_t* tickets;   // pieces written, by the CTA of a unit's first: zero between calls
   int32_t* status;    // [kMaxCtas]
-  float4* piece_o;    // [CTAs][2][2 row tiles][32 chunks of 4 dims][128 rows]
+  SplitUnit* split;   // [CTAs] the split unit that begins in the CTA's share
+  float* piece_o;     // [CTAs][2 units][2 row tiles][128 rows][128]
   float2* piece_ml;   // [CTAs][2][2][128]
   int batch, num_q_heads, num_kv_heads, group, total_q, causal;
   int max_blocks_per_seq, num_blocks, kv_dtype, kv_layout;
