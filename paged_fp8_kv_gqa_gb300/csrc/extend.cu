@@ -24,7 +24,7 @@
 // epilogue.
 //
 // Warps: 0-3 and 4-7 softmax of chain 0 and 1 (a thread owns a row), 8-11 epilogue, 12
-// tensor core, 13 units and copies, 14-19 codes to 16-bit values. TMEM: S0, S1 (P over
+// tensor core, 13 units and loads, 14-19 codes to 16-bit values. TMEM: S0, S1 (P over
 // them), O0, O1: 4 x 128 columns.
 //
 // Hidden values do not leak: see prompt attention; here rows past the sequence and values
@@ -74,6 +74,11 @@ struct Unit {
   int slot;      // place of this piece's (O, m, l); -1: the unit is one piece
 };
 
+// A sequence's rows and tokens.
+struct Seq {
+  int q0, n, ctx;  // ctx: -1 if the length is invalid
+};
+
 struct Shared {
   uint64_t raw_full[7], raw_empty[7];
   uint64_t kv_full[kKvStages], kv_empty[kKvStages];
@@ -91,9 +96,11 @@ struct Shared {
   uint32_t wait_limit;           // of every wait; 0: the CTA is aborted
   uint32_t tmem;
   // the line (block-wide scan)
-  long long scan[32];
-  long long total, start_at;     // length of the line; where the first sequence begins
-  int start_seq, ctas;           // ctas: that share the line
+  long long scan[kExtendThreads / 32][2];
+  long long share, extra;        // of a CTA on the line (one more for the first `extra` CTAs)
+  long long start_at;            // where the CTA's first sequence begins
+  Seq start;
+  int start_seq;
 };
 
 constexpr int kSmemTiles = (2 + kKvStages) * kTileBytes;
@@ -107,9 +114,6 @@ static_assert(kExtendSmem <= 227 * 1024, "shared memory budget");
 // kUnitCost + base + min(step (i + 1), rows) long, the keys that its last token sees and a
 // constant for its start and end (in keys).
 constexpr int kUnitCost = 128;
-struct Seq {
-  int q0, n, ctx;  // ctx: -1 if the length is invalid
-};
 struct Cost {
   int np;
   long long base;
@@ -149,25 +153,38 @@ __device__ __forceinline__ Cost seq_cost(const ExtendParams& p, const Seq& s) {
   return c;
 }
 
-// Block-wide exclusive scan; every thread calls it.
-__device__ __forceinline__ long long scan_all(long long v, Shared& sh, long long& sum) {
+// Quotient of positions of the line (64-bit division is a long chain of instructions).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
+// Block-wide exclusive scan of a sequence's length on the line, and the sums of it and of the
+// rows; every thread calls it.
+__device__ __forceinline__ long long scan_all(long long v, int rows, Shared& sh, long long& sum,
+                                              long long& sum_rows) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long incl = v;
+  long long incl = v, all_rows = rows;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const long long x = __shfl_up_sync(kAll, incl, off);
     if (lane >= off) incl += x;
+    all_rows += __shfl_xor_sync(kAll, all_rows, off);
   }
-  if (lane == 31) sh.scan[warp] = incl;
+  if (lane == 31) sh.scan[warp][0] = incl, sh.scan[warp][1] = all_rows;
   __syncthreads();
-  long long before = 0;
-  sum = 0;
-  for (int w = 0; w < kExtendThreads / 32; ++w) {
-    if (w == warp) before = sum;
-    sum += sh.scan[w];
+  long long w = lane < kExtendThreads / 32 ? sh.scan[lane][0] : 0;
+  long long r = lane < kExtendThreads / 32 ? sh.scan[lane][1] : 0;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long x = __shfl_up_sync(kAll, w, off);
+    if (lane >= off) w += x;
+    r += __shfl_xor_sync(kAll, r, off);
   }
+  sum = __shfl_sync(kAll, w, 31);
+  sum_rows = r;
+  const long long before = __shfl_sync(kAll, w, max(warp - 1, 0));
   __syncthreads();
-  return before + incl - v;
+  return (warp > 0 ? before : 0) + incl - v;
 }
 
 struct Ctx {
@@ -249,34 +266,83 @@ struct PageIds {
   }
 };
 
-__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+// Four whole rows of a matrix (a box of one row), one behind the other.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int r0,
+                                            int r1, int r2, int r3) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_addr(dst)),
-      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(0), "r"(r0), "r"(r1), "r"(r2),
+      "r"(r3)
       : "memory");
+}
+
+// Codes of a unit's tiles into the ring; item: the ring's number of its first tile.
+template <int kFmt>
+__device__ __forceinline__ bool load_tiles(const Ctx& c, const Unit& w, const CUtensorMap* tm_k,
+                                           const CUtensorMap* tm_v, int item, int& issued) {
+  const ExtendParams& p = c.p;
+  Shared& sh = c.sh;
+  constexpr int kStages = Raw<kFmt>::kStages, kSlice = Raw<kFmt>::kSlice;
+  const int lane = threadIdx.x & 31;
+  const TileOrder order(w);
+  const int pages = (w.len_k + kBlockSize - 1) / kBlockSize;
+  const bool nhd = kFmt != XQA_KV_E2M1 && p.kv_layout == XQA_LAYOUT_NHD;
+  PageIds k_ids, v_ids;
+  k_ids.start(p.block_tables + (size_t)w.seq * p.max_blocks_per_seq + w.page0, pages, order.n - 1);
+  v_ids = k_ids;
+  for (int t = 0; t < 2 * order.n; ++t) {
+    bool is_v;
+    const int j = order.at(t, is_v);
+    const int it = item + t, st = it % kStages;
+    const int id = is_v ? v_ids.of(j) : k_ids.of(j);  // page `lane & 7` of the tile
+    const bool want = lane < kTilePages && j * kTilePages + lane < pages;
+    const bool good = want && (uint32_t)id < (uint32_t)p.num_blocks;
+    const uint32_t some = __ballot_sync(kAll, good), none = __ballot_sync(kAll, want && !good);
+    if (it >= kStages && !c.wait(&sh.raw_empty[st], (it / kStages - 1) & 1)) return false;
+    issued = it + 1;
+    if (lane == 0) {
+      sh.bad_pages[st] = none;
+      if (none) record_status(&sh.status, XQA_ERR_BAD_BLOCK_ID);
+      mbar_arrive_expect_tx(&sh.raw_full[st], (nhd ? __popc(some) : kTilePages) * kSlice);
+    }
+    __syncwarp();
+    uint8_t* dst = c.raw + st * Raw<kFmt>::kBytes + lane * kSlice;
+    const CUtensorMap* tm = is_v ? tm_v : tm_k;
+    if (nhd) {
+      if (good) tma_load_kv(dst, tm, &sh.raw_full[st], 0, w.head, id * kBlockSize);
+    } else {
+      // slices are rows of one matrix: four at a time. In place of pages that are not there or
+      // not good, the pool's first: their tokens are hidden or replaced
+      const int row = good ? id * p.num_kv_heads + w.head : w.head;
+      const int r1 = __shfl_down_sync(kAll, row, 1), r2 = __shfl_down_sync(kAll, row, 2);
+      const int r3 = __shfl_down_sync(kAll, row, 3);
+      if (lane == 0 || lane == 4) tma_gather4(dst, tm, &sh.raw_full[st], row, r1, r2, r3);
+    }
+    __syncwarp();
+  }
+  return true;
 }
 
 // ---- warp 13: the units of this CTA, their queries and codes ----
 template <int kFmt>
 __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
-                                          const CUtensorMap* tm_k, const CUtensorMap* tm_v, bool bad_scale,
-                                          int& raw_issued, int& q_issued) {
+                                          const CUtensorMap* tm_k, const CUtensorMap* tm_v,
+                                          bool bad_scale, int& raw_issued, int& q_issued) {
   const ExtendParams& p = c.p;
   Shared& sh = c.sh;
-  constexpr int kStages = Raw<kFmt>::kStages;
   const int lane = threadIdx.x & 31;
   const int per = 2 * p.tile_tokens;
-  const long long share = sh.total / sh.ctas, extra = sh.total % sh.ctas;
+  const long long share = sh.share, extra = sh.extra;
   const int cta = blockIdx.x;
   const long long lo = cta * share + min((long long)cta, extra);
   const long long hi = lo + share + (cta < extra ? 1 : 0);
   auto owner = [&](long long x) {  // CTA of a position of the line
     const long long large = extra * (share + 1);
-    return (int)(x < large ? x / (share + 1) : extra + (x - large) / share);
+    return (int)(x < large ? quotient(x, share + 1) : extra + quotient(x - large, share));
   };
-  int base = sh.start_seq & ~31, b = sh.start_seq;  // sequences base .. base + 31, one a lane
-  Seq mine;
+  int base = -1, b = sh.start_seq, item = 0;  // sequences base .. base + 31, one a lane
+  Seq mine{0, 0, 0};
   auto read_chunk = [&]() {
     mine.q0 = mine.n = 0;
     mine.ctx = 0;
@@ -284,21 +350,13 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
   };
   SplitUnit split_unit{0, 0, 0, 0, 0};  // the one whose first piece is this CTA's
   long long at = sh.start_at;  // where sequence b begins
-  if (lo < hi) read_chunk();
-  Seq s;
-  Cost cost;
-  auto pick = [&]() {
-    s.q0 = __shfl_sync(kAll, mine.q0, b - base);
-    s.n = __shfl_sync(kAll, mine.n, b - base);
-    s.ctx = __shfl_sync(kAll, mine.ctx, b - base);
-    cost = seq_cost(p, s);
-  };
+  Seq s = sh.start;
+  Cost cost = seq_cost(p, s);
   int head = 0, pair = 0;
   long long pos = lo;
-  if (lo < hi) {  // the unit that holds lo
-    pick();
+  {  // the unit that holds lo
     const long long one = cost.head();
-    head = (int)((lo - at) / one);
+    head = (int)quotient(lo - at, one);
     const long long rem = lo - at - head * one;
     int a = 0, z = cost.np - 1;  // the last unit that begins at or before rem
     while (a < z) {
@@ -375,13 +433,7 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
       }
       mbar_arrive(&sh.unit_full[slot]);
     }
-    const TileOrder order(w);
-    if (order.n > 0) {
-      const int32_t* table = p.block_tables + (size_t)b * p.max_blocks_per_seq + w.page0;
-      const int pages = (w.len_k + kBlockSize - 1) / kBlockSize;
-      PageIds k_ids, v_ids;
-      k_ids.start(table, pages, order.n - 1);
-      v_ids.start(table, pages, order.n - 1);
+    if (max(w.n[0], w.n[1]) > 0) {
       if (q_issued > 0 && !c.wait(&sh.q_empty, (q_issued - 1) & 1)) return;
       if (lane == 0) {
         const int half = p.group * p.tile_tokens * 128;  // bytes of a half tile
@@ -396,36 +448,10 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
                         w.head, w.q_row + r * p.tile_tokens);
         }
       }
+      __syncwarp();
       ++q_issued;
-      for (int t = 0; t < 2 * order.n; ++t) {
-        bool is_v;
-        const int j = order.at(t, is_v);
-        const int st = raw_issued % kStages;
-        const int id = is_v ? v_ids.of(j) : k_ids.of(j);
-        if (raw_issued >= kStages && !c.wait(&sh.raw_empty[st], (raw_issued / kStages - 1) & 1))
-          return;
-        const bool want = lane < kTilePages && j * kTilePages + lane < pages;
-        const bool good = want && (uint32_t)id < (uint32_t)p.num_blocks;
-        const uint32_t n_good = __popc(__ballot_sync(kAll, good));
-        const uint32_t n_bad = __ballot_sync(kAll, want && !good);
-        if (lane == 0) {
-          sh.bad_pages[st] = n_bad;
-          if (n_bad) record_status(&sh.status, XQA_ERR_BAD_BLOCK_ID);
-          mbar_arrive_expect_tx(&sh.raw_full[st], n_good * Raw<kFmt>::kSlice);
-        }
-        __syncwarp();
-        if (good) {
-          uint8_t* dst = c.raw + st * Raw<kFmt>::kBytes + lane * Raw<kFmt>::kSlice;
-          if (kFmt != XQA_KV_E2M1 && p.kv_layout == XQA_LAYOUT_NHD)
-            tma_load_kv(dst, is_v ? tm_v : tm_k, &sh.raw_full[st], 0, w.head, id * kBlockSize);
-          else
-            bulk_copy(dst, (is_v ? p.v_pool : p.k_pool) +
-                               ((size_t)id * p.num_kv_heads + w.head) * Raw<kFmt>::kSlice,
-                      Raw<kFmt>::kSlice, &sh.raw_full[st]);
-        }
-        __syncwarp();
-        ++raw_issued;
-      }
+      if (!load_tiles<kFmt>(c, w, tm_k, tm_v, item, raw_issued)) return;
+      item += 2 * max(w.n[0], w.n[1]);
     }
     // on to the next unit
     pos = u0 + len;
@@ -434,6 +460,10 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
     at = pos;
     if (++head < p.num_kv_heads || pos >= hi) continue;
     head = 0;
+    if (base < 0) {
+      base = b & ~31;
+      read_chunk();
+    }
     for (;;) {  // the next sequence with tokens (there is one: the line goes on)
       const uint32_t some = __ballot_sync(kAll, mine.n > 0 && base + lane > b);
       if (some) {
@@ -445,7 +475,10 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
       b = base - 1;
       read_chunk();
     }
-    pick();
+    s.q0 = __shfl_sync(kAll, mine.q0, b - base);
+    s.n = __shfl_sync(kAll, mine.n, b - base);
+    s.ctx = __shfl_sync(kAll, mine.ctx, b - base);
+    cost = seq_cost(p, s);
   }
 }
 
@@ -1016,16 +1049,12 @@ __global__ void __launch_bounds__(kExtendThreads, 1)
     mbar_init(&sh.drain, 1);
     sh.wait_limit = kWaitLimit;
     sh.status = aligned ? XQA_OK : XQA_ERR_LAUNCH;
-    sh.start_seq = 0;
-    sh.start_at = 0;
     fence_mbar_init();
   }
   if (warp == 13 && (threadIdx.x & 31) == 0) {
     prefetch_tensormap(&tm_q);
-    if (kFmt != XQA_KV_E2M1 && p.kv_layout == XQA_LAYOUT_NHD) {
-      prefetch_tensormap(&tm_k);
-      prefetch_tensormap(&tm_v);
-    }
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
   }
   if (warp == 12) tmem_alloc(&sh.tmem, 512);
   tc_fence_before();
@@ -1033,45 +1062,50 @@ __global__ void __launch_bounds__(kExtendThreads, 1)
   tc_fence_after();
   griddep_wait();  // inputs are read, and outputs written, after the kernels before this one
   // the line's length, and the sequence that holds this CTA's first position
-  long long total = 0, rows = 0;
-  int ctas = 1;
+  const float ks = p.k_scale_ptr ? *p.k_scale_ptr : p.k_scale;
+  const float vs = p.v_scale_ptr ? *p.v_scale_ptr : p.v_scale;
+  long long total = 0, rows = 0, mine = 0, excl = 0;
+  Seq s{0, 0, 0};
   for (int b0 = 0; b0 < p.batch; b0 += kExtendThreads) {
     const int b = b0 + threadIdx.x;
-    Seq s{0, 0, 0};
+    s = Seq{0, 0, 0};
     if (b < p.batch) s = read_seq(p, b, &sh.status);
-    long long sum;
-    scan_all(seq_cost(p, s).head() * p.num_kv_heads, sh, sum);
+    mine = seq_cost(p, s).head() * p.num_kv_heads;
+    long long sum, sum_rows;
+    excl = total + scan_all(mine, s.n, sh, sum, sum_rows);
     total += sum;
-    scan_all(s.n, sh, sum);
-    rows += sum;
+    rows += sum_rows;
   }
   // sequences that overlap (offsets that descend) could have any number of units
   if (rows > p.total_q) total = 0;
+  int ctas = 1;
   if (total > 0) ctas = (int)min((long long)gridDim.x, max(1ll, total / kExtendMinShare));
-  const long long share = total / ctas, extra = total % ctas;
+  const long long share = quotient(total, ctas), extra = total - share * ctas;
   const long long lo = blockIdx.x * share + min((long long)blockIdx.x, extra);
   const bool works = total > 0 && blockIdx.x < ctas;
-  if (works) {
+  if (p.batch > kExtendThreads && works) {  // once more: a thread keeps one sequence
     long long before = 0;
     for (int b0 = 0; b0 < p.batch; b0 += kExtendThreads) {
       const int b = b0 + threadIdx.x;
-      Seq s{0, 0, 0};
+      s = Seq{0, 0, 0};
       if (b < p.batch) s = read_seq(p, b, &sh.status);
-      const long long mine = seq_cost(p, s).head() * p.num_kv_heads;
-      long long sum;
-      const long long excl = before + scan_all(mine, sh, sum);
-      if (excl <= lo && lo < excl + mine) sh.start_seq = b, sh.start_at = excl;
+      mine = seq_cost(p, s).head() * p.num_kv_heads;
+      long long sum, sum_rows;
+      excl = before + scan_all(mine, s.n, sh, sum, sum_rows);
       before += sum;
+      if (excl <= lo && lo < excl + mine) sh.start_seq = b, sh.start_at = excl, sh.start = s;
       if (lo < before) break;
     }
+  } else if (excl <= lo && lo < excl + mine) {
+    sh.start_seq = threadIdx.x;
+    sh.start_at = excl;
+    sh.start = s;
   }
   if (threadIdx.x == 0) {
-    sh.total = total;
-    sh.ctas = ctas;
+    sh.share = share;
+    sh.extra = extra;
   }
   __syncthreads();
-  const float ks = p.k_scale_ptr ? *p.k_scale_ptr : p.k_scale;
-  const float vs = p.v_scale_ptr ? *p.v_scale_ptr : p.v_scale;
   const float sc = (float)(p.qk_scale_base * (double)ks);
   const bool bad_scale = !(sc > 0.f && sc < INFINITY);
   if (bad_scale && works && threadIdx.x == 0) record_status(&sh.status, XQA_ERR_VALUE);

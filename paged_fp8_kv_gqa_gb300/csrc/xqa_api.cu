@@ -489,16 +489,31 @@ xqa_status_t resolve_extend(const xqa_extend_shape_t* s, ExtendResolved* r) {
   return XQA_OK;
 }
 
-// Token-major pools: x = D, y = kv head, z = token row; a box is a page's 16 rows of one head.
-xqa_status_t encode_nhd_map(CUtensorMap* map, const uint8_t* pool, int hkv, int nb) {
+// A pool without swizzle. Token-major: x = D, y = kv head, z = token row; a box is a page's 16
+// rows of one head. Else a row is a (page, kv head) slice, in elements of 8 bytes (a box has
+// at most 256), for gathers of four rows.
+xqa_status_t encode_plain_map(CUtensorMap* map, const uint8_t* pool, int hkv, int nb, int kv_dtype,
+                              int kv_layout) {
   cuuint32_t estr[3] = {1, 1, 1};
-  cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)hkv, (cuuint64_t)nb * kBlockSize};
-  cuuint64_t strides[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)hkv * kHeadDim};
-  cuuint32_t box[3] = {(cuuint32_t)kHeadDim, 1, (cuuint32_t)kBlockSize};
-  const CUresult res = g_encode.load(std::memory_order_acquire)(
-      map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(pool), dims, strides, box, estr,
-      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult res;
+  if (kv_layout == XQA_LAYOUT_NHD) {
+    cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)hkv, (cuuint64_t)nb * kBlockSize};
+    cuuint64_t strides[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)hkv * kHeadDim};
+    cuuint32_t box[3] = {(cuuint32_t)kHeadDim, 1, (cuuint32_t)kBlockSize};
+    res = g_encode.load(std::memory_order_acquire)(
+        map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(pool), dims, strides, box, estr,
+        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  } else {
+    const int bytes = kv_dtype == XQA_KV_E2M1 ? xqa::kSliceBytes4 : xqa::kPageBytes;
+    cuuint64_t dims[2] = {(cuuint64_t)bytes / 8, (cuuint64_t)nb * hkv};
+    cuuint64_t strides[1] = {(cuuint64_t)bytes};
+    cuuint32_t box[2] = {(cuuint32_t)bytes / 8, 1};
+    res = g_encode.load(std::memory_order_acquire)(
+        map, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, const_cast<uint8_t*>(pool), dims, strides, box, estr,
+        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  }
   return res == CUDA_SUCCESS ? XQA_OK : XQA_ERR_LAUNCH;
 }
 
@@ -808,13 +823,14 @@ xqa_status_t xqa_extend(const void* q, const uint8_t* k_cache, const uint8_t* v_
     return XQA_ERR_ALIGN;
   if ((st = ensure_device_setup()) != XQA_OK) return st;
   const int tokens = 128 / r.group;
-  alignas(64) CUtensorMap tm_q, tm_k = {}, tm_v = {};
+  alignas(64) CUtensorMap tm_q, tm_k, tm_v;
   if ((st = encode_rows_map(&tm_q, q, r.q, shape->total_q, shape->num_kv_heads, r.group, tokens,
                             shape->dtype, true)) != XQA_OK)
     return st;
-  if (shape->kv_layout == XQA_LAYOUT_NHD &&
-      ((st = encode_nhd_map(&tm_k, k_cache, shape->num_kv_heads, shape->num_blocks)) != XQA_OK ||
-       (st = encode_nhd_map(&tm_v, v_cache, shape->num_kv_heads, shape->num_blocks)) != XQA_OK))
+  if ((st = encode_plain_map(&tm_k, k_cache, shape->num_kv_heads, shape->num_blocks, shape->kv_dtype,
+                             shape->kv_layout)) != XQA_OK ||
+      (st = encode_plain_map(&tm_v, v_cache, shape->num_kv_heads, shape->num_blocks, shape->kv_dtype,
+                             shape->kv_layout)) != XQA_OK)
     return st;
   const xqa::WsLayout lay = xqa::ws_layout(0, 0);
   uint8_t* base = reinterpret_cast<uint8_t*>(workspace);
