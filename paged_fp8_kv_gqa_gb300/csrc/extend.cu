@@ -110,19 +110,22 @@ static_assert(sizeof(Shared) <= 1024, "shared state");
 static_assert(kExtendSmem <= 227 * 1024, "shared memory budget");
 
 // ---- the line of work ----
-// A sequence of n tokens: np = ceil(n / 2T) units for each kv head; unit i is
-// kUnitCost + base + min(step (i + 1), rows) long, the keys that its last token sees and a
-// constant for its start and end (in keys).
-constexpr int kUnitCost = 128;
+// A sequence of n tokens: np = ceil(n / 2T) units for each kv head; unit i sees base +
+// min(step (i + 1), rows) keys at most, and is kKeyCost long for each of them, or kKeyCostOne if
+// it fills one row tile only (a 128-key tile takes 1.6 and 0.9 us), and kUnitCost more for its
+// start and end.
+constexpr int kKeyCost = 16, kKeyCostOne = 10, kUnitCost = 256 * kKeyCost;
 struct Cost {
   int np;
   long long base;
   int step, rows;
-  __device__ __forceinline__ long long upto(int i) const {  // cost of the units before i
-    return i * (kUnitCost + base) + (long long)step * ((long long)i * (i + 1) / 2);
+  int last_key;  // cost of a key in the last unit
+  __device__ __forceinline__ long long upto(int i) const {  // cost of the units before i < np
+    return i * (kUnitCost + kKeyCost * base) + kKeyCost * (step * ((long long)i * (i + 1) / 2));
   }
+  __device__ __forceinline__ int key(int i) const { return i == np - 1 ? last_key : kKeyCost; }
   __device__ __forceinline__ long long unit(int i) const {
-    return kUnitCost + base + min((long long)step * (i + 1), (long long)rows);
+    return kUnitCost + key(i) * (base + min((long long)step * (i + 1), (long long)rows));
   }
   __device__ __forceinline__ long long head() const { return np == 0 ? 0 : upto(np - 1) + unit(np - 1); }
 };
@@ -150,6 +153,7 @@ __device__ __forceinline__ Cost seq_cost(const ExtendParams& p, const Seq& s) {
   c.base = causal ? max(0, s.ctx - s.n) : max(0, s.ctx);
   c.step = causal ? per : 0;
   c.rows = causal ? s.n : 0;
+  c.last_key = s.n - (c.np - 1) * per <= p.tile_tokens ? kKeyCostOne : kKeyCost;
   return c;
 }
 
@@ -277,10 +281,13 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+constexpr int kTilesBeforeQ = 3;
+static_assert(kTilesBeforeQ < kKvStages + kRawBytes / (kTile * kHeadDim), "room of the rings");
 // Codes of a unit's tiles into the ring; item: the ring's number of its first tile.
 template <int kFmt>
-__device__ __forceinline__ bool load_tiles(const Ctx& c, const Unit& w, const CUtensorMap* tm_k,
-                                           const CUtensorMap* tm_v, int item, int& issued) {
+__device__ __forceinline__ bool load_tiles(const Ctx& c, const Unit& w, const CUtensorMap* tm_q,
+                                           const CUtensorMap* tm_k, const CUtensorMap* tm_v, int item,
+                                           int& issued, int& q_issued) {
   const ExtendParams& p = c.p;
   Shared& sh = c.sh;
   constexpr int kStages = Raw<kFmt>::kStages, kSlice = Raw<kFmt>::kSlice;
@@ -291,7 +298,32 @@ __device__ __forceinline__ bool load_tiles(const Ctx& c, const Unit& w, const CU
   PageIds k_ids, v_ids;
   k_ids.start(p.block_tables + (size_t)w.seq * p.max_blocks_per_seq + w.page0, pages, order.n - 1);
   v_ids = k_ids;
+  const int q_tiles = w.split ? 1 : 2;
+  if (lane < 2 * q_tiles && w.n[lane >> 1] > 0)  // into L2 while the unit before still uses Q's place
+    tma_prefetch_4d(tm_q, 64 * (lane & 1), 0, w.head, w.q_row + (lane >> 1) * p.tile_tokens);
   for (int t = 0; t < 2 * order.n; ++t) {
+    // Q behind the first tiles, which so are on their way while the unit before ends (Q first:
+    // 10 to 24 us more a unit). The rings have room for them and more: no tile behind waits
+    // for one that waits for Q.
+    if (t == min(kTilesBeforeQ, 2 * order.n - 1)) {
+      if (q_issued > 0 && !c.wait(&sh.q_empty, (q_issued - 1) & 1)) return false;
+      if (lane == 0) {
+        const int half = p.group * p.tile_tokens * 128;  // bytes of a half tile
+        int row_tiles = 0;
+        for (int r = 0; r < q_tiles; ++r) row_tiles += w.n[r] > 0;
+        mbar_arrive_expect_tx(&sh.q_full, 2 * half * row_tiles);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (r >= q_tiles || w.n[r] == 0) continue;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            tma_load_4d(c.tiles + r * kTileBytes + h * kHalfBytes, tm_q, &sh.q_full, 64 * h, 0,
+                        w.head, w.q_row + r * p.tile_tokens);
+        }
+      }
+      __syncwarp();
+      ++q_issued;
+    }
     bool is_v;
     const int j = order.at(t, is_v);
     const int it = item + t, st = it % kStages;
@@ -403,8 +435,10 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
         split_unit.head = head;
         split_unit.bad = w.bad;
       }
+      const int tile_cost = kTile * cost.key(pair);
       auto tile_of = [&](long long x) {
-        return (int)min((long long)tiles, max(0ll, (x - kUnitCost + kTile / 2) / kTile));
+        return (int)min((long long)tiles,
+                        quotient(max(0ll, x - kUnitCost + tile_cost / 2), tile_cost));
       };
       if (x0 > 0) t0 = tile_of(x0);
       if (x1 < len) t1 = tile_of(x1);
@@ -412,13 +446,11 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
     w.page0 = t0 * kTilePages;
     w.len_k = max(0, min(len_k, t1 * kTile) - t0 * kTile);
     w.vis0 = p.causal ? vis0 - t0 * kTile : w.len_k;
-    int used = 0;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int toks = min(p.tile_tokens, w.tokens - r * p.tile_tokens);
       const int seen = p.causal ? min(w.len_k, w.vis0 + r * p.tile_tokens + toks - 1) : w.len_k;
       w.n[r] = toks > 0 && seen > 0 ? (seen - 1) / kTile + 1 : 0;
-      used += w.n[r] > 0;
     }
     w.split = w.tokens <= p.tile_tokens && w.n[0] >= 2;
     if (w.split) w.n[1] = w.n[0];
@@ -434,23 +466,7 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
       mbar_arrive(&sh.unit_full[slot]);
     }
     if (max(w.n[0], w.n[1]) > 0) {
-      if (q_issued > 0 && !c.wait(&sh.q_empty, (q_issued - 1) & 1)) return;
-      if (lane == 0) {
-        const int half = p.group * p.tile_tokens * 128;  // bytes of a half tile
-        const int row_tiles = w.split ? 1 : used;        // tile 0 alone, or both, or tile 1 alone
-        mbar_arrive_expect_tx(&sh.q_full, 2 * half * row_tiles);
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          if (w.n[r] == 0 || (w.split && r == 1)) continue;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            tma_load_4d(c.tiles + r * kTileBytes + h * kHalfBytes, tm_q, &sh.q_full, 64 * h, 0,
-                        w.head, w.q_row + r * p.tile_tokens);
-        }
-      }
-      __syncwarp();
-      ++q_issued;
-      if (!load_tiles<kFmt>(c, w, tm_k, tm_v, item, raw_issued)) return;
+      if (!load_tiles<kFmt>(c, w, tm_q, tm_k, tm_v, item, raw_issued, q_issued)) return;
       item += 2 * max(w.n[0], w.n[1]);
     }
     // on to the next unit
@@ -1079,7 +1095,7 @@ __global__ void __launch_bounds__(kExtendThreads, 1)
   // sequences that overlap (offsets that descend) could have any number of units
   if (rows > p.total_q) total = 0;
   int ctas = 1;
-  if (total > 0) ctas = (int)min((long long)gridDim.x, max(1ll, total / kExtendMinShare));
+  if (total > 0) ctas = (int)min((long long)gridDim.x, max(1ll, total / (kExtendMinShare * kKeyCost)));
   const long long share = quotient(total, ctas), extra = total - share * ctas;
   const long long lo = blockIdx.x * share + min((long long)blockIdx.x, extra);
   const bool works = total > 0 && blockIdx.x < ctas;
