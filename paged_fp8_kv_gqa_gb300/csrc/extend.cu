@@ -100,7 +100,7 @@ struct Shared {
   long long share, extra;        // of a CTA on the line (one more for the first `extra` CTAs)
   long long start_at;            // where the CTA's first sequence begins
   Seq start;
-  int start_seq;
+  int start_seq, ctas;           // ctas: that share the line
 };
 
 constexpr int kSmemTiles = (2 + kKvStages) * kTileBytes;
@@ -115,6 +115,7 @@ static_assert(kExtendSmem <= 227 * 1024, "shared memory budget");
 // it fills one row tile only (a 128-key tile takes 1.6 and 0.9 us), and kUnitCost more for its
 // start and end.
 constexpr int kKeyCost = 16, kKeyCostOne = 10, kUnitCost = 256 * kKeyCost;
+constexpr int kCutTiles = 8;  // units of fewer tiles are not cut
 struct Cost {
   int np;
   long long base;
@@ -368,10 +369,14 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
   const long long share = sh.share, extra = sh.extra;
   const int cta = blockIdx.x;
   const long long lo = cta * share + min((long long)cta, extra);
-  const long long hi = lo + share + (cta < extra ? 1 : 0);
-  auto owner = [&](long long x) {  // CTA of a position of the line
-    const long long large = extra * (share + 1);
-    return (int)(x < large ? quotient(x, share + 1) : extra + quotient(x - large, share));
+  const long long hi = lo + share + (cta < extra ? 1 : 0);  // (begin_of(cta + 1))
+  auto begin_of = [&](int c) { return c * share + min((long long)c, extra); };
+  const float per_share = __frcp_rn((float)share);
+  auto owner = [&](long long x) {  // CTA of a position of the line: an estimate, put right
+    int c = min((int)((float)x * per_share), sh.ctas - 1);
+    while (begin_of(c) > x) --c;
+    while (c + 1 < sh.ctas && begin_of(c + 1) <= x) ++c;
+    return c;
   };
   int base = -1, b = sh.start_seq, item = 0;  // sequences base .. base + 31, one a lane
   Seq mine{0, 0, 0};
@@ -388,7 +393,7 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
   long long pos = lo;
   {  // the unit that holds lo
     const long long one = cost.head();
-    head = (int)quotient(lo - at, one);
+    head = lo == at ? 0 : (int)quotient(lo - at, one);
     const long long rem = lo - at - head * one;
     int a = 0, z = cost.np - 1;  // the last unit that begins at or before rem
     while (a < z) {
@@ -426,22 +431,42 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
     const int tiles = last > 0 ? (last - 1) / kTile + 1 : 0;
     w.slot = -1;
     int t0 = 0, t1 = tiles;
+    bool some = true;  // there is a tile for this CTA
     if (x0 > 0 || x1 < len) {
-      w.slot = 2 * cta + (x0 > 0 ? 0 : 1);
-      if (x0 == 0) {  // its other pieces are those of the next CTAs
-        split_unit.pieces = owner(u0 + len - 1) - cta + 1;
-        split_unit.q_row = w.q_row;
-        split_unit.tokens = w.tokens;
-        split_unit.head = head;
-        split_unit.bad = w.bad;
-      }
-      const int tile_cost = kTile * cost.key(pair);
+      // Tile at which a cut at position x of the unit falls. A short unit is not cut, and no
+      // end of less than a quarter of a CTA's share (four tiles at most) is cut off: leaving
+      // a piece and joining it costs about as much. Such a cut moves to the unit's end.
+      const bool full = cost.key(pair) == kKeyCost;  // (divisors known to the compiler)
+      constexpr int kTileCost = kTile * kKeyCost, kTileCostOne = kTile * kKeyCostOne;
+      auto in_tiles = [&](long long x) { return full ? x / kTileCost : x / kTileCostOne; };
+      const int least = (int)min(4ll, max(1ll, in_tiles(share >> 2)));
       auto tile_of = [&](long long x) {
-        return (int)min((long long)tiles,
-                        quotient(max(0ll, x - kUnitCost + tile_cost / 2), tile_cost));
+        const long long y = x - kUnitCost + (full ? kTileCost : kTileCostOne) / 2;
+        const int at = (int)min((long long)tiles, in_tiles(max(0ll, y)));
+        if (tiles < kCutTiles) return 2 * at < tiles ? 0 : tiles;
+        return at < least ? 0 : tiles - at < least ? tiles : at;
       };
       if (x0 > 0) t0 = tile_of(x0);
       if (x1 < len) t1 = tile_of(x1);
+      int first = owner(u0), last_cta = owner(u0 + len - 1);
+      if (tiles == 0) {
+        some = x0 == 0;
+      } else {
+        some = t1 > t0;
+        // cuts at an end leave nothing to the unit's first or last CTAs
+        while (first < last_cta && tile_of(begin_of(first + 1) - u0) == 0) ++first;
+        while (first < last_cta && tile_of(begin_of(last_cta) - u0) == tiles) --last_cta;
+        if (some && first < last_cta) {
+          w.slot = 2 * cta + (cta == first);
+          if (cta == first) {  // its other pieces are those of the next CTAs
+            split_unit.pieces = last_cta - first + 1;
+            split_unit.q_row = w.q_row;
+            split_unit.tokens = w.tokens;
+            split_unit.head = head;
+            split_unit.bad = w.bad;
+          }
+        }
+      }
     }
     w.page0 = t0 * kTilePages;
     w.len_k = max(0, min(len_k, t1 * kTile) - t0 * kTile);
@@ -455,7 +480,7 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
     w.split = w.tokens <= p.tile_tokens && w.n[0] >= 2;
     if (w.split) w.n[1] = w.n[0];
     w.hidden = max(0, min(w.vis0, w.len_k));
-    if (lane == 0) {
+    if (some && lane == 0) {
       sh.unit[slot] = w;
       sh.not_finite[slot] = 0;
       if (const uint32_t more = max(w.n[0], w.n[1]) >> 16) {  // (an abort stays one)
@@ -465,7 +490,8 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
       }
       mbar_arrive(&sh.unit_full[slot]);
     }
-    if (max(w.n[0], w.n[1]) > 0) {
+    if (!some) --i;  // the unit's place serves the next one
+    else if (max(w.n[0], w.n[1]) > 0) {
       if (!load_tiles<kFmt>(c, w, tm_q, tm_k, tm_v, item, raw_issued, q_issued)) return;
       item += 2 * max(w.n[0], w.n[1]);
     }
@@ -1120,6 +1146,7 @@ __global__ void __launch_bounds__(kExtendThreads, 1)
   if (threadIdx.x == 0) {
     sh.share = share;
     sh.extra = extra;
+    sh.ctas = ctas;
   }
   __syncthreads();
   const float sc = (float)(p.qk_scale_base * (double)ks);
@@ -1333,7 +1360,8 @@ cudaError_t launch_extend(const CUtensorMap& tm_q, const CUtensorMap& tm_k, cons
       e = f16 ? launch<XQA_KV_E2M1, XQA_F16>(tm_q, tm_k, tm_v, p, cfg)
               : launch<XQA_KV_E2M1, XQA_BF16>(tm_q, tm_k, tm_v, p, cfg);
   }
-  if (e != cudaSuccess || ctas == 1) return e;  // (one CTA has nothing to share)
+  // one CTA shares nothing, and so do units of tables that are too short for a cut
+  if (e != cudaSuccess || ctas == 1 || p.max_blocks_per_seq <= (kCutTiles - 1) * kTilePages) return e;
   cfg.gridDim = dim3((unsigned)(ctas * kJoinBlocks));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;

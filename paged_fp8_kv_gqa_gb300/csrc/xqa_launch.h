@@ -92,7 +92,7 @@ struct PrefillParams {
 
 // The least share of the line of work (extend.cu: keys seen, summed over the units) that a
 // CTA takes; fewer CTAs work on shorter lines.
-constexpr int kExtendMinShare = 640;
+constexpr int kExtendMinShare = 384;
 
 // A unit of tokens whose keys several CTAs share; pieces < 2: none.
 struct SplitUnit {
