@@ -1201,121 +1201,179 @@ __global__ void __launch_bounds__(kExtendThreads, 1)
 }
 
 // ---- the join of split units' pieces ----
-// A warp has a row, 4 dims a lane; the pieces' (m, l) are read a piece a lane. Up to
-// kWarpPieces pieces are one warp's work; of more, the block's warps take equal runs, each
-// with its own maximum, and join once more through shared memory.
-constexpr int kJoinBlocks = 4;  // for each CTA of the kernel before
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kWarpPieces = 8;
+// A team of 16 lanes has a row, 8 dims a lane. The pieces' (m, l) are read a piece a lane,
+// which so weighs its piece for all; then each piece costs eight fused products a lane. Up to
+// kTeamPieces pieces are one team's work; of more, the block's teams take equal runs, each with
+// its own maximum, and join through shared memory. The kernel is a chain of memory round
+// trips: the units, (m, l) and O at once, out.
+constexpr int kJoinThreads = 256, kTeams = kJoinThreads / 16, kTeamPieces = 8;
+constexpr int kJoinBlocks = 4;  // for each CTA of the kernel before: what an SM holds at once
 
-struct Row {  // O, m, l of a row (O: this lane's 4 dims)
-  float4 o;
-  float m, l;
-};
-__device__ __forceinline__ void add_row(Row& a, const Row& b) {
-  if (b.l == 0.f) return;  // without keys: its O was not written
-  const float m = a.l == 0.f ? b.m : fmaxf(a.m, b.m);
-  // a piece with keys keeps the least weight there is: its infinities and NaN are the row's
-  const float wa = a.l == 0.f ? 0.f : fmaxf(ex2(a.m - m), 0x1p-149f), wb = fmaxf(ex2(b.m - m), 0x1p-149f);
-  a.o.x = (wa == 0.f ? 0.f : wa * a.o.x) + wb * b.o.x;
-  a.o.y = (wa == 0.f ? 0.f : wa * a.o.y) + wb * b.o.y;
-  a.o.z = (wa == 0.f ? 0.f : wa * a.o.z) + wb * b.o.z;
-  a.o.w = (wa == 0.f ? 0.f : wa * a.o.w) + wb * b.o.w;
-  a.l = (wa == 0.f ? 0.f : wa * a.l) + wb * b.l;
-  a.m = m;
+// Weights of up to 16 parts of a row, one a lane (l = 0: a part without keys, whose O was not
+// written); m and l become the whole's. A part with keys keeps the least weight there is: its
+// infinities and NaN are the row's.
+__device__ __forceinline__ float weigh(float& m, float& l) {
+  const bool some = l != 0.f;
+  float top = some ? m : -INFINITY;
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+  const float w = some ? fmaxf(ex2(m - top), 0x1p-149f) : 0.f;
+  float sum = some ? w * l : 0.f;
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
+  m = top;
+  l = sum;
+  return w;
+}
+__device__ __forceinline__ void add(float4& a, float w, const float4& o) {
+  a.x = fmaf(w, o.x, a.x);
+  a.y = fmaf(w, o.y, a.y);
+  a.z = fmaf(w, o.z, a.z);
+  a.w = fmaf(w, o.w, a.w);
 }
 
 template <int kType>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const ExtendParams p, int ctas) {
-  __shared__ int first[kMaxCtas + 1];  // work items before each CTA's split unit
-  __shared__ float4 part_o[kJoinWarps][32];
-  __shared__ float2 part_ml[kJoinWarps];
+__global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) join_kernel(const ExtendParams p, int ctas) {
+  __shared__ int first[kMaxCtas];      // work items before each split unit
+  __shared__ SplitUnit unit[kMaxCtas];
+  __shared__ short begin[kMaxCtas];    // the CTA of its first piece
+  __shared__ float4 part_o[kTeams][2][16];
+  __shared__ float2 part_ml[kTeams];
+  __shared__ int2 sums[kJoinThreads / 32];
   griddep_launch_dependents();
   griddep_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // an item: eight rows, a warp each, or a row of many pieces
-  auto items = [&](const SplitUnit& u) {
-    const int rows = u.tokens * p.group;
-    return u.pieces < 2 ? 0 : u.pieces <= kWarpPieces ? (rows + kJoinWarps - 1) / kJoinWarps : rows;
-  };
-  int total = 0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l16 = lane & 15, team = tid >> 4;
+  const float vs = p.v_scale_ptr ? *p.v_scale_ptr : p.v_scale;
+  // an item: a row a team, or a row of many pieces
+  int total = 0, units = 0;
   for (int c0 = 0; c0 < ctas; c0 += kJoinThreads) {
     const int c = c0 + tid;
-    int n = 0;
-    if (c < ctas) n = items(p.split[c]);
+    SplitUnit u{0, 0, 0, 0, 0};
+    if (c < ctas) u = p.split[c];
+    const int rows = u.pieces > 1 ? u.tokens * p.group : 0;
+    const int n = u.pieces <= kTeamPieces ? (rows + kTeams - 1) / kTeams : rows;
+    const unsigned some = __ballot_sync(kAll, n > 0);
     int incl = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int x = __shfl_up_sync(kAll, incl, off);
       if (lane >= off) incl += x;
     }
-    __shared__ int sums[kJoinWarps];
-    if (lane == 31) sums[warp] = incl;
+    if (lane == 31) sums[warp] = make_int2(incl, __popc(some));
     __syncthreads();
-    int before = total;
-    for (int w = 0; w < kJoinWarps; ++w) {
-      if (w < warp) before += sums[w];
-      total += sums[w];
+    int before = total, at = units;
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+      if (w < warp) before += sums[w].x, at += sums[w].y;
+      total += sums[w].x;
+      units += sums[w].y;
     }
-    if (c < ctas) first[c] = before + incl - n;
+    if (n > 0) {
+      at += __popc(some & ((1u << lane) - 1));
+      first[at] = before + incl - n;
+      begin[at] = (short)c;
+      unit[at] = u;
+    }
     __syncthreads();
   }
-  if (tid == 0) first[ctas] = total;
-  __syncthreads();
-  const float vs = p.v_scale_ptr ? *p.v_scale_ptr : p.v_scale;
   for (int item = blockIdx.x; item < total; item += gridDim.x) {
-    int lo = 0, hi = ctas - 1;  // the last unit that begins at or before the item
+    int lo = 0, hi = units - 1;  // the last unit that begins at or before the item
     while (lo < hi) {
       const int m = (lo + hi + 1) >> 1;
       if (first[m] <= item) lo = m;
       else hi = m - 1;
     }
-    const SplitUnit u = p.split[lo];
-    const bool many = u.pieces > kWarpPieces;
-    const int at = item - first[lo], r = many ? at : at * kJoinWarps + warp;
-    const int rows = u.tokens * p.group;
+    const int cta = begin[lo], pieces = unit[lo].pieces, rows = unit[lo].tokens * p.group;
+    const bool many = pieces > kTeamPieces;
+    const int at = item - first[lo], r = many ? at : at * kTeams + team;
     const bool valid = r < rows;
     const int t = min(r, rows - 1) / p.group, g = min(r, rows - 1) - t * p.group;
     const int s = t >= p.tile_tokens;
     const int row = (t - s * p.tile_tokens) * p.group + g;
-    // piece k is in slot 1 of the first CTA, slot 0 of the others
-    auto place = [&](int k) {
-      return ((size_t)(4 * (lo + k) + (k == 0 ? 2 : 0) + s)) * kTile + row;
-    };
-    Row sum{make_float4(0.f, 0.f, 0.f, 0.f), kNoRowMax, 0.f};
-    const int per = many ? (u.pieces + kJoinWarps - 1) / kJoinWarps : u.pieces;
-    const int k0 = many ? warp * per : 0, k1 = min(u.pieces, k0 + per);
-    for (int k = k0; k < k1; k += 8) {  // eight pieces' rows in flight
-      const float2 ml = lane < 8 && k + lane < k1 ? __ldcg(p.piece_ml + place(k + lane))
-                                                  : make_float2(kNoRowMax, 0.f);
-      float4 o[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k + e < k1)
-          o[e] = __ldcg(reinterpret_cast<const float4*>(p.piece_o + place(k + e) * kHeadDim) + lane);
+    // piece k is in slot 1 of the first CTA, slot 0 of the others; a CTA has 2 x 2 tiles of rows
+    const size_t place0 = (size_t)(4 * cta + s) * kTile + row;
+    auto tile = [](int k) { return (4 * k + (k == 0 ? 2 : 0)) * kTile; };
+    const int per = many ? (pieces + kTeams - 1) / kTeams : pieces;
+    const int k0 = many ? team * per : 0, n = min(pieces - k0, per);  // (n <= 0: none)
+    const float* o = p.piece_o + place0 * kHeadDim + 4 * l16;  // dims 4 l16 .., 64 + 4 l16 ..
+    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    float m = kNoRowMax, l = 0.f;
+    // (teams of a warp may have different numbers of rounds: its shuffles are for both)
+    for (int c0 = 0; c0 < per; c0 += 16) {
+      float cm = kNoRowMax, cl = 0.f;
+      if (c0 + l16 < n) {
+        const float2 ml = __ldcg(p.piece_ml + place0 + tile(k0 + c0 + l16));
+        cm = ml.x, cl = ml.y;
       }
+      constexpr int kAtOnce = 4;
+      float4 sum[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+      float w = 0.f;
+      for (int e0 = 0; e0 < min(per - c0, 16); e0 += kAtOnce) {
+        float4 v[kAtOnce][2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        add_row(sum, Row{o[e], __shfl_sync(kAll, ml.x, e), __shfl_sync(kAll, ml.y, e)});
+        for (int e = 0; e < kAtOnce; ++e) {
+          v[e][0] = v[e][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c0 + e0 + e < n) {
+            const float* x = o + (size_t)tile(k0 + c0 + e0 + e) * kHeadDim;
+            v[e][0] = __ldcg(reinterpret_cast<const float4*>(x));
+            v[e][1] = __ldcg(reinterpret_cast<const float4*>(x + 64));
+          }
+        }
+        if (e0 == 0) w = weigh(cm, cl);
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e) {
+          const float we = __shfl_sync(kAll, w, e0 + e, 16);
+          if (we != 0.f) add(sum[0], we, v[e][0]), add(sum[1], we, v[e][1]);
+        }
+      }
+      if (c0 == 0) {
+        acc[0] = sum[0], acc[1] = sum[1], m = cm, l = cl;
+      } else {  // join with the rounds before
+        float m2 = l16 == 0 ? m : cm, l2 = l16 == 0 ? l : l16 == 1 ? cl : 0.f;
+        const float w2 = weigh(m2, l2);
+        const float wa = __shfl_sync(kAll, w2, 0, 16), wb = __shfl_sync(kAll, w2, 1, 16);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float4 both = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (wa != 0.f) add(both, wa, acc[x]);
+          if (wb != 0.f) add(both, wb, sum[x]);
+          acc[x] = both;
+        }
+        m = m2, l = l2;
+      }
     }
     if (many) {
       __syncthreads();  // the item before is read
-      part_o[warp][lane] = sum.o;
-      if (lane == 0) part_ml[warp] = make_float2(sum.m, sum.l);
+      part_o[team][0][l16] = acc[0];
+      part_o[team][1][l16] = acc[1];
+      if (l16 == 0) part_ml[team] = make_float2(m, l);
       __syncthreads();
       if (warp != 0) continue;
-      for (int w = 1; w < kJoinWarps; ++w) add_row(sum, Row{part_o[w][lane], part_ml[w].x, part_ml[w].y});
+      const float2 ml = part_ml[l16];
+      m = ml.x, l = ml.y;
+      const float w = weigh(m, l);
+      acc[0] = acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < kTeams; ++e) {
+        const float we = __shfl_sync(kAll, w, e, 16);
+        if (we != 0.f) add(acc[0], we, part_o[e][0][l16]), add(acc[1], we, part_o[e][1][l16]);
+      }
+      if (team != 0) continue;
     }
     if (!valid) continue;
     const float nan = __int_as_float(0x7fc00000);
-    const float rl = u.bad ? nan : sum.l == 0.f ? 0.f : vs / sum.l;
-    const long long q = (long long)u.q_row + t;
-    const int h = u.head * p.group + g;
-    reinterpret_cast<uint2*>(p.out + q * p.out_row_stride + h * p.out_head_stride)[lane] =
-        make_uint2(pack2<kType>(sum.o.x * rl, sum.o.y * rl), pack2<kType>(sum.o.z * rl, sum.o.w * rl));
-    if (p.lse && lane == 0)
+    const bool bad = unit[lo].bad;
+    const float rl = bad ? nan : l == 0.f ? 0.f : vs / l;
+    const long long q = (long long)unit[lo].q_row + t;
+    const int h = unit[lo].head * p.group + g;
+    uint16_t* out = p.out + q * p.out_row_stride + h * p.out_head_stride + 4 * l16;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      *reinterpret_cast<uint2*>(out + 64 * x) = make_uint2(
+          pack2<kType>(acc[x].x * rl, acc[x].y * rl), pack2<kType>(acc[x].z * rl, acc[x].w * rl));
+    if (p.lse && l16 == 0)
       p.lse[q * p.num_q_heads + h] =
-          u.bad ? nan : sum.l == 0.f ? -INFINITY : (sum.m + __log2f(sum.l)) * 0.6931471805599453f;
+          bad ? nan : l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
   }
 }
 
