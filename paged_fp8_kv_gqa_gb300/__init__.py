@@ -847,8 +847,7 @@ def xqa_extend(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, k_sc
     if out is None:
         if not plain_out:
             raise ValueError("the shape descriptor names strides of out: pass out")
-        with _allocating(stream) if stream is not None else _NO_CONTEXT:
-            out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        out = _like(q, q.shape, stream)
     elif out.shape != q.shape or _heads(out, "out", dtype) != (
             shape.out_row_stride or shape.num_q_heads * 128, shape.out_head_stride or 128):
         raise ValueError("out does not match q or the shape descriptor")
@@ -888,6 +887,14 @@ def _pages_descriptor(n_lens: int, bt_shape, n_free: int, n_first: int, num_rows
     return XqaPages(n_lens, 16, bt_shape[1], n_free, num_rows)
 
 
+def _like(t: torch.Tensor, shape, stream) -> torch.Tensor:
+    """An uninitialised tensor of t's type and device that a call on ``stream`` writes."""
+    if stream is None:
+        return torch.empty(shape, dtype=t.dtype, device=t.device)
+    with _allocating(stream):
+        return torch.empty(shape, dtype=t.dtype, device=t.device)
+
+
 def _all_i32(dev: int, *tensors) -> bool:
     for t in tensors:
         if not (t.dtype is _I32 and t.get_device() == dev and t.is_contiguous()):
@@ -917,13 +924,12 @@ def xqa_assign_pages(new_tokens, context_lens, block_tables, free_pages, num_fre
             n, num_rows = context_lens.numel(), int(num_rows)
             if num_rows < 0:
                 raise ValueError("num_rows must not be negative")
-            with _allocating(stream) if stream is not None else _NO_CONTEXT:
-                if cu_seqlens is None:
-                    cu_seqlens = torch.empty(n + 1, dtype=_I32, device=context_lens.device)
-                if slots is None:
-                    slots = torch.empty(num_rows, dtype=_I32, device=context_lens.device)
-                if positions is None:
-                    positions = torch.empty(num_rows, dtype=_I32, device=context_lens.device)
+            if cu_seqlens is None:
+                cu_seqlens = _like(context_lens, n + 1, stream)
+            if slots is None:
+                slots = _like(context_lens, num_rows, stream)
+            if positions is None:
+                positions = _like(context_lens, num_rows, stream)
             if _all_i32(dev, cu_seqlens, slots, positions):
                 pages = _pages_descriptor(n, block_tables.shape, free_pages.numel(), new_tokens.numel(),
                                           num_rows, num_free.numel(), 1, new_free.numel(), 1,
@@ -1086,14 +1092,13 @@ def xqa_select(q, bounds, block_tables, context_lens, max_pages: int = 0, first_
         if (dev >= 0 and torch._C._cuda_getDevice() == dev and q.dtype is _F16 and q.is_contiguous()
                 and bounds.dtype is _U8 and bounds.get_device() == dev and bounds.is_contiguous()
                 and _all_i32(dev, block_tables, context_lens)):
-            with _allocating(stream) if stream is not None else _NO_CONTEXT:
-                if selected is None:
-                    selected = torch.empty((shape.batch, shape.num_kv_heads, max(shape.max_pages, 0)),
-                                           dtype=_I32, device=q.device)
-                if selected_lens is None:
-                    selected_lens = torch.empty((shape.batch, shape.num_kv_heads), dtype=_I32,
-                                                device=q.device)
-                if workspace is None:
+            if selected is None:
+                selected = _like(context_lens, (shape.batch, shape.num_kv_heads,
+                                                max(shape.max_pages, 0)), stream)
+            if selected_lens is None:
+                selected_lens = _like(context_lens, (shape.batch, shape.num_kv_heads), stream)
+            if workspace is None:
+                with _allocating(stream):
                     workspace = alloc_select_workspace(shape, q.device)
             fits = _all_i32(dev, selected, selected_lens) and _select_fits(
                 bytes(shape), q.shape, bounds.shape, block_tables.shape, context_lens.numel(),
@@ -1130,6 +1135,18 @@ def make_selected_shape(q, k_cache, selected, sm_scale: float = 0.0, max_ctas: i
     return shape
 
 
+@functools.lru_cache(maxsize=1024)
+def _selected_fits(shape: bytes, q, k_cache, v_cache, selected, selected_lens, n_out) -> bool:
+    """Raises unless tensors of these shapes are what the descriptor says."""
+    s = XqaShape.from_buffer_copy(shape)
+    if (tuple(selected) != (s.batch, s.num_kv_heads, s.max_blocks_per_seq)
+            or tuple(selected_lens) != (s.batch, s.num_kv_heads)):
+        raise ValueError("selected or selected_lens does not match the shape descriptor")
+    if len(q) != 3:
+        raise ValueError("q must be [B, Hq, 128]: one new token for each sequence")
+    return _decode_fits(shape, q, k_cache, v_cache, selected[::2], s.batch, n_out)
+
+
 def xqa_decode_selected(q, k_cache, v_cache, selected, selected_lens, k_scale, v_scale, out=None,
                         workspace=None, shape: XqaShape | None = None, stream=None,
                         sm_scale: float = 0.0, max_ctas: int = 0, min_pages_per_cta: int = 0,
@@ -1140,28 +1157,38 @@ def xqa_decode_selected(q, k_cache, v_cache, selected, selected_lens, k_scale, v
     if shape is None:
         shape = make_selected_shape(q, k_cache, selected, sm_scale, max_ctas, min_pages_per_cta,
                                     kv_dtype=kv_dtype, kv_layout=kv_layout)
-    if selected.dim() != 3 or tuple(selected.shape) != (shape.batch, shape.num_kv_heads,
-                                                        shape.max_blocks_per_seq):
-        raise ValueError("selected does not match the shape descriptor")
-    if tuple(selected_lens.shape) != (shape.batch, shape.num_kv_heads):
-        raise ValueError("selected_lens must be [B, Hkv]")
     fresh = out is None
-    if out is None or workspace is None:
-        with _allocating(stream) if stream is not None else _NO_CONTEXT:
-            if out is None:
-                out = torch.empty_like(q)
-            if workspace is None:
-                workspace = alloc_workspace(shape, q.device)
-    a = _decode_args(q, k_cache, v_cache, selected.view(-1, selected.shape[2]),
-                     selected_lens, out, workspace, shape, fresh=fresh)
-    dev = q.get_device()
-    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
+    if fresh:
+        out = _like(q, q.shape, stream)
+    if workspace is None:
+        with _allocating(stream):
+            workspace = alloc_workspace(shape, q.device)
+    fits = False
+    try:  # the usual call, without a function call for each tensor
+        dev = q.get_device()
+        if (dev >= 0 and torch._C._cuda_getDevice() == dev and q.dtype is _F16 and q.is_contiguous()
+                and k_cache.dtype is _U8 and k_cache.get_device() == dev and k_cache.is_contiguous()
+                and v_cache.dtype is _U8 and v_cache.get_device() == dev and v_cache.is_contiguous()
+                and (fresh or (out.dtype is _F16 and out.get_device() == dev and out.is_contiguous()))
+                and workspace.dtype is _U8 and workspace.get_device() == dev and workspace.is_contiguous()
+                and _all_i32(dev, selected, selected_lens)):
+            fits = _selected_fits(bytes(shape), q.shape, k_cache.shape, v_cache.shape, selected.shape,
+                                  selected_lens.shape, None if fresh else out.numel())
+    except AttributeError:
+        pass
+    if not fits:
+        _on_current((q, _F16, "q"), (k_cache, _U8, "k_cache"), (v_cache, _U8, "v_cache"),
+                    (selected, _I32, "selected"), (selected_lens, _I32, "selected_lens"),
+                    (out, _F16, "out"), (workspace, _U8, "workspace"))
+        raise ValueError("invalid arguments")
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _device_stream(stream)[1]
     ks, ksp = (k_scale, None) if type(k_scale) is float else _scale_arg(k_scale, dev, "k_scale")
     vs, vsp = (v_scale, None) if type(v_scale) is float else _scale_arg(v_scale, dev, "v_scale")
     if (ksp is None) != (vsp is None):
         raise ValueError("k_scale and v_scale must both be numbers, or both CUDA tensors")
-    code = load_library().xqa_decode_selected(a[0], a[1], a[2], a[3], a[4], ks, vs, ksp, vsp, a[5],
-                                              ctypes.byref(shape), a[6], workspace.numel(), handle)
+    code = load_library().xqa_decode_selected(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), selected.data_ptr(), selected_lens.data_ptr(),
+        ks, vs, ksp, vsp, out.data_ptr(), ctypes.byref(shape), workspace.data_ptr(), workspace.numel(), handle)
     if code:
         raise XqaError(code, "xqa_decode_selected")
     return out
