@@ -40,12 +40,13 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // floor(log2 x) of a normal x > 0
 __device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
 
+// Of pairs; a NaN stays one.
 __device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
-  const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  const __half2 m = __hmax2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 __device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
-  const __half2 m = __hmin2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  const __half2 m = __hmin2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
@@ -56,21 +57,37 @@ __device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
 // ---------------------------------------------------------------------------
 constexpr int kBoundsThreads = 128;
 
-// 16 neighbouring dims of a token as 8 half2 (exact: see the formats).
+// Codes of 16 neighbouring dims of a token, and their values as 8 half2 (exact: see the formats).
 template <int kFmt>
-__device__ __forceinline__ void key16(const uint8_t* slice, size_t token_stride, int t, int c,
-                                      uint32_t (&o)[8]) {
+struct Key16 {
+  uint4 w;
+};
+template <>
+struct Key16<XQA_KV_E2M1> {
+  uint2 w;
+  uint32_t s8;
+};
+template <int kFmt>
+__device__ __forceinline__ Key16<kFmt> read_key(const uint8_t* slice, size_t token_stride, int t, int c) {
+  Key16<kFmt> k;
   if constexpr (kFmt == XQA_KV_E2M1) {
-    const uint2 w = *reinterpret_cast<const uint2*>(slice + t * (kHeadDim / 2) + 8 * c);
-    const uint32_t s8 = slice[kCodeBytes4 + t * (kHeadDim / kGroup4) + c];
-    const uint32_t sc = e4m3x2_to_f16x2(s8 | s8 << 8);
-    e2m1x8_to_f16x2(w.x, o);
-    e2m1x8_to_f16x2(w.y, o + 4);
+    k.w = *reinterpret_cast<const uint2*>(slice + t * (kHeadDim / 2) + 8 * c);
+    k.s8 = slice[kCodeBytes4 + t * (kHeadDim / kGroup4) + c];
+  } else {
+    k.w = *reinterpret_cast<const uint4*>(slice + t * token_stride + 16 * c);
+  }
+  return k;
+}
+template <int kFmt>
+__device__ __forceinline__ void key_values(const Key16<kFmt>& k, uint32_t (&o)[8]) {
+  if constexpr (kFmt == XQA_KV_E2M1) {
+    const uint32_t sc = e4m3x2_to_f16x2(k.s8 | k.s8 << 8);
+    e2m1x8_to_f16x2(k.w.x, o);
+    e2m1x8_to_f16x2(k.w.y, o + 4);
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = hmul2(o[i], sc);
   } else {
-    const uint4 w = *reinterpret_cast<const uint4*>(slice + t * token_stride + 16 * c);
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    const uint32_t x[4] = {k.w.x, k.w.y, k.w.z, k.w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       o[2 * i] = KvConv<kFmt>::k_lo(x[i]);
@@ -79,67 +96,102 @@ __device__ __forceinline__ void key16(const uint8_t* slice, size_t token_stride,
   }
 }
 
+// This lane's codes of a slice: dims 16 (lane & 7) .. of tokens lane / 8, + 4, ... below `fill`.
 template <int kFmt>
-__device__ __forceinline__ void bound_slice(const BoundsParams& p, int page, int head, int fill) {
-  const int lane = threadIdx.x & 31, c = lane & 7, t0 = lane >> 3;
+__device__ __forceinline__ void read_slice(const BoundsParams& p, int page, int head, int fill,
+                                           Key16<kFmt> (&k)[4]) {
+  const int lane = threadIdx.x & 31;
   const bool nhd = kFmt != XQA_KV_E2M1 && p.kv_layout == XQA_LAYOUT_NHD;
   const size_t stride = nhd ? (size_t)p.num_kv_heads * kHeadDim : kHeadDim;
   const uint8_t* slice =
       p.k_cache + (nhd ? ((size_t)page * kBlockSize * p.num_kv_heads + head) * kHeadDim
                        : ((size_t)page * p.num_kv_heads + head) *
                              (kFmt == XQA_KV_E2M1 ? (size_t)kSliceBytes4 : (size_t)kPageBytes));
-  uint32_t hi[8], lo[8], top = 0;
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    if (4 * s + (lane >> 3) < fill) k[s] = read_key<kFmt>(slice, stride, 4 * s + (lane >> 3), lane & 7);
+}
+
+template <int kFmt>
+__device__ __forceinline__ void bound_slice(const BoundsParams& p, int page, int head, int fill,
+                                            const Key16<kFmt> (&codes)[4]) {
+  const int lane = threadIdx.x & 31, t0 = lane >> 3;
+  uint32_t hi[8], lo[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) hi[i] = 0xfc00fc00u, lo[i] = 0x7c007c00u;  // -inf, inf
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    const int t = 4 * s + t0;
-    if (t >= fill) continue;
+    if (4 * s + t0 >= fill) continue;
     uint32_t k[8];
-    key16<kFmt>(slice, stride, t, c, k);
+    key_values<kFmt>(codes[s], k);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       hi[i] = hmax2(hi[i], k[i]);
       lo[i] = hmin2(lo[i], k[i]);
-      top = __vmaxu2(top, k[i] & 0x7fff7fffu);  // magnitudes order like their patterns
     }
   }
+  // lanes 8 and 16 apart hold other tokens of the same dims: each keeps one half, then one
+  // quarter of the dims (pairs 2 t0, 2 t0 + 1 in the end)
 #pragma unroll
-  for (int off = 8; off < 32; off <<= 1)
+  for (int half = 4; half >= 2; half >>= 1) {
+    const int off = 4 * half;
+    const bool up = lane & off;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      hi[i] = hmax2(hi[i], __shfl_xor_sync(kAll, hi[i], off));
-      lo[i] = hmin2(lo[i], __shfl_xor_sync(kAll, lo[i], off));
+    for (int i = 0; i < half; ++i) {
+      const uint32_t h = __shfl_xor_sync(kAll, up ? hi[i] : hi[i + half], off);
+      const uint32_t l = __shfl_xor_sync(kAll, up ? lo[i] : lo[i + half], off);
+      hi[i] = hmax2(up ? hi[i + half] : hi[i], h);
+      lo[i] = hmin2(up ? lo[i + half] : lo[i], l);
     }
+  }
+  const int pair = (lane & 16 ? 4 : 0) + (lane & 8 ? 2 : 0);  // of this lane's 16 dims
+  // magnitudes order like their patterns, infinities and NaN last
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    top = __vmaxu2(top, __vmaxu2(hi[i] & 0x7fff7fffu, lo[i] & 0x7fff7fffu));
   const uint32_t big = __reduce_max_sync(kAll, max(top & 0xffffu, top >> 16));
   int e = 0;
   if (big >= 0x7c00u) e = kNotFinite;
   else if (big > 0) e = exponent(__half2float(__ushort_as_half((unsigned short)big))) - 6;
-  // lanes 0-7 write the upper bounds, 8-15 the lower ones, lane 16 the exponent
-  uint4 out = make_uint4(0, 0, 0, 0);
-  uint32_t* w = &out.x;
-  if (lane < 16 && e != kNotFinite) {
-    const float step = pow2(-e);  // |e| <= 22
-    const bool upper = lane < 8;
+  uint32_t up4 = 0, low4 = 0;  // four dims each
+  if (e != kNotFinite) {
+    const float step = pow2(-e);  // |e| <= 22; the products are exact
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t v = upper ? hi[i] : lo[i];
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
-      const float a = f.x * step, b = f.y * step;  // exact
-      const int x = (int)(upper ? ceilf(a) : floorf(a)), y = (int)(upper ? ceilf(b) : floorf(b));
-      w[i >> 1] |= ((uint32_t)(x & 255) | (uint32_t)(y & 255) << 8) << (16 * (i & 1));
+    for (int i = 0; i < 2; ++i) {
+      const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
+      const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&lo[i]));
+      up4 |= ((uint32_t)(__float2int_ru(u.x * step) & 255) | (uint32_t)(__float2int_ru(u.y * step) & 255) << 8)
+             << (16 * i);
+      low4 |= ((uint32_t)(__float2int_rd(d.x * step) & 255) | (uint32_t)(__float2int_rd(d.y * step) & 255) << 8)
+              << (16 * i);
     }
   }
-  if (lane == 16) out.x = (uint32_t)(e & 255);
-  if (lane <= 16)
-    *reinterpret_cast<uint4*>(p.bounds + ((size_t)page * p.num_kv_heads + head) * kBoundsBytes +
-                              16 * lane) = out;
+  uint8_t* out = p.bounds + ((size_t)page * p.num_kv_heads + head) * kBoundsBytes;
+  const int dim = 16 * (lane & 7) + 2 * pair;
+  *reinterpret_cast<uint32_t*>(out + dim) = up4;
+  *reinterpret_cast<uint32_t*>(out + kHeadDim + dim) = low4;
+  if (lane < 4) *reinterpret_cast<uint32_t*>(out + 2 * kHeadDim + 4 * lane) = lane == 0 ? (uint32_t)(e & 255) : 0u;
 }
 
 template <int kFmt>
-__global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsParams p, int rows_per) {
+__global__ void __launch_bounds__(kBoundsThreads, 6) bounds_kernel(const BoundsParams p, int rows_per) {
+  // offsets and lengths of a batch that is not large: every step of the search for a row's
+  // sequence would be a round trip to memory (49k rows 12.8 us)
+  constexpr int kHeld = 256;
+  __shared__ int cu_held[kHeld + 1], ctx_held[kHeld];
   griddep_launch_dependents();
   griddep_wait();
+  const bool held = p.batch <= kHeld;
+  if (held) {
+    for (int i = threadIdx.x; i <= p.batch; i += kBoundsThreads) {
+      cu_held[i] = p.cu_seqlens[i];
+      if (i < p.batch) ctx_held[i] = p.context_lens[i];
+    }
+    __syncthreads();
+  }
+  const int32_t* cu = held ? cu_held : p.cu_seqlens;
+  const int32_t* lens = held ? ctx_held : p.context_lens;
   const int lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * (kBoundsThreads / 32) + (threadIdx.x >> 5);
   const long long r0 = unit / p.num_kv_heads * rows_per;
@@ -148,14 +200,14 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsPara
   // a row a lane: is it its page's first new one, and which page is that
   int page = -1, fill = 0;
   const long long r = r0 + lane;
-  if (lane < rows_per && r < p.num_rows && r >= p.cu_seqlens[0] && r < p.cu_seqlens[p.batch]) {
+  if (lane < rows_per && r < p.num_rows && r >= cu[0] && r < cu[p.batch]) {
     int lo = 0, hi = p.batch - 1;  // last sequence that begins at or before r
     while (lo < hi) {
       const int m = (lo + hi + 1) >> 1;
-      if (p.cu_seqlens[m] <= r) lo = m;
+      if (cu[m] <= r) lo = m;
       else hi = m - 1;
     }
-    const int q0 = p.cu_seqlens[lo], q1 = p.cu_seqlens[lo + 1], ctx = p.context_lens[lo];
+    const int q0 = cu[lo], q1 = cu[lo + 1], ctx = lens[lo];
     if (r >= q0 && r < q1) {
       if (ctx < 0 || ctx < (long long)q1 - q0 || ctx > (long long)p.max_blocks_per_seq * kBlockSize) {
         raise(p.status, XQA_ERR_CTX_TOO_LONG);
@@ -173,9 +225,21 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsPara
       }
     }
   }
-  for (uint32_t some = __ballot_sync(kAll, page >= 0); some; some &= some - 1) {
-    const int src = __ffs(some) - 1;
-    bound_slice<kFmt>(p, __shfl_sync(kAll, page, src), head, __shfl_sync(kAll, fill, src));
+  // two slices' codes in flight
+  for (uint32_t some = __ballot_sync(kAll, page >= 0); some;) {
+    Key16<kFmt> k[2][4];
+    int id[2], n[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int src = some ? __ffs(some) - 1 : 0;
+      id[e] = some ? __shfl_sync(kAll, page, src) : -1;
+      n[e] = __shfl_sync(kAll, fill, src);
+      some &= some - 1;  // (0 stays 0)
+      if (id[e] >= 0) read_slice<kFmt>(p, id[e], head, n[e], k[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (id[e] >= 0) bound_slice<kFmt>(p, id[e], head, n[e], k[e]);
   }
 }
 
@@ -602,9 +666,9 @@ cudaError_t launch(void (*kernel)(Args...), int ctas, int threads, cudaStream_t 
 }  // namespace
 
 cudaError_t launch_bounds(const BoundsParams& p, cudaStream_t stream) {
-  // a row a warp while they are few (a decode step's are all pages of their own), else 16:
-  // of a prompt's rows, those of one or two pages
-  const int rows_per = p.num_rows <= 4096 ? 1 : kBlockSize;
+  // a row a warp while they are few (a decode step's are all pages of their own), else a row a
+  // lane: of a prompt's rows, those of two or three pages
+  const int rows_per = p.num_rows <= 4096 ? 1 : 32;
   const long long units = ((long long)p.num_rows + rows_per - 1) / rows_per * p.num_kv_heads;
   const int ctas = (int)((units + kBoundsThreads / 32 - 1) / (kBoundsThreads / 32));
   switch (p.kv_dtype) {
