@@ -391,9 +391,9 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
   Cost cost = seq_cost(p, s);
   int head = 0, pair = 0;
   long long pos = lo;
-  {  // the unit that holds lo
+  if (lo > at) {  // the unit that holds lo
     const long long one = cost.head();
-    head = lo == at ? 0 : (int)quotient(lo - at, one);
+    if (lo - at >= one) head = (int)quotient(lo - at, one);
     const long long rem = lo - at - head * one;
     int a = 0, z = cost.np - 1;  // the last unit that begins at or before rem
     while (a < z) {
@@ -1108,7 +1108,22 @@ __global__ void __launch_bounds__(kExtendThreads, 1)
   const float vs = p.v_scale_ptr ? *p.v_scale_ptr : p.v_scale;
   long long total = 0, rows = 0, mine = 0, excl = 0;
   Seq s{0, 0, 0};
-  for (int b0 = 0; b0 < p.batch; b0 += kExtendThreads) {
+  const bool few = p.batch <= 32;  // every warp scans them for itself
+  if (few) {
+    const int lane = threadIdx.x & 31;
+    if (lane < p.batch) s = read_seq(p, lane, &sh.status);
+    mine = seq_cost(p, s).head() * p.num_kv_heads;
+    total = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long x = __shfl_up_sync(kAll, total, off);
+      if (lane >= off) total += x;
+    }
+    excl = total - mine;
+    total = __shfl_sync(kAll, total, 31);
+    rows = ((long long)__reduce_add_sync(kAll, s.n >> 16) << 16) + __reduce_add_sync(kAll, s.n & 0xffff);
+  }
+  for (int b0 = 0; !few && b0 < p.batch; b0 += kExtendThreads) {
     const int b = b0 + threadIdx.x;
     s = Seq{0, 0, 0};
     if (b < p.batch) s = read_seq(p, b, &sh.status);
@@ -1122,7 +1137,7 @@ __global__ void __launch_bounds__(kExtendThreads, 1)
   if (rows > p.total_q) total = 0;
   int ctas = 1;
   if (total > 0) ctas = (int)min((long long)gridDim.x, max(1ll, total / (kExtendMinShare * kKeyCost)));
-  const long long share = quotient(total, ctas), extra = total - share * ctas;
+  const long long share = ctas == 1 ? total : quotient(total, ctas), extra = total - share * ctas;
   const long long lo = blockIdx.x * share + min((long long)blockIdx.x, extra);
   const bool works = total > 0 && blockIdx.x < ctas;
   if (p.batch > kExtendThreads && works) {  // once more: a thread keeps one sequence
@@ -1138,7 +1153,7 @@ __global__ void __launch_bounds__(kExtendThreads, 1)
       if (excl <= lo && lo < excl + mine) sh.start_seq = b, sh.start_at = excl, sh.start = s;
       if (lo < before) break;
     }
-  } else if (excl <= lo && lo < excl + mine) {
+  } else if (excl <= lo && lo < excl + mine && (!few || threadIdx.x < 32)) {
     sh.start_seq = threadIdx.x;
     sh.start_at = excl;
     sh.start = s;
