@@ -503,7 +503,7 @@ typedef struct xqa_select_shape {
   int32_t first_pages;        /* a sequence's first pages that are always taken, >= 0 */
   int32_t last_pages;         /* its last ones, >= 1 (the new token's page among them);
                                  first_pages + last_pages <= max_pages */
-  int32_t max_ctas;           /* upper bound on CTAs; 0 = 3 per SM */
+  int32_t max_ctas;           /* upper bound on CTAs; 0 = 2 per SM */
 } xqa_select_shape_t;
 
 /* Bytes of device workspace xqa_select needs for `shape`. Host only. */

@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kBoundsThreads, 6) bounds_kernel(const BoundsP
 // the choice: a CTA scores a chunk of a segment's pages (segment: sequence and kv head); the
 // one that is last to finish a segment's chunks takes its best pages.
 // ---------------------------------------------------------------------------
-constexpr int kSelectThreads = 256;
+constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr uint32_t kKeyAlways = 0xffffffffu, kKeyFirst = 0xfffffffeu;  // above every score's
 
@@ -279,7 +279,8 @@ static_assert(kWarpPages * kSelectWarps == kSelectPages, "pages of a CTA at a ti
 struct SelectShared {
   alignas(16) uint32_t keys[kKeysInSmem];
   int bins[kBins];
-  alignas(16) uint32_t ab[kQueryParts][kHeadDim];  // A (low half), B of some of the heads
+  uint32_t ab[kQueryParts][kHeadDim];  // A (low half), B of some of the heads
+  alignas(16) uint32_t pairs[2][kHeadDim / 2];  // A, B of all, of dims 2 i, 2 i + 1
   uint32_t amax[kSelectWarps];
   int count[kSelectWarps][3];
   uint32_t edge[kSelectWarps][2];
@@ -323,18 +324,17 @@ __device__ __forceinline__ void score_pages(const SelectParams& p, int seg, int 
   }
   sh.ab[tid / kHeadDim][tid % kHeadDim] = (uint32_t)(a & 0xffff) | (uint32_t)n << 16;
   __syncthreads();
-  uint32_t qa[8], qb[8];  // A and B of dims 16 c .. 16 c + 15, in pairs
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint4 v = make_uint4(0, 0, 0, 0);
+  if (tid < kHeadDim / 2) {
+    uint32_t v0 = 0, v1 = 0;
 #pragma unroll
     for (int r = 0; r < kQueryParts; ++r) {
-      const uint4 x = *reinterpret_cast<const uint4*>(&sh.ab[r][16 * c + 4 * i]);
-      v.x = __vadd2(v.x, x.x), v.y = __vadd2(v.y, x.y), v.z = __vadd2(v.z, x.z), v.w = __vadd2(v.w, x.w);
+      v0 = __vadd2(v0, sh.ab[r][2 * tid]);
+      v1 = __vadd2(v1, sh.ab[r][2 * tid + 1]);
     }
-    qa[2 * i] = prmt(v.x, v.y, 0x5410u), qa[2 * i + 1] = prmt(v.z, v.w, 0x5410u);
-    qb[2 * i] = prmt(v.x, v.y, 0x7632u), qb[2 * i + 1] = prmt(v.z, v.w, 0x7632u);
+    sh.pairs[0][tid] = prmt(v0, v1, 0x5410u);
+    sh.pairs[1][tid] = prmt(v0, v1, 0x7632u);
   }
+  __syncthreads();
   constexpr int kStep = kWarpPages * kSelectWarps;
   for (int j0 = from + kWarpPages * warp; j0 < to; j0 += kStep) {
     const int next = lane < kWarpPages && j0 + kStep + lane < to ? table[j0 + kStep + lane] : 0;
@@ -352,21 +352,29 @@ __device__ __forceinline__ void score_pages(const SelectParams& p, int seg, int 
       lo[s] = *reinterpret_cast<const uint4*>(bd + kHeadDim + 16 * c);
       e[s] = (int)(signed char)bd[2 * kHeadDim];
     }
+    int sum[kWarpPages / 4];
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {  // upper bounds with A, lower ones with B
+      const uint4 w0 = *reinterpret_cast<const uint4*>(&sh.pairs[side][8 * c]);
+      const uint4 w1 = *reinterpret_cast<const uint4*>(&sh.pairs[side][8 * c + 4]);
+#pragma unroll
+      for (int s = 0; s < kWarpPages / 4; ++s) {
+        const uint4 x = side ? lo[s] : hi[s];
+        int v = side ? sum[s] : 0;
+        v = dp2_lo(w0.x, x.x, v), v = dp2_hi(w0.y, x.x, v);
+        v = dp2_lo(w0.z, x.y, v), v = dp2_hi(w0.w, x.y, v);
+        v = dp2_lo(w1.x, x.z, v), v = dp2_hi(w1.y, x.z, v);
+        v = dp2_lo(w1.z, x.w, v), v = dp2_hi(w1.w, x.w, v);
+        sum[s] = v;
+      }
+    }
     uint32_t key = 0;
 #pragma unroll
     for (int s = 0; s < kWarpPages / 4; ++s) {
-      int sum = 0;
-      sum = dp2_lo(qa[0], hi[s].x, sum), sum = dp2_hi(qa[1], hi[s].x, sum);
-      sum = dp2_lo(qa[2], hi[s].y, sum), sum = dp2_hi(qa[3], hi[s].y, sum);
-      sum = dp2_lo(qa[4], hi[s].z, sum), sum = dp2_hi(qa[5], hi[s].z, sum);
-      sum = dp2_lo(qa[6], hi[s].w, sum), sum = dp2_hi(qa[7], hi[s].w, sum);
-      sum = dp2_lo(qb[0], lo[s].x, sum), sum = dp2_hi(qb[1], lo[s].x, sum);
-      sum = dp2_lo(qb[2], lo[s].y, sum), sum = dp2_hi(qb[3], lo[s].y, sum);
-      sum = dp2_lo(qb[4], lo[s].z, sum), sum = dp2_hi(qb[5], lo[s].z, sum);
-      sum = dp2_lo(qb[6], lo[s].w, sum), sum = dp2_hi(qb[7], lo[s].w, sum);
+      int v = sum[s];
 #pragma unroll
-      for (int off = 1; off < 8; off <<= 1) sum += __shfl_xor_sync(kAll, sum, off);
-      const uint32_t k = e[s] == kNotFinite ? kKeyFirst : key_of((float)sum * pow2(max(e[s], -126)));
+      for (int off = 1; off < 8; off <<= 1) v += __shfl_xor_sync(kAll, v, off);
+      const uint32_t k = e[s] == kNotFinite ? kKeyFirst : key_of((float)v * pow2(max(e[s], -126)));
       const uint32_t got = __shfl_sync(kAll, k, (lane & 3) * 8);  // page 4 s + (lane & 3)
       if (lane >> 2 == s) key = got;
     }
@@ -442,7 +450,7 @@ __device__ __forceinline__ void take_pages(const SelectParams& p, int seg, int n
         if (k >= low && k <= high) atomicAdd(&sh.bins[(k - low) >> shift], 1);
       }
       __syncthreads();
-      // bins from the top: 8 to a thread, thread 0 the highest; left at zero for the next
+      // bins from the top: 4 to a thread, thread 0 the highest; left at zero for the next
       constexpr int kPer = kBins / kSelectThreads;
       int mine[kPer], sum = 0;
 #pragma unroll

@@ -155,8 +155,8 @@ struct BoundsParams {
 };
 
 // xqa_select. CTAs that fit an SM at once (its launch bounds) and pages that a CTA scores at
-// a time: 16 for each of its 8 warps.
-constexpr int kSelectCtas = 3, kSelectPages = 128;
+// a time: 16 for each of its 16 warps.
+constexpr int kSelectCtas = 2, kSelectPages = 256;
 struct SelectParams {
   const uint16_t* q;  // [B, Hq, 128] fp16
   const uint8_t* bounds;
