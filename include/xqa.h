@@ -497,7 +497,7 @@ typedef struct xqa_select_shape {
   int32_t num_kv_heads;       /* Hkv */
   int32_t head_dim;           /* D = 128 */
   int32_t block_size;         /* BS = 16 tokens per page */
-  int32_t max_blocks_per_seq; /* MBS: row length of block_tables */
+  int32_t max_blocks_per_seq; /* MBS: row length of block_tables (<= 2^24) */
   int32_t num_blocks;         /* NB: pages in the pool */
   int32_t max_pages;          /* K: row length of selected */
   int32_t first_pages;        /* a sequence's first pages that are always taken, >= 0 */

@@ -1162,10 +1162,11 @@ __global__ void __launch_bounds__(kExtendThreads, 1)
     sh.share = share;
     sh.extra = extra;
     sh.ctas = ctas;
+    p.split[blockIdx.x] = SplitUnit{0, 0, 0, 0, 0};  // until there is one (or the CTA gives up)
   }
   __syncthreads();
-  const float sc = (float)(p.qk_scale_base * (double)ks);
-  const bool bad_scale = !(sc > 0.f && sc < INFINITY);
+  const float sc = fmaxf((float)(p.qk_scale_base * (double)ks), 0x1p-126f);
+  const bool bad_scale = !(ks > 0.f && sc < INFINITY);
   if (bad_scale && works && threadIdx.x == 0) record_status(&sh.status, XQA_ERR_VALUE);
   int raw_issued = 0, q_issued = 0;
   if (aligned && works) {
@@ -1208,7 +1209,6 @@ __global__ void __launch_bounds__(kExtendThreads, 1)
   tc_fence_after();
   if (warp == 12) tmem_dealloc(sh.tmem, 512);
   if (threadIdx.x == 0) {
-    if (!works) p.split[blockIdx.x] = SplitUnit{0, 0, 0, 0, 0};
     if (sh.wait_limit == 0) record_status(&sh.status, XQA_ERR_DEVICE_TIMEOUT);
     p.status[blockIdx.x] = sh.status;
     if (blockIdx.x == 0) p.header[0] = gridDim.x;

@@ -537,7 +537,7 @@ xqa_status_t resolve_select(const xqa_select_shape_t* s, SelectResolved* r) {
   // int32 segments, table entries and selected pages
   const long long nseg = (long long)s->batch * s->num_kv_heads;
   if (nseg >= (1ll << 31) / s->max_blocks_per_seq || nseg >= (1ll << 31) / s->max_pages ||
-      nseg * r->group >= (1ll << 31) / kHeadDim || s->max_blocks_per_seq > (1 << 26))
+      nseg * r->group >= (1ll << 31) / kHeadDim || s->max_blocks_per_seq > (1 << 24))
     return XQA_ERR_SHAPE;
   r->ctas = s->max_ctas;
   if (r->ctas == 0) {

@@ -74,7 +74,7 @@ def test_choices_that_are_refused(lib):  # noqa: F811
     for bad in (dict(batch=0), dict(num_kv_heads=0), dict(num_q_heads=0), dict(num_q_heads=30), dict(num_q_heads=68),
                 dict(head_dim=64), dict(block_size=32), dict(max_blocks_per_seq=0), dict(num_blocks=0),
                 dict(max_pages=0), dict(first_pages=-1), dict(last_pages=0), dict(first_pages=19),
-                dict(first_pages=2**31 - 1), dict(max_ctas=-1), dict(batch=2**20, max_blocks_per_seq=2**10),
+                dict(first_pages=2**31 - 1), dict(max_ctas=-1), dict(batch=1, max_blocks_per_seq=2**24 + 1), dict(batch=2**20, max_blocks_per_seq=2**10),
                 dict(batch=2**20, max_pages=2**10)):
         s = xqa.XqaSelectShape(**{**SELECT, **bad})
         assert select(lib, s) == xqa.XQA_ERR_SHAPE, bad

@@ -267,3 +267,17 @@ def test_binding_refusals():
         with pytest.raises((ValueError, xqa.XqaError)):
             xqa.xqa_release_pages(**{**base, **bad})
     assert d["lens"].tolist() == [10, 16]
+
+
+def test_the_largest_batch():
+    """16384 sequences, the most that shared memory holds, with and without a cluster."""
+    batch = 16384
+    for extra, rows in ((0, 2000), (6000, 30000)):
+        g = np.random.default_rng(rows)
+        ctx = g.integers(0, 33, batch)
+        new = np.zeros(batch, np.int64)
+        new[g.integers(0, batch, 900 + extra)] = 2
+        pages = int(((ctx + new + 15) // 16).sum())
+        pool = Pool([int(x) for x in ctx], 3, pages + 5, seed=rows)
+        check_assign(pool, [int(x) for x in new], rows)
+        check_release(pool, [int(x) for x in g.integers(0, 2, batch)])
