@@ -244,11 +244,12 @@ struct TileOrder {
   }
 };
 
-// Page ids of a table row, read 32 at a time by a whole warp, one group ahead (tiles are
-// taken from the last to the first).
+// Page ids of a table row, read 32 at a time (four tiles) by a whole warp. Tiles are taken from
+// the last to the first, V's one or two behind K's: two groups are in use, the next is on its
+// way.
 struct PageIds {
   const int32_t* row;
-  int pages, group, cur, next;
+  int pages, group, high, low, next;
   __device__ __forceinline__ int read(int g) const {
     const int i = g * 32 + (threadIdx.x & 31);
     return g >= 0 && i < pages ? row[i] : -1;
@@ -257,17 +258,19 @@ struct PageIds {
     row = r;
     pages = n;
     group = tile >> 2;
-    cur = read(group);
-    next = read(group - 1);
+    high = read(group);
+    low = read(group - 1);
+    next = read(group - 2);
   }
-  // id of page `lane & 7` of a tile (the same or a lower one than before)
-  __device__ __forceinline__ int of(int tile) {
-    if (tile >> 2 != group) {
-      group = tile >> 2;
-      cur = next;
-      next = read(group - 1);
+  // id of page `lane & 7` of a tile; top: V's next tile, the highest still to come
+  __device__ __forceinline__ int of(int tile, int top) {
+    if (top >> 2 != group) {
+      group = top >> 2;
+      high = low;
+      low = next;
+      next = read(group - 2);
     }
-    return __shfl_sync(kAll, cur, (tile & 3) * 8 + (threadIdx.x & 7));
+    return __shfl_sync(kAll, tile >> 2 == group ? high : low, (tile & 3) * 8 + (threadIdx.x & 7));
   }
 };
 
@@ -296,12 +299,14 @@ __device__ __forceinline__ bool load_tiles(const Ctx& c, const Unit& w, const CU
   const TileOrder order(w);
   const int pages = (w.len_k + kBlockSize - 1) / kBlockSize;
   const bool nhd = kFmt != XQA_KV_E2M1 && p.kv_layout == XQA_LAYOUT_NHD;
-  PageIds k_ids, v_ids;
-  k_ids.start(p.block_tables + (size_t)w.seq * p.max_blocks_per_seq + w.page0, pages, order.n - 1);
-  v_ids = k_ids;
+  PageIds ids;
+  ids.start(p.block_tables + (size_t)w.seq * p.max_blocks_per_seq + w.page0, pages, order.n - 1);
   const int q_tiles = w.split ? 1 : 2;
   if (lane < 2 * q_tiles && w.n[lane >> 1] > 0)  // into L2 while the unit before still uses Q's place
     tma_prefetch_4d(tm_q, 64 * (lane & 1), 0, w.head, w.q_row + (lane >> 1) * p.tile_tokens);
+  // (few instructions: one warp's, one after the other, are what a tile waits for)
+  int jk = order.n - 1, jv = order.n - 1, st = item % kStages;
+  uint32_t parity = (item / kStages - 1) & 1;  // (the phase before a ring's first is over)
   for (int t = 0; t < 2 * order.n; ++t) {
     // Q behind the first tiles, which so are on their way while the unit before ends (Q first:
     // 10 to 24 us more a unit). The rings have room for them and more: no tile behind waits
@@ -325,33 +330,43 @@ __device__ __forceinline__ bool load_tiles(const Ctx& c, const Unit& w, const CU
       __syncwarp();
       ++q_issued;
     }
-    bool is_v;
-    const int j = order.at(t, is_v);
-    const int it = item + t, st = it % kStages;
-    const int id = is_v ? v_ids.of(j) : k_ids.of(j);  // page `lane & 7` of the tile
+    const bool is_v = jk < 0 || (t >= order.lag && !((t - order.lag) & 1));
+    const int j = is_v ? jv : jk;
+    const int id = ids.of(j, jv);  // page `lane & 7` of the tile
+    jv -= is_v;
+    jk -= !is_v;
     const bool want = lane < kTilePages && j * kTilePages + lane < pages;
     const bool good = want && (uint32_t)id < (uint32_t)p.num_blocks;
-    const uint32_t some = __ballot_sync(kAll, good), none = __ballot_sync(kAll, want && !good);
-    if (it >= kStages && !c.wait(&sh.raw_empty[st], (it / kStages - 1) & 1)) return false;
-    issued = it + 1;
-    if (lane == 0) {
-      sh.bad_pages[st] = none;
-      if (none) record_status(&sh.status, XQA_ERR_BAD_BLOCK_ID);
-      mbar_arrive_expect_tx(&sh.raw_full[st], (nhd ? __popc(some) : kTilePages) * kSlice);
-    }
-    __syncwarp();
+    const uint32_t none = __ballot_sync(kAll, want && !good);
+    uint64_t* full = &sh.raw_full[st];
     uint8_t* dst = c.raw + st * Raw<kFmt>::kBytes + lane * kSlice;
     const CUtensorMap* tm = is_v ? tm_v : tm_k;
     if (nhd) {
-      if (good) tma_load_kv(dst, tm, &sh.raw_full[st], 0, w.head, id * kBlockSize);
+      const uint32_t bytes = __popc(__ballot_sync(kAll, good)) * kSlice;
+      if (!c.wait(&sh.raw_empty[st], parity)) return false;
+      if (lane == 0) {
+        sh.bad_pages[st] = none;
+        mbar_arrive_expect_tx(full, bytes);
+      }
+      __syncwarp();
+      if (good) tma_load_kv(dst, tm, full, 0, w.head, id * kBlockSize);
     } else {
       // slices are rows of one matrix: four at a time. In place of pages that are not there or
       // not good, the pool's first: their tokens are hidden or replaced
       const int row = good ? id * p.num_kv_heads + w.head : w.head;
       const int r1 = __shfl_down_sync(kAll, row, 1), r2 = __shfl_down_sync(kAll, row, 2);
       const int r3 = __shfl_down_sync(kAll, row, 3);
-      if (lane == 0 || lane == 4) tma_gather4(dst, tm, &sh.raw_full[st], row, r1, r2, r3);
+      if (!c.wait(&sh.raw_empty[st], parity)) return false;
+      if (lane == 0) {
+        sh.bad_pages[st] = none;
+        mbar_arrive_expect_tx(full, kTilePages * kSlice);
+      }
+      __syncwarp();
+      if (lane == 0 || lane == 4) tma_gather4(dst, tm, full, row, r1, r2, r3);
     }
+    if (none) record_status(&sh.status, XQA_ERR_BAD_BLOCK_ID);
+    issued = item + t + 1;
+    if (++st == kStages) st = 0, parity ^= 1;
     __syncwarp();
   }
   return true;
@@ -1162,7 +1177,6 @@ __global__ void __launch_bounds__(kExtendThreads, 1)
     sh.share = share;
     sh.extra = extra;
     sh.ctas = ctas;
-    p.split[blockIdx.x] = SplitUnit{0, 0, 0, 0, 0};  // until there is one (or the CTA gives up)
   }
   __syncthreads();
   const float sc = fmaxf((float)(p.qk_scale_base * (double)ks), 0x1p-126f);
@@ -1209,6 +1223,9 @@ __global__ void __launch_bounds__(kExtendThreads, 1)
   tc_fence_after();
   if (warp == 12) tmem_dealloc(sh.tmem, 512);
   if (threadIdx.x == 0) {
+    // no unit to join if the CTA had none or gave up. (Cleared at the start, in front of the
+    // roles, the same store cost 10 % of long chunks: 4 chunks 655 us, 719 so.)
+    if (!works || !aligned || sh.wait_limit == 0) p.split[blockIdx.x] = SplitUnit{0, 0, 0, 0, 0};
     if (sh.wait_limit == 0) record_status(&sh.status, XQA_ERR_DEVICE_TIMEOUT);
     p.status[blockIdx.x] = sh.status;
     if (blockIdx.x == 0) p.header[0] = gridDim.x;
