@@ -151,32 +151,35 @@ __device__ __forceinline__ int find_segment(const int32_t* seg_start, int lo, in
 // TMA coordinates of 32 consecutive owned pages of one warp, one per lane.
 struct PageBatch {
   int y;    // HND: row of the (page, kv head) slice; NHD: first token row of the page
-  int bad;  // block id outside [0, NB)
-  int seg;  // segment of the page
+  int tag;  // bit 0: block id outside [0, NB); above it the kv head within the cache
 };
 
-// Head of segment s within the cache. (Tables of a kv head's own, xqa_decode_selected, make
-// each (sequence, kv head) a sequence of one head; the cache has cache_heads all the same.)
-__device__ __forceinline__ int cache_head(const PartialParams& p, int s) {
-  return s - s / p.cache_heads * p.cache_heads;
+// Row of block_tables of segment s, and its head within the cache. (Tables of a kv head's own,
+// xqa_decode_selected, make each (sequence, kv head) a sequence of one head; the cache has
+// cache_heads all the same. One division serves both: a second one cost 1 % of a step.)
+__device__ __forceinline__ int table_row(const PartialParams& p, int s, int& head) {
+  const int b = s / p.cache_heads;
+  head = s - b * p.cache_heads;
+  return b * p.seq_rows + head * p.head_rows;
 }
 
 template <int kWarps>
 __device__ __forceinline__ PageBatch load_batch(const PartialParams& p, const int32_t* segs,
                                                 int s_first, int nseg, int cbeg, int npages,
                                                 int warp, int base, int lane) {
-  PageBatch r{0, 0, s_first};
+  PageBatch r{0, 0};
   const int q = warp + kWarps * (base + lane);
   if (q < npages) {
     const int pg = cbeg + q;
     const int s = find_segment(segs, s_first, nseg, pg);
     if (base == 0) stamp_after(15, s);
-    const int b = s / p.num_kv_heads, kvh = cache_head(p, s);
+    int kvh;
+    const int row = table_row(p, s, kvh);
     const int j = pg - segs[s];
-    const int id = p.block_tables[(size_t)b * p.max_blocks_per_seq + j];
-    r.bad = (id < 0 || id >= p.num_blocks) ? 1 : 0;
-    r.y = r.bad ? 0 : (p.kv_layout == XQA_LAYOUT_HND ? (id * p.cache_heads + kvh) : id) * kBlockSize;
-    r.seg = s;
+    const int id = p.block_tables[(size_t)row * p.max_blocks_per_seq + j];
+    const int bad = (id < 0 || id >= p.num_blocks) ? 1 : 0;
+    r.tag = bad | kvh << 1;
+    r.y = bad ? 0 : (p.kv_layout == XQA_LAYOUT_HND ? (id * p.cache_heads + kvh) : id) * kBlockSize;
   }
   return r;
 }
@@ -968,9 +971,10 @@ __device__ __forceinline__ void piece_owners(Sh& sh, const RangeView& rv) {
 template <class G>
 __device__ __forceinline__ void issue_page(const PartialParams& p, const CUtensorMap* tm_k,
                                            const CUtensorMap* tm_v, CtaShared<G>& sh,
-                                           uint8_t* stages, int slot, int y, int bad, int sg,
+                                           uint8_t* stages, int slot, int y, int tag,
                                            uint64_t policy) {
   uint8_t* st = stages + slot * G::kStage;
+  const int bad = tag & 1;
   sh.stage_bad[slot] = bad;
   fence_proxy_async_smem();  // this slot's earlier shared reads come before the TMA writes
   if (bad) {
@@ -982,7 +986,7 @@ __device__ __forceinline__ void issue_page(const PartialParams& p, const CUtenso
       tma_load_2d(st, tm_k, &sh.full_bar[slot], 0, y, policy);
       tma_load_2d(st + kPageBytes, tm_v, &sh.full_bar[slot], 0, y, policy);
     } else {  // NHD: box (128 dims, 1 kv head, 16 tokens) at (0, kvh, page*16)
-      const int kvh = cache_head(p, sg);
+      const int kvh = tag >> 1;
       tma_load_3d(st, tm_k, &sh.full_bar[slot], 0, kvh, y, policy);
       tma_load_3d(st + kPageBytes, tm_v, &sh.full_bar[slot], 0, kvh, y, policy);
     }
@@ -1264,8 +1268,8 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
   if (p.hints != nullptr && lane < 2 && (kWarps <= kHintPages / 2 || warp < kHintPages / 2)) {
     const int row = p.kv_layout == XQA_LAYOUT_HND
                         ? cur.y
-                        : (cur.y / kBlockSize * p.cache_heads + cache_head(p, cur.seg)) * kBlockSize;
-    p.hints[(size_t)blockIdx.x * kHintPages + 2 * warp + lane] = lane < owned && !cur.bad ? row : -1;
+                        : (cur.y / kBlockSize * p.cache_heads + (cur.tag >> 1)) * kBlockSize;
+    p.hints[(size_t)blockIdx.x * kHintPages + 2 * warp + lane] = lane < owned && !(cur.tag & 1) ? row : -1;
   }
   int cur_base = 0;
   WarpRing ring{0, 0, 0, 0};  // 4 bits only
@@ -1277,7 +1281,7 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
       cur_base += 32;
       nxt = load_batch<kWarps>(p, segs, s_first, s_hi + 1, cbeg, npages, warp, cur_base + 32, lane);
     }
-    return __shfl_sync(kFull, cur.bad ? -1 : cur.y / kBlockSize, k - cur_base);
+    return __shfl_sync(kFull, cur.tag & 1 ? -1 : cur.y / kBlockSize, k - cur_base);
   };
   auto issue_next = [&]() {
     if constexpr (G::kFour) {
@@ -1293,11 +1297,10 @@ __device__ __forceinline__ void cta_mode_range(const PartialParams& p, const CUt
       nxt = load_batch<kWarps>(p, segs, s_first, s_hi + 1, cbeg, npages, warp, cur_base + 32, lane);
     }
     const int y = __shfl_sync(kFull, cur.y, k - cur_base);
-    const int bad = __shfl_sync(kFull, cur.bad, k - cur_base);
-    const int sg = __shfl_sync(kFull, cur.seg, k - cur_base);
+    const int tag = __shfl_sync(kFull, cur.tag, k - cur_base);
     const int slot = (warp + kWarps * k) % kStages;
     __syncwarp();  // all lanes' reads of this slot's previous page are done
-    if (lane == 0) issue_page<G>(p, tm_k, tm_v, sh, sm.stages, slot, y, bad, sg, policy);
+    if (lane == 0) issue_page<G>(p, tm_k, tm_v, sh, sm.stages, slot, y, tag, policy);
     __syncwarp();
   };
 #pragma unroll 1
@@ -1842,18 +1845,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       return j;
     };
     auto fetch = [&](int j) {
-      PageBatch r{0, 0, 0};
+      PageBatch r{0, 0};
       if (j < nsr) {
         int pb, len;
         part(j, pb, len);
         const int sg = s_first + j;
-        r.seg = sg;
         if (lane < len) {
-          const int bb = sg / p.num_kv_heads, kvh = cache_head(p, sg);
+          int kvh;
+          const int row = table_row(p, sg, kvh);
           const int id =
-              p.block_tables[(size_t)bb * p.max_blocks_per_seq + (pb + lane - segs[sg])];
-          r.bad = (id < 0 || id >= p.num_blocks) ? 1 : 0;
-          r.y = r.bad ? 0
+              p.block_tables[(size_t)row * p.max_blocks_per_seq + (pb + lane - segs[sg])];
+          const int bad = (id < 0 || id >= p.num_blocks) ? 1 : 0;
+          r.tag = bad | kvh << 1;
+          r.y = bad ? 0
                       : (p.kv_layout == XQA_LAYOUT_HND ? (id * p.cache_heads + kvh) : id) * kBlockSize;
         }
       }
@@ -1869,7 +1873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         part(ij, pb, len);
         if (ioff < len) {
           ++issued;
-          return __shfl_sync(kFull, wcur.bad ? -1 : wcur.y / kBlockSize, ioff++);
+          return __shfl_sync(kFull, wcur.tag & 1 ? -1 : wcur.y / kBlockSize, ioff++);
         }
         ij = ij_next;
         ioff = 0;
@@ -1890,12 +1894,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         part(ij, pb, len);
         if (ioff < len) {
           const int y = __shfl_sync(kFull, wcur.y, ioff);
-          const int bad = __shfl_sync(kFull, wcur.bad, ioff);
+          const int tag = __shfl_sync(kFull, wcur.tag, ioff);
           ++ioff;
           const int k = issued++;
           const int slot = (warp + kWarps * k) % kStages;
           __syncwarp();  // all lanes' reads of this slot's previous page are done
-          if (lane == 0) issue_page<G>(p, &tm_k, &tm_v, sh, sm.stages, slot, y, bad, wcur.seg, policy);
+          if (lane == 0) issue_page<G>(p, &tm_k, &tm_v, sh, sm.stages, slot, y, tag, policy);
           __syncwarp();
           return;
         }

@@ -256,6 +256,8 @@ xqa_status_t attend_partial_impl(const void* q, const uint8_t* k_cache, const ui
   p.num_q_heads = per_head ? r.group : r.hq;
   p.num_kv_heads = per_head ? 1 : r.hkv;
   p.cache_heads = r.hkv;
+  p.seq_rows = per_head ? r.hkv : 1;
+  p.head_rows = per_head ? 1 : 0;
   p.group = r.group;
   p.max_blocks_per_seq = r.mbs;
   p.num_blocks = r.nb;

@@ -23,6 +23,8 @@ struct PartialParams {
   int batch, num_q_heads, num_kv_heads, group, max_blocks_per_seq, num_blocks;
   int cache_heads;           // kv heads of the cache (num_kv_heads, unless every kv head has
                              // a table of its own: then num_kv_heads is 1)
+  int seq_rows, head_rows;   // rows of block_tables from a sequence and from a kv head to the
+                             // next: 1 and 0, unless every kv head has its own
   int q_len;                 // new tokens per sequence (q, out: [B, q_len, Hq, D])
   int n_max, min_pages;      // split rule inputs (same values the planner got)
   int fused_merge;           // 1: the last CTA of a split segment merges it
