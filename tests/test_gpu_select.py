@@ -72,7 +72,7 @@ def test_bounds(new, ctx, kv_dtype, kv_layout):
 
 
 def test_bounds_of_many_rows():
-    new = [2100, 1, 1900, 700]  # more than 4096 rows: sixteen to a warp
+    new = [2100, 1, 1900, 700]  # more than 4096 rows: a warp takes more of them
     ctx = [2100, 2000, 1907, 715]
     c = Cache(ctx, 2, "e4m3", "nhd", seed=1)
     got, before = bounds_of(c, new)
@@ -218,6 +218,17 @@ def test_ties_go_to_the_lower_page():
     s.check(123, 1, 1)
     s.q.zero_()
     s.check(17, 1, 2)
+
+
+def test_ties_over_the_longest_table():
+    # every lane of the CTA that chooses counts 2^15 equal keys
+    mbs, nb = 1 << 24, 7
+    bounds = torch.zeros((nb, 1, 272), dtype=torch.uint8, device="cuda")
+    table = (torch.arange(mbs, device="cuda") % nb).to(torch.int32).reshape(1, mbs)
+    q = torch.ones((1, 1, 128), dtype=torch.float16, device="cuda")
+    selected, lens = xqa.xqa_select(q, bounds, table, i32([16 * mbs]), 6, 1, 2)
+    assert selected[0, 0].tolist() == [0, 1, 2, 3, (mbs - 2) % nb, (mbs - 1) % nb]
+    assert lens.tolist() == [[96]]
 
 
 def test_large_and_odd_queries_and_bounds():
