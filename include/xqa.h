@@ -437,11 +437,12 @@ typedef struct xqa_pages {
  *   device_status device int32 or NULL: receives the first of these errors if it holds
  *                 XQA_OK. A sequence that meets one gains nothing in this call, the others
  *                 do: XQA_ERR_CTX_TOO_LONG (a negative number or length, or more than MBS *
- *                 16 tokens), XQA_ERR_BAD_OFFSETS (its rows would pass num_rows; so would
- *                 every later one's with new tokens), XQA_ERR_NO_PAGES (the stack has too few
- *                 pages for it and those before it; later ones that need no page are
- *                 served). XQA_ERR_BAD_BLOCK_ID: a page outside [0, NB) in the stack or the
- *                 table; entries are written as they are, slots as -1
+ *                 16 tokens), XQA_ERR_BAD_OFFSETS (its rows, behind those of every
+ *                 sequence before it, would pass num_rows; so would every later one's),
+ *                 XQA_ERR_NO_PAGES (the stack has too few pages for it and those before it;
+ *                 later ones that need no page are served). XQA_ERR_BAD_BLOCK_ID: a page
+ *                 outside [0, NB) in the stack or the table; entries are written as they
+ *                 are, slots as -1
  *
  * What the next calls take: block_tables and new_lens as context_lens for all of them,
  * cu_seqlens for xqa_append, xqa_page_bounds and xqa_extend. One kernel, no host

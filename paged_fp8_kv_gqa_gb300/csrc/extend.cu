@@ -17,7 +17,7 @@
 // anywhere, at 128-key tiles, without the host knowing a length. A unit cut into pieces
 // leaves (O, m, l) of each in 32 bits in the workspace, and a second, small kernel joins
 // them with the whole GPU. (Joined by the CTA that wrote a unit's last piece, 32 tokens over
-// 131072 took 1340 us, 16 x 32 over 2048 85 us.)
+// 131072 took 1340 us, 16 x 32 over 2048 85 us; so 33 and 37 us.)
 //
 // A unit of at most T tokens fills one row tile only; both chains of product, softmax
 // and product then work on it, on every other key tile each, and are joined in the
@@ -26,6 +26,12 @@
 // Warps: 0-3 and 4-7 softmax of chain 0 and 1 (a thread owns a row), 8-11 epilogue, 12
 // tensor core, 13 units and loads, 14-19 codes to 16-bit values. TMEM: S0, S1 (P over
 // them), O0, O1: 4 x 128 columns.
+//
+// Bound by the chain of product, softmax and product where units have two row tiles (4 chunks
+// of 1024-2048 tokens up to contexts of 6000-16384, 32/4 heads, E5M2: 649 us, 0.79 of the
+// library product's rate for the visible pairs), by one row tile's softmax and the tiles'
+// conversion where they have one (16 x 2-32 tokens over 4000-17000, 32/4, E4M3: 77 us, 168 MB,
+// 0.32 of the copy rate), by its latencies if it is short (5 tokens over 128: 9.8 us).
 //
 // Hidden values do not leak: see prompt attention; here rows past the sequence and values
 // that are not finite are zeroed as they are converted. A page whose table entry is out of
@@ -112,7 +118,7 @@ static_assert(kExtendSmem <= 227 * 1024, "shared memory budget");
 // ---- the line of work ----
 // A sequence of n tokens: np = ceil(n / 2T) units for each kv head; unit i sees base +
 // min(step (i + 1), rows) keys at most, and is kKeyCost long for each of them, or kKeyCostOne if
-// it fills one row tile only (a 128-key tile takes 1.6 and 0.9 us), and kUnitCost more for its
+// it fills one row tile only (a 128-key tile takes 1.6 and 1.05 us), and kUnitCost more for its
 // start and end.
 constexpr int kKeyCost = 16, kKeyCostOne = 10, kUnitCost = 256 * kKeyCost;
 constexpr int kCutTiles = 8;  // units of fewer tiles are not cut

@@ -17,7 +17,8 @@
 // of the stack's height and the first write, so the new ones may take their place.
 //
 // Bound by latency: three dependent reads and two block-wide scans. The work itself is 12
-// bytes a row and 8 a page.
+// bytes a row and 8 a page. Measured: a step of 16 tokens 3.5 us; 512 sequences of 0-512 new tokens
+// 7.5 us; 2 of 16 sequences released 5.2 us, 200 of 512 7.7 us.
 #include <cooperative_groups.h>
 
 #include "xqa_device.cuh"
@@ -342,8 +343,8 @@ cudaLaunchConfig_t config(int ctas, int threads, size_t smem, cudaStream_t strea
 }  // namespace
 
 // A small CTA where one round of it takes every sequence and row, a large one where it has few
-// rows or pages to write, else the cluster. Step of 16 tokens: 4.7 us in 256 threads, 6.4 in
-// 1024 (a barrier of 32 warps at each turn).
+// rows or pages to write, else the cluster. When this was chosen a step of 16 tokens took 4.7 us
+// in 256 threads, 6.4 in 1024 (a barrier of 32 warps at each turn); 3.5 us now.
 cudaError_t launch_assign(const PagesParams& p, cudaStream_t stream) {
   const bool small = p.batch <= kSmallThreads && p.num_rows <= 4 * kSmallThreads;
   const int ctas = p.num_rows <= 4 * kLargeThreads ? 1 : kClusterCtas;
