@@ -694,6 +694,30 @@ __device__ __forceinline__ void convert16(const Codes16<kFmt>& c, uint32_t (&o)[
   }
 }
 
+// Whether one of 16 values is an infinity or NaN (0: none).
+template <int kFmt>
+__device__ __forceinline__ uint32_t not_finite16(const Codes16<kFmt>& c) {
+  if constexpr (kFmt == XQA_KV_E2M1) {
+    return (c.s8 & 0x7fu) == 0x7fu;
+  } else {  // a byte's largest exponent, or E4M3's one pattern, is the one that carries
+    constexpr uint32_t top = kFmt == XQA_KV_E5M2 ? 0x7c7c7c7cu : 0x7f7f7f7fu;
+    constexpr uint32_t one = 0x80808080u - top;
+    return (((c.w.x & top) + one) | ((c.w.y & top) + one) | ((c.w.z & top) + one) |
+            ((c.w.w & top) + one)) & 0x80808080u;
+  }
+}
+
+template <int kFmt>
+__device__ __forceinline__ void clear16(uint8_t* raw, int row, int group) {
+  if constexpr (kFmt == XQA_KV_E2M1) {
+    uint8_t* page = raw + (row >> 4) * kSliceBytes4;
+    *reinterpret_cast<uint2*>(page + (row & 15) * (kHeadDim / 2) + 8 * group) = make_uint2(0, 0);
+    page[kCodeBytes4 + (row & 15) * (kHeadDim / kGroup4) + group] = 0;
+  } else {
+    *reinterpret_cast<uint4*>(raw + row * kHeadDim + 16 * group) = make_uint4(0, 0, 0, 0);
+  }
+}
+
 template <int kFmt, int kType>
 __device__ __forceinline__ void convert_role(const Ctx& c) {
   Shared& sh = c.sh;
@@ -717,7 +741,7 @@ __device__ __forceinline__ void convert_role(const Ctx& c) {
       const int rs = item % kStages, st = item % kKvStages;
       if (!c.wait(&sh.raw_full[rs], (item / kStages) & 1)) return;
       if (item >= kKvStages && !c.wait(&sh.kv_empty[st], (item / kKvStages - 1) & 1)) return;
-      const uint8_t* raw = c.raw + rs * Raw<kFmt>::kBytes;
+      uint8_t* raw = c.raw + rs * Raw<kFmt>::kBytes;
       uint8_t* dst = c.kv(st) + half * kHalfBytes;
       const int bad = *(volatile int*)&sh.bad_pages[rs];
       const bool masked = is_v && (j + 1) * kTile > u.hidden;
@@ -731,8 +755,17 @@ __device__ __forceinline__ void convert_role(const Ctx& c) {
         *reinterpret_cast<uint4*>(dst + row * 128 + swz0) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(dst + row * 128 + swz1) = make_uint4(o[4], o[5], o[6], o[7]);
       };
-      if (masked || bad) {
-        const int past = u.len_k - j * kTile, from = u.hidden - j * kTile;
+      const int past = u.len_k - j * kTile, from = u.hidden - j * kTile;
+      uint32_t odd = bad;  // pages that are not there, hidden values that are not finite
+      if (masked && !bad) {  // tokens behind the last one become zeros where they lie
+#pragma unroll 1
+        for (int row = row0; row < kTile; row += kStep) {
+          if (row >= past) clear16<kFmt>(raw, row, group);
+          else if (row >= from) odd |= not_finite16<kFmt>(read16<kFmt>(raw, row, group));
+        }
+        odd = __any_sync(kAll, odd);
+      }
+      if (odd) {
 #pragma unroll 1
         for (int row = row0; row < kTile; row += kStep) {
           uint32_t o[8];
