@@ -117,10 +117,9 @@ static_assert(kExtendSmem <= 227 * 1024, "shared memory budget");
 
 // ---- the line of work ----
 // A sequence of n tokens: np = ceil(n / 2T) units for each kv head; unit i sees base +
-// min(step (i + 1), rows) keys at most, and is kKeyCost long for each of them, or kKeyCostOne if
-// it fills one row tile only (a 128-key tile takes 1.6 and 1.05 us), and kUnitCost more for its
-// start and end.
-constexpr int kKeyCost = 16, kKeyCostOne = 10, kUnitCost = 256 * kKeyCost;
+// min(step (i + 1), rows) keys at most, and is kKeyCost long for each of them, or key_cost_one if
+// it fills one row tile only, and kUnitCost more for its start and end.
+constexpr int kKeyCost = 16, kUnitCost = 256 * kKeyCost;
 constexpr int kCutTiles = 8;  // units of fewer tiles are not cut
 struct Cost {
   int np;
@@ -160,7 +159,7 @@ __device__ __forceinline__ Cost seq_cost(const ExtendParams& p, const Seq& s) {
   c.base = causal ? max(0, s.ctx - s.n) : max(0, s.ctx);
   c.step = causal ? per : 0;
   c.rows = causal ? s.n : 0;
-  c.last_key = s.n - (c.np - 1) * per <= p.tile_tokens ? kKeyCostOne : kKeyCost;
+  c.last_key = s.n - (c.np - 1) * per <= p.tile_tokens ? p.key_cost_one : kKeyCost;
   return c;
 }
 
@@ -455,14 +454,19 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
     bool some = true;  // there is a tile for this CTA
     if (x0 > 0 || x1 < len) {
       // Tile at which a cut at position x of the unit falls. A short unit is not cut, and no
-      // end of less than a quarter of a CTA's share (four tiles at most) is cut off: leaving
-      // a piece and joining it costs about as much. Such a cut moves to the unit's end.
+      // end of less than a quarter of a CTA's share (and of what a unit's start and end cost) is
+      // cut off: leaving a piece and joining it costs about as much. Such a cut moves to the
+      // unit's end. (Four tiles of two row tiles: 16 short turns 77.4 us, so 74.2.)
       const bool full = cost.key(pair) == kKeyCost;  // (divisors known to the compiler)
-      constexpr int kTileCost = kTile * kKeyCost, kTileCostOne = kTile * kKeyCostOne;
-      auto in_tiles = [&](long long x) { return full ? x / kTileCost : x / kTileCostOne; };
-      const int least = (int)min(4ll, max(1ll, in_tiles(share >> 2)));
+      const int cost_one = p.key_cost_one;
+      auto in_tiles = [&](long long x) {
+        return full                       ? x / (kTile * kKeyCost)
+               : cost_one == kKeyCostOne ? x / (kTile * kKeyCostOne)
+                                         : x / (kTile * kKeyCostOneSlow);
+      };
+      const int least = (int)min(full ? 2ll : 4ll, max(1ll, in_tiles(share >> 2)));
       auto tile_of = [&](long long x) {
-        const long long y = x - kUnitCost + (full ? kTileCost : kTileCostOne) / 2;
+        const long long y = x - kUnitCost + kTile / 2 * cost.key(pair);
         const int at = (int)min((long long)tiles, in_tiles(max(0ll, y)));
         if (tiles < kCutTiles) return 2 * at < tiles ? 0 : tiles;
         return at < least ? 0 : tiles - at < least ? tiles : at;

@@ -861,6 +861,13 @@ xqa_status_t xqa_extend(const void* q, const uint8_t* k_cache, const uint8_t* v_
   p.kv_dtype = shape->kv_dtype;
   p.kv_layout = shape->kv_layout;
   p.tile_tokens = tokens;
+  // A 128-key tile of one row tile and of two, us (32/4 and 24/8 heads): 1.01 and 1.56 of 8 bits as
+  // fp16, 1.16 and 1.72 as bf16 (a longer conversion); token-major 1.22 and 1.56, 1.28 and 1.74
+  // (eight copies a tile in place of two); of 4 bits 1.10 and 1.70, 1.41 and 1.83. So 12 or 10 of
+  // 16: with 10 for all, 16 short turns over 4000-17000 (bf16, E4M3 NHD) took 77.9 us, not 74.2.
+  const bool slow = shape->kv_layout == XQA_LAYOUT_NHD ||
+                    (shape->dtype == XQA_BF16 && shape->kv_dtype == XQA_KV_E2M1);
+  p.key_cost_one = slow ? xqa::kKeyCostOneSlow : xqa::kKeyCostOne;
   p.qk_scale_base = (double)r.sm_scale * 1.4426950408889634;
   p.k_scale = k_scale;
   p.v_scale = v_scale;

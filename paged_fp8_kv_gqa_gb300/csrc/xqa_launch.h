@@ -101,6 +101,10 @@ struct SplitUnit {
   int pieces, q_row, tokens, head, bad;
 };
 
+// Length of a key of a one-row-tile unit on chunk attention's line of work, where one of two row
+// tiles is 16.
+constexpr int kKeyCostOne = 10, kKeyCostOneSlow = 12;
+
 struct ExtendParams {
   const int32_t* cu_q;  // [batch + 1]
   const int32_t* context_lens;
@@ -117,6 +121,7 @@ struct ExtendParams {
   int batch, num_q_heads, num_kv_heads, group, total_q, causal;
   int max_blocks_per_seq, num_blocks, kv_dtype, kv_layout;
   int tile_tokens;    // T: tokens of a 128-row tile
+  int key_cost_one;   // of a key of a unit of one row tile (kKeyCostOne or kKeyCostOneSlow)
   double qk_scale_base;      // sm_scale * log2(e); the logit scale is this * k_scale
   float k_scale, v_scale;    // per-tensor scales (used when the pointers are null)
   const float* k_scale_ptr;
