@@ -17,7 +17,7 @@
 // anywhere, at 128-key tiles, without the host knowing a length. A unit cut into pieces
 // leaves (O, m, l) of each in 32 bits in the workspace, and a second, small kernel joins
 // them with the whole GPU. (Joined by the CTA that wrote a unit's last piece, 32 tokens over
-// 131072 took 1340 us, 16 x 32 over 2048 85 us; so 33 and 37 us.)
+// 131072 took 1340 us, 16 x 32 over 2048 85 us; so 29 and 35 us.)
 //
 // A unit of at most T tokens fills one row tile only; both chains of product, softmax
 // and product then work on it, on every other key tile each, and are joined in the
@@ -28,10 +28,10 @@
 // them), O0, O1: 4 x 128 columns.
 //
 // Bound by the chain of product, softmax and product where units have two row tiles (4 chunks
-// of 1024-2048 tokens up to contexts of 6000-16384, 32/4 heads, E5M2: 649 us, 0.79 of the
+// of 1024-2048 tokens up to contexts of 6000-16384, 32/4 heads, E5M2: 642 us, 0.80 of the
 // library product's rate for the visible pairs), by one row tile's softmax and the tiles'
-// conversion where they have one (16 x 2-32 tokens over 4000-17000, 32/4, E4M3: 77 us, 168 MB,
-// 0.32 of the copy rate), by its latencies if it is short (5 tokens over 128: 9.8 us).
+// conversion where they have one (16 x 2-32 tokens over 4000-17000, 32/4, E4M3: 72 us, 168 MB,
+// 0.34 of the copy rate), by its latencies if it is short (5 tokens over 128: 9.0 us).
 //
 // Hidden values do not leak: see prompt attention; here rows past the sequence and values
 // that are not finite are zeroed as they are converted. A page whose table entry is out of
@@ -1276,26 +1276,30 @@ __global__ void __launch_bounds__(kExtendThreads, 1)
 }
 
 // ---- the join of split units' pieces ----
-// A team of 16 lanes has a row, 8 dims a lane. The pieces' (m, l) are read a piece a lane,
-// which so weighs its piece for all; then each piece costs eight fused products a lane. Up to
+// A team of 8 lanes has a row, 16 dims a lane. The pieces' (m, l) are read a piece a lane,
+// which so weighs its piece for all; then each piece costs sixteen fused products a lane. Up to
 // kTeamPieces pieces are one team's work; of more, the block's teams take equal runs, each with
 // its own maximum, and join through shared memory. The kernel is a chain of memory round
-// trips: the units, (m, l) and O at once, out.
-constexpr int kJoinThreads = 256, kTeams = kJoinThreads / 16, kTeamPieces = 8;
-constexpr int kJoinBlocks = 4;  // for each CTA of the kernel before: what an SM holds at once
+// trips (the units, (m, l) and O at once, out) and the instructions that are a row's whatever
+// its team: teams of 16 lanes in four blocks an SM (64 registers) took 17 us of 4 chunks, so 10.
+constexpr int kTeamLanes = 8, kTeamVec = kHeadDim / 4 / kTeamLanes;
+constexpr int kJoinThreads = 256, kTeams = kJoinThreads / kTeamLanes, kTeamPieces = 8;
+constexpr int kJoinBlocks = 2;  // for each CTA of the kernel before: what an SM holds at once
+static_assert(kTeams == 32, "parts of a row: one a lane");
 
-// Weights of up to 16 parts of a row, one a lane (l = 0: a part without keys, whose O was not
+// Weights of parts of a row, one a lane of kLanes (l = 0: a part without keys, whose O was not
 // written); m and l become the whole's. A part with keys keeps the least weight there is: its
 // infinities and NaN are the row's.
+template <int kLanes>
 __device__ __forceinline__ float weigh(float& m, float& l) {
   const bool some = l != 0.f;
   float top = some ? m : -INFINITY;
 #pragma unroll
-  for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+  for (int off = kLanes / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
   const float w = some ? fmaxf(ex2(m - top), 0x1p-149f) : 0.f;
   float sum = some ? w * l : 0.f;
 #pragma unroll
-  for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
+  for (int off = kLanes / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
   m = top;
   l = sum;
   return w;
@@ -1312,12 +1316,13 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) join_kernel(const E
   __shared__ int first[kMaxCtas];      // work items before each split unit
   __shared__ SplitUnit unit[kMaxCtas];
   __shared__ short begin[kMaxCtas];    // the CTA of its first piece
-  __shared__ float4 part_o[kTeams][2][16];
+  __shared__ float4 part_o[kTeams][kTeamVec * kTeamLanes];
   __shared__ float2 part_ml[kTeams];
   __shared__ int2 sums[kJoinThreads / 32];
   griddep_launch_dependents();
   griddep_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l16 = lane & 15, team = tid >> 4;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int at8 = tid % kTeamLanes, team = tid / kTeamLanes;
   const float vs = p.v_scale_ptr ? *p.v_scale_ptr : p.v_scale;
   // an item: a row a team, or a row of many pieces
   int total = 0, units = 0;
@@ -1370,83 +1375,92 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) join_kernel(const E
     auto tile = [](int k) { return (4 * k + (k == 0 ? 2 : 0)) * kTile; };
     const int per = many ? (pieces + kTeams - 1) / kTeams : pieces;
     const int k0 = many ? team * per : 0, n = min(pieces - k0, per);  // (n <= 0: none)
-    const float* o = p.piece_o + place0 * kHeadDim + 4 * l16;  // dims 4 l16 .., 64 + 4 l16 ..
-    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    const float* o = p.piece_o + place0 * kHeadDim + 4 * at8;  // dims 4 at8 + 32 x ..
+    float4 acc[kTeamVec];
+#pragma unroll
+    for (int x = 0; x < kTeamVec; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = kNoRowMax, l = 0.f;
-    // (teams of a warp may have different numbers of rounds: its shuffles are for both)
-    for (int c0 = 0; c0 < per; c0 += 16) {
+    // (teams of a warp may have different numbers of rounds: its shuffles are for all)
+    for (int c0 = 0; c0 < per; c0 += kTeamLanes) {
       float cm = kNoRowMax, cl = 0.f;
-      if (c0 + l16 < n) {
-        const float2 ml = __ldcg(p.piece_ml + place0 + tile(k0 + c0 + l16));
+      if (c0 + at8 < n) {
+        const float2 ml = __ldcg(p.piece_ml + place0 + tile(k0 + c0 + at8));
         cm = ml.x, cl = ml.y;
       }
       constexpr int kAtOnce = 4;
-      float4 sum[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+      static_assert(kTeamLanes % kAtOnce == 0, "lanes of a round");
       float w = 0.f;
-      for (int e0 = 0; e0 < min(per - c0, 16); e0 += kAtOnce) {
-        float4 v[kAtOnce][2];
+      for (int e0 = 0; e0 < min(per - c0, kTeamLanes); e0 += kAtOnce) {
+        float4 v[kAtOnce][kTeamVec];
 #pragma unroll
         for (int e = 0; e < kAtOnce; ++e) {
-          v[e][0] = v[e][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (c0 + e0 + e < n) {
-            const float* x = o + (size_t)tile(k0 + c0 + e0 + e) * kHeadDim;
-            v[e][0] = __ldcg(reinterpret_cast<const float4*>(x));
-            v[e][1] = __ldcg(reinterpret_cast<const float4*>(x + 64));
+          const bool there = c0 + e0 + e < n;
+          const float* x0 = o + (size_t)tile(k0 + c0 + e0 + e) * kHeadDim;
+#pragma unroll
+          for (int x = 0; x < kTeamVec; ++x)
+            v[e][x] = there ? __ldcg(reinterpret_cast<const float4*>(x0 + 4 * kTeamLanes * x))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (e0 == 0) {
+          // what these pieces, and the rounds before, weigh in the whole
+          const float om = m, ol = l;
+          w = weigh<kTeamLanes>(cm, cl);
+          m = cm, l = cl;
+          if (c0 > 0) {
+            m = ol == 0.f ? cm : cl == 0.f ? om : fmaxf(om, cm);
+            const float wa = ol != 0.f ? fmaxf(ex2(om - m), 0x1p-149f) : 0.f;
+            const float wb = cl != 0.f ? fmaxf(ex2(cm - m), 0x1p-149f) : 0.f;
+            l = (ol != 0.f ? wa * ol : 0.f) + (cl != 0.f ? wb * cl : 0.f);
+            if (w != 0.f) w = fmaxf(w * wb, 0x1p-149f);
+#pragma unroll
+            for (int x = 0; x < kTeamVec; ++x) {
+              float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (wa != 0.f) add(a, wa, acc[x]);
+              acc[x] = a;
+            }
           }
         }
-        if (e0 == 0) w = weigh(cm, cl);
 #pragma unroll
         for (int e = 0; e < kAtOnce; ++e) {
-          const float we = __shfl_sync(kAll, w, e0 + e, 16);
-          if (we != 0.f) add(sum[0], we, v[e][0]), add(sum[1], we, v[e][1]);
+          const float we = __shfl_sync(kAll, w, e0 + e, kTeamLanes);
+          if (we == 0.f) continue;
+#pragma unroll
+          for (int x = 0; x < kTeamVec; ++x) add(acc[x], we, v[e][x]);
         }
       }
-      if (c0 == 0) {
-        acc[0] = sum[0], acc[1] = sum[1], m = cm, l = cl;
-      } else {  // join with the rounds before
-        float m2 = l16 == 0 ? m : cm, l2 = l16 == 0 ? l : l16 == 1 ? cl : 0.f;
-        const float w2 = weigh(m2, l2);
-        const float wa = __shfl_sync(kAll, w2, 0, 16), wb = __shfl_sync(kAll, w2, 1, 16);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float4 both = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (wa != 0.f) add(both, wa, acc[x]);
-          if (wb != 0.f) add(both, wb, sum[x]);
-          acc[x] = both;
-        }
-        m = m2, l = l2;
-      }
     }
-    if (many) {
-      __syncthreads();  // the item before is read
-      part_o[team][0][l16] = acc[0];
-      part_o[team][1][l16] = acc[1];
-      if (l16 == 0) part_ml[team] = make_float2(m, l);
-      __syncthreads();
-      if (warp != 0) continue;
-      const float2 ml = part_ml[l16];
-      m = ml.x, l = ml.y;
-      const float w = weigh(m, l);
-      acc[0] = acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int e = 0; e < kTeams; ++e) {
-        const float we = __shfl_sync(kAll, w, e, 16);
-        if (we != 0.f) add(acc[0], we, part_o[e][0][l16]), add(acc[1], we, part_o[e][1][l16]);
-      }
-      if (team != 0) continue;
-    }
-    if (!valid) continue;
-    const float nan = __int_as_float(0x7fc00000);
     const bool bad = unit[lo].bad;
-    const float rl = bad ? nan : l == 0.f ? 0.f : vs / l;
+    const float nan = __int_as_float(0x7fc00000);
     const long long q = (long long)unit[lo].q_row + t;
     const int h = unit[lo].head * p.group + g;
-    uint16_t* out = p.out + q * p.out_row_stride + h * p.out_head_stride + 4 * l16;
+    uint16_t* out = p.out + q * p.out_row_stride + h * p.out_head_stride;
+    auto write = [&](int dim, const float4& a, float rl) {
+      *reinterpret_cast<uint2*>(out + dim) =
+          make_uint2(pack2<kType>(a.x * rl, a.y * rl), pack2<kType>(a.z * rl, a.w * rl));
+    };
+    if (many) {
+      __syncthreads();  // the item before is read
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-      *reinterpret_cast<uint2*>(out + 64 * x) = make_uint2(
-          pack2<kType>(acc[x].x * rl, acc[x].y * rl), pack2<kType>(acc[x].z * rl, acc[x].w * rl));
-    if (p.lse && l16 == 0)
+      for (int x = 0; x < kTeamVec; ++x) part_o[team][kTeamLanes * x + at8] = acc[x];
+      if (at8 == 0) part_ml[team] = make_float2(m, l);
+      __syncthreads();
+      if (warp != 0) continue;
+      const float2 ml = part_ml[lane];
+      m = ml.x, l = ml.y;
+      const float w = weigh<kTeams>(m, l);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);  // dims 4 lane ..
+#pragma unroll 8
+      for (int e = 0; e < kTeams; ++e) {
+        const float we = __shfl_sync(kAll, w, e);
+        if (we != 0.f) add(a, we, part_o[e][lane]);
+      }
+      write(4 * lane, a, bad ? nan : l == 0.f ? 0.f : vs / l);
+    } else if (valid) {
+      const float rl = bad ? nan : l == 0.f ? 0.f : vs / l;
+#pragma unroll
+      for (int x = 0; x < kTeamVec; ++x) write(4 * at8 + 4 * kTeamLanes * x, acc[x], rl);
+    }
+    if (p.lse && valid && (many ? lane : at8) == 0)
       p.lse[q * p.num_q_heads + h] =
           bad ? nan : l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
   }

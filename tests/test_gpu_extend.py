@@ -181,6 +181,12 @@ def test_pieces_of_long_contexts(new, ctx, kv_dtype, kv_layout):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("max_ctas", [40, 1024])
+def test_a_unit_in_tens_and_hundreds_of_pieces(max_ctas):
+    c = Call([20], [140000], hq=8, hkv=1, seed=12, kv_dtype="e4m3")
+    c.check(c.run(max_ctas=max_ctas))
+
+
 def test_custom_scales_views_and_device_scales():
     c = Call([33, 70], [400, 70], hq=8, hkv=2, seed=21, ks=0.2937, vs=1.7)
     wide = torch.zeros(103, 12, 128, dtype=c.t, device="cuda")
