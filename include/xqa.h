@@ -523,7 +523,8 @@ xqa_status_t xqa_select_workspace_size(const xqa_select_shape_t* shape, size_t* 
  *   selected_lens device, int32 [B, Hkv]: tokens in them; what xqa_decode_selected takes
  *   workspace     device, >= xqa_select_workspace_size bytes, 256-byte aligned, zero-filled
  *                 once before its first use; every completed call leaves it ready for the
- *                 next. Not one that other calls use, nor one of another shape
+ *                 next, of any shape. A workspace of another call of at least that size may
+ *                 serve too. Concurrent calls must not share one
  *
  * score(page) = 2^e * sum_d (A_d * upper_d + B_d * lower_d), where A_d (B_d) is the sum of
  * the positive (negative) q8_gd over the G heads, q8 = q / 2^f rounded to nearest even, f

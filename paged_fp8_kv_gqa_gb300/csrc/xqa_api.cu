@@ -521,7 +521,7 @@ xqa_status_t encode_plain_map(CUtensorMap* map, const uint8_t* pool, int hkv, in
 
 struct SelectResolved {
   int group, ctas, chunks, chunk_pages, key_stride;
-  size_t ticket_off, keys_off, bytes;
+  size_t bytes;
 };
 
 xqa_status_t resolve_select(const xqa_select_shape_t* s, SelectResolved* r) {
@@ -558,10 +558,11 @@ xqa_status_t resolve_select(const xqa_select_shape_t* s, SelectResolved* r) {
   r->chunk_pages = (int)chunk;
   r->chunks = (int)((s->max_blocks_per_seq + chunk - 1) / chunk);
   if (nseg * r->chunks < r->ctas) r->ctas = (int)(nseg * r->chunks);
-  r->ticket_off = kPrefillWorkspaceBytes;
-  r->keys_off = (r->ticket_off + 4 * (size_t)nseg + 255) & ~(size_t)255;
+  // Tickets are decode's words, at a place that no dimension moves: keys lie behind them, so one
+  // workspace serves any shape and the other calls too. Only segments of several chunks take
+  // one, of which there are at most ctas / 2.
   r->key_stride = (s->max_blocks_per_seq + 3) & ~3;
-  r->bytes = r->keys_off + 4 * (size_t)nseg * r->key_stride;
+  r->bytes = kPrefillWorkspaceBytes + 4 * (size_t)nseg * r->key_stride;
   return XQA_OK;
 }
 
@@ -989,8 +990,8 @@ xqa_status_t xqa_select(const void* q, const uint8_t* bounds, const int32_t* blo
   p.selected_lens = selected_lens;
   p.header = ws_i32(workspace);
   p.status = reinterpret_cast<int32_t*>(base + lay.status_off);
-  p.tickets = reinterpret_cast<int32_t*>(base + r.ticket_off);
-  p.keys = reinterpret_cast<uint32_t*>(base + r.keys_off);
+  p.tickets = reinterpret_cast<int32_t*>(base + lay.ticket_off);
+  p.keys = reinterpret_cast<uint32_t*>(base + kPrefillWorkspaceBytes);
   p.batch = shape->batch;
   p.num_kv_heads = shape->num_kv_heads;
   p.group = r.group;

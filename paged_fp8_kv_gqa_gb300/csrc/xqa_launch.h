@@ -173,7 +173,8 @@ struct SelectParams {
   int32_t* selected_lens;  // [B * Hkv]
   int32_t* header;         // workspace header (CTAs launched)
   int32_t* status;         // [kMaxCtas]
-  int32_t* tickets;        // [B * Hkv] chunks scored: zero between calls
+  int32_t* tickets;        // [segments of several chunks: <= kMaxCtas / 2] chunks scored: zero
+                           // between calls
   uint32_t* keys;          // [B * Hkv, key_stride]
   int key_stride;          // MBS, a multiple of 4
   int batch, num_kv_heads, group, max_blocks_per_seq, num_blocks;
