@@ -440,7 +440,8 @@ typedef struct xqa_pages {
  *                 16 tokens), XQA_ERR_BAD_OFFSETS (its rows, behind those of every
  *                 sequence before it, would pass num_rows; so would every later one's),
  *                 XQA_ERR_NO_PAGES (the stack has too few pages for it and those before it;
- *                 later ones that need no page are served). XQA_ERR_BAD_BLOCK_ID: a page
+ *                 later ones that need no page are served; a num_free below 0 or above NB
+ *                 counts as 0, which new_free then is). XQA_ERR_BAD_BLOCK_ID: a page
  *                 outside [0, NB) in the stack or the table; entries are written as they
  *                 are, slots as -1
  *
@@ -462,7 +463,9 @@ xqa_status_t xqa_assign_pages(const int32_t* new_tokens, const int32_t* context_
  *   device_status as for xqa_assign_pages: XQA_ERR_BAD_BLOCK_ID (an entry outside [0, NB):
  *                 it is left out), XQA_ERR_CTX_TOO_LONG (a length below 0 or above MBS * 16:
  *                 none of the sequence's pages goes back), XQA_ERR_NO_PAGES (more than NB
- *                 pages would be free: those past NB are dropped)
+ *                 pages would be free: those past NB are dropped; or num_free is below 0 or
+ *                 above NB: the call releases nothing, free_pages stays, new_lens is
+ *                 context_lens and new_free is num_free)
  * A page must not go back twice. One kernel, no host synchronisation, no workspace; may be
  * captured into a CUDA graph. */
 xqa_status_t xqa_release_pages(const uint8_t* done, const int32_t* context_lens,

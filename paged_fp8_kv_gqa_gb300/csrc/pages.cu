@@ -92,12 +92,12 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Height of the stack, 0 if the word cannot be one.
+// Height of the stack, -1 if the word cannot be one.
 __device__ __forceinline__ int stack_height(const PagesParams& p) {
   const int f = *p.num_free;
   if (f >= 0 && f <= p.num_blocks) return f;
-  if (threadIdx.x == 0) raise(p.status, XQA_ERR_NO_PAGES);
-  return 0;
+  raise(p.status, XQA_ERR_NO_PAGES);
+  return -1;
 }
 
 template <int kThreads, bool kCluster>
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) assign_kernel(const PagesParams p) {
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x;
-  if (tid == 0) height = stack_height(p);  // (read behind the first scan)
+  if (tid == 0) height = max(stack_height(p), 0);  // (read behind the first scan)
   Two before{0, 0};
   long long rows = 0;  // served so far
   int taken = 0;
@@ -302,6 +302,11 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const PagesParams p) 
     __syncthreads();
   }
   const int free_now = height;
+  if (free_now < 0) {  // where the stack ends is not known: nothing goes back, nothing is lost
+    for (int b = blockIdx.x * kThreads + tid; b < p.batch; b += ctas * kThreads) p.new_lens[b] = p.context_lens[b];
+    if (blockIdx.x == 0 && tid == 0) *p.new_free = *p.num_free;
+    return;
+  }
   Two all;
   const Two mine = scan2<kThreads>(Two{tid < warps ? count[tid] : 0, 0}, sums, all);
   if (tid < warps) count[tid] = (int)mine.rows;
