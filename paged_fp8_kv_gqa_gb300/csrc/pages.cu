@@ -260,21 +260,23 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const PagesParams p) 
   }
   if (tid == 0) first[p.batch] = entries;
   __syncthreads();
-  const int run = (int)(((long long)entries + 32 * warps - 1) / (32 * warps) * 32);
-  const int from = (int)min((long long)warp * run, (long long)entries), to = min(from + run, entries);
+  // (places in the list are unsigned: an end or a step past the last of 2^31 of them wraps otherwise)
+  const uint32_t run = (uint32_t)(((long long)entries + 32 * warps - 1) / (32 * warps) * 32);
+  const uint32_t from = (uint32_t)min((long long)warp * run, (long long)entries);
+  const uint32_t to = min(from + run, (uint32_t)entries);
   // A lane's entries ascend: its sequence is looked for again only where one ends.
   struct At {
     const int32_t* row;  // row[i]: the table's entry of list entry i < next
-    int next;
+    uint32_t next;
   };
-  auto read = [&](int i0, At& at, int (&id)[kPerLane]) {  // entries i0 + 32 e + lane; -1 past the run
+  auto read = [&](uint32_t i0, At& at, int (&id)[kPerLane]) {  // entries i0 + 32 e + lane; -1 past the run
 #pragma unroll
     for (int e = 0; e < kPerLane; ++e) {
-      const int i = i0 + 32 * e + lane;
+      const uint32_t i = i0 + 32 * e + lane;
       id[e] = -1;
       if (i >= to) continue;
       if (i >= at.next) {
-        const int b = last_at_most(first, p.batch, i);
+        const int b = last_at_most(first, p.batch, (int)i);
         at.row = p.block_tables + ((long long)b * p.max_blocks_per_seq - first[b]);
         at.next = first[b + 1];
       }
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const PagesParams p) 
   };
   int good = 0, id[kPerLane];
   At place{nullptr, 0};
-  for (int i0 = from; i0 < to; i0 += 32 * kPerLane) {
+  for (uint32_t i0 = from; i0 < to; i0 += 32 * kPerLane) {
     read(i0, place, id);
 #pragma unroll
     for (int e = 0; e < kPerLane; ++e) {
@@ -317,7 +319,7 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const PagesParams p) 
     *p.new_free = (int)min(free_now + all.rows, (long long)p.num_blocks);
   long long at = (long long)free_now + count[warp];
   place.next = 0;
-  for (int i0 = from; i0 < to; i0 += 32 * kPerLane) {
+  for (uint32_t i0 = from; i0 < to; i0 += 32 * kPerLane) {
     if (run > 32 * kPerLane) read(i0, place, id);  // (one round's are still there)
 #pragma unroll
     for (int e = 0; e < kPerLane; ++e) {
