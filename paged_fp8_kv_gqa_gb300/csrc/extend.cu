@@ -119,7 +119,7 @@ static_assert(kExtendSmem <= 227 * 1024, "shared memory budget");
 // A sequence of n tokens: np = ceil(n / 2T) units for each kv head; unit i sees base +
 // min(step (i + 1), rows) keys at most, and is kKeyCost long for each of them, or key_cost_one if
 // it fills one row tile only, and kUnitCost more for its start and end.
-constexpr int kKeyCost = 16, kUnitCost = 256 * kKeyCost;
+constexpr int kKeyCost = 16, kUnitCost = kExtendUnitKeys * kKeyCost;
 constexpr int kCutTiles = 8;  // units of fewer tiles are not cut
 struct Cost {
   int np;

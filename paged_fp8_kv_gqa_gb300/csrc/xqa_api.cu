@@ -480,10 +480,11 @@ xqa_status_t resolve_extend(const xqa_extend_shape_t* s, ExtendResolved* r) {
     r->ctas = sms;
   }
   if (r->ctas > xqa::kMaxCtas) r->ctas = xqa::kMaxCtas;
-  // no more than the longest line of these dimensions has shares for
+  // no more than the longest line of these dimensions has shares for (of sequences that hold
+  // their new tokens: where there are more queries than tokens, hidden keys are counted too)
   const long long seqs = s->batch < s->total_q ? s->batch : s->total_q;
   const long long units = (s->total_q / (2 * (128 / r->group)) + seqs) * s->num_kv_heads;
-  const long long line = units * (128 + (long long)s->max_blocks_per_seq * kBlockSize);
+  const long long line = units * (xqa::kExtendUnitKeys + (long long)s->max_blocks_per_seq * kBlockSize);
   if (r->ctas > line / xqa::kExtendMinShare)
     r->ctas = line < xqa::kExtendMinShare ? 1 : (int)(line / xqa::kExtendMinShare);
   r->pieces_off = (kPrefillWorkspaceBytes + (size_t)r->ctas * sizeof(xqa::SplitUnit) + 255) & ~(size_t)255;

@@ -93,8 +93,9 @@ struct PrefillParams {
 };
 
 // The least share of the line of work (extend.cu: keys seen, summed over the units) that a
-// CTA takes; fewer CTAs work on shorter lines.
-constexpr int kExtendMinShare = 384;
+// CTA takes; fewer CTAs work on shorter lines. A unit's start and end count as kExtendUnitKeys
+// keys.
+constexpr int kExtendMinShare = 384, kExtendUnitKeys = 256;
 
 // A unit of tokens whose keys several CTAs share; pieces < 2: none.
 struct SplitUnit {
