@@ -20,8 +20,8 @@
  *   - The library allocates no memory and reads no environment variables,
  *     never calls abort/exit and never synchronises except in the xqa_read_*
  *     helpers, which say so. Host state it keeps: a per-device "kernel
- *     attributes set" flag and SM count, and the cached cuTensorMapEncodeTiled
- *     entry point.
+ *     attributes set" flag, SM count and cluster size that fits, and the cached
+ *     cuTensorMapEncodeTiled entry point.
  *     Device state it keeps: the XQA_STATIC_WORKSPACE_BYTES array of
  *     xqa_decode_static_workspace (one per device, shared by every call of
  *     that entry point). Between calls, a caller's workspace keeps the merge

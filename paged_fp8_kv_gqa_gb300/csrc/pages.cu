@@ -30,7 +30,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kClusterCtas = 16;  // (more than 8: where a GPC has them, as an sm_103 has)
+constexpr int kClusterCtas = 16;  // at most; fewer where the device has no place for so many
 constexpr int kSmallThreads = 256, kLargeThreads = 1024;
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -350,32 +350,57 @@ cudaLaunchConfig_t config(int ctas, int threads, size_t smem, cudaStream_t strea
 }  // namespace
 
 // A small CTA where one round of it takes every sequence and row, a large one where it has few
-// rows or pages to write, else the cluster. When this was chosen a step of 16 tokens took 4.7 us
+// rows or pages to write, else a cluster of `cluster` CTAs (1: one alone). When this was chosen a step of 16 tokens took 4.7 us
 // in 256 threads, 6.4 in 1024 (a barrier of 32 warps at each turn); 3.5 us now.
-cudaError_t launch_assign(const PagesParams& p, cudaStream_t stream) {
+cudaError_t launch_assign(const PagesParams& p, int cluster, cudaStream_t stream) {
   const bool small = p.batch <= kSmallThreads && p.num_rows <= 4 * kSmallThreads;
-  const int ctas = p.num_rows <= 4 * kLargeThreads ? 1 : kClusterCtas;
+  const bool many = p.num_rows > 4 * kLargeThreads;
+  const int ctas = many ? cluster : 1;
   const size_t smem = sizeof(int) * (3 * (size_t)p.batch + 2);
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = config(ctas, small ? kSmallThreads : kLargeThreads, smem, stream, attr);
   if (small) return cudaLaunchKernelEx(&cfg, assign_kernel<kSmallThreads, false>, p);
-  return ctas > 1 ? cudaLaunchKernelEx(&cfg, assign_kernel<kLargeThreads, true>, p)
-                  : cudaLaunchKernelEx(&cfg, assign_kernel<kLargeThreads, false>, p);
+  return many ? cudaLaunchKernelEx(&cfg, assign_kernel<kLargeThreads, true>, p)
+              : cudaLaunchKernelEx(&cfg, assign_kernel<kLargeThreads, false>, p);
 }
 
 // (how many pages go back is known to the device alone: the tables' width stands for it)
-cudaError_t launch_release(const PagesParams& p, cudaStream_t stream) {
+cudaError_t launch_release(const PagesParams& p, int cluster, cudaStream_t stream) {
   const bool small = p.batch <= kSmallThreads &&
                      (long long)p.batch * p.max_blocks_per_seq <= 32ll * kPerLane * (kSmallThreads / 32);
   const size_t smem = sizeof(int) * (2 * (size_t)p.batch + 1);
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = config(small ? 1 : kClusterCtas, small ? kSmallThreads : kLargeThreads,
+  const cudaLaunchConfig_t cfg = config(small ? 1 : cluster, small ? kSmallThreads : kLargeThreads,
                                         smem, stream, attr);
   return small ? cudaLaunchKernelEx(&cfg, release_kernel<kSmallThreads, false>, p)
                : cudaLaunchKernelEx(&cfg, release_kernel<kLargeThreads, true>, p);
 }
 
-cudaError_t set_pages_attributes() {
+namespace {
+
+// The largest cluster, halving from kClusterCtas, that `fits`.
+template <class Fits>
+int largest_cluster(Fits fits) {
+  int ctas = kClusterCtas;
+  while (ctas > 1 && !fits(ctas)) ctas /= 2;
+  return ctas;
+}
+
+// Whether a cluster of `ctas` CTAs of the kernel with the most shared memory it may ask for has
+// a place. (16 are more than every device of an architecture need offer, and a context may be
+// limited to some of the SMs.)
+bool has_place(void (*kernel)(PagesParams), int ctas, size_t smem) {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = config(ctas, kLargeThreads, smem, nullptr, attr);
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess) return clusters > 0;
+  cudaGetLastError();  // (as a size that does not fit may be reported)
+  return false;
+}
+
+}  // namespace
+
+cudaError_t set_pages_attributes(int* cluster) {
   const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
   const int assign = sizeof(int) * (3 * kMaxPagesBatch + 2), release = sizeof(int) * (2 * kMaxPagesBatch + 1);
   cudaError_t e;
@@ -384,7 +409,12 @@ cudaError_t set_pages_attributes() {
   if ((e = cudaFuncSetAttribute(assign_kernel<kLargeThreads, true>, any, 1)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(release_kernel<kLargeThreads, true>, any, 1)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(assign_kernel<kLargeThreads, false>, a, assign)) != cudaSuccess) return e;
-  return cudaFuncSetAttribute(release_kernel<kLargeThreads, true>, a, release);
+  if ((e = cudaFuncSetAttribute(release_kernel<kLargeThreads, true>, a, release)) != cudaSuccess) return e;
+  *cluster = largest_cluster([&](int ctas) {
+    return has_place(assign_kernel<kLargeThreads, true>, ctas, assign) &&
+           has_place(release_kernel<kLargeThreads, true>, ctas, release);
+  });
+  return cudaSuccess;
 }
 
 }  // namespace xqa

@@ -17,7 +17,7 @@ namespace xqa {
 cudaError_t set_partial_attributes();
 cudaError_t set_prefill_attributes();
 cudaError_t set_extend_attributes();
-cudaError_t set_pages_attributes();
+cudaError_t set_pages_attributes(int* cluster);
 }
 
 namespace {
@@ -28,6 +28,7 @@ using xqa::kHeadDim;
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_attrs_set[kMaxDevices];
 std::atomic<int> g_sms[kMaxDevices];  // SM count, set with the attributes
+std::atomic<int> g_cluster[kMaxDevices];  // CTAs of a cluster of the calls over pages, likewise
 std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode{nullptr};
 
 struct Resolved {
@@ -108,20 +109,30 @@ int device_sms() {
   return g_sms[dev].load(std::memory_order_acquire);
 }
 
+// CTAs of a cluster that hands out or takes back pages (as device_sms; 1 if unknown).
+int device_cluster() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 1;
+  const int ctas = g_cluster[dev].load(std::memory_order_acquire);
+  return ctas > 0 ? ctas : 1;
+}
+
 xqa_status_t ensure_device_setup() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return XQA_ERR_DEVICE;
   if (dev < 0 || dev >= kMaxDevices) return XQA_ERR_DEVICE;
   if (g_attrs_set[dev].load(std::memory_order_acquire) == 0) {
+    int cluster = 1;
     if (xqa::set_partial_attributes() != cudaSuccess ||
         xqa::set_prefill_attributes() != cudaSuccess ||
         xqa::set_extend_attributes() != cudaSuccess ||
-        xqa::set_pages_attributes() != cudaSuccess)
+        xqa::set_pages_attributes(&cluster) != cudaSuccess)
       return XQA_ERR_LAUNCH;
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return XQA_ERR_DEVICE;
     g_sms[dev].store(sms, std::memory_order_release);
+    g_cluster[dev].store(cluster, std::memory_order_release);
     g_attrs_set[dev].store(1, std::memory_order_release);
   }
   if (g_encode.load(std::memory_order_acquire) == nullptr) {
@@ -905,7 +916,7 @@ xqa_status_t xqa_assign_pages(const int32_t* new_tokens, const int32_t* context_
   p.slots = slots;
   p.positions = positions;
   p.status = device_status;
-  return xqa::launch_assign(p, (cudaStream_t)stream) == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
+  return xqa::launch_assign(p, device_cluster(), (cudaStream_t)stream) == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
 }
 
 xqa_status_t xqa_release_pages(const uint8_t* done, const int32_t* context_lens,
@@ -926,7 +937,7 @@ xqa_status_t xqa_release_pages(const uint8_t* done, const int32_t* context_lens,
   p.new_lens = new_lens;
   p.new_free = new_free;
   p.status = device_status;
-  return xqa::launch_release(p, (cudaStream_t)stream) == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
+  return xqa::launch_release(p, device_cluster(), (cudaStream_t)stream) == cudaSuccess ? XQA_OK : XQA_ERR_LAUNCH;
 }
 
 xqa_status_t xqa_page_bounds(const uint8_t* k_cache, const int32_t* block_tables,

@@ -183,8 +183,8 @@ struct SelectParams {
   int chunks, chunk_pages;
 };
 
-cudaError_t launch_assign(const PagesParams& p, cudaStream_t stream);
-cudaError_t launch_release(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_assign(const PagesParams& p, int cluster, cudaStream_t stream);
+cudaError_t launch_release(const PagesParams& p, int cluster, cudaStream_t stream);
 cudaError_t launch_bounds(const BoundsParams& p, cudaStream_t stream);
 cudaError_t launch_select(const SelectParams& p, int ctas, cudaStream_t stream);
 cudaError_t launch_prefill(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
