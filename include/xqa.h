@@ -161,7 +161,10 @@ xqa_status_t xqa_kernels_per_call(const xqa_shape_t* shape, int32_t* kernels);
  *                 xqa_combine) leaves it needing a fresh zero fill
  *
  * out[b, h, :] = sum_t softmax_t(sm_scale * <q[b,h], k_t>) * v_t over the
- * ctx_b tokens of kv head h / G, rounded to fp16 (round to nearest even).
+ * ctx_b tokens of kv head h / G, rounded to fp16 (round to nearest even). A token
+ * whose logit is minus infinity (a key with an infinity) has weight 0; a row all of
+ * whose logits are is zero, as one of an empty sequence, here and in xqa_prefill and
+ * xqa_extend.
  * Kernels enqueued: the split-KV partial kernel, which derives the split plan
  * itself and merges split segments when merge_mode is 0; before it the planner
  * when the batch is too large for the partial kernel to hold the segment table
@@ -324,15 +327,14 @@ xqa_status_t xqa_prefill_workspace_size(const xqa_prefill_shape_t* shape, size_t
  *                 serve both. Concurrent calls must not share one
  *
  * out[i, h] = sum_j softmax_j(sm_scale * <q[i, h], k[j, h / G]>) * v[j, h / G] over the
- * keys that query i sees. A row that sees none is zero, its lse -inf. Products
- * accumulate in 32 bits, the softmax is in 32 bits, its weights are rounded to
- * shape->dtype for the second product, out is rounded once. What a query does not see
- * does not reach its row, infinities and NaN included. Rows of q and out behind
- * cu_seqlens_q[B] are left alone. A sequence whose offsets are bad
- * (XQA_ERR_BAD_OFFSETS, see xqa_read_status) is skipped, and where offsets descend so
+ * keys that query i sees. A row that sees none is zero, its lse -inf, and so is one whose
+ * logits are all minus infinity. Products accumulate in 32 bits, the softmax is in 32
+ * bits, its weights are rounded to shape->dtype for the second product, out is rounded
+ * once. What a query does not see does not reach its row, infinities and NaN included.
+ * Rows of q and out behind cu_seqlens_q[B] are left alone. A sequence whose offsets are
+ * bad (XQA_ERR_BAD_OFFSETS, see xqa_read_status) is skipped, and where offsets descend so
  * that sequences overlap, some behind them may be; if only its key offsets are bad, its
- * rows are NaN. One kernel, no host synchronisation; may be captured into a CUDA
- * graph. */
+ * rows are NaN. One kernel, no host synchronisation; may be captured into a CUDA graph. */
 xqa_status_t xqa_prefill(const void* q, const void* k, const void* v, const int32_t* cu_seqlens_q,
                          const int32_t* cu_seqlens_k, void* out, float* lse,
                          const xqa_prefill_shape_t* shape, void* workspace,
@@ -388,12 +390,12 @@ xqa_status_t xqa_extend_workspace_size(const xqa_extend_shape_t* shape, size_t* 
  *
  * out[i, h] = sum_t softmax_t(sm_scale * k_scale * <q[i, h], K_t>) * v_scale * V_t over
  * the tokens that query i sees. A row that sees none (a context shorter than the new
- * tokens) is zero, its lse -inf. Codes are taken exactly; products accumulate in 32 bits,
- * the softmax is in 32 bits, its weights are rounded to shape->dtype for the second
- * product, out is rounded once. What a query does not see does not reach its row,
- * infinities and NaN included. Rows behind cu_seqlens[B] are left alone. Results do not
- * depend on what else is in the batch beyond the order of 32-bit sums (where a long
- * sequence is cut into pieces).
+ * tokens) is zero, its lse -inf, and so is one whose logits are all minus infinity. Codes
+ * are taken exactly; products accumulate in 32 bits, the softmax is in 32 bits, its
+ * weights are rounded to shape->dtype for the second product, out is rounded once. What a
+ * query does not see does not reach its row, infinities and NaN included. Rows behind
+ * cu_seqlens[B] are left alone. Results do not depend on what else is in the batch beyond
+ * the order of 32-bit sums (where a long sequence is cut into pieces).
  *
  * Errors that only the device sees (xqa_read_status): XQA_ERR_BAD_BLOCK_ID (the rows that
  * see a token of the page are NaN), XQA_ERR_CTX_TOO_LONG (the sequence's rows are NaN),

@@ -2,7 +2,8 @@
 //
 //   out[i, h] = sum_t softmax_t(sm_scale k_scale <q[i, h], K_t>) v_scale V_t,
 //   t < ctx, and for causal calls t <= ctx - n + i (i of the sequence's n queries, t its
-//   cached tokens, the chunk's own among them); a row that sees nothing is zero.
+//   cached tokens, the chunk's own among them); a row that sees nothing, or logits of -inf
+//   alone, is zero.
 //
 // Prompt attention's mathematics (a running maximum and sum over 128-key tiles, products
 // on tcgen05, two 128-row tiles worked in turn) on keys and values that are read as they

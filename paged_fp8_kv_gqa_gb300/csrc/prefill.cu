@@ -2,7 +2,7 @@
 //
 //   out[i, h] = sum_j softmax_j(sm_scale <q[i, h], k[j, h / G]>) v[j, h / G],
 //   j < len_k, and for causal calls j <= len_k - len_q + i (i, j counted within
-//   the sequence); a row that sees nothing is zero.
+//   the sequence); a row that sees nothing, or logits of -inf alone, is zero.
 //
 // One persistent CTA per SM works through units of 2 x 128 rows: the G query
 // heads of one kv head for 2 x T consecutive tokens of one sequence, T =
@@ -661,7 +661,7 @@ __device__ __forceinline__ void epilogue_role(const Ctx& c) {
       // infinities and NaN of masked V tiles (zeroed there), for rows that see them
       const bool patch = *(volatile int*)&sh.not_finite[i % kUnitSlots] != 0;
       const int vis = visible(p, u, rp);
-      const float rl = ml.y == 0.f ? 0.f : 1.f / ml.y;  // a row that sees nothing: 0
+      const float rl = ml.y == 0.f ? 0.f : 1.f / ml.y;  // a row without a weight: 0
       uint16_t* dst[4];  // this lane's unit of the four lanes' rows
       if (!kCut) {
         const unsigned long long mine = rp.valid ? reinterpret_cast<unsigned long long>(out) : 0ull;
