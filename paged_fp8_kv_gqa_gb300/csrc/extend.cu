@@ -406,7 +406,7 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
     mine.ctx = 0;
     if (base + lane < p.batch) mine = read_seq(p, base + lane, &sh.status);
   };
-  SplitUnit split_unit{0, 0, 0, 0, 0};  // the one whose first piece is this CTA's
+  SplitUnit split_unit{0, 0, 0, 0};  // the one whose first piece is this CTA's
   long long at = sh.start_at;  // where sequence b begins
   Seq s = sh.start;
   Cost cost = seq_cost(p, s);
@@ -489,7 +489,6 @@ __device__ __forceinline__ void load_role(const Ctx& c, const CUtensorMap* tm_q,
             split_unit.q_row = w.q_row;
             split_unit.tokens = w.tokens;
             split_unit.head = head;
-            split_unit.bad = w.bad;
           }
         }
       }
@@ -1269,7 +1268,7 @@ __global__ void __launch_bounds__(kExtendThreads, 1)
   if (threadIdx.x == 0) {
     // no unit to join if the CTA had none or gave up. (Cleared at the start, in front of the
     // roles, the same store cost 10 % of long chunks: 4 chunks 655 us, 719 so.)
-    if (!works || !aligned || sh.wait_limit == 0) p.split[blockIdx.x] = SplitUnit{0, 0, 0, 0, 0};
+    if (!works || !aligned || sh.wait_limit == 0) p.split[blockIdx.x] = SplitUnit{0, 0, 0, 0};
     if (sh.wait_limit == 0) record_status(&sh.status, XQA_ERR_DEVICE_TIMEOUT);
     p.status[blockIdx.x] = sh.status;
     if (blockIdx.x == 0) p.header[0] = gridDim.x;
@@ -1329,7 +1328,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) join_kernel(const E
   int total = 0, units = 0;
   for (int c0 = 0; c0 < ctas; c0 += kJoinThreads) {
     const int c = c0 + tid;
-    SplitUnit u{0, 0, 0, 0, 0};
+    SplitUnit u{0, 0, 0, 0};
     if (c < ctas) u = p.split[c];
     const int rows = u.pieces > 1 ? u.tokens * p.group : 0;
     const int n = u.pieces <= kTeamPieces ? (rows + kTeams - 1) / kTeams : rows;
@@ -1430,8 +1429,6 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) join_kernel(const E
         }
       }
     }
-    const bool bad = unit[lo].bad;
-    const float nan = __int_as_float(0x7fc00000);
     const long long q = (long long)unit[lo].q_row + t;
     const int h = unit[lo].head * p.group + g;
     uint16_t* out = p.out + q * p.out_row_stride + h * p.out_head_stride;
@@ -1455,15 +1452,15 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) join_kernel(const E
         const float we = __shfl_sync(kAll, w, e);
         if (we != 0.f) add(a, we, part_o[e][lane]);
       }
-      write(4 * lane, a, bad ? nan : l == 0.f ? 0.f : vs / l);
+      write(4 * lane, a, l == 0.f ? 0.f : vs / l);
     } else if (valid) {
-      const float rl = bad ? nan : l == 0.f ? 0.f : vs / l;
+      const float rl = l == 0.f ? 0.f : vs / l;
 #pragma unroll
       for (int x = 0; x < kTeamVec; ++x) write(4 * at8 + 4 * kTeamLanes * x, acc[x], rl);
     }
     if (p.lse && valid && (many ? lane : at8) == 0)
       p.lse[q * p.num_q_heads + h] =
-          bad ? nan : l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+          l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
   }
 }
 

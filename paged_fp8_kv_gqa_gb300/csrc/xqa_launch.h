@@ -97,9 +97,10 @@ struct PrefillParams {
 // keys.
 constexpr int kExtendMinShare = 384, kExtendUnitKeys = 256;
 
-// A unit of tokens whose keys several CTAs share; pieces < 2: none.
+// A unit of tokens whose keys several CTAs share; pieces < 2: none. (A unit of a bad length or
+// scale has no keys to share.)
 struct SplitUnit {
-  int pieces, q_row, tokens, head, bad;
+  int pieces, q_row, tokens, head;
 };
 
 // Length of a key of a one-row-tile unit on chunk attention's line of work, where one of two row

@@ -16,10 +16,8 @@ def ctas_of(lib, batch, hq, hkv, mbs, total_q, max_ctas):  # noqa: F811
     s = xqa.XqaExtendShape(batch, hq, hkv, 128, 16, mbs, 100000, total_q, 0, 0, 0, 1, 0.0, max_ctas)
     n = ctypes.c_size_t()
     assert lib.xqa_extend_workspace_size(ctypes.byref(s), ctypes.byref(n)) == xqa.XQA_OK
-    for ctas in range(1, max_ctas + 1):  # (a header for each is 20 bytes, its pieces 266 240)
-        if (12544 + 20 * ctas + 255) // 256 * 256 + ctas * 2 * 256 * 130 * 4 == n.value:
-            return ctas
-    raise AssertionError(n.value)
+    # a fixed part, a few words for each CTA, and its two pieces of 256 rows of 128 + 2 floats
+    return (n.value - 12544) // (2 * 256 * 130 * 4)
 
 
 def line_shares(new, ctx, hq, hkv, causal, key_one):
