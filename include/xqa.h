@@ -369,6 +369,8 @@ xqa_status_t xqa_extend_workspace_size(const xqa_extend_shape_t* shape, size_t* 
 /* Attention of chunks of new tokens over the paged cache: any number of new tokens for
  * each sequence, from one to a whole prompt, their keys and values already in the cache
  * (xqa_append), read there as they lie.
+ * Single tokens may stand beside chunks; where all or most sequences have one, xqa_decode
+ * (of those sequences' rows of the tables) takes less time for them.
  *
  *   q             device, shape->dtype [total_q, Hq, 128] (strided), 16-byte aligned,
  *                 packed by sequence

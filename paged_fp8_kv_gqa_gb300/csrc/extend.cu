@@ -1229,7 +1229,8 @@ __global__ void __launch_bounds__(kExtendThreads, 1)
   if (aligned && works) {
     const Ctx c{p, sh, smem, raw, stats, sh.tmem};
     __syncwarp();
-    // 256 x 136 + 128 x 96 + 256 x 56 are the launch's 640 x 96
+    // 256 x 136 + 128 x 96 + 256 x 56 are the launch's 640 x 96. (The code is compiled for 96:
+    // 20 bytes a thread are spilled, 28 over 4 bits.)
     if (warp >= 12) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
       if (warp == 12) tensor_role<kType>(c);

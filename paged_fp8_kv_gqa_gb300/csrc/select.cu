@@ -19,11 +19,13 @@
 // order, so a choice depends neither on the split of the work nor on the batch, and ties are
 // ties. 2^f is common to all pages of a choice and left out.
 //
-// Both are bound by bytes: 2048 + 272 (1152 + 272 in 4 bits) for a slice's bounds, 272 for a
+// Their floors are bytes: 2048 + 272 (1152 + 272 in 4 bits) for a slice's bounds, 272 for a
 // score, against 4096 for a page's keys and values. Measured: bounds of 49k rows x 4 heads 9.8 us
-// (3650 GB/s; by the packed minima and maxima's issue slots), of 16 rows 2.7 us; choices of
-// 128 of 1100 pages x 64 12.7 us, of 256 of 8192 pages x 8 13.9 us (20 MB of bounds, the rest
-// the latencies of scores, ticket, threshold and order), of 4 of 5 pages 1.6 us.
+// (3650 GB/s; by latency: a warp waits for its page ids and then for the codes of two slices at
+// a time, in about two rounds of CTAs; loads are its largest stall, with 49 % of the issue
+// slots used), of 16 rows 2.7 us; choices of 128 of 1100 pages x 64 12.7 us, of 256 of 8192
+// pages x 8 13.9 us (20 MB of bounds, the rest the latencies of scores, ticket, threshold and
+// order), of 4 of 5 pages 1.6 us.
 #include "xqa_device.cuh"
 #include "xqa_launch.h"
 
@@ -578,6 +580,7 @@ __device__ __forceinline__ void take_pages(const SelectParams& p, int seg, int n
   }
 }
 
+// (two CTAs an SM leave 64 registers: 48 bytes a thread are spilled)
 __global__ void __launch_bounds__(kSelectThreads, kSelectCtas) select_kernel(const SelectParams p) {
   __shared__ __align__(16) SelectShared sh;
   griddep_launch_dependents();
